@@ -117,6 +117,86 @@ typedef struct {
 uly_status ulysses_swap_batch(const uly_swap_desc *descs_host, int32_t n_descs, int64_t B, int64_t N,
                               int32_t d, int32_t P, uly_dtype dtype, void *stream);
 
+/* ------------------------------- norm, rotation and move of Q, K and V */
+
+/*
+ * Rotary position embedding of a call, read on the host before it returns.
+ * Pair f (0 <= f < rot_dim/2) of a head turns by the angle
+ *   t = positions[axis_host[f]][token] * inv_freq_host[f]
+ * and is the values (f, f + rot_dim/2) of the head (interleaved = 0) or
+ * (2f, 2f + 1) (interleaved = 1); values from rot_dim on are not rotated:
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t).
+ * Any int64 position is valid, negative ones too; the angle is formed modulo
+ * a turn with an error below |position| * 2^-53 turns.
+ */
+typedef struct {
+    const int64_t *positions;    /* device [num_axes][P][B][N/P] (8-byte aligned), or
+                                    NULL: the token's index n in its sequence, every axis */
+    const double *inv_freq_host; /* [rot_dim/2], finite; may be NULL if rot_dim = 0 */
+    const int32_t *axis_host;    /* [rot_dim/2] values in [0, num_axes), or NULL: axis 0 */
+    int32_t rot_dim;             /* 0 (no rotation) or a multiple of 16 up to d */
+    int32_t num_axes;            /* 1..8 (time, height and width: 3) */
+    int32_t interleaved;         /* 0 or 1 */
+} uly_rope_desc;
+
+/* Bytes of device workspace ulysses_qkv_norm_rope_bwd needs (0 if d is not supported). */
+size_t ulysses_qkv_norm_rope_workspace_size(int32_t d);
+
+/*
+ * The step before the first all-to-all, and the all-to-all with it: an RMS
+ * norm of every query and key head with a learned weight, the rotary position
+ * embedding, and the seq->head move of Q, K and V, in one pass (the layer's
+ * projection outputs are read once).  The pages leave the norm and the
+ * embedding to the model; the move is ulysses_seq_to_head's.  For a head row
+ * x of Q or K:
+ *   y = rotate(w * x / sqrt(mean(x^2) + eps))
+ * in fp32, rounded once; V is copied bit for bit.
+ *
+ * q_seq         : device [P][B][N/P][Hq][d], k_seq, v_seq with Hkv heads, read only.
+ * q/k/v_stride  : elements from one token to the next, so that the three may
+ *                 be views of one projection output [tokens][(Hq+2Hkv)*d];
+ *                 0 = contiguous.  At least H*d, and a multiple of 16 bytes.
+ * q_weight, k_weight : device [d], or both NULL (no norm, rotation only).
+ * q_out, k_out, v_out : device, contiguous.  to_head = 1: the head layout
+ *                 [P][B][N][H/P][d] (Hq % P == 0, Hkv % P == 0); to_head = 0:
+ *                 the sequence layout.  No output may overlap an input or
+ *                 another output.  v_seq and v_out may both be NULL.
+ * N % P == 0, Hq % Hkv == 0, d in {64, 128}; P*B*(N/P) < 2^31 tokens;
+ * eps >= 0.  One token (N = P = 1) is an ordinary call.
+ */
+uly_status ulysses_qkv_norm_rope_fwd(const void *q_seq, const void *k_seq, const void *v_seq,
+                                     const void *q_weight, const void *k_weight, void *q_out, void *k_out,
+                                     void *v_out, int64_t B, int64_t N, int32_t Hq, int32_t Hkv, int32_t d,
+                                     int32_t P, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                     const uly_rope_desc *rope_host, float eps, int32_t to_head,
+                                     uly_dtype dtype, void *stream);
+
+/*
+ * Its backward, head->seq move included.  With g = rotate^-1(dy), r = 1 /
+ * sqrt(mean(x^2) + eps) and xhat = x r:
+ *   dx = r (w * g - xhat mean(w * g * xhat)),   dw = sum over rows of g * xhat
+ * dV is copied back bit for bit.
+ *
+ * q_seq, k_seq and their strides : the forward's inputs (not read, and may be
+ *                 NULL, without a norm).
+ * dq_out, dk_out, dv_out : device, gradients of the forward's outputs, in their layout.
+ * dq_seq, dk_seq, dv_seq : device, written; strides as the inputs' above, so
+ *                 that the three may be views of one buffer.  dv_out and
+ *                 dv_seq may both be NULL.
+ * dq_weight, dk_weight : device [d], written; each may be NULL.  Summed in
+ *                 fp32 in an order that depends on the sizes alone.
+ * workspace     : device, >= ulysses_qkv_norm_rope_workspace_size(d) bytes.
+ * Calls that may run at the same time need workspaces of their own.
+ */
+uly_status ulysses_qkv_norm_rope_bwd(const void *q_seq, const void *k_seq, const void *q_weight,
+                                     const void *k_weight, const void *dq_out, const void *dk_out,
+                                     const void *dv_out, void *dq_seq, void *dk_seq, void *dv_seq,
+                                     void *dq_weight, void *dk_weight, int64_t B, int64_t N, int32_t Hq,
+                                     int32_t Hkv, int32_t d, int32_t P, int64_t q_stride, int64_t k_stride,
+                                     int64_t dq_stride, int64_t dk_stride, int64_t dv_stride,
+                                     const uly_rope_desc *rope_host, float eps, int32_t to_head,
+                                     uly_dtype dtype, void *workspace, size_t workspace_bytes, void *stream);
+
 /* ------------------------------------------------------------ attention */
 
 /*
@@ -343,6 +423,38 @@ uly_status ulysses_sharded_ce_loss(const void *logits, const int64_t *labels, vo
                                    float *shard_loss, int64_t *shard_good, float *total_loss,
                                    int64_t B, int64_t N, int32_t V, int32_t P, uly_dtype dtype,
                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The LM head and ulysses_sharded_ce_loss in one, without the logits: the
+ * same shifted labels, per-shard means and good-token-weighted total, of
+ *   logits[row][v] = <hidden[row], weight[v]>
+ * which are formed in pieces of at most 8192 rows with a label and never
+ * kept: a long sequence's logits and their gradient outweigh everything else
+ * the step holds (at 65,536 tokens and a vocabulary of 151,936, 20 GB each in
+ * bf16).  Rows without a label (ignored ones, and the last of each sequence)
+ * take no part: their hidden values are not read.
+ *
+ * hidden     : device, [P][B][N/P][D].      weight : device, [V][D].
+ * labels     : as in ulysses_sharded_ce_loss.
+ * dhidden    : device, like hidden, or NULL: d total / d hidden (0 on rows without a label).
+ * dweight    : device, like weight, or NULL: d total / d weight.
+ * shard_loss, shard_good, total_loss : as in ulysses_sharded_ce_loss.
+ * workspace  : device, >= ulysses_sharded_linear_ce_workspace_size(..., for_grad
+ *              = 1 if dhidden or dweight is given) bytes.  Calls that may run
+ *              at the same time need workspaces of their own.
+ * Products are accumulated in fp32; softmax and loss are fp32.  bf16: the
+ * gradient of the logits is rounded to bf16 as an operand of the two gradient
+ * products; each gradient is rounded to bf16 once.
+ * D * element size a multiple of 16 bytes, D <= 65536, V <= 2^21
+ * (ULY_ERR_UNSUPPORTED otherwise); N % P == 0.
+ */
+size_t ulysses_sharded_linear_ce_workspace_size(int64_t B, int64_t N, int32_t D, int32_t V, int32_t P,
+                                                int32_t for_grad, uly_dtype dtype);
+uly_status ulysses_sharded_linear_ce_loss(const void *hidden, const void *weight, const int64_t *labels,
+                                          void *dhidden, void *dweight, float *shard_loss, int64_t *shard_good,
+                                          float *total_loss, int64_t B, int64_t N, int32_t D, int32_t V,
+                                          int32_t P, uly_dtype dtype, void *workspace, size_t workspace_bytes,
+                                          void *stream);
 
 /* ------------------------------------------------------------ diagnostics */
 

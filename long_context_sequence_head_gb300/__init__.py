@@ -32,9 +32,11 @@ _STATUS = {0: "ULY_OK", 1: "ULY_ERR_INVALID_ARG", 2: "ULY_ERR_UNSUPPORTED", 3: "
 
 # every symbol include/ulysses.h declares
 EXPORTED = ("ulysses_seq_to_head", "ulysses_head_to_seq", "ulysses_swap_batch", "ulysses_attn_workspace_size",
+            "ulysses_qkv_norm_rope_workspace_size", "ulysses_qkv_norm_rope_fwd", "ulysses_qkv_norm_rope_bwd",
             "ulysses_attn_tile_order",
             "ulysses_attn_fwd", "ulysses_attn_bwd", "ulysses_attn_fwd_seq", "ulysses_attn_bwd_seq",
             "ulysses_attn_bwd_noalloc", "ulysses_sharded_ce_workspace_size", "ulysses_sharded_ce_loss",
+            "ulysses_sharded_linear_ce_workspace_size", "ulysses_sharded_linear_ce_loss",
             "ulysses_ring_attn_workspace_size", "ulysses_ring_attn_fwd", "ulysses_ring_attn_bwd",
             "ulysses_get_device_status",
             "ulysses_set_wait_limit_ns", "ulysses_selftest_wait_timeout", "ulysses_selftest_bounds",
@@ -95,6 +97,18 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.ulysses_sharded_ce_workspace_size.restype = sz
     lib.ulysses_sharded_ce_loss.argtypes = [vp] * 6 + [i64, i64, i32, i32, i32, vp, sz, vp]
     lib.ulysses_sharded_ce_loss.restype = i32
+    lib.ulysses_qkv_norm_rope_workspace_size.argtypes = [i32]
+    lib.ulysses_qkv_norm_rope_workspace_size.restype = sz
+    lib.ulysses_qkv_norm_rope_fwd.argtypes = ([vp] * 8 + [i64, i64, i32, i32, i32, i32] + [i64] * 3
+                                              + [vp, f32, i32, i32, vp])
+    lib.ulysses_qkv_norm_rope_fwd.restype = i32
+    lib.ulysses_qkv_norm_rope_bwd.argtypes = ([vp] * 12 + [i64, i64, i32, i32, i32, i32] + [i64] * 5
+                                              + [vp, f32, i32, i32, vp, sz, vp])
+    lib.ulysses_qkv_norm_rope_bwd.restype = i32
+    lib.ulysses_sharded_linear_ce_workspace_size.argtypes = [i64, i64, i32, i32, i32, i32, i32]
+    lib.ulysses_sharded_linear_ce_workspace_size.restype = sz
+    lib.ulysses_sharded_linear_ce_loss.argtypes = [vp] * 8 + [i64, i64, i32, i32, i32, i32, vp, sz, vp]
+    lib.ulysses_sharded_linear_ce_loss.restype = i32
     lib.ulysses_get_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.ulysses_set_wait_limit_ns.argtypes = [u64]
     lib.ulysses_selftest_wait_timeout.argtypes = [u64, vp]
@@ -331,6 +345,204 @@ def ulysses_all_to_all_head_to_seq(x_head: torch.Tensor, group=None, out: Option
     return ulysses_a2a_unpack(recv, P, out)
 
 
+# ------------------------------------- norm, rotation and move of Q, K, V
+
+class _RopeDesc(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("inv_freq_host", ctypes.c_void_p), ("axis_host", ctypes.c_void_p),
+                ("rot_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+def _rope_desc(inv_freq, positions, axis_of_freq, interleaved, shape):
+    """The host description of a rotation and the arrays it points to."""
+    inv = np.ascontiguousarray(np.asarray([] if inv_freq is None else inv_freq, dtype=np.float64))
+    if inv.ndim != 1:
+        raise ValueError(f"inv_freq must hold rot_dim/2 frequencies, got shape {inv.shape}")
+    axes, axis = 1, None
+    if positions is not None:
+        if positions.dtype != torch.int64:
+            raise ValueError(f"positions must be int64, got {positions.dtype}")
+        if tuple(positions.shape) == shape:
+            pass
+        elif positions.dim() == 4 and tuple(positions.shape[1:]) == shape:
+            axes = positions.shape[0]
+        else:
+            raise ValueError(f"positions must be {list(shape)} or [axes] + {list(shape)}, got {list(positions.shape)}")
+    if axis_of_freq is not None:
+        axis = np.ascontiguousarray(np.asarray(axis_of_freq, dtype=np.int32))
+        if axis.shape != inv.shape:
+            raise ValueError(f"axis_of_freq must name one axis per frequency, got shape {axis.shape}")
+    desc = _RopeDesc(positions.data_ptr() if positions is not None else None, inv.ctypes.data,
+                     axis.ctypes.data if axis is not None else None, 2 * len(inv), axes, int(bool(interleaved)))
+    return desc, (inv, axis)
+
+
+def _token_stride(name, t, d) -> int:
+    """Elements from one token to the next of a [P][B][N/P][H][d] tensor whose
+    heads are contiguous and whose tokens are evenly spaced, as a slice of
+    heads of a packed [P][B][N/P][Hq+2Hkv][d] projection output is."""
+    P, B, Np, H, dd = t.shape
+    sP, sB, sT, sH, sd = t.stride()
+    ok = dd == d and sd == 1 and (H == 1 or sH == d)
+    step = sT if Np > 1 else (sB if B > 1 else (sP if P > 1 else H * d))
+    if not (ok and (B == 1 or sB == Np * step) and (P == 1 or sP == B * Np * step)):
+        raise ValueError(f"{name}: heads must be contiguous and tokens evenly spaced, got strides {t.stride()}")
+    return step
+
+
+def _norm_rope_args(P, like, far, weights, to_head, positions):
+    """Checks shapes, types and devices before any pointer reaches the library.
+    like: (name, tensor or None, heads) in the sequence layout, q first; far:
+    the same on the other side; returns (B, Np, d)."""
+    q = like[0][1]
+    if q.dim() != 5:
+        raise ValueError(f"{like[0][0]} must be 5-D [P][B][N/P][H][d], got {tuple(q.shape)}")
+    if q.shape[0] != P:
+        raise ValueError(f"the leading dimension of {like[0][0]} must be P={P}, got {q.shape[0]}")
+    _, B, Np, _, d = q.shape
+    for name, t, H in like:
+        if t is not None and (tuple(t.shape) != (P, B, Np, H, d) or t.dtype != q.dtype):
+            raise ValueError(f"{name} must be {(P, B, Np, H, d)} of {q.dtype}, got {tuple(t.shape)} of {t.dtype}")
+    for name, t, H in far:
+        if to_head and H % P:
+            raise ValueError(f"the heads of {name} ({H}) must be a multiple of P={P}")
+        want = (P, B, Np * P, H // P, d) if to_head else (P, B, Np, H, d)
+        if t is not None and (tuple(t.shape) != want or t.dtype != q.dtype):
+            raise ValueError(f"{name} must be {want} of {q.dtype}, got {tuple(t.shape)} of {t.dtype}")
+    for name, t in weights:
+        if t is not None and (tuple(t.shape) != (d,) or t.dtype != q.dtype):
+            raise ValueError(f"{name} must be [{d}] of {q.dtype}, got {list(t.shape)} of {t.dtype}")
+    for t in [t for _, t, _ in like] + [t for _, t, _ in far] + [t for _, t in weights] + [positions]:
+        if t is not None:
+            _on(q, t)
+    for t in [t for _, t, _ in far] + [t for _, t in weights] + [positions]:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+    return B, Np, d
+
+
+def _on(first, t):
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    if t.device != first.device:
+        raise ValueError(f"all tensors must live on {first.device}, got {t.device}")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _Launch:
+    """The device and stream of a call: `with _Launch(device, stream) as s`
+    makes the tensors' device current and yields the raw stream; scratch()
+    hands out a workspace that the allocator keeps until that stream is done
+    with it."""
+
+    def __init__(self, device, stream):
+        if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+            raise ValueError(f"the stream must belong to {device}")
+        self.device, self.stream = device, stream
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def raw(self):
+        return _stream(self.stream)
+
+    def scratch(self, workspace, nbytes):
+        if workspace is not None:
+            if not workspace.is_cuda or workspace.device != self.device or not workspace.is_contiguous():
+                raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
+            return _workspace(workspace, nbytes, self.device)
+        return self.keep(_workspace(None, nbytes, self.device))
+
+    def keep(self, t):
+        """t, allocated on the current stream, not reused before the call's stream is done with it."""
+        if self.stream is not None:
+            t.record_stream(self.stream if isinstance(self.stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
+                int(self.stream), device=self.device))
+        return t
+
+
+def ulysses_qkv_norm_rope_workspace_size(d: int) -> int:
+    return int(load().ulysses_qkv_norm_rope_workspace_size(d))
+
+
+def ulysses_qkv_norm_rope_fwd(q_seq, k_seq, v_seq, q_out, k_out, v_out, P: int, inv_freq=None, q_weight=None,
+                              k_weight=None, positions: Optional[torch.Tensor] = None, axis_of_freq=None,
+                              interleaved: bool = False, eps: float = 1e-6, to_head: bool = True, stream=None):
+    """RMS norm of every Q and K head, rotary embedding and the seq->head move
+    of Q, K and V in one pass (see include/ulysses.h).
+
+    q_seq, k_seq, v_seq [P][B][N/P][H][d]: contiguous, or slices of the heads
+    of one packed projection output.  q_out, k_out, v_out: head layout
+    (to_head) or sequence layout, contiguous; v_seq and v_out may be None.
+    inv_freq: rot_dim/2 frequencies (None: no rotation); positions: int64
+    [P][B][N/P], or [axes][P][B][N/P] with axis_of_freq naming each
+    frequency's axis (None: the token's index).  q_weight and k_weight [d], or
+    None for both: no norm."""
+    Hq, Hkv = q_seq.shape[-2], k_seq.shape[-2]
+    if (v_seq is None) != (v_out is None) or (q_weight is None) != (k_weight is None):
+        raise ValueError("v_seq and v_out, and q_weight and k_weight, go together")
+    if q_out is None or k_out is None:
+        raise ValueError("q_out and k_out are required")
+    B, Np, d = _norm_rope_args(P, (("q_seq", q_seq, Hq), ("k_seq", k_seq, Hkv), ("v_seq", v_seq, Hkv)),
+                               (("q_out", q_out, Hq), ("k_out", k_out, Hkv), ("v_out", v_out, Hkv)),
+                               (("q_weight", q_weight), ("k_weight", k_weight)), to_head, positions)
+    desc, _keep = _rope_desc(inv_freq, positions, axis_of_freq, interleaved, (P, B, Np))
+    with _Launch(q_seq.device, stream) as at:
+        _check("ulysses_qkv_norm_rope_fwd", load().ulysses_qkv_norm_rope_fwd(
+            q_seq.data_ptr(), k_seq.data_ptr(), _ptr(v_seq), _ptr(q_weight), _ptr(k_weight), q_out.data_ptr(),
+            k_out.data_ptr(), _ptr(v_out), B, Np * P, Hq, Hkv, d, P, _token_stride("q_seq", q_seq, d),
+            _token_stride("k_seq", k_seq, d), 0 if v_seq is None else _token_stride("v_seq", v_seq, d),
+            ctypes.addressof(desc), float(eps), int(bool(to_head)), _dt(q_seq), at.raw()))
+    return q_out, k_out, v_out
+
+
+def ulysses_qkv_norm_rope_bwd(q_seq, k_seq, dq_out, dk_out, dv_out, dq_seq, dk_seq, dv_seq, P: int, inv_freq=None,
+                              q_weight=None, k_weight=None, dq_weight: Optional[torch.Tensor] = None,
+                              dk_weight: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                              axis_of_freq=None, interleaved: bool = False, eps: float = 1e-6, to_head: bool = True,
+                              workspace: Optional[torch.Tensor] = None, stream=None):
+    """Backward of ulysses_qkv_norm_rope_fwd: the gradients of its outputs in,
+    those of its inputs (and, if given, of the norm weights) out.  q_seq and
+    k_seq are the forward's inputs (None without a norm); dq_seq, dk_seq and
+    dv_seq may be slices of the heads of one packed buffer."""
+    norm = q_weight is not None
+    if (dv_seq is None) != (dv_out is None) or norm != (k_weight is not None):
+        raise ValueError("dv_seq and dv_out, and q_weight and k_weight, go together")
+    if norm and (q_seq is None or k_seq is None):
+        raise ValueError("the norm's backward needs q_seq and k_seq")
+    if not norm and (dq_weight is not None or dk_weight is not None):
+        raise ValueError("without norm weights there are no weight gradients")
+    Hq, Hkv = dq_seq.shape[-2], dk_seq.shape[-2]
+    if not norm:
+        q_seq = k_seq = None
+    B, Np, d = _norm_rope_args(P, (("dq_seq", dq_seq, Hq), ("dk_seq", dk_seq, Hkv), ("dv_seq", dv_seq, Hkv),
+                                   ("q_seq", q_seq, Hq), ("k_seq", k_seq, Hkv)),
+                               (("dq_out", dq_out, Hq), ("dk_out", dk_out, Hkv), ("dv_out", dv_out, Hkv)),
+                               (("q_weight", q_weight), ("k_weight", k_weight), ("dq_weight", dq_weight),
+                                ("dk_weight", dk_weight)), to_head, positions)
+    desc, _keep = _rope_desc(inv_freq, positions, axis_of_freq, interleaved, (P, B, Np))
+    with _Launch(dq_seq.device, stream) as at:
+        ws = at.scratch(workspace, ulysses_qkv_norm_rope_workspace_size(d)) if norm else None
+        _check("ulysses_qkv_norm_rope_bwd", load().ulysses_qkv_norm_rope_bwd(
+            _ptr(q_seq), _ptr(k_seq), _ptr(q_weight), _ptr(k_weight), dq_out.data_ptr(), dk_out.data_ptr(),
+            _ptr(dv_out), dq_seq.data_ptr(), dk_seq.data_ptr(), _ptr(dv_seq), _ptr(dq_weight), _ptr(dk_weight),
+            B, Np * P, Hq, Hkv, d, P, 0 if q_seq is None else _token_stride("q_seq", q_seq, d),
+            0 if k_seq is None else _token_stride("k_seq", k_seq, d), _token_stride("dq_seq", dq_seq, d),
+            _token_stride("dk_seq", dk_seq, d), 0 if dv_seq is None else _token_stride("dv_seq", dv_seq, d),
+            ctypes.addressof(desc), float(eps), int(bool(to_head)), _dt(dq_seq), _ptr(ws),
+            0 if ws is None else ws.numel() * ws.element_size(), at.raw()))
+    return dq_seq, dk_seq, dv_seq
+
+
 # -------------------------------------------------------------- attention
 
 def ulysses_attn_tile_order(N: int, causal: bool = True, cu_seqlens=None, for_bwd: bool = False) -> np.ndarray:
@@ -545,6 +757,59 @@ def ulysses_sharded_ce_loss(logits, labels, P: int, dlogits: Optional[torch.Tens
         logits.data_ptr(), labels.data_ptr(), dlogits.data_ptr() if dlogits is not None else None,
         shard_loss.data_ptr(), shard_good.data_ptr(), total.data_ptr(), B, N, V, P, _dt(logits),
         ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
+    return shard_loss, shard_good, total[:1]
+
+
+def ulysses_sharded_linear_ce_workspace_size(B: int, N: int, D: int, V: int, P: int, for_grad: bool,
+                                             dtype: torch.dtype) -> int:
+    dt = ULY_BF16 if dtype == torch.bfloat16 else ULY_FP32
+    return int(load().ulysses_sharded_linear_ce_workspace_size(B, N, D, V, P, int(bool(for_grad)), dt))
+
+
+def ulysses_sharded_linear_ce_loss(hidden, weight, labels, P: int, dhidden: Optional[torch.Tensor] = None,
+                                   dweight: Optional[torch.Tensor] = None,
+                                   workspace: Optional[torch.Tensor] = None, stream=None,
+                                   outputs: Optional[Sequence[torch.Tensor]] = None):
+    """The LM head and ulysses_sharded_ce_loss in one, without the logits.
+
+    hidden [P][B][N/P][D], weight [V][D] (bf16/fp32), labels [P][B][N/P] int64
+    (unshifted, -100 = ignored).  Returns (shard_loss [P] fp32, shard_good [P]
+    int64, total [1] fp32) on the device; fills dhidden (like hidden) and
+    dweight (like weight) if given.  `outputs` may supply those three tensors.
+    """
+    if hidden.dim() != 4 or hidden.shape[0] != P:
+        raise ValueError(f"hidden must be [P={P}][B][N/P][D], got {tuple(hidden.shape)}")
+    _, B, Np, D = hidden.shape
+    if weight.dim() != 2 or weight.shape[1] != D or weight.dtype != hidden.dtype:
+        raise ValueError(f"weight must be [V][{D}] of {hidden.dtype}, got {tuple(weight.shape)} of {weight.dtype}")
+    V = weight.shape[0]
+    if labels.dtype != torch.int64 or tuple(labels.shape) != (P, B, Np):
+        raise ValueError("labels must be int64 [P][B][N/P]")
+    for name, t, like in (("dhidden", dhidden, hidden), ("dweight", dweight, weight)):
+        if t is not None and (tuple(t.shape) != tuple(like.shape) or t.dtype != like.dtype):
+            raise ValueError(f"{name} must be {tuple(like.shape)} of {like.dtype}, got {tuple(t.shape)} of {t.dtype}")
+    if outputs is not None:
+        shard_loss, shard_good, total = outputs
+        if (shard_loss.dtype != torch.float32 or shard_loss.numel() != P or shard_good.dtype != torch.int64
+                or shard_good.numel() != P or total.dtype != torch.float32 or total.numel() < 1):
+            raise ValueError("outputs must be (fp32 [P], int64 [P], fp32 [>=1])")
+    for t in (hidden, weight, labels, dhidden, dweight) + tuple(outputs or ()):
+        if t is not None:
+            _on(hidden, t)
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous")
+    dev, grad = hidden.device, dhidden is not None or dweight is not None
+    with _Launch(dev, stream) as at:
+        if outputs is None:
+            shard_loss = at.keep(torch.empty(P, dtype=torch.float32, device=dev))
+            shard_good = at.keep(torch.empty(P, dtype=torch.int64, device=dev))
+            total = at.keep(torch.empty(4, dtype=torch.float32, device=dev))
+        need = ulysses_sharded_linear_ce_workspace_size(B, Np * P, D, V, P, grad, hidden.dtype)
+        ws = at.scratch(workspace, need)
+        _check("ulysses_sharded_linear_ce_loss", load().ulysses_sharded_linear_ce_loss(
+            hidden.data_ptr(), weight.data_ptr(), labels.data_ptr(), _ptr(dhidden), _ptr(dweight),
+            shard_loss.data_ptr(), shard_good.data_ptr(), total.data_ptr(), B, Np * P, D, V, P, _dt(hidden),
+            ws.data_ptr(), ws.numel() * ws.element_size(), at.raw()))
     return shard_loss, shard_good, total[:1]
 
 

@@ -192,11 +192,56 @@ cudaError_t launch_attn_bwd_bf16(const AttnShape &s, const void *q, const void *
 
 cudaError_t launch_selftest_timeout(uint64_t limit_ns, cudaStream_t stream);
 
+// -------------------------------------------- norm, rotation and move of Q, K, V
+// Most blocks of a backward launch, and so most weight-gradient partials.
+constexpr int kNormRopeMaxBlocks = 1280;
+constexpr int kNormRopeMaxHalf = 64;
+
+struct NormRopeParams {
+    // near side: the sequence layout, token strides in elements.  The backward
+    // reads q and k for the norm; v only tells it that there is a V.
+    const void *q, *k, *v;
+    int64_t qs, ks, vs;
+    // far side: outputs of the forward, gradients read by the backward
+    void *qo, *ko, *vo;
+    // backward: gradients of q, k and v, token strides in elements
+    void *dq, *dk, *dv;
+    int64_t dqs, dks, dvs;
+    const void *wq, *wk;  // norm weights [d], both or neither
+    void *dwq, *dwk;      // their gradients, each may be null
+    float *partial;       // [blocks][2][d]
+    const int64_t *positions;  // [axes][P][B][N/P] or null
+    int64_t tokens;            // P * B * N/P
+    int64_t N;
+    int Np, B;  // tokens per shard, sequences
+    int Hq, Hkv, Hqp, Hkvp;
+    int to_head;
+    int half;  // rot / 2
+    float eps;
+    int splits, rows_per_split;  // set by the launch
+    uint64_t turn[kNormRopeMaxHalf];  // inv_freq / 2 pi as a 64-bit fraction of a turn
+    uint8_t axis[kNormRopeMaxHalf];
+};
+uint64_t turn_fraction(double inv_freq);
+cudaError_t launch_norm_rope(NormRopeParams &p, int d, bool inter, bool bwd, int esize, cudaStream_t s);
+
 // ------------------------------------------------------- sharded loss
 cudaError_t launch_sharded_ce(const void *logits, const int64_t *labels, void *dlogits, float *shard_loss,
                               int64_t *shard_good, float *total, int64_t B, int64_t N, int64_t V, int P, int esize,
                               void *workspace, cudaStream_t stream);
 size_t sharded_ce_workspace(int64_t B, int64_t N, int P);
+// Its first and last steps: labels shifted over the whole sequence with each
+// shard's good-token count, and the shards' means with their total.
+cudaError_t launch_shift_count(const int64_t *labels, int32_t *shifted, unsigned long long *good, int64_t B, int64_t N,
+                               int P, int64_t V, cudaStream_t stream);
+cudaError_t launch_shard_totals(const float *row_loss, const unsigned long long *good, float *shard_loss,
+                                int64_t *shard_good, float *total, int64_t B, int64_t N, int P, cudaStream_t stream);
+
+// ------------------------------------------ LM head and sharded loss in one
+cudaError_t launch_sharded_linear_ce(const void *hidden, const void *weight, const int64_t *labels, void *dhidden,
+                                     void *dweight, float *shard_loss, int64_t *shard_good, float *total, int64_t B,
+                                     int64_t N, int D, int V, int P, int esize, void *workspace, cudaStream_t stream);
+size_t sharded_linear_ce_workspace(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize);
 
 }  // namespace uly
 

@@ -4,6 +4,7 @@
 #include <ulysses.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -163,6 +164,88 @@ uly_status check_swap_args(const void *a, const void *b, int64_t B, int64_t N, i
 
 uly_status from_cuda(cudaError_t e) { return e == cudaSuccess ? ULY_OK : ULY_ERR_CUDA; }
 
+// A tensor's rows: `rows` runs of `width` bytes, `pitch` bytes apart.
+struct Rows {
+    const void *p;
+    int64_t rows, width, pitch;
+};
+
+// Rows that share a byte.  Two views with a common pitch (columns of one
+// buffer) may interleave; otherwise their whole ranges must be apart.
+bool rows_overlap(const Rows &a, const Rows &b)
+{
+    if (a.p == nullptr || b.p == nullptr ||
+        !overlap(a.p, (a.rows - 1) * a.pitch + a.width, b.p, (b.rows - 1) * b.pitch + b.width))
+        return false;
+    if (a.pitch != b.pitch)
+        return true;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    // where the later view starts within the earlier one's row
+    const int64_t col = static_cast<int64_t>(x < y ? y - x : x - y) % a.pitch;
+    const int64_t first = x < y ? a.width : b.width, second = x < y ? b.width : a.width;
+    return col < first || col + second > a.pitch;
+}
+
+// Sizes and rotation shared by ulysses_qkv_norm_rope_fwd and _bwd; fills p.
+uly_status check_norm_rope(uly::NormRopeParams &p, int64_t B, int64_t N, int32_t Hq, int32_t Hkv, int32_t d, int32_t P,
+                           const uly_rope_desc *rope, float eps, int32_t to_head, uly_dtype dt)
+{
+    if (rope == nullptr || B < 1 || N < 1 || P < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || N % P != 0 ||
+        (to_head != 0 && to_head != 1) || esize_of(dt) == 0 || !(eps >= 0.f) || !std::isfinite(eps))
+        return ULY_ERR_INVALID_ARG;
+    if (to_head && (Hq % P != 0 || Hkv % P != 0))
+        return ULY_ERR_INVALID_ARG;
+    if (d != 64 && d != 128)
+        return ULY_ERR_UNSUPPORTED;
+    if (N > (int64_t(1) << 31) - 1 || B > (int64_t(1) << 31) - 1 || B * N > (int64_t(1) << 31) - 1 || Hq > 65536)
+        return ULY_ERR_UNSUPPORTED;
+    if (rope->rot_dim < 0 || rope->rot_dim > d || rope->num_axes < 1 || rope->num_axes > 8 ||
+        (rope->interleaved != 0 && rope->interleaved != 1) || (rope->rot_dim > 0 && rope->inv_freq_host == nullptr))
+        return ULY_ERR_INVALID_ARG;
+    if (rope->rot_dim % 16 != 0)
+        return ULY_ERR_UNSUPPORTED;
+    p.half = rope->rot_dim / 2;
+    for (int f = 0; f < p.half; ++f) {
+        const int32_t axis = rope->axis_host ? rope->axis_host[f] : 0;
+        if (!std::isfinite(rope->inv_freq_host[f]) || axis < 0 || axis >= rope->num_axes)
+            return ULY_ERR_INVALID_ARG;
+        p.turn[f] = uly::turn_fraction(rope->inv_freq_host[f]);
+        p.axis[f] = static_cast<uint8_t>(axis);
+    }
+    if (reinterpret_cast<uintptr_t>(rope->positions) % 8 != 0)
+        return ULY_ERR_MISALIGNED;
+    p.positions = rope->positions;
+    p.tokens = B * N;
+    p.N = N;
+    p.Np = static_cast<int>(N / P);
+    p.B = static_cast<int>(B);
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.Hqp = to_head ? Hq / P : Hq;
+    p.Hkvp = to_head ? Hkv / P : Hkv;
+    p.to_head = to_head;
+    p.eps = eps;
+    return ULY_OK;
+}
+
+uly_status check_linear_ce(int64_t B, int64_t N, int32_t D, int32_t V, int32_t P, uly_dtype dt)
+{
+    if (B < 1 || N < 1 || D < 1 || V < 1 || P < 1 || N % P != 0 || esize_of(dt) == 0)
+        return ULY_ERR_INVALID_ARG;
+    const int64_t most = (int64_t(1) << 31) - 1;
+    if (B > most || N > most || B * N > most || D > 65536 || V > (1 << 21) || D * esize_of(dt) % 16 != 0)
+        return ULY_ERR_UNSUPPORTED;
+    return ULY_OK;
+}
+
+// A token stride in elements (0: contiguous); false if it is too small or not a multiple of 16 bytes.
+bool token_stride(int64_t given, int H, int d, int es, int64_t &out)
+{
+    const int64_t least = static_cast<int64_t>(H) * d;
+    out = given == 0 ? least : given;
+    return out >= least && out <= (int64_t(1) << 32) && out * es % 16 == 0;
+}
+
 }  // namespace
 
 namespace uly {
@@ -282,6 +365,111 @@ uly_status ulysses_swap_batch(const uly_swap_desc *descs_host, int32_t n_descs, 
     if (uly::tensor_map_encoder() == nullptr || uly::device_status_ptr() == nullptr)
         return ULY_ERR_CUDA;
     return from_cuda(uly::launch_swap_batch(descs, n_descs, B, N, d, P, es, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ulysses_qkv_norm_rope_workspace_size(int32_t d)
+{
+    if (d != 64 && d != 128)
+        return 0;
+    return sizeof(float) * 2 * static_cast<size_t>(d) * uly::kNormRopeMaxBlocks;
+}
+
+uly_status ulysses_qkv_norm_rope_fwd(const void *q_seq, const void *k_seq, const void *v_seq, const void *q_weight,
+                                     const void *k_weight, void *q_out, void *k_out, void *v_out, int64_t B, int64_t N,
+                                     int32_t Hq, int32_t Hkv, int32_t d, int32_t P, int64_t q_stride,
+                                     int64_t k_stride, int64_t v_stride, const uly_rope_desc *rope_host, float eps,
+                                     int32_t to_head, uly_dtype dtype, void *stream)
+{
+    ULY_NVTX_RANGE();
+    if (!q_seq || !k_seq || !q_out || !k_out || (v_seq == nullptr) != (v_out == nullptr) ||
+        (q_weight == nullptr) != (k_weight == nullptr))
+        return ULY_ERR_INVALID_ARG;
+    uly::NormRopeParams p = {};
+    const uly_status st = check_norm_rope(p, B, N, Hq, Hkv, d, P, rope_host, eps, to_head, dtype);
+    if (st != ULY_OK)
+        return st;
+    const int es = esize_of(dtype);
+    if (!token_stride(q_stride, Hq, d, es, p.qs) || !token_stride(k_stride, Hkv, d, es, p.ks) ||
+        !token_stride(v_stride, Hkv, d, es, p.vs))
+        return ULY_ERR_INVALID_ARG;
+    const void *ptrs[8] = {q_seq, k_seq, v_seq, q_weight, k_weight, q_out, k_out, v_out};
+    for (const void *x : ptrs)
+        if (!aligned16(x))
+            return ULY_ERR_MISALIGNED;
+    const int64_t T = p.tokens, wq = static_cast<int64_t>(Hq) * d * es, wk = static_cast<int64_t>(Hkv) * d * es,
+                  wd = static_cast<int64_t>(d) * es;
+    const Rows in[6] = {{q_seq, T, wq, p.qs * es},  {k_seq, T, wk, p.ks * es},
+                        {v_seq, T, wk, p.vs * es},  {q_weight, 1, wd, wd},
+                        {k_weight, 1, wd, wd},      {p.positions, 1, T * 8 * rope_host->num_axes, 1}};
+    const Rows out[3] = {{q_out, 1, T * wq, 1}, {k_out, 1, T * wk, 1}, {v_out, 1, T * wk, 1}};
+    for (int i = 0; i < 3; ++i) {
+        for (const Rows &x : in)
+            if (rows_overlap(out[i], x))
+                return ULY_ERR_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (rows_overlap(out[i], out[j]))
+                return ULY_ERR_OVERLAP;
+    }
+    p.q = q_seq, p.k = k_seq, p.v = v_seq, p.wq = q_weight, p.wk = k_weight;
+    p.qo = q_out, p.ko = k_out, p.vo = v_out;
+    return from_cuda(uly::launch_norm_rope(p, d, rope_host->interleaved != 0, false, es,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+uly_status ulysses_qkv_norm_rope_bwd(const void *q_seq, const void *k_seq, const void *q_weight, const void *k_weight,
+                                     const void *dq_out, const void *dk_out, const void *dv_out, void *dq_seq,
+                                     void *dk_seq, void *dv_seq, void *dq_weight, void *dk_weight, int64_t B,
+                                     int64_t N, int32_t Hq, int32_t Hkv, int32_t d, int32_t P, int64_t q_stride,
+                                     int64_t k_stride, int64_t dq_stride, int64_t dk_stride, int64_t dv_stride,
+                                     const uly_rope_desc *rope_host, float eps, int32_t to_head, uly_dtype dtype,
+                                     void *workspace, size_t workspace_bytes, void *stream)
+{
+    ULY_NVTX_RANGE();
+    const bool norm = q_weight != nullptr;
+    if (!dq_out || !dk_out || !dq_seq || !dk_seq || (dv_out == nullptr) != (dv_seq == nullptr) ||
+        norm != (k_weight != nullptr) || (norm && (!q_seq || !k_seq || !workspace)) ||
+        (!norm && (dq_weight || dk_weight)))
+        return ULY_ERR_INVALID_ARG;
+    uly::NormRopeParams p = {};
+    const uly_status st = check_norm_rope(p, B, N, Hq, Hkv, d, P, rope_host, eps, to_head, dtype);
+    if (st != ULY_OK)
+        return st;
+    const int es = esize_of(dtype);
+    if (!token_stride(q_stride, Hq, d, es, p.qs) || !token_stride(k_stride, Hkv, d, es, p.ks) ||
+        !token_stride(dq_stride, Hq, d, es, p.dqs) || !token_stride(dk_stride, Hkv, d, es, p.dks) ||
+        !token_stride(dv_stride, Hkv, d, es, p.dvs))
+        return ULY_ERR_INVALID_ARG;
+    if (!norm)
+        q_seq = k_seq = nullptr;
+    const void *ptrs[13] = {q_seq,  k_seq,  q_weight, k_weight,  dq_out,    dk_out,   dv_out,
+                            dq_seq, dk_seq, dv_seq,   dq_weight, dk_weight, workspace};
+    for (const void *x : ptrs)
+        if (!aligned16(x))
+            return ULY_ERR_MISALIGNED;
+    const int64_t T = p.tokens, wq = static_cast<int64_t>(Hq) * d * es, wk = static_cast<int64_t>(Hkv) * d * es,
+                  wd = static_cast<int64_t>(d) * es;
+    const int64_t ws = static_cast<int64_t>(ulysses_qkv_norm_rope_workspace_size(d));
+    const Rows in[8] = {{q_seq, T, wq, p.qs * es}, {k_seq, T, wk, p.ks * es}, {q_weight, 1, wd, wd},
+                        {k_weight, 1, wd, wd},     {dq_out, 1, T * wq, 1},    {dk_out, 1, T * wk, 1},
+                        {dv_out, 1, T * wk, 1},    {p.positions, 1, T * 8 * rope_host->num_axes, 1}};
+    const Rows out[6] = {{dq_seq, T, wq, p.dqs * es}, {dk_seq, T, wk, p.dks * es}, {dv_seq, T, wk, p.dvs * es},
+                         {dq_weight, 1, wd, wd},      {dk_weight, 1, wd, wd},      {norm ? workspace : nullptr, 1, ws, 1}};
+    for (int i = 0; i < 6; ++i) {
+        for (const Rows &x : in)
+            if (rows_overlap(out[i], x))
+                return ULY_ERR_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (rows_overlap(out[i], out[j]))
+                return ULY_ERR_OVERLAP;
+    }
+    if (norm && workspace_bytes < static_cast<size_t>(ws))
+        return ULY_ERR_WORKSPACE;
+    p.q = q_seq, p.k = k_seq, p.v = dv_out, p.wq = q_weight, p.wk = k_weight;
+    p.qo = const_cast<void *>(dq_out), p.ko = const_cast<void *>(dk_out), p.vo = const_cast<void *>(dv_out);
+    p.dq = dq_seq, p.dk = dk_seq, p.dv = dv_seq, p.dwq = dq_weight, p.dwk = dk_weight;
+    p.partial = static_cast<float *>(workspace);
+    return from_cuda(uly::launch_norm_rope(p, d, rope_host->interleaved != 0, true, es,
+                                           static_cast<cudaStream_t>(stream)));
 }
 
 uly_status ulysses_attn_tile_order(int64_t N, int32_t causal, const int32_t *cu_seqlens_host, int32_t num_docs,
@@ -604,6 +792,53 @@ uly_status ulysses_sharded_ce_loss(const void *logits, const int64_t *labels, vo
         return ULY_ERR_CUDA;
     return from_cuda(uly::launch_sharded_ce(logits, labels, dlogits, shard_loss, shard_good, total_loss, B, N, V, P,
                                             esize_of(dtype), workspace, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ulysses_sharded_linear_ce_workspace_size(int64_t B, int64_t N, int32_t D, int32_t V, int32_t P,
+                                                int32_t for_grad, uly_dtype dtype)
+{
+    if (check_linear_ce(B, N, D, V, P, dtype) != ULY_OK || (for_grad != 0 && for_grad != 1))
+        return 0;
+    return uly::sharded_linear_ce_workspace(B, N, D, V, P, for_grad != 0, esize_of(dtype));
+}
+
+uly_status ulysses_sharded_linear_ce_loss(const void *hidden, const void *weight, const int64_t *labels, void *dhidden,
+                                          void *dweight, float *shard_loss, int64_t *shard_good, float *total_loss,
+                                          int64_t B, int64_t N, int32_t D, int32_t V, int32_t P, uly_dtype dtype,
+                                          void *workspace, size_t workspace_bytes, void *stream)
+{
+    ULY_NVTX_RANGE();
+    if (!hidden || !weight || !labels || !shard_loss || !shard_good || !total_loss || !workspace)
+        return ULY_ERR_INVALID_ARG;
+    const uly_status st = check_linear_ce(B, N, D, V, P, dtype);
+    if (st != ULY_OK)
+        return st;
+    const int es = esize_of(dtype);
+    const size_t need = uly::sharded_linear_ce_workspace(B, N, D, V, P, dhidden || dweight, es);
+    const int64_t hb = B * N * D * es, wb = static_cast<int64_t>(V) * D * es;
+    const Rows all[9] = {{hidden, 1, hb, 1},
+                         {weight, 1, wb, 1},
+                         {labels, 1, B * N * 8, 1},
+                         {dhidden, 1, hb, 1},
+                         {dweight, 1, wb, 1},
+                         {shard_loss, 1, static_cast<int64_t>(P) * 4, 1},
+                         {shard_good, 1, static_cast<int64_t>(P) * 8, 1},
+                         {total_loss, 1, 4, 1},
+                         {workspace, 1, static_cast<int64_t>(need), 1}};
+    for (const Rows &x : all)
+        if (!aligned16(x.p))
+            return ULY_ERR_MISALIGNED;
+    for (int i = 3; i < 9; ++i)  // what is written
+        for (int j = 0; j < i; ++j)
+            if (rows_overlap(all[i], all[j]))
+                return ULY_ERR_OVERLAP;
+    if (workspace_bytes < need)
+        return ULY_ERR_WORKSPACE;
+    if (uly::tensor_map_encoder() == nullptr || uly::device_status_ptr() == nullptr)
+        return ULY_ERR_CUDA;
+    return from_cuda(uly::launch_sharded_linear_ce(hidden, weight, labels, dhidden, dweight, shard_loss, shard_good,
+                                                   total_loss, B, N, D, V, P, es, workspace,
+                                                   static_cast<cudaStream_t>(stream)));
 }
 
 uly_status ulysses_get_device_status(void *stream, uint32_t *site_out)

@@ -1,0 +1,256 @@
+"""The LM head and sharded loss in one, on the GPU against the fp64 oracle.
+
+Tolerances count roundings, u = 2^-24.  A product over K terms in fp32 is off
+by at most 2 K u of the sum of its absolute terms (2: an accumulation may
+truncate).  So a logit is off by d_r <= 2 D u max_v <|h_r|, |w_v|>, a
+probability by the factor exp(2 d_r) and a row's loss by 2 d_r, plus 32 u of
+the values themselves (exponential, sums of tile partials, logarithm).  The
+gradient of the logits, g, is rounded for the products: in bf16 twice (e to
+fp16, 2^-11, or 2^-25 of its tile's largest; g to bf16, 2^-8), in fp32 by less
+than 8 u.  Each gradient adds its product's error and its own rounding.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle.norm_rope as nr
+from oracle import shift_labels_batched
+from parity_utils import REL_TOL, Guards, bytes_equal, log_errors, rel_fro
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+def make(P, B, N, D, V, dtype, ignore=0.2, lean=8.0, seed=0, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    w = (torch.randn(V, D, generator=g) / D ** 0.5 * scale).to(dtype)
+    labels = torch.randint(0, V, (B, N), generator=g)
+    h = torch.randn(B, N, D, generator=g)
+    h = h + lean * torch.rand(B, N, 1, generator=g) * w[labels.roll(-1, 1)].float()
+    labels[torch.rand(B, N, generator=g) < ignore] = -100
+    shard = lambda t: t.reshape(B, P, N // P, *t.shape[2:]).transpose(0, 1).contiguous()
+    return shard(h.to(dtype)), w, shard(labels)
+
+
+def full(x):
+    return x.transpose(0, 1).reshape(x.shape[1], -1, *x.shape[3:])
+
+
+def run(uly, h, w, labels, dh=True, dw=True, **more):
+    g = Guards()
+    P, B, Np, D = h.shape
+    outs = (g.empty((P,), FP32, float("nan")), g.empty((P,), torch.int64), g.empty((1,), FP32, float("nan")))
+    grads = [g.empty(t.shape, t.dtype, float("nan")) if on else None for t, on in ((h, dh), (w, dw))]
+    need = uly.ulysses_sharded_linear_ce_workspace_size(B, Np * P, D, w.shape[0], P, dh or dw, h.dtype)
+    ws = g.workspace(need)
+    ws.fill_(0xFF)  # NaN in every type where nothing is written
+    uly.ulysses_sharded_linear_ce_loss(h.cuda(), w.cuda(), labels.cuda(), P, dhidden=grads[0], dweight=grads[1],
+                                       workspace=ws, outputs=outs, **more)
+    torch.cuda.synchronize()
+    g.check()
+    return outs, grads
+
+
+def compare(outs, grads, h, w, labels, what, norm=True):
+    P = h.shape[0]
+    h64, w64 = full(h).double().numpy(), w.double().numpy()
+    sh = shift_labels_batched(full(labels).numpy())
+    per, counts, total, dh, dw, g = nr.linear_ce(h64, w64, sh, P)
+    sl, sg, tot = (t.cpu().double().numpy() for t in outs)
+    assert sg.astype(np.int64).tolist() == counts.tolist()
+    good = (sh != -100).reshape(-1)
+    rows = np.where(good[:, None], h64.reshape(-1, h64.shape[-1]), 0.0)
+    D, V = w64.shape[1], w64.shape[0]
+    size = (np.abs(rows) @ np.abs(w64).T).max(1)          # of a logit's terms
+    d = 2 * D * U * size                                  # of a logit
+    tol_row = 2 * d + 32 * U * (1 + size)
+    tol_loss = tol_row[good].max() if good.any() else 0.0
+    assert np.abs(sl - per).max() <= tol_loss + 2 * U * np.abs(per).max(), (what, sl, per, tol_loss)
+    assert abs(tot[0] - total) <= tol_loss + 4 * U * abs(total), (what, tot, total, tol_loss)
+    T = max(int(good.sum()), 1)
+    y = sh.reshape(-1)
+    p = np.abs(g * T)
+    p[np.arange(len(y))[good], y[good]] = 1 - p[good, y[good]]
+    half = torch.finfo(h.dtype).eps / 2
+    tag = "bf16" if h.dtype == BF16 else "fp32"
+    rounded = (2.0 ** -8 + 2.0 ** -11) if tag == "bf16" else 8 * U
+    # g's error: the probability's, then its rounding
+    dg = (p * np.expm1(2 * d + 16 * U)[:, None] + (2.0 ** -25 if tag == "bf16" else 0.0) * good[:, None]) / T
+    dg += rounded * (np.abs(g) + dg)
+    errs = {}
+    for name, got, ref, side in (("dh", grads[0], dh.reshape(-1, D), lambda q: q @ np.abs(w64)),
+                                 ("dw", grads[1], dw, lambda q: q.T @ np.abs(rows))):
+        if got is None:
+            continue
+        got = (full(got.cpu()) if name == "dh" else got.cpu()).double().numpy().reshape(ref.shape)
+        K = V if name == "dh" else T
+        before = side(dg) + 2 * K * U * side(np.abs(g) + dg)
+        tol = half * (np.abs(ref) + before) + before + 2.0 ** -133  # the last: below the smallest subnormal step
+        assert np.isfinite(got).all(), (what, name)
+        over = np.abs(got - ref) - tol
+        assert (over <= 0).all(), (what, name, float(over.max()), np.unravel_index(over.argmax(), over.shape))
+        errs[name] = rel_fro(got, ref)
+        if norm and np.linalg.norm(ref) > 0:
+            assert errs[name] <= REL_TOL[tag], (what, name, errs[name])
+    log_errors(f"linear ce {what} {tag}", total=abs(tot[0] - total), **errs)
+
+
+CASES = [
+    # P, B, N, D, V, dtype
+    (1, 1, 2, 8, 1, BF16),          # one row, one word: loss 0
+    (1, 1, 2, 8, 3, FP32),
+    (2, 1, 64, 64, 100, BF16),
+    (4, 2, 64, 128, 1000, BF16),
+    (4, 2, 64, 128, 1000, FP32),
+    (3, 1, 99, 72, 257, BF16),      # nothing a multiple of a tile
+    (2, 3, 150, 200, 513, BF16),
+    (1, 1, 300, 100, 255, FP32),
+    (1, 2, 260, 520, 777, FP32),
+    (2, 1, 700, 264, 2049, BF16),   # several row tiles, column tiles and products of 64
+    (1, 1, 65, 1032, 4099, BF16),
+    (1, 1, 513, 256, 256, BF16),    # whole tiles and one row more
+]
+
+
+@pytest.mark.parametrize("P,B,N,D,V,dtype", CASES)
+def test_loss_and_gradients(uly, P, B, N, D, V, dtype):
+    h, w, labels = make(P, B, N, D, V, dtype, seed=N + V)
+    outs, grads = run(uly, h, w, labels)
+    assert uly.ulysses_get_device_status()[0] == 0
+    compare(outs, grads, h, w, labels, f"P{P} B{B} N{N} D{D} V{V}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_one_gradient_or_none_gives_the_same_results(uly, dtype):
+    h, w, labels = make(2, 1, 130, 136, 700, dtype, seed=5)
+    outs, grads = run(uly, h, w, labels)
+    for dh, dw in ((True, False), (False, True), (False, False)):
+        o2, g2 = run(uly, h, w, labels, dh=dh, dw=dw)
+        assert all(bytes_equal(a, b) for a, b in zip(outs, o2))
+        for a, b in zip(grads, g2):
+            assert b is None or bytes_equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_no_label_at_all(uly, dtype):
+    h, w, labels = make(2, 1, 40, 64, 300, dtype, ignore=0.0)
+    labels[:] = -100
+    h[:] = float("nan")  # rows without a label are not read
+    outs, grads = run(uly, h, w, labels)
+    assert outs[0].cpu().tolist() == [0, 0] and outs[1].cpu().tolist() == [0, 0] and float(outs[2]) == 0.0
+    assert float(grads[0].abs().max()) == 0.0 and float(grads[1].abs().max()) == 0.0
+    assert uly.ulysses_get_device_status()[0] == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_nan_rows_without_a_label_touch_nothing(uly, dtype):
+    P, B, N = 2, 2, 90
+    h, w, labels = make(P, B, N, 72, 333, dtype, ignore=0.4, seed=9)
+    sh = torch.from_numpy(shift_labels_batched(full(labels).numpy())).reshape(B, P, N // P).transpose(0, 1)
+    clean_outs, clean = run(uly, h, w, labels)
+    h2 = h.clone()
+    h2[sh == -100] = float("nan")
+    outs, grads = run(uly, h2, w, labels)
+    assert all(bytes_equal(a, b) for a, b in zip(list(clean_outs) + clean, list(outs) + grads))
+    assert float(grads[0].cpu()[sh == -100].abs().max()) == 0.0
+
+
+def test_a_shard_without_labels_and_invalid_labels(uly):
+    h, w, labels = make(4, 1, 64, 64, 100, BF16, ignore=0.0, seed=11)
+    labels[1] = -100
+    labels[2, 0, 0] = -100  # the target of shard 1's last token
+    outs, grads = run(uly, h, w, labels)
+    assert uly.ulysses_get_device_status()[0] == 0
+    assert outs[1].cpu().tolist()[1] == 0
+    compare(outs, grads, h, w, labels, "empty shard")
+    bad = labels.clone()
+    bad[0, 0, 5] = 100  # out of range: ignored and reported
+    bad[3, 0, 5] = -7
+    outs, grads = run(uly, h, w, bad)
+    assert uly.ulysses_get_device_status()[0] == 1
+    bad[0, 0, 5] = bad[3, 0, 5] = -100
+    compare(outs, grads, h, w, bad, "invalid labels")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_large_logits_and_certain_rows(uly, dtype):
+    """Logits in the hundreds: the maximum is taken out before any exponential; p reaches 1 and 0.
+    A logit's own rounding moves a probability by percents there, so only the element-wise bound holds."""
+    h, w, labels = make(1, 1, 80, 64, 600, dtype, lean=40.0, seed=13, scale=8.0)
+    outs, grads = run(uly, h, w, labels)
+    compare(outs, grads, h, w, labels, "large logits", norm=False)
+    h, w, labels = make(1, 1, 80, 64, 600, dtype, lean=0.0, seed=14, scale=30.0)
+    outs, grads = run(uly, h, w, labels)
+    compare(outs, grads, h, w, labels, "large logits, wrong labels", norm=False)
+
+
+@pytest.mark.parametrize("rows,dtype", [(8192, BF16), (8193, BF16), (8194, BF16), (20000, BF16), (9000, FP32)])
+def test_pieces(uly, rows, dtype):
+    """More rows with labels than one piece holds; the last row of a sequence has none."""
+    h, w, labels = make(1, 1, rows, 24, 70, dtype, ignore=0.0, seed=rows)
+    outs, grads = run(uly, h, w, labels)
+    compare(outs, grads, h, w, labels, f"{rows} rows")
+    # enough rows for three pieces, labels for one
+    if rows == 20000:
+        labels[:, :, 2000:] = -100
+        outs, grads = run(uly, h, w, labels)
+        compare(outs, grads, h, w, labels, "one piece of three")
+
+
+def test_same_bits_on_every_run_and_stream_and_graph(uly):
+    h, w, labels = make(2, 2, 300, 264, 1111, BF16, seed=21)
+    outs, grads = run(uly, h, w, labels)
+    want = list(outs) + grads
+    for _ in range(2):
+        o, g = run(uly, h, w, labels)
+        assert all(bytes_equal(a, b) for a, b in zip(want, list(o) + g))
+    P, B, Np, D = h.shape
+    hc, wc, lc = h.cuda(), w.cuda(), labels.cuda()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    dh, dw = torch.empty_like(hc), torch.empty_like(wc)
+    got = uly.ulysses_sharded_linear_ce_loss(hc, wc, lc, P, dhidden=dh, dweight=dw, stream=side)
+    side.synchronize()
+    assert all(bytes_equal(a, b) for a, b in zip(want, list(got) + [dh, dw]))
+    ws = torch.empty(uly.ulysses_sharded_linear_ce_workspace_size(B, Np * P, D, len(w), P, True, BF16),
+                     dtype=torch.uint8, device="cuda")
+    held, lab = torch.zeros_like(hc), torch.full_like(lc, -100)
+    out = (torch.empty(P, device="cuda"), torch.empty(P, dtype=torch.int64, device="cuda"),
+           torch.empty(1, device="cuda"))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        uly.ulysses_sharded_linear_ce_loss(held, wc, lab, P, dhidden=dh, dweight=dw, workspace=ws, outputs=out)
+    held.copy_(hc)
+    lab.copy_(lc)  # the number of good rows is read on the device
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(bytes_equal(a, b) for a, b in zip(want, list(out) + [dh, dw]))
+
+
+def test_agrees_with_the_loss_over_kept_logits(uly):
+    """The same total as ulysses_sharded_ce_loss on logits formed first (fp32)."""
+    h, w, labels = make(4, 1, 128, 64, 500, FP32, seed=31)
+    outs, _ = run(uly, h, w, labels, dh=False, dw=False)
+    logits = (h.double() @ w.double().T).float().cuda()
+    sl, sg, tot = uly.ulysses_sharded_ce_loss(logits, labels.cuda(), 4)
+    torch.cuda.synchronize()
+    assert bytes_equal(outs[1], sg)
+    assert abs(float(outs[2]) - float(tot)) <= 1e-5 * float(tot)
+
+
+def _random_cases(n, seed=77):
+    rng = np.random.default_rng(seed)
+    out = []
+    for _ in range(n):
+        P = int(rng.choice([1, 2, 3, 4]))
+        N = P * int(rng.integers(1, 400 // P))
+        D = 8 * int(rng.integers(1, 60))
+        V = int(rng.choice([int(rng.integers(2, 300)), int(rng.integers(300, 3000))]))
+        out.append((P, int(rng.integers(1, 3)), N, D, V, BF16 if rng.integers(0, 2) else FP32))
+    return out
+
+
+@pytest.mark.parametrize("P,B,N,D,V,dtype", _random_cases(10))
+def test_random_shapes(uly, P, B, N, D, V, dtype):
+    test_loss_and_gradients(uly, P, B, N, D, V, dtype)
