@@ -4,7 +4,7 @@
 // losses weighted by their good tokens as in sharded_loss.cu, and the
 // gradients of the total with respect to h and W.  The logits
 //   x_rv = <h_r, w_v>
-// are never kept: the good rows are taken in pieces of at most kPieceRows, and
+// are never kept: the good rows are taken in pieces of a few thousand, and
 // for each piece
 //   1. logits   x = h W^T; every (row, column tile) leaves its maximum c (in
 //               units of log2), its sum s of e = 2^(x log2 e - c), the row's
@@ -16,50 +16,67 @@
 // That is three products instead of the four that recomputing the logits from
 // a kept log-sum-exp would take.  Rows without a label are left out before the
 // first product: the good rows are gathered next to each other.
-#include "uly_internal.h"
+#include "linear_ce.h"
 
 namespace uly {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kStatCols = 64;
+constexpr int kRowThreads = 512;
+// Rows of a piece.  Larger pieces spread the fp32 dW that is carried from
+// piece to piece (read and written once each) over more products; the buffer
+// of exponentials grows with them (2 bytes a value, 10 in fp32).
+constexpr int kPieceBf16 = 8192, kPieceFp32 = 2048;
 
-template <typename T>
-struct Types;
-template <>
-struct Types<uint16_t> {
-    using E = uint16_t;  // fp16 bits of e, then bf16 bits of g
-};
-template <>
-struct Types<float> {
-    using E = float;
-};
+__device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu); }
 
-__device__ __forceinline__ float ld(const uint16_t *p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
-__device__ __forceinline__ float ld(const float *p) { return *p; }
-__device__ __forceinline__ void st(uint16_t *p, float v) { *p = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu); }
-__device__ __forceinline__ void st(float *p, float v) { *p = v; }
-
-__device__ __forceinline__ uint16_t half_bits(float v)
+__device__ __forceinline__ float2 f16x2_values(uint32_t b)
 {
-    uint16_t r;
-    asm("cvt.rn.f16.f32 %0, %1;" : "=h"(r) : "f"(v));
-    return r;
-}
-__device__ __forceinline__ float half_value(uint16_t b)
-{
-    float r;
-    asm("cvt.f32.f16 %0, %1;" : "=f"(r) : "h"(b));
-    return r;
+    float lo, hi;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}\n"
+        : "=f"(lo), "=f"(hi)
+        : "r"(b));
+    return make_float2(lo, hi);
 }
 
-// Rows of the piece starting at good row `base`: device data, since the number
-// of good rows is.
-__device__ __forceinline__ int piece_count(const int *n_good, int64_t base, int rows)
+// Three bf16 parts of x: x1 + x2 + x3 = x up to 2^-26 |x|.
+struct Parts {
+    uint16_t p[3];
+};
+__device__ __forceinline__ Parts split3(float x)
 {
-    const int64_t left = *n_good - base;
-    return left <= 0 ? 0 : (left < rows ? static_cast<int>(left) : rows);
+    Parts r;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        r.p[i] = bf16_bits(x);
+        x -= bf16_value(r.p[i]);
+    }
+    return r;
+}
+
+// Eight values as planes, 16 bytes each, `plane` elements apart.
+__device__ __forceinline__ void store_planes(uint16_t *out, int64_t plane, const float (&x)[8])
+{
+    Parts q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        q[j] = split3(x[j]);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = q[2 * j].p[i] | static_cast<uint32_t>(q[2 * j + 1].p[i]) << 16;
+        *reinterpret_cast<uint4 *>(out + i * plane) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Eight values of an fp32 row of D values (a multiple of 4), zeros past its end.
+__device__ __forceinline__ void load8(const float *row, int i, int D, float (&x)[8])
+{
+    const float4 a = *reinterpret_cast<const float4 *>(row + i);
+    const float4 b = i + 4 < D ? *reinterpret_cast<const float4 *>(row + i + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
 // Good rows in order: index[i] = row of the i-th one, n_good = how many.
@@ -89,176 +106,83 @@ __global__ void __launch_bounds__(1024) compact_kernel(const int32_t *__restrict
         *n_good = done;
 }
 
-// The piece's hidden rows next to each other, zeros up to a multiple of 64.
-template <typename T>
-__global__ void gather_kernel(const T *__restrict__ hidden, const int32_t *__restrict__ index,
-                              const int *__restrict__ n_good, int64_t base, int rows, int D, T *__restrict__ out)
+// The piece's hidden rows next to each other (fp32: as planes), with their
+// labels; zeros up to a multiple of 64 rows, where dW's contraction ends.
+template <bool kSplit>
+__global__ void gather_kernel(const __grid_constant__ CeArgs a, const void *__restrict__ hidden,
+                              const int32_t *__restrict__ shifted, int32_t *__restrict__ label, void *__restrict__ out,
+                              int64_t ldh)
 {
-    const int cnt = piece_count(n_good, base, rows), r = blockIdx.x;
-    if (r >= (cnt + 63) / 64 * 64)
+    const int cnt = ce_piece_rows(a), r = blockIdx.x;
+    if (r >= (cnt + kCeStep - 1) / kCeStep * kCeStep)
         return;
-    const uint4 *src = r < cnt ? reinterpret_cast<const uint4 *>(hidden + static_cast<int64_t>(index[base + r]) * D) : nullptr;
-    uint4 *dst = reinterpret_cast<uint4 *>(out + static_cast<int64_t>(r) * D);
-    for (int i = threadIdx.x; i < D * static_cast<int>(sizeof(T)) / 16; i += blockDim.x)
-        dst[i] = src ? src[i] : make_uint4(0, 0, 0, 0);
+    const bool live = r < cnt;
+    const int64_t src = live ? a.index[a.base + r] : 0;
+    if (threadIdx.x == 0)
+        label[r] = live ? shifted[src] : -1;
+    for (int i = threadIdx.x * 8; i < a.D; i += blockDim.x * 8) {
+        if constexpr (kSplit) {
+            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (live)
+                load8(static_cast<const float *>(hidden) + src * a.D, i, a.D, x);
+            store_planes(static_cast<uint16_t *>(out) + r * ldh + i, ldh * a.rows, x);
+        } else {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (live)
+                x = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(hidden) + src * a.D + i);
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + r * ldh + i) = x;
+        }
+    }
+}
+
+// fp32 weight as planes.
+__global__ void split_weight_kernel(const float *__restrict__ w, int D, int V, uint16_t *__restrict__ out, int64_t ldw)
+{
+    const int64_t v = blockIdx.x;
+    for (int i = threadIdx.x * 8; i < D; i += blockDim.x * 8) {
+        float x[8];
+        load8(w + v * D, i, D, x);
+        store_planes(out + v * ldw + i, ldw * V, x);
+    }
 }
 
 // Zero gradient of the rows without a label.
-template <typename T>
-__global__ void zero_ignored_kernel(const int32_t *__restrict__ shifted, int D, T *__restrict__ dhidden)
+__global__ void zero_ignored_kernel(const int32_t *__restrict__ shifted, int vecs, uint4 *__restrict__ dhidden)
 {
     const int64_t r = blockIdx.x;
     if (shifted[r] >= 0)
         return;
-    uint4 *dst = reinterpret_cast<uint4 *>(dhidden + r * D);
-    for (int i = threadIdx.x; i < D * static_cast<int>(sizeof(T)) / 16; i += blockDim.x)
-        dst[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < vecs; i += blockDim.x)
+        dhidden[r * vecs + i] = make_uint4(0, 0, 0, 0);
 }
 
-enum { kLogits = 0, kDh = 1, kDw = 2 };
-
-struct GemmArgs {
-    const void *h, *w;  // gathered rows [rows][D], weight [V][D]
-    void *g;            // [rows][ldg]
-    int64_t ldg;
-    const int32_t *index, *shifted;
-    const int *n_good;
-    int64_t base;
-    int rows, D, V;
-    float2 *stats;  // [rows][stat_tiles] (c, s)
-    int stat_tiles;
-    float *target;  // [rows] target logits
-    int keep;       // logits: keep e
-    void *dh, *dw;
-    float *acc;  // [V][D] across pieces
-};
-
-// C[m][n] = sum_k A(m, k) B(n, k), 64 x 64 tiles, 4 x 4 a thread.
-template <typename T, int kMode>
-__global__ void __launch_bounds__(256) gemm_kernel(const __grid_constant__ GemmArgs a)
+// One CTA per row of the piece: the row's loss, and with a gradient e -> g, in
+// place in bf16, to planes in fp32.  e stays relative to its own columns'
+// maximum until here, as fp16 (2^-11 of e; below 2^-14 of that maximum the
+// error is 2^-25 of it): stored as bf16, g would be rounded to 8 bits twice.
+template <bool kSplit>
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ CeArgs a, uint16_t *__restrict__ g,
+                                                           const int32_t *__restrict__ label,
+                                                           float *__restrict__ row_loss)
 {
-    using E = typename Types<T>::E;
-    const int cnt = piece_count(a.n_good, a.base, a.rows);
-    const bool last = a.base + a.rows >= *a.n_good;
-    if (kMode != kDw && static_cast<int>(blockIdx.y) * 64 >= cnt)
+    const int cnt = ce_piece_rows(a), r = blockIdx.x;
+    if (r >= (cnt + kCeStep - 1) / kCeStep * kCeStep)
         return;
-    if (kMode == kDw && cnt == 0 && a.base > 0)
-        return;
-    const int M = kMode == kDw ? a.V : cnt, N = kMode == kLogits ? a.V : a.D;
-    const int K = kMode == kLogits ? a.D : (kMode == kDh ? a.V : cnt);
-    const T *h = static_cast<const T *>(a.h), *w = static_cast<const T *>(a.w);
-    E *g = static_cast<E *>(a.g);
-    __shared__ float As[16][65], Bs[16][65];
-    const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float c[4][4] = {};
-    for (int k0 = 0; k0 < K; k0 += 16) {
-        for (int i = threadIdx.x; i < 1024; i += 256) {
-            // k fastest for the operands whose rows run along k
-            const int kf = i % 16, rf = i / 16, rs = i % 64, ks = i / 64;
-            if (kMode == kDw) {
-                const int m = m0 + rs, k = k0 + ks;
-                As[ks][rs] = m < M && k < K ? ld(g + k * a.ldg + m) : 0.f;
-            } else {
-                const int m = m0 + rf, k = k0 + kf;
-                const bool in = m < M && k < K;
-                As[kf][rf] = !in ? 0.f : (kMode == kLogits ? ld(h + static_cast<int64_t>(m) * a.D + k) : ld(g + m * a.ldg + k));
-            }
-            if (kMode == kLogits) {
-                const int n = n0 + rf, k = k0 + kf;
-                Bs[kf][rf] = n < N && k < K ? ld(w + static_cast<int64_t>(n) * a.D + k) : 0.f;
-            } else {
-                const int n = n0 + rs, k = k0 + ks;
-                Bs[ks][rs] = n < N && k < K ? ld((kMode == kDh ? w : h) + static_cast<int64_t>(k) * a.D + n) : 0.f;
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    c[i][j] = fmaf(As[k][ty * 4 + i], Bs[k][tx * 4 + j], c[i][j]);
-        __syncthreads();
-    }
-    const float inv_t = 1.f / static_cast<float>(*a.n_good > 1 ? *a.n_good : 1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = m0 + ty * 4 + i;
-        if (kMode == kLogits) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                mx = fmaxf(mx, n0 + tx * 4 + j < N ? c[i][j] : -INFINITY);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1)
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const float c2 = mx * kLog2e;
-            const int y = m < M ? a.shifted[a.index[a.base + m]] : -1;
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = n0 + tx * 4 + j;
-                if (n >= N)
-                    continue;
-                const float e = exp2f(fmaf(c[i][j], kLog2e, -c2));
-                sum += e;
-                if (m >= M)
-                    continue;
-                if (n == y)
-                    a.target[m] = c[i][j];
-                if (a.keep) {
-                    if constexpr (sizeof(E) == 2)
-                        g[m * a.ldg + n] = half_bits(e);
-                    else
-                        g[m * a.ldg + n] = e;
-                }
-            }
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1)
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (tx == 0 && m < M)
-                a.stats[static_cast<int64_t>(m) * a.stat_tiles + blockIdx.x] = make_float2(c2, sum);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = n0 + tx * 4 + j;
-                if (m >= M || n >= N)
-                    continue;
-                if (kMode == kDh) {
-                    st(static_cast<T *>(a.dh) + static_cast<int64_t>(a.index[a.base + m]) * a.D + n, c[i][j] * inv_t);
-                } else {
-                    const int64_t o = static_cast<int64_t>(m) * a.D + n;
-                    const float v = c[i][j] + (a.base > 0 ? a.acc[o] : 0.f);
-                    if (last)
-                        st(static_cast<T *>(a.dw) + o, v * inv_t);
-                    else
-                        a.acc[o] = v;
-                }
-            }
-        }
-    }
-}
-
-// One CTA per row of the piece: the row's loss, and with the gradient e -> g.
-template <typename T>
-__global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ GemmArgs a, float *__restrict__ row_loss)
-{
-    using E = typename Types<T>::E;
-    const int cnt = piece_count(a.n_good, a.base, a.rows), r = blockIdx.x;
-    if (r >= (cnt + 63) / 64 * 64)
-        return;
-    E *g = static_cast<E *>(a.g) + r * a.ldg;
+    uint16_t *grow = g + r * a.ldg;
+    const int64_t plane = a.ldg * a.rows;
     if (r >= cnt) {
         if (a.keep)
-            for (int v = threadIdx.x; v < a.V; v += 256)
-                g[v] = 0;
+            for (int v = threadIdx.x * 8; v < a.V; v += kRowThreads * 8)
+#pragma unroll
+                for (int i = 0; i < (kSplit ? 3 : 1); ++i)
+                    *reinterpret_cast<uint4 *>(grow + i * plane + v) = make_uint4(0, 0, 0, 0);
         return;
     }
-    __shared__ float red[2][8];
+    constexpr int kWarps = kRowThreads / 32;
+    __shared__ float red[2][kWarps];
     const float2 *stats = a.stats + static_cast<int64_t>(r) * a.stat_tiles;
     float C = -INFINITY;
-    for (int t = threadIdx.x; t < a.stat_tiles; t += 256)
+    for (int t = threadIdx.x; t < a.stat_tiles; t += kRowThreads)
         C = fmaxf(C, stats[t].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -266,10 +190,10 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ GemmA
     if (lane_id() == 0)
         red[0][warp_id()] = C;
     __syncthreads();
-    for (int w = 0; w < 8; ++w)
+    for (int w = 0; w < kWarps; ++w)
         C = fmaxf(C, red[0][w]);
     float S = 0.f;
-    for (int t = threadIdx.x; t < a.stat_tiles; t += 256)
+    for (int t = threadIdx.x; t < a.stat_tiles; t += kRowThreads)
         S += stats[t].y * exp2f(stats[t].x - C);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -278,30 +202,44 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ GemmA
         red[1][warp_id()] = S;
     __syncthreads();
     S = 0.f;
-    for (int w = 0; w < 8; ++w)
+    for (int w = 0; w < kWarps; ++w)
         S += red[1][w];
-    const int row = a.index[a.base + r];
-    const int y = a.shifted[row];
-    if (threadIdx.x == 0)
-        row_loss[row] = (log2f(S) - fmaf(a.target[r], kLog2e, -C)) * kLn2;
+    const int y = label[r];
+    if (threadIdx.x == 0)  // ln S + C ln 2 - x_y, with C taken out of x_y before anything is rounded
+        row_loss[a.index[a.base + r]] = (log2f(S) - fmaf(a.target[r], kLog2e, -C)) * kLn2;
     if (!a.keep)
         return;
     const float inv = 1.f / S;
-    for (int v = threadIdx.x; v < a.V; v += 256) {
-        const float f = exp2f(stats[v / kStatCols].x - C) * inv;
-        if constexpr (sizeof(E) == 2)
-            st(g + v, half_value(g[v]) * f - (v == y ? 1.f : 0.f));
+    for (int v = threadIdx.x * 8; v < a.V; v += kRowThreads * 8) {
+        const float f = exp2f(stats[v / kCeStatCols].x - C) * inv;
+        float x[8];
+        if constexpr (kSplit) {
+            load8(static_cast<const float *>(a.e) + r * a.ldg, v, v + 8, x);
+        } else {
+            const uint4 e = *reinterpret_cast<const uint4 *>(grow + v);
+            const uint32_t w[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 p = f16x2_values(w[j]);
+                x[2 * j] = p.x, x[2 * j + 1] = p.y;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            x[j] = x[j] * f - (v + j == y ? 1.f : 0.f);
+        if constexpr (kSplit)
+            store_planes(grow + v, plane, x);
         else
-            g[v] = g[v] * f - (v == y ? 1.f : 0.f);
+            *reinterpret_cast<uint4 *>(grow + v) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
     }
 }
 
-constexpr int kPieceRows = 8192;
 size_t up(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Layout {
-    size_t good, n_good, shifted, row_loss, index, target, stats, h, g, acc, total;
-    int64_t ldg;
+    size_t good, n_good, shifted, row_loss, index, label, target, stats, h, w, e, g, acc, partial, total;
+    int64_t ldh, ldg;
     int rows, stat_tiles;
 };
 
@@ -309,9 +247,12 @@ Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
 {
     Layout L = {};
     const int64_t T = B * N;
-    L.rows = static_cast<int>(std::min<int64_t>(kPieceRows, (T + 63) / 64 * 64));
+    const bool split = esize == 4;
+    L.rows = static_cast<int>(std::min<int64_t>(split ? kPieceFp32 : kPieceBf16, (T + 63) / 64 * 64));
     L.ldg = (V + 63) / 64 * 64;
-    L.stat_tiles = (V + kStatCols - 1) / kStatCols;
+    L.ldh = (D + 7) / 8 * 8;
+    L.stat_tiles = (V + kCeStatCols - 1) / kCeStatCols;
+    const size_t planes = split ? 3 : 1, kept = static_cast<size_t>(L.rows) * L.ldg;
     size_t o = 0;
     auto take = [&](size_t &at, size_t bytes) { at = o, o += up(bytes); };
     take(L.good, sizeof(unsigned long long) * P);
@@ -319,40 +260,51 @@ Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
     take(L.shifted, sizeof(int32_t) * T);
     take(L.row_loss, sizeof(float) * T);
     take(L.index, sizeof(int32_t) * T);
+    take(L.label, sizeof(int32_t) * L.rows);
     take(L.target, sizeof(float) * L.rows);
     take(L.stats, sizeof(float2) * L.rows * static_cast<size_t>(L.stat_tiles));
-    take(L.h, static_cast<size_t>(L.rows) * D * esize);
+    take(L.h, planes * L.rows * L.ldh * 2);
+    if (split)
+        take(L.w, planes * V * L.ldh * 2);
     if (grad) {
-        take(L.g, static_cast<size_t>(L.rows) * L.ldg * esize);
+        take(L.g, planes * kept * 2);
+        L.e = L.g;  // bf16: e becomes g in place
+        if (split)
+            take(L.e, kept * 4);
+        const size_t tiles = static_cast<size_t>((V + kCeTile - 1) / kCeTile) * ((D + kCeTile - 1) / kCeTile);
         if (T > L.rows)
-            take(L.acc, sizeof(float) * static_cast<size_t>(V) * D);
+            take(L.acc, sizeof(float) * kCeTileFloats * tiles);
+        take(L.partial, sizeof(float) * kCeTileFloats * 2 *
+                            std::max(ce_most_workers(kCeDh, L.rows, D, V), ce_most_workers(kCeDw, L.rows, D, V)));
     }
     L.total = o;
     return L;
 }
 
-template <typename T>
+template <bool kSplit>
 cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, void *dhidden, void *dweight,
                 float *shard_loss, int64_t *shard_good, float *total, int64_t B, int64_t N, int D, int V, int P,
                 uint8_t *ws, cudaStream_t s)
 {
+    constexpr int kEsize = kSplit ? 4 : 2;
     const bool grad = dhidden || dweight;
-    const Layout L = layout(B, N, D, V, P, grad, sizeof(T));
+    const Layout L = layout(B, N, D, V, P, grad, kEsize);
     const int64_t rows = B * N;
     auto *good = reinterpret_cast<unsigned long long *>(ws + L.good);
     auto *shifted = reinterpret_cast<int32_t *>(ws + L.shifted);
     auto *row_loss = reinterpret_cast<float *>(ws + L.row_loss);
-    GemmArgs a = {};
-    a.h = ws + L.h;
-    a.w = weight;
-    a.g = ws + L.g;
-    a.ldg = L.ldg;
-    a.index = reinterpret_cast<int32_t *>(ws + L.index);
-    a.shifted = shifted;
+    auto *index = reinterpret_cast<int32_t *>(ws + L.index);
+    auto *label = reinterpret_cast<int32_t *>(ws + L.label);
+    auto *g = reinterpret_cast<uint16_t *>(ws + L.g);
+    CeArgs a = {};
     a.n_good = reinterpret_cast<int *>(ws + L.n_good);
     a.rows = L.rows;
     a.D = D;
     a.V = V;
+    a.ldg = L.ldg;
+    a.e = ws + L.e;
+    a.index = index;
+    a.label = label;
     a.stats = reinterpret_cast<float2 *>(ws + L.stats);
     a.stat_tiles = L.stat_tiles;
     a.target = reinterpret_cast<float *>(ws + L.target);
@@ -360,26 +312,37 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
     a.dh = dhidden;
     a.dw = dweight;
     a.acc = reinterpret_cast<float *>(ws + L.acc);
+    a.partial = reinterpret_cast<float *>(ws + L.partial);
     cudaError_t e = launch_shift_count(labels, shifted, good, B, N, P, V, s);
     if (e == cudaSuccess)
         e = cudaMemsetAsync(row_loss, 0, sizeof(float) * rows, s);
     if (e != cudaSuccess)
         return e;
-    compact_kernel<<<1, 1024, 0, s>>>(shifted, rows, reinterpret_cast<int32_t *>(ws + L.index),
-                                      reinterpret_cast<int *>(ws + L.n_good));
+    compact_kernel<<<1, 1024, 0, s>>>(shifted, rows, index, a.n_good);
     if (dhidden)
-        zero_ignored_kernel<T><<<static_cast<unsigned>(rows), 128, 0, s>>>(shifted, D, static_cast<T *>(dhidden));
-    const unsigned mt = (L.rows + 63) / 64, vt = (V + 63) / 64, dt = (D + 63) / 64;
+        zero_ignored_kernel<<<static_cast<unsigned>(rows), 128, 0, s>>>(shifted, D * kEsize / 16,
+                                                                        static_cast<uint4 *>(dhidden));
+    const void *w = weight;
+    int64_t ldw = D;
+    if (kSplit) {
+        w = ws + L.w;
+        ldw = L.ldh;
+        split_weight_kernel<<<V, 128, 0, s>>>(static_cast<const float *>(weight), D, V,
+                                              reinterpret_cast<uint16_t *>(ws + L.w), ldw);
+    }
     for (int64_t base = 0; base < rows; base += L.rows) {
         a.base = base;
-        gather_kernel<T><<<L.rows, 128, 0, s>>>(static_cast<const T *>(hidden), a.index, a.n_good, base, L.rows, D,
-                                                reinterpret_cast<T *>(ws + L.h));
-        gemm_kernel<T, kLogits><<<dim3(vt, mt), 256, 0, s>>>(a);
-        rows_kernel<T><<<L.rows, 256, 0, s>>>(a, row_loss);
+        gather_kernel<kSplit><<<L.rows, 128, 0, s>>>(a, hidden, shifted, label, ws + L.h, L.ldh);
+        e = launch_ce_product(kCeLogits, a, ws + L.h, L.ldh, w, ldw, g, kEsize, s);
+        if (e != cudaSuccess)
+            return e;
+        rows_kernel<kSplit><<<L.rows, kRowThreads, 0, s>>>(a, g, label, row_loss);
         if (dhidden)
-            gemm_kernel<T, kDh><<<dim3(dt, mt), 256, 0, s>>>(a);
-        if (dweight)
-            gemm_kernel<T, kDw><<<dim3(dt, vt), 256, 0, s>>>(a);
+            e = launch_ce_product(kCeDh, a, ws + L.h, L.ldh, w, ldw, g, kEsize, s);
+        if (e == cudaSuccess && dweight)
+            e = launch_ce_product(kCeDw, a, ws + L.h, L.ldh, w, ldw, g, kEsize, s);
+        if (e != cudaSuccess)
+            return e;
     }
     return launch_shard_totals(row_loss, good, shard_loss, shard_good, total, B, N, P, s);
 }
@@ -397,9 +360,9 @@ cudaError_t launch_sharded_linear_ce(const void *hidden, const void *weight, con
 {
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     if (esize == 2)
-        return run<uint16_t>(hidden, weight, labels, dhidden, dweight, shard_loss, shard_good, total, B, N, D, V, P,
-                             ws, s);
-    return run<float>(hidden, weight, labels, dhidden, dweight, shard_loss, shard_good, total, B, N, D, V, P, ws, s);
+        return run<false>(hidden, weight, labels, dhidden, dweight, shard_loss, shard_good, total, B, N, D, V, P, ws,
+                          s);
+    return run<true>(hidden, weight, labels, dhidden, dweight, shard_loss, shard_good, total, B, N, D, V, P, ws, s);
 }
 
 }  // namespace uly

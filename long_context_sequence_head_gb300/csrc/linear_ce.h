@@ -1,0 +1,61 @@
+// Shared by the two translation units of the fused LM-head loss: linear_ce.cu
+// (rows, pieces, host) and linear_ce_gemm.cu (the three matrix products).
+#pragma once
+
+#include "uly_internal.h"
+
+namespace uly {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// The products run on CTA pairs: 256 x 256 output tiles, 64 values of the
+// contraction per step.
+constexpr int kCeTile = 256;
+constexpr int kCeStep = 64;
+constexpr int kCeStatCols = 128;  // columns behind one (c, s) of the softmax
+constexpr int kCeMaxPairs = 80;
+// floats a pair leaves for one tile
+constexpr int64_t kCeTileFloats = static_cast<int64_t>(kCeTile) * kCeTile;
+
+enum CeProduct {
+    kCeLogits = 0,  // x  = h W^T   [rows][V]
+    kCeDh = 1,      // dh = g W     [rows][D]
+    kCeDw = 2,      // dW = g^T h   [V][D]
+};
+
+struct CeArgs {
+    int *n_good;            // good rows of the whole call (device)
+    int64_t base;           // first good row of the piece
+    int rows;               // rows a piece may have
+    int D, V;
+    int64_t ldg;            // row pitch of e and g, elements
+    void *e;                // [rows][ldg]: fp16 (bf16 inputs) or fp32 exponentials
+    const int32_t *index;   // good row -> row of hidden
+    const int32_t *label;   // [rows] of the piece
+    float2 *stats;          // [rows][stat_tiles] (c, s)
+    int stat_tiles;
+    float *target;          // [rows] logits of the labels
+    int keep;               // with a gradient: keep e
+    void *dh, *dw;
+    float *acc;             // dW over the pieces, in tiles (see tile_slot)
+    float *partial;         // tiles split over the contraction
+};
+
+// Rows of the piece: device data, since the number of good rows is.
+__device__ __forceinline__ int ce_piece_rows(const CeArgs &a)
+{
+    const int64_t left = *a.n_good - a.base;
+    return left <= 0 ? 0 : (left < a.rows ? static_cast<int>(left) : a.rows);
+}
+
+// Most pairs that may share a product's leftover tiles (host, for the workspace).
+int ce_most_workers(CeProduct what, int rows, int D, int V);
+
+// esize: 2 (bf16) or 4 (fp32, the operands as three bf16 planes each).  h: the
+// piece's rows; w: the weight; g: the logits' gradient; ldh, ldw: row pitches
+// in elements.
+cudaError_t launch_ce_product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh, const void *w, int64_t ldw,
+                              const void *g, int esize, cudaStream_t s);
+
+}  // namespace uly

@@ -1,0 +1,634 @@
+// The three matrix products of the fused LM-head loss on the 5th-generation
+// tensor cores, one persistent kernel per product.
+//
+// A CTA pair owns a 256 x 256 output tile: each CTA loads its 128 rows of A
+// and its 128 columns of B (TMA, 128-byte swizzle), one thread of the pair
+// issues tcgen05.mma.cta_group::2 (M = 256, N = 256), and each CTA's TMEM holds
+// 128 rows of the fp32 result, twice, so that one tile is written out while
+// the next is formed.  A pair reads half of what two single CTAs would: 64
+// bytes a clock and SM from L2 at full rate.  The operands come as they lie:
+// a matrix whose rows run along the contraction is K-major, one whose rows run
+// along the output (W in dh; g and h in dW) is MN-major.
+//
+// Warps 0-7 write results out (TMEM lane quarter warp % 4, columns 128 (warp /
+// 4) ..), warp 8 loads, warp 9 issues products.
+//
+// Tiles beyond the last full round over the pairs are split along the
+// contraction when that saves more than joining them costs: every pair takes
+// an equal run of the leftover steps, leaves its fp32 tile in `partial`, and a
+// second kernel adds the runs in order.  The split depends on the sizes and
+// the number of good rows alone, so results repeat bit for bit.
+//
+// The tensor cores' accumulation rounds toward zero: a sum shrinks by up to
+// 2^-24 of itself with every instruction (16 values of the contraction).  Over
+// D = 2560 that moved the loss by 2.2e-6 of its value, over V = 151936 it
+// would move dh by 4e-4.  So an accumulator is taken out of TMEM after
+// kChunkSteps steps and summed in registers, with ordinary rounding, while the
+// next one fills: after 512 values for the logits, whose error the loss shows
+// undiminished, after 4096 for the gradients, which are rounded to bf16.
+//
+// fp32 (kSplit): every operand is three bf16 planes (x = x1 + x2 + x3 up to
+// 2^-26 of x) and a product is the six plane products above 2^-24, smallest
+// first; an accumulator takes 64 values of the contraction (24 instructions).
+#include "linear_ce.h"
+
+namespace uly {
+namespace {
+
+constexpr int kStages = 5;
+constexpr int kHalf = 128;                               // rows of A, columns of B per CTA
+constexpr int kOperandBytes = kHalf * kCeStep * 2;       // 16 KB
+constexpr int kStageBytes = 2 * kOperandBytes;           // this CTA's part
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kCols = 128;                               // columns per writing warp
+constexpr int kWarpStaging = 32 * 256;                   // 32 rows of 256 bytes
+constexpr int kBars = 2 * kStages + 5;
+constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kWarpStaging + 8 * kBars + 16 + 1024;
+constexpr int kPlanePairs = 6;
+constexpr int kMinRun = 8;       // least steps of a run
+constexpr int kSplitGain = 32;   // steps a split must save
+
+template <int kWhat, bool kSplit>
+constexpr int kChunkSteps = kSplit ? 1 : (kWhat == kCeLogits ? 8 : 64);
+
+// ------------------------------------------------------------- schedule
+struct Plan {
+    int mt, nt, kb;   // tiles along the rows and columns of the result, steps of the contraction
+    int whole;        // tiles [0, whole) are done by one pair each
+    int workers;      // pairs sharing the tiles from `whole` on
+};
+
+__host__ __device__ inline int ce_workers(int64_t tiles, int kb, int pairs, int &whole)
+{
+    const int rem = static_cast<int>(tiles % pairs);
+    whole = static_cast<int>(tiles);
+    if (rem == 0 || static_cast<int64_t>(kb) * (pairs - rem) <= static_cast<int64_t>(kSplitGain) * pairs)
+        return 0;
+    const int64_t most = static_cast<int64_t>(rem) * kb / kMinRun;
+    const int workers = most < pairs ? static_cast<int>(most) : pairs;
+    if (workers <= rem)
+        return 0;
+    whole = static_cast<int>(tiles) - rem;
+    return workers;
+}
+
+template <int kWhat>
+__device__ __forceinline__ Plan make_plan(const CeArgs &a, int cnt, int pairs)
+{
+    Plan p;
+    const int M = kWhat == kCeDw ? a.V : cnt, N = kWhat == kCeLogits ? a.V : a.D;
+    const int K = kWhat == kCeLogits ? a.D : (kWhat == kCeDh ? a.V : cnt);
+    p.mt = (M + kCeTile - 1) / kCeTile;
+    p.nt = (N + kCeTile - 1) / kCeTile;
+    p.kb = (K + kCeStep - 1) / kCeStep;
+    p.workers = 0;
+    p.whole = p.mt * p.nt;
+    if (kWhat != kCeLogits)  // a softmax needs whole sums
+        p.workers = ce_workers(static_cast<int64_t>(p.mt) * p.nt, p.kb, pairs, p.whole);
+    return p;
+}
+
+// One tile, or a run of a tile's steps, in the order a pair takes them.  The
+// loader, the issuer and the writers walk the same list.
+struct Unit {
+    int tile, k0, k1;
+    int run;  // -1: the whole tile; else 0 or 1, the pair's first or second run
+};
+
+struct Units {
+    Plan p;
+    int pair, pairs, next_tile, run;
+    int64_t lo, hi;
+
+    __device__ Units(const Plan &plan, int pair_, int pairs_) : p(plan), pair(pair_), pairs(pairs_), next_tile(pair_), run(0)
+    {
+        const int64_t steps = static_cast<int64_t>(p.mt * static_cast<int64_t>(p.nt) - p.whole) * p.kb;
+        lo = pair < p.workers ? steps * pair / p.workers : 0;
+        hi = pair < p.workers ? steps * (pair + 1) / p.workers : 0;
+    }
+    __device__ __forceinline__ bool next(Unit &u)
+    {
+        if (next_tile < p.whole) {
+            u = Unit{next_tile, 0, p.kb, -1};
+            next_tile += pairs;
+            return true;
+        }
+        if (lo >= hi)
+            return false;
+        const int t = static_cast<int>(lo / p.kb), k0 = static_cast<int>(lo - static_cast<int64_t>(t) * p.kb);
+        const int k1 = hi - lo < p.kb - k0 ? k0 + static_cast<int>(hi - lo) : p.kb;
+        u = Unit{p.whole + t, k0, k1, run++};
+        lo += k1 - k0;
+        return true;
+    }
+};
+
+// Tile order.  Logits: rows fastest, so that a round over the pairs reads a
+// few column panels of W once against all rows, which stay in L2.  dh and dW:
+// columns (D) fastest, so that g, the large operand, is read once a round.
+template <int kWhat>
+__device__ __forceinline__ void tile_origin(const Plan &p, int tile, int &m0, int &n0)
+{
+    if (kWhat == kCeLogits) {
+        n0 = tile / p.mt * kCeTile;
+        m0 = tile % p.mt * kCeTile;
+    } else {
+        m0 = tile / p.nt * kCeTile;
+        n0 = tile % p.nt * kCeTile;
+    }
+}
+
+// A tile's fp32 values in memory, as the writers hold them: per CTA and warp
+// 32 groups of 4 columns, each 32 rows x 16 bytes, so that a warp's access is
+// 512 bytes in a row.
+__device__ __forceinline__ float4 *tile_slot(float *buf, int64_t slot, int cta, int warp, int lane)
+{
+    return reinterpret_cast<float4 *>(buf + slot * kCeTileFloats) + (cta * kEpiWarps + warp) * (32 * 32) + lane;
+}
+
+// ------------------------------------------------------------ writing out
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The warp's 32 rows x 128 columns (row = lane) to memory, 256 bytes of a row
+// per half warp: through shared memory, units of 16 bytes permuted within the
+// row so that neither side meets a bank conflict.  row_off: element offset of
+// this lane's row, negative: not written.  Columns from `limit` on are not
+// written (a multiple of 16 bytes).
+enum OutType { kBf16, kF16, kF32 };
+template <OutType kType>
+__device__ __forceinline__ void store_rows(const float (&x)[kCols], void *out, int64_t row_off, int col0, int limit,
+                                           uint8_t *staging, int lane)
+{
+    constexpr int kPer = kType == kF32 ? 4 : 8;  // values per unit
+    constexpr int kParts = kCols / (16 * kPer);
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) {
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+            const float *v = x + (part * 16 + u) * kPer;
+            uint4 val;
+            if constexpr (kType == kF32)
+                val = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                 __float_as_uint(v[3]));
+            else if constexpr (kType == kBf16)
+                val = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                 pack_bf16x2(v[6], v[7]));
+            else
+                val = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]),
+                                 pack_f16x2(v[6], v[7]));
+            *reinterpret_cast<uint4 *>(staging + lane * 256 + ((u ^ (lane & 15)) << 4)) = val;
+        }
+        __syncwarp();
+        const int u = lane & 15, col = col0 + (part * 16 + u) * kPer;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int row = 2 * i + (lane >> 4);
+            const int64_t off = __shfl_sync(0xffffffffu, row_off, row);
+            const uint4 val = *reinterpret_cast<const uint4 *>(staging + row * 256 + ((u ^ (row & 15)) << 4));
+            if (off >= 0 && col < limit)
+                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(out) + (off + col) * (16 / kPer)) = val;
+        }
+        __syncwarp();
+    }
+}
+
+// Logits: the row's maximum and sum over this warp's columns, its target's
+// logit, and the exponentials.
+template <bool kSplit>
+__device__ __forceinline__ void finish_logits(const CeArgs &a, float (&x)[kCols], int cnt, int m, int col0,
+                                              uint8_t *staging, int lane)
+{
+    if (col0 >= a.V)
+        return;
+    const bool live = m < cnt;
+    const int y = live ? a.label[m] : -1;
+    if (y >= col0 && y < col0 + kCols) {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+            if (y == col0 + j)
+                a.target[m] = x[j];
+    }
+    if (col0 + kCols > a.V) {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+            if (col0 + j >= a.V)
+                x[j] = -INFINITY;
+    }
+    float pm[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        pm[j] = x[j];
+#pragma unroll
+    for (int j = 8; j < kCols; ++j)
+        pm[j & 7] = fmaxf(pm[j & 7], x[j]);
+    const float c = kLog2e * fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
+                                   fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
+    float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+        x[j] = ex2_approx(fmaf(x[j], kLog2e, -c));
+        ps[j & 3] += x[j];
+    }
+    if (live)
+        a.stats[static_cast<int64_t>(m) * a.stat_tiles + col0 / kCeStatCols] =
+            make_float2(c, (ps[0] + ps[1]) + (ps[2] + ps[3]));
+    if (a.keep)
+        store_rows<kSplit ? kF32 : kF16>(x, a.e, live ? m * a.ldg : -1, col0, static_cast<int>(a.ldg), staging, lane);
+}
+
+// dh and dW: scaled by 1 / T and rounded once.  dW over several pieces is kept
+// in fp32 until the last one.
+template <int kWhat, bool kSplit>
+__device__ __forceinline__ void finish_grad(const CeArgs &a, float (&x)[kCols], int cnt, int tile, int m, int col0,
+                                            int cta, int warp, uint8_t *staging, int lane)
+{
+    const int n_good = *a.n_good;
+    int64_t off = -1;
+    void *out = a.dh;
+    if (kWhat == kCeDh) {
+        if (m < cnt)
+            off = static_cast<int64_t>(a.index[a.base + m]) * a.D;
+    } else {
+        out = a.dw;
+        if (m < a.V)
+            off = static_cast<int64_t>(m) * a.D;
+        if (a.base > 0) {
+            const float4 *acc = tile_slot(a.acc, tile, cta, warp, lane);
+#pragma unroll
+            for (int j = 0; j < kCols / 4; ++j) {
+                const float4 v = acc[j * 32];
+                x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
+            }
+        }
+        if (a.base + a.rows < n_good) {
+            float4 *acc = tile_slot(a.acc, tile, cta, warp, lane);
+#pragma unroll
+            for (int j = 0; j < kCols / 4; ++j)
+                acc[j * 32] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+            return;
+        }
+    }
+    const float inv = 1.f / static_cast<float>(n_good > 1 ? n_good : 1);
+#pragma unroll
+    for (int j = 0; j < kCols; ++j)
+        x[j] *= inv;
+    store_rows<kSplit ? kF32 : kBf16>(x, out, off, col0, a.D, staging, lane);
+}
+
+template <int kWhat, bool kSplit>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    ce_product_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                      const __grid_constant__ CeArgs a, const WaitCfg w)
+{
+    const int cnt = ce_piece_rows(a);
+    if (cnt == 0 && (kWhat != kCeDw || a.base > 0))
+        return;  // the whole grid agrees; dW without any row is written as zeros by the first piece
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint8_t *staging = smem + kStages * kStageBytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(staging + kEpiWarps * kWarpStaging);
+    uint64_t *empty = full + kStages, *acc_full = empty + kStages, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
+    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile uint32_t *abort_flag = tmem_ptr + 1;
+    const int warp = warp_id(), lane = lane_id();
+    const int cta = static_cast<int>(cluster_ctarank());
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const Plan plan = make_plan<kWhat>(a, cnt, pairs);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 2 * kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kEpiWarps) {
+        tmem_alloc_pair(tmem_ptr, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // the other CTA's barriers are set up
+    tc_fence_after();
+    const uint32_t tbase = *tmem_ptr;
+    constexpr int kPerStep = kSplit ? kPlanePairs : 1;
+
+    if (warp == kEpiWarps) {
+        // ------------------------------------------------ loads
+        if (lane == 0) {
+            prefetch_tmap(&ta);
+            prefetch_tmap(&tb);
+            Units units(plan, pair, pairs);
+            Unit u;
+            uint32_t it = 0;
+            bool ok = true;
+            while (ok && units.next(u)) {
+                int m0, n0;
+                tile_origin<kWhat>(plan, u.tile, m0, n0);
+                m0 += cta * kHalf;
+                n0 += cta * kHalf;
+                for (int k = u.k0; ok && k < u.k1; ++k) {
+#pragma unroll 1
+                    for (int pp = 0; pp < kPerStep; ++pp, ++it) {
+                        // plane products, smallest first: (1,3) (3,1) (2,2) (1,2) (2,1) (1,1)
+                        const int pa = kSplit ? (0x021010 >> (4 * (5 - pp))) & 15 : 0;
+                        const int pb = kSplit ? (0x201100 >> (4 * (5 - pp))) & 15 : 0;
+                        const int s = it % kStages;
+                        if (*abort_flag || !mbar_wait(&empty[s], ((it / kStages) & 1) ^ 1, w, 0xa1)) {
+                            ok = false;
+                            break;
+                        }
+                        if (cta == 0)
+                            mbar_expect_tx(&full[s], 2 * kStageBytes);
+                        const uint32_t bar = cluster_addr(&full[s], 0);
+                        uint8_t *sa = smem + s * kStageBytes, *sb = sa + kOperandBytes;
+                        const int kc = k * kCeStep;
+                        if (kWhat == kCeDw) {
+                            tma_load_3d_pair(sa, &ta, bar, m0, kc, pa);
+                            tma_load_3d_pair(sa + kOperandBytes / 2, &ta, bar, m0 + 64, kc, pa);
+                        } else {
+                            tma_load_3d_pair(sa, &ta, bar, kc, m0, pa);
+                        }
+                        if (kWhat != kCeLogits) {
+                            tma_load_3d_pair(sb, &tb, bar, n0, kc, pb);
+                            tma_load_3d_pair(sb + kOperandBytes / 2, &tb, bar, n0 + 64, kc, pb);
+                        } else {
+                            tma_load_3d_pair(sb, &tb, bar, kc, n0, pb);
+                        }
+                    }
+                }
+            }
+            // the last uses of the stages: their releases arrive from CTA 0, and this CTA stays until they have
+            for (uint32_t i = it > kStages ? it - kStages : 0; ok && i < it; ++i)
+                ok = mbar_wait(&empty[i % kStages], (i / kStages) & 1, w, 0xa6);
+            if (!ok) {
+                *abort_flag = 1;
+                // wait (bounded) for the loads still in flight; CTA 0 holds their barriers
+                if (cta == 0)
+                    for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+                        mbar_wait(&full[i % kStages], (i / kStages) & 1, w, 0xaf);
+            }
+        }
+    } else if (warp == kEpiWarps + 1) {
+        // ------------------------------------------------ products
+        if (lane == 0 && cta == 0) {
+            constexpr uint32_t idesc = idesc_bf16(256, 256, kWhat == kCeDw, kWhat != kCeLogits);
+            Units units(plan, pair, pairs);
+            Unit u;
+            uint32_t it = 0, chunk = 0;
+            bool ok = true;
+            while (ok && units.next(u)) {
+                int left = (u.k1 - u.k0) * kPerStep;  // loads of this unit
+                while (ok && left > 0) {
+                    constexpr int most = kChunkSteps<kWhat, kSplit> * kPerStep;
+                    const int n = left < most ? left : most;  // loads of this accumulation
+                    const uint32_t acc = chunk & 1;
+                    if (*abort_flag || !mbar_wait_cluster(&acc_empty[acc], ((chunk >> 1) & 1) ^ 1, w, 0xa2)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    for (int i = 0; i < n; ++i, ++it) {
+                        const int s = it % kStages;
+                        if (!mbar_wait(&full[s], (it / kStages) & 1, w, 0xa3)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kOperandBytes;
+#pragma unroll
+                        for (int kk = 0; kk < kCeStep / 16; ++kk) {
+                            const uint64_t da = kWhat == kCeDw ? desc_sw128(sa + kk * 2048, kOperandBytes / 2, 1024)
+                                                               : desc_sw128(sa + kk * 32, 16, 1024);
+                            const uint64_t db = kWhat != kCeLogits
+                                                    ? desc_sw128(sb + kk * 2048, kOperandBytes / 2, 1024)
+                                                    : desc_sw128(sb + kk * 32, 16, 1024);
+                            mma_ss_pair(tbase + acc * 256, da, db, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+                        }
+                        mma_commit_pair(&empty[s]);
+                    }
+                    if (!ok)
+                        break;
+                    mma_commit_pair(&acc_full[acc]);
+                    ++chunk;
+                    left -= n;
+                }
+            }
+            if (!ok)
+                *abort_flag = 1;
+            mma_commit_pair(drain);
+        }
+        if (lane == 0)
+            mbar_wait(drain, 0, w, 0xa4);  // in both CTAs: every product and release is through
+    } else {
+        // ------------------------------------------------ results
+        Units units(plan, pair, pairs);
+        Unit u;
+        uint32_t chunk = 0;
+        const int col = (warp >> 2) * kCols;
+        uint8_t *stage = staging + warp * kWarpStaging;
+        bool ok = true;
+        while (ok && units.next(u)) {
+            int m0, n0;
+            tile_origin<kWhat>(plan, u.tile, m0, n0);
+            const int m = m0 + cta * kHalf + (warp & 3) * 32 + lane;
+            float x[kCols];
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+                x[j] = 0.f;
+            constexpr int per = kChunkSteps<kWhat, kSplit>;
+            const int chunks = (u.k1 - u.k0 + per - 1) / per;
+            for (int c = 0; c < chunks; ++c, ++chunk) {
+                const uint32_t acc = chunk & 1;
+                if (!mbar_wait_warp(&acc_full[acc], (chunk >> 1) & 1, w, 0xa5)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t t = tbase + acc * 256 + col + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+#pragma unroll
+                for (int j = 0; j < kCols; j += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(t + j, v);
+                    tmem_ld_wait(v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        x[j + i] += __uint_as_float(v[i]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(cluster_addr(&acc_empty[acc], 0));
+            }
+            if (!ok)
+                break;
+            if (u.run >= 0) {
+                float4 *slot = tile_slot(a.partial, 2 * pair + u.run, cta, warp, lane);
+#pragma unroll
+                for (int j = 0; j < kCols / 4; ++j)
+                    slot[j * 32] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+            } else if constexpr (kWhat == kCeLogits) {
+                finish_logits<kSplit>(a, x, cnt, m, n0 + col, stage, lane);
+            } else {
+                finish_grad<kWhat, kSplit>(a, x, cnt, u.tile, m, n0 + col, cta, warp, stage, lane);
+            }
+        }
+        if (!ok)
+            *abort_flag = 1;
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // both CTAs are done with each other's memory and TMEM
+    tc_fence_after();
+    if (warp == kEpiWarps)
+        tmem_dealloc_pair(tbase, 512);
+}
+
+// Adds the runs of the split tiles, in the order of the contraction.  One
+// block per (tile, CTA half), the warps as in the product kernel.
+template <int kWhat, bool kSplit>
+__global__ void __launch_bounds__(32 * kEpiWarps) ce_join_kernel(const __grid_constant__ CeArgs a, int pairs)
+{
+    extern __shared__ __align__(16) uint8_t join_staging[];
+    const int cnt = ce_piece_rows(a);
+    if (cnt == 0)
+        return;
+    const Plan p = make_plan<kWhat>(a, cnt, pairs);
+    const int split = blockIdx.x >> 1, cta = blockIdx.x & 1, tile = p.whole + split;
+    if (p.workers == 0 || tile >= p.mt * p.nt)
+        return;
+    const int64_t steps = static_cast<int64_t>(p.mt * p.nt - p.whole) * p.kb;
+    const int64_t t0 = static_cast<int64_t>(split) * p.kb, t1 = t0 + p.kb;
+    const int warp = warp_id(), lane = lane_id();
+    float x[kCols];
+#pragma unroll
+    for (int j = 0; j < kCols; ++j)
+        x[j] = 0.f;
+    // workers whose runs [steps w / workers, steps (w + 1) / workers) meet the tile
+    int first = static_cast<int>(t0 * p.workers / steps);
+    first = first > 0 ? first - 1 : 0;
+    for (int k = first; k < p.workers; ++k) {
+        const int64_t lo = steps * k / p.workers, hi = steps * (k + 1) / p.workers;
+        if (hi <= t0)
+            continue;
+        if (lo >= t1)
+            break;
+        const float4 *slot = tile_slot(a.partial, 2 * k + (lo < t0 ? 1 : 0), cta, warp, lane);
+#pragma unroll
+        for (int j = 0; j < kCols / 4; ++j) {
+            const float4 v = slot[j * 32];
+            x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
+        }
+    }
+    int m0, n0;
+    tile_origin<kWhat>(p, tile, m0, n0);
+    finish_grad<kWhat, kSplit>(a, x, cnt, tile, m0 + cta * kHalf + (warp & 3) * 32 + lane, n0 + (warp >> 2) * kCols,
+                               cta, warp, join_staging + warp * kWarpStaging, lane);
+}
+
+// --------------------------------------------------------------- host
+// Box of a K-major operand: 64 values of the contraction x 128 rows; of an
+// MN-major one: 64 columns x 64 values of the contraction.
+bool make_map(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64_t pitch, int planes, int box_rows)
+{
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                          static_cast<cuuint64_t>(planes)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch) * 2, static_cast<cuuint64_t>(pitch) * rows * 2};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kWhat, bool kSplit>
+cudaError_t launch(const CeArgs &a, const CUtensorMap &ta, const CUtensorMap &tb, cudaStream_t s)
+{
+    auto kernel = ce_product_kernel<kWhat, kSplit>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess)
+        return e;
+    // pairs resident at once: the schedule gives each an equal share
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (num_sms() / 2));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int pairs = 0;
+    e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
+    if (e != cudaSuccess)
+        return e;
+    pairs = std::max(1, std::min(std::min(pairs, num_sms() / 2), kCeMaxPairs));
+    kernel<<<2 * pairs, kThreads, kSmem, s>>>(ta, tb, a, wait_cfg());
+    if constexpr (kWhat != kCeLogits) {
+        // never split below this many steps: nothing to join
+        const int kb = ((kWhat == kCeDh ? a.V : a.rows) + kCeStep - 1) / kCeStep;
+        if (kb > kSplitGain) {
+            constexpr int smem = kEpiWarps * kWarpStaging;
+            e = cudaFuncSetAttribute(ce_join_kernel<kWhat, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess)
+                return e;
+            ce_join_kernel<kWhat, kSplit><<<2 * (pairs - 1), 32 * kEpiWarps, smem, s>>>(a, pairs);
+        }
+    }
+    return cudaGetLastError();
+}
+
+template <bool kSplit>
+cudaError_t product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh, const void *w, int64_t ldw,
+                    const void *g, cudaStream_t s)
+{
+    constexpr int planes = kSplit ? 3 : 1;
+    CUtensorMap ta, tb;
+    bool ok;
+    switch (what) {
+    case kCeLogits:
+        ok = make_map(&ta, h, a.D, a.rows, ldh, planes, kHalf) && make_map(&tb, w, a.D, a.V, ldw, planes, kHalf);
+        return ok ? launch<kCeLogits, kSplit>(a, ta, tb, s) : cudaErrorInvalidValue;
+    case kCeDh:
+        ok = make_map(&ta, g, a.V, a.rows, a.ldg, planes, kHalf) && make_map(&tb, w, a.D, a.V, ldw, planes, kCeStep);
+        return ok ? launch<kCeDh, kSplit>(a, ta, tb, s) : cudaErrorInvalidValue;
+    default:
+        ok = make_map(&ta, g, a.V, a.rows, a.ldg, planes, kCeStep) &&
+             make_map(&tb, h, a.D, a.rows, ldh, planes, kCeStep);
+        return ok ? launch<kCeDw, kSplit>(a, ta, tb, s) : cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+int ce_most_workers(CeProduct what, int rows, int D, int V)
+{
+    const int64_t mt = ((what == kCeDw ? V : rows) + kCeTile - 1) / kCeTile, nt = (D + kCeTile - 1) / kCeTile;
+    const int64_t kb = ((what == kCeDw ? rows : V) + kCeStep - 1) / kCeStep;
+    if (kb <= kSplitGain)
+        return 0;
+    return static_cast<int>(std::min<int64_t>(kCeMaxPairs, std::min<int64_t>(mt * nt, kCeMaxPairs) * kb / kMinRun));
+}
+
+cudaError_t launch_ce_product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh, const void *w, int64_t ldw,
+                              const void *g, int esize, cudaStream_t s)
+{
+    return esize == 2 ? product<false>(what, a, h, ldh, w, ldw, g, s) : product<true>(what, a, h, ldh, w, ldw, g, s);
+}
+
+}  // namespace uly

@@ -218,7 +218,10 @@ struct NormRopeParams {
     int to_head;
     int half;  // rot / 2
     float eps;
-    int splits, rows_per_split;  // set by the launch
+    // set by the launch: warps per token, rows each takes, and 2^32 / (H/P)
+    // rounded up (0 for H/P = 1)
+    int splits, rows_per_split;
+    unsigned magic_q, magic_k;
     uint64_t turn[kNormRopeMaxHalf];  // inv_freq / 2 pi as a 64-bit fraction of a turn
     uint8_t axis[kNormRopeMaxHalf];
 };

@@ -235,6 +235,29 @@ def test_zero_nan_and_infinite_rows_stay_in_their_rows(uly):
         assert bytes_equal(a, b)
 
 
+@pytest.mark.parametrize("inter", [False, True])
+def test_values_that_do_not_turn_are_copied(uly, inter):
+    """Without a norm, values from rot_dim on are untouched, whatever stands
+    beside them (compared as values: a conversion to bf16 has one NaN, so a
+    NaN's payload bits do not come back)."""
+    same = lambda a, b: torch.equal(torch.isnan(a.cpu()), torch.isnan(b)) and bytes_equal(
+        a.cpu().masked_fill(torch.isnan(a.cpu()), 0), b.masked_fill(torch.isnan(b), 0))
+    c = make(1, 1, 4, 2, 2, 128, BF16, 32, norm=False, positions="far")
+    c["x"][..., 40] = float("inf")
+    c["x"][..., 100] = float("nan")
+    _, y, _ = run_fwd(uly, c, inter)
+    x = split(c, c["x"])
+    for i in range(2):
+        assert same(y[i].reshape(x[i].shape)[..., 32:], x[i][..., 32:])
+        assert torch.isfinite(y[i][..., :32].float()).all()
+    dx = [torch.empty_like(t, device="cuda") for t in x]
+    dy = [t.cuda().reshape(d.shape) for t, d in zip(x, c["dy"])]
+    uly.ulysses_qkv_norm_rope_bwd(None, None, *dy, *dx, 1, **kwargs(c, inter))
+    for i in range(2):
+        assert same(dx[i][..., 32:], x[i][..., 32:])
+        assert torch.isfinite(dx[i][..., :32].float()).all()
+
+
 def test_weight_gradients_are_the_same_on_every_run(uly):
     c = make(2, 1, 3000, 8, 2, 128, BF16, 128)
     x = split(c, c["x"].cuda())
