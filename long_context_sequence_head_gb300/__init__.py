@@ -354,25 +354,27 @@ class _RopeDesc(ctypes.Structure):
 
 def _rope_desc(inv_freq, positions, axis_of_freq, interleaved, shape):
     """The host description of a rotation and the arrays it points to."""
-    inv = np.ascontiguousarray(np.asarray([] if inv_freq is None else inv_freq, dtype=np.float64))
+    inv = inv_freq
+    if not (isinstance(inv, np.ndarray) and inv.dtype == np.float64 and inv.flags.c_contiguous):
+        inv = np.ascontiguousarray(np.asarray([] if inv is None else inv, dtype=np.float64))
     if inv.ndim != 1:
         raise ValueError(f"inv_freq must hold rot_dim/2 frequencies, got shape {inv.shape}")
     axes, axis = 1, None
     if positions is not None:
         if positions.dtype != torch.int64:
             raise ValueError(f"positions must be int64, got {positions.dtype}")
-        if tuple(positions.shape) == shape:
-            pass
-        elif positions.dim() == 4 and tuple(positions.shape[1:]) == shape:
+        if positions.shape != shape:
+            if positions.dim() != 4 or positions.shape[1:] != shape:
+                raise ValueError(f"positions must be {list(shape)} or [axes] + {list(shape)}, "
+                                 f"got {list(positions.shape)}")
             axes = positions.shape[0]
-        else:
-            raise ValueError(f"positions must be {list(shape)} or [axes] + {list(shape)}, got {list(positions.shape)}")
     if axis_of_freq is not None:
         axis = np.ascontiguousarray(np.asarray(axis_of_freq, dtype=np.int32))
         if axis.shape != inv.shape:
             raise ValueError(f"axis_of_freq must name one axis per frequency, got shape {axis.shape}")
-    desc = _RopeDesc(positions.data_ptr() if positions is not None else None, inv.ctypes.data,
-                     axis.ctypes.data if axis is not None else None, 2 * len(inv), axes, int(bool(interleaved)))
+    desc = _RopeDesc(None if positions is None else positions.data_ptr(), inv.__array_interface__["data"][0],
+                     None if axis is None else axis.__array_interface__["data"][0], 2 * inv.shape[0], axes,
+                     1 if interleaved else 0)
     return desc, (inv, axis)
 
 
@@ -381,6 +383,8 @@ def _token_stride(name, t, d) -> int:
     heads are contiguous and whose tokens are evenly spaced, as a slice of
     heads of a packed [P][B][N/P][Hq+2Hkv][d] projection output is."""
     P, B, Np, H, dd = t.shape
+    if t.is_contiguous():
+        return H * d
     sP, sB, sT, sH, sd = t.stride()
     ok = dd == d and sd == 1 and (H == 1 or sH == d)
     step = sT if Np > 1 else (sB if B > 1 else (sP if P > 1 else H * d))
@@ -391,32 +395,48 @@ def _token_stride(name, t, d) -> int:
 
 def _norm_rope_args(P, like, far, weights, to_head, positions):
     """Checks shapes, types and devices before any pointer reaches the library.
-    like: (name, tensor or None, heads) in the sequence layout, q first; far:
+    like: (name, tensor or None, heads) in the sequence layout, Q's first; far:
     the same on the other side; returns (B, Np, d)."""
     q = like[0][1]
     if q.dim() != 5:
         raise ValueError(f"{like[0][0]} must be 5-D [P][B][N/P][H][d], got {tuple(q.shape)}")
-    if q.shape[0] != P:
-        raise ValueError(f"the leading dimension of {like[0][0]} must be P={P}, got {q.shape[0]}")
-    _, B, Np, _, d = q.shape
-    for name, t, H in like:
-        if t is not None and (tuple(t.shape) != (P, B, Np, H, d) or t.dtype != q.dtype):
-            raise ValueError(f"{name} must be {(P, B, Np, H, d)} of {q.dtype}, got {tuple(t.shape)} of {t.dtype}")
+    Ps, B, Np, _, d = q.shape
+    if Ps != P:
+        raise ValueError(f"the leading dimension of {like[0][0]} must be P={P}, got {Ps}")
+    dtype, device = q.dtype, q.get_device()
+
+    def check(name, t, want):
+        if t.shape != want or t.dtype is not dtype:
+            raise ValueError(f"{name} must be {list(want)} of {dtype}, got {list(t.shape)} of {t.dtype}")
+
+    def place(t, whole):
+        at = t.get_device()
+        if at < 0:
+            raise ValueError("tensors must live on a CUDA device")
+        if at != device:
+            raise ValueError(f"all tensors must live on {q.device}, got {t.device}")
+        if whole and not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+
+    whole = [] if positions is None else [positions]
     for name, t, H in far:
         if to_head and H % P:
             raise ValueError(f"the heads of {name} ({H}) must be a multiple of P={P}")
-        want = (P, B, Np * P, H // P, d) if to_head else (P, B, Np, H, d)
-        if t is not None and (tuple(t.shape) != want or t.dtype != q.dtype):
-            raise ValueError(f"{name} must be {want} of {q.dtype}, got {tuple(t.shape)} of {t.dtype}")
-    for name, t in weights:
-        if t is not None and (tuple(t.shape) != (d,) or t.dtype != q.dtype):
-            raise ValueError(f"{name} must be [{d}] of {q.dtype}, got {list(t.shape)} of {t.dtype}")
-    for t in [t for _, t, _ in like] + [t for _, t, _ in far] + [t for _, t in weights] + [positions]:
         if t is not None:
-            _on(q, t)
-    for t in [t for _, t, _ in far] + [t for _, t in weights] + [positions]:
-        if t is not None and not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
+            check(name, t, (P, B, Np * P, H // P, d) if to_head else (P, B, Np, H, d))
+            whole.append(t)
+    for name, t in weights:
+        if t is not None:
+            check(name, t, (d,))
+            whole.append(t)
+    for name, t, H in like:
+        if t is not None:
+            check(name, t, (P, B, Np, H, d))
+    for _, t, _ in like:
+        if t is not None:
+            place(t, False)
+    for t in whole:
+        place(t, True)
     return B, Np, d
 
 
@@ -432,13 +452,13 @@ def _ptr(t):
 
 
 class _Launch:
-    """The device and stream of a call: `with _Launch(device, stream) as s`
-    makes the tensors' device current and yields the raw stream; scratch()
-    hands out a workspace that the allocator keeps until that stream is done
-    with it."""
+    """The device and stream of a call: makes the tensors' device current and
+    allocates on the call's stream, so that neither earlier work on the
+    current stream nor later reuse can meet the kernels' use of the memory."""
+    __slots__ = ("device", "stream", "guard")
 
     def __init__(self, device, stream):
-        if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device != device:
             raise ValueError(f"the stream must belong to {device}")
         self.device, self.stream = device, stream
         self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
@@ -453,21 +473,25 @@ class _Launch:
             self.guard.__exit__(*exc)
 
     def raw(self):
+        if self.stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
         return _stream(self.stream)
 
-    def scratch(self, workspace, nbytes):
-        if workspace is not None:
-            if not workspace.is_cuda or workspace.device != self.device or not workspace.is_contiguous():
-                raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
-            return _workspace(workspace, nbytes, self.device)
-        return self.keep(_workspace(None, nbytes, self.device))
+    def empty(self, n, dtype):
+        if self.stream is None:
+            return torch.empty(n, dtype=dtype, device=self.device)
+        s = self.stream
+        if not isinstance(s, torch.cuda.Stream):
+            s = torch.cuda.ExternalStream(int(s), device=self.device) if int(s) else torch.cuda.default_stream(self.device)
+        with torch.cuda.stream(s):
+            return torch.empty(n, dtype=dtype, device=self.device)
 
-    def keep(self, t):
-        """t, allocated on the current stream, not reused before the call's stream is done with it."""
-        if self.stream is not None:
-            t.record_stream(self.stream if isinstance(self.stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
-                int(self.stream), device=self.device))
-        return t
+    def scratch(self, workspace, nbytes):
+        if workspace is None:
+            return self.empty(max(nbytes, 256), torch.uint8)
+        if not workspace.is_cuda or workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
+        return _workspace(workspace, nbytes, self.device)
 
 
 def ulysses_qkv_norm_rope_workspace_size(d: int) -> int:
@@ -801,9 +825,9 @@ def ulysses_sharded_linear_ce_loss(hidden, weight, labels, P: int, dhidden: Opti
     dev, grad = hidden.device, dhidden is not None or dweight is not None
     with _Launch(dev, stream) as at:
         if outputs is None:
-            shard_loss = at.keep(torch.empty(P, dtype=torch.float32, device=dev))
-            shard_good = at.keep(torch.empty(P, dtype=torch.int64, device=dev))
-            total = at.keep(torch.empty(4, dtype=torch.float32, device=dev))
+            shard_loss = at.empty(P, torch.float32)
+            shard_good = at.empty(P, torch.int64)
+            total = at.empty(1, torch.float32)
         need = ulysses_sharded_linear_ce_workspace_size(B, Np * P, D, V, P, grad, hidden.dtype)
         ws = at.scratch(workspace, need)
         _check("ulysses_sharded_linear_ce_loss", load().ulysses_sharded_linear_ce_loss(

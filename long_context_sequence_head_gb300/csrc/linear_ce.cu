@@ -26,6 +26,10 @@ constexpr int kRowThreads = 512;
 // piece to piece (read and written once each) over more products; the buffer
 // of exponentials grows with them (2 bytes a value, 10 in fp32).
 constexpr int kPieceBf16 = 8192, kPieceFp32 = 2048;
+// From this many rows on, a bf16 weight whose rows are not whole 128-byte
+// lines is copied to a pitch that is (TMA reads two lines for every 128 bytes
+// of a row that starts inside one).
+constexpr int64_t kLayRows = 1024;
 
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu); }
@@ -79,41 +83,174 @@ __device__ __forceinline__ void load8(const float *row, int i, int D, float (&x)
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
-// Good rows in order: index[i] = row of the i-th one, n_good = how many.
-__global__ void __launch_bounds__(1024) compact_kernel(const int32_t *__restrict__ shifted, int64_t rows,
-                                                       int32_t *__restrict__ index, int *__restrict__ n_good)
+// One block: the labels shifted over the whole sequence, each shard's good
+// rows, and the good rows in order (index[i] = row of the i-th one).  A row's
+// loss starts as 0.  Labels out of range are reported and ignored.  4096 rows a
+// round: 2 us each, against 4 ms of products behind as many rows.
+__global__ void __launch_bounds__(1024) labels_kernel(const int64_t *__restrict__ labels, int32_t *__restrict__ shifted,
+                                                      unsigned long long *__restrict__ good,
+                                                      float *__restrict__ row_loss, int32_t *__restrict__ index,
+                                                      int *__restrict__ n_good, int *__restrict__ shards_done,
+                                                      unsigned rows, unsigned Np, unsigned B, int P, int V,
+                                                      unsigned *status)
 {
+    constexpr int kEach = 4;
     __shared__ int warp_sum[32];
+    for (int r = threadIdx.x; r < P; r += 1024)
+        good[r] = 0;
+    if (threadIdx.x == 0)
+        *shards_done = 0;
+    __syncthreads();
     int done = 0;
-    for (int64_t base = 0; base < rows; base += 1024) {
-        const int64_t r = base + threadIdx.x;
-        const bool good = r < rows && shifted[r] >= 0;
-        const unsigned mask = __ballot_sync(0xffffffffu, good);
-        if (lane_id() == 0)
-            warp_sum[warp_id()] = __popc(mask);
-        __syncthreads();
-        int before = done, all = 0;
-        for (int w = 0; w < 32; ++w) {
-            before += w < warp_id() ? warp_sum[w] : 0;
-            all += warp_sum[w];
+    for (int64_t base = 0; base < rows; base += 1024 * kEach) {
+        const int64_t first = base + static_cast<int64_t>(threadIdx.x) * kEach;
+        int32_t y[kEach];
+        int mine = 0;
+        // place in the shard's sequence; the next token is the next row, or,
+        // at the end of a shard, the first of the same sequence in the next
+        unsigned t = static_cast<unsigned>(first < rows ? first : 0) % Np;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i, ++t) {
+            y[i] = -100;
+            if (first + i >= rows)
+                continue;
+            if (t == Np)
+                t = 0;
+            const int64_t next = first + i + 1 + (t + 1 == Np ? static_cast<int64_t>(B - 1) * Np : 0);
+            if (next < rows) {
+                const int64_t lab = labels[next];
+                if (lab >= 0 && lab < V)
+                    y[i] = static_cast<int32_t>(lab);
+                else if (lab != -100)
+                    atomicOr(status, kDevBadArg);
+            }
+            mine += y[i] >= 0;
         }
-        if (good)
-            index[before + __popc(mask & ((1u << lane_id()) - 1u))] = static_cast<int32_t>(r);
-        done += all;
+        // places of this thread's good rows among all
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane_id() >= o ? v : 0;
+        }
+        if (lane_id() == 31)
+            warp_sum[warp_id()] = upto;
+        __syncthreads();
+        int sum = warp_sum[lane_id()];  // every warp scans the 32 sums
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            sum += lane_id() >= o ? v : 0;
+        }
+        const int before = __shfl_sync(0xffffffffu, sum, warp_id() > 0 ? warp_id() - 1 : 0);
+        int at = done + upto - mine + (warp_id() > 0 ? before : 0);
+        done += __shfl_sync(0xffffffffu, sum, 31);
+        // a warp's 128 rows are of one shard, mostly
+        const int64_t w0 = base + static_cast<int64_t>(warp_id()) * 32 * kEach;
+        const unsigned r0 = static_cast<unsigned>(w0 < rows ? w0 : 0) / (Np * B);
+        const bool one = w0 + 32 * kEach <= static_cast<int64_t>(r0 + 1) * Np * B;
+        if (one && lane_id() == 31 && upto > 0)
+            atomicAdd(&good[r0], static_cast<unsigned long long>(upto));
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            if (first + i >= rows)
+                continue;
+            shifted[first + i] = y[i];
+            row_loss[first + i] = 0.f;
+            if (y[i] >= 0) {
+                index[at++] = static_cast<int32_t>(first + i);
+                if (!one)
+                    atomicAdd(&good[static_cast<unsigned>(first + i) / (Np * B)], 1ull);
+            }
+        }
         __syncthreads();
     }
     if (threadIdx.x == 0)
         *n_good = done;
 }
 
+// A sum held as hi + lo: 48 bits without the slow 64-bit units.
+__device__ __forceinline__ float2 two_sum(float2 s, float2 v)
+{
+    const float hi = s.x + v.x, t = hi - s.x;
+    if (!isfinite(hi))
+        return make_float2(hi, 0.f);
+    const float err = (s.x - (hi - t)) + (v.x - t) + s.y + v.y;
+    const float top = hi + err;
+    return make_float2(top, err - (top - hi));
+}
+
+__device__ __forceinline__ float2 warp_two_sum(float2 s)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        s = two_sum(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)));
+    return s;
+}
+
+// Every shard's mean over its good rows, a block per shard, and from the last
+// block to finish the total sum_r loss_r good_r / max(sum_r good_r, 1).  Every
+// sum is taken in one order.
+__global__ void __launch_bounds__(1024) totals_kernel(const float *__restrict__ row_loss,
+                                                      const unsigned long long *__restrict__ good, int64_t per_shard,
+                                                      int P, float *shard_loss, int64_t *__restrict__ shard_good,
+                                                      float *__restrict__ total, int *__restrict__ shards_done)
+{
+    __shared__ float2 part[32];
+    __shared__ int last;
+    const int r = blockIdx.x;
+    const float *base = row_loss + r * per_shard;
+    float2 s = make_float2(0.f, 0.f);
+    for (int64_t i = threadIdx.x; i < per_shard; i += 1024)
+        s = two_sum(s, make_float2(base[i], 0.f));
+    s = warp_two_sum(s);
+    if (lane_id() == 0)
+        part[warp_id()] = s;
+    __syncthreads();
+    if (warp_id() == 0) {
+        s = warp_two_sum(part[lane_id()]);
+        if (lane_id() == 0) {
+            const long long n = static_cast<long long>(good[r]);
+            shard_loss[r] = n > 0 ? static_cast<float>((static_cast<double>(s.x) + s.y) / static_cast<double>(n)) : 0.f;
+            shard_good[r] = n;
+            __threadfence();
+            last = atomicAdd(shards_done, 1) == P - 1;
+            __threadfence();
+        }
+    }
+    __syncthreads();
+    if (!last || warp_id() != 0)
+        return;
+    double num = 0.0;
+    long long den = 0;
+    for (int k = lane_id(); k < P; k += 32) {
+        const long long n = static_cast<long long>(good[k]);
+        num += static_cast<double>(__ldcg(shard_loss + k)) * static_cast<double>(n);
+        den += n;
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+        num += __shfl_xor_sync(0xffffffffu, num, o);
+        den += __shfl_xor_sync(0xffffffffu, den, o);
+    }
+    if (lane_id() == 0)
+        *total = static_cast<float>(num / static_cast<double>(den > 1 ? den : 1));
+}
+
 // The piece's hidden rows next to each other (fp32: as planes), with their
-// labels; zeros up to a multiple of 64 rows, where dW's contraction ends.
+// labels; zeros up to a multiple of 64 rows, where dW's contraction ends.  The
+// first piece also clears the gradient of the rows without a label: its block
+// r looks at row r of the call.
 template <bool kSplit>
 __global__ void gather_kernel(const __grid_constant__ CeArgs a, const void *__restrict__ hidden,
                               const int32_t *__restrict__ shifted, int32_t *__restrict__ label, void *__restrict__ out,
-                              int64_t ldh)
+                              int64_t ldh, int64_t rows)
 {
     const int cnt = ce_piece_rows(a), r = blockIdx.x;
+    if (a.base == 0 && a.dh != nullptr && r < rows && shifted[r] < 0) {
+        const int vecs = a.D * (kSplit ? 4 : 2) / 16;
+        for (int i = threadIdx.x; i < vecs; i += blockDim.x)
+            static_cast<uint4 *>(a.dh)[static_cast<int64_t>(r) * vecs + i] = make_uint4(0, 0, 0, 0);
+    }
     if (r >= (cnt + kCeStep - 1) / kCeStep * kCeStep)
         return;
     const bool live = r < cnt;
@@ -135,25 +272,22 @@ __global__ void gather_kernel(const __grid_constant__ CeArgs a, const void *__re
     }
 }
 
-// fp32 weight as planes.
-__global__ void split_weight_kernel(const float *__restrict__ w, int D, int V, uint16_t *__restrict__ out, int64_t ldw)
+// The weight as the products want it: fp32 as planes, bf16 on a pitch of
+// whole 128-byte lines.
+template <bool kSplit>
+__global__ void lay_weight_kernel(const void *__restrict__ w, int D, int V, uint16_t *__restrict__ out, int64_t ldw)
 {
     const int64_t v = blockIdx.x;
     for (int i = threadIdx.x * 8; i < D; i += blockDim.x * 8) {
-        float x[8];
-        load8(w + v * D, i, D, x);
-        store_planes(out + v * ldw + i, ldw * V, x);
+        if constexpr (kSplit) {
+            float x[8];
+            load8(static_cast<const float *>(w) + v * D, i, D, x);
+            store_planes(out + v * ldw + i, ldw * V, x);
+        } else {
+            *reinterpret_cast<uint4 *>(out + v * ldw + i) =
+                *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w) + v * D + i);
+        }
     }
-}
-
-// Zero gradient of the rows without a label.
-__global__ void zero_ignored_kernel(const int32_t *__restrict__ shifted, int vecs, uint4 *__restrict__ dhidden)
-{
-    const int64_t r = blockIdx.x;
-    if (shifted[r] >= 0)
-        return;
-    for (int i = threadIdx.x; i < vecs; i += blockDim.x)
-        dhidden[r * vecs + i] = make_uint4(0, 0, 0, 0);
 }
 
 // One CTA per row of the piece: the row's loss, and with a gradient e -> g, in
@@ -241,6 +375,7 @@ struct Layout {
     size_t good, n_good, shifted, row_loss, index, label, target, stats, h, w, e, g, acc, partial, total;
     int64_t ldh, ldg;
     int rows, stat_tiles;
+    bool lay_weight;
 };
 
 Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
@@ -250,13 +385,13 @@ Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
     const bool split = esize == 4;
     L.rows = static_cast<int>(std::min<int64_t>(split ? kPieceFp32 : kPieceBf16, (T + 63) / 64 * 64));
     L.ldg = (V + 63) / 64 * 64;
-    L.ldh = (D + 7) / 8 * 8;
+    L.ldh = (D + 63) / 64 * 64;
     L.stat_tiles = (V + kCeStatCols - 1) / kCeStatCols;
     const size_t planes = split ? 3 : 1, kept = static_cast<size_t>(L.rows) * L.ldg;
     size_t o = 0;
     auto take = [&](size_t &at, size_t bytes) { at = o, o += up(bytes); };
     take(L.good, sizeof(unsigned long long) * P);
-    take(L.n_good, sizeof(int));
+    take(L.n_good, 2 * sizeof(int));
     take(L.shifted, sizeof(int32_t) * T);
     take(L.row_loss, sizeof(float) * T);
     take(L.index, sizeof(int32_t) * T);
@@ -264,7 +399,8 @@ Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
     take(L.target, sizeof(float) * L.rows);
     take(L.stats, sizeof(float2) * L.rows * static_cast<size_t>(L.stat_tiles));
     take(L.h, planes * L.rows * L.ldh * 2);
-    if (split)
+    L.lay_weight = split || (D % 64 != 0 && grad && T >= kLayRows);
+    if (L.lay_weight)
         take(L.w, planes * V * L.ldh * 2);
     if (grad) {
         take(L.g, planes * kept * 2);
@@ -313,26 +449,23 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
     a.dw = dweight;
     a.acc = reinterpret_cast<float *>(ws + L.acc);
     a.partial = reinterpret_cast<float *>(ws + L.partial);
-    cudaError_t e = launch_shift_count(labels, shifted, good, B, N, P, V, s);
-    if (e == cudaSuccess)
-        e = cudaMemsetAsync(row_loss, 0, sizeof(float) * rows, s);
-    if (e != cudaSuccess)
-        return e;
-    compact_kernel<<<1, 1024, 0, s>>>(shifted, rows, index, a.n_good);
-    if (dhidden)
-        zero_ignored_kernel<<<static_cast<unsigned>(rows), 128, 0, s>>>(shifted, D * kEsize / 16,
-                                                                        static_cast<uint4 *>(dhidden));
+    int *shards_done = a.n_good + 1;
+    labels_kernel<<<1, 1024, 0, s>>>(labels, shifted, good, row_loss, index, a.n_good, shards_done,
+                                     static_cast<unsigned>(rows), static_cast<unsigned>(N / P),
+                                     static_cast<unsigned>(B), P, V, device_status_ptr());
+    cudaError_t e = cudaSuccess;
     const void *w = weight;
     int64_t ldw = D;
-    if (kSplit) {
+    if (L.lay_weight) {
         w = ws + L.w;
         ldw = L.ldh;
-        split_weight_kernel<<<V, 128, 0, s>>>(static_cast<const float *>(weight), D, V,
-                                              reinterpret_cast<uint16_t *>(ws + L.w), ldw);
+        lay_weight_kernel<kSplit><<<V, 128, 0, s>>>(weight, D, V, reinterpret_cast<uint16_t *>(ws + L.w), ldw);
     }
     for (int64_t base = 0; base < rows; base += L.rows) {
         a.base = base;
-        gather_kernel<kSplit><<<L.rows, 128, 0, s>>>(a, hidden, shifted, label, ws + L.h, L.ldh);
+        const int64_t blocks = base == 0 ? std::max<int64_t>(rows, L.rows) : L.rows;
+        gather_kernel<kSplit><<<static_cast<unsigned>(blocks), 128, 0, s>>>(a, hidden, shifted, label, ws + L.h, L.ldh,
+                                                                           rows);
         e = launch_ce_product(kCeLogits, a, ws + L.h, L.ldh, w, ldw, g, kEsize, s);
         if (e != cudaSuccess)
             return e;
@@ -344,7 +477,8 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
         if (e != cudaSuccess)
             return e;
     }
-    return launch_shard_totals(row_loss, good, shard_loss, shard_good, total, B, N, P, s);
+    totals_kernel<<<P, 1024, 0, s>>>(row_loss, good, rows / P, P, shard_loss, shard_good, total, shards_done);
+    return cudaGetLastError();
 }
 
 }  // namespace

@@ -1,8 +1,8 @@
 // The three matrix products of the fused LM-head loss on the 5th-generation
 // tensor cores, one persistent kernel per product.
 //
-// A CTA pair owns a 256 x 256 output tile: each CTA loads its 128 rows of A
-// and its 128 columns of B (TMA, 128-byte swizzle), one thread of the pair
+// A CTA pair owns a 256 x 256 output tile (fewer columns where D asks for it):
+// each CTA loads its 128 rows of A and its 128 columns of B (TMA, 128-byte swizzle), one thread of the pair
 // issues tcgen05.mma.cta_group::2 (M = 256, N = 256), and each CTA's TMEM holds
 // 128 rows of the fp32 result, twice, so that one tile is written out while
 // the next is formed.  A pair reads half of what two single CTAs would: 64
@@ -30,6 +30,8 @@
 // fp32 (kSplit): every operand is three bf16 planes (x = x1 + x2 + x3 up to
 // 2^-26 of x) and a product is the six plane products above 2^-24, smallest
 // first; an accumulator takes 64 values of the contraction (24 instructions).
+#include <atomic>
+
 #include "linear_ce.h"
 
 namespace uly {
@@ -46,6 +48,7 @@ constexpr int kWarpStaging = 32 * 256;                   // 32 rows of 256 bytes
 constexpr int kBars = 2 * kStages + 5;
 constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kWarpStaging + 8 * kBars + 16 + 1024;
 constexpr int kPlanePairs = 6;
+constexpr int kCeMaxDevices = 64;
 constexpr int kMinRun = 8;       // least steps of a run
 constexpr int kSplitGain = 32;   // steps a split must save
 
@@ -55,6 +58,7 @@ constexpr int kChunkSteps = kSplit ? 1 : (kWhat == kCeLogits ? 8 : 64);
 // ------------------------------------------------------------- schedule
 struct Plan {
     int mt, nt, kb;   // tiles along the rows and columns of the result, steps of the contraction
+    int cols;         // columns of a tile
     int whole;        // tiles [0, whole) are done by one pair each
     int workers;      // pairs sharing the tiles from `whole` on
 };
@@ -82,6 +86,8 @@ __device__ __forceinline__ Plan make_plan(const CeArgs &a, int cnt, int pairs)
     p.mt = (M + kCeTile - 1) / kCeTile;
     p.nt = (N + kCeTile - 1) / kCeTile;
     p.kb = (K + kCeStep - 1) / kCeStep;
+    // D in equal tiles: 776 as four of 224 instead of three of 256 and one of 8
+    p.cols = kWhat == kCeLogits ? kCeTile : ((N + p.nt - 1) / p.nt + 31) / 32 * 32;
     p.workers = 0;
     p.whole = p.mt * p.nt;
     if (kWhat != kCeLogits)  // a softmax needs whole sums
@@ -135,7 +141,7 @@ __device__ __forceinline__ void tile_origin(const Plan &p, int tile, int &m0, in
         m0 = tile % p.mt * kCeTile;
     } else {
         m0 = tile / p.nt * kCeTile;
-        n0 = tile % p.nt * kCeTile;
+        n0 = tile % p.nt * p.cols;
     }
 }
 
@@ -155,56 +161,90 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return r;
 }
 
+__device__ __forceinline__ uint4 words(const float *v)
+{
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+
+__device__ __forceinline__ uint4 bf16s(const float *v)
+{
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
+}
+
 // The warp's 32 rows x 128 columns (row = lane) to memory, 256 bytes of a row
 // per half warp: through shared memory, units of 16 bytes permuted within the
-// row so that neither side meets a bank conflict.  row_off: element offset of
-// this lane's row, negative: not written.  Columns from `limit` on are not
-// written (a multiple of 16 bytes).
-enum OutType { kBf16, kF16, kF32 };
-template <OutType kType>
-__device__ __forceinline__ void store_rows(const float (&x)[kCols], void *out, int64_t row_off, int col0, int limit,
-                                           uint8_t *staging, int lane)
+// row so that neither side meets a bank conflict.  row: where this lane's row
+// goes, negative: nowhere.  Columns from `limit` on are not written (a
+// multiple of 16 bytes).
+template <bool kF32>
+__device__ __forceinline__ void store_rows(const float (&x)[kCols], void *out, int row, int64_t pitch, int col0,
+                                           int limit, uint8_t *staging, int lane)
 {
-    constexpr int kPer = kType == kF32 ? 4 : 8;  // values per unit
+    constexpr int kPer = kF32 ? 4 : 8;  // values per unit
     constexpr int kParts = kCols / (16 * kPer);
 #pragma unroll
     for (int part = 0; part < kParts; ++part) {
 #pragma unroll
         for (int u = 0; u < 16; ++u) {
             const float *v = x + (part * 16 + u) * kPer;
-            uint4 val;
-            if constexpr (kType == kF32)
-                val = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                 __float_as_uint(v[3]));
-            else if constexpr (kType == kBf16)
-                val = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                 pack_bf16x2(v[6], v[7]));
-            else
-                val = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]),
-                                 pack_f16x2(v[6], v[7]));
-            *reinterpret_cast<uint4 *>(staging + lane * 256 + ((u ^ (lane & 15)) << 4)) = val;
+            *reinterpret_cast<uint4 *>(staging + lane * 256 + ((u ^ (lane & 15)) << 4)) = kF32 ? words(v) : bf16s(v);
         }
         __syncwarp();
         const int u = lane & 15, col = col0 + (part * 16 + u) * kPer;
+        uint8_t *to = static_cast<uint8_t *>(out) + static_cast<int64_t>(col) * (16 / kPer);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const int row = 2 * i + (lane >> 4);
-            const int64_t off = __shfl_sync(0xffffffffu, row_off, row);
-            const uint4 val = *reinterpret_cast<const uint4 *>(staging + row * 256 + ((u ^ (row & 15)) << 4));
-            if (off >= 0 && col < limit)
-                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(out) + (off + col) * (16 / kPer)) = val;
+            const int r = 2 * i + (lane >> 4), at = __shfl_sync(0xffffffffu, row, r);
+            const uint4 val = *reinterpret_cast<const uint4 *>(staging + r * 256 + ((u ^ (r & 15)) << 4));
+            if (at >= 0 && col < limit)
+                *reinterpret_cast<uint4 *>(to + at * (pitch * (16 / kPer))) = val;
         }
         __syncwarp();
+    }
+}
+
+// The exponentials to their buffer by TMA: boxes of 32 rows x 128 bytes in the
+// swizzled layout of the map, two at a time.  Rows past the piece's last are
+// written too where the buffer has them; nobody reads them.
+template <bool kSplit>
+__device__ __forceinline__ void store_exponentials(const CUtensorMap *te, const float (&x)[kCols], int row0, int col0,
+                                                   int limit, uint8_t *staging, int lane)
+{
+    constexpr int kPer = kSplit ? 4 : 8, kBox = 8 * kPer;  // values per unit, columns per box
+#pragma unroll
+    for (int part = 0; part < kCols / (2 * kBox); ++part) {
+        if (lane == 0)
+            bulk_wait_read<0>();  // what was staged before is on its way
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+            const float *v = x + (part * 16 + u) * kPer;
+            const uint4 val = kSplit ? words(v)
+                                     : make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]),
+                                                  pack_f16x2(v[4 % kPer], v[5 % kPer]),
+                                                  pack_f16x2(v[6 % kPer], v[7 % kPer]));
+            *reinterpret_cast<uint4 *>(staging + (u >> 3) * 4096 + lane * 128 + (((u & 7) ^ (lane & 7)) << 4)) = val;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+                if (col0 + (2 * part + b) * kBox < limit)
+                    tma_store_2d(te, staging + b * 4096, col0 + (2 * part + b) * kBox, row0);
+            bulk_commit();
+        }
     }
 }
 
 // Logits: the row's maximum and sum over this warp's columns, its target's
 // logit, and the exponentials.
 template <bool kSplit>
-__device__ __forceinline__ void finish_logits(const CeArgs &a, float (&x)[kCols], int cnt, int m, int col0,
-                                              uint8_t *staging, int lane)
+__device__ __forceinline__ void finish_logits(const CeArgs &a, const CUtensorMap *te, float (&x)[kCols], int cnt, int m,
+                                              int col0, uint8_t *staging, int lane)
 {
-    if (col0 >= a.V)
+    if (col0 >= a.V || m - lane >= cnt)
         return;
     const bool live = m < cnt;
     const int y = live ? a.label[m] : -1;
@@ -229,62 +269,70 @@ __device__ __forceinline__ void finish_logits(const CeArgs &a, float (&x)[kCols]
         pm[j & 7] = fmaxf(pm[j & 7], x[j]);
     const float c = kLog2e * fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
                                    fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
-    float ps[4] = {0.f, 0.f, 0.f, 0.f};
+    const float2 l2 = make_float2(kLog2e, kLog2e), c2 = make_float2(-c, -c);
+    float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-        x[j] = ex2_approx(fmaf(x[j], kLog2e, -c));
-        ps[j & 3] += x[j];
+    for (int j = 0; j < kCols; j += 2) {
+        const float2 t = ffma2(make_float2(x[j], x[j + 1]), l2, c2);
+        x[j] = ex2_approx(t.x);
+        x[j + 1] = ex2_approx(t.y);
+        ps[(j >> 1) & 3] = fadd2(ps[(j >> 1) & 3], make_float2(x[j], x[j + 1]));
     }
+    const float2 s = fadd2(fadd2(ps[0], ps[1]), fadd2(ps[2], ps[3]));
     if (live)
-        a.stats[static_cast<int64_t>(m) * a.stat_tiles + col0 / kCeStatCols] =
-            make_float2(c, (ps[0] + ps[1]) + (ps[2] + ps[3]));
+        a.stats[static_cast<int64_t>(m) * a.stat_tiles + col0 / kCeStatCols] = make_float2(c, s.x + s.y);
     if (a.keep)
-        store_rows<kSplit ? kF32 : kF16>(x, a.e, live ? m * a.ldg : -1, col0, static_cast<int>(a.ldg), staging, lane);
+        store_exponentials<kSplit>(te, x, m - lane, col0, static_cast<int>(a.ldg), staging, lane);
+}
+
+// Where row m of dh (its place in hidden) or dW goes; negative past the end.
+template <int kWhat>
+__device__ __forceinline__ int grad_row(const CeArgs &a, int cnt, int m)
+{
+    if (m >= (kWhat == kCeDh ? cnt : a.V))
+        return -1;
+    return kWhat == kCeDh ? a.index[a.base + m] : m;
+}
+
+__device__ __forceinline__ float grad_scale(const CeArgs &a)
+{
+    const int n = *a.n_good;
+    return 1.f / static_cast<float>(n > 1 ? n : 1);
 }
 
 // dh and dW: scaled by 1 / T and rounded once.  dW over several pieces is kept
 // in fp32 until the last one.
 template <int kWhat, bool kSplit>
 __device__ __forceinline__ void finish_grad(const CeArgs &a, float (&x)[kCols], int cnt, int tile, int m, int col0,
-                                            int cta, int warp, uint8_t *staging, int lane)
+                                            int cta, int warp, int limit, uint8_t *staging, int lane)
 {
-    const int n_good = *a.n_good;
-    int64_t off = -1;
-    void *out = a.dh;
-    if (kWhat == kCeDh) {
-        if (m < cnt)
-            off = static_cast<int64_t>(a.index[a.base + m]) * a.D;
-    } else {
-        out = a.dw;
-        if (m < a.V)
-            off = static_cast<int64_t>(m) * a.D;
-        if (a.base > 0) {
-            const float4 *acc = tile_slot(a.acc, tile, cta, warp, lane);
+    if (kWhat == kCeDw && a.base > 0) {
+        const float4 *acc = tile_slot(a.acc, tile, cta, warp, lane);
 #pragma unroll
-            for (int j = 0; j < kCols / 4; ++j) {
-                const float4 v = acc[j * 32];
-                x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
-            }
-        }
-        if (a.base + a.rows < n_good) {
-            float4 *acc = tile_slot(a.acc, tile, cta, warp, lane);
-#pragma unroll
-            for (int j = 0; j < kCols / 4; ++j)
-                acc[j * 32] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-            return;
+        for (int j = 0; j < kCols / 4; ++j) {
+            const float4 v = acc[j * 32];
+            x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
         }
     }
-    const float inv = 1.f / static_cast<float>(n_good > 1 ? n_good : 1);
+    if (kWhat == kCeDw && a.base + a.rows < *a.n_good) {
+        float4 *acc = tile_slot(a.acc, tile, cta, warp, lane);
+#pragma unroll
+        for (int j = 0; j < kCols / 4; ++j)
+            acc[j * 32] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+        return;
+    }
+    const float inv = grad_scale(a);
 #pragma unroll
     for (int j = 0; j < kCols; ++j)
         x[j] *= inv;
-    store_rows<kSplit ? kF32 : kBf16>(x, out, off, col0, a.D, staging, lane);
+    store_rows<kSplit>(x, kWhat == kCeDh ? a.dh : a.dw, grad_row<kWhat>(a, cnt, m), a.D, col0, min(limit, a.D), staging,
+                       lane);
 }
 
 template <int kWhat, bool kSplit>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ce_product_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-                      const __grid_constant__ CeArgs a, const WaitCfg w)
+                      const __grid_constant__ CUtensorMap te, const __grid_constant__ CeArgs a, const WaitCfg w)
 {
     const int cnt = ce_piece_rows(a);
     if (cnt == 0 && (kWhat != kCeDw || a.base > 0))
@@ -338,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 int m0, n0;
                 tile_origin<kWhat>(plan, u.tile, m0, n0);
                 m0 += cta * kHalf;
-                n0 += cta * kHalf;
+                n0 += cta * (plan.cols / 2);
                 for (int k = u.k0; ok && k < u.k1; ++k) {
 #pragma unroll 1
                     for (int pp = 0; pp < kPerStep; ++pp, ++it) {
@@ -384,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == kEpiWarps + 1) {
         // ------------------------------------------------ products
         if (lane == 0 && cta == 0) {
-            constexpr uint32_t idesc = idesc_bf16(256, 256, kWhat == kCeDw, kWhat != kCeLogits);
+            const uint32_t idesc = idesc_bf16(256, plan.cols, kWhat == kCeDw, kWhat != kCeLogits);
             Units units(plan, pair, pairs);
             Unit u;
             uint32_t it = 0, chunk = 0;
@@ -445,11 +493,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tile_origin<kWhat>(plan, u.tile, m0, n0);
             const int m = m0 + cta * kHalf + (warp & 3) * 32 + lane;
             float x[kCols];
-#pragma unroll
-            for (int j = 0; j < kCols; ++j)
-                x[j] = 0.f;
             constexpr int per = kChunkSteps<kWhat, kSplit>;
             const int chunks = (u.k1 - u.k0 + per - 1) / per;
+            if (chunks == 0) {
+#pragma unroll
+                for (int j = 0; j < kCols; ++j)
+                    x[j] = 0.f;
+            }
             for (int c = 0; c < chunks; ++c, ++chunk) {
                 const uint32_t acc = chunk & 1;
                 if (!mbar_wait_warp(&acc_full[acc], (chunk >> 1) & 1, w, 0xa5)) {
@@ -458,19 +508,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t t = tbase + acc * 256 + col + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+                if (c == 0) {
+                    uint32_t *v = reinterpret_cast<uint32_t *>(x);
 #pragma unroll
-                for (int j = 0; j < kCols; j += 32) {
-                    uint32_t v[32];
-                    tmem_ld32(t + j, v);
-                    tmem_ld_wait(v);
+                    for (int j = 0; j < kCols; j += 32)
+                        tmem_ld32p(t + j, v + j);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        x[j + i] += __uint_as_float(v[i]);
+                    for (int j = 0; j < kCols; j += 32)
+                        tmem_ld_fence32p(v + j);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kCols; j += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(t + j, v);
+                        tmem_ld_wait(v);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 s = fadd2(make_float2(x[j + i], x[j + i + 1]),
+                                                   make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+                            x[j + i] = s.x;
+                            x[j + i + 1] = s.y;
+                        }
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_cluster(cluster_addr(&acc_empty[acc], 0));
+                    mbar_arrive_cluster_relaxed(cluster_addr(&acc_empty[acc], 0));
             }
             if (!ok)
                 break;
@@ -480,13 +545,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < kCols / 4; ++j)
                     slot[j * 32] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
             } else if constexpr (kWhat == kCeLogits) {
-                finish_logits<kSplit>(a, x, cnt, m, n0 + col, stage, lane);
+                finish_logits<kSplit>(a, &te, x, cnt, m, n0 + col, stage, lane);
             } else {
-                finish_grad<kWhat, kSplit>(a, x, cnt, u.tile, m, n0 + col, cta, warp, stage, lane);
+                finish_grad<kWhat, kSplit>(a, x, cnt, u.tile, m, n0 + col, cta, warp, n0 + plan.cols, stage, lane);
             }
         }
         if (!ok)
             *abort_flag = 1;
+        if (kWhat == kCeLogits && lane == 0)
+            bulk_wait_read<0>();  // staged rows are read before the CTA's shared memory goes
     }
 
     __syncwarp();
@@ -498,96 +565,149 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_dealloc_pair(tbase, 512);
 }
 
-// Adds the runs of the split tiles, in the order of the contraction.  One
-// block per (tile, CTA half), the warps as in the product kernel.
+// Adds the runs of the split tiles, in the order of the contraction.  A warp
+// takes 32 rows x 16 columns, since few tiles are split and each may have
+// dozens of runs; a block is one (tile, CTA half, 32 rows x 128 columns).
 template <int kWhat, bool kSplit>
-__global__ void __launch_bounds__(32 * kEpiWarps) ce_join_kernel(const __grid_constant__ CeArgs a, int pairs)
+__global__ void __launch_bounds__(256) ce_join_kernel(const __grid_constant__ CeArgs a, int pairs)
 {
-    extern __shared__ __align__(16) uint8_t join_staging[];
+    constexpr int kPart = 16;
     const int cnt = ce_piece_rows(a);
     if (cnt == 0)
         return;
     const Plan p = make_plan<kWhat>(a, cnt, pairs);
-    const int split = blockIdx.x >> 1, cta = blockIdx.x & 1, tile = p.whole + split;
+    const int slab = blockIdx.x % kEpiWarps, cta = blockIdx.x / kEpiWarps % 2, split = blockIdx.x / (2 * kEpiWarps);
+    const int tile = p.whole + split;
     if (p.workers == 0 || tile >= p.mt * p.nt)
         return;
     const int64_t steps = static_cast<int64_t>(p.mt * p.nt - p.whole) * p.kb;
     const int64_t t0 = static_cast<int64_t>(split) * p.kb, t1 = t0 + p.kb;
-    const int warp = warp_id(), lane = lane_id();
-    float x[kCols];
+    const int part = warp_id(), lane = lane_id();
+    float x[kPart];
 #pragma unroll
-    for (int j = 0; j < kCols; ++j)
+    for (int j = 0; j < kPart; ++j)
         x[j] = 0.f;
+    auto add = [&](const float4 *slot) {
+#pragma unroll
+        for (int j = 0; j < kPart / 4; ++j) {
+            const float4 v = slot[(part * (kPart / 4) + j) * 32];
+            x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
+        }
+    };
     // workers whose runs [steps w / workers, steps (w + 1) / workers) meet the tile
     int first = static_cast<int>(t0 * p.workers / steps);
     first = first > 0 ? first - 1 : 0;
-    for (int k = first; k < p.workers; ++k) {
-        const int64_t lo = steps * k / p.workers, hi = steps * (k + 1) / p.workers;
-        if (hi <= t0)
-            continue;
-        if (lo >= t1)
-            break;
-        const float4 *slot = tile_slot(a.partial, 2 * k + (lo < t0 ? 1 : 0), cta, warp, lane);
-#pragma unroll
-        for (int j = 0; j < kCols / 4; ++j) {
-            const float4 v = slot[j * 32];
-            x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
-        }
-    }
+    while (steps * (first + 1) / p.workers <= t0)
+        ++first;
+    int end = first;
+    while (end < p.workers && steps * end / p.workers < t1)
+        ++end;
+#pragma unroll 4
+    for (int k = first; k < end; ++k)
+        add(tile_slot(a.partial, 2 * k + (steps * k / p.workers < t0 ? 1 : 0), cta, slab, lane));
     int m0, n0;
     tile_origin<kWhat>(p, tile, m0, n0);
-    finish_grad<kWhat, kSplit>(a, x, cnt, tile, m0 + cta * kHalf + (warp & 3) * 32 + lane, n0 + (warp >> 2) * kCols,
-                               cta, warp, join_staging + warp * kWarpStaging, lane);
+    const int m = m0 + cta * kHalf + (slab & 3) * 32 + lane, col = n0 + (slab >> 2) * kCols + part * kPart;
+    const int row = grad_row<kWhat>(a, cnt, m);
+    bool keep = false;
+    if (kWhat == kCeDw) {
+        float4 *acc = tile_slot(a.acc, tile, cta, slab, lane) + part * (kPart / 4) * 32;
+        if (a.base > 0)
+#pragma unroll
+            for (int j = 0; j < kPart / 4; ++j) {
+                const float4 v = acc[j * 32];
+                x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
+            }
+        keep = a.base + a.rows < *a.n_good;
+        if (keep)
+#pragma unroll
+            for (int j = 0; j < kPart / 4; ++j)
+                acc[j * 32] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+    }
+    if (keep || row < 0)
+        return;
+    const float inv = grad_scale(a);
+#pragma unroll
+    for (int j = 0; j < kPart; ++j)
+        x[j] *= inv;
+    constexpr int kPer = kSplit ? 4 : 8;  // values of 16 bytes
+    uint8_t *out = static_cast<uint8_t *>(kWhat == kCeDh ? a.dh : a.dw) +
+                   (static_cast<int64_t>(row) * a.D + col) * (16 / kPer);
+#pragma unroll
+    for (int j = 0; j < kPart; j += kPer)
+        if (col + j < min(n0 + p.cols, a.D))
+            *reinterpret_cast<uint4 *>(out + j * (16 / kPer)) = kSplit ? words(x + j) : bf16s(x + j);
 }
 
 // --------------------------------------------------------------- host
+bool encode(CUtensorMap *map, CUtensorMapDataType type, int esize, int rank, const void *base, int64_t cols,
+            int64_t rows, int64_t pitch, int planes, int box_cols, int box_rows)
+{
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                          static_cast<cuuint64_t>(planes)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch) * esize, static_cast<cuuint64_t>(pitch) * rows * esize};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return tensor_map_encoder()(map, type, rank, const_cast<void *>(base), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Box of a K-major operand: 64 values of the contraction x 128 rows; of an
 // MN-major one: 64 columns x 64 values of the contraction.
 bool make_map(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64_t pitch, int planes, int box_rows)
 {
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
-                          static_cast<cuuint64_t>(planes)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch) * 2, static_cast<cuuint64_t>(pitch) * rows * 2};
-    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
-                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 3, base, cols, rows, pitch, planes, 64, box_rows);
+}
+
+// Box of the exponentials: 128 bytes x 32 rows.
+bool make_exp_map(CUtensorMap *map, const CeArgs &a, bool f32)
+{
+    return encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, f32 ? 4 : 2, 2, a.e,
+                  a.ldg, a.rows, a.ldg, 1, f32 ? 32 : 64, 32);
 }
 
 template <int kWhat, bool kSplit>
-cudaError_t launch(const CeArgs &a, const CUtensorMap &ta, const CUtensorMap &tb, cudaStream_t s)
+cudaError_t launch(const CeArgs &a, const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &te,
+                   cudaStream_t s)
 {
     auto kernel = ce_product_kernel<kWhat, kSplit>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    // Pairs resident at once (the schedule gives each an equal share), asked
+    // for once per device; two threads that ask at the same time find the same.
+    static std::atomic<int> known[kCeMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
-    // pairs resident at once: the schedule gives each an equal share
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (num_sms() / 2));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int pairs = 0;
-    e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
-    if (e != cudaSuccess)
-        return e;
-    pairs = std::max(1, std::min(std::min(pairs, num_sms() / 2), kCeMaxPairs));
-    kernel<<<2 * pairs, kThreads, kSmem, s>>>(ta, tb, a, wait_cfg());
+    if (dev >= kCeMaxDevices)
+        return cudaErrorInvalidDevice;
+    int pairs = known[dev].load();
+    if (pairs == 0) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess)
+            return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * (num_sms() / 2));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
+        if (e != cudaSuccess)
+            return e;
+        pairs = std::max(1, std::min(std::min(pairs, num_sms() / 2), kCeMaxPairs));
+        known[dev].store(pairs);
+    }
+    kernel<<<2 * pairs, kThreads, kSmem, s>>>(ta, tb, te, a, wait_cfg());
     if constexpr (kWhat != kCeLogits) {
         // never split below this many steps: nothing to join
         const int kb = ((kWhat == kCeDh ? a.V : a.rows) + kCeStep - 1) / kCeStep;
-        if (kb > kSplitGain) {
-            constexpr int smem = kEpiWarps * kWarpStaging;
-            e = cudaFuncSetAttribute(ce_join_kernel<kWhat, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e != cudaSuccess)
-                return e;
-            ce_join_kernel<kWhat, kSplit><<<2 * (pairs - 1), 32 * kEpiWarps, smem, s>>>(a, pairs);
+        if (kb > kSplitGain && pairs > 1) {
+            ce_join_kernel<kWhat, kSplit><<<2 * kEpiWarps * (pairs - 1), 256, 0, s>>>(a, pairs);
         }
     }
     return cudaGetLastError();
@@ -598,19 +718,20 @@ cudaError_t product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh,
                     const void *g, cudaStream_t s)
 {
     constexpr int planes = kSplit ? 3 : 1;
-    CUtensorMap ta, tb;
+    CUtensorMap ta, tb, te = {};  // te: the logits' exponentials alone
     bool ok;
     switch (what) {
     case kCeLogits:
         ok = make_map(&ta, h, a.D, a.rows, ldh, planes, kHalf) && make_map(&tb, w, a.D, a.V, ldw, planes, kHalf);
-        return ok ? launch<kCeLogits, kSplit>(a, ta, tb, s) : cudaErrorInvalidValue;
+        ok = ok && (!a.keep || make_exp_map(&te, a, kSplit));
+        return ok ? launch<kCeLogits, kSplit>(a, ta, tb, te, s) : cudaErrorInvalidValue;
     case kCeDh:
         ok = make_map(&ta, g, a.V, a.rows, a.ldg, planes, kHalf) && make_map(&tb, w, a.D, a.V, ldw, planes, kCeStep);
-        return ok ? launch<kCeDh, kSplit>(a, ta, tb, s) : cudaErrorInvalidValue;
+        return ok ? launch<kCeDh, kSplit>(a, ta, tb, te, s) : cudaErrorInvalidValue;
     default:
         ok = make_map(&ta, g, a.V, a.rows, a.ldg, planes, kCeStep) &&
              make_map(&tb, h, a.D, a.rows, ldh, planes, kCeStep);
-        return ok ? launch<kCeDw, kSplit>(a, ta, tb, s) : cudaErrorInvalidValue;
+        return ok ? launch<kCeDw, kSplit>(a, ta, tb, te, s) : cudaErrorInvalidValue;
     }
 }
 

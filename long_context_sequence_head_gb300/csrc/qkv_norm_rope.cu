@@ -20,8 +20,10 @@
 // Memory-bound: every value is read and written once.  A warp takes one
 // token's rows, so that its cosines and sines are made once and shared by its
 // heads; a lane holds the two chunks of a row (8 bytes each) whose values turn
-// with each other, so that the rotation needs no exchange between lanes; the
-// next kUnroll rows are loaded before the first is used.
+// with each other, so that the rotation needs no exchange between lanes.  Rows
+// come in runs through a ring of bulk copies that each warp keeps for
+// itself, so that what is in flight costs no registers, and the next tokens
+// are on their way while one is worked on.
 #include <cmath>
 
 #include "uly_internal.h"
@@ -29,19 +31,27 @@
 namespace uly {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+// Rows of a run (bytes), runs on their way per warp, resident blocks per SM.
+// 64K tokens, 32 + 8 + 8 heads of 128, bf16, us: forward 252 (3 runs of 4 KB
+// x 4 blocks, and 2 x 4), 258 (2 x 5), 260 (2 x 6); backward 360 (1 x 5), 364
+// (1 x 4), 378 (2 x 3), and over 430 with runs of 2 KB or registers spilled.
+constexpr int kFwdRun = 4096, kBwdRun = 4096;
+constexpr int kFwdRing = 2, kBwdRing = 1;
+constexpr int kFwdBlocks = 4, kBwdBlocks = 5;
 
 // A row of kD values over kLanes lanes: two chunks of kC values each, as kP
 // pairs for the packed fp32 arithmetic.
-template <typename T, int kD_>
+template <typename T, int kD_, int kRunBytes_>
 struct Shape {
+    static constexpr int kRunBytes = kRunBytes_;
     static constexpr int kD = kD_;
     static constexpr int kC = 8 / sizeof(T);
     static constexpr int kP = kC / 2;
     static constexpr int kLanes = kD / (2 * kC);
     static constexpr int kRows = 32 / kLanes;  // rows a warp takes at once
+    static constexpr int kRun = kRunBytes / (kD * sizeof(T));  // rows of a run
 };
 
 template <typename T>
@@ -68,17 +78,10 @@ __device__ __forceinline__ float2 swap(float2 v) { return make_float2(v.y, v.x);
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 struct Token {
-    int64_t m;  // row of the sequence layout: ((s * B + b) * Np + t)
-    int64_t n;  // index in its sequence
+    uint32_t m;  // row of the sequence layout: ((s * B + b) * Np + t)
+    uint32_t n;  // index in its sequence
     int b;
 };
-
-__device__ __forceinline__ Token token_of(const NormRopeParams &p, uint32_t m)
-{
-    const uint32_t sb = m / static_cast<uint32_t>(p.Np), t = m - sb * static_cast<uint32_t>(p.Np);
-    const uint32_t s = sb / static_cast<uint32_t>(p.B);
-    return Token{m, static_cast<int64_t>(s) * p.Np + t, static_cast<int>(sb - s * p.B)};
-}
 
 // Heads of one tensor on the far side: the head layout [P][B][N][H/P][d] or
 // the sequence layout, contiguous.  h / (H/P) by a product: exact below 65536.
@@ -87,37 +90,72 @@ struct Far {
     unsigned magic;
     int per;
 
+    __device__ __forceinline__ Far() {}
     __device__ __forceinline__ Far(const NormRopeParams &p, const Token &k, int H, int Hp, unsigned magic_, int d)
         : magic(magic_), per(Hp)
     {
         if (p.to_head) {
-            first = (k.b * p.N + k.n) * Hp * d;
+            first = (k.b * p.N + k.n) * static_cast<int64_t>(Hp) * d;
             rank = p.N * p.B * Hp * d;
         } else {
-            first = k.m * H * d;
+            first = static_cast<int64_t>(k.m) * H * d;
             rank = 0;
         }
     }
+    __device__ __forceinline__ int rank_of(int h) const
+    {
+        return magic ? static_cast<int>(__umulhi(static_cast<unsigned>(h), magic)) : h;
+    }
     __device__ __forceinline__ int64_t at(int h, int d) const
     {
-        const int r = magic ? static_cast<int>(__umulhi(static_cast<unsigned>(h), magic)) : h;
-        return first + r * rank + static_cast<int64_t>(h - r * per) * d;
+        const int r = rank_of(h);
+        return first + r * rank + (h - r * per) * d;
     }
 };
 
-// cos and sin of the token's rot/2 angles into the warp's shared table
-__device__ __forceinline__ void angles(const NormRopeParams &p, const Token &k, float2 *table, int lane)
-{
-    __syncwarp();  // the last token's reads are done
-    for (int f = lane; f < p.half; f += 32) {
-        const int64_t pos = p.positions ? p.positions[p.axis[f] * p.tokens + k.m] : k.n;
-        const uint64_t frac = p.turn[f] * static_cast<uint64_t>(pos);
-        float sn, cs;
-        sincospif(static_cast<float>(static_cast<int64_t>(frac)) * 0x1p-63f, &sn, &cs);  // in (-1, 1] half turns
-        table[f] = make_float2(cs, sn);
+// cos and sin of a token's rot/2 angles in the warp's shared table.  A lane
+// makes at most two; the positions of the next token are read while this one
+// is worked on.
+struct Angles {
+    int64_t pos[2];
+    uint32_t held, made;  // the token whose positions these are, and the one the table is of
+
+    __device__ __forceinline__ Angles() : held(~0u), made(~0u) {}
+    __device__ __forceinline__ void read(const NormRopeParams &p, uint32_t m, int lane)
+    {
+        held = m;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (lane + 32 * i < p.half)
+                pos[i] = p.positions[p.axis[lane + 32 * i] * p.tokens + m];
     }
-    __syncwarp();
-}
+    // true if the table is new; `next`: the warp's next token
+    __device__ __forceinline__ bool make(const NormRopeParams &p, const Token &k, uint32_t next, float2 *table,
+                                         int lane)
+    {
+        if (made == k.m)
+            return false;
+        made = k.m;
+        if (p.positions && held != k.m)
+            read(p, k.m, lane);
+        __syncwarp();  // the last token's reads are done
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int f = lane + 32 * i;
+            if (f < p.half) {
+                const uint64_t frac = p.turn[f] * static_cast<uint64_t>(p.positions ? pos[i] : k.n);
+                float sn, cs;
+                // its upper 32 bits, as half turns in [-1, 1)
+                sincospif(static_cast<float>(static_cast<int32_t>(frac >> 32)) * 0x1p-31f, &sn, &cs);
+                table[f] = make_float2(cs, sn);
+            }
+        }
+        __syncwarp();
+        if (p.positions && next < p.tokens)
+            read(p, next, lane);
+        return true;
+    }
+};
 
 // Where a lane's chunks lie.  Half-split pairs: lanes below half / kC hold
 // values f.. and half + f.. that turn with each other, the others two chunks
@@ -139,33 +177,28 @@ __device__ __forceinline__ void chunk_places(int half, int i, int &lo, int &hi)
 
 // The rotation of a lane's chunks: lo' = lo c_lo + o s_lo, hi' = hi c_hi + o s_hi,
 // where o is the other chunk (half-split) or the chunk with its pairs swapped
-// (interleaved).  kBack: its transpose.
-template <typename S, bool kInter, bool kBack>
+// (interleaved).  kBack: its transpose.  Without a weight the half-split pairs
+// have c_lo = c_hi and s_lo = -s_hi, and are held once.
+template <typename S, bool kInter, bool kBack, bool kWeighed>
 struct Turn {
-    float2 cl[S::kP], sl[S::kP], ch[S::kP], sh[S::kP];
+    static constexpr bool kOnce = !kInter && !kWeighed;
+    float2 cl[S::kP], sl[S::kP], ch[kOnce ? 1 : S::kP], sh[kOnce ? 1 : S::kP];
     bool turns;  // both chunks do or neither (rot is a multiple of 16): an infinity must not meet a zero sine
 
-    __device__ __forceinline__ Turn(const float2 *table, int half, int lo, int hi)
+    __device__ __forceinline__ void load(const float2 *table, int half, int lo, int hi)
     {
         const float sign = kBack ? -1.f : 1.f;
         turns = kInter ? lo < 2 * half : lo < half;
 #pragma unroll
         for (int j = 0; j < S::kP; ++j) {
-            cl[j] = ch[j] = both(1.f);
-            sl[j] = sh[j] = both(0.f);
-            if (!turns)
-                continue;
-            if (kInter) {
-                const float2 t = table[lo / 2 + j], u = table[hi / 2 + j];
-                cl[j] = both(t.x);
-                ch[j] = both(u.x);
-                sl[j] = make_float2(-sign * t.y, sign * t.y);
-                sh[j] = make_float2(-sign * u.y, sign * u.y);
-            } else {
-                const float2 t = table[lo + 2 * j], u = table[lo + 2 * j + 1];
-                cl[j] = ch[j] = make_float2(t.x, u.x);
-                sl[j] = make_float2(-sign * t.y, -sign * u.y);
-                sh[j] = make_float2(sign * t.y, sign * u.y);
+            float2 t = make_float2(1.f, 0.f), u = t;
+            if (turns)
+                t = table[kInter ? lo / 2 + j : lo + 2 * j], u = table[kInter ? hi / 2 + j : lo + 2 * j + 1];
+            cl[j] = kInter ? both(t.x) : make_float2(t.x, u.x);
+            sl[j] = kInter ? make_float2(-sign * t.y, sign * t.y) : make_float2(-sign * t.y, -sign * u.y);
+            if constexpr (!kOnce) {
+                ch[j] = kInter ? both(u.x) : cl[j];
+                sh[j] = kInter ? make_float2(-sign * u.y, sign * u.y) : make_float2(-sl[j].x, -sl[j].y);
             }
         }
     }
@@ -186,10 +219,10 @@ struct Turn {
         for (int j = 0; j < S::kP; ++j) {
             const float2 a = lo[j], b = hi[j];
             lo[j] = fmul2(a, cl[j]);
-            hi[j] = fmul2(b, ch[j]);
+            hi[j] = fmul2(b, kOnce ? cl[j] : ch[kOnce ? 0 : j]);
             if (turns) {
                 lo[j] = ffma2(kInter ? swap(a) : b, sl[j], lo[j]);
-                hi[j] = ffma2(kInter ? swap(b) : a, sh[j], hi[j]);
+                hi[j] = ffma2(kInter ? swap(b) : a, kOnce ? make_float2(-sl[j].x, -sl[j].y) : sh[kOnce ? 0 : j], hi[j]);
             }
         }
     }
@@ -202,13 +235,6 @@ __device__ __forceinline__ float row_sum(float v)
     for (int o = kLanes / 2; o > 0; o >>= 1)
         v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
-}
-
-template <typename T, typename S>
-__device__ __forceinline__ void load_weights(const void *w, int lo, int hi, float2 *wl, float2 *wh)
-{
-    unpack<T>(*reinterpret_cast<const uint2 *>(static_cast<const T *>(w) + lo), wl);
-    unpack<T>(*reinterpret_cast<const uint2 *>(static_cast<const T *>(w) + hi), wh);
 }
 
 struct Raw {
@@ -228,226 +254,369 @@ __device__ __forceinline__ void store_row(T *row, int lo, int hi, const Raw &v)
     *reinterpret_cast<uint2 *>(row + hi) = v.hi;
 }
 
-// A unit is one token and a run [r0, r1) of its rows: Q's heads, K's, V's.
-struct Run {
-    int q0, q1, k0, k1, v0, v1;
+// A place in a warp's list of runs.  Unit u (a token, or a part of a token's
+// runs) goes to warp u modulo the number of warps, so that all warps work on
+// neighbouring memory.  A unit's runs are kRun rows each of the token's list:
+// Q's heads, then K's, then V's.
+template <typename S>
+struct Cursor {
+    uint32_t u, units, stride;
+    int r, end;  // this run, and the first run past the unit
+    Token k;
 
-    __device__ __forceinline__ Run(const NormRopeParams &p, int part)
+    __device__ __forceinline__ Cursor(const NormRopeParams &p, uint32_t warp, uint32_t warps)
+        : u(warp), units(static_cast<uint32_t>(p.tokens * p.splits)), stride(warps)
     {
-        const int r0 = part * p.rows_per_split, r1 = r0 + p.rows_per_split, kv = p.Hq + p.Hkv;
-        q0 = min(r0, p.Hq), q1 = min(r1, p.Hq);
-        k0 = max(r0 - p.Hq, 0), k1 = min(r1 - p.Hq, p.Hkv);
-        v0 = max(r0 - kv, 0), v1 = p.v ? min(r1 - kv, p.Hkv) : 0;
+        enter(p);
+    }
+    static __device__ __forceinline__ int rows(const NormRopeParams &p) { return p.Hq + (p.v ? 2 : 1) * p.Hkv; }
+    __device__ __forceinline__ bool more() const { return u < units; }
+    __device__ __forceinline__ void enter(const NormRopeParams &p)
+    {
+        const uint32_t splits = p.splits, m = splits == 1 ? u : u / splits;
+        const uint32_t sb = m / static_cast<uint32_t>(p.Np), s = sb / static_cast<uint32_t>(p.B);
+        k = Token{m, s * p.Np + (m - sb * p.Np), static_cast<int>(sb - s * p.B)};
+        r = static_cast<int>(u - m * splits) * p.runs_per_split;
+        end = min((rows(p) + S::kRun - 1) / S::kRun, r + p.runs_per_split);
+    }
+    // to the next run
+    __device__ __forceinline__ void step(const NormRopeParams &p)
+    {
+        if (++r < end)
+            return;
+        u += stride;
+        if (more())
+            enter(p);
+    }
+    __device__ __forceinline__ int row0() const { return r * S::kRun; }
+    __device__ __forceinline__ int row1(const NormRopeParams &p) const { return min(rows(p), (r + 1) * S::kRun); }
+    // heads [h0, h1) of tensor t in this run; `at`: the run's row of head h0
+    __device__ __forceinline__ void heads(const NormRopeParams &p, int t, int &h0, int &h1, int &at) const
+    {
+        const int first = t == 0 ? 0 : (t == 1 ? p.Hq : p.Hq + p.Hkv);
+        h0 = max(row0() - first, 0);
+        h1 = min(row1(p) - first, t ? p.Hkv : p.Hq);
+        at = first + h0 - row0();
+    }
+    __device__ __forceinline__ Far far(const NormRopeParams &p, int t) const
+    {
+        return t ? Far(p, k, p.Hkv, p.Hkvp, p.magic_k, S::kD) : Far(p, k, p.Hq, p.Hqp, p.magic_q, S::kD);
     }
 };
 
-// heads [h0, h1): load kUnroll of this lane's rows, then hand them on
-template <typename S, typename Load, typename Use>
-__device__ __forceinline__ void for_heads(int h0, int h1, int sub, Load load, Use use)
-{
-    using R = decltype(load(0));
-    for (int hb = h0; hb < h1; hb += kUnroll * S::kRows) {
-        R raw[kUnroll];
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const int h = hb + i * S::kRows + sub;
-            raw[i] = load(h < h1 ? h : h0);  // past the end: a row that is there
+// The ring a warp keeps: kRing slots of kParts runs.
+template <int kRing, int kParts, int kRunBytes>
+struct Ring {
+    uint8_t *data;
+    uint64_t *bars;
+
+    __device__ __forceinline__ Ring(uint8_t *smem, int warp, int lane)
+    {
+        data = smem + warp * (kRing * kParts * kRunBytes);
+        bars = reinterpret_cast<uint64_t *>(smem + kWarps * (kRing * kParts * kRunBytes)) + warp * kRing;
+        if (lane == 0) {
+            for (int i = 0; i < kRing; ++i)
+                mbar_init(&bars[i], 1);
+            fence_mbar_init();
         }
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i)
-            if (hb + i * S::kRows < h1) {
-                const int h = hb + i * S::kRows + sub;
-                use(h, h < h1, raw[i]);
-            }
+        __syncwarp();
     }
+    static constexpr int kBytes = kWarps * kRing * (kParts * kRunBytes + 8);
+};
+
+template <typename T, int kD, bool kInter, bool kNorm>
+__global__ void __launch_bounds__(kThreads, kFwdBlocks) norm_rope_fwd_kernel(const __grid_constant__ NormRopeParams p,
+                                                                            const WaitCfg wait)
+{
+    using S = Shape<T, kD, kFwdRun>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float2 table[kWarps][kD / 2];
+    __shared__ __align__(16) T weights[2][kD];
+    const int warp = warp_id(), lane = lane_id(), sub = lane / S::kLanes;
+    if (kNorm) {
+        for (int i = threadIdx.x; i < kD; i += kThreads) {
+            weights[0][i] = static_cast<const T *>(p.wq)[i];
+            weights[1][i] = static_cast<const T *>(p.wk)[i];
+        }
+        __syncthreads();
+    }
+    const Ring<kFwdRing, 1, kFwdRun> ring(smem, warp, lane);
+    int lo, hi;
+    chunk_places<S, kInter>(p.half, lane % S::kLanes, lo, hi);
+    Cursor<S> now(p, blockIdx.x * kWarps + warp, gridDim.x * kWarps);
+    Cursor<S> ahead = now;
+    auto fetch = [&](int slot) {  // a copy per tensor
+        if (lane == 0)
+            mbar_expect_tx(&ring.bars[slot], (ahead.row1(p) - ahead.row0()) * kD * sizeof(T));
+        __syncwarp();
+        int h0, h1, row;
+        ahead.heads(p, lane, h0, h1, row);
+        if (lane < 3 && h0 < h1) {
+            const T *src = static_cast<const T *>(lane == 0 ? p.q : (lane == 1 ? p.k : p.v)) +
+                           ahead.k.m * (lane == 0 ? p.qs : (lane == 1 ? p.ks : p.vs)) + h0 * kD;
+            bulk_g2s(ring.data + slot * kFwdRun + row * kD * sizeof(T), src, (h1 - h0) * kD * sizeof(T),
+                     &ring.bars[slot]);
+        }
+        ahead.step(p);
+    };
+    int started = 0, done = 0;  // runs fetched and worked on
+    for (; started < kFwdRing && ahead.more(); ++started)
+        fetch(started);
+    Angles at;
+    int last = -1;
+    Turn<S, kInter, false, kNorm> turn;
+    Far far;
+    while (now.more()) {
+        const int slot = done % kFwdRing;
+        if (now.row0() < p.Hq + p.Hkv && at.make(p, now.k, now.k.m + now.stride, table[warp], lane))
+            last = -1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&ring.bars[slot], (done / kFwdRing) & 1, wait, 0xb1)))
+            break;
+        const T *data = reinterpret_cast<const T *>(ring.data + slot * kFwdRun);
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t) {
+            int h0, h1, row;
+            now.heads(p, t, h0, h1, row);
+            if (h0 >= h1)
+                continue;
+            if (t != last) {
+                last = t;
+                turn.load(table[warp], p.half, lo, hi);
+                if constexpr (kNorm) {
+                    const Raw raw = load_row<T>(weights[t], lo, hi);
+                    float2 wl[S::kP], wh[S::kP];
+                    unpack<T>(raw.lo, wl);
+                    unpack<T>(raw.hi, wh);
+                    turn.weigh(wl, wh);
+                }
+            }
+            far = now.far(p, t);
+            T *out = static_cast<T *>(t ? p.ko : p.qo);
+            const T *rows = data + (row - h0) * kD;
+#pragma unroll 2
+            for (int hb = h0; hb < h1; hb += S::kRows) {
+                const int h = hb + sub;
+                const Raw raw = load_row<T>(rows + min(h, h1 - 1) * kD, lo, hi);
+                float2 x[S::kP], y[S::kP];
+                unpack<T>(raw.lo, x);
+                unpack<T>(raw.hi, y);
+                float rstd = 1.f;
+                if (kNorm) {
+                    float2 ss = both(0.f), st = ss;
+#pragma unroll
+                    for (int j = 0; j < S::kP; ++j) {
+                        ss = ffma2(x[j], x[j], ss);
+                        st = ffma2(y[j], y[j], st);
+                    }
+                    ss = fadd2(ss, st);
+                    rstd = rsqrtf(row_sum<S::kLanes>(ss.x + ss.y) * (1.f / kD) + p.eps);
+                }
+                turn.apply(x, y);
+                if (kNorm) {
+#pragma unroll
+                    for (int j = 0; j < S::kP; ++j) {
+                        x[j] = fmul2(x[j], both(rstd));
+                        y[j] = fmul2(y[j], both(rstd));
+                    }
+                }
+                if (h < h1)
+                    store_row<T>(out + far.at(h, kD), lo, hi, Raw{pack<T>(x), pack<T>(y)});
+            }
+        }
+        int h0, h1, row;
+        now.heads(p, 2, h0, h1, row);
+        if (h0 < h1) {
+            far = now.far(p, 2);
+#pragma unroll 2
+            for (int h = h0 + sub; h < h1; h += S::kRows)
+                store_row<T>(static_cast<T *>(p.vo) + far.at(h, kD), lo, hi,
+                             load_row<T>(data + (row + h - h0) * kD, lo, hi));
+        }
+        __syncwarp();  // the slot is read
+        if (ahead.more()) {
+            fetch(slot);
+            ++started;
+        }
+        ++done;
+        now.step(p);
+    }
+    // after a wait that ran out: the copies still on their way (bounded)
+    for (; done < started; ++done)
+        mbar_wait(&ring.bars[done % kFwdRing], (done / kFwdRing) & 1, wait, 0xbf);
 }
 
 template <typename T, int kD, bool kInter, bool kNorm>
-__global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(const __grid_constant__ NormRopeParams p)
+__global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p,
+                                                                            const WaitCfg wait)
 {
-    using S = Shape<T, kD>;
+    using S = Shape<T, kD, kBwdRun>;
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float2 table[kWarps][kD / 2];
+    __shared__ __align__(16) T weights[2][kD];
     const int warp = warp_id(), lane = lane_id(), sub = lane / S::kLanes;
+    if (kNorm) {
+        for (int i = threadIdx.x; i < kD; i += kThreads) {
+            weights[0][i] = static_cast<const T *>(p.wq)[i];
+            weights[1][i] = static_cast<const T *>(p.wk)[i];
+        }
+        __syncthreads();
+    }
+    constexpr int kParts = kNorm ? 2 : 1;  // a run of dy and one of x
+    const Ring<kBwdRing, kParts, kBwdRun> ring(smem, warp, lane);
     int lo, hi;
     chunk_places<S, kInter>(p.half, lane % S::kLanes, lo, hi);
-    const int64_t units = p.tokens * p.splits;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < units;
-         u += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const Token k = token_of(p, static_cast<uint32_t>(u / p.splits));
-        const Run run(p, static_cast<int>(u % p.splits));
-        if (run.v0 == 0)
-            angles(p, k, table[warp], lane);
-        auto heads = [&](int h0, int h1, const void *in, int64_t stride, void *out, int H, int Hp, unsigned magic,
-                         const void *w) {
-            if (h0 >= h1)
-                return;
-            Turn<S, kInter, false> turn(table[warp], p.half, lo, hi);
-            if (kNorm) {
-                float2 wl[S::kP], wh[S::kP];
-                load_weights<T, S>(w, lo, hi, wl, wh);
-                turn.weigh(wl, wh);
+    // the warp's part of dw, kept between runs: [q, k][slot][d]
+    constexpr int kSlots = S::kRows < 2 ? 1 : 2;
+    constexpr int kSums = kNorm ? 2 * kSlots * kD : 2;
+    __shared__ float2 sums[kWarps][kSums / 2];
+    if (kNorm)
+        for (int i = lane; i < kSums / 2; i += 32)
+            sums[warp][i] = both(0.f);
+    __syncwarp();
+    Cursor<S> now(p, blockIdx.x * kWarps + warp, gridDim.x * kWarps);
+    Cursor<S> ahead = now;
+    auto fetch = [&](int slot) {
+        // Lanes 0, 1, 2 (mod 4): dy of Q, K and V, a copy per rank; lanes 3 and 7: x of Q and K
+        uint8_t *to = ring.data + slot * (kParts * kBwdRun);
+        const int row0 = ahead.row0(), row1 = ahead.row1(p), xrows = max(min(row1, p.Hq + p.Hkv) - row0, 0);
+        if (lane == 0)
+            mbar_expect_tx(&ring.bars[slot], (row1 - row0 + (kNorm ? xrows : 0)) * kD * sizeof(T));
+        __syncwarp();
+        const int kind = lane & 3, t = kind < 3 ? kind : lane >> 2;
+        int h0, h1, row;
+        ahead.heads(p, t, h0, h1, row);
+        if (kind < 3) {
+            const Far far = ahead.far(p, t);
+            const T *src = static_cast<const T *>(t == 0 ? p.qo : (t == 1 ? p.ko : p.vo));
+            for (int i = far.rank_of(h0) + (lane >> 2); h0 < h1; i += 8) {
+                const int a = max(h0, i * far.per), b = min(h1, (i + 1) * far.per);
+                if (a >= b)
+                    break;
+                bulk_g2s(to + (row + a - h0) * kD * sizeof(T), src + far.at(a, kD), (b - a) * kD * sizeof(T),
+                         &ring.bars[slot]);
             }
-            const T *src = static_cast<const T *>(in) + k.m * stride;
-            const Far far(p, k, H, Hp, magic, kD);
-            for_heads<S>(
-                h0, h1, sub, [&](int h) { return load_row<T>(src + static_cast<int64_t>(h) * kD, lo, hi); },
-                [&](int h, bool live, const Raw &raw) {
-                    float2 a[S::kP], b[S::kP];
-                    unpack<T>(raw.lo, a);
-                    unpack<T>(raw.hi, b);
-                    float rstd = 1.f;
-                    if (kNorm) {
-                        float2 ss = both(0.f);
+        } else if (kNorm && t < 2 && h0 < h1) {
+            bulk_g2s(to + kBwdRun + row * kD * sizeof(T),
+                     static_cast<const T *>(t ? p.k : p.q) + ahead.k.m * (t ? p.ks : p.qs) + h0 * kD,
+                     (h1 - h0) * kD * sizeof(T), &ring.bars[slot]);
+        }
+        ahead.step(p);
+    };
+    int started = 0, done = 0;
+    for (; started < kBwdRing && ahead.more(); ++started)
+        fetch(started);
+    Angles at;
+    Turn<S, kInter, true, false> turn;
+    while (now.more()) {
+        const int slot = done % kBwdRing;
+        if (now.row0() < p.Hq + p.Hkv && at.make(p, now.k, now.k.m + now.stride, table[warp], lane))
+            turn.load(table[warp], p.half, lo, hi);
+        if (!__all_sync(0xffffffffu, mbar_wait(&ring.bars[slot], (done / kBwdRing) & 1, wait, 0xb2)))
+            break;
+        const T *data = reinterpret_cast<const T *>(ring.data + slot * (kParts * kBwdRun));
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t) {
+            int h0, h1, row;
+            now.heads(p, t, h0, h1, row);
+            if (h0 >= h1)
+                continue;
+            T *out = static_cast<T *>(t ? p.dk : p.dq) + static_cast<int64_t>(now.k.m) * (t ? p.dks : p.dqs);
+            const T *rows = data + (row - h0) * kD, *xrows = rows + kBwdRun / sizeof(T);
+            float2 w[2][S::kP], sum[2][S::kP];
+            if (kNorm) {
+                const Raw raw = load_row<T>(weights[t], lo, hi);
+                unpack<T>(raw.lo, w[0]);
+                unpack<T>(raw.hi, w[1]);
+            }
 #pragma unroll
-                        for (int j = 0; j < S::kP; ++j)
-                            ss = ffma2(b[j], b[j], ffma2(a[j], a[j], ss));
-                        rstd = rsqrtf(row_sum<S::kLanes>(ss.x + ss.y) * (1.f / kD) + p.eps);
-                    }
-                    turn.apply(a, b);
-                    if (kNorm) {
+            for (int j = 0; j < S::kP; ++j)
+                sum[0][j] = sum[1][j] = both(0.f);
+#pragma unroll 1
+            for (int hb = h0; hb < h1; hb += S::kRows) {
+                const int h = hb + sub, hr = min(h, h1 - 1);
+                const bool live = h < h1;
+                const Raw raw = load_row<T>(rows + hr * kD, lo, hi);
+                float2 g[2][S::kP];
+                unpack<T>(raw.lo, g[0]);
+                unpack<T>(raw.hi, g[1]);
+                turn.apply(g[0], g[1]);
+                if (kNorm) {
+                    const Raw rawx = load_row<T>(xrows + hr * kD, lo, hi);
+                    float2 x[2][S::kP], ss[2] = {both(0.f), both(0.f)}, dot[2] = {both(0.f), both(0.f)};
+                    unpack<T>(rawx.lo, x[0]);
+                    unpack<T>(rawx.hi, x[1]);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int j = 0; j < S::kP; ++j) {
-                            a[j] = fmul2(a[j], both(rstd));
-                            b[j] = fmul2(b[j], both(rstd));
+                            ss[c] = ffma2(x[c][j], x[c][j], ss[c]);
+                            dot[c] = ffma2(w[c][j], fmul2(g[c][j], x[c][j]), dot[c]);
+                        }
+                    ss[0] = fadd2(ss[0], ss[1]);
+                    dot[0] = fadd2(dot[0], dot[1]);
+                    const float rstd = rsqrtf(row_sum<S::kLanes>(ss[0].x + ss[0].y) * (1.f / kD) + p.eps);
+                    // mean(w g xhat) r: what x loses, before the last factor r
+                    const float m = row_sum<S::kLanes>(dot[0].x + dot[0].y) * (1.f / kD) * rstd * rstd;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int j = 0; j < S::kP; ++j) {
+                            if (live)
+                                sum[c][j] = ffma2(fmul2(g[c][j], x[c][j]), both(rstd), sum[c][j]);
+                            g[c][j] = fmul2(ffma2(x[c][j], both(-m), fmul2(w[c][j], g[c][j])), both(rstd));
+                        }
+                }
+                if (live)
+                    store_row<T>(out + h * kD, lo, hi, Raw{pack<T>(g[0]), pack<T>(g[1])});
+            }
+            if (kNorm) {
+                float *to = reinterpret_cast<float *>(sums[warp]) + (t * kSlots + sub) * kD;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int j = 0; j < S::kP; ++j) {
+                        float2 v = sum[c][j];
+#pragma unroll
+                        for (int o = 16; o >= S::kLanes * kSlots; o >>= 1)
+                            v = fadd2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o),
+                                                     __shfl_xor_sync(0xffffffffu, v.y, o)));
+                        if (sub < kSlots) {
+                            float2 *place = reinterpret_cast<float2 *>(to + (c ? hi : lo) + 2 * j);
+                            *place = fadd2(*place, v);
                         }
                     }
-                    if (live)
-                        store_row<T>(static_cast<T *>(out) + far.at(h, kD), lo, hi, Raw{pack<T>(a), pack<T>(b)});
-                });
-        };
-        heads(run.q0, run.q1, p.q, p.qs, p.qo, p.Hq, p.Hqp, p.magic_q, p.wq);
-        heads(run.k0, run.k1, p.k, p.ks, p.ko, p.Hkv, p.Hkvp, p.magic_k, p.wk);
-        if (run.v0 < run.v1) {
-            const T *src = static_cast<const T *>(p.v) + k.m * p.vs;
-            const Far far(p, k, p.Hkv, p.Hkvp, p.magic_k, kD);
-            for_heads<S>(
-                run.v0, run.v1, sub, [&](int h) { return load_row<T>(src + static_cast<int64_t>(h) * kD, lo, hi); },
-                [&](int h, bool live, const Raw &raw) {
-                    if (live)
-                        store_row<T>(static_cast<T *>(p.vo) + far.at(h, kD), lo, hi, raw);
-                });
+            }
         }
-    }
-}
-
-template <typename T, int kD, bool kInter, bool kNorm>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p)
-{
-    using S = Shape<T, kD>;
-    __shared__ float2 table[kWarps][kD / 2];
-    const int warp = warp_id(), lane = lane_id(), sub = lane / S::kLanes;
-    int lo, hi;
-    chunk_places<S, kInter>(p.half, lane % S::kLanes, lo, hi);
-    // this lane's part of dw: [q, k][lo, hi]
-    float2 dw[2][2][S::kP];
-#pragma unroll
-    for (int j = 0; j < S::kP; ++j)
-        dw[0][0][j] = dw[0][1][j] = dw[1][0][j] = dw[1][1][j] = both(0.f);
-    const int64_t units = p.tokens * p.splits;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < units;
-         u += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const Token k = token_of(p, static_cast<uint32_t>(u / p.splits));
-        const Run run(p, static_cast<int>(u % p.splits));
-        if (run.v0 == 0)
-            angles(p, k, table[warp], lane);
-        auto heads = [&](int h0, int h1, const void *in, int64_t stride, const void *dy, void *dx, int64_t dstride,
-                         int H, int Hp, unsigned magic, const void *w, float2 (&sum)[2][S::kP]) {
-            if (h0 >= h1)
-                return;
-            const Turn<S, kInter, true> turn(table[warp], p.half, lo, hi);
-            float2 wl[S::kP], wh[S::kP];
-            if (kNorm)
-                load_weights<T, S>(w, lo, hi, wl, wh);
-            const T *src = static_cast<const T *>(in) + (kNorm ? k.m * stride : 0);
-            T *dst = static_cast<T *>(dx) + k.m * dstride;
-            const Far far(p, k, H, Hp, magic, kD);
-            struct Two {
-                Raw dy, x;
-            };
-            for_heads<S>(
-                h0, h1, sub,
-                [&](int h) {
-                    Two t;
-                    t.dy = load_row<T>(static_cast<const T *>(dy) + far.at(h, kD), lo, hi);
-                    if (kNorm)
-                        t.x = load_row<T>(src + static_cast<int64_t>(h) * kD, lo, hi);
-                    return t;
-                },
-                [&](int h, bool live, const Two &raw) {
-                    float2 g[2][S::kP];
-                    unpack<T>(raw.dy.lo, g[0]);
-                    unpack<T>(raw.dy.hi, g[1]);
-                    turn.apply(g[0], g[1]);
-                    if (kNorm) {
-                        float2 x[2][S::kP], ss = both(0.f), dot = both(0.f), gx[2][S::kP];
-                        unpack<T>(raw.x.lo, x[0]);
-                        unpack<T>(raw.x.hi, x[1]);
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-#pragma unroll
-                            for (int j = 0; j < S::kP; ++j) {
-                                const float2 w2 = c ? wh[j] : wl[j];
-                                ss = ffma2(x[c][j], x[c][j], ss);
-                                gx[c][j] = fmul2(g[c][j], x[c][j]);
-                                dot = ffma2(w2, gx[c][j], dot);
-                                g[c][j] = fmul2(w2, g[c][j]);
-                            }
-                        const float rstd = rsqrtf(row_sum<S::kLanes>(ss.x + ss.y) * (1.f / kD) + p.eps);
-                        // mean(w g xhat) r: what x loses, before the last factor r
-                        const float m = row_sum<S::kLanes>(dot.x + dot.y) * (1.f / kD) * rstd * rstd;
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-#pragma unroll
-                            for (int j = 0; j < S::kP; ++j) {
-                                if (live)
-                                    sum[c][j] = ffma2(gx[c][j], both(rstd), sum[c][j]);
-                                g[c][j] = fmul2(ffma2(x[c][j], both(-m), g[c][j]), both(rstd));
-                            }
-                    }
-                    if (live)
-                        store_row<T>(dst + static_cast<int64_t>(h) * kD, lo, hi, Raw{pack<T>(g[0]), pack<T>(g[1])});
-                });
-        };
-        heads(run.q0, run.q1, p.q, p.qs, p.qo, p.dq, p.dqs, p.Hq, p.Hqp, p.magic_q, p.wq, dw[0]);
-        heads(run.k0, run.k1, p.k, p.ks, p.ko, p.dk, p.dks, p.Hkv, p.Hkvp, p.magic_k, p.wk, dw[1]);
-        if (run.v0 < run.v1) {
-            T *dst = static_cast<T *>(p.dv) + k.m * p.dvs;
-            const Far far(p, k, p.Hkv, p.Hkvp, p.magic_k, kD);
-            for_heads<S>(
-                run.v0, run.v1, sub,
-                [&](int h) { return load_row<T>(static_cast<const T *>(p.vo) + far.at(h, kD), lo, hi); },
-                [&](int h, bool live, const Raw &raw) {
-                    if (live)
-                        store_row<T>(dst + static_cast<int64_t>(h) * kD, lo, hi, raw);
-                });
+        int h0, h1, row;
+        now.heads(p, 2, h0, h1, row);
+        if (h0 < h1) {
+            T *out = static_cast<T *>(p.dv) + static_cast<int64_t>(now.k.m) * p.dvs;
+#pragma unroll 2
+            for (int h = h0 + sub; h < h1; h += S::kRows)
+                store_row<T>(out + h * kD, lo, hi, load_row<T>(data + (row + h - h0) * kD, lo, hi));
         }
+        __syncwarp();  // the slot is read
+        if (ahead.more()) {
+            fetch(slot);
+            ++started;
+        }
+        ++done;
+        now.step(p);
     }
+    // after a wait that ran out: the copies still on their way (bounded)
+    for (; done < started; ++done)
+        mbar_wait(&ring.bars[done % kBwdRing], (done / kBwdRing) & 1, wait, 0xbf);
     if constexpr (kNorm) {
-        // the block's weight-gradient partial: row slots within the warp, then the
-        // warps, always in the same order
-        __shared__ float sums[kWarps][2][kD];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int j = 0; j < S::kP; ++j) {
-                    float2 v = dw[t][c][j];
-#pragma unroll
-                    for (int o = S::kLanes; o < 32; o <<= 1) {
-                        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-                        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-                    }
-                    if (sub == 0)
-                        *reinterpret_cast<float2 *>(&sums[warp][t][(c ? hi : lo) + 2 * j]) = v;
-                }
+        // the block's weight-gradient partial: row slots and warps, always in the same order
         __syncthreads();
         for (int i = threadIdx.x; i < 2 * kD; i += kThreads) {
-            float s = 0.f;
+            float v = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
-                s += sums[w][i / kD][i % kD];
-            p.partial[static_cast<int64_t>(blockIdx.x) * 2 * kD + i] = s;
+#pragma unroll
+                for (int k = 0; k < kSlots; ++k)
+                    v += reinterpret_cast<const float *>(sums[w])[(i / kD * kSlots + k) * kD + i % kD];
+            p.partial[static_cast<int64_t>(blockIdx.x) * 2 * kD + i] = v;
         }
     }
 }
@@ -482,23 +651,29 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float *__restr
 template <typename T, int kD, bool kInter, bool kNorm>
 cudaError_t run(NormRopeParams &p, bool bwd, cudaStream_t s)
 {
-    constexpr int kRows = Shape<T, kD>::kRows;
-    const int rows = p.Hq + p.Hkv + (p.v ? p.Hkv : 0);
-    // few tokens: a token's rows go to several warps
-    const int64_t want = static_cast<int64_t>(num_sms()) * 16;
-    int splits = static_cast<int>(std::min<int64_t>((rows + kRows - 1) / kRows, (want + p.tokens - 1) / p.tokens));
-    p.rows_per_split = ((rows + splits - 1) / splits + kRows - 1) / kRows * kRows;
-    p.splits = (rows + p.rows_per_split - 1) / p.rows_per_split;
+    const int kRun = (bwd ? kBwdRun : kFwdRun) / static_cast<int>(kD * sizeof(T));
+    const int runs = (p.Hq + (p.v ? 2 : 1) * p.Hkv + kRun - 1) / kRun;
+    const int64_t resident = static_cast<int64_t>(num_sms()) * (bwd ? kBwdBlocks : kFwdBlocks);
+    // few tokens: a token's runs go to several warps
+    const int splits = static_cast<int>(std::min<int64_t>(runs, (resident * kWarps + p.tokens - 1) / p.tokens));
+    p.runs_per_split = (runs + splits - 1) / splits;
+    p.splits = (runs + p.runs_per_split - 1) / p.runs_per_split;
     p.magic_q = p.Hqp == 1 ? 0u : 0xffffffffu / p.Hqp + 1;
     p.magic_k = p.Hkvp == 1 ? 0u : 0xffffffffu / p.Hkvp + 1;
-    const int64_t need = (p.tokens * p.splits + kWarps - 1) / kWarps;
-    int64_t grid = std::min<int64_t>(need, static_cast<int64_t>(num_sms()) * 8);
+    const int64_t grid = std::min<int64_t>((p.tokens * p.splits + kWarps - 1) / kWarps, resident);
     if (!bwd) {
-        norm_rope_fwd_kernel<T, kD, kInter, kNorm><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p);
+        auto kernel = norm_rope_fwd_kernel<T, kD, kInter, kNorm>;
+        constexpr int smem = Ring<kFwdRing, 1, kFwdRun>::kBytes;
+        static_assert(smem <= 40 * 1024, "with the static part, what a launch may take without asking");
+        kernel<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p, wait_cfg());
         return cudaGetLastError();
     }
-    grid = std::min<int64_t>(grid, kNormRopeMaxBlocks);
-    norm_rope_bwd_kernel<T, kD, kInter, kNorm><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p);
+    if (grid > kNormRopeMaxBlocks)
+        return cudaErrorInvalidConfiguration;
+    auto kernel = norm_rope_bwd_kernel<T, kD, kInter, kNorm>;
+    constexpr int smem = Ring<kBwdRing, kNorm ? 2 : 1, kBwdRun>::kBytes;
+    static_assert(smem + static_cast<int>(sizeof(float)) * 18 * kD <= 48 * 1024, "as above");
+    kernel<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p, wait_cfg());
     if (kNorm && (p.dwq || p.dwk))
         norm_rope_dw_kernel<T><<<2 * kD / 32, dim3(32, 32), 0, s>>>(p.partial, static_cast<int>(grid), kD,
                                                                     static_cast<T *>(p.dwq), static_cast<T *>(p.dwk));

@@ -444,10 +444,13 @@ cudaError_t run(const void *logits, const int64_t *labels, void *dlogits, float 
                 float *total, int64_t B, int64_t N, int64_t V, int P, int32_t *shifted, float *row_loss,
                 unsigned long long *good, cudaStream_t s)
 {
+    const int64_t Np = N / P;
     const int64_t rows = B * N;
-    cudaError_t e = launch_shift_count(labels, shifted, good, B, N, P, V, s);
+    cudaError_t e = cudaMemsetAsync(good, 0, sizeof(unsigned long long) * P, s);
     if (e != cudaSuccess)
         return e;
+    shift_count_kernel<<<static_cast<unsigned>((rows + 255) / 256), 256, 0, s>>>(labels, shifted, good, B, N, Np, P,
+                                                                                 V, device_status_ptr());
     const bool vec = (V % 8 == 0) && (reinterpret_cast<uintptr_t>(logits) % 16 == 0) &&
                      (dlogits == nullptr || reinterpret_cast<uintptr_t>(dlogits) % 16 == 0);
     // with the gradient: the smallest cluster whose chunks fit on chip
@@ -493,30 +496,12 @@ cudaError_t run(const void *logits, const int64_t *labels, void *dlogits, float 
     else
         ce_rows_kernel<T, false><<<static_cast<unsigned>(rows), kRowThreads, 0, s>>>(
             static_cast<const T *>(logits), shifted, good, P, V, row_loss, static_cast<T *>(dlogits));
-    return launch_shard_totals(row_loss, good, shard_loss, shard_good, total, B, N, P, s);
-}
-
-}  // namespace
-
-cudaError_t launch_shift_count(const int64_t *labels, int32_t *shifted, unsigned long long *good, int64_t B, int64_t N,
-                               int P, int64_t V, cudaStream_t s)
-{
-    cudaError_t e = cudaMemsetAsync(good, 0, sizeof(unsigned long long) * P, s);
-    if (e != cudaSuccess)
-        return e;
-    const int64_t rows = B * N;
-    shift_count_kernel<<<static_cast<unsigned>((rows + 255) / 256), 256, 0, s>>>(labels, shifted, good, B, N, N / P, P,
-                                                                                 V, device_status_ptr());
-    return cudaGetLastError();
-}
-
-cudaError_t launch_shard_totals(const float *row_loss, const unsigned long long *good, float *shard_loss,
-                                int64_t *shard_good, float *total, int64_t B, int64_t N, int P, cudaStream_t s)
-{
-    shard_reduce_kernel<<<P, 1024, 0, s>>>(row_loss, good, B * (N / P), shard_loss, shard_good);
+    shard_reduce_kernel<<<P, 1024, 0, s>>>(row_loss, good, B * Np, shard_loss, shard_good);
     total_kernel<<<1, 1, 0, s>>>(shard_loss, shard_good, P, total);
     return cudaGetLastError();
 }
+
+}  // namespace
 
 cudaError_t launch_sharded_ce(const void *logits, const int64_t *labels, void *dlogits, float *shard_loss,
                               int64_t *shard_good, float *total, int64_t B, int64_t N, int64_t V, int P, int esize,

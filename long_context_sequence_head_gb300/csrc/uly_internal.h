@@ -218,9 +218,9 @@ struct NormRopeParams {
     int to_head;
     int half;  // rot / 2
     float eps;
-    // set by the launch: warps per token, rows each takes, and 2^32 / (H/P)
+    // set by the launch: warps per token, runs each takes, and 2^32 / (H/P)
     // rounded up (0 for H/P = 1)
-    int splits, rows_per_split;
+    int splits, runs_per_split;
     unsigned magic_q, magic_k;
     uint64_t turn[kNormRopeMaxHalf];  // inv_freq / 2 pi as a 64-bit fraction of a turn
     uint8_t axis[kNormRopeMaxHalf];
@@ -233,12 +233,6 @@ cudaError_t launch_sharded_ce(const void *logits, const int64_t *labels, void *d
                               int64_t *shard_good, float *total, int64_t B, int64_t N, int64_t V, int P, int esize,
                               void *workspace, cudaStream_t stream);
 size_t sharded_ce_workspace(int64_t B, int64_t N, int P);
-// Its first and last steps: labels shifted over the whole sequence with each
-// shard's good-token count, and the shards' means with their total.
-cudaError_t launch_shift_count(const int64_t *labels, int32_t *shifted, unsigned long long *good, int64_t B, int64_t N,
-                               int P, int64_t V, cudaStream_t stream);
-cudaError_t launch_shard_totals(const float *row_loss, const unsigned long long *good, float *shard_loss,
-                                int64_t *shard_good, float *total, int64_t B, int64_t N, int P, cudaStream_t stream);
 
 // ------------------------------------------ LM head and sharded loss in one
 cudaError_t launch_sharded_linear_ce(const void *hidden, const void *weight, const int64_t *labels, void *dhidden,
