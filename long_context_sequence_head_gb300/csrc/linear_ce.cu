@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(1024) labels_kernel(const int64_t *__restrict_
 {
     constexpr int kEach = 4;
     __shared__ int warp_sum[32];
+    grid_next();
     for (int r = threadIdx.x; r < P; r += 1024)
         good[r] = 0;
     if (threadIdx.x == 0)
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(1024) totals_kernel(const float *__restrict__ 
 {
     __shared__ float2 part[32];
     __shared__ int last;
+    grid_wait();
     const int r = blockIdx.x;
     const float *base = row_loss + r * per_shard;
     float2 s = make_float2(0.f, 0.f);
@@ -245,6 +247,8 @@ __global__ void gather_kernel(const __grid_constant__ CeArgs a, const void *__re
                               const int32_t *__restrict__ shifted, int32_t *__restrict__ label, void *__restrict__ out,
                               int64_t ldh, int64_t rows)
 {
+    grid_wait();
+    grid_next();
     const int cnt = ce_piece_rows(a), r = blockIdx.x;
     if (a.base == 0 && a.dh != nullptr && r < rows && shifted[r] < 0) {
         const int vecs = a.D * (kSplit ? 4 : 2) / 16;
@@ -277,6 +281,8 @@ __global__ void gather_kernel(const __grid_constant__ CeArgs a, const void *__re
 template <bool kSplit>
 __global__ void lay_weight_kernel(const void *__restrict__ w, int D, int V, uint16_t *__restrict__ out, int64_t ldw)
 {
+    grid_wait();
+    grid_next();
     const int64_t v = blockIdx.x;
     for (int i = threadIdx.x * 8; i < D; i += blockDim.x * 8) {
         if constexpr (kSplit) {
@@ -299,6 +305,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
                                                            const int32_t *__restrict__ label,
                                                            float *__restrict__ row_loss)
 {
+    grid_wait();
+    grid_next();
     const int cnt = ce_piece_rows(a), r = blockIdx.x;
     if (r >= (cnt + kCeStep - 1) / kCeStep * kCeStep)
         return;
@@ -453,32 +461,36 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
     labels_kernel<<<1, 1024, 0, s>>>(labels, shifted, good, row_loss, index, a.n_good, shards_done,
                                      static_cast<unsigned>(rows), static_cast<unsigned>(N / P),
                                      static_cast<unsigned>(B), P, V, device_status_ptr());
-    cudaError_t e = cudaSuccess;
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
     const void *w = weight;
     int64_t ldw = D;
     if (L.lay_weight) {
         w = ws + L.w;
         ldw = L.ldh;
-        lay_weight_kernel<kSplit><<<V, 128, 0, s>>>(weight, D, V, reinterpret_cast<uint16_t *>(ws + L.w), ldw);
+        e = launch_after(lay_weight_kernel<kSplit>, V, 128, 0, s, weight, D, V,
+                         reinterpret_cast<uint16_t *>(ws + L.w), ldw);
     }
     for (int64_t base = 0; base < rows; base += L.rows) {
         a.base = base;
         const int64_t blocks = base == 0 ? std::max<int64_t>(rows, L.rows) : L.rows;
-        gather_kernel<kSplit><<<static_cast<unsigned>(blocks), 128, 0, s>>>(a, hidden, shifted, label, ws + L.h, L.ldh,
-                                                                           rows);
-        e = launch_ce_product(kCeLogits, a, ws + L.h, L.ldh, w, ldw, g, kEsize, s);
-        if (e != cudaSuccess)
-            return e;
-        rows_kernel<kSplit><<<L.rows, kRowThreads, 0, s>>>(a, g, label, row_loss);
-        if (dhidden)
+        if (e == cudaSuccess)
+            e = launch_after(gather_kernel<kSplit>, blocks, 128, 0, s, a, hidden, shifted, label, ws + L.h, L.ldh,
+                             rows);
+        if (e == cudaSuccess)
+            e = launch_ce_product(kCeLogits, a, ws + L.h, L.ldh, w, ldw, g, kEsize, s);
+        if (e == cudaSuccess)
+            e = launch_after(rows_kernel<kSplit>, L.rows, kRowThreads, 0, s, a, g, label, row_loss);
+        if (e == cudaSuccess && dhidden)
             e = launch_ce_product(kCeDh, a, ws + L.h, L.ldh, w, ldw, g, kEsize, s);
         if (e == cudaSuccess && dweight)
             e = launch_ce_product(kCeDw, a, ws + L.h, L.ldh, w, ldw, g, kEsize, s);
         if (e != cudaSuccess)
             return e;
     }
-    totals_kernel<<<P, 1024, 0, s>>>(row_loss, good, rows / P, P, shard_loss, shard_good, total, shards_done);
-    return cudaGetLastError();
+    return launch_after(totals_kernel, P, 1024, 0, s, row_loss, good, rows / P, P, shard_loss, shard_good, total,
+                        shards_done);
 }
 
 }  // namespace

@@ -13,7 +13,7 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // contraction per step.
 constexpr int kCeTile = 256;
 constexpr int kCeStep = 64;
-constexpr int kCeStatCols = 128;  // columns behind one (c, s) of the softmax
+constexpr int kCeStatCols = 64;  // columns behind one (c, s) of the softmax
 constexpr int kCeMaxPairs = 80;
 // floats a pair leaves for one tile
 constexpr int64_t kCeTileFloats = static_cast<int64_t>(kCeTile) * kCeTile;

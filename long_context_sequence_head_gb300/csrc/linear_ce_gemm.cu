@@ -10,8 +10,10 @@
 // a matrix whose rows run along the contraction is K-major, one whose rows run
 // along the output (W in dh; g and h in dW) is MN-major.
 //
-// Warps 0-7 write results out (TMEM lane quarter warp % 4, columns 128 (warp /
-// 4) ..), warp 8 loads, warp 9 issues products.
+// Warps 0-15 write results out (TMEM lane quarter warp % 4, columns 64 (warp /
+// 4) ..): the logits' exponentials take longer than a short contraction's
+// products, and four warps a scheduler hide each other's latencies where two
+// do not.  Warp 16 loads, warp 17 issues products.
 //
 // Tiles beyond the last full round over the pairs are split along the
 // contraction when that saves more than joining them costs: every pair takes
@@ -41,10 +43,10 @@ constexpr int kStages = 5;
 constexpr int kHalf = 128;                               // rows of A, columns of B per CTA
 constexpr int kOperandBytes = kHalf * kCeStep * 2;       // 16 KB
 constexpr int kStageBytes = 2 * kOperandBytes;           // this CTA's part
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
 constexpr int kThreads = 32 * (kEpiWarps + 2);
-constexpr int kCols = 128;                               // columns per writing warp
-constexpr int kWarpStaging = 32 * 256;                   // 32 rows of 256 bytes
+constexpr int kCols = kCeStatCols;                       // columns per writing warp
+constexpr int kWarpStaging = 32 * 128;                   // 32 rows of 128 bytes
 constexpr int kBars = 2 * kStages + 5;
 constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kWarpStaging + 8 * kBars + 16 + 1024;
 constexpr int kPlanePairs = 6;
@@ -146,11 +148,11 @@ __device__ __forceinline__ void tile_origin(const Plan &p, int tile, int &m0, in
 }
 
 // A tile's fp32 values in memory, as the writers hold them: per CTA and warp
-// 32 groups of 4 columns, each 32 rows x 16 bytes, so that a warp's access is
+// 16 groups of 4 columns, each 32 rows x 16 bytes, so that a warp's access is
 // 512 bytes in a row.
 __device__ __forceinline__ float4 *tile_slot(float *buf, int64_t slot, int cta, int warp, int lane)
 {
-    return reinterpret_cast<float4 *>(buf + slot * kCeTileFloats) + (cta * kEpiWarps + warp) * (32 * 32) + lane;
+    return reinterpret_cast<float4 *>(buf + slot * kCeTileFloats) + (cta * kEpiWarps + warp) * (kCols / 4 * 32) + lane;
 }
 
 // ------------------------------------------------------------ writing out
@@ -172,8 +174,8 @@ __device__ __forceinline__ uint4 bf16s(const float *v)
                       pack_bf16x2(v[6], v[7]));
 }
 
-// The warp's 32 rows x 128 columns (row = lane) to memory, 256 bytes of a row
-// per half warp: through shared memory, units of 16 bytes permuted within the
+// The warp's 32 rows x 64 columns (row = lane) to memory, 128 bytes of a row
+// per 8 lanes: through shared memory, units of 16 bytes permuted within the
 // row so that neither side meets a bank conflict.  row: where this lane's row
 // goes, negative: nowhere.  Columns from `limit` on are not written (a
 // multiple of 16 bytes).
@@ -182,21 +184,20 @@ __device__ __forceinline__ void store_rows(const float (&x)[kCols], void *out, i
                                            int limit, uint8_t *staging, int lane)
 {
     constexpr int kPer = kF32 ? 4 : 8;  // values per unit
-    constexpr int kParts = kCols / (16 * kPer);
 #pragma unroll
-    for (int part = 0; part < kParts; ++part) {
+    for (int part = 0; part < kCols / (8 * kPer); ++part) {
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {
-            const float *v = x + (part * 16 + u) * kPer;
-            *reinterpret_cast<uint4 *>(staging + lane * 256 + ((u ^ (lane & 15)) << 4)) = kF32 ? words(v) : bf16s(v);
+        for (int u = 0; u < 8; ++u) {
+            const float *v = x + (part * 8 + u) * kPer;
+            *reinterpret_cast<uint4 *>(staging + lane * 128 + ((u ^ (lane & 7)) << 4)) = kF32 ? words(v) : bf16s(v);
         }
         __syncwarp();
-        const int u = lane & 15, col = col0 + (part * 16 + u) * kPer;
+        const int u = lane & 7, col = col0 + (part * 8 + u) * kPer;
         uint8_t *to = static_cast<uint8_t *>(out) + static_cast<int64_t>(col) * (16 / kPer);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int r = 2 * i + (lane >> 4), at = __shfl_sync(0xffffffffu, row, r);
-            const uint4 val = *reinterpret_cast<const uint4 *>(staging + r * 256 + ((u ^ (r & 15)) << 4));
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3), at = __shfl_sync(0xffffffffu, row, r);
+            const uint4 val = *reinterpret_cast<const uint4 *>(staging + r * 128 + ((u ^ (r & 7)) << 4));
             if (at >= 0 && col < limit)
                 *reinterpret_cast<uint4 *>(to + at * (pitch * (16 / kPer))) = val;
         }
@@ -205,34 +206,31 @@ __device__ __forceinline__ void store_rows(const float (&x)[kCols], void *out, i
 }
 
 // The exponentials to their buffer by TMA: boxes of 32 rows x 128 bytes in the
-// swizzled layout of the map, two at a time.  Rows past the piece's last are
-// written too where the buffer has them; nobody reads them.
+// swizzled layout of the map.  Rows past the piece's last are written too
+// where the buffer has them; nobody reads them.
 template <bool kSplit>
 __device__ __forceinline__ void store_exponentials(const CUtensorMap *te, const float (&x)[kCols], int row0, int col0,
                                                    int limit, uint8_t *staging, int lane)
 {
     constexpr int kPer = kSplit ? 4 : 8, kBox = 8 * kPer;  // values per unit, columns per box
 #pragma unroll
-    for (int part = 0; part < kCols / (2 * kBox); ++part) {
+    for (int part = 0; part < kCols / kBox; ++part) {
         if (lane == 0)
             bulk_wait_read<0>();  // what was staged before is on its way
         __syncwarp();
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {
-            const float *v = x + (part * 16 + u) * kPer;
+        for (int u = 0; u < 8; ++u) {
+            const float *v = x + (part * 8 + u) * kPer;
             const uint4 val = kSplit ? words(v)
                                      : make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]),
                                                   pack_f16x2(v[4 % kPer], v[5 % kPer]),
                                                   pack_f16x2(v[6 % kPer], v[7 % kPer]));
-            *reinterpret_cast<uint4 *>(staging + (u >> 3) * 4096 + lane * 128 + (((u & 7) ^ (lane & 7)) << 4)) = val;
+            *reinterpret_cast<uint4 *>(staging + lane * 128 + ((u ^ (lane & 7)) << 4)) = val;
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-                if (col0 + (2 * part + b) * kBox < limit)
-                    tma_store_2d(te, staging + b * 4096, col0 + (2 * part + b) * kBox, row0);
+        if (lane == 0 && col0 + part * kBox < limit) {
+            tma_store_2d(te, staging, col0 + part * kBox, row0);
             bulk_commit();
         }
     }
@@ -334,9 +332,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ce_product_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                       const __grid_constant__ CUtensorMap te, const __grid_constant__ CeArgs a, const WaitCfg w)
 {
-    const int cnt = ce_piece_rows(a);
-    if (cnt == 0 && (kWhat != kCeDw || a.base > 0))
-        return;  // the whole grid agrees; dW without any row is written as zeros by the first piece
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint8_t *staging = smem + kStages * kStageBytes;
@@ -347,7 +342,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int warp = warp_id(), lane = lane_id();
     const int cta = static_cast<int>(cluster_ctarank());
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const Plan plan = make_plan<kWhat>(a, cnt, pairs);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -363,6 +357,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
     if (warp == kEpiWarps) {
+        if (lane == 0) {
+            prefetch_tmap(&ta);
+            prefetch_tmap(&tb);
+        }
+        __syncwarp();
         tmem_alloc_pair(tmem_ptr, 512);
         tmem_relinquish_pair();
     }
@@ -371,13 +370,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync_all();  // the other CTA's barriers are set up
     tc_fence_after();
     const uint32_t tbase = *tmem_ptr;
+    grid_wait();
+    grid_next();
+    const int cnt = ce_piece_rows(a);
+    Plan plan = make_plan<kWhat>(a, cnt, pairs);
+    if (cnt == 0 && (kWhat != kCeDw || a.base > 0))
+        plan.whole = plan.workers = 0;  // nothing to do; dW without any row is written as zeros by the first piece
     constexpr int kPerStep = kSplit ? kPlanePairs : 1;
 
     if (warp == kEpiWarps) {
         // ------------------------------------------------ loads
         if (lane == 0) {
-            prefetch_tmap(&ta);
-            prefetch_tmap(&tb);
             Units units(plan, pair, pairs);
             Unit u;
             uint32_t it = 0;
@@ -519,12 +522,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tmem_ld_fence32p(v + j);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < kCols; j += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(t + j, v);
-                        tmem_ld_wait(v);
+                    for (int j = 0; j < kCols; j += 16) {
+                        uint32_t v[16];
+                        tmem_ld16_wait(t + j, v);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
+                        for (int i = 0; i < 16; i += 2) {
                             const float2 s = fadd2(make_float2(x[j + i], x[j + i + 1]),
                                                    make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
                             x[j + i] = s.x;
@@ -567,11 +569,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // Adds the runs of the split tiles, in the order of the contraction.  A warp
 // takes 32 rows x 16 columns, since few tiles are split and each may have
-// dozens of runs; a block is one (tile, CTA half, 32 rows x 128 columns).
+// dozens of runs; a block is one (tile, CTA half, 32 rows x 64 columns).
+constexpr int kJoinThreads = kCols / 16 * 32;
 template <int kWhat, bool kSplit>
-__global__ void __launch_bounds__(256) ce_join_kernel(const __grid_constant__ CeArgs a, int pairs)
+__global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const __grid_constant__ CeArgs a, int pairs)
 {
     constexpr int kPart = 16;
+    grid_wait();
+    grid_next();
     const int cnt = ce_piece_rows(a);
     if (cnt == 0)
         return;
@@ -702,15 +707,14 @@ cudaError_t launch(const CeArgs &a, const CUtensorMap &ta, const CUtensorMap &tb
         pairs = std::max(1, std::min(std::min(pairs, num_sms() / 2), kCeMaxPairs));
         known[dev].store(pairs);
     }
-    kernel<<<2 * pairs, kThreads, kSmem, s>>>(ta, tb, te, a, wait_cfg());
+    e = launch_after(kernel, 2 * pairs, kThreads, kSmem, s, ta, tb, te, a, wait_cfg());
     if constexpr (kWhat != kCeLogits) {
         // never split below this many steps: nothing to join
         const int kb = ((kWhat == kCeDh ? a.V : a.rows) + kCeStep - 1) / kCeStep;
-        if (kb > kSplitGain && pairs > 1) {
-            ce_join_kernel<kWhat, kSplit><<<2 * kEpiWarps * (pairs - 1), 256, 0, s>>>(a, pairs);
-        }
+        if (e == cudaSuccess && kb > kSplitGain && pairs > 1)
+            e = launch_after(ce_join_kernel<kWhat, kSplit>, 2 * kEpiWarps * (pairs - 1), kJoinThreads, 0, s, a, pairs);
     }
-    return cudaGetLastError();
+    return e;
 }
 
 template <bool kSplit>

@@ -453,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float2 table[kWarps][kD / 2];
     __shared__ __align__(16) T weights[2][kD];
+    grid_next();
     const int warp = warp_id(), lane = lane_id(), sub = lane / S::kLanes;
     if (kNorm) {
         for (int i = threadIdx.x; i < kD; i += kThreads) {
@@ -628,17 +629,18 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float *__restr
                                                             T *__restrict__ dwq, T *__restrict__ dwk)
 {
     __shared__ float run[32][33];
-    const int col = blockIdx.x * 32 + threadIdx.x;
+    grid_wait();
+    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32, col = blockIdx.x * 32 + tx;
     float s = 0.f;
-    for (int b = threadIdx.y; b < blocks; b += 32)
+    for (int b = ty; b < blocks; b += 32)
         s += partial[static_cast<int64_t>(b) * 2 * d + col];
-    run[threadIdx.y][threadIdx.x] = s;
+    run[ty][tx] = s;
     __syncthreads();
-    if (threadIdx.y != 0)
+    if (ty != 0)
         return;
     s = 0.f;
     for (int k = 0; k < 32; ++k)
-        s += run[k][threadIdx.x];
+        s += run[k][tx];
     T *dw = col < d ? dwq : dwk;
     if (dw == nullptr)
         return;
@@ -674,10 +676,13 @@ cudaError_t run(NormRopeParams &p, bool bwd, cudaStream_t s)
     constexpr int smem = Ring<kBwdRing, kNorm ? 2 : 1, kBwdRun>::kBytes;
     static_assert(smem + static_cast<int>(sizeof(float)) * 18 * kD <= 48 * 1024, "as above");
     kernel<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p, wait_cfg());
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
     if (kNorm && (p.dwq || p.dwk))
-        norm_rope_dw_kernel<T><<<2 * kD / 32, dim3(32, 32), 0, s>>>(p.partial, static_cast<int>(grid), kD,
-                                                                    static_cast<T *>(p.dwq), static_cast<T *>(p.dwk));
-    return cudaGetLastError();
+        return launch_after(norm_rope_dw_kernel<T>, 2 * kD / 32, 1024, 0, s, p.partial, static_cast<int>(grid), kD,
+                            static_cast<T *>(p.dwq), static_cast<T *>(p.dwk));
+    return cudaSuccess;
 }
 
 template <typename T, int kD>

@@ -90,6 +90,24 @@ inline int group_for(int64_t work_per_problem, int64_t longest_unit, int64_t npr
     return g < 1 ? 1 : static_cast<int>(g);
 }
 
+// Launches a kernel that calls grid_wait(): its blocks may be set up while the
+// kernel before it on the stream finishes, which hides a launch of small ones.
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), int64_t grid, int block, size_t smem, cudaStream_t s, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(block));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 inline WaitCfg wait_cfg() { return WaitCfg{device_status_ptr(), wait_limit_ns()}; }
 
 // ---------------------------------------------------------------- swap
