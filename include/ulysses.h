@@ -428,8 +428,8 @@ uly_status ulysses_sharded_ce_loss(const void *logits, const int64_t *labels, vo
  * The LM head and ulysses_sharded_ce_loss in one, without the logits: the
  * same shifted labels, per-shard means and good-token-weighted total, of
  *   logits[row][v] = <hidden[row], weight[v]>
- * which are formed in pieces of at most 8192 rows with a label and never
- * kept: a long sequence's logits and their gradient outweigh everything else
+ * which are formed in pieces of rows with a label (as many as 2.5 GB of
+ * workspace hold, at least 1024, at most 65536) and never kept: a long sequence's logits and their gradient outweigh everything else
  * the step holds (at 65,536 tokens and a vocabulary of 151,936, 20 GB each in
  * bf16).  Rows without a label (ignored ones, and the last of each sequence)
  * take no part: their hidden values are not read.

@@ -21,11 +21,13 @@
 namespace uly {
 namespace {
 
-constexpr int kRowThreads = 512;
-// Rows of a piece.  Larger pieces spread the fp32 dW that is carried from
-// piece to piece (read and written once each) over more products; the buffer
-// of exponentials grows with them (2 bytes a value, 10 in fp32).
-constexpr int kPieceBf16 = 8192, kPieceFp32 = 2048;
+// Rows of a piece: as many as hold kPieceBytes of exponentials and gradients (2
+// bytes a value, 10 in fp32), at least 1024.  Larger pieces spread the fp32 dW
+// that is carried from piece to piece (read and written once each) over more
+// products.
+constexpr int64_t kPieceBytes = int64_t(2500) << 20;
+// Vocabularies above this take 512 threads a row, others 128.
+constexpr int kLongRow = 8192;
 // From this many rows on, a bf16 weight whose rows are not whole 128-byte
 // lines is copied to a pitch that is (TMA reads two lines for every 128 bytes
 // of a row that starts inside one).
@@ -81,93 +83,6 @@ __device__ __forceinline__ void load8(const float *row, int i, int D, float (&x)
     const float4 a = *reinterpret_cast<const float4 *>(row + i);
     const float4 b = i + 4 < D ? *reinterpret_cast<const float4 *>(row + i + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-
-// One block: the labels shifted over the whole sequence, each shard's good
-// rows, and the good rows in order (index[i] = row of the i-th one).  A row's
-// loss starts as 0.  Labels out of range are reported and ignored.  4096 rows a
-// round: 2 us each, against 4 ms of products behind as many rows.
-__global__ void __launch_bounds__(1024) labels_kernel(const int64_t *__restrict__ labels, int32_t *__restrict__ shifted,
-                                                      unsigned long long *__restrict__ good,
-                                                      float *__restrict__ row_loss, int32_t *__restrict__ index,
-                                                      int *__restrict__ n_good, int *__restrict__ shards_done,
-                                                      unsigned rows, unsigned Np, unsigned B, int P, int V,
-                                                      unsigned *status)
-{
-    constexpr int kEach = 4;
-    __shared__ int warp_sum[32];
-    grid_next();
-    for (int r = threadIdx.x; r < P; r += 1024)
-        good[r] = 0;
-    if (threadIdx.x == 0)
-        *shards_done = 0;
-    __syncthreads();
-    int done = 0;
-    for (int64_t base = 0; base < rows; base += 1024 * kEach) {
-        const int64_t first = base + static_cast<int64_t>(threadIdx.x) * kEach;
-        int32_t y[kEach];
-        int mine = 0;
-        // place in the shard's sequence; the next token is the next row, or,
-        // at the end of a shard, the first of the same sequence in the next
-        unsigned t = static_cast<unsigned>(first < rows ? first : 0) % Np;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i, ++t) {
-            y[i] = -100;
-            if (first + i >= rows)
-                continue;
-            if (t == Np)
-                t = 0;
-            const int64_t next = first + i + 1 + (t + 1 == Np ? static_cast<int64_t>(B - 1) * Np : 0);
-            if (next < rows) {
-                const int64_t lab = labels[next];
-                if (lab >= 0 && lab < V)
-                    y[i] = static_cast<int32_t>(lab);
-                else if (lab != -100)
-                    atomicOr(status, kDevBadArg);
-            }
-            mine += y[i] >= 0;
-        }
-        // places of this thread's good rows among all
-        int upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, o);
-            upto += lane_id() >= o ? v : 0;
-        }
-        if (lane_id() == 31)
-            warp_sum[warp_id()] = upto;
-        __syncthreads();
-        int sum = warp_sum[lane_id()];  // every warp scans the 32 sums
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, sum, o);
-            sum += lane_id() >= o ? v : 0;
-        }
-        const int before = __shfl_sync(0xffffffffu, sum, warp_id() > 0 ? warp_id() - 1 : 0);
-        int at = done + upto - mine + (warp_id() > 0 ? before : 0);
-        done += __shfl_sync(0xffffffffu, sum, 31);
-        // a warp's 128 rows are of one shard, mostly
-        const int64_t w0 = base + static_cast<int64_t>(warp_id()) * 32 * kEach;
-        const unsigned r0 = static_cast<unsigned>(w0 < rows ? w0 : 0) / (Np * B);
-        const bool one = w0 + 32 * kEach <= static_cast<int64_t>(r0 + 1) * Np * B;
-        if (one && lane_id() == 31 && upto > 0)
-            atomicAdd(&good[r0], static_cast<unsigned long long>(upto));
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            if (first + i >= rows)
-                continue;
-            shifted[first + i] = y[i];
-            row_loss[first + i] = 0.f;
-            if (y[i] >= 0) {
-                index[at++] = static_cast<int32_t>(first + i);
-                if (!one)
-                    atomicAdd(&good[static_cast<unsigned>(first + i) / (Np * B)], 1ull);
-            }
-        }
-        __syncthreads();
-    }
-    if (threadIdx.x == 0)
-        *n_good = done;
 }
 
 // A sum held as hi + lo: 48 bits without the slow 64-bit units.
@@ -238,90 +153,210 @@ __global__ void __launch_bounds__(1024) totals_kernel(const float *__restrict__ 
         *total = static_cast<float>(num / static_cast<double>(den > 1 ? den : 1));
 }
 
+// One block: the labels shifted over the whole sequence, each shard's good
+// rows, and the good rows in order (index[i] = row of the i-th one).  A row's
+// loss starts as 0.  Labels out of range are reported and ignored.  8192 rows a
+// round of about 6 us, against 8 ms of products behind as many rows.
+__global__ void __launch_bounds__(1024) labels_kernel(const int64_t *__restrict__ labels, int32_t *__restrict__ shifted,
+                                                      unsigned long long *__restrict__ good,
+                                                      float *__restrict__ row_loss, int32_t *__restrict__ index,
+                                                      int *__restrict__ n_good, int *__restrict__ shards_done,
+                                                      unsigned rows, unsigned Np, unsigned B, int P, int V,
+                                                      unsigned *status)
+{
+    constexpr int kEach = 8;
+    __shared__ int warp_sum[32];
+    grid_next();
+    for (int r = threadIdx.x; r < P; r += 1024)
+        good[r] = 0;
+    if (threadIdx.x == 0)
+        *shards_done = 0;
+    __syncthreads();
+    int done = 0;
+    for (int64_t base = 0; base < rows; base += 1024 * kEach) {
+        const int64_t first = base + static_cast<int64_t>(threadIdx.x) * kEach;
+        int32_t y[kEach];
+        int mine = 0;
+        // place in the shard's sequence; the next token is the next row, or,
+        // at the end of a shard, the first of the same sequence in the next
+        unsigned t = static_cast<unsigned>(first < rows ? first : 0) % Np;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i, ++t) {
+            y[i] = -100;
+            if (first + i >= rows)
+                continue;
+            if (t == Np)
+                t = 0;
+            const int64_t next = first + i + 1 + (t + 1 == Np ? static_cast<int64_t>(B - 1) * Np : 0);
+            if (next < rows) {
+                const int64_t lab = labels[next];
+                if (lab >= 0 && lab < V)
+                    y[i] = static_cast<int32_t>(lab);
+                else if (lab != -100)
+                    atomicOr(status, kDevBadArg);
+            }
+            mine += y[i] >= 0;
+        }
+        // places of this thread's good rows among all
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane_id() >= o ? v : 0;
+        }
+        if (lane_id() == 31)
+            warp_sum[warp_id()] = upto;
+        __syncthreads();
+        int sum = warp_sum[lane_id()];  // every warp scans the 32 sums
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            sum += lane_id() >= o ? v : 0;
+        }
+        const int before = __shfl_sync(0xffffffffu, sum, warp_id() > 0 ? warp_id() - 1 : 0);
+        int at = done + upto - mine + (warp_id() > 0 ? before : 0);
+        done += __shfl_sync(0xffffffffu, sum, 31);
+        // a warp's 256 rows are of one shard, mostly
+        const int64_t w0 = base + static_cast<int64_t>(warp_id()) * 32 * kEach;
+        const unsigned r0 = static_cast<unsigned>(w0 < rows ? w0 : 0) / (Np * B);
+        const bool one = w0 + 32 * kEach <= static_cast<int64_t>(r0 + 1) * Np * B;
+        if (one && lane_id() == 31 && upto > 0)
+            atomicAdd(&good[r0], static_cast<unsigned long long>(upto));
+        if (first + kEach <= rows) {
+#pragma unroll
+            for (int i = 0; i < kEach; i += 4) {
+                *reinterpret_cast<int4 *>(shifted + first + i) = make_int4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+                *reinterpret_cast<float4 *>(row_loss + first + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            if (first + i >= rows)
+                continue;
+            if (first + kEach > rows) {
+                shifted[first + i] = y[i];
+                row_loss[first + i] = 0.f;
+            }
+            if (y[i] >= 0) {
+                index[at++] = static_cast<int32_t>(first + i);
+                if (!one)
+                    atomicAdd(&good[static_cast<unsigned>(first + i) / (Np * B)], 1ull);
+            }
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0)
+        *n_good = done;
+}
+
+// Eight values of row `row`, columns [i, i + 8), to the products' layout.
+template <bool kSplit>
+__device__ __forceinline__ void lay8(const void *src, int64_t row, int i, int D, uint16_t *out, int64_t to, int64_t pitch,
+                                     int64_t plane)
+{
+    if constexpr (kSplit) {
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (src)
+            load8(static_cast<const float *>(src) + row * D, i, D, x);
+        store_planes(out + to * pitch + i, plane, x);
+    } else {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (src)
+            x = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src) + row * D + i);
+        *reinterpret_cast<uint4 *>(out + to * pitch + i) = x;
+    }
+}
+
 // The piece's hidden rows next to each other (fp32: as planes), with their
 // labels; zeros up to a multiple of 64 rows, where dW's contraction ends.  The
-// first piece also clears the gradient of the rows without a label: its block
-// r looks at row r of the call.
+// first piece also clears the gradient of the rows without a label: its row r
+// then stands for row r of the call too.  A thread takes eight values.
 template <bool kSplit>
-__global__ void gather_kernel(const __grid_constant__ CeArgs a, const void *__restrict__ hidden,
-                              const int32_t *__restrict__ shifted, int32_t *__restrict__ label, void *__restrict__ out,
-                              int64_t ldh, int64_t rows)
+__global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ CeArgs a, const void *__restrict__ hidden,
+                                                     const int32_t *__restrict__ shifted, int32_t *__restrict__ label,
+                                                     uint16_t *__restrict__ out, int64_t ldh, int64_t rows)
 {
     grid_wait();
     grid_next();
-    const int cnt = ce_piece_rows(a), r = blockIdx.x;
+    const int cnt = ce_piece_rows(a), vecs = (a.D + 7) / 8;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x, r = at / vecs;
+    const int i = static_cast<int>(at - r * vecs) * 8;
     if (a.base == 0 && a.dh != nullptr && r < rows && shifted[r] < 0) {
-        const int vecs = a.D * (kSplit ? 4 : 2) / 16;
-        for (int i = threadIdx.x; i < vecs; i += blockDim.x)
-            static_cast<uint4 *>(a.dh)[static_cast<int64_t>(r) * vecs + i] = make_uint4(0, 0, 0, 0);
+        uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.dh) + (r * a.D + i) * (kSplit ? 4 : 2));
+        to[0] = make_uint4(0, 0, 0, 0);
+        if (kSplit && i + 4 < a.D)
+            to[1] = make_uint4(0, 0, 0, 0);
     }
     if (r >= (cnt + kCeStep - 1) / kCeStep * kCeStep)
         return;
     const bool live = r < cnt;
     const int64_t src = live ? a.index[a.base + r] : 0;
-    if (threadIdx.x == 0)
+    if (i == 0)
         label[r] = live ? shifted[src] : -1;
-    for (int i = threadIdx.x * 8; i < a.D; i += blockDim.x * 8) {
-        if constexpr (kSplit) {
-            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (live)
-                load8(static_cast<const float *>(hidden) + src * a.D, i, a.D, x);
-            store_planes(static_cast<uint16_t *>(out) + r * ldh + i, ldh * a.rows, x);
-        } else {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (live)
-                x = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(hidden) + src * a.D + i);
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + r * ldh + i) = x;
-        }
-    }
+    lay8<kSplit>(live ? hidden : nullptr, src, i, a.D, out, r, ldh, ldh * a.rows);
 }
 
 // The weight as the products want it: fp32 as planes, bf16 on a pitch of
 // whole 128-byte lines.
 template <bool kSplit>
-__global__ void lay_weight_kernel(const void *__restrict__ w, int D, int V, uint16_t *__restrict__ out, int64_t ldw)
+__global__ void __launch_bounds__(256) lay_weight_kernel(const void *__restrict__ w, int D, int V,
+                                                         uint16_t *__restrict__ out, int64_t ldw)
 {
     grid_wait();
     grid_next();
-    const int64_t v = blockIdx.x;
-    for (int i = threadIdx.x * 8; i < D; i += blockDim.x * 8) {
-        if constexpr (kSplit) {
-            float x[8];
-            load8(static_cast<const float *>(w) + v * D, i, D, x);
-            store_planes(out + v * ldw + i, ldw * V, x);
-        } else {
-            *reinterpret_cast<uint4 *>(out + v * ldw + i) =
-                *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w) + v * D + i);
-        }
-    }
+    const int vecs = (D + 7) / 8;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x, v = at / vecs;
+    if (v < V)
+        lay8<kSplit>(w, v, static_cast<int>(at - v * vecs) * 8, D, out, v, ldw, ldw * V);
 }
 
-// One CTA per row of the piece: the row's loss, and with a gradient e -> g, in
-// place in bf16, to planes in fp32.  e stays relative to its own columns'
+// One CTA per row of the piece, or several that share a row's columns where
+// there are few rows: the row's loss, and with a gradient e -> g, in place in
+// bf16, to planes in fp32.  e stays relative to its own columns'
 // maximum until here, as fp16 (2^-11 of e; below 2^-14 of that maximum the
 // error is 2^-25 of it): stored as bf16, g would be rounded to 8 bits twice.
-template <bool kSplit>
+template <bool kSplit, int kRowThreads>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ CeArgs a, uint16_t *__restrict__ g,
                                                            const int32_t *__restrict__ label,
-                                                           float *__restrict__ row_loss)
+                                                           float *__restrict__ row_loss, int parts)
 {
     grid_wait();
     grid_next();
-    const int cnt = ce_piece_rows(a), r = blockIdx.x;
+    const int cnt = ce_piece_rows(a), r = blockIdx.x / parts, part = blockIdx.x % parts;
     if (r >= (cnt + kCeStep - 1) / kCeStep * kCeStep)
         return;
     uint16_t *grow = g + r * a.ldg;
     const int64_t plane = a.ldg * a.rows;
     if (r >= cnt) {
         if (a.keep)
-            for (int v = threadIdx.x * 8; v < a.V; v += kRowThreads * 8)
+            for (int v = (part * kRowThreads + threadIdx.x) * 8; v < a.V; v += parts * kRowThreads * 8)
 #pragma unroll
                 for (int i = 0; i < (kSplit ? 3 : 1); ++i)
                     *reinterpret_cast<uint4 *>(grow + i * plane + v) = make_uint4(0, 0, 0, 0);
         return;
     }
     constexpr int kWarps = kRowThreads / 32;
+    constexpr int kAhead = kSplit ? 2 : 4;  // vectors of 8 values loaded before the first is used
     __shared__ float red[2][kWarps];
+    const int v_step = parts * kRowThreads * 8, v_first = (part * kRowThreads + threadIdx.x) * 8;
+    struct Eight {
+        uint4 v[kSplit ? 2 : 1];
+    } next[kAhead];
+    auto fetch = [&](int v0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int v = v0 + i * v_step;
+            if (v < a.V) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.e) +
+                                                                   (r * a.ldg + v) * (kSplit ? 4 : 2));
+                next[i].v[0] = src[0];
+                if constexpr (kSplit)
+                    next[i].v[1] = src[1];
+            }
+        }
+    };
+    if (a.keep)
+        fetch(v_first);  // on its way while the row's statistics are joined
     const float2 *stats = a.stats + static_cast<int64_t>(r) * a.stat_tiles;
     float C = -INFINITY;
     for (int t = threadIdx.x; t < a.stat_tiles; t += kRowThreads)
@@ -347,33 +382,48 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     for (int w = 0; w < kWarps; ++w)
         S += red[1][w];
     const int y = label[r];
-    if (threadIdx.x == 0)  // ln S + C ln 2 - x_y, with C taken out of x_y before anything is rounded
+    if (part == 0 && threadIdx.x == 0)  // ln S + C ln 2 - x_y, with C taken out of x_y before anything is rounded
         row_loss[a.index[a.base + r]] = (log2f(S) - fmaf(a.target[r], kLog2e, -C)) * kLn2;
     if (!a.keep)
         return;
     const float inv = 1.f / S;
-    for (int v = threadIdx.x * 8; v < a.V; v += kRowThreads * 8) {
-        const float f = exp2f(stats[v / kCeStatCols].x - C) * inv;
-        float x[8];
-        if constexpr (kSplit) {
-            load8(static_cast<const float *>(a.e) + r * a.ldg, v, v + 8, x);
-        } else {
-            const uint4 e = *reinterpret_cast<const uint4 *>(grow + v);
-            const uint32_t w[4] = {e.x, e.y, e.z, e.w};
+    for (int v0 = v_first; v0 < a.V; v0 += kAhead * v_step) {
+        Eight now[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            now[i] = next[i];
+        fetch(v0 + kAhead * v_step);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int v = v0 + i * v_step;
+            if (v >= a.V)
+                break;
+            const float f = exp2f(stats[v / kCeStatCols].x - C) * inv;
+            float x[8];
+            const uint32_t w[4] = {now[i].v[0].x, now[i].v[0].y, now[i].v[0].z, now[i].v[0].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 p = f16x2_values(w[j]);
-                x[2 * j] = p.x, x[2 * j + 1] = p.y;
+                if constexpr (kSplit) {
+                    x[j] = __uint_as_float(w[j]);
+                } else {
+                    const float2 p = f16x2_values(w[j]);
+                    x[2 * j] = p.x, x[2 * j + 1] = p.y;
+                }
             }
-        }
+            if constexpr (kSplit) {
+                const uint4 h = now[i].v[1];
+                x[4] = __uint_as_float(h.x), x[5] = __uint_as_float(h.y), x[6] = __uint_as_float(h.z),
+                x[7] = __uint_as_float(h.w);
+            }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            x[j] = x[j] * f - (v + j == y ? 1.f : 0.f);
-        if constexpr (kSplit)
-            store_planes(grow + v, plane, x);
-        else
-            *reinterpret_cast<uint4 *>(grow + v) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+            for (int j = 0; j < 8; ++j)
+                x[j] = x[j] * f - (v + j == y ? 1.f : 0.f);
+            if constexpr (kSplit)
+                store_planes(grow + v, plane, x);
+            else
+                *reinterpret_cast<uint4 *>(grow + v) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                                  pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        }
     }
 }
 
@@ -391,8 +441,9 @@ Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
     Layout L = {};
     const int64_t T = B * N;
     const bool split = esize == 4;
-    L.rows = static_cast<int>(std::min<int64_t>(split ? kPieceFp32 : kPieceBf16, (T + 63) / 64 * 64));
     L.ldg = (V + 63) / 64 * 64;
+    const int64_t fit = std::max<int64_t>(1024, kPieceBytes / (L.ldg * (split ? 10 : 2)) / kCeTile * kCeTile);
+    L.rows = static_cast<int>(std::min<int64_t>(std::min<int64_t>(fit, 65536), (T + 63) / 64 * 64));
     L.ldh = (D + 63) / 64 * 64;
     L.stat_tiles = (V + kCeStatCols - 1) / kCeStatCols;
     const size_t planes = split ? 3 : 1, kept = static_cast<size_t>(L.rows) * L.ldg;
@@ -457,6 +508,9 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
     a.dw = dweight;
     a.acc = reinterpret_cast<float *>(ws + L.acc);
     a.partial = reinterpret_cast<float *>(ws + L.partial);
+    // Few rows: each goes to several blocks, of at least two vectors a thread.
+    const int parts = static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>(V / (2 * 8 * (V > kLongRow ? 512 : 128)), 4 * num_sms() / std::max<int64_t>(1, rows))));
     int *shards_done = a.n_good + 1;
     labels_kernel<<<1, 1024, 0, s>>>(labels, shifted, good, row_loss, index, a.n_good, shards_done,
                                      static_cast<unsigned>(rows), static_cast<unsigned>(N / P),
@@ -466,22 +520,25 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
         return e;
     const void *w = weight;
     int64_t ldw = D;
+    const int64_t vecs = (D + 7) / 8;
     if (L.lay_weight) {
         w = ws + L.w;
         ldw = L.ldh;
-        e = launch_after(lay_weight_kernel<kSplit>, V, 128, 0, s, weight, D, V,
+        e = launch_after(lay_weight_kernel<kSplit>, (static_cast<int64_t>(V) * vecs + 255) / 256, 256, 0, s, weight, D, V,
                          reinterpret_cast<uint16_t *>(ws + L.w), ldw);
     }
     for (int64_t base = 0; base < rows; base += L.rows) {
         a.base = base;
-        const int64_t blocks = base == 0 ? std::max<int64_t>(rows, L.rows) : L.rows;
+        const int64_t blocks = ((base == 0 ? std::max<int64_t>(rows, L.rows) : L.rows) * vecs + 255) / 256;
         if (e == cudaSuccess)
-            e = launch_after(gather_kernel<kSplit>, blocks, 128, 0, s, a, hidden, shifted, label, ws + L.h, L.ldh,
-                             rows);
+            e = launch_after(gather_kernel<kSplit>, blocks, 256, 0, s, a, hidden, shifted, label,
+                             reinterpret_cast<uint16_t *>(ws + L.h), L.ldh, rows);
         if (e == cudaSuccess)
             e = launch_ce_product(kCeLogits, a, ws + L.h, L.ldh, w, ldw, g, kEsize, s);
         if (e == cudaSuccess)
-            e = launch_after(rows_kernel<kSplit>, L.rows, kRowThreads, 0, s, a, g, label, row_loss);
+            e = launch_after(V > kLongRow ? rows_kernel<kSplit, 512> : rows_kernel<kSplit, 128>,
+                             static_cast<int64_t>(L.rows) * parts, V > kLongRow ? 512 : 128, 0, s, a, g, label, row_loss,
+                             parts);
         if (e == cudaSuccess && dhidden)
             e = launch_ce_product(kCeDh, a, ws + L.h, L.ldh, w, ldw, g, kEsize, s);
         if (e == cudaSuccess && dweight)
@@ -489,6 +546,8 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
         if (e != cudaSuccess)
             return e;
     }
+    if (e != cudaSuccess)
+        return e;
     return launch_after(totals_kernel, P, 1024, 0, s, row_loss, good, rows / P, P, shard_loss, shard_good, total,
                         shards_done);
 }

@@ -163,15 +163,26 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return r;
 }
 
-__device__ __forceinline__ uint4 words(const float *v)
+// 16 bytes of a row: four fp32 values or eight bf16 ones.
+template <bool kF32>
+__device__ __forceinline__ uint4 unit(const float *v)
 {
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    if constexpr (kF32)
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    else
+        return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                          pack_bf16x2(v[6], v[7]));
 }
 
-__device__ __forceinline__ uint4 bf16s(const float *v)
+// The same for exponentials: fp32 or fp16.
+template <bool kF32>
+__device__ __forceinline__ uint4 exp_unit(const float *v)
 {
-    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                      pack_bf16x2(v[6], v[7]));
+    if constexpr (kF32)
+        return unit<true>(v);
+    else
+        return make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]),
+                          pack_f16x2(v[6], v[7]));
 }
 
 // The warp's 32 rows x 64 columns (row = lane) to memory, 128 bytes of a row
@@ -188,8 +199,8 @@ __device__ __forceinline__ void store_rows(const float (&x)[kCols], void *out, i
     for (int part = 0; part < kCols / (8 * kPer); ++part) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const float *v = x + (part * 8 + u) * kPer;
-            *reinterpret_cast<uint4 *>(staging + lane * 128 + ((u ^ (lane & 7)) << 4)) = kF32 ? words(v) : bf16s(v);
+            *reinterpret_cast<uint4 *>(staging + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+                unit<kF32>(x + (part * 8 + u) * kPer);
         }
         __syncwarp();
         const int u = lane & 7, col = col0 + (part * 8 + u) * kPer;
@@ -219,14 +230,9 @@ __device__ __forceinline__ void store_exponentials(const CUtensorMap *te, const 
             bulk_wait_read<0>();  // what was staged before is on its way
         __syncwarp();
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const float *v = x + (part * 8 + u) * kPer;
-            const uint4 val = kSplit ? words(v)
-                                     : make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]),
-                                                  pack_f16x2(v[4 % kPer], v[5 % kPer]),
-                                                  pack_f16x2(v[6 % kPer], v[7 % kPer]));
-            *reinterpret_cast<uint4 *>(staging + lane * 128 + ((u ^ (lane & 7)) << 4)) = val;
-        }
+        for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<uint4 *>(staging + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+                exp_unit<kSplit>(x + (part * 8 + u) * kPer);
         fence_async_smem();
         __syncwarp();
         if (lane == 0 && col0 + part * kBox < limit) {
@@ -542,6 +548,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok)
                 break;
             if (u.run >= 0) {
+                if (kWhat == kCeDh && m - lane >= cnt)
+                    continue;  // nobody reads these rows
                 float4 *slot = tile_slot(a.partial, 2 * pair + u.run, cta, warp, lane);
 #pragma unroll
                 for (int j = 0; j < kCols / 4; ++j)
@@ -568,13 +576,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // Adds the runs of the split tiles, in the order of the contraction.  A warp
-// takes 32 rows x 16 columns, since few tiles are split and each may have
-// dozens of runs; a block is one (tile, CTA half, 32 rows x 64 columns).
-constexpr int kJoinThreads = kCols / 16 * 32;
+// takes 32 rows x 8 columns (fp32: 4), one 16-byte store a row, since few tiles
+// are split and each may have dozens of runs; a block is one (tile, CTA half,
+// 32 rows x 64 columns).
+template <bool kSplit>
+constexpr int kJoinCols = kSplit ? 4 : 8;
 template <int kWhat, bool kSplit>
-__global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const __grid_constant__ CeArgs a, int pairs)
+__global__ void __launch_bounds__(kCols / kJoinCols<kSplit> * 32) ce_join_kernel(const __grid_constant__ CeArgs a,
+                                                                                int pairs)
 {
-    constexpr int kPart = 16;
+    constexpr int kPart = kJoinCols<kSplit>, kVecs = kPart / 4;
     grid_wait();
     grid_next();
     const int cnt = ce_piece_rows(a);
@@ -585,63 +596,63 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const __grid_cons
     const int tile = p.whole + split;
     if (p.workers == 0 || tile >= p.mt * p.nt)
         return;
+    const int part = warp_id(), lane = lane_id();
+    int m0, n0;
+    tile_origin<kWhat>(p, tile, m0, n0);
+    const int m = m0 + cta * kHalf + (slab & 3) * 32 + lane, col = n0 + (slab >> 2) * kCols + part * kPart;
+    const int row = grad_row<kWhat>(a, cnt, m);
+    if (row < 0 || col >= min(n0 + p.cols, a.D))
+        return;
     const int64_t steps = static_cast<int64_t>(p.mt * p.nt - p.whole) * p.kb;
     const int64_t t0 = static_cast<int64_t>(split) * p.kb, t1 = t0 + p.kb;
-    const int part = warp_id(), lane = lane_id();
+    // workers whose runs [steps w / workers, steps (w + 1) / workers) meet the tile
+    int first = static_cast<int>(t0 * p.workers / steps);
+    first = first > 0 ? first - 1 : 0;
+    while (steps * (first + 1) / p.workers <= t0)
+        ++first;
+    int end = static_cast<int>(t1 * p.workers / steps);
+    end = end > 0 ? end - 1 : 0;
+    while (end < p.workers && steps * end / p.workers < t1)
+        ++end;
     float x[kPart];
 #pragma unroll
     for (int j = 0; j < kPart; ++j)
         x[j] = 0.f;
     auto add = [&](const float4 *slot) {
 #pragma unroll
-        for (int j = 0; j < kPart / 4; ++j) {
-            const float4 v = slot[(part * (kPart / 4) + j) * 32];
+        for (int j = 0; j < kVecs; ++j) {
+            const float4 v = slot[(part * kVecs + j) * 32];
             x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
         }
     };
-    // workers whose runs [steps w / workers, steps (w + 1) / workers) meet the tile
-    int first = static_cast<int>(t0 * p.workers / steps);
-    first = first > 0 ? first - 1 : 0;
-    while (steps * (first + 1) / p.workers <= t0)
-        ++first;
-    int end = first;
-    while (end < p.workers && steps * end / p.workers < t1)
-        ++end;
-#pragma unroll 4
-    for (int k = first; k < end; ++k)
-        add(tile_slot(a.partial, 2 * k + (steps * k / p.workers < t0 ? 1 : 0), cta, slab, lane));
-    int m0, n0;
-    tile_origin<kWhat>(p, tile, m0, n0);
-    const int m = m0 + cta * kHalf + (slab & 3) * 32 + lane, col = n0 + (slab >> 2) * kCols + part * kPart;
-    const int row = grad_row<kWhat>(a, cnt, m);
-    bool keep = false;
+    // the tile's first run may be its worker's second
+    add(tile_slot(a.partial, 2 * first + (steps * first / p.workers < t0 ? 1 : 0), cta, slab, lane));
+    const float4 *slots = tile_slot(a.partial, 0, cta, slab, lane);
+#pragma unroll 8
+    for (int k = first + 1; k < end; ++k)
+        add(slots + static_cast<int64_t>(2 * k) * (kCeTileFloats / 4));
     if (kWhat == kCeDw) {
-        float4 *acc = tile_slot(a.acc, tile, cta, slab, lane) + part * (kPart / 4) * 32;
+        float4 *acc = tile_slot(a.acc, tile, cta, slab, lane) + part * kVecs * 32;
         if (a.base > 0)
 #pragma unroll
-            for (int j = 0; j < kPart / 4; ++j) {
+            for (int j = 0; j < kVecs; ++j) {
                 const float4 v = acc[j * 32];
                 x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
             }
-        keep = a.base + a.rows < *a.n_good;
-        if (keep)
+        if (a.base + a.rows < *a.n_good) {
 #pragma unroll
-            for (int j = 0; j < kPart / 4; ++j)
+            for (int j = 0; j < kVecs; ++j)
                 acc[j * 32] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+            return;
+        }
     }
-    if (keep || row < 0)
-        return;
     const float inv = grad_scale(a);
 #pragma unroll
     for (int j = 0; j < kPart; ++j)
         x[j] *= inv;
-    constexpr int kPer = kSplit ? 4 : 8;  // values of 16 bytes
     uint8_t *out = static_cast<uint8_t *>(kWhat == kCeDh ? a.dh : a.dw) +
-                   (static_cast<int64_t>(row) * a.D + col) * (16 / kPer);
-#pragma unroll
-    for (int j = 0; j < kPart; j += kPer)
-        if (col + j < min(n0 + p.cols, a.D))
-            *reinterpret_cast<uint4 *>(out + j * (16 / kPer)) = kSplit ? words(x + j) : bf16s(x + j);
+                   (static_cast<int64_t>(row) * a.D + col) * (kSplit ? 4 : 2);
+    *reinterpret_cast<uint4 *>(out) = unit<kSplit>(x);
 }
 
 // --------------------------------------------------------------- host
@@ -712,7 +723,8 @@ cudaError_t launch(const CeArgs &a, const CUtensorMap &ta, const CUtensorMap &tb
         // never split below this many steps: nothing to join
         const int kb = ((kWhat == kCeDh ? a.V : a.rows) + kCeStep - 1) / kCeStep;
         if (e == cudaSuccess && kb > kSplitGain && pairs > 1)
-            e = launch_after(ce_join_kernel<kWhat, kSplit>, 2 * kEpiWarps * (pairs - 1), kJoinThreads, 0, s, a, pairs);
+            e = launch_after(ce_join_kernel<kWhat, kSplit>, 2 * kEpiWarps * (pairs - 1),
+                             kCols / kJoinCols<kSplit> * 32, 0, s, a, pairs);
     }
     return e;
 }

@@ -277,7 +277,7 @@ struct Cursor {
         const uint32_t sb = m / static_cast<uint32_t>(p.Np), s = sb / static_cast<uint32_t>(p.B);
         k = Token{m, s * p.Np + (m - sb * p.Np), static_cast<int>(sb - s * p.B)};
         r = static_cast<int>(u - m * splits) * p.runs_per_split;
-        end = min((rows(p) + S::kRun - 1) / S::kRun, r + p.runs_per_split);
+        end = min(p.runs, r + p.runs_per_split);
     }
     // to the next run
     __device__ __forceinline__ void step(const NormRopeParams &p)
@@ -655,6 +655,7 @@ cudaError_t run(NormRopeParams &p, bool bwd, cudaStream_t s)
 {
     const int kRun = (bwd ? kBwdRun : kFwdRun) / static_cast<int>(kD * sizeof(T));
     const int runs = (p.Hq + (p.v ? 2 : 1) * p.Hkv + kRun - 1) / kRun;
+    p.runs = runs;
     const int64_t resident = static_cast<int64_t>(num_sms()) * (bwd ? kBwdBlocks : kFwdBlocks);
     // few tokens: a token's runs go to several warps
     const int splits = static_cast<int>(std::min<int64_t>(runs, (resident * kWarps + p.tokens - 1) / p.tokens));

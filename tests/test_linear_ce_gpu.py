@@ -185,14 +185,15 @@ def test_large_logits_and_certain_rows(uly, dtype):
     compare(outs, grads, h, w, labels, "large logits, wrong labels", norm=False)
 
 
-@pytest.mark.parametrize("rows,dtype", [(8192, BF16), (8193, BF16), (8194, BF16), (20000, BF16), (9000, FP32)])
+@pytest.mark.parametrize("rows,dtype", [(8192, BF16), (8193, BF16), (8194, BF16), (20000, BF16), (9000, FP32),
+                                        (65537, BF16), (65538, BF16), (140000, BF16), (70000, FP32)])
 def test_pieces(uly, rows, dtype):
     """More rows with labels than one piece holds; the last row of a sequence has none."""
     h, w, labels = make(1, 1, rows, 24, 70, dtype, ignore=0.0, seed=rows)
     outs, grads = run(uly, h, w, labels)
     compare(outs, grads, h, w, labels, f"{rows} rows")
     # enough rows for three pieces, labels for one
-    if rows == 20000:
+    if rows >= 20000:
         labels[:, :, 2000:] = -100
         outs, grads = run(uly, h, w, labels)
         compare(outs, grads, h, w, labels, "one piece of three")
