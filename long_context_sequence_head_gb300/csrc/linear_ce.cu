@@ -494,6 +494,11 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
     CeArgs a = {};
     a.n_good = reinterpret_cast<int *>(ws + L.n_good);
     a.rows = L.rows;
+    // few tiles: narrower ones, so that more SMs have some
+    a.logit_cols = kCeTile;
+    const int64_t row_tiles = (L.rows + kCeTile - 1) / kCeTile;
+    while (a.logit_cols > kCeStatCols && row_tiles * ((V + a.logit_cols - 1) / a.logit_cols) <= num_sms() / 4)
+        a.logit_cols /= 2;
     a.D = D;
     a.V = V;
     a.ldg = L.ldg;

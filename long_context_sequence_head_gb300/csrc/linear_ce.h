@@ -28,6 +28,7 @@ struct CeArgs {
     int *n_good;            // good rows of the whole call (device)
     int64_t base;           // first good row of the piece
     int rows;               // rows a piece may have
+    int logit_cols;         // columns of a tile of logits: 256, 128 or 64
     int D, V;
     int64_t ldg;            // row pitch of e and g, elements
     void *e;                // [rows][ldg]: fp16 (bf16 inputs) or fp32 exponentials

@@ -86,10 +86,15 @@ __device__ __forceinline__ Plan make_plan(const CeArgs &a, int cnt, int pairs)
     const int M = kWhat == kCeDw ? a.V : cnt, N = kWhat == kCeLogits ? a.V : a.D;
     const int K = kWhat == kCeLogits ? a.D : (kWhat == kCeDh ? a.V : cnt);
     p.mt = (M + kCeTile - 1) / kCeTile;
-    p.nt = (N + kCeTile - 1) / kCeTile;
     p.kb = (K + kCeStep - 1) / kCeStep;
-    // D in equal tiles: 776 as four of 224 instead of three of 256 and one of 8
-    p.cols = kWhat == kCeLogits ? kCeTile : ((N + p.nt - 1) / p.nt + 31) / 32 * 32;
+    if (kWhat == kCeLogits) {
+        p.cols = a.logit_cols;
+        p.nt = (N + p.cols - 1) / p.cols;
+    } else {
+        // D in equal tiles: 776 as four of 224 instead of three of 256 and one of 8
+        p.nt = (N + kCeTile - 1) / kCeTile;
+        p.cols = ((N + p.nt - 1) / p.nt + 31) / 32 * 32;
+    }
     p.workers = 0;
     p.whole = p.mt * p.nt;
     if (kWhat != kCeLogits)  // a softmax needs whole sums
@@ -139,7 +144,7 @@ template <int kWhat>
 __device__ __forceinline__ void tile_origin(const Plan &p, int tile, int &m0, int &n0)
 {
     if (kWhat == kCeLogits) {
-        n0 = tile / p.mt * kCeTile;
+        n0 = tile / p.mt * p.cols;
         m0 = tile % p.mt * kCeTile;
     } else {
         m0 = tile / p.nt * kCeTile;
@@ -383,6 +388,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (cnt == 0 && (kWhat != kCeDw || a.base > 0))
         plan.whole = plan.workers = 0;  // nothing to do; dW without any row is written as zeros by the first piece
     constexpr int kPerStep = kSplit ? kPlanePairs : 1;
+    // bytes of B a CTA loads in a step: its half of the columns (MN-major: in blocks of 64)
+    const bool second_block = plan.cols / 2 > 64;
+    const uint32_t b_bytes = kWhat == kCeLogits ? plan.cols / 2 * (kCeStep * 2)
+                                                : (second_block ? kOperandBytes : kOperandBytes / 2);
 
     if (warp == kEpiWarps) {
         // ------------------------------------------------ loads
@@ -408,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             break;
                         }
                         if (cta == 0)
-                            mbar_expect_tx(&full[s], 2 * kStageBytes);
+                            mbar_expect_tx(&full[s], 2 * (kOperandBytes + b_bytes));
                         const uint32_t bar = cluster_addr(&full[s], 0);
                         uint8_t *sa = smem + s * kStageBytes, *sb = sa + kOperandBytes;
                         const int kc = k * kCeStep;
@@ -420,7 +429,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                         if (kWhat != kCeLogits) {
                             tma_load_3d_pair(sb, &tb, bar, n0, kc, pb);
-                            tma_load_3d_pair(sb + kOperandBytes / 2, &tb, bar, n0 + 64, kc, pb);
+                            if (second_block)
+                                tma_load_3d_pair(sb + kOperandBytes / 2, &tb, bar, n0 + 64, kc, pb);
                         } else {
                             tma_load_3d_pair(sb, &tb, bar, kc, n0, pb);
                         }
@@ -555,7 +565,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < kCols / 4; ++j)
                     slot[j * 32] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
             } else if constexpr (kWhat == kCeLogits) {
-                finish_logits<kSplit>(a, &te, x, cnt, m, n0 + col, stage, lane);
+                if (col < plan.cols)
+                    finish_logits<kSplit>(a, &te, x, cnt, m, n0 + col, stage, lane);
             } else {
                 finish_grad<kWhat, kSplit>(a, x, cnt, u.tile, m, n0 + col, cta, warp, n0 + plan.cols, stage, lane);
             }
@@ -575,84 +586,111 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_dealloc_pair(tbase, 512);
 }
 
-// Adds the runs of the split tiles, in the order of the contraction.  A warp
-// takes 32 rows x 8 columns (fp32: 4), one 16-byte store a row, since few tiles
-// are split and each may have dozens of runs; a block is one (tile, CTA half,
-// 32 rows x 64 columns).
+// Adds the runs of the split tiles, in the order of the contraction.  An item
+// is 32 rows x 64 columns of one tile: a warp takes 8 columns (fp32: 4; one
+// 16-byte store a row) of one of kGroups shares of the runs, and the shares'
+// sums are added in order.  Where a few tiles are split, each into dozens of
+// runs, the block's full size of 1024 threads is shared out; where dozens are,
+// each has two or three runs and one group will do.
 template <bool kSplit>
 constexpr int kJoinCols = kSplit ? 4 : 8;
-template <int kWhat, bool kSplit>
-__global__ void __launch_bounds__(kCols / kJoinCols<kSplit> * 32) ce_join_kernel(const __grid_constant__ CeArgs a,
-                                                                                int pairs)
+template <bool kSplit>
+constexpr int kJoinGroups = kSplit ? 2 : 4;
+template <bool kSplit, int kGroups>
+constexpr int kJoinThreads = kGroups * (kCols / kJoinCols<kSplit>) * 32;
+template <int kWhat, bool kSplit, int kGroups>
+__global__ void __launch_bounds__(kJoinThreads<kSplit, kGroups>) ce_join_kernel(const __grid_constant__ CeArgs a,
+                                                                               int pairs)
 {
-    constexpr int kPart = kJoinCols<kSplit>, kVecs = kPart / 4;
+    constexpr int kPart = kJoinCols<kSplit>, kVecs = kPart / 4, kParts = kCols / kPart;
+    static_assert(kJoinThreads<kSplit, kGroups> <= 1024, "a block");
+    __shared__ float sums[kGroups > 1 ? kGroups - 1 : 1][kParts][kPart][32];
     grid_wait();
     grid_next();
     const int cnt = ce_piece_rows(a);
     if (cnt == 0)
         return;
     const Plan p = make_plan<kWhat>(a, cnt, pairs);
-    const int slab = blockIdx.x % kEpiWarps, cta = blockIdx.x / kEpiWarps % 2, split = blockIdx.x / (2 * kEpiWarps);
-    const int tile = p.whole + split;
-    if (p.workers == 0 || tile >= p.mt * p.nt)
+    if (p.workers == 0)
         return;
-    const int part = warp_id(), lane = lane_id();
-    int m0, n0;
-    tile_origin<kWhat>(p, tile, m0, n0);
-    const int m = m0 + cta * kHalf + (slab & 3) * 32 + lane, col = n0 + (slab >> 2) * kCols + part * kPart;
-    const int row = grad_row<kWhat>(a, cnt, m);
-    if (row < 0 || col >= min(n0 + p.cols, a.D))
-        return;
-    const int64_t steps = static_cast<int64_t>(p.mt * p.nt - p.whole) * p.kb;
-    const int64_t t0 = static_cast<int64_t>(split) * p.kb, t1 = t0 + p.kb;
-    // workers whose runs [steps w / workers, steps (w + 1) / workers) meet the tile
-    int first = static_cast<int>(t0 * p.workers / steps);
-    first = first > 0 ? first - 1 : 0;
-    while (steps * (first + 1) / p.workers <= t0)
-        ++first;
-    int end = static_cast<int>(t1 * p.workers / steps);
-    end = end > 0 ? end - 1 : 0;
-    while (end < p.workers && steps * end / p.workers < t1)
-        ++end;
-    float x[kPart];
+    const int part = warp_id() % kParts, group = warp_id() / kParts, lane = lane_id();
+    const int rem = p.mt * p.nt - p.whole;
+    const int64_t steps = static_cast<int64_t>(rem) * p.kb;
+    for (int item = blockIdx.x; item < rem * 2 * kEpiWarps; item += gridDim.x) {
+        const int slab = item % kEpiWarps, cta = item / kEpiWarps % 2, split = item / (2 * kEpiWarps);
+        const int tile = p.whole + split;
+        int m0, n0;
+        tile_origin<kWhat>(p, tile, m0, n0);
+        const int m_slab = m0 + cta * kHalf + (slab & 3) * 32, col = n0 + (slab >> 2) * kCols + part * kPart;
+        const int limit = min(n0 + p.cols, a.D);
+        if (m_slab >= (kWhat == kCeDh ? cnt : a.V) || n0 + (slab >> 2) * kCols >= limit)
+            continue;  // the whole block agrees
+        const int64_t t0 = static_cast<int64_t>(split) * p.kb, t1 = t0 + p.kb;
+        // workers whose runs [steps w / workers, steps (w + 1) / workers) meet the tile
+        int first = static_cast<int>(t0 * p.workers / steps);
+        first = first > 0 ? first - 1 : 0;
+        while (steps * (first + 1) / p.workers <= t0)
+            ++first;
+        int end = static_cast<int>(t1 * p.workers / steps);
+        end = end > 0 ? end - 1 : 0;
+        while (end < p.workers && steps * end / p.workers < t1)
+            ++end;
+        float x[kPart];
 #pragma unroll
-    for (int j = 0; j < kPart; ++j)
-        x[j] = 0.f;
-    auto add = [&](const float4 *slot) {
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            const float4 v = slot[(part * kVecs + j) * 32];
-            x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
-        }
-    };
-    // the tile's first run may be its worker's second
-    add(tile_slot(a.partial, 2 * first + (steps * first / p.workers < t0 ? 1 : 0), cta, slab, lane));
-    const float4 *slots = tile_slot(a.partial, 0, cta, slab, lane);
-#pragma unroll 8
-    for (int k = first + 1; k < end; ++k)
-        add(slots + static_cast<int64_t>(2 * k) * (kCeTileFloats / 4));
-    if (kWhat == kCeDw) {
-        float4 *acc = tile_slot(a.acc, tile, cta, slab, lane) + part * kVecs * 32;
-        if (a.base > 0)
+        for (int j = 0; j < kPart; ++j)
+            x[j] = 0.f;
+        const int each = (end - first + kGroups - 1) / kGroups, k0 = first + group * each,
+                  k1 = min(end, k0 + each);
+#pragma unroll 4
+        for (int k = k0; k < k1; ++k) {
+            // the tile's first run may be its worker's second
+            const int run = k == first && steps * first / p.workers < t0 ? 1 : 0;
+            const float4 *slot = tile_slot(a.partial, 2 * k + run, cta, slab, lane);
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
-                const float4 v = acc[j * 32];
+                const float4 v = slot[(part * kVecs + j) * 32];
                 x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
             }
-        if (a.base + a.rows < *a.n_good) {
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j)
-                acc[j * 32] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-            return;
         }
-    }
-    const float inv = grad_scale(a);
+        if constexpr (kGroups > 1) {
+            __syncthreads();  // the last item's sums are read
+            if (group > 0)
 #pragma unroll
-    for (int j = 0; j < kPart; ++j)
-        x[j] *= inv;
-    uint8_t *out = static_cast<uint8_t *>(kWhat == kCeDh ? a.dh : a.dw) +
-                   (static_cast<int64_t>(row) * a.D + col) * (kSplit ? 4 : 2);
-    *reinterpret_cast<uint4 *>(out) = unit<kSplit>(x);
+                for (int j = 0; j < kPart; ++j)
+                    sums[group - 1][part][j][lane] = x[j];
+            __syncthreads();
+            if (group > 0)
+                continue;
+        }
+#pragma unroll
+        for (int g = 0; g < kGroups - 1; ++g)
+#pragma unroll
+            for (int j = 0; j < kPart; ++j)
+                x[j] += sums[g][part][j][lane];
+        if (kWhat == kCeDw) {
+            float4 *acc = tile_slot(a.acc, tile, cta, slab, lane) + part * kVecs * 32;
+            if (a.base > 0)
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) {
+                    const float4 v = acc[j * 32];
+                    x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
+                }
+            if (a.base + a.rows < *a.n_good) {
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j)
+                    acc[j * 32] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+                continue;
+            }
+        }
+        const int row = grad_row<kWhat>(a, cnt, m_slab + lane);
+        const float inv = grad_scale(a);
+#pragma unroll
+        for (int j = 0; j < kPart; ++j)
+            x[j] *= inv;
+        if (row >= 0 && col < limit)
+            *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(kWhat == kCeDh ? a.dh : a.dw) +
+                                       (static_cast<int64_t>(row) * a.D + col) * (kSplit ? 4 : 2)) = unit<kSplit>(x);
+    }
 }
 
 // --------------------------------------------------------------- host
@@ -720,11 +758,23 @@ cudaError_t launch(const CeArgs &a, const CUtensorMap &ta, const CUtensorMap &tb
     }
     e = launch_after(kernel, 2 * pairs, kThreads, kSmem, s, ta, tb, te, a, wait_cfg());
     if constexpr (kWhat != kCeLogits) {
-        // never split below this many steps: nothing to join
-        const int kb = ((kWhat == kCeDh ? a.V : a.rows) + kCeStep - 1) / kCeStep;
-        if (e == cudaSuccess && kb > kSplitGain && pairs > 1)
-            e = launch_after(ce_join_kernel<kWhat, kSplit>, 2 * kEpiWarps * (pairs - 1),
-                             kCols / kJoinCols<kSplit> * 32, 0, s, a, pairs);
+        // Nothing to join if no number of good rows could make the product split
+        // (dh: any number of row tiles up to the most; dW: any contraction).
+        const int M = kWhat == kCeDh ? a.rows : a.V, K = kWhat == kCeDh ? a.V : a.rows;
+        const int mt = (M + kCeTile - 1) / kCeTile, nt = (a.D + kCeTile - 1) / kCeTile, kb = (K + kCeStep - 1) / kCeStep;
+        int whole, most = 0;
+        if (kb > kSplitGain) {
+            most = std::min(mt * nt, pairs - 1);
+            if (kWhat == kCeDw && ce_workers(static_cast<int64_t>(mt) * nt, kb, pairs, whole) == 0)
+                most = 0;  // fewer rows split even less
+        }
+        const int items = most * 2 * kEpiWarps;
+        constexpr int kMany = kJoinGroups<kSplit>;
+        if (e == cudaSuccess && items > 0)
+            e = items <= 2 * num_sms()
+                    ? launch_after(ce_join_kernel<kWhat, kSplit, kMany>, items, kJoinThreads<kSplit, kMany>, 0, s, a, pairs)
+                    : launch_after(ce_join_kernel<kWhat, kSplit, 1>, std::min(items, 8 * num_sms()),
+                                   kJoinThreads<kSplit, 1>, 0, s, a, pairs);
     }
     return e;
 }
@@ -738,7 +788,8 @@ cudaError_t product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh,
     bool ok;
     switch (what) {
     case kCeLogits:
-        ok = make_map(&ta, h, a.D, a.rows, ldh, planes, kHalf) && make_map(&tb, w, a.D, a.V, ldw, planes, kHalf);
+        ok = make_map(&ta, h, a.D, a.rows, ldh, planes, kHalf) &&
+             make_map(&tb, w, a.D, a.V, ldw, planes, a.logit_cols / 2);
         ok = ok && (!a.keep || make_exp_map(&te, a, kSplit));
         return ok ? launch<kCeLogits, kSplit>(a, ta, tb, te, s) : cudaErrorInvalidValue;
     case kCeDh:
