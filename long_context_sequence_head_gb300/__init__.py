@@ -398,8 +398,6 @@ def _norm_rope_args(P, like, far, weights, to_head, positions):
     like: (name, tensor or None, heads) in the sequence layout, Q's first; far:
     the same on the other side; returns (B, Np, d)."""
     q = like[0][1]
-    if q.dim() != 5:
-        raise ValueError(f"{like[0][0]} must be 5-D [P][B][N/P][H][d], got {tuple(q.shape)}")
     Ps, B, Np, _, d = q.shape
     if Ps != P:
         raise ValueError(f"the leading dimension of {like[0][0]} must be P={P}, got {Ps}")
@@ -438,6 +436,12 @@ def _norm_rope_args(P, like, far, weights, to_head, positions):
     for t in whole:
         place(t, True)
     return B, Np, d
+
+
+def _five(**tensors):
+    for name, t in tensors.items():
+        if t is None or t.dim() != 5:
+            raise ValueError(f"{name} must be 5-D [P][B][N/P][H][d], got {None if t is None else tuple(t.shape)}")
 
 
 def _on(first, t):
@@ -511,7 +515,8 @@ def ulysses_qkv_norm_rope_fwd(q_seq, k_seq, v_seq, q_out, k_out, v_out, P: int, 
     [P][B][N/P], or [axes][P][B][N/P] with axis_of_freq naming each
     frequency's axis (None: the token's index).  q_weight and k_weight [d], or
     None for both: no norm."""
-    Hq, Hkv = q_seq.shape[-2], k_seq.shape[-2]
+    _five(q_seq=q_seq, k_seq=k_seq)
+    Hq, Hkv = q_seq.shape[3], k_seq.shape[3]
     if (v_seq is None) != (v_out is None) or (q_weight is None) != (k_weight is None):
         raise ValueError("v_seq and v_out, and q_weight and k_weight, go together")
     if q_out is None or k_out is None:
@@ -545,7 +550,10 @@ def ulysses_qkv_norm_rope_bwd(q_seq, k_seq, dq_out, dk_out, dv_out, dq_seq, dk_s
         raise ValueError("the norm's backward needs q_seq and k_seq")
     if not norm and (dq_weight is not None or dk_weight is not None):
         raise ValueError("without norm weights there are no weight gradients")
-    Hq, Hkv = dq_seq.shape[-2], dk_seq.shape[-2]
+    _five(dq_seq=dq_seq, dk_seq=dk_seq)
+    if dq_out is None or dk_out is None:
+        raise ValueError("dq_out and dk_out are required")
+    Hq, Hkv = dq_seq.shape[3], dk_seq.shape[3]
     if not norm:
         q_seq = k_seq = None
     B, Np, d = _norm_rope_args(P, (("dq_seq", dq_seq, Hq), ("dk_seq", dk_seq, Hkv), ("dv_seq", dv_seq, Hkv),

@@ -278,7 +278,9 @@ __device__ __forceinline__ void finish_logits(const CeArgs &a, const CUtensorMap
         pm[j & 7] = fmaxf(pm[j & 7], x[j]);
     const float c = kLog2e * fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
                                    fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
-    const float2 l2 = make_float2(kLog2e, kLog2e), c2 = make_float2(-c, -c);
+    // a row of -inf alone has no maximum to take out: its exponentials are 0
+    const float out = c == -INFINITY ? 0.f : -c;
+    const float2 l2 = make_float2(kLog2e, kLog2e), c2 = make_float2(out, out);
     float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
     for (int j = 0; j < kCols; j += 2) {

@@ -255,3 +255,79 @@ def _random_cases(n, seed=77):
 @pytest.mark.parametrize("P,B,N,D,V,dtype", _random_cases(10))
 def test_random_shapes(uly, P, B, N, D, V, dtype):
     test_loss_and_gradients(uly, P, B, N, D, V, dtype)
+
+
+def test_two_calls_at_once(uly):
+    """Two calls with workspaces of their own on two streams, attention on a third."""
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    cases = []
+    for seed in (1, 2):
+        h, w, labels = (t.cuda() for t in make(2, 1, 1500, 264, 3001, BF16, seed=seed))
+        dh, dw = torch.empty_like(h), torch.empty_like(w)
+        total = uly.ulysses_sharded_linear_ce_loss(h, w, labels, 2, dhidden=dh, dweight=dw)[2]
+        cases.append((h, w, labels, [total.clone(), dh.clone(), dw.clone()]))
+    q = torch.randn(2, 1, 1024, 8, 128, device="cuda").to(BF16)
+    k = torch.randn(2, 1, 1024, 2, 128, device="cuda").to(BF16)
+    o, lse = torch.empty_like(q), torch.empty(2, 1, 8, 1024, device="cuda")
+    for _ in range(5):
+        torch.cuda.synchronize()
+        got = []
+        for (h, w, labels, _), s in zip(cases, streams):
+            dh, dw = torch.zeros_like(h), torch.zeros_like(w)
+            s.wait_stream(torch.cuda.current_stream())
+            total = uly.ulysses_sharded_linear_ce_loss(h, w, labels, 2, dhidden=dh, dweight=dw, stream=s)[2]
+            got.append([total, dh, dw])
+        uly.ulysses_attn_fwd(q, k, k, o, lse, stream=streams[2])
+        torch.cuda.synchronize()
+        assert uly.ulysses_get_device_status()[0] == 0
+        for (_, _, _, want), g in zip(cases, got):
+            assert all(bytes_equal(a, b) for a, b in zip(want, g))
+
+
+def test_first_call_of_a_process_captured():
+    """Nothing has to run before a capture: the kernels are set up on the host."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, numpy as np, long_context_sequence_head_gb300 as uly
+h, w = (torch.randn(*s, device="cuda").bfloat16() for s in ((2, 1, 100, 136), (500, 136)))
+y = torch.randint(0, 500, (2, 1, 100), device="cuda")
+grads = dict(dhidden=torch.empty_like(h), dweight=torch.empty_like(w))
+ws = torch.empty(uly.ulysses_sharded_linear_ce_workspace_size(1, 200, 136, 500, 2, True, torch.bfloat16),
+                 dtype=torch.uint8, device="cuda")
+out = tuple(torch.empty(n, dtype=t, device="cuda") for n, t in ((2, torch.float32), (2, torch.int64), (1, torch.float32)))
+x = [torch.randn(1, 1, 8, 4, 128, device="cuda").bfloat16() for _ in range(3)]
+o = [torch.empty_like(t) for t in x]
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    uly.ulysses_sharded_linear_ce_loss(h, w, y, 2, **grads, workspace=ws, outputs=out)
+    uly.ulysses_qkv_norm_rope_fwd(*x, *o, 1, inv_freq=np.ones(64))
+g.replay()
+torch.cuda.synchronize()
+total = uly.ulysses_sharded_linear_ce_loss(h, w, y, 2)[2]
+assert torch.equal(total, out[2]) and uly.ulysses_get_device_status()[0] == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
+
+
+def test_the_longest_vocabulary(uly):
+    """2^21 words, targets among the last; against fp64 on the GPU (tolerances as the bf16 norm bound)."""
+    V, D = 1 << 21, 16
+    g = torch.Generator(device="cuda").manual_seed(0)
+    h = torch.randn(1, 1, 40, D, device="cuda", generator=g).to(BF16)
+    w = (torch.randn(V, D, device="cuda", generator=g) / 4).to(BF16)
+    y = torch.randint(V - 10, V, (1, 1, 40), device="cuda", generator=g)
+    dh, dw = torch.empty_like(h), torch.empty_like(w)
+    total = uly.ulysses_sharded_linear_ce_loss(h, w, y, 1, dhidden=dh, dweight=dw)[2]
+    rows, t = h[0, 0, :-1].double(), y[0, 0, 1:]
+    x = rows @ w.double().T
+    want = (x.logsumexp(1) - x[torch.arange(39), t]).mean()
+    p = x.softmax(1)
+    p[torch.arange(39), t] -= 1
+    p /= 39
+    assert abs(float(total) - float(want)) <= 1e-5 * float(want)
+    assert rel_fro(dh[0, 0, :-1], (p @ w.double()).cpu()) <= REL_TOL["bf16"]
+    assert rel_fro(dw, (p.T @ rows).cpu()) <= REL_TOL["bf16"]

@@ -304,3 +304,22 @@ def test_captured_and_on_another_stream(uly):
     graph.replay()
     torch.cuda.synchronize()
     assert all(bytes_equal(a, b) for a, b in zip(y + want + wantw, y2 + dx2 + dw2))
+
+
+def test_offsets_past_32_bits(uly):
+    """2^20 tokens of 24 heads, 3.2e9 values: the last tokens as a call of their own on them gives."""
+    n, inv = 1 << 20, 1e6 ** (-np.arange(64) / 64)
+    x = torch.empty(1, 1, n, 24, 128, device="cuda", dtype=BF16).normal_()
+    parts = x.split([16, 4, 4], dim=3)
+    y = [torch.empty(1, 1, n, h, 128, device="cuda", dtype=BF16) for h in (16, 4, 4)]
+    uly.ulysses_qkv_norm_rope_fwd(*parts, *y, 1, inv_freq=inv)
+    tail = [t[:, :, -5:].contiguous() for t in parts]
+    want = [torch.empty_like(t) for t in tail]
+    at = torch.arange(n - 5, n, device="cuda").view(1, 1, 5)
+    uly.ulysses_qkv_norm_rope_fwd(*tail, *want, 1, inv_freq=inv, positions=at)
+    assert all(bytes_equal(a[:, :, -5:], b) for a, b in zip(y, want))
+    dx = torch.empty_like(x)
+    uly.ulysses_qkv_norm_rope_bwd(None, None, *y, *dx.split([16, 4, 4], dim=3), 1, inv_freq=inv)
+    back = [torch.empty_like(t) for t in tail]
+    uly.ulysses_qkv_norm_rope_bwd(None, None, *want, *back, 1, inv_freq=inv, positions=at)
+    assert all(bytes_equal(a[:, :, -5:], b) for a, b in zip(dx.split([16, 4, 4], dim=3), back))
