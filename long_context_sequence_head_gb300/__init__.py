@@ -382,9 +382,9 @@ def _token_stride(name, t, d) -> int:
     """Elements from one token to the next of a [P][B][N/P][H][d] tensor whose
     heads are contiguous and whose tokens are evenly spaced, as a slice of
     heads of a packed [P][B][N/P][Hq+2Hkv][d] projection output is."""
-    P, B, Np, H, dd = t.shape
     if t.is_contiguous():
-        return H * d
+        return t.shape[3] * d
+    P, B, Np, H, dd = t.shape
     sP, sB, sT, sH, sd = t.stride()
     ok = dd == d and sd == 1 and (H == 1 or sH == d)
     step = sT if Np > 1 else (sB if B > 1 else (sP if P > 1 else H * d))
@@ -438,6 +438,16 @@ def _norm_rope_args(P, like, far, weights, to_head, positions):
     return B, Np, d
 
 
+def _is(t, shape, dtype, device):
+    """A contiguous tensor of this shape and type on this device, or None."""
+    return t is None or (t.shape == shape and t.dtype is dtype and t.get_device() == device and t.is_contiguous())
+
+
+def _view(t, shape, dtype, device):
+    """The same, contiguous or not."""
+    return t is None or (t.shape == shape and t.dtype is dtype and t.get_device() == device)
+
+
 def _five(**tensors):
     for name, t in tensors.items():
         if t is None or t.dim() != 5:
@@ -465,7 +475,7 @@ class _Launch:
         if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device != device:
             raise ValueError(f"the stream must belong to {device}")
         self.device, self.stream = device, stream
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        self.guard = None if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
     def __enter__(self):
         if self.guard is not None:
@@ -515,22 +525,33 @@ def ulysses_qkv_norm_rope_fwd(q_seq, k_seq, v_seq, q_out, k_out, v_out, P: int, 
     [P][B][N/P], or [axes][P][B][N/P] with axis_of_freq naming each
     frequency's axis (None: the token's index).  q_weight and k_weight [d], or
     None for both: no norm."""
-    _five(q_seq=q_seq, k_seq=k_seq)
-    Hq, Hkv = q_seq.shape[3], k_seq.shape[3]
     if (v_seq is None) != (v_out is None) or (q_weight is None) != (k_weight is None):
         raise ValueError("v_seq and v_out, and q_weight and k_weight, go together")
+    _five(q_seq=q_seq, k_seq=k_seq)
     if q_out is None or k_out is None:
         raise ValueError("q_out and k_out are required")
-    B, Np, d = _norm_rope_args(P, (("q_seq", q_seq, Hq), ("k_seq", k_seq, Hkv), ("v_seq", v_seq, Hkv)),
-                               (("q_out", q_out, Hq), ("k_out", k_out, Hkv), ("v_out", v_out, Hkv)),
-                               (("q_weight", q_weight), ("k_weight", k_weight)), to_head, positions)
+    Ps, B, Np, Hq, d = q_seq.shape
+    near_k, w = k_seq.shape, (d,)
+    Hkv = near_k[3]
+    far_q, far_k = (((P, B, Np * P, Hq // P, d), (P, B, Np * P, Hkv // P, d)) if to_head and P > 0
+                    else (q_seq.shape, near_k))
+    dtype, device = q_seq.dtype, q_seq.get_device()
+    if not (device >= 0 and Ps == P and near_k == (P, B, Np, Hkv, d) and Hq % P == 0 and Hkv % P == 0
+            and _view(k_seq, near_k, dtype, device) and _view(v_seq, near_k, dtype, device)
+            and _is(q_out, far_q, dtype, device) and _is(k_out, far_k, dtype, device) and _is(v_out, far_k, dtype, device)
+            and _is(q_weight, w, dtype, device) and _is(k_weight, w, dtype, device)
+            and (positions is None or (positions.get_device() == device and positions.is_contiguous()))):
+        # says what is wrong, or that nothing is (heads need not be a multiple of P in the sequence layout)
+        _norm_rope_args(P, (("q_seq", q_seq, Hq), ("k_seq", k_seq, Hkv), ("v_seq", v_seq, Hkv)),
+                        (("q_out", q_out, Hq), ("k_out", k_out, Hkv), ("v_out", v_out, Hkv)),
+                        (("q_weight", q_weight), ("k_weight", k_weight)), to_head, positions)
     desc, _keep = _rope_desc(inv_freq, positions, axis_of_freq, interleaved, (P, B, Np))
     with _Launch(q_seq.device, stream) as at:
         _check("ulysses_qkv_norm_rope_fwd", load().ulysses_qkv_norm_rope_fwd(
             q_seq.data_ptr(), k_seq.data_ptr(), _ptr(v_seq), _ptr(q_weight), _ptr(k_weight), q_out.data_ptr(),
             k_out.data_ptr(), _ptr(v_out), B, Np * P, Hq, Hkv, d, P, _token_stride("q_seq", q_seq, d),
             _token_stride("k_seq", k_seq, d), 0 if v_seq is None else _token_stride("v_seq", v_seq, d),
-            ctypes.addressof(desc), float(eps), int(bool(to_head)), _dt(q_seq), at.raw()))
+            ctypes.addressof(desc), eps, 1 if to_head else 0, _dt(q_seq), at.raw()))
     return q_out, k_out, v_out
 
 
@@ -553,14 +574,27 @@ def ulysses_qkv_norm_rope_bwd(q_seq, k_seq, dq_out, dk_out, dv_out, dq_seq, dk_s
     _five(dq_seq=dq_seq, dk_seq=dk_seq)
     if dq_out is None or dk_out is None:
         raise ValueError("dq_out and dk_out are required")
-    Hq, Hkv = dq_seq.shape[3], dk_seq.shape[3]
     if not norm:
         q_seq = k_seq = None
-    B, Np, d = _norm_rope_args(P, (("dq_seq", dq_seq, Hq), ("dk_seq", dk_seq, Hkv), ("dv_seq", dv_seq, Hkv),
-                                   ("q_seq", q_seq, Hq), ("k_seq", k_seq, Hkv)),
-                               (("dq_out", dq_out, Hq), ("dk_out", dk_out, Hkv), ("dv_out", dv_out, Hkv)),
-                               (("q_weight", q_weight), ("k_weight", k_weight), ("dq_weight", dq_weight),
-                                ("dk_weight", dk_weight)), to_head, positions)
+    Ps, B, Np, Hq, d = dq_seq.shape
+    near_q, near_k, w = dq_seq.shape, dk_seq.shape, (d,)
+    Hkv = near_k[3]
+    far_q, far_k = (((P, B, Np * P, Hq // P, d), (P, B, Np * P, Hkv // P, d)) if to_head and P > 0
+                    else (near_q, near_k))
+    dtype, device = dq_seq.dtype, dq_seq.get_device()
+    if not (device >= 0 and Ps == P and near_k == (P, B, Np, Hkv, d) and Hq % P == 0 and Hkv % P == 0
+            and _view(dk_seq, near_k, dtype, device) and _view(dv_seq, near_k, dtype, device)
+            and _view(q_seq, near_q, dtype, device) and _view(k_seq, near_k, dtype, device)
+            and _is(dq_out, far_q, dtype, device) and _is(dk_out, far_k, dtype, device)
+            and _is(dv_out, far_k, dtype, device) and _is(q_weight, w, dtype, device)
+            and _is(k_weight, w, dtype, device) and _is(dq_weight, w, dtype, device)
+            and _is(dk_weight, w, dtype, device)
+            and (positions is None or (positions.get_device() == device and positions.is_contiguous()))):
+        _norm_rope_args(P, (("dq_seq", dq_seq, Hq), ("dk_seq", dk_seq, Hkv), ("dv_seq", dv_seq, Hkv),
+                            ("q_seq", q_seq, Hq), ("k_seq", k_seq, Hkv)),
+                        (("dq_out", dq_out, Hq), ("dk_out", dk_out, Hkv), ("dv_out", dv_out, Hkv)),
+                        (("q_weight", q_weight), ("k_weight", k_weight), ("dq_weight", dq_weight),
+                         ("dk_weight", dk_weight)), to_head, positions)
     desc, _keep = _rope_desc(inv_freq, positions, axis_of_freq, interleaved, (P, B, Np))
     with _Launch(dq_seq.device, stream) as at:
         ws = at.scratch(workspace, ulysses_qkv_norm_rope_workspace_size(d)) if norm else None
@@ -570,8 +604,8 @@ def ulysses_qkv_norm_rope_bwd(q_seq, k_seq, dq_out, dk_out, dv_out, dq_seq, dk_s
             B, Np * P, Hq, Hkv, d, P, 0 if q_seq is None else _token_stride("q_seq", q_seq, d),
             0 if k_seq is None else _token_stride("k_seq", k_seq, d), _token_stride("dq_seq", dq_seq, d),
             _token_stride("dk_seq", dk_seq, d), 0 if dv_seq is None else _token_stride("dv_seq", dv_seq, d),
-            ctypes.addressof(desc), float(eps), int(bool(to_head)), _dt(dq_seq), _ptr(ws),
-            0 if ws is None else ws.numel() * ws.element_size(), at.raw()))
+            ctypes.addressof(desc), eps, 1 if to_head else 0, _dt(dq_seq), _ptr(ws),
+            0 if ws is None else ws.nbytes, at.raw()))
     return dq_seq, dk_seq, dv_seq
 
 

@@ -85,72 +85,26 @@ __device__ __forceinline__ void load8(const float *row, int i, int D, float (&x)
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
-// A sum held as hi + lo: 48 bits without the slow 64-bit units.
-__device__ __forceinline__ float2 two_sum(float2 s, float2 v)
+// The totals of a call without gradients.
+__global__ void __launch_bounds__(1024) totals_kernel(const CeTotals t)
 {
-    const float hi = s.x + v.x, t = hi - s.x;
-    if (!isfinite(hi))
-        return make_float2(hi, 0.f);
-    const float err = (s.x - (hi - t)) + (v.x - t) + s.y + v.y;
-    const float top = hi + err;
-    return make_float2(top, err - (top - hi));
-}
-
-__device__ __forceinline__ float2 warp_two_sum(float2 s)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        s = two_sum(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)));
-    return s;
-}
-
-// Every shard's mean over its good rows, a block per shard, and from the last
-// block to finish the total sum_r loss_r good_r / max(sum_r good_r, 1).  Every
-// sum is taken in one order.
-__global__ void __launch_bounds__(1024) totals_kernel(const float *__restrict__ row_loss,
-                                                      const unsigned long long *__restrict__ good, int64_t per_shard,
-                                                      int P, float *shard_loss, int64_t *__restrict__ shard_good,
-                                                      float *__restrict__ total, int *__restrict__ shards_done)
-{
-    __shared__ float2 part[32];
-    __shared__ int last;
     grid_wait();
-    const int r = blockIdx.x;
-    const float *base = row_loss + r * per_shard;
-    float2 s = make_float2(0.f, 0.f);
-    for (int64_t i = threadIdx.x; i < per_shard; i += 1024)
-        s = two_sum(s, make_float2(base[i], 0.f));
-    s = warp_two_sum(s);
-    if (lane_id() == 0)
-        part[warp_id()] = s;
-    __syncthreads();
-    if (warp_id() == 0) {
-        s = warp_two_sum(part[lane_id()]);
-        if (lane_id() == 0) {
-            const long long n = static_cast<long long>(good[r]);
-            shard_loss[r] = n > 0 ? static_cast<float>((static_cast<double>(s.x) + s.y) / static_cast<double>(n)) : 0.f;
-            shard_good[r] = n;
-            __threadfence();
-            last = atomicAdd(shards_done, 1) == P - 1;
-            __threadfence();
-        }
+    __shared__ float2 part[32];
+    for (int r = 0; r < t.P; ++r) {
+        const float *base = t.row_loss + r * t.per_shard;
+        float2 s = make_float2(0.f, 0.f);
+        for (int64_t i = threadIdx.x; i < t.per_shard; i += 1024)
+            s = two_sum(s, make_float2(base[i], 0.f));
+        s = warp_two_sum(s);
+        if (lane_id() == 0)
+            part[warp_id()] = s;
+        __syncthreads();
+        if (warp_id() == 0)
+            ce_shard(t, r, warp_two_sum(part[lane_id()]));
+        __syncthreads();
     }
-    __syncthreads();
-    if (!last || warp_id() != 0)
-        return;
-    double num = 0.0;
-    long long den = 0;
-    for (int k = lane_id(); k < P; k += 32) {
-        const long long n = static_cast<long long>(good[k]);
-        num += static_cast<double>(__ldcg(shard_loss + k)) * static_cast<double>(n);
-        den += n;
-    }
-    for (int o = 16; o > 0; o >>= 1) {
-        num += __shfl_xor_sync(0xffffffffu, num, o);
-        den += __shfl_xor_sync(0xffffffffu, den, o);
-    }
-    if (lane_id() == 0)
-        *total = static_cast<float>(num / static_cast<double>(den > 1 ? den : 1));
+    if (warp_id() == 0)
+        ce_total(t);
 }
 
 // One block: the labels shifted over the whole sequence, each shard's good
@@ -160,8 +114,7 @@ __global__ void __launch_bounds__(1024) totals_kernel(const float *__restrict__ 
 __global__ void __launch_bounds__(1024) labels_kernel(const int64_t *__restrict__ labels, int32_t *__restrict__ shifted,
                                                       unsigned long long *__restrict__ good,
                                                       float *__restrict__ row_loss, int32_t *__restrict__ index,
-                                                      int *__restrict__ n_good, int *__restrict__ shards_done,
-                                                      unsigned rows, unsigned Np, unsigned B, int P, int V,
+                                                      int *__restrict__ n_good, unsigned rows, unsigned Np, unsigned B, int P, int V,
                                                       unsigned *status)
 {
     constexpr int kEach = 8;
@@ -169,8 +122,6 @@ __global__ void __launch_bounds__(1024) labels_kernel(const int64_t *__restrict_
     grid_next();
     for (int r = threadIdx.x; r < P; r += 1024)
         good[r] = 0;
-    if (threadIdx.x == 0)
-        *shards_done = 0;
     __syncthreads();
     int done = 0;
     for (int64_t base = 0; base < rows; base += 1024 * kEach) {
@@ -450,7 +401,7 @@ Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
     size_t o = 0;
     auto take = [&](size_t &at, size_t bytes) { at = o, o += up(bytes); };
     take(L.good, sizeof(unsigned long long) * P);
-    take(L.n_good, 2 * sizeof(int));
+    take(L.n_good, sizeof(int));
     take(L.shifted, sizeof(int32_t) * T);
     take(L.row_loss, sizeof(float) * T);
     take(L.index, sizeof(int32_t) * T);
@@ -516,9 +467,8 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
     // Few rows: each goes to several blocks, of at least two vectors a thread.
     const int parts = static_cast<int>(std::max<int64_t>(
         1, std::min<int64_t>(V / (2 * 8 * (V > kLongRow ? 512 : 128)), 4 * num_sms() / std::max<int64_t>(1, rows))));
-    int *shards_done = a.n_good + 1;
-    labels_kernel<<<1, 1024, 0, s>>>(labels, shifted, good, row_loss, index, a.n_good, shards_done,
-                                     static_cast<unsigned>(rows), static_cast<unsigned>(N / P),
+    a.totals = CeTotals{row_loss, good, rows / P, P, shard_loss, total, shard_good};
+    labels_kernel<<<1, 1024, 0, s>>>(labels, shifted, good, row_loss, index, a.n_good, static_cast<unsigned>(rows), static_cast<unsigned>(N / P),
                                      static_cast<unsigned>(B), P, V, device_status_ptr());
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
@@ -544,17 +494,20 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
             e = launch_after(V > kLongRow ? rows_kernel<kSplit, 512> : rows_kernel<kSplit, 128>,
                              static_cast<int64_t>(L.rows) * parts, V > kLongRow ? 512 : 128, 0, s, a, g, label, row_loss,
                              parts);
+        // the last product of a call makes the totals beside its own work
+        const bool end = base + L.rows >= rows;
+        a.make_totals = end && !dweight;
         if (e == cudaSuccess && dhidden)
             e = launch_ce_product(kCeDh, a, ws + L.h, L.ldh, w, ldw, g, kEsize, s);
+        a.make_totals = end;
         if (e == cudaSuccess && dweight)
             e = launch_ce_product(kCeDw, a, ws + L.h, L.ldh, w, ldw, g, kEsize, s);
         if (e != cudaSuccess)
             return e;
     }
-    if (e != cudaSuccess)
-        return e;
-    return launch_after(totals_kernel, P, 1024, 0, s, row_loss, good, rows / P, P, shard_loss, shard_good, total,
-                        shards_done);
+    if (e == cudaSuccess && !grad)
+        e = launch_after(totals_kernel, 1, 1024, 0, s, a.totals);
+    return e;
 }
 
 }  // namespace

@@ -24,6 +24,16 @@ enum CeProduct {
     kCeDw = 2,      // dW = g^T h   [V][D]
 };
 
+// What a call returns beside the gradients.
+struct CeTotals {
+    const float *row_loss;
+    const unsigned long long *good;  // [P] good rows
+    int64_t per_shard;               // rows
+    int P;
+    float *shard_loss, *total;
+    int64_t *shard_good;
+};
+
 struct CeArgs {
     int *n_good;            // good rows of the whole call (device)
     int64_t base;           // first good row of the piece
@@ -41,7 +51,58 @@ struct CeArgs {
     void *dh, *dw;
     float *acc;             // dW over the pieces, in tiles (see tile_slot)
     float *partial;         // tiles split over the contraction
+    int make_totals;        // this product's idle warp makes the totals
+    CeTotals totals;
 };
+
+// A sum held as hi + lo: 48 bits without the slow 64-bit units.
+__device__ __forceinline__ float2 two_sum(float2 s, float2 v)
+{
+    const float hi = s.x + v.x, t = hi - s.x;
+    if (!isfinite(hi))
+        return make_float2(hi, 0.f);
+    const float err = (s.x - (hi - t)) + (v.x - t) + s.y + v.y;
+    const float top = hi + err;
+    return make_float2(top, err - (top - hi));
+}
+
+__device__ __forceinline__ float2 warp_two_sum(float2 s)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        s = two_sum(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)));
+    return s;
+}
+
+// Shard r's mean over its good rows from the sum of its rows' losses, and the
+// total sum_r loss_r good_r / max(sum_r good_r, 1): by one warp, every sum in
+// one order.
+__device__ __forceinline__ void ce_shard(const CeTotals &t, int r, float2 sum)
+{
+    if (lane_id() == 0) {
+        const long long n = static_cast<long long>(t.good[r]);
+        t.shard_loss[r] = n > 0 ? static_cast<float>((static_cast<double>(sum.x) + sum.y) / static_cast<double>(n)) : 0.f;
+        t.shard_good[r] = n;
+    }
+}
+
+__device__ __forceinline__ void ce_total(const CeTotals &t)
+{
+    __syncwarp();  // lane 0's shard means
+    double num = 0.0;
+    long long den = 0;
+    for (int k = lane_id(); k < t.P; k += 32) {
+        const long long n = static_cast<long long>(t.good[k]);
+        num += static_cast<double>(t.shard_loss[k]) * static_cast<double>(n);
+        den += n;
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+        num += __shfl_xor_sync(0xffffffffu, num, o);
+        den += __shfl_xor_sync(0xffffffffu, den, o);
+    }
+    if (lane_id() == 0)
+        *t.total = static_cast<float>(num / static_cast<double>(den > 1 ? den : 1));
+}
 
 // Rows of the piece: device data, since the number of good rows is.
 __device__ __forceinline__ int ce_piece_rows(const CeArgs &a)

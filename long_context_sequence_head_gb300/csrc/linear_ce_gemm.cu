@@ -340,6 +340,20 @@ __device__ __forceinline__ void finish_grad(const CeArgs &a, float (&x)[kCols], 
                        lane);
 }
 
+// The call's totals by one warp alone.
+__device__ __noinline__ void totals_by_warp(const CeTotals &t)
+{
+    for (int r = 0; r < t.P; ++r) {
+        const float *base = t.row_loss + r * t.per_shard;
+        float2 s = make_float2(0.f, 0.f);
+#pragma unroll 8
+        for (int64_t i = lane_id(); i < t.per_shard; i += 32)
+            s = two_sum(s, make_float2(base[i], 0.f));
+        ce_shard(t, r, warp_two_sum(s));
+    }
+    ce_total(t);
+}
+
 template <int kWhat, bool kSplit>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ce_product_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
@@ -499,6 +513,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 *abort_flag = 1;
             mma_commit_pair(drain);
         }
+        if (kWhat != kCeLogits && cta == 1 && pair == 0 && a.make_totals)
+            totals_by_warp(a.totals);  // this CTA's issuer has nothing else to do
+        __syncwarp();
         if (lane == 0)
             mbar_wait(drain, 0, w, 0xa4);  // in both CTAs: every product and release is through
     } else {
