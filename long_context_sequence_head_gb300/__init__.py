@@ -843,17 +843,18 @@ def ulysses_sharded_linear_ce_loss(hidden, weight, labels, P: int, dhidden: Opti
     int64, total [1] fp32) on the device; fills dhidden (like hidden) and
     dweight (like weight) if given.  `outputs` may supply those three tensors.
     """
-    if hidden.dim() != 4 or hidden.shape[0] != P:
-        raise ValueError(f"hidden must be [P={P}][B][N/P][D], got {tuple(hidden.shape)}")
-    _, B, Np, D = hidden.shape
-    if weight.dim() != 2 or weight.shape[1] != D or weight.dtype != hidden.dtype:
-        raise ValueError(f"weight must be [V][{D}] of {hidden.dtype}, got {tuple(weight.shape)} of {weight.dtype}")
-    V = weight.shape[0]
-    if labels.dtype != torch.int64 or tuple(labels.shape) != (P, B, Np):
+    hs, ws_ = hidden.shape, weight.shape
+    if len(hs) != 4 or hs[0] != P:
+        raise ValueError(f"hidden must be [P={P}][B][N/P][D], got {tuple(hs)}")
+    _, B, Np, D = hs
+    dtype, device = hidden.dtype, hidden.get_device()
+    if len(ws_) != 2 or ws_[1] != D or weight.dtype is not dtype:
+        raise ValueError(f"weight must be [V][{D}] of {dtype}, got {tuple(ws_)} of {weight.dtype}")
+    if labels.dtype is not torch.int64 or labels.shape != (P, B, Np):
         raise ValueError("labels must be int64 [P][B][N/P]")
-    for name, t, like in (("dhidden", dhidden, hidden), ("dweight", dweight, weight)):
-        if t is not None and (tuple(t.shape) != tuple(like.shape) or t.dtype != like.dtype):
-            raise ValueError(f"{name} must be {tuple(like.shape)} of {like.dtype}, got {tuple(t.shape)} of {t.dtype}")
+    for name, t, like in (("dhidden", dhidden, hs), ("dweight", dweight, ws_)):
+        if t is not None and (t.shape != like or t.dtype is not dtype):
+            raise ValueError(f"{name} must be {tuple(like)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
     if outputs is not None:
         shard_loss, shard_good, total = outputs
         if (shard_loss.dtype != torch.float32 or shard_loss.numel() != P or shard_good.dtype != torch.int64
@@ -861,21 +862,25 @@ def ulysses_sharded_linear_ce_loss(hidden, weight, labels, P: int, dhidden: Opti
             raise ValueError("outputs must be (fp32 [P], int64 [P], fp32 [>=1])")
     for t in (hidden, weight, labels, dhidden, dweight) + tuple(outputs or ()):
         if t is not None:
-            _on(hidden, t)
+            if t.get_device() != device or device < 0:
+                _on(hidden, t)
             if not t.is_contiguous():
                 raise ValueError("tensors must be contiguous")
-    dev, grad = hidden.device, dhidden is not None or dweight is not None
-    with _Launch(dev, stream) as at:
+    V, grad = ws_[0], dhidden is not None or dweight is not None
+    with _Launch(hidden.device, stream) as at:
         if outputs is None:
             shard_loss = at.empty(P, torch.float32)
             shard_good = at.empty(P, torch.int64)
             total = at.empty(1, torch.float32)
-        need = ulysses_sharded_linear_ce_workspace_size(B, Np * P, D, V, P, grad, hidden.dtype)
+        # the library checks the size of a workspace that is given
+        need = 0 if workspace is not None else ulysses_sharded_linear_ce_workspace_size(B, Np * P, D, V, P, grad, dtype)
         ws = at.scratch(workspace, need)
         _check("ulysses_sharded_linear_ce_loss", load().ulysses_sharded_linear_ce_loss(
             hidden.data_ptr(), weight.data_ptr(), labels.data_ptr(), _ptr(dhidden), _ptr(dweight),
             shard_loss.data_ptr(), shard_good.data_ptr(), total.data_ptr(), B, Np * P, D, V, P, _dt(hidden),
-            ws.data_ptr(), ws.numel() * ws.element_size(), at.raw()))
+            ws.data_ptr(), ws.nbytes, at.raw()))
+    if outputs is None:
+        return shard_loss, shard_good, total
     return shard_loss, shard_good, total[:1]
 
 
