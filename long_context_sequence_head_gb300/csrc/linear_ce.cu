@@ -22,16 +22,14 @@ namespace uly {
 namespace {
 
 // Rows of a piece: as many as hold kPieceBytes of exponentials and gradients (2
-// bytes a value, 10 in fp32), at least 1024.  Larger pieces spread the fp32 dW
-// that is carried from piece to piece (read and written once each) over more
-// products.
+// bytes a value, 10 in fp32), at least 1024 and at most 65,536.  dW is carried
+// from piece to piece in fp32: at D = 2560 and V = 151,936 its 1.6 GB read and
+// written are 0.46 ms beside 12 ms of products for a piece of 8448 rows.
 constexpr int64_t kPieceBytes = int64_t(2500) << 20;
-// Vocabularies above this take 512 threads a row, others 128.
-constexpr int kLongRow = 8192;
-// From this many rows on, a bf16 weight whose rows are not whole 128-byte
-// lines is copied to a pitch that is (TMA reads two lines for every 128 bytes
-// of a row that starts inside one).
-constexpr int64_t kLayRows = 1024;
+// Vocabularies above this take 512 threads a row, others 128.  Whole calls with
+// 512 / 128, us: 4096 rows x 16,000 words (D = 256) 194 / 175, x 3208 107 / 86;
+// 1024 rows x 50,257 (D = 776) 320 / 327, 512 x 32,000 90 / 97.
+constexpr int kLongRow = 24576;
 
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu); }
@@ -114,8 +112,8 @@ __global__ void __launch_bounds__(1024) totals_kernel(const CeTotals t)
 __global__ void __launch_bounds__(1024) labels_kernel(const int64_t *__restrict__ labels, int32_t *__restrict__ shifted,
                                                       unsigned long long *__restrict__ good,
                                                       float *__restrict__ row_loss, int32_t *__restrict__ index,
-                                                      int *__restrict__ n_good, unsigned rows, unsigned Np, unsigned B, int P, int V,
-                                                      unsigned *status)
+                                                      int *__restrict__ n_good, unsigned rows, unsigned Np, unsigned B,
+                                                      int P, int V, unsigned *status)
 {
     constexpr int kEach = 8;
     __shared__ int warp_sum[32];
@@ -247,18 +245,16 @@ __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ CeA
     lay8<kSplit>(live ? hidden : nullptr, src, i, a.D, out, r, ldh, ldh * a.rows);
 }
 
-// The weight as the products want it: fp32 as planes, bf16 on a pitch of
-// whole 128-byte lines.
-template <bool kSplit>
-__global__ void __launch_bounds__(256) lay_weight_kernel(const void *__restrict__ w, int D, int V,
-                                                         uint16_t *__restrict__ out, int64_t ldw)
+// fp32 weight as planes.
+__global__ void __launch_bounds__(256) split_weight_kernel(const float *__restrict__ w, int D, int V,
+                                                           uint16_t *__restrict__ out, int64_t ldw)
 {
     grid_wait();
     grid_next();
     const int vecs = (D + 7) / 8;
     const int64_t at = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x, v = at / vecs;
     if (v < V)
-        lay8<kSplit>(w, v, static_cast<int>(at - v * vecs) * 8, D, out, v, ldw, ldw * V);
+        lay8<true>(w, v, static_cast<int>(at - v * vecs) * 8, D, out, v, ldw, ldw * V);
 }
 
 // One CTA per row of the piece, or several that share a row's columns where
@@ -266,6 +262,9 @@ __global__ void __launch_bounds__(256) lay_weight_kernel(const void *__restrict_
 // bf16, to planes in fp32.  e stays relative to its own columns'
 // maximum until here, as fp16 (2^-11 of e; below 2^-14 of that maximum the
 // error is 2^-25 of it): stored as bf16, g would be rounded to 8 bits twice.
+// Memory-bound: 5,734 rows of 151,936 in 0.55 ms, 6.3 TB/s; 4,830 of 50,257 in
+// 0.16 ms, 6.1 TB/s (the row's statistics are joined while its first values are
+// on their way; loaded after them it took 0.18).
 template <bool kSplit, int kRowThreads>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ CeArgs a, uint16_t *__restrict__ g,
                                                            const int32_t *__restrict__ label,
@@ -384,7 +383,6 @@ struct Layout {
     size_t good, n_good, shifted, row_loss, index, label, target, stats, h, w, e, g, acc, partial, total;
     int64_t ldh, ldg;
     int rows, stat_tiles;
-    bool lay_weight;
 };
 
 Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
@@ -409,8 +407,7 @@ Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
     take(L.target, sizeof(float) * L.rows);
     take(L.stats, sizeof(float2) * L.rows * static_cast<size_t>(L.stat_tiles));
     take(L.h, planes * L.rows * L.ldh * 2);
-    L.lay_weight = split || (D % 64 != 0 && grad && T >= kLayRows);
-    if (L.lay_weight)
+    if (split)
         take(L.w, planes * V * L.ldh * 2);
     if (grad) {
         take(L.g, planes * kept * 2);
@@ -420,8 +417,8 @@ Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
         const size_t tiles = static_cast<size_t>((V + kCeTile - 1) / kCeTile) * ((D + kCeTile - 1) / kCeTile);
         if (T > L.rows)
             take(L.acc, sizeof(float) * kCeTileFloats * tiles);
-        take(L.partial, sizeof(float) * kCeTileFloats * 2 *
-                            std::max(ce_most_workers(kCeDh, L.rows, D, V), ce_most_workers(kCeDw, L.rows, D, V)));
+        take(L.partial, sizeof(float) * kCeTileFloats *
+                            std::max(ce_most_parts(kCeDh, L.rows, D, V), ce_most_parts(kCeDw, L.rows, D, V)));
     }
     L.total = o;
     return L;
@@ -445,11 +442,6 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
     CeArgs a = {};
     a.n_good = reinterpret_cast<int *>(ws + L.n_good);
     a.rows = L.rows;
-    // few tiles: narrower ones, so that more SMs have some
-    a.logit_cols = kCeTile;
-    const int64_t row_tiles = (L.rows + kCeTile - 1) / kCeTile;
-    while (a.logit_cols > kCeStatCols && row_tiles * ((V + a.logit_cols - 1) / a.logit_cols) <= num_sms() / 4)
-        a.logit_cols /= 2;
     a.D = D;
     a.V = V;
     a.ldg = L.ldg;
@@ -468,19 +460,20 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
     const int parts = static_cast<int>(std::max<int64_t>(
         1, std::min<int64_t>(V / (2 * 8 * (V > kLongRow ? 512 : 128)), 4 * num_sms() / std::max<int64_t>(1, rows))));
     a.totals = CeTotals{row_loss, good, rows / P, P, shard_loss, total, shard_good};
-    labels_kernel<<<1, 1024, 0, s>>>(labels, shifted, good, row_loss, index, a.n_good, static_cast<unsigned>(rows), static_cast<unsigned>(N / P),
-                                     static_cast<unsigned>(B), P, V, device_status_ptr());
+    labels_kernel<<<1, 1024, 0, s>>>(labels, shifted, good, row_loss, index, a.n_good, static_cast<unsigned>(rows),
+                                     static_cast<unsigned>(N / P), static_cast<unsigned>(B), P, V,
+                                     device_status_ptr());
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
     const void *w = weight;
     int64_t ldw = D;
     const int64_t vecs = (D + 7) / 8;
-    if (L.lay_weight) {
+    if (kSplit) {
         w = ws + L.w;
         ldw = L.ldh;
-        e = launch_after(lay_weight_kernel<kSplit>, (static_cast<int64_t>(V) * vecs + 255) / 256, 256, 0, s, weight, D, V,
-                         reinterpret_cast<uint16_t *>(ws + L.w), ldw);
+        e = launch_after(split_weight_kernel, (static_cast<int64_t>(V) * vecs + 255) / 256, 256, 0, s,
+                         static_cast<const float *>(weight), D, V, reinterpret_cast<uint16_t *>(ws + L.w), ldw);
     }
     for (int64_t base = 0; base < rows; base += L.rows) {
         a.base = base;

@@ -38,7 +38,6 @@ struct CeArgs {
     int *n_good;            // good rows of the whole call (device)
     int64_t base;           // first good row of the piece
     int rows;               // rows a piece may have
-    int logit_cols;         // columns of a tile of logits: 256, 128 or 64
     int D, V;
     int64_t ldg;            // row pitch of e and g, elements
     void *e;                // [rows][ldg]: fp16 (bf16 inputs) or fp32 exponentials
@@ -111,8 +110,8 @@ __device__ __forceinline__ int ce_piece_rows(const CeArgs &a)
     return left <= 0 ? 0 : (left < a.rows ? static_cast<int>(left) : a.rows);
 }
 
-// Most pairs that may share a product's leftover tiles (host, for the workspace).
-int ce_most_workers(CeProduct what, int rows, int D, int V);
+// Most tiles that a product may leave in `partial` (host, for the workspace).
+int ce_most_parts(CeProduct what, int rows, int D, int V);
 
 // esize: 2 (bf16) or 4 (fp32, the operands as three bf16 planes each).  h: the
 // piece's rows; w: the weight; g: the logits' gradient; ldh, ldw: row pitches

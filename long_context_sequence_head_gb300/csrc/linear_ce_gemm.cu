@@ -2,13 +2,22 @@
 // tensor cores, one persistent kernel per product.
 //
 // A CTA pair owns a 256 x 256 output tile (fewer columns where D asks for it):
-// each CTA loads its 128 rows of A and its 128 columns of B (TMA, 128-byte swizzle), one thread of the pair
-// issues tcgen05.mma.cta_group::2 (M = 256, N = 256), and each CTA's TMEM holds
-// 128 rows of the fp32 result, twice, so that one tile is written out while
-// the next is formed.  A pair reads half of what two single CTAs would: 64
-// bytes a clock and SM from L2 at full rate.  The operands come as they lie:
-// a matrix whose rows run along the contraction is K-major, one whose rows run
-// along the output (W in dh; g and h in dW) is MN-major.
+// each CTA loads its 128 rows of A and its 128 columns of B (TMA, 128-byte
+// swizzle), one thread of the pair issues tcgen05.mma.cta_group::2 (M = 256, N =
+// 256), and each CTA's TMEM holds 128 rows of the fp32 result, twice, so that
+// one tile is written out while the next is formed.  A pair reads half of what
+// two single CTAs would: 64 bytes a clock and SM from L2 at full rate.  The
+// operands come as they lie: a matrix whose rows run along the contraction is
+// K-major, one whose rows run along the output (W in dh; g and h in dW) is
+// MN-major.
+//
+// Measured (5,734 rows with labels, D = 2560, V = 151,936, bf16): logits 2.57
+// ms, dh 2.47, dW 2.41, that is 1.74 to 1.85 PFLOP/s against 1.90 of the
+// library's product in a burst; back to back the card's power limit sets the
+// clock (the same products of a constant matrix take 2.1 ms).  A step of 64
+// takes 343 ns, which is 14 TB/s from L2: at D = 776 and V = 50,257 narrower
+// tiles (224 columns) do not shorten it, and the products run at 0.66 to 0.75
+// of the tensor cores' rate.
 //
 // Warps 0-15 write results out (TMEM lane quarter warp % 4, columns 64 (warp /
 // 4) ..): the logits' exponentials take longer than a short contraction's
@@ -16,10 +25,14 @@
 // do not.  Warp 16 loads, warp 17 issues products.
 //
 // Tiles beyond the last full round over the pairs are split along the
-// contraction when that saves more than joining them costs: every pair takes
-// an equal run of the leftover steps, leaves its fp32 tile in `partial`, and a
-// second kernel adds the runs in order.  The split depends on the sizes and
-// the number of good rows alone, so results repeat bit for bit.
+// contraction when that saves more than joining them costs: each into as many
+// equal runs as there are pairs for, every pair leaves its fp32 tile in
+// `partial`, and a second kernel adds the runs in order.  The pairs on one run
+// of neighbouring tiles read the same panels at the same time; an even spread
+// of all steps over all pairs, which lets them drift apart, took 415 us where
+// no split took 251 (dh of 4,500 rows, 72 tiles on 76 pairs, D = 776, V =
+// 50,257), since every tile then reads its panels from DRAM.  The split depends
+// on the sizes and the number of good rows alone, so results repeat bit for bit.
 //
 // The tensor cores' accumulation rounds toward zero: a sum shrinks by up to
 // 2^-24 of itself with every instruction (16 values of the contraction).  Over
@@ -51,8 +64,12 @@ constexpr int kBars = 2 * kStages + 5;
 constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kWarpStaging + 8 * kBars + 16 + 1024;
 constexpr int kPlanePairs = 6;
 constexpr int kCeMaxDevices = 64;
-constexpr int kMinRun = 8;       // least steps of a run
-constexpr int kSplitGain = 32;   // steps a split must save
+constexpr int kMinRun = 8;  // least steps of a run
+// Steps a split must save: a step takes 0.34 us, the runs' tiles and the join 10
+// to 20 us.  Whole calls at 32 / 64 / 128, us: 300 rows x 2048 x 5000 62 / 74 /
+// 72, 1180 x 496 x 3440 52 / 57 / 57, 256 x 352 x 6410 43 / 43 / 64, 6765 x 200 x
+// 3208 110 / 103 / 111.
+constexpr int kSplitGain = 32;
 
 template <int kWhat, bool kSplit>
 constexpr int kChunkSteps = kSplit ? 1 : (kWhat == kCeLogits ? 8 : 64);
@@ -62,21 +79,18 @@ struct Plan {
     int mt, nt, kb;   // tiles along the rows and columns of the result, steps of the contraction
     int cols;         // columns of a tile
     int whole;        // tiles [0, whole) are done by one pair each
-    int workers;      // pairs sharing the tiles from `whole` on
+    int rem, runs;    // the others, each in so many runs (0: none)
 };
 
-__host__ __device__ inline int ce_workers(int64_t tiles, int kb, int pairs, int &whole)
+// Runs of each of the tiles left over from full rounds; 0: those are done whole too.
+__host__ __device__ inline int ce_runs(int64_t tiles, int kb, int pairs)
 {
     const int rem = static_cast<int>(tiles % pairs);
-    whole = static_cast<int>(tiles);
-    if (rem == 0 || static_cast<int64_t>(kb) * (pairs - rem) <= static_cast<int64_t>(kSplitGain) * pairs)
+    if (rem == 0)
         return 0;
-    const int64_t most = static_cast<int64_t>(rem) * kb / kMinRun;
-    const int workers = most < pairs ? static_cast<int>(most) : pairs;
-    if (workers <= rem)
-        return 0;
-    whole = static_cast<int>(tiles) - rem;
-    return workers;
+    int runs = pairs / rem;
+    runs = runs < kb / kMinRun ? runs : kb / kMinRun;
+    return runs > 1 && kb - kb / runs > kSplitGain ? runs : 0;
 }
 
 template <int kWhat>
@@ -87,18 +101,13 @@ __device__ __forceinline__ Plan make_plan(const CeArgs &a, int cnt, int pairs)
     const int K = kWhat == kCeLogits ? a.D : (kWhat == kCeDh ? a.V : cnt);
     p.mt = (M + kCeTile - 1) / kCeTile;
     p.kb = (K + kCeStep - 1) / kCeStep;
-    if (kWhat == kCeLogits) {
-        p.cols = a.logit_cols;
-        p.nt = (N + p.cols - 1) / p.cols;
-    } else {
-        // D in equal tiles: 776 as four of 224 instead of three of 256 and one of 8
-        p.nt = (N + kCeTile - 1) / kCeTile;
-        p.cols = ((N + p.nt - 1) / p.nt + 31) / 32 * 32;
-    }
-    p.workers = 0;
-    p.whole = p.mt * p.nt;
-    if (kWhat != kCeLogits)  // a softmax needs whole sums
-        p.workers = ce_workers(static_cast<int64_t>(p.mt) * p.nt, p.kb, pairs, p.whole);
+    p.nt = (N + kCeTile - 1) / kCeTile;
+    // D in equal tiles: 776 as four of 224 instead of three of 256 and one of 8
+    p.cols = kWhat == kCeLogits ? kCeTile : ((N + p.nt - 1) / p.nt + 31) / 32 * 32;
+    const int tiles = p.mt * p.nt;
+    p.runs = kWhat == kCeLogits ? 0 : ce_runs(tiles, p.kb, pairs);  // a softmax needs whole sums
+    p.rem = p.runs > 0 ? tiles % pairs : 0;
+    p.whole = tiles - p.rem;
     return p;
 }
 
@@ -106,33 +115,31 @@ __device__ __forceinline__ Plan make_plan(const CeArgs &a, int cnt, int pairs)
 // loader, the issuer and the writers walk the same list.
 struct Unit {
     int tile, k0, k1;
-    int run;  // -1: the whole tile; else 0 or 1, the pair's first or second run
+    bool part;  // a run: its tile goes to the pair's place in `partial`
 };
 
 struct Units {
     Plan p;
-    int pair, pairs, next_tile, run;
-    int64_t lo, hi;
+    int pair, pairs, next_tile;
+    bool run;  // the pair's run is still to come
 
-    __device__ Units(const Plan &plan, int pair_, int pairs_) : p(plan), pair(pair_), pairs(pairs_), next_tile(pair_), run(0)
+    __device__ Units(const Plan &plan, int pair_, int pairs_)
+        : p(plan), pair(pair_), pairs(pairs_), next_tile(pair_), run(pair_ < plan.rem * plan.runs)
     {
-        const int64_t steps = static_cast<int64_t>(p.mt * static_cast<int64_t>(p.nt) - p.whole) * p.kb;
-        lo = pair < p.workers ? steps * pair / p.workers : 0;
-        hi = pair < p.workers ? steps * (pair + 1) / p.workers : 0;
     }
     __device__ __forceinline__ bool next(Unit &u)
     {
         if (next_tile < p.whole) {
-            u = Unit{next_tile, 0, p.kb, -1};
+            u = Unit{next_tile, 0, p.kb, false};
             next_tile += pairs;
             return true;
         }
-        if (lo >= hi)
+        if (!run)
             return false;
-        const int t = static_cast<int>(lo / p.kb), k0 = static_cast<int>(lo - static_cast<int64_t>(t) * p.kb);
-        const int k1 = hi - lo < p.kb - k0 ? k0 + static_cast<int>(hi - lo) : p.kb;
-        u = Unit{p.whole + t, k0, k1, run++};
-        lo += k1 - k0;
+        run = false;
+        const int r = pair / p.rem;
+        u = Unit{p.whole + pair - r * p.rem, static_cast<int>(static_cast<int64_t>(p.kb) * r / p.runs),
+                 static_cast<int>(static_cast<int64_t>(p.kb) * (r + 1) / p.runs), true};
         return true;
     }
 };
@@ -402,12 +409,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int cnt = ce_piece_rows(a);
     Plan plan = make_plan<kWhat>(a, cnt, pairs);
     if (cnt == 0 && (kWhat != kCeDw || a.base > 0))
-        plan.whole = plan.workers = 0;  // nothing to do; dW without any row is written as zeros by the first piece
+        plan.whole = plan.rem = 0;  // nothing to do; dW without any row is written as zeros by the first piece
     constexpr int kPerStep = kSplit ? kPlanePairs : 1;
-    // bytes of B a CTA loads in a step: its half of the columns (MN-major: in blocks of 64)
+    // a narrow MN-major B: one block of 64 columns per CTA instead of two
     const bool second_block = plan.cols / 2 > 64;
-    const uint32_t b_bytes = kWhat == kCeLogits ? plan.cols / 2 * (kCeStep * 2)
-                                                : (second_block ? kOperandBytes : kOperandBytes / 2);
+    const uint32_t b_bytes = second_block ? kOperandBytes : kOperandBytes / 2;
 
     if (warp == kEpiWarps) {
         // ------------------------------------------------ loads
@@ -576,16 +582,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (!ok)
                 break;
-            if (u.run >= 0) {
+            if (u.part) {
                 if (kWhat == kCeDh && m - lane >= cnt)
                     continue;  // nobody reads these rows
-                float4 *slot = tile_slot(a.partial, 2 * pair + u.run, cta, warp, lane);
+                float4 *slot = tile_slot(a.partial, pair, cta, warp, lane);
 #pragma unroll
                 for (int j = 0; j < kCols / 4; ++j)
                     slot[j * 32] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
             } else if constexpr (kWhat == kCeLogits) {
-                if (col < plan.cols)
-                    finish_logits<kSplit>(a, &te, x, cnt, m, n0 + col, stage, lane);
+                finish_logits<kSplit>(a, &te, x, cnt, m, n0 + col, stage, lane);
             } else {
                 finish_grad<kWhat, kSplit>(a, x, cnt, u.tile, m, n0 + col, cta, warp, n0 + plan.cols, stage, lane);
             }
@@ -609,8 +614,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // is 32 rows x 64 columns of one tile: a warp takes 8 columns (fp32: 4; one
 // 16-byte store a row) of one of kGroups shares of the runs, and the shares'
 // sums are added in order.  Where a few tiles are split, each into dozens of
-// runs, the block's full size of 1024 threads is shared out; where dozens are,
-// each has two or three runs and one group will do.
+// runs, 1024 threads share them out (12 rows, D = 112, V = 138,259: the whole
+// call 76 us, with one group 91); where dozens are, each has two or three runs
+// and one group will do (28 tiles: 9 us, with four groups 22).
 template <bool kSplit>
 constexpr int kJoinCols = kSplit ? 4 : 8;
 template <bool kSplit>
@@ -630,12 +636,8 @@ __global__ void __launch_bounds__(kJoinThreads<kSplit, kGroups>) ce_join_kernel(
     if (cnt == 0)
         return;
     const Plan p = make_plan<kWhat>(a, cnt, pairs);
-    if (p.workers == 0)
-        return;
     const int part = warp_id() % kParts, group = warp_id() / kParts, lane = lane_id();
-    const int rem = p.mt * p.nt - p.whole;
-    const int64_t steps = static_cast<int64_t>(rem) * p.kb;
-    for (int item = blockIdx.x; item < rem * 2 * kEpiWarps; item += gridDim.x) {
+    for (int item = blockIdx.x; item < p.rem * 2 * kEpiWarps; item += gridDim.x) {
         const int slab = item % kEpiWarps, cta = item / kEpiWarps % 2, split = item / (2 * kEpiWarps);
         const int tile = p.whole + split;
         int m0, n0;
@@ -644,27 +646,14 @@ __global__ void __launch_bounds__(kJoinThreads<kSplit, kGroups>) ce_join_kernel(
         const int limit = min(n0 + p.cols, a.D);
         if (m_slab >= (kWhat == kCeDh ? cnt : a.V) || n0 + (slab >> 2) * kCols >= limit)
             continue;  // the whole block agrees
-        const int64_t t0 = static_cast<int64_t>(split) * p.kb, t1 = t0 + p.kb;
-        // workers whose runs [steps w / workers, steps (w + 1) / workers) meet the tile
-        int first = static_cast<int>(t0 * p.workers / steps);
-        first = first > 0 ? first - 1 : 0;
-        while (steps * (first + 1) / p.workers <= t0)
-            ++first;
-        int end = static_cast<int>(t1 * p.workers / steps);
-        end = end > 0 ? end - 1 : 0;
-        while (end < p.workers && steps * end / p.workers < t1)
-            ++end;
         float x[kPart];
 #pragma unroll
         for (int j = 0; j < kPart; ++j)
             x[j] = 0.f;
-        const int each = (end - first + kGroups - 1) / kGroups, k0 = first + group * each,
-                  k1 = min(end, k0 + each);
+        const int each = (p.runs + kGroups - 1) / kGroups, r0 = group * each, r1 = min(p.runs, r0 + each);
 #pragma unroll 4
-        for (int k = k0; k < k1; ++k) {
-            // the tile's first run may be its worker's second
-            const int run = k == first && steps * first / p.workers < t0 ? 1 : 0;
-            const float4 *slot = tile_slot(a.partial, 2 * k + run, cta, slab, lane);
+        for (int r = r0; r < r1; ++r) {
+            const float4 *slot = tile_slot(a.partial, r * p.rem + split, cta, slab, lane);
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
                 const float4 v = slot[(part * kVecs + j) * 32];
@@ -777,16 +766,15 @@ cudaError_t launch(const CeArgs &a, const CUtensorMap &ta, const CUtensorMap &tb
     }
     e = launch_after(kernel, 2 * pairs, kThreads, kSmem, s, ta, tb, te, a, wait_cfg());
     if constexpr (kWhat != kCeLogits) {
-        // Nothing to join if no number of good rows could make the product split
-        // (dh: any number of row tiles up to the most; dW: any contraction).
-        const int M = kWhat == kCeDh ? a.rows : a.V, K = kWhat == kCeDh ? a.V : a.rows;
-        const int mt = (M + kCeTile - 1) / kCeTile, nt = (a.D + kCeTile - 1) / kCeTile, kb = (K + kCeStep - 1) / kCeStep;
-        int whole, most = 0;
-        if (kb > kSplitGain) {
-            most = std::min(mt * nt, pairs - 1);
-            if (kWhat == kCeDw && ce_workers(static_cast<int64_t>(mt) * nt, kb, pairs, whole) == 0)
-                most = 0;  // fewer rows split even less
-        }
+        // Most tiles that any number of good rows could leave to be joined: at
+        // most half the pairs are (two runs each).  dW's tiles are known here,
+        // and fewer rows shorten its contraction and split it less.
+        const int K = kWhat == kCeDh ? a.V : a.rows, kb = (K + kCeStep - 1) / kCeStep;
+        const int nt = (a.D + kCeTile - 1) / kCeTile;
+        const int tiles = ((kWhat == kCeDh ? a.rows : a.V) + kCeTile - 1) / kCeTile * nt;
+        int most = kb > kSplitGain ? std::min(tiles, pairs / 2) : 0;
+        if (kWhat == kCeDw && ce_runs(tiles, kb, pairs) == 0)
+            most = 0;
         const int items = most * 2 * kEpiWarps;
         constexpr int kMany = kJoinGroups<kSplit>;
         if (e == cudaSuccess && items > 0)
@@ -808,7 +796,7 @@ cudaError_t product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh,
     switch (what) {
     case kCeLogits:
         ok = make_map(&ta, h, a.D, a.rows, ldh, planes, kHalf) &&
-             make_map(&tb, w, a.D, a.V, ldw, planes, a.logit_cols / 2);
+             make_map(&tb, w, a.D, a.V, ldw, planes, kHalf);
         ok = ok && (!a.keep || make_exp_map(&te, a, kSplit));
         return ok ? launch<kCeLogits, kSplit>(a, ta, tb, te, s) : cudaErrorInvalidValue;
     case kCeDh:
@@ -823,13 +811,11 @@ cudaError_t product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh,
 
 }  // namespace
 
-int ce_most_workers(CeProduct what, int rows, int D, int V)
+int ce_most_parts(CeProduct what, int rows, int D, int V)
 {
     const int64_t mt = ((what == kCeDw ? V : rows) + kCeTile - 1) / kCeTile, nt = (D + kCeTile - 1) / kCeTile;
     const int64_t kb = ((what == kCeDw ? rows : V) + kCeStep - 1) / kCeStep;
-    if (kb <= kSplitGain)
-        return 0;
-    return static_cast<int>(std::min<int64_t>(kCeMaxPairs, std::min<int64_t>(mt * nt, kCeMaxPairs) * kb / kMinRun));
+    return kb <= kSplitGain ? 0 : static_cast<int>(std::min<int64_t>(kCeMaxPairs, mt * nt * (kb / kMinRun)));
 }
 
 cudaError_t launch_ce_product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh, const void *w, int64_t ldw,
