@@ -6,13 +6,18 @@
 //   x_rv = <h_r, w_v>
 // are never kept: the good rows are taken in pieces of a few thousand, and
 // for each piece
-//   1. logits   x = h W^T; every (row, column tile) leaves its maximum c (in
-//               units of log2), its sum s of e = 2^(x log2 e - c), the row's
-//               target logit, and e itself in the piece buffer;
+//   1. logits   x = h W^T; every (row, 64 columns) leaves c, the sum s of
+//               e = 2^(x log2 e - c), the row's target logit, and e itself;
 //   2. rows     C = max c, S = sum s 2^(c - C); loss = ln S + (C ln 2 - x_y);
-//               e becomes g = softmax - onehot = e 2^(c - C) / S - [v == y];
-//   3. dh       = g W / T for the piece's rows;
-//   4. dW      += g^T h / T, in fp32 across the pieces, rounded once at the end.
+//               e_y -= S, h' = h / S;
+//   3. dh       = e W / (S T) for the piece's rows;
+//   4. dW      += e^T h' / T, in fp32 across the pieces, rounded once at the end.
+// c is 0 for all columns of nearly every row, so that e already is the softmax's
+// numerator and is used as it lies: the division by S goes to dh's rows and to
+// h, and of e only the label's value is touched.  Rewriting e as the logits'
+// gradient, softmax - onehot, took 0.55 of 8.9 ms at 5,734 rows of 151,936 and
+// 0.16 of 1.08 at 4,830 of 50,257; a row whose logits leave +-33 still has its
+// values brought to one c, by powers of two.
 // That is three products instead of the four that recomputing the logits from
 // a kept log-sum-exp would take.  Rows without a label are left out before the
 // first product: the good rows are gathered next to each other.
@@ -21,27 +26,15 @@
 namespace uly {
 namespace {
 
-// Rows of a piece: as many as hold kPieceBytes of exponentials and gradients (2
-// bytes a value, 10 in fp32), at least 1024 and at most 65,536.  dW is carried
-// from piece to piece in fp32: at D = 2560 and V = 151,936 its 1.6 GB read and
-// written are 0.46 ms beside 12 ms of products for a piece of 8448 rows.
+// Rows of a piece: as many as hold kPieceBytes of exponentials (2 bytes a value,
+// 6 in fp32), at least 1024 and at most 65,536.  dW is carried from piece to
+// piece in fp32: at D = 2560 and V = 151,936 its 1.6 GB read and written are 0.46
+// ms beside 12 ms of products for a piece of 8448 rows.
 constexpr int64_t kPieceBytes = int64_t(2500) << 20;
-// Vocabularies above this take 512 threads a row, others 128.  Whole calls with
-// 512 / 128, us: 4096 rows x 16,000 words (D = 256) 194 / 175, x 3208 107 / 86;
-// 1024 rows x 50,257 (D = 776) 320 / 327, 512 x 32,000 90 / 97.
-constexpr int kLongRow = 24576;
+constexpr int kRowThreads = 128;
 
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu); }
-
-__device__ __forceinline__ float2 f16x2_values(uint32_t b)
-{
-    float lo, hi;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}\n"
-        : "=f"(lo), "=f"(hi)
-        : "r"(b));
-    return make_float2(lo, hi);
-}
 
 // Three bf16 parts of x: x1 + x2 + x3 = x up to 2^-26 |x|.
 struct Parts {
@@ -257,122 +250,119 @@ __global__ void __launch_bounds__(256) split_weight_kernel(const float *__restri
         lay8<true>(w, v, static_cast<int>(at - v * vecs) * 8, D, out, v, ldw, ldw * V);
 }
 
-// One CTA per row of the piece, or several that share a row's columns where
-// there are few rows: the row's loss, and with a gradient e -> g, in place in
-// bf16, to planes in fp32.  e stays relative to its own columns'
-// maximum until here, as fp16 (2^-11 of e; below 2^-14 of that maximum the
-// error is 2^-25 of it): stored as bf16, g would be rounded to 8 bits twice.
-// Memory-bound: 5,734 rows of 151,936 in 0.55 ms, 6.3 TB/s; 4,830 of 50,257 in
-// 0.16 ms, 6.1 TB/s (the row's statistics are joined while its first values are
-// on their way; loaded after them it took 0.18).
-template <bool kSplit, int kRowThreads>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ CeArgs a, uint16_t *__restrict__ g,
+// Softmax statistics of some columns: C and S of sum e = S 2^C, and the least c.
+struct Stat {
+    float C, S, least;
+
+    // a C of -inf is that of no columns, with S = 0
+    __device__ __forceinline__ void join(float c, float s, float l)
+    {
+        const float m = fmaxf(C, c);
+        S = (C == m ? S : S * exp2f(C - m)) + (c == m ? s : s * exp2f(c - m));
+        C = m;
+        least = fminf(least, l);
+    }
+};
+
+// One block per row of the piece: its loss, and with a gradient the row's scale
+// 1 / S, e at the label, the row of h' (where dW is wanted), and e on one c where
+// it is not yet.
+template <bool kSplit>
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ CeArgs a,
+                                                           const void *__restrict__ hidden,
                                                            const int32_t *__restrict__ label,
-                                                           float *__restrict__ row_loss, int parts)
+                                                           float *__restrict__ row_loss, uint16_t *__restrict__ out,
+                                                           int64_t ldh)
 {
     grid_wait();
     grid_next();
-    const int cnt = ce_piece_rows(a), r = blockIdx.x / parts, part = blockIdx.x % parts;
-    if (r >= (cnt + kCeStep - 1) / kCeStep * kCeStep)
+    const int cnt = ce_piece_rows(a), r = blockIdx.x;
+    if (r >= cnt)
         return;
-    uint16_t *grow = g + r * a.ldg;
-    const int64_t plane = a.ldg * a.rows;
-    if (r >= cnt) {
-        if (a.keep)
-            for (int v = (part * kRowThreads + threadIdx.x) * 8; v < a.V; v += parts * kRowThreads * 8)
-#pragma unroll
-                for (int i = 0; i < (kSplit ? 3 : 1); ++i)
-                    *reinterpret_cast<uint4 *>(grow + i * plane + v) = make_uint4(0, 0, 0, 0);
-        return;
-    }
     constexpr int kWarps = kRowThreads / 32;
-    constexpr int kAhead = kSplit ? 2 : 4;  // vectors of 8 values loaded before the first is used
-    __shared__ float red[2][kWarps];
-    const int v_step = parts * kRowThreads * 8, v_first = (part * kRowThreads + threadIdx.x) * 8;
-    struct Eight {
-        uint4 v[kSplit ? 2 : 1];
-    } next[kAhead];
-    auto fetch = [&](int v0) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int v = v0 + i * v_step;
-            if (v < a.V) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.e) +
-                                                                   (r * a.ldg + v) * (kSplit ? 4 : 2));
-                next[i].v[0] = src[0];
-                if constexpr (kSplit)
-                    next[i].v[1] = src[1];
-            }
-        }
-    };
-    if (a.keep)
-        fetch(v_first);  // on its way while the row's statistics are joined
+    __shared__ Stat red[kWarps];
     const float2 *stats = a.stats + static_cast<int64_t>(r) * a.stat_tiles;
-    float C = -INFINITY;
-    for (int t = threadIdx.x; t < a.stat_tiles; t += kRowThreads)
-        C = fmaxf(C, stats[t].x);
+    Stat st = {-INFINITY, 0.f, INFINITY};
+#pragma unroll 4
+    for (int t = threadIdx.x; t < a.stat_tiles; t += kRowThreads) {
+        const float2 v = stats[t];
+        st.join(v.x, v.y, v.x);
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        C = fmaxf(C, __shfl_xor_sync(0xffffffffu, C, o));
+    for (int o = 16; o > 0; o >>= 1) {
+        const float c = __shfl_xor_sync(0xffffffffu, st.C, o), s = __shfl_xor_sync(0xffffffffu, st.S, o);
+        st.join(c, s, __shfl_xor_sync(0xffffffffu, st.least, o));
+    }
     if (lane_id() == 0)
-        red[0][warp_id()] = C;
+        red[warp_id()] = st;
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w)
-        C = fmaxf(C, red[0][w]);
-    float S = 0.f;
-    for (int t = threadIdx.x; t < a.stat_tiles; t += kRowThreads)
-        S += stats[t].y * exp2f(stats[t].x - C);
+    st = red[0];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        S += __shfl_xor_sync(0xffffffffu, S, o);
-    if (lane_id() == 0)
-        red[1][warp_id()] = S;
-    __syncthreads();
-    S = 0.f;
-    for (int w = 0; w < kWarps; ++w)
-        S += red[1][w];
+    for (int w = 1; w < kWarps; ++w)
+        st.join(red[w].C, red[w].S, red[w].least);
     const int y = label[r];
-    if (part == 0 && threadIdx.x == 0)  // ln S + C ln 2 - x_y, with C taken out of x_y before anything is rounded
-        row_loss[a.index[a.base + r]] = (log2f(S) - fmaf(a.target[r], kLog2e, -C)) * kLn2;
+    const int64_t row = a.index[a.base + r];
+    if (threadIdx.x == 0) {
+        // ln S + C ln 2 - x_y, with the whole powers of two taken out of x_y before anything is rounded
+        const uint32_t bits = __float_as_uint(st.S), exponent = bits >> 23;
+        const bool normal = exponent > 0 && exponent < 255;
+        const float k = normal ? static_cast<float>(static_cast<int>(exponent) - 127) : 0.f;
+        const float m = normal ? __uint_as_float((bits & 0x007fffffu) | 0x3f800000u) : st.S;
+        row_loss[row] = (log2f(m) - fmaf(a.target[r], kLog2e, -(st.C + k))) * kLn2;
+    }
     if (!a.keep)
         return;
-    const float inv = 1.f / S;
-    for (int v0 = v_first; v0 < a.V; v0 += kAhead * v_step) {
-        Eight now[kAhead];
+    // The label's value (p - 1) S is most of the row's gradient.  In bf16 the
+    // scale takes up what its rounding loses, and is off by that (2^-8 at most)
+    // for the others, which are rounded as much.
+    const float g = ex2_approx(fmaf(a.target[r], kLog2e, -st.C)) - st.S, held = bf16_value(bf16_bits(g));
+    const float scale = (kSplit || held == 0.f ? 1.f : g / held) * (1.f / st.S);
+    uint16_t *erow = a.e + r * a.ldg;
+    const int64_t plane = a.ldg * a.rows;
+    if (st.least < st.C) {
+        for (int v = threadIdx.x * 8; v < a.V; v += kRowThreads * 8) {
+            const float f = exp2f(stats[v / kCeStatCols].x - st.C);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            now[i] = next[i];
-        fetch(v0 + kAhead * v_step);
+            for (int i = 0; i < (kSplit ? 3 : 1); ++i) {
+                uint4 *at = reinterpret_cast<uint4 *>(erow + i * plane + v);
+                uint4 q = *at;
+                uint32_t *w = reinterpret_cast<uint32_t *>(&q);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int v = v0 + i * v_step;
-            if (v >= a.V)
-                break;
-            const float f = exp2f(stats[v / kCeStatCols].x - C) * inv;
-            float x[8];
-            const uint32_t w[4] = {now[i].v[0].x, now[i].v[0].y, now[i].v[0].z, now[i].v[0].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (kSplit) {
-                    x[j] = __uint_as_float(w[j]);
-                } else {
-                    const float2 p = f16x2_values(w[j]);
-                    x[2 * j] = p.x, x[2 * j + 1] = p.y;
-                }
+                for (int j = 0; j < 4; ++j)
+                    w[j] = pack_bf16x2(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xffff0000u) * f);
+                *at = q;
             }
-            if constexpr (kSplit) {
-                const uint4 h = now[i].v[1];
-                x[4] = __uint_as_float(h.x), x[5] = __uint_as_float(h.y), x[6] = __uint_as_float(h.z),
-                x[7] = __uint_as_float(h.w);
-            }
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        a.row_scale[r] = scale;
+        if constexpr (kSplit) {
+            const Parts q = split3(g);
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                erow[i * plane + y] = q.p[i];
+        } else {
+            erow[y] = bf16_bits(g);
+        }
+    }
+    if (a.dw == nullptr)
+        return;
+    for (int i = threadIdx.x * 8; i < a.D; i += kRowThreads * 8) {
+        float x[8];
+        if constexpr (kSplit) {
+            load8(static_cast<const float *>(hidden) + row * a.D, i, a.D, x);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                x[j] = x[j] * f - (v + j == y ? 1.f : 0.f);
-            if constexpr (kSplit)
-                store_planes(grow + v, plane, x);
-            else
-                *reinterpret_cast<uint4 *>(grow + v) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                                  pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+                x[j] *= scale;
+            store_planes(out + r * ldh + i, ldh * a.rows, x);
+        } else {
+            uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(hidden) + row * a.D + i);
+            uint32_t *w = reinterpret_cast<uint32_t *>(&q);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = pack_bf16x2(__uint_as_float(w[j] << 16) * scale, __uint_as_float(w[j] & 0xffff0000u) * scale);
+            *reinterpret_cast<uint4 *>(out + r * ldh + i) = q;
         }
     }
 }
@@ -380,7 +370,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
 size_t up(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Layout {
-    size_t good, n_good, shifted, row_loss, index, label, target, stats, h, w, e, g, acc, partial, total;
+    size_t good, n_good, shifted, row_loss, index, label, target, row_scale, stats, h, w, e, acc, partial, total;
     int64_t ldh, ldg;
     int rows, stat_tiles;
 };
@@ -391,7 +381,7 @@ Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
     const int64_t T = B * N;
     const bool split = esize == 4;
     L.ldg = (V + 63) / 64 * 64;
-    const int64_t fit = std::max<int64_t>(1024, kPieceBytes / (L.ldg * (split ? 10 : 2)) / kCeTile * kCeTile);
+    const int64_t fit = std::max<int64_t>(1024, kPieceBytes / (L.ldg * (split ? 6 : 2)) / kCeTile * kCeTile);
     L.rows = static_cast<int>(std::min<int64_t>(std::min<int64_t>(fit, 65536), (T + 63) / 64 * 64));
     L.ldh = (D + 63) / 64 * 64;
     L.stat_tiles = (V + kCeStatCols - 1) / kCeStatCols;
@@ -405,15 +395,13 @@ Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
     take(L.index, sizeof(int32_t) * T);
     take(L.label, sizeof(int32_t) * L.rows);
     take(L.target, sizeof(float) * L.rows);
+    take(L.row_scale, sizeof(float) * L.rows);
     take(L.stats, sizeof(float2) * L.rows * static_cast<size_t>(L.stat_tiles));
     take(L.h, planes * L.rows * L.ldh * 2);
     if (split)
         take(L.w, planes * V * L.ldh * 2);
     if (grad) {
-        take(L.g, planes * kept * 2);
-        L.e = L.g;  // bf16: e becomes g in place
-        if (split)
-            take(L.e, kept * 4);
+        take(L.e, planes * kept * 2);
         const size_t tiles = static_cast<size_t>((V + kCeTile - 1) / kCeTile) * ((D + kCeTile - 1) / kCeTile);
         if (T > L.rows)
             take(L.acc, sizeof(float) * kCeTileFloats * tiles);
@@ -438,27 +426,25 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
     auto *row_loss = reinterpret_cast<float *>(ws + L.row_loss);
     auto *index = reinterpret_cast<int32_t *>(ws + L.index);
     auto *label = reinterpret_cast<int32_t *>(ws + L.label);
-    auto *g = reinterpret_cast<uint16_t *>(ws + L.g);
+    auto *h = reinterpret_cast<uint16_t *>(ws + L.h);
     CeArgs a = {};
     a.n_good = reinterpret_cast<int *>(ws + L.n_good);
     a.rows = L.rows;
     a.D = D;
     a.V = V;
     a.ldg = L.ldg;
-    a.e = ws + L.e;
+    a.e = reinterpret_cast<uint16_t *>(ws + L.e);
     a.index = index;
     a.label = label;
     a.stats = reinterpret_cast<float2 *>(ws + L.stats);
     a.stat_tiles = L.stat_tiles;
     a.target = reinterpret_cast<float *>(ws + L.target);
+    a.row_scale = reinterpret_cast<float *>(ws + L.row_scale);
     a.keep = grad;
     a.dh = dhidden;
     a.dw = dweight;
     a.acc = reinterpret_cast<float *>(ws + L.acc);
     a.partial = reinterpret_cast<float *>(ws + L.partial);
-    // Few rows: each goes to several blocks, of at least two vectors a thread.
-    const int parts = static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>(V / (2 * 8 * (V > kLongRow ? 512 : 128)), 4 * num_sms() / std::max<int64_t>(1, rows))));
     a.totals = CeTotals{row_loss, good, rows / P, P, shard_loss, total, shard_good};
     labels_kernel<<<1, 1024, 0, s>>>(labels, shifted, good, row_loss, index, a.n_good, static_cast<unsigned>(rows),
                                      static_cast<unsigned>(N / P), static_cast<unsigned>(B), P, V,
@@ -479,22 +465,19 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
         a.base = base;
         const int64_t blocks = ((base == 0 ? std::max<int64_t>(rows, L.rows) : L.rows) * vecs + 255) / 256;
         if (e == cudaSuccess)
-            e = launch_after(gather_kernel<kSplit>, blocks, 256, 0, s, a, hidden, shifted, label,
-                             reinterpret_cast<uint16_t *>(ws + L.h), L.ldh, rows);
+            e = launch_after(gather_kernel<kSplit>, blocks, 256, 0, s, a, hidden, shifted, label, h, L.ldh, rows);
         if (e == cudaSuccess)
-            e = launch_ce_product(kCeLogits, a, ws + L.h, L.ldh, w, ldw, g, kEsize, s);
+            e = launch_ce_product(kCeLogits, a, h, L.ldh, w, ldw, kEsize, s);
         if (e == cudaSuccess)
-            e = launch_after(V > kLongRow ? rows_kernel<kSplit, 512> : rows_kernel<kSplit, 128>,
-                             static_cast<int64_t>(L.rows) * parts, V > kLongRow ? 512 : 128, 0, s, a, g, label, row_loss,
-                             parts);
+            e = launch_after(rows_kernel<kSplit>, L.rows, kRowThreads, 0, s, a, hidden, label, row_loss, h, L.ldh);
         // the last product of a call makes the totals beside its own work
         const bool end = base + L.rows >= rows;
         a.make_totals = end && !dweight;
         if (e == cudaSuccess && dhidden)
-            e = launch_ce_product(kCeDh, a, ws + L.h, L.ldh, w, ldw, g, kEsize, s);
+            e = launch_ce_product(kCeDh, a, h, L.ldh, w, ldw, kEsize, s);
         a.make_totals = end;
         if (e == cudaSuccess && dweight)
-            e = launch_ce_product(kCeDw, a, ws + L.h, L.ldh, w, ldw, g, kEsize, s);
+            e = launch_ce_product(kCeDw, a, h, L.ldh, w, ldw, kEsize, s);
         if (e != cudaSuccess)
             return e;
     }

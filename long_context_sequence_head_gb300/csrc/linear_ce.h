@@ -15,13 +15,17 @@ constexpr int kCeTile = 256;
 constexpr int kCeStep = 64;
 constexpr int kCeStatCols = 64;  // columns behind one (c, s) of the softmax
 constexpr int kCeMaxPairs = 80;
+// Logits within +-2^kCeFree after the exponential need no maximum taken out:
+// sums of 2^21 of them, and their products with anything below 2^58, stay
+// within fp32, and what lies 2^-78 below the smallest such maximum is lost.
+constexpr float kCeFree = 48.f;
 // floats a pair leaves for one tile
 constexpr int64_t kCeTileFloats = static_cast<int64_t>(kCeTile) * kCeTile;
 
 enum CeProduct {
     kCeLogits = 0,  // x  = h W^T   [rows][V]
-    kCeDh = 1,      // dh = g W     [rows][D]
-    kCeDw = 2,      // dW = g^T h   [V][D]
+    kCeDh = 1,      // dh = e W     [rows][D], rows scaled by 1 / S
+    kCeDw = 2,      // dW = e^T h'  [V][D], h' = h / S
 };
 
 // What a call returns beside the gradients.
@@ -39,13 +43,14 @@ struct CeArgs {
     int64_t base;           // first good row of the piece
     int rows;               // rows a piece may have
     int D, V;
-    int64_t ldg;            // row pitch of e and g, elements
-    void *e;                // [rows][ldg]: fp16 (bf16 inputs) or fp32 exponentials
+    int64_t ldg;            // row pitch of e, elements
+    uint16_t *e;            // [planes][rows][ldg] exponentials, then their difference to S at the label
     const int32_t *index;   // good row -> row of hidden
     const int32_t *label;   // [rows] of the piece
     float2 *stats;          // [rows][stat_tiles] (c, s)
     int stat_tiles;
     float *target;          // [rows] logits of the labels
+    float *row_scale;       // [rows] 1 / S
     int keep;               // with a gradient: keep e
     void *dh, *dw;
     float *acc;             // dW over the pieces, in tiles (see tile_slot)
@@ -114,9 +119,9 @@ __device__ __forceinline__ int ce_piece_rows(const CeArgs &a)
 int ce_most_parts(CeProduct what, int rows, int D, int V);
 
 // esize: 2 (bf16) or 4 (fp32, the operands as three bf16 planes each).  h: the
-// piece's rows; w: the weight; g: the logits' gradient; ldh, ldw: row pitches
-// in elements.
+// piece's rows (dW: divided by S); w: the weight; ldh, ldw: row pitches in
+// elements.
 cudaError_t launch_ce_product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh, const void *w, int64_t ldw,
-                              const void *g, int esize, cudaStream_t s);
+                              int esize, cudaStream_t s);
 
 }  // namespace uly

@@ -168,13 +168,6 @@ __device__ __forceinline__ float4 *tile_slot(float *buf, int64_t slot, int cta, 
 }
 
 // ------------------------------------------------------------ writing out
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // 16 bytes of a row: four fp32 values or eight bf16 ones.
 template <bool kF32>
 __device__ __forceinline__ uint4 unit(const float *v)
@@ -184,17 +177,6 @@ __device__ __forceinline__ uint4 unit(const float *v)
     else
         return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                           pack_bf16x2(v[6], v[7]));
-}
-
-// The same for exponentials: fp32 or fp16.
-template <bool kF32>
-__device__ __forceinline__ uint4 exp_unit(const float *v)
-{
-    if constexpr (kF32)
-        return unit<true>(v);
-    else
-        return make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]),
-                          pack_f16x2(v[6], v[7]));
 }
 
 // The warp's 32 rows x 64 columns (row = lane) to memory, 128 bytes of a row
@@ -228,39 +210,50 @@ __device__ __forceinline__ void store_rows(const float (&x)[kCols], void *out, i
     }
 }
 
-// The exponentials to their buffer by TMA: boxes of 32 rows x 128 bytes in the
-// swizzled layout of the map.  Rows past the piece's last are written too
-// where the buffer has them; nobody reads them.
+// The exponentials to their buffer by TMA, a box of 32 rows x 64 columns in the
+// swizzled layout of the map, in fp32 one for each plane.
 template <bool kSplit>
-__device__ __forceinline__ void store_exponentials(const CUtensorMap *te, const float (&x)[kCols], int row0, int col0,
-                                                   int limit, uint8_t *staging, int lane)
+__device__ __forceinline__ void store_exponentials(const CeArgs &a, const CUtensorMap *te, float (&x)[kCols], int row0,
+                                                   int col0, uint8_t *staging, int lane)
 {
-    constexpr int kPer = kSplit ? 4 : 8, kBox = 8 * kPer;  // values per unit, columns per box
 #pragma unroll
-    for (int part = 0; part < kCols / kBox; ++part) {
+    for (int plane = 0; plane < (kSplit ? 3 : 1); ++plane) {
         if (lane == 0)
             bulk_wait_read<0>();  // what was staged before is on its way
         __syncwarp();
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            *reinterpret_cast<uint4 *>(staging + lane * 128 + ((u ^ (lane & 7)) << 4)) =
-                exp_unit<kSplit>(x + (part * 8 + u) * kPer);
+        for (int u = 0; u < 8; ++u) {
+            const uint4 q = unit<false>(x + u * 8);
+            *reinterpret_cast<uint4 *>(staging + lane * 128 + ((u ^ (lane & 7)) << 4)) = q;
+            if (kSplit && plane < 2) {  // what is left for the next planes
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[u * 8 + 2 * i] -= __uint_as_float(w[i] << 16);
+                    x[u * 8 + 2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+                }
+            }
+        }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0 && col0 + part * kBox < limit) {
-            tma_store_2d(te, staging, col0 + part * kBox, row0);
+        if (lane == 0) {
+            tma_store_2d(te, staging, col0, plane * a.rows + row0);
             bulk_commit();
         }
     }
 }
 
-// Logits: the row's maximum and sum over this warp's columns, its target's
-// logit, and the exponentials.
+// Logits: the row's sum of e = 2^(x log2 e - c) over this warp's columns, its
+// target's logit, and e itself.  c is 0 as long as the columns' largest x log2 e
+// lies within kCeFree of it, otherwise that maximum, rounded so that another
+// c changes e by a power of two alone.  The rows between the piece's last and the
+// end of its step of 64 have h = 0 and leave e = 1, finite values that meet zeros
+// in dW.
 template <bool kSplit>
 __device__ __forceinline__ void finish_logits(const CeArgs &a, const CUtensorMap *te, float (&x)[kCols], int cnt, int m,
                                               int col0, uint8_t *staging, int lane)
 {
-    if (col0 >= a.V || m - lane >= cnt)
+    if (col0 >= a.V || m - lane >= (cnt + kCeStep - 1) / kCeStep * kCeStep)
         return;
     const bool live = m < cnt;
     const int y = live ? a.label[m] : -1;
@@ -283,10 +276,10 @@ __device__ __forceinline__ void finish_logits(const CeArgs &a, const CUtensorMap
 #pragma unroll
     for (int j = 8; j < kCols; ++j)
         pm[j & 7] = fmaxf(pm[j & 7], x[j]);
-    const float c = kLog2e * fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
-                                   fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
-    // a row of -inf alone has no maximum to take out: its exponentials are 0
-    const float out = c == -INFINITY ? 0.f : -c;
+    const float top = kLog2e * fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
+                                     fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
+    // columns of -inf alone have no maximum to take out: their exponentials are 0
+    const float c = fabsf(top) <= kCeFree ? 0.f : rintf(top), out = c == -INFINITY ? 0.f : -c;
     const float2 l2 = make_float2(kLog2e, kLog2e), c2 = make_float2(out, out);
     float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -300,7 +293,7 @@ __device__ __forceinline__ void finish_logits(const CeArgs &a, const CUtensorMap
     if (live)
         a.stats[static_cast<int64_t>(m) * a.stat_tiles + col0 / kCeStatCols] = make_float2(c, s.x + s.y);
     if (a.keep)
-        store_exponentials<kSplit>(te, x, m - lane, col0, static_cast<int>(a.ldg), staging, lane);
+        store_exponentials<kSplit>(a, te, x, m - lane, col0, staging, lane);
 }
 
 // Where row m of dh (its place in hidden) or dW goes; negative past the end.
@@ -312,13 +305,16 @@ __device__ __forceinline__ int grad_row(const CeArgs &a, int cnt, int m)
     return kWhat == kCeDh ? a.index[a.base + m] : m;
 }
 
-__device__ __forceinline__ float grad_scale(const CeArgs &a)
+// What row m of the result is multiplied by: 1 / T, and in dh the softmax's 1 / S.
+template <int kWhat>
+__device__ __forceinline__ float grad_scale(const CeArgs &a, int cnt, int m)
 {
     const int n = *a.n_good;
-    return 1.f / static_cast<float>(n > 1 ? n : 1);
+    const float inv = 1.f / static_cast<float>(n > 1 ? n : 1);
+    return kWhat == kCeDh ? (m < cnt ? inv * a.row_scale[m] : 0.f) : inv;
 }
 
-// dh and dW: scaled by 1 / T and rounded once.  dW over several pieces is kept
+// dh and dW: scaled and rounded once.  dW over several pieces is kept
 // in fp32 until the last one.
 template <int kWhat, bool kSplit>
 __device__ __forceinline__ void finish_grad(const CeArgs &a, float (&x)[kCols], int cnt, int tile, int m, int col0,
@@ -339,7 +335,7 @@ __device__ __forceinline__ void finish_grad(const CeArgs &a, float (&x)[kCols], 
             acc[j * 32] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
         return;
     }
-    const float inv = grad_scale(a);
+    const float inv = grad_scale<kWhat>(a, cnt, m);
 #pragma unroll
     for (int j = 0; j < kCols; ++j)
         x[j] *= inv;
@@ -691,7 +687,7 @@ __global__ void __launch_bounds__(kJoinThreads<kSplit, kGroups>) ce_join_kernel(
             }
         }
         const int row = grad_row<kWhat>(a, cnt, m_slab + lane);
-        const float inv = grad_scale(a);
+        const float inv = grad_scale<kWhat>(a, cnt, m_slab + lane);
 #pragma unroll
         for (int j = 0; j < kPart; ++j)
             x[j] *= inv;
@@ -722,11 +718,12 @@ bool make_map(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, in
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 3, base, cols, rows, pitch, planes, 64, box_rows);
 }
 
-// Box of the exponentials: 128 bytes x 32 rows.
-bool make_exp_map(CUtensorMap *map, const CeArgs &a, bool f32)
+// Box of the exponentials on their way out: 64 columns x 32 rows; the planes
+// lie below each other.
+bool make_exp_map(CUtensorMap *map, const CeArgs &a, int planes)
 {
-    return encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, f32 ? 4 : 2, 2, a.e,
-                  a.ldg, a.rows, a.ldg, 1, f32 ? 32 : 64, 32);
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 2, a.e, a.ldg, static_cast<int64_t>(a.rows) * planes, a.ldg,
+                  1, 64, 32);
 }
 
 template <int kWhat, bool kSplit>
@@ -788,7 +785,7 @@ cudaError_t launch(const CeArgs &a, const CUtensorMap &ta, const CUtensorMap &tb
 
 template <bool kSplit>
 cudaError_t product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh, const void *w, int64_t ldw,
-                    const void *g, cudaStream_t s)
+                    cudaStream_t s)
 {
     constexpr int planes = kSplit ? 3 : 1;
     CUtensorMap ta, tb, te = {};  // te: the logits' exponentials alone
@@ -797,13 +794,13 @@ cudaError_t product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh,
     case kCeLogits:
         ok = make_map(&ta, h, a.D, a.rows, ldh, planes, kHalf) &&
              make_map(&tb, w, a.D, a.V, ldw, planes, kHalf);
-        ok = ok && (!a.keep || make_exp_map(&te, a, kSplit));
+        ok = ok && (!a.keep || make_exp_map(&te, a, planes));
         return ok ? launch<kCeLogits, kSplit>(a, ta, tb, te, s) : cudaErrorInvalidValue;
     case kCeDh:
-        ok = make_map(&ta, g, a.V, a.rows, a.ldg, planes, kHalf) && make_map(&tb, w, a.D, a.V, ldw, planes, kCeStep);
+        ok = make_map(&ta, a.e, a.V, a.rows, a.ldg, planes, kHalf) && make_map(&tb, w, a.D, a.V, ldw, planes, kCeStep);
         return ok ? launch<kCeDh, kSplit>(a, ta, tb, te, s) : cudaErrorInvalidValue;
     default:
-        ok = make_map(&ta, g, a.V, a.rows, a.ldg, planes, kCeStep) &&
+        ok = make_map(&ta, a.e, a.V, a.rows, a.ldg, planes, kCeStep) &&
              make_map(&tb, h, a.D, a.rows, ldh, planes, kCeStep);
         return ok ? launch<kCeDw, kSplit>(a, ta, tb, te, s) : cudaErrorInvalidValue;
     }
@@ -819,9 +816,9 @@ int ce_most_parts(CeProduct what, int rows, int D, int V)
 }
 
 cudaError_t launch_ce_product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh, const void *w, int64_t ldw,
-                              const void *g, int esize, cudaStream_t s)
+                              int esize, cudaStream_t s)
 {
-    return esize == 2 ? product<false>(what, a, h, ldh, w, ldw, g, s) : product<true>(what, a, h, ldh, w, ldw, g, s);
+    return esize == 2 ? product<false>(what, a, h, ldh, w, ldw, s) : product<true>(what, a, h, ldh, w, ldw, s);
 }
 
 }  // namespace uly

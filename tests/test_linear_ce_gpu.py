@@ -2,12 +2,15 @@
 
 Tolerances count roundings, u = 2^-24.  A product over K terms in fp32 is off
 by at most 2 K u of the sum of its absolute terms (2: an accumulation may
-truncate).  So a logit is off by d_r <= 2 D u max_v <|h_r|, |w_v|>, a
-probability by the factor exp(2 d_r) and a row's loss by 2 d_r, plus 32 u of
-the values themselves (exponential, sums of tile partials, logarithm).  The
-gradient of the logits, g, is rounded for the products: in bf16 twice (e to
-fp16, 2^-11, or 2^-25 of its tile's largest; g to bf16, 2^-8), in fp32 by less
-than 8 u.  Each gradient adds its product's error and its own rounding.
+truncate).  So a logit is off by d_r <= 2 D u max_v <|h_r|, |w_v|>, and
+by 2 u of itself more where it is taken in units of log2; a probability by the
+factor exp(2 d_r) and a row's loss by 2 d_r, plus 32 u of the values themselves
+(exponential, sums of tile partials, logarithm).  The operands of the gradient
+products are rounded: in bf16 the gradient of the logits times the softmax's
+denominator S by 2^-8, with a scale in place of 1 / S that is off by 2^-8 at
+most and makes up for it at the label, and for dW h times that scale by 2^-8 too;
+in fp32 by less than 8 u altogether.  Each gradient adds its product's error and
+its own rounding.
 """
 import numpy as np
 import pytest
@@ -63,7 +66,7 @@ def compare(outs, grads, h, w, labels, what, norm=True):
     rows = np.where(good[:, None], h64.reshape(-1, h64.shape[-1]), 0.0)
     D, V = w64.shape[1], w64.shape[0]
     size = (np.abs(rows) @ np.abs(w64).T).max(1)          # of a logit's terms
-    d = 2 * D * U * size                                  # of a logit
+    d = (2 * D + 2) * U * size                            # of a logit
     tol_row = 2 * d + 32 * U * (1 + size)
     tol_loss = tol_row[good].max() if good.any() else 0.0
     assert np.abs(sl - per).max() <= tol_loss + 2 * U * np.abs(per).max(), (what, sl, per, tol_loss)
@@ -74,10 +77,11 @@ def compare(outs, grads, h, w, labels, what, norm=True):
     p[np.arange(len(y))[good], y[good]] = 1 - p[good, y[good]]
     half = torch.finfo(h.dtype).eps / 2
     tag = "bf16" if h.dtype == BF16 else "fp32"
-    rounded = (2.0 ** -8 + 2.0 ** -11) if tag == "bf16" else 8 * U
     # g's error: the probability's, then its rounding
-    dg = (p * np.expm1(2 * d + 16 * U)[:, None] + (2.0 ** -25 if tag == "bf16" else 0.0) * good[:, None]) / T
-    dg += rounded * (np.abs(g) + dg)
+    rounded = np.full(g.shape, 2.0 ** -7 + 2.0 ** -14 if tag == "bf16" else 8 * U)
+    rounded[np.arange(len(y))[good], y[good]] = 8 * U
+    dg0 = p * np.expm1(2 * d + 16 * U)[:, None] / T
+    dg0 += rounded * (np.abs(g) + dg0)
     errs = {}
     for name, got, ref, side in (("dh", grads[0], dh.reshape(-1, D), lambda q: q @ np.abs(w64)),
                                  ("dw", grads[1], dw, lambda q: q.T @ np.abs(rows))):
@@ -85,6 +89,7 @@ def compare(outs, grads, h, w, labels, what, norm=True):
             continue
         got = (full(got.cpu()) if name == "dh" else got.cpu()).double().numpy().reshape(ref.shape)
         K = V if name == "dh" else T
+        dg = dg0 + (2.0 ** -8 * (np.abs(g) + dg0) if name == "dw" and tag == "bf16" else 0.0)  # h / S
         before = side(dg) + 2 * K * U * side(np.abs(g) + dg)
         tol = half * (np.abs(ref) + before) + before + 2.0 ** -133  # the last: below the smallest subnormal step
         assert np.isfinite(got).all(), (what, name)
@@ -183,6 +188,27 @@ def test_large_logits_and_certain_rows(uly, dtype):
     h, w, labels = make(1, 1, 80, 64, 600, dtype, lean=0.0, seed=14, scale=30.0)
     outs, grads = run(uly, h, w, labels)
     compare(outs, grads, h, w, labels, "large logits, wrong labels", norm=False)
+
+
+@pytest.mark.parametrize("level", [[20, 60, -80, 0], [-70, -70, -71, -90], [120, 119.5, 40, -300], [30, -40, 32, 34],
+                                   [0, -200, 0, -50]])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_logits_that_differ_between_columns(uly, level, dtype):
+    """Every 64 columns at a level of their own, from rows that scale it by 0 to 1.2: exponentials
+    within e^33 are kept as they are, others relative to their columns' largest."""
+    D, N = 64, 100
+    g = torch.Generator().manual_seed(17)
+    u = torch.ones(D) / 8
+    at = torch.tensor(level, dtype=torch.float32).repeat_interleave(64)[:, None]
+    w = (at * u + torch.randn(len(at), D, generator=g) / 8)[:250].to(dtype)
+    h = (torch.linspace(0, 1.2, N)[:, None] * u + torch.randn(N, D, generator=g) / 8)[None, None].to(dtype)
+    labels = torch.randint(0, 250, (1, 1, N), generator=g)
+    outs, grads = run(uly, h, w, labels)
+    compare(outs, grads, h, w, labels, f"levels {level}", norm=False)
+    for dh, dw in ((True, False), (False, True), (False, False)):
+        o2, g2 = run(uly, h, w, labels, dh=dh, dw=dw)
+        assert all(bytes_equal(a, b) for a, b in zip(outs, o2))
+        assert all(b is None or bytes_equal(a, b) for a, b in zip(grads, g2))
 
 
 @pytest.mark.parametrize("rows,dtype", [(8192, BF16), (8193, BF16), (8194, BF16), (20000, BF16), (9000, FP32),
