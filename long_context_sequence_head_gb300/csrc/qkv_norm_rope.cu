@@ -257,7 +257,8 @@ __device__ __forceinline__ void store_row(T *row, int lo, int hi, const Raw &v)
 // A place in a warp's list of runs.  Unit u (a token, or a part of a token's
 // runs) goes to warp u modulo the number of warps, so that all warps work on
 // neighbouring memory.  A unit's runs are kRun rows each of the token's list:
-// Q's heads, then K's, then V's.
+// Q's heads, then K's, then V's.  The first `whole` tokens are units of their
+// own, the others come in parts.
 template <typename S>
 struct Cursor {
     uint32_t u, units, stride;
@@ -265,7 +266,7 @@ struct Cursor {
     Token k;
 
     __device__ __forceinline__ Cursor(const NormRopeParams &p, uint32_t warp, uint32_t warps)
-        : u(warp), units(static_cast<uint32_t>(p.tokens * p.splits)), stride(warps)
+        : u(warp), units(static_cast<uint32_t>(p.whole + (p.tokens - p.whole) * p.splits)), stride(warps)
     {
         enter(p);
     }
@@ -273,11 +274,17 @@ struct Cursor {
     __device__ __forceinline__ bool more() const { return u < units; }
     __device__ __forceinline__ void enter(const NormRopeParams &p)
     {
-        const uint32_t splits = p.splits, m = splits == 1 ? u : u / splits;
+        uint32_t m = u;
+        r = 0;
+        end = p.runs;
+        if (u >= static_cast<uint32_t>(p.whole)) {
+            const uint32_t at = u - static_cast<uint32_t>(p.whole), token = at / p.splits;
+            m = static_cast<uint32_t>(p.whole) + token;
+            r = static_cast<int>(at - token * p.splits) * p.runs_per_split;
+            end = min(p.runs, r + p.runs_per_split);
+        }
         const uint32_t sb = m / static_cast<uint32_t>(p.Np), s = sb / static_cast<uint32_t>(p.B);
         k = Token{m, s * p.Np + (m - sb * p.Np), static_cast<int>(sb - s * p.B)};
-        r = static_cast<int>(u - m * splits) * p.runs_per_split;
-        end = min(p.runs, r + p.runs_per_split);
     }
     // to the next run
     __device__ __forceinline__ void step(const NormRopeParams &p)
@@ -453,7 +460,6 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float2 table[kWarps][kD / 2];
     __shared__ __align__(16) T weights[2][kD];
-    grid_next();
     const int warp = warp_id(), lane = lane_id(), sub = lane / S::kLanes;
     if (kNorm) {
         for (int i = threadIdx.x; i < kD; i += kThreads) {
@@ -622,27 +628,44 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
     }
 }
 
-// dw[i] = sum over the blocks' partials, in block order within each of 32
-// strided runs and then over the runs: the same order on every launch.
+// dw[i] = sum over the blocks' partials: 128 strided runs of them, in block
+// order, then the runs, always in the same order.  A block takes 8 values and
+// has its loads on their way together: 2 us behind the backward, 4 with blocks of
+// 32 values and loads one by one.
+constexpr int kDwCols = 8, kDwRuns = 128;
 template <typename T>
-__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float *__restrict__ partial, int blocks, int d,
-                                                            T *__restrict__ dwq, T *__restrict__ dwk)
+__global__ void __launch_bounds__(kDwCols *kDwRuns) norm_rope_dw_kernel(const float *__restrict__ partial, int blocks,
+                                                                       int d, T *__restrict__ dwq,
+                                                                       T *__restrict__ dwk)
 {
-    __shared__ float run[32][33];
+    __shared__ float run[kDwCols][kDwRuns + 1];
     grid_wait();
-    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32, col = blockIdx.x * 32 + tx;
+    const int tx = threadIdx.x % kDwCols, ty = threadIdx.x / kDwCols;
+    constexpr int kAhead = 6;
     float s = 0.f;
-    for (int b = ty; b < blocks; b += 32)
-        s += partial[static_cast<int64_t>(b) * 2 * d + col];
-    run[ty][tx] = s;
+    for (int b0 = ty; b0 < blocks; b0 += kDwRuns * kAhead) {
+        float v[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int b = b0 + kDwRuns * i;
+            v[i] = b < blocks ? partial[static_cast<int64_t>(b) * 2 * d + blockIdx.x * kDwCols + tx] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            s += v[i];
+    }
+    run[tx][ty] = s;
     __syncthreads();
-    if (ty != 0)
+    if (warp_id() >= kDwCols)
         return;
     s = 0.f;
-    for (int k = 0; k < 32; ++k)
-        s += run[k][tx];
+#pragma unroll
+    for (int k = 0; k < kDwRuns; k += 32)
+        s += run[warp_id()][lane_id() + k];
+    s = row_sum<32>(s);
+    const int col = blockIdx.x * kDwCols + warp_id();
     T *dw = col < d ? dwq : dwk;
-    if (dw == nullptr)
+    if (dw == nullptr || lane_id() != 0)
         return;
     if constexpr (sizeof(T) == 2)
         dw[col % d] = static_cast<T>(pack_bf16x2(s, 0.f) & 0xffffu);
@@ -657,13 +680,31 @@ cudaError_t run(NormRopeParams &p, bool bwd, cudaStream_t s)
     const int runs = (p.Hq + (p.v ? 2 : 1) * p.Hkv + kRun - 1) / kRun;
     p.runs = runs;
     const int64_t resident = static_cast<int64_t>(num_sms()) * (bwd ? kBwdBlocks : kFwdBlocks);
-    // few tokens: a token's runs go to several warps
-    const int splits = static_cast<int>(std::min<int64_t>(runs, (resident * kWarps + p.tokens - 1) / p.tokens));
-    p.runs_per_split = (runs + splits - 1) / splits;
+    // Tokens that are fewer than the warps come in the parts that end first:
+    // rounds of parts x runs of a part.  So do the backward's last tokens, when
+    // every warp has had the same number of whole ones: 2048 tokens of 32 + 8 + 8
+    // heads 25.3 us (parts for as many warps as there are 31.5), 4095 fp32 ones of
+    // 12 + 6 + 6 25.1 (all whole 27.4).  In the forward the parts' angles cost
+    // what their rounds save: 8192 tokens 41.6 us, all whole 40.5.
+    const int64_t warps = resident * kWarps;
+    p.whole = bwd || p.tokens < warps ? p.tokens / warps * warps : p.tokens;
+    const int64_t rest = p.tokens - p.whole;
+    p.runs_per_split = runs;
+    int64_t best = INT64_MAX;
+    for (int64_t k = 1; rest > 0 && k <= std::min<int64_t>(runs, (warps + rest - 1) / rest); ++k) {
+        const int64_t per = (runs + k - 1) / k, parts = (runs + per - 1) / per;
+        const int64_t time = (rest * parts + warps - 1) / warps * per;
+        if (time < best) {
+            best = time;
+            p.runs_per_split = static_cast<int>(per);
+        }
+    }
     p.splits = (runs + p.runs_per_split - 1) / p.runs_per_split;
+    if (p.splits == 1)
+        p.whole = p.tokens;
     p.magic_q = p.Hqp == 1 ? 0u : 0xffffffffu / p.Hqp + 1;
     p.magic_k = p.Hkvp == 1 ? 0u : 0xffffffffu / p.Hkvp + 1;
-    const int64_t grid = std::min<int64_t>((p.tokens * p.splits + kWarps - 1) / kWarps, resident);
+    const int64_t grid = std::min<int64_t>((p.whole + (p.tokens - p.whole) * p.splits + kWarps - 1) / kWarps, resident);
     if (!bwd) {
         auto kernel = norm_rope_fwd_kernel<T, kD, kInter, kNorm>;
         constexpr int smem = Ring<kFwdRing, 1, kFwdRun>::kBytes;
@@ -681,7 +722,7 @@ cudaError_t run(NormRopeParams &p, bool bwd, cudaStream_t s)
     if (e != cudaSuccess)
         return e;
     if (kNorm && (p.dwq || p.dwk))
-        return launch_after(norm_rope_dw_kernel<T>, 2 * kD / 32, 1024, 0, s, p.partial, static_cast<int>(grid), kD,
+        return launch_after(norm_rope_dw_kernel<T>, 2 * kD / kDwCols, kDwCols * kDwRuns, 0, s, p.partial, static_cast<int>(grid), kD,
                             static_cast<T *>(p.dwq), static_cast<T *>(p.dwk));
     return cudaSuccess;
 }

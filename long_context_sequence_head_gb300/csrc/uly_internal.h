@@ -236,8 +236,10 @@ struct NormRopeParams {
     int to_head;
     int half;  // rot / 2
     float eps;
-    // set by the launch: runs of a token, warps per token, runs each takes, and
-    // 2^32 / (H/P) rounded up (0 for H/P = 1)
+    // set by the launch: tokens that are worked on whole, runs of a token, parts
+    // of the other tokens and the runs of a part, and 2^32 / (H/P) rounded up (0
+    // for H/P = 1)
+    int64_t whole;
     int runs, splits, runs_per_split;
     unsigned magic_q, magic_k;
     uint64_t turn[kNormRopeMaxHalf];  // inv_freq / 2 pi as a 64-bit fraction of a turn
