@@ -193,8 +193,8 @@ __global__ void __launch_bounds__(1024) labels_kernel(const int64_t *__restrict_
 
 // Eight values of row `row`, columns [i, i + 8), to the products' layout.
 template <bool kSplit>
-__device__ __forceinline__ void lay8(const void *src, int64_t row, int i, int D, uint16_t *out, int64_t to, int64_t pitch,
-                                     int64_t plane)
+__device__ __forceinline__ void lay8(const void *src, int64_t row, int i, int D, uint16_t *out, int64_t to,
+                                     int64_t pitch, int64_t plane)
 {
     if constexpr (kSplit) {
         float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -405,8 +405,8 @@ Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
         const size_t tiles = static_cast<size_t>((V + kCeTile - 1) / kCeTile) * ((D + kCeTile - 1) / kCeTile);
         if (T > L.rows)
             take(L.acc, sizeof(float) * kCeTileFloats * tiles);
-        take(L.partial, sizeof(float) * kCeTileFloats *
-                            std::max(ce_most_parts(kCeDh, L.rows, D, V), ce_most_parts(kCeDw, L.rows, D, V)));
+        const int parts = std::max(ce_most_parts(kCeDh, L.rows, D, V, esize), ce_most_parts(kCeDw, L.rows, D, V, esize));
+        take(L.partial, sizeof(float) * kCeTileFloats * parts);
     }
     L.total = o;
     return L;

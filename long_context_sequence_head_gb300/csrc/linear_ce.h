@@ -85,7 +85,8 @@ __device__ __forceinline__ void ce_shard(const CeTotals &t, int r, float2 sum)
 {
     if (lane_id() == 0) {
         const long long n = static_cast<long long>(t.good[r]);
-        t.shard_loss[r] = n > 0 ? static_cast<float>((static_cast<double>(sum.x) + sum.y) / static_cast<double>(n)) : 0.f;
+        const double all = static_cast<double>(sum.x) + sum.y;
+        t.shard_loss[r] = n > 0 ? static_cast<float>(all / static_cast<double>(n)) : 0.f;
         t.shard_good[r] = n;
     }
 }
@@ -116,7 +117,7 @@ __device__ __forceinline__ int ce_piece_rows(const CeArgs &a)
 }
 
 // Most tiles that a product may leave in `partial` (host, for the workspace).
-int ce_most_parts(CeProduct what, int rows, int D, int V);
+int ce_most_parts(CeProduct what, int rows, int D, int V, int esize);
 
 // esize: 2 (bf16) or 4 (fp32, the operands as three bf16 planes each).  h: the
 // piece's rows (dW: divided by S); w: the weight; ldh, ldw: row pitches in

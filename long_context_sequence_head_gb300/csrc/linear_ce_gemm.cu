@@ -64,12 +64,14 @@ constexpr int kBars = 2 * kStages + 5;
 constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kWarpStaging + 8 * kBars + 16 + 1024;
 constexpr int kPlanePairs = 6;
 constexpr int kCeMaxDevices = 64;
-constexpr int kMinRun = 8;  // least steps of a run
-// Steps a split must save: a step takes 0.34 us, the runs' tiles and the join 10
-// to 20 us.  Whole calls at 32 / 64 / 128, us: 300 rows x 2048 x 5000 62 / 74 /
-// 72, 1180 x 496 x 3440 52 / 57 / 57, 256 x 352 x 6410 43 / 43 / 64, 6765 x 200 x
-// 3208 110 / 103 / 111.
-constexpr int kSplitGain = 32;
+// Least steps of a run, and steps a split must save: a step takes 0.34 us (fp32:
+// six products, 2 us), the runs' tiles and the join 10 to 20 us.  Whole calls
+// with a gain of 32 / 64 / 128, us: 300 rows x 2048 x 5000 62 / 74 / 72, 1180 x 496
+// x 3440 52 / 57 / 57, 256 x 352 x 6410 43 / 43 / 64, 6765 x 200 x 3208 110 / 103 /
+// 111; in fp32 with runs of 2 and a gain of 12 / 8 and 32: 32 rows x 256 x 1000
+// 52 / 78, 32 x 1096 x 1656 84 / 129, 3000 x 448 x 2000 146 / 178.
+__host__ __device__ constexpr int min_run(bool split) { return split ? 2 : 8; }
+__host__ __device__ constexpr int split_gain(bool split) { return split ? 12 : 32; }
 
 template <int kWhat, bool kSplit>
 constexpr int kChunkSteps = kSplit ? 1 : (kWhat == kCeLogits ? 8 : 64);
@@ -83,17 +85,17 @@ struct Plan {
 };
 
 // Runs of each of the tiles left over from full rounds; 0: those are done whole too.
-__host__ __device__ inline int ce_runs(int64_t tiles, int kb, int pairs)
+__host__ __device__ inline int ce_runs(int64_t tiles, int kb, int pairs, bool split)
 {
     const int rem = static_cast<int>(tiles % pairs);
     if (rem == 0)
         return 0;
     int runs = pairs / rem;
-    runs = runs < kb / kMinRun ? runs : kb / kMinRun;
-    return runs > 1 && kb - kb / runs > kSplitGain ? runs : 0;
+    runs = runs < kb / min_run(split) ? runs : kb / min_run(split);
+    return runs > 1 && kb - kb / runs > split_gain(split) ? runs : 0;
 }
 
-template <int kWhat>
+template <int kWhat, bool kSplit>
 __device__ __forceinline__ Plan make_plan(const CeArgs &a, int cnt, int pairs)
 {
     Plan p;
@@ -105,7 +107,7 @@ __device__ __forceinline__ Plan make_plan(const CeArgs &a, int cnt, int pairs)
     // D in equal tiles: 776 as four of 224 instead of three of 256 and one of 8
     p.cols = kWhat == kCeLogits ? kCeTile : ((N + p.nt - 1) / p.nt + 31) / 32 * 32;
     const int tiles = p.mt * p.nt;
-    p.runs = kWhat == kCeLogits ? 0 : ce_runs(tiles, p.kb, pairs);  // a softmax needs whole sums
+    p.runs = kWhat == kCeLogits ? 0 : ce_runs(tiles, p.kb, pairs, kSplit);  // a softmax needs whole sums
     p.rem = p.runs > 0 ? tiles % pairs : 0;
     p.whole = tiles - p.rem;
     return p;
@@ -403,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grid_wait();
     grid_next();
     const int cnt = ce_piece_rows(a);
-    Plan plan = make_plan<kWhat>(a, cnt, pairs);
+    Plan plan = make_plan<kWhat, kSplit>(a, cnt, pairs);
     if (cnt == 0 && (kWhat != kCeDw || a.base > 0))
         plan.whole = plan.rem = 0;  // nothing to do; dW without any row is written as zeros by the first piece
     constexpr int kPerStep = kSplit ? kPlanePairs : 1;
@@ -631,7 +633,7 @@ __global__ void __launch_bounds__(kJoinThreads<kSplit, kGroups>) ce_join_kernel(
     const int cnt = ce_piece_rows(a);
     if (cnt == 0)
         return;
-    const Plan p = make_plan<kWhat>(a, cnt, pairs);
+    const Plan p = make_plan<kWhat, kSplit>(a, cnt, pairs);
     const int part = warp_id() % kParts, group = warp_id() / kParts, lane = lane_id();
     for (int item = blockIdx.x; item < p.rem * 2 * kEpiWarps; item += gridDim.x) {
         const int slab = item % kEpiWarps, cta = item / kEpiWarps % 2, split = item / (2 * kEpiWarps);
@@ -769,14 +771,15 @@ cudaError_t launch(const CeArgs &a, const CUtensorMap &ta, const CUtensorMap &tb
         const int K = kWhat == kCeDh ? a.V : a.rows, kb = (K + kCeStep - 1) / kCeStep;
         const int nt = (a.D + kCeTile - 1) / kCeTile;
         const int tiles = ((kWhat == kCeDh ? a.rows : a.V) + kCeTile - 1) / kCeTile * nt;
-        int most = kb > kSplitGain ? std::min(tiles, pairs / 2) : 0;
-        if (kWhat == kCeDw && ce_runs(tiles, kb, pairs) == 0)
+        int most = kb > split_gain(kSplit) ? std::min(tiles, pairs / 2) : 0;
+        if (kWhat == kCeDw && ce_runs(tiles, kb, pairs, kSplit) == 0)
             most = 0;
         const int items = most * 2 * kEpiWarps;
         constexpr int kMany = kJoinGroups<kSplit>;
         if (e == cudaSuccess && items > 0)
             e = items <= 2 * num_sms()
-                    ? launch_after(ce_join_kernel<kWhat, kSplit, kMany>, items, kJoinThreads<kSplit, kMany>, 0, s, a, pairs)
+                    ? launch_after(ce_join_kernel<kWhat, kSplit, kMany>, items, kJoinThreads<kSplit, kMany>, 0, s, a,
+                                   pairs)
                     : launch_after(ce_join_kernel<kWhat, kSplit, 1>, std::min(items, 8 * num_sms()),
                                    kJoinThreads<kSplit, 1>, 0, s, a, pairs);
     }
@@ -808,11 +811,14 @@ cudaError_t product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh,
 
 }  // namespace
 
-int ce_most_parts(CeProduct what, int rows, int D, int V)
+int ce_most_parts(CeProduct what, int rows, int D, int V, int esize)
 {
     const int64_t mt = ((what == kCeDw ? V : rows) + kCeTile - 1) / kCeTile, nt = (D + kCeTile - 1) / kCeTile;
     const int64_t kb = ((what == kCeDw ? rows : V) + kCeStep - 1) / kCeStep;
-    return kb <= kSplitGain ? 0 : static_cast<int>(std::min<int64_t>(kCeMaxPairs, mt * nt * (kb / kMinRun)));
+    const bool split = esize == 4;
+    if (kb <= split_gain(split))
+        return 0;
+    return static_cast<int>(std::min<int64_t>(kCeMaxPairs, mt * nt * (kb / min_run(split))));
 }
 
 cudaError_t launch_ce_product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh, const void *w, int64_t ldw,

@@ -722,8 +722,8 @@ cudaError_t run(NormRopeParams &p, bool bwd, cudaStream_t s)
     if (e != cudaSuccess)
         return e;
     if (kNorm && (p.dwq || p.dwk))
-        return launch_after(norm_rope_dw_kernel<T>, 2 * kD / kDwCols, kDwCols * kDwRuns, 0, s, p.partial, static_cast<int>(grid), kD,
-                            static_cast<T *>(p.dwq), static_cast<T *>(p.dwk));
+        return launch_after(norm_rope_dw_kernel<T>, 2 * kD / kDwCols, kDwCols * kDwRuns, 0, s, p.partial,
+                            static_cast<int>(grid), kD, static_cast<T *>(p.dwq), static_cast<T *>(p.dwk));
     return cudaSuccess;
 }
 
