@@ -429,10 +429,11 @@ uly_status ulysses_sharded_ce_loss(const void *logits, const int64_t *labels, vo
  * same shifted labels, per-shard means and good-token-weighted total, of
  *   logits[row][v] = <hidden[row], weight[v]>
  * which are formed in pieces of rows with a label (as many as 2.5 GB of
- * workspace hold, at least 1024, at most 65536) and never kept: a long sequence's logits and their gradient outweigh everything else
- * the step holds (at 65,536 tokens and a vocabulary of 151,936, 20 GB each in
- * bf16).  Rows without a label (ignored ones, and the last of each sequence)
- * take no part: their hidden values are not read.
+ * workspace hold, at least 1024, at most 65536) and never kept: a long
+ * sequence's logits and their gradient outweigh everything else the step holds
+ * (at 65,536 tokens and a vocabulary of 151,936, 20 GB each in bf16).  Rows
+ * without a label (ignored ones, and the last of each sequence) take no part:
+ * their hidden values are not read.
  *
  * hidden     : device, [P][B][N/P][D].      weight : device, [V][D].
  * labels     : as in ulysses_sharded_ce_loss.
@@ -445,9 +446,9 @@ uly_status ulysses_sharded_ce_loss(const void *logits, const int64_t *labels, vo
  * Products are accumulated in fp32; softmax and loss are fp32.  bf16: the
  * operands of the two gradient products, the softmax's numerators and, for
  * dweight, the hidden rows divided by its denominators, are rounded to bf16;
- * each gradient is rounded to bf16 once.  fp32: operands are taken
- * as three bf16 parts each, off by less than 2^-26 of a value (values above
- * 3.39e38, bf16's largest, count as infinite).
+ * each gradient is rounded to bf16 once.  fp32: operands are taken as three
+ * bf16 parts each, off by less than 2^-26 of a value (values above 3.39e38,
+ * bf16's largest, count as infinite).
  * D * element size a multiple of 16 bytes, D <= 65536, V <= 2^21
  * (ULY_ERR_UNSUPPORTED otherwise); N % P == 0.
  */

@@ -15,9 +15,10 @@ constexpr int kCeTile = 256;
 constexpr int kCeStep = 64;
 constexpr int kCeStatCols = 64;  // columns behind one (c, s) of the softmax
 constexpr int kCeMaxPairs = 80;
-// Logits within +-2^kCeFree after the exponential need no maximum taken out:
-// sums of 2^21 of them, and their products with anything below 2^58, stay
-// within fp32, and what lies 2^-78 below the smallest such maximum is lost.
+// Columns whose largest exponential lies within 2^+-kCeFree need no maximum taken
+// out: sums of 2^21 such, and their products with values below 2^58, stay within
+// fp32; exponentials are lost 2^-78 below the least such maximum, and of h / S
+// values of h below 2^-57 (in fp32 their last 16 bits below 2^-33).
 constexpr float kCeFree = 48.f;
 // floats a pair leaves for one tile
 constexpr int64_t kCeTileFloats = static_cast<int64_t>(kCeTile) * kCeTile;
