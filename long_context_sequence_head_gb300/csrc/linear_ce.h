@@ -52,6 +52,7 @@ struct CeArgs {
     int stat_tiles;
     float *target;          // [rows] logits of the labels
     float *row_scale;       // [rows] 1 / S
+    int h_planes;           // bf16: parts that h' has in dW, 1 or 2
     int keep;               // with a gradient: keep e
     void *dh, *dw;
     float *acc;             // dW over the pieces, in tiles (see tile_slot)

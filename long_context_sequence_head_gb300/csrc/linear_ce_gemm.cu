@@ -408,7 +408,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Plan plan = make_plan<kWhat, kSplit>(a, cnt, pairs);
     if (cnt == 0 && (kWhat != kCeDw || a.base > 0))
         plan.whole = plan.rem = 0;  // nothing to do; dW without any row is written as zeros by the first piece
-    constexpr int kPerStep = kSplit ? kPlanePairs : 1;
+    // loads and products of a step
+    const int per_step = kSplit ? kPlanePairs : (kWhat == kCeDw ? a.h_planes : 1);
     // a narrow MN-major B: one block of 64 columns per CTA instead of two
     const bool second_block = plan.cols / 2 > 64;
     const uint32_t b_bytes = second_block ? kOperandBytes : kOperandBytes / 2;
@@ -427,10 +428,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 n0 += cta * (plan.cols / 2);
                 for (int k = u.k0; ok && k < u.k1; ++k) {
 #pragma unroll 1
-                    for (int pp = 0; pp < kPerStep; ++pp, ++it) {
-                        // plane products, smallest first: (1,3) (3,1) (2,2) (1,2) (2,1) (1,1)
+                    for (int pp = 0; pp < per_step; ++pp, ++it) {
+                        // plane products, smallest first: (1,3) (3,1) (2,2) (1,2) (2,1) (1,1); bf16: (1,2) (1,1)
                         const int pa = kSplit ? (0x021010 >> (4 * (5 - pp))) & 15 : 0;
-                        const int pb = kSplit ? (0x201100 >> (4 * (5 - pp))) & 15 : 0;
+                        const int pb = kSplit ? (0x201100 >> (4 * (5 - pp))) & 15 : per_step - 1 - pp;
                         const int s = it % kStages;
                         if (*abort_flag || !mbar_wait(&empty[s], ((it / kStages) & 1) ^ 1, w, 0xa1)) {
                             ok = false;
@@ -477,9 +478,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t it = 0, chunk = 0;
             bool ok = true;
             while (ok && units.next(u)) {
-                int left = (u.k1 - u.k0) * kPerStep;  // loads of this unit
+                int left = (u.k1 - u.k0) * per_step;  // loads of this unit
                 while (ok && left > 0) {
-                    constexpr int most = kChunkSteps<kWhat, kSplit> * kPerStep;
+                    const int most = kChunkSteps<kWhat, kSplit> * per_step;
                     const int n = left < most ? left : most;  // loads of this accumulation
                     const uint32_t acc = chunk & 1;
                     if (*abort_flag || !mbar_wait_cluster(&acc_empty[acc], ((chunk >> 1) & 1) ^ 1, w, 0xa2)) {
@@ -804,7 +805,7 @@ cudaError_t product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh,
         return ok ? launch<kCeDh, kSplit>(a, ta, tb, te, s) : cudaErrorInvalidValue;
     default:
         ok = make_map(&ta, a.e, a.V, a.rows, a.ldg, planes, kCeStep) &&
-             make_map(&tb, h, a.D, a.rows, ldh, planes, kCeStep);
+             make_map(&tb, h, a.D, a.rows, ldh, kSplit ? planes : a.h_planes, kCeStep);
         return ok ? launch<kCeDw, kSplit>(a, ta, tb, te, s) : cudaErrorInvalidValue;
     }
 }

@@ -8,7 +8,8 @@ factor exp(2 d_r) and a row's loss by 2 d_r, plus 32 u of the values themselves
 (exponential, sums of tile partials, logarithm).  The operands of the gradient
 products are rounded: in bf16 the gradient of the logits times the softmax's
 denominator S by 2^-8, with a scale in place of 1 / S that is off by 2^-8 at
-most and makes up for it at the label, and for dW h times that scale by 2^-8 too;
+most and makes up for it at the label, and for dW h times that scale by 2^-8 too
+(calls of up to 128 rows: 2^-16);
 in fp32 by less than 8 u altogether.  Each gradient adds its product's error and
 its own rounding.
 """
@@ -89,7 +90,8 @@ def compare(outs, grads, h, w, labels, what, norm=True):
             continue
         got = (full(got.cpu()) if name == "dh" else got.cpu()).double().numpy().reshape(ref.shape)
         K = V if name == "dh" else T
-        dg = dg0 + (2.0 ** -8 * (np.abs(g) + dg0) if name == "dw" and tag == "bf16" else 0.0)  # h / S
+        scaled = 2.0 ** (-16 if len(y) <= 128 else -8)  # h / S
+        dg = dg0 + (scaled * (np.abs(g) + dg0) if name == "dw" and tag == "bf16" else 0.0)
         before = side(dg) + 2 * K * U * side(np.abs(g) + dg)
         tol = half * (np.abs(ref) + before) + before + 2.0 ** -133  # the last: below the smallest subnormal step
         assert np.isfinite(got).all(), (what, name)
