@@ -359,7 +359,8 @@ __device__ __noinline__ void totals_by_warp(const CeTotals &t)
     ce_total(t);
 }
 
-template <int kWhat, bool kSplit>
+// kParts: of B, in bf16.
+template <int kWhat, bool kSplit, int kParts>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ce_product_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                       const __grid_constant__ CUtensorMap te, const __grid_constant__ CeArgs a, const WaitCfg w)
@@ -409,7 +410,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (cnt == 0 && (kWhat != kCeDw || a.base > 0))
         plan.whole = plan.rem = 0;  // nothing to do; dW without any row is written as zeros by the first piece
     // loads and products of a step
-    const int per_step = kSplit ? kPlanePairs : (kWhat == kCeDw ? a.h_planes : 1);
+    constexpr int per_step = kSplit ? kPlanePairs : kParts;
     // a narrow MN-major B: one block of 64 columns per CTA instead of two
     const bool second_block = plan.cols / 2 > 64;
     const uint32_t b_bytes = second_block ? kOperandBytes : kOperandBytes / 2;
@@ -417,9 +418,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == kEpiWarps) {
         // ------------------------------------------------ loads
         if (lane == 0) {
+            // A step's instructions are what a pair can lose time on: one
+            // thread loads and one issues, and a step of 64 is 512 cycles of
+            // products.  So stages and parities are counted, addresses kept.
+            const uint32_t bar0 = cluster_addr(&full[0], 0);
             Units units(plan, pair, pairs);
             Unit u;
-            uint32_t it = 0;
+            uint32_t it = 0, s = 0, parity = 1;
             bool ok = true;
             while (ok && units.next(u)) {
                 int m0, n0;
@@ -432,14 +437,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         // plane products, smallest first: (1,3) (3,1) (2,2) (1,2) (2,1) (1,1); bf16: (1,2) (1,1)
                         const int pa = kSplit ? (0x021010 >> (4 * (5 - pp))) & 15 : 0;
                         const int pb = kSplit ? (0x201100 >> (4 * (5 - pp))) & 15 : per_step - 1 - pp;
-                        const int s = it % kStages;
-                        if (*abort_flag || !mbar_wait(&empty[s], ((it / kStages) & 1) ^ 1, w, 0xa1)) {
+                        if (!mbar_try_wait(&empty[s], parity) &&
+                            (*abort_flag || !mbar_wait(&empty[s], parity, w, 0xa1))) {
                             ok = false;
                             break;
                         }
                         if (cta == 0)
                             mbar_expect_tx(&full[s], 2 * (kOperandBytes + b_bytes));
-                        const uint32_t bar = cluster_addr(&full[s], 0);
+                        const uint32_t bar = bar0 + 8 * s;
                         uint8_t *sa = smem + s * kStageBytes, *sb = sa + kOperandBytes;
                         const int kc = k * kCeStep;
                         if (kWhat == kCeDw) {
@@ -454,6 +459,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                 tma_load_3d_pair(sb + kOperandBytes / 2, &tb, bar, n0 + 64, kc, pb);
                         } else {
                             tma_load_3d_pair(sb, &tb, bar, kc, n0, pb);
+                        }
+                        if (++s == kStages) {
+                            s = 0;
+                            parity ^= 1;
                         }
                     }
                 }
@@ -475,7 +484,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t idesc = idesc_bf16(256, plan.cols, kWhat == kCeDw, kWhat != kCeLogits);
             Units units(plan, pair, pairs);
             Unit u;
-            uint32_t it = 0, chunk = 0;
+            uint32_t s = 0, parity = 0, chunk = 0;
+            // operands of a step's first instruction, of the first stage
+            const uint64_t da0 = kWhat == kCeDw ? desc_sw128(smem_u32(smem), kOperandBytes / 2, 1024)
+                                                : desc_sw128(smem_u32(smem), 16, 1024);
+            const uint64_t db0 = kWhat != kCeLogits
+                                     ? desc_sw128(smem_u32(smem) + kOperandBytes, kOperandBytes / 2, 1024)
+                                     : desc_sw128(smem_u32(smem) + kOperandBytes, 16, 1024);
+            constexpr uint32_t a_next = (kWhat == kCeDw ? 2048 : 32) / 16, b_next = (kWhat != kCeLogits ? 2048 : 32) / 16;
             bool ok = true;
             while (ok && units.next(u)) {
                 int left = (u.k1 - u.k0) * per_step;  // loads of this unit
@@ -488,24 +504,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         break;
                     }
                     tc_fence_after();
-                    for (int i = 0; i < n; ++i, ++it) {
-                        const int s = it % kStages;
-                        if (!mbar_wait(&full[s], (it / kStages) & 1, w, 0xa3)) {
+                    for (int i = 0; i < n; ++i) {
+                        if (!mbar_wait(&full[s], parity, w, 0xa3)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kOperandBytes;
+                        const uint64_t da = da0 + s * (kStageBytes / 16), db = db0 + s * (kStageBytes / 16);
 #pragma unroll
-                        for (int kk = 0; kk < kCeStep / 16; ++kk) {
-                            const uint64_t da = kWhat == kCeDw ? desc_sw128(sa + kk * 2048, kOperandBytes / 2, 1024)
-                                                               : desc_sw128(sa + kk * 32, 16, 1024);
-                            const uint64_t db = kWhat != kCeLogits
-                                                    ? desc_sw128(sb + kk * 2048, kOperandBytes / 2, 1024)
-                                                    : desc_sw128(sb + kk * 32, 16, 1024);
-                            mma_ss_pair(tbase + acc * 256, da, db, idesc, (i > 0 || kk > 0) ? 1u : 0u);
-                        }
+                        for (int kk = 0; kk < kCeStep / 16; ++kk)
+                            mma_ss_pair(tbase + acc * 256, da + kk * a_next, db + kk * b_next, idesc,
+                                        (i > 0 || kk > 0) ? 1u : 0u);
                         mma_commit_pair(&empty[s]);
+                        if (++s == kStages) {
+                            s = 0;
+                            parity ^= 1;
+                        }
                     }
                     if (!ok)
                         break;
@@ -729,11 +743,11 @@ bool make_exp_map(CUtensorMap *map, const CeArgs &a, int planes)
                   1, 64, 32);
 }
 
-template <int kWhat, bool kSplit>
+template <int kWhat, bool kSplit, int kParts = 1>
 cudaError_t launch(const CeArgs &a, const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &te,
                    cudaStream_t s)
 {
-    auto kernel = ce_product_kernel<kWhat, kSplit>;
+    auto kernel = ce_product_kernel<kWhat, kSplit, kParts>;
     // Pairs resident at once (the schedule gives each an equal share), asked
     // for once per device; two threads that ask at the same time find the same.
     static std::atomic<int> known[kCeMaxDevices];
@@ -806,7 +820,10 @@ cudaError_t product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh,
     default:
         ok = make_map(&ta, a.e, a.V, a.rows, a.ldg, planes, kCeStep) &&
              make_map(&tb, h, a.D, a.rows, ldh, kSplit ? planes : a.h_planes, kCeStep);
-        return ok ? launch<kCeDw, kSplit>(a, ta, tb, te, s) : cudaErrorInvalidValue;
+        if (!ok)
+            return cudaErrorInvalidValue;
+        return !kSplit && a.h_planes == 2 ? launch<kCeDw, kSplit, kSplit ? 1 : 2>(a, ta, tb, te, s)
+                                          : launch<kCeDw, kSplit>(a, ta, tb, te, s);
     }
 }
 
