@@ -8,16 +8,18 @@
 // one tile is written out while the next is formed.  A pair reads half of what
 // two single CTAs would: 64 bytes a clock and SM from L2 at full rate.  The
 // operands come as they lie: a matrix whose rows run along the contraction is
-// K-major, one whose rows run along the output (W in dh; g and h in dW) is
+// K-major, one whose rows run along the output (W in dh; e and h in dW) is
 // MN-major.
 //
 // Measured (5,734 rows with labels, D = 2560, V = 151,936, bf16): logits 2.57
-// ms, dh 2.47, dW 2.41, that is 1.74 to 1.85 PFLOP/s against 1.90 of the
+// ms, dh 2.55, dW 2.41, that is 1.74 to 1.85 PFLOP/s against 1.90 of the
 // library's product in a burst; back to back the card's power limit sets the
-// clock (the same products of a constant matrix take 2.1 ms).  A step of 64
-// takes 343 ns, which is 14 TB/s from L2: at D = 776 and V = 50,257 narrower
-// tiles (224 columns) do not shorten it, and the products run at 0.66 to 0.75
-// of the tensor cores' rate.
+// clock (the same products of a constant matrix take 2.1 ms).  At D = 776 and V =
+// 50,257 (4,830 rows) the tensor cores are busy 0.64 to 0.76 of 291, 294 and 266
+// us: a step of 64 brings 32 KB to every SM, which at 64 bytes a clock takes the
+// 512 clocks of its products.  With half the products issued the three take 269,
+// 311 and 252 us, with half the loads 251, 242 and 248; narrower tiles (224
+// columns) and a sixth stage change nothing.
 //
 // Warps 0-15 write results out (TMEM lane quarter warp % 4, columns 64 (warp /
 // 4) ..): the logits' exponentials take longer than a short contraction's
@@ -148,7 +150,7 @@ struct Units {
 
 // Tile order.  Logits: rows fastest, so that a round over the pairs reads a
 // few column panels of W once against all rows, which stay in L2.  dh and dW:
-// columns (D) fastest, so that g, the large operand, is read once a round.
+// columns (D) fastest, so that e, the large operand, is read once a round.
 template <int kWhat>
 __device__ __forceinline__ void tile_origin(const Plan &p, int tile, int &m0, int &n0)
 {
