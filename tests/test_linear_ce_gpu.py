@@ -117,6 +117,8 @@ CASES = [
     (2, 1, 700, 264, 2049, BF16),   # several row tiles, column tiles and products of 64
     (1, 1, 65, 1032, 4099, BF16),
     (1, 1, 513, 256, 256, BF16),    # whole tiles and one row more
+    (2, 1, 128, 328, 1500, BF16),   # the most rows whose h / S has two parts, and one more
+    (1, 1, 129, 328, 1500, BF16),
 ]
 
 
@@ -163,6 +165,26 @@ def test_nan_rows_without_a_label_touch_nothing(uly, dtype):
     assert float(grads[0].cpu()[sh == -100].abs().max()) == 0.0
 
 
+@pytest.mark.parametrize("N", [24, 300])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_a_row_that_is_not_finite_stays_one_row(uly, dtype, bad, N):
+    """A NaN or an infinity in a row with a label: its loss, its shard's and the total are NaN, and so
+    are its dh and dW; the other rows' dh are as without it."""
+    h, w, labels = make(2, 1, N, 72, 333, dtype, ignore=0.0, seed=23)
+    _, clean = run(uly, h, w, labels)
+    h[1, 0, 3, 5] = bad
+    outs, grads = run(uly, h, w, labels)
+    assert torch.isfinite(outs[0][0]) and torch.isnan(outs[0][1]) and torch.isnan(outs[2]).all()
+    dh, dw = grads[0].cpu().reshape(N, -1), grads[1].cpu()
+    row = N // 2 + 3
+    assert torch.isnan(dh[row]).all()
+    others = [i for i in range(N) if i != row]
+    assert bytes_equal(dh[others], clean[0].cpu().reshape(N, -1)[others])
+    assert torch.isnan(dw[:, 5]).all()
+    assert uly.ulysses_get_device_status()[0] == 0
+
+
 def test_a_shard_without_labels_and_invalid_labels(uly):
     h, w, labels = make(4, 1, 64, 64, 100, BF16, ignore=0.0, seed=11)
     labels[1] = -100
@@ -194,11 +216,11 @@ def test_large_logits_and_certain_rows(uly, dtype):
 
 @pytest.mark.parametrize("level", [[20, 60, -80, 0], [-70, -70, -71, -90], [120, 119.5, 40, -300], [30, -40, 32, 34],
                                    [0, -200, 0, -50]])
-@pytest.mark.parametrize("dtype", [BF16, FP32])
-def test_logits_that_differ_between_columns(uly, level, dtype):
+@pytest.mark.parametrize("N,dtype", [(100, BF16), (200, BF16), (100, FP32)])
+def test_logits_that_differ_between_columns(uly, level, N, dtype):
     """Every 64 columns at a level of their own, from rows that scale it by 0 to 1.2: exponentials
     within e^33 are kept as they are, others relative to their columns' largest."""
-    D, N = 64, 100
+    D = 64
     g = torch.Generator().manual_seed(17)
     u = torch.ones(D) / 8
     at = torch.tensor(level, dtype=torch.float32).repeat_interleave(64)[:, None]
