@@ -46,7 +46,11 @@
 //
 // fp32 (kSplit): every operand is three bf16 planes (x = x1 + x2 + x3 up to
 // 2^-26 of x) and a product is the six plane products above 2^-24, smallest
-// first; an accumulator takes 64 values of the contraction (24 instructions).
+// first; an accumulator takes 64 values of the contraction (24 instructions).  A
+// step's planes are loaded once for all six: the first two of A and B have two
+// stages, the third, which the first two products alone use, one.  With loads of
+// their own for every product the call of 2048 rows x 1024 x 32,000 took 1.54 ms
+// instead of 1.32, 4096 x 2048 x 32,000 5.94 instead of 5.10.
 #include <atomic>
 
 #include "linear_ce.h"
@@ -64,7 +68,7 @@ constexpr int kCols = kCeStatCols;                       // columns per writing 
 constexpr int kWarpStaging = 32 * 128;                   // 32 rows of 128 bytes
 constexpr int kBars = 2 * kStages + 5;
 constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kWarpStaging + 8 * kBars + 16 + 1024;
-constexpr int kPlanePairs = 6;
+constexpr int kThird = 2;  // fp32: barrier of the third planes' stage, behind those of the two other stages
 constexpr int kCeMaxDevices = 64;
 // Least steps of a run, and steps a split must save: a step takes 0.34 us (fp32:
 // six products, 2 us), the runs' tiles and the join 10 to 20 us.  Whole calls
@@ -74,6 +78,8 @@ constexpr int kCeMaxDevices = 64;
 // 52 / 78, 32 x 1096 x 1656 84 / 129, 3000 x 448 x 2000 146 / 178.
 __host__ __device__ constexpr int min_run(bool split) { return split ? 2 : 8; }
 __host__ __device__ constexpr int split_gain(bool split) { return split ? 12 : 32; }
+
+static_assert(kStages * 2 >= 10 && kStages > kThird, "fp32: ten operands of a step and the next");
 
 template <int kWhat, bool kSplit>
 constexpr int kChunkSteps = kSplit ? 1 : (kWhat == kCeLogits ? 8 : 64);
@@ -411,8 +417,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Plan plan = make_plan<kWhat, kSplit>(a, cnt, pairs);
     if (cnt == 0 && (kWhat != kCeDw || a.base > 0))
         plan.whole = plan.rem = 0;  // nothing to do; dW without any row is written as zeros by the first piece
-    // loads and products of a step
-    constexpr int per_step = kSplit ? kPlanePairs : kParts;
     // a narrow MN-major B: one block of 64 columns per CTA instead of two
     const bool second_block = plan.cols / 2 > 64;
     const uint32_t b_bytes = second_block ? kOperandBytes : kOperandBytes / 2;
@@ -424,6 +428,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // thread loads and one issues, and a step of 64 is 512 cycles of
             // products.  So stages and parities are counted, addresses kept.
             const uint32_t bar0 = cluster_addr(&full[0], 0);
+            auto ready = [&](int i, uint32_t par) {
+                return mbar_try_wait(&empty[i], par) || (!*abort_flag && mbar_wait(&empty[i], par, w, 0xa1));
+            };
+            auto load_a = [&](uint8_t *to, uint32_t bar, int m, int kc, int plane) {
+                if (kWhat == kCeDw) {
+                    tma_load_3d_pair(to, &ta, bar, m, kc, plane);
+                    tma_load_3d_pair(to + kOperandBytes / 2, &ta, bar, m + 64, kc, plane);
+                } else {
+                    tma_load_3d_pair(to, &ta, bar, kc, m, plane);
+                }
+            };
+            auto load_b = [&](uint8_t *to, uint32_t bar, int n, int kc, int plane) {
+                if (kWhat != kCeLogits) {
+                    tma_load_3d_pair(to, &tb, bar, n, kc, plane);
+                    if (second_block)
+                        tma_load_3d_pair(to + kOperandBytes / 2, &tb, bar, n + 64, kc, plane);
+                } else {
+                    tma_load_3d_pair(to, &tb, bar, kc, n, plane);
+                }
+            };
             Units units(plan, pair, pairs);
             Unit u;
             uint32_t it = 0, s = 0, parity = 1;
@@ -434,50 +458,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 m0 += cta * kHalf;
                 n0 += cta * (plan.cols / 2);
                 for (int k = u.k0; ok && k < u.k1; ++k) {
-#pragma unroll 1
-                    for (int pp = 0; pp < per_step; ++pp, ++it) {
-                        // plane products, smallest first: (1,3) (3,1) (2,2) (1,2) (2,1) (1,1); bf16: (1,2) (1,1)
-                        const int pa = kSplit ? (0x021010 >> (4 * (5 - pp))) & 15 : 0;
-                        const int pb = kSplit ? (0x201100 >> (4 * (5 - pp))) & 15 : per_step - 1 - pp;
-                        if (!mbar_try_wait(&empty[s], parity) &&
-                            (*abort_flag || !mbar_wait(&empty[s], parity, w, 0xa1))) {
-                            ok = false;
+                    const int kc = k * kCeStep;
+                    if constexpr (kSplit) {
+                        ok = ready(s, parity);
+                        if (!ok)
                             break;
-                        }
                         if (cta == 0)
-                            mbar_expect_tx(&full[s], 2 * (kOperandBytes + b_bytes));
-                        const uint32_t bar = bar0 + 8 * s;
-                        uint8_t *sa = smem + s * kStageBytes, *sb = sa + kOperandBytes;
-                        const int kc = k * kCeStep;
-                        if (kWhat == kCeDw) {
-                            tma_load_3d_pair(sa, &ta, bar, m0, kc, pa);
-                            tma_load_3d_pair(sa + kOperandBytes / 2, &ta, bar, m0 + 64, kc, pa);
-                        } else {
-                            tma_load_3d_pair(sa, &ta, bar, kc, m0, pa);
+                            mbar_expect_tx(&full[s], 4 * (kOperandBytes + b_bytes));
+                        for (int plane = 0; plane < 2; ++plane) {
+                            uint8_t *to = smem + (4 * s + 2 * plane) * kOperandBytes;
+                            load_a(to, bar0 + 8 * s, m0, kc, plane);
+                            load_b(to + kOperandBytes, bar0 + 8 * s, n0, kc, plane);
                         }
-                        if (kWhat != kCeLogits) {
-                            tma_load_3d_pair(sb, &tb, bar, n0, kc, pb);
-                            if (second_block)
-                                tma_load_3d_pair(sb + kOperandBytes / 2, &tb, bar, n0 + 64, kc, pb);
-                        } else {
-                            tma_load_3d_pair(sb, &tb, bar, kc, n0, pb);
-                        }
-                        if (++s == kStages) {
-                            s = 0;
-                            parity ^= 1;
+                        ok = ready(kThird, (it & 1) ^ 1);
+                        if (!ok)
+                            break;
+                        if (cta == 0)
+                            mbar_expect_tx(&full[kThird], 2 * (kOperandBytes + b_bytes));
+                        load_a(smem + 8 * kOperandBytes, bar0 + 8 * kThird, m0, kc, 2);
+                        load_b(smem + 9 * kOperandBytes, bar0 + 8 * kThird, n0, kc, 2);
+                        ++it;
+                        s ^= 1;
+                        parity ^= s == 0;
+                    } else {
+#pragma unroll 1
+                        for (int part = kParts - 1; part >= 0; --part, ++it) {
+                            ok = ready(s, parity);
+                            if (!ok)
+                                break;
+                            if (cta == 0)
+                                mbar_expect_tx(&full[s], 2 * (kOperandBytes + b_bytes));
+                            uint8_t *to = smem + s * kStageBytes;
+                            load_a(to, bar0 + 8 * s, m0, kc, 0);
+                            load_b(to + kOperandBytes, bar0 + 8 * s, n0, kc, part);
+                            if (++s == kStages) {
+                                s = 0;
+                                parity ^= 1;
+                            }
                         }
                     }
                 }
             }
             // the last uses of the stages: their releases arrive from CTA 0, and this CTA stays until they have
-            for (uint32_t i = it > kStages ? it - kStages : 0; ok && i < it; ++i)
-                ok = mbar_wait(&empty[i % kStages], (i / kStages) & 1, w, 0xa6);
+            constexpr uint32_t ring = kSplit ? 2 : kStages;
+            const uint32_t last = it > ring ? it - ring : 0;
+            for (uint32_t i = last; ok && i < it; ++i)
+                ok = mbar_wait(&empty[i % ring], (i / ring) & 1, w, 0xa6);
+            if (kSplit && ok && it > 0)
+                ok = mbar_wait(&empty[kThird], (it - 1) & 1, w, 0xa6);
             if (!ok) {
                 *abort_flag = 1;
                 // wait (bounded) for the loads still in flight; CTA 0 holds their barriers
-                if (cta == 0)
-                    for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-                        mbar_wait(&full[i % kStages], (i / kStages) & 1, w, 0xaf);
+                if (cta == 0) {
+                    for (uint32_t i = last; i < it; ++i)
+                        mbar_wait(&full[i % ring], (i / ring) & 1, w, 0xaf);
+                    if (kSplit)  // and the step that was begun
+                        mbar_wait(&full[s], parity ^ 1, w, 0xaf);
+                    if (kSplit && it > 0)
+                        mbar_wait(&full[kThird], (it - 1) & 1, w, 0xaf);
+                }
             }
         }
     } else if (warp == kEpiWarps + 1) {
@@ -487,40 +526,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             Units units(plan, pair, pairs);
             Unit u;
             uint32_t s = 0, parity = 0, chunk = 0;
-            // operands of a step's first instruction, of the first stage
+            // A and B of a step's first instruction, were they at the ring's start
             const uint64_t da0 = kWhat == kCeDw ? desc_sw128(smem_u32(smem), kOperandBytes / 2, 1024)
                                                 : desc_sw128(smem_u32(smem), 16, 1024);
-            const uint64_t db0 = kWhat != kCeLogits
-                                     ? desc_sw128(smem_u32(smem) + kOperandBytes, kOperandBytes / 2, 1024)
-                                     : desc_sw128(smem_u32(smem) + kOperandBytes, 16, 1024);
-            constexpr uint32_t a_next = (kWhat == kCeDw ? 2048 : 32) / 16, b_next = (kWhat != kCeLogits ? 2048 : 32) / 16;
+            const uint64_t db0 = kWhat != kCeLogits ? desc_sw128(smem_u32(smem), kOperandBytes / 2, 1024)
+                                                    : desc_sw128(smem_u32(smem), 16, 1024);
+            auto multiply = [&](uint32_t d, uint64_t da, uint64_t db, bool add) {
+                constexpr uint32_t a_next = (kWhat == kCeDw ? 2048 : 32) / 16;
+                constexpr uint32_t b_next = (kWhat != kCeLogits ? 2048 : 32) / 16;
+#pragma unroll
+                for (int kk = 0; kk < kCeStep / 16; ++kk)
+                    mma_ss_pair(d, da + kk * a_next, db + kk * b_next, idesc, (add || kk > 0) ? 1u : 0u);
+            };
+            constexpr uint32_t slot = kOperandBytes / 16;
+            uint32_t third = 0;  // parity
             bool ok = true;
             while (ok && units.next(u)) {
-                int left = (u.k1 - u.k0) * per_step;  // loads of this unit
+                constexpr int per_step = kSplit ? 1 : kParts;
+                int left = (u.k1 - u.k0) * per_step;  // stages of this unit
                 while (ok && left > 0) {
-                    const int most = kChunkSteps<kWhat, kSplit> * per_step;
-                    const int n = left < most ? left : most;  // loads of this accumulation
-                    const uint32_t acc = chunk & 1;
+                    constexpr int most = kChunkSteps<kWhat, kSplit> * per_step;
+                    const int n = left < most ? left : most;  // stages of this accumulation
+                    const uint32_t acc = chunk & 1, d = tbase + acc * 256;
                     if (*abort_flag || !mbar_wait_cluster(&acc_empty[acc], ((chunk >> 1) & 1) ^ 1, w, 0xa2)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     for (int i = 0; i < n; ++i) {
-                        if (!mbar_wait(&full[s], parity, w, 0xa3)) {
-                            ok = false;
+                        ok = mbar_wait(&full[s], parity, w, 0xa3) &&
+                             (!kSplit || mbar_wait(&full[kThird], third, w, 0xa3));
+                        if (!ok)
                             break;
-                        }
                         tc_fence_after();
-                        const uint64_t da = da0 + s * (kStageBytes / 16), db = db0 + s * (kStageBytes / 16);
-#pragma unroll
-                        for (int kk = 0; kk < kCeStep / 16; ++kk)
-                            mma_ss_pair(tbase + acc * 256, da + kk * a_next, db + kk * b_next, idesc,
-                                        (i > 0 || kk > 0) ? 1u : 0u);
-                        mma_commit_pair(&empty[s]);
-                        if (++s == kStages) {
-                            s = 0;
-                            parity ^= 1;
+                        if constexpr (kSplit) {
+                            const uint64_t a1 = da0 + 4 * s * slot, b1 = db0 + (4 * s + 1) * slot;
+                            const uint64_t a2 = a1 + 2 * slot, b2 = b1 + 2 * slot;
+                            multiply(d, a1, db0 + 9 * slot, i > 0);
+                            multiply(d, da0 + 8 * slot, b1, true);
+                            mma_commit_pair(&empty[kThird]);
+                            third ^= 1;
+                            multiply(d, a2, b2, true);
+                            multiply(d, a1, b2, true);
+                            multiply(d, a2, b1, true);
+                            multiply(d, a1, b1, true);
+                            mma_commit_pair(&empty[s]);
+                            s ^= 1;
+                            parity ^= s == 0;
+                        } else {
+                            multiply(d, da0 + 2 * s * slot, db0 + (2 * s + 1) * slot, i > 0);
+                            mma_commit_pair(&empty[s]);
+                            if (++s == kStages) {
+                                s = 0;
+                                parity ^= 1;
+                            }
                         }
                     }
                     if (!ok)
