@@ -112,7 +112,8 @@ __device__ __forceinline__ Plan make_plan(const CeArgs &a, int cnt, int pairs)
     p.mt = (M + kCeTile - 1) / kCeTile;
     p.kb = (K + kCeStep - 1) / kCeStep;
     p.nt = (N + kCeTile - 1) / kCeTile;
-    // D in equal tiles: 776 as four of 224 instead of three of 256 and one of 8
+    // D in equal tiles: 776 as four of 224 instead of three of 256 and one of 8 (of
+    // 208, whose rows start off 64 bytes, 2 % slower)
     p.cols = kWhat == kCeLogits ? kCeTile : ((N + p.nt - 1) / p.nt + 31) / 32 * 32;
     const int tiles = p.mt * p.nt;
     p.runs = kWhat == kCeLogits ? 0 : ce_runs(tiles, p.kb, pairs, kSplit);  // a softmax needs whole sums
