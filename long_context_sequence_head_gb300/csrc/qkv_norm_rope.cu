@@ -33,13 +33,31 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-// Rows of a run (bytes), runs on their way per warp, resident blocks per SM.
-// 64K tokens, 32 + 8 + 8 heads of 128, bf16, us: forward 252 (3 runs of 4 KB
-// x 4 blocks, and 2 x 4), 258 (2 x 5), 260 (2 x 6); backward 360 (1 x 5), 364
-// (1 x 4), 378 (2 x 3), and over 430 with runs of 2 KB or registers spilled.
-constexpr int kFwdRun = 4096, kBwdRun = 4096;
-constexpr int kFwdRing = 2, kBwdRing = 1;
-constexpr int kFwdBlocks = 4, kBwdBlocks = 5;
+// Rows of a run (bytes) and resident blocks per SM; each warp has a ring of kRing
+// runs.  Where little is computed per byte (fp32, or no norm) fewer runs on their
+// way are better, or reads and writes get into each other's way.  us, bf16: 64K
+// tokens, 32 + 8 + 8 heads of 128; fp32: 32K tokens, 16 + 4 + 4.
+//   forward, normed   249 (6 KB x 5 blocks), 259 (6 KB x 6), 261 (4 KB x 5), 264 (6
+//                     KB x 4), 286 (4 KB x 4), 257 (rings of two, 4 KB x 4, which
+//                     take 42 us at 8K tokens instead of 44)
+//   not normed        249 (4 KB x 4), 256 (4 KB x 5), 268 (6 KB x 5)
+//   fp32              132 (4 KB x 4), 131 (4 KB x 5), 138 (6 KB x 5)
+//   backward, normed  359 (4 KB x 5), 364 (x 4), over 430 with 2 KB or spills
+//   not normed        246 (4 KB x 4), 258 (x 5), 274 (x 3)
+//   fp32              180 (4 KB x 4), 190 (x 5), 195 (x 3)
+constexpr int kRing = 1;
+template <typename T, bool kNorm>
+constexpr bool kLight = sizeof(T) == 4 || !kNorm;
+template <typename T, bool kNorm>
+struct Fwd {
+    static constexpr int kRun = kLight<T, kNorm> ? 4096 : 6144;
+    static constexpr int kBlocks = kLight<T, kNorm> ? 4 : 5;
+};
+template <typename T, bool kNorm>
+struct Bwd {
+    static constexpr int kRun = 4096;
+    static constexpr int kBlocks = kLight<T, kNorm> ? 4 : 5;
+};
 
 // A row of kD values over kLanes lanes: two chunks of kC values each, as kP
 // pairs for the packed fp32 arithmetic.
@@ -113,37 +131,54 @@ struct Far {
     }
 };
 
+// The frequencies and their axes, in shared memory: lanes that index the kernel's
+// parameters at different places are served one by one.
+template <int kD>
+struct Freqs {
+    uint64_t turn[kD / 2];
+    uint8_t axis[kD / 2];
+
+    __device__ __forceinline__ void load(const NormRopeParams &p)
+    {
+        for (int i = threadIdx.x; i < p.half; i += kThreads) {
+            turn[i] = p.turn[i];
+            axis[i] = p.axis[i];
+        }
+    }
+};
+
 // cos and sin of a token's rot/2 angles in the warp's shared table.  A lane
 // makes at most two; the positions of the next token are read while this one
 // is worked on.
+template <int kD>
 struct Angles {
     int64_t pos[2];
     uint32_t held, made;  // the token whose positions these are, and the one the table is of
 
     __device__ __forceinline__ Angles() : held(~0u), made(~0u) {}
-    __device__ __forceinline__ void read(const NormRopeParams &p, uint32_t m, int lane)
+    __device__ __forceinline__ void read(const NormRopeParams &p, const Freqs<kD> &fr, uint32_t m, int lane)
     {
         held = m;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (lane + 32 * i < p.half)
-                pos[i] = p.positions[p.axis[lane + 32 * i] * p.tokens + m];
+                pos[i] = p.positions[fr.axis[lane + 32 * i] * p.tokens + m];
     }
     // true if the table is new; `next`: the warp's next token
-    __device__ __forceinline__ bool make(const NormRopeParams &p, const Token &k, uint32_t next, float2 *table,
-                                         int lane)
+    __device__ __forceinline__ bool make(const NormRopeParams &p, const Freqs<kD> &fr, const Token &k, uint32_t next,
+                                         float2 *table, int lane)
     {
         if (made == k.m)
             return false;
         made = k.m;
         if (p.positions && held != k.m)
-            read(p, k.m, lane);
+            read(p, fr, k.m, lane);
         __syncwarp();  // the last token's reads are done
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int f = lane + 32 * i;
             if (f < p.half) {
-                const uint64_t frac = p.turn[f] * static_cast<uint64_t>(p.positions ? pos[i] : k.n);
+                const uint64_t frac = fr.turn[f] * static_cast<uint64_t>(p.positions ? pos[i] : k.n);
                 float sn, cs;
                 // its upper 32 bits, as half turns in [-1, 1)
                 sincospif(static_cast<float>(static_cast<int32_t>(frac >> 32)) * 0x1p-31f, &sn, &cs);
@@ -152,7 +187,7 @@ struct Angles {
         }
         __syncwarp();
         if (p.positions && next < p.tokens)
-            read(p, next, lane);
+            read(p, fr, next, lane);
         return true;
     }
 };
@@ -332,22 +367,25 @@ struct Ring {
 };
 
 template <typename T, int kD, bool kInter, bool kNorm>
-__global__ void __launch_bounds__(kThreads, kFwdBlocks) norm_rope_fwd_kernel(const __grid_constant__ NormRopeParams p,
-                                                                            const WaitCfg wait)
+__global__ void __launch_bounds__(kThreads, Fwd<T, kNorm>::kBlocks)
+    norm_rope_fwd_kernel(const __grid_constant__ NormRopeParams p, const WaitCfg wait)
 {
-    using S = Shape<T, kD, kFwdRun>;
+    constexpr int kRunBytes = Fwd<T, kNorm>::kRun;
+    using S = Shape<T, kD, kRunBytes>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float2 table[kWarps][kD / 2];
     __shared__ __align__(16) T weights[2][kD];
+    __shared__ Freqs<kD> freqs;
     const int warp = warp_id(), lane = lane_id(), sub = lane / S::kLanes;
+    freqs.load(p);
     if (kNorm) {
         for (int i = threadIdx.x; i < kD; i += kThreads) {
             weights[0][i] = static_cast<const T *>(p.wq)[i];
             weights[1][i] = static_cast<const T *>(p.wk)[i];
         }
-        __syncthreads();
     }
-    const Ring<kFwdRing, 1, kFwdRun> ring(smem, warp, lane);
+    __syncthreads();
+    const Ring<kRing, 1, kRunBytes> ring(smem, warp, lane);
     int lo, hi;
     chunk_places<S, kInter>(p.half, lane % S::kLanes, lo, hi);
     Cursor<S> now(p, blockIdx.x * kWarps + warp, gridDim.x * kWarps);
@@ -361,25 +399,25 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks) norm_rope_fwd_kernel(con
         if (lane < 3 && h0 < h1) {
             const T *src = static_cast<const T *>(lane == 0 ? p.q : (lane == 1 ? p.k : p.v)) +
                            ahead.k.m * (lane == 0 ? p.qs : (lane == 1 ? p.ks : p.vs)) + h0 * kD;
-            bulk_g2s(ring.data + slot * kFwdRun + row * kD * sizeof(T), src, (h1 - h0) * kD * sizeof(T),
+            bulk_g2s(ring.data + slot * kRunBytes + row * kD * sizeof(T), src, (h1 - h0) * kD * sizeof(T),
                      &ring.bars[slot]);
         }
         ahead.step(p);
     };
     int started = 0, done = 0;  // runs fetched and worked on
-    for (; started < kFwdRing && ahead.more(); ++started)
+    for (; started < kRing && ahead.more(); ++started)
         fetch(started);
-    Angles at;
+    Angles<kD> at;
     int last = -1;
     Turn<S, kInter, false, kNorm> turn;
     Far far;
     while (now.more()) {
-        const int slot = done % kFwdRing;
-        if (now.row0() < p.Hq + p.Hkv && at.make(p, now.k, now.k.m + now.stride, table[warp], lane))
+        const int slot = done % kRing;
+        if (now.row0() < p.Hq + p.Hkv && at.make(p, freqs, now.k, now.k.m + now.stride, table[warp], lane))
             last = -1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&ring.bars[slot], (done / kFwdRing) & 1, wait, 0xb1)))
+        if (!__all_sync(0xffffffffu, mbar_wait(&ring.bars[slot], (done / kRing) & 1, wait, 0xb1)))
             break;
-        const T *data = reinterpret_cast<const T *>(ring.data + slot * kFwdRun);
+        const T *data = reinterpret_cast<const T *>(ring.data + slot * kRunBytes);
 #pragma unroll 1
         for (int t = 0; t < 2; ++t) {
             int h0, h1, row;
@@ -449,27 +487,30 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks) norm_rope_fwd_kernel(con
     }
     // after a wait that ran out: the copies still on their way (bounded)
     for (; done < started; ++done)
-        mbar_wait(&ring.bars[done % kFwdRing], (done / kFwdRing) & 1, wait, 0xbf);
+        mbar_wait(&ring.bars[done % kRing], (done / kRing) & 1, wait, 0xbf);
 }
 
 template <typename T, int kD, bool kInter, bool kNorm>
-__global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p,
-                                                                            const WaitCfg wait)
+__global__ void __launch_bounds__(kThreads, Bwd<T, kNorm>::kBlocks)
+    norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p, const WaitCfg wait)
 {
-    using S = Shape<T, kD, kBwdRun>;
+    constexpr int kRunBytes = Bwd<T, kNorm>::kRun;
+    using S = Shape<T, kD, kRunBytes>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float2 table[kWarps][kD / 2];
     __shared__ __align__(16) T weights[2][kD];
+    __shared__ Freqs<kD> freqs;
     const int warp = warp_id(), lane = lane_id(), sub = lane / S::kLanes;
+    freqs.load(p);
     if (kNorm) {
         for (int i = threadIdx.x; i < kD; i += kThreads) {
             weights[0][i] = static_cast<const T *>(p.wq)[i];
             weights[1][i] = static_cast<const T *>(p.wk)[i];
         }
-        __syncthreads();
     }
+    __syncthreads();
     constexpr int kParts = kNorm ? 2 : 1;  // a run of dy and one of x
-    const Ring<kBwdRing, kParts, kBwdRun> ring(smem, warp, lane);
+    const Ring<kRing, kParts, kRunBytes> ring(smem, warp, lane);
     int lo, hi;
     chunk_places<S, kInter>(p.half, lane % S::kLanes, lo, hi);
     // the warp's part of dw, kept between runs: [q, k][slot][d]
@@ -484,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
     Cursor<S> ahead = now;
     auto fetch = [&](int slot) {
         // Lanes 0, 1, 2 (mod 4): dy of Q, K and V, a copy per rank; lanes 3 and 7: x of Q and K
-        uint8_t *to = ring.data + slot * (kParts * kBwdRun);
+        uint8_t *to = ring.data + slot * (kParts * kRunBytes);
         const int row0 = ahead.row0(), row1 = ahead.row1(p), xrows = max(min(row1, p.Hq + p.Hkv) - row0, 0);
         if (lane == 0)
             mbar_expect_tx(&ring.bars[slot], (row1 - row0 + (kNorm ? xrows : 0)) * kD * sizeof(T));
@@ -503,24 +544,24 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
                          &ring.bars[slot]);
             }
         } else if (kNorm && t < 2 && h0 < h1) {
-            bulk_g2s(to + kBwdRun + row * kD * sizeof(T),
+            bulk_g2s(to + kRunBytes + row * kD * sizeof(T),
                      static_cast<const T *>(t ? p.k : p.q) + ahead.k.m * (t ? p.ks : p.qs) + h0 * kD,
                      (h1 - h0) * kD * sizeof(T), &ring.bars[slot]);
         }
         ahead.step(p);
     };
     int started = 0, done = 0;
-    for (; started < kBwdRing && ahead.more(); ++started)
+    for (; started < kRing && ahead.more(); ++started)
         fetch(started);
-    Angles at;
+    Angles<kD> at;
     Turn<S, kInter, true, false> turn;
     while (now.more()) {
-        const int slot = done % kBwdRing;
-        if (now.row0() < p.Hq + p.Hkv && at.make(p, now.k, now.k.m + now.stride, table[warp], lane))
+        const int slot = done % kRing;
+        if (now.row0() < p.Hq + p.Hkv && at.make(p, freqs, now.k, now.k.m + now.stride, table[warp], lane))
             turn.load(table[warp], p.half, lo, hi);
-        if (!__all_sync(0xffffffffu, mbar_wait(&ring.bars[slot], (done / kBwdRing) & 1, wait, 0xb2)))
+        if (!__all_sync(0xffffffffu, mbar_wait(&ring.bars[slot], (done / kRing) & 1, wait, 0xb2)))
             break;
-        const T *data = reinterpret_cast<const T *>(ring.data + slot * (kParts * kBwdRun));
+        const T *data = reinterpret_cast<const T *>(ring.data + slot * (kParts * kRunBytes));
 #pragma unroll 1
         for (int t = 0; t < 2; ++t) {
             int h0, h1, row;
@@ -528,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
             if (h0 >= h1)
                 continue;
             T *out = static_cast<T *>(t ? p.dk : p.dq) + static_cast<int64_t>(now.k.m) * (t ? p.dks : p.dqs);
-            const T *rows = data + (row - h0) * kD, *xrows = rows + kBwdRun / sizeof(T);
+            const T *rows = data + (row - h0) * kD, *xrows = rows + kRunBytes / sizeof(T);
             float2 w[2][S::kP], sum[2][S::kP];
             if (kNorm) {
                 const Raw raw = load_row<T>(weights[t], lo, hi);
@@ -612,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
     }
     // after a wait that ran out: the copies still on their way (bounded)
     for (; done < started; ++done)
-        mbar_wait(&ring.bars[done % kBwdRing], (done / kBwdRing) & 1, wait, 0xbf);
+        mbar_wait(&ring.bars[done % kRing], (done / kRing) & 1, wait, 0xbf);
     if constexpr (kNorm) {
         // the block's weight-gradient partial: row slots and warps, always in the same order
         __syncthreads();
@@ -676,16 +717,17 @@ __global__ void __launch_bounds__(kDwCols *kDwRuns) norm_rope_dw_kernel(const fl
 template <typename T, int kD, bool kInter, bool kNorm>
 cudaError_t run(NormRopeParams &p, bool bwd, cudaStream_t s)
 {
+    constexpr int kFwdRun = Fwd<T, kNorm>::kRun, kBwdRun = Bwd<T, kNorm>::kRun;
     const int kRun = (bwd ? kBwdRun : kFwdRun) / static_cast<int>(kD * sizeof(T));
     const int runs = (p.Hq + (p.v ? 2 : 1) * p.Hkv + kRun - 1) / kRun;
     p.runs = runs;
-    const int64_t resident = static_cast<int64_t>(num_sms()) * (bwd ? kBwdBlocks : kFwdBlocks);
+    const int64_t resident = static_cast<int64_t>(num_sms()) * (bwd ? Bwd<T, kNorm>::kBlocks : Fwd<T, kNorm>::kBlocks);
     // Tokens that are fewer than the warps come in the parts that end first:
     // rounds of parts x runs of a part.  So do the backward's last tokens, when
     // every warp has had the same number of whole ones: 2048 tokens of 32 + 8 + 8
     // heads 25.3 us (parts for as many warps as there are 31.5), 4095 fp32 ones of
     // 12 + 6 + 6 25.1 (all whole 27.4).  In the forward the parts' angles cost
-    // what their rounds save: 8192 tokens 41.6 us, all whole 40.5.
+    // what their rounds save (8192 tokens 43.7 us either way).
     const int64_t warps = resident * kWarps;
     p.whole = bwd || p.tokens < warps ? p.tokens / warps * warps : p.tokens;
     const int64_t rest = p.tokens - p.whole;
@@ -707,7 +749,7 @@ cudaError_t run(NormRopeParams &p, bool bwd, cudaStream_t s)
     const int64_t grid = std::min<int64_t>((p.whole + (p.tokens - p.whole) * p.splits + kWarps - 1) / kWarps, resident);
     if (!bwd) {
         auto kernel = norm_rope_fwd_kernel<T, kD, kInter, kNorm>;
-        constexpr int smem = Ring<kFwdRing, 1, kFwdRun>::kBytes;
+        constexpr int smem = Ring<kRing, 1, kFwdRun>::kBytes;
         static_assert(smem <= 40 * 1024, "with the static part, what a launch may take without asking");
         kernel<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p, wait_cfg());
         return cudaGetLastError();
@@ -715,8 +757,8 @@ cudaError_t run(NormRopeParams &p, bool bwd, cudaStream_t s)
     if (grid > kNormRopeMaxBlocks)
         return cudaErrorInvalidConfiguration;
     auto kernel = norm_rope_bwd_kernel<T, kD, kInter, kNorm>;
-    constexpr int smem = Ring<kBwdRing, kNorm ? 2 : 1, kBwdRun>::kBytes;
-    static_assert(smem + static_cast<int>(sizeof(float)) * 18 * kD <= 48 * 1024, "as above");
+    constexpr int smem = Ring<kRing, kNorm ? 2 : 1, kBwdRun>::kBytes;
+    static_assert(smem + static_cast<int>(sizeof(float)) * 24 * kD <= 48 * 1024, "as above");
     kernel<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p, wait_cfg());
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
