@@ -21,9 +21,9 @@
 // token's rows, so that its cosines and sines are made once and shared by its
 // heads; a lane holds the two chunks of a row (8 bytes each) whose values turn
 // with each other, so that the rotation needs no exchange between lanes.  Rows
-// come in runs through a ring of bulk copies that each warp keeps for
-// itself, so that what is in flight costs no registers, and the next tokens
-// are on their way while one is worked on.
+// come in runs, by bulk copies into shared memory that each warp keeps for
+// itself: what is in flight costs no registers, and while a warp works on its
+// run those of the SM's other warps are on their way.
 #include <cmath>
 
 #include "uly_internal.h"
