@@ -444,9 +444,10 @@ uly_status ulysses_sharded_ce_loss(const void *logits, const int64_t *labels, vo
  *              = 1 if dhidden or dweight is given) bytes.  Calls that may run
  *              at the same time need workspaces of their own.
  * Products are accumulated in fp32; softmax and loss are fp32.  bf16: the
- * operands of the two gradient products, the softmax's numerators and, for
- * dweight, the hidden rows divided by its denominators (these in two parts for
- * up to 128 rows), are rounded to bf16; each gradient is rounded to bf16 once.
+ * label's term of a row's gradient, (p - 1) weight[label] and (p - 1) hidden, is
+ * formed in fp32; of the other words' terms, p weight[v] and p hidden, the
+ * softmax's numerators and, for dweight, the hidden rows divided by its
+ * denominators are rounded to bf16; each gradient is rounded to bf16 once.
  * fp32: operands are taken as three bf16 parts each, off by less than 2^-26 of a
  * value (values above 3.39e38, bf16's largest, count as infinite).
  * D * element size a multiple of 16 bytes, D <= 65536, V <= 2^21

@@ -9,9 +9,16 @@
 //   1. logits   x = h W^T; every (row, 64 columns) leaves c, the sum s of
 //               e = 2^(x log2 e - c), the row's target logit, and e itself;
 //   2. rows     C = max c, S = sum s 2^(c - C); loss = ln S + (C ln 2 - x_y);
-//               e_y -= S, h' = h / S;
-//   3. dh       = e W / (S T) for the piece's rows;
-//   4. dW      += e^T h' / T, in fp32 across the pieces, rounded once at the end.
+//               l = (e_y - S) / S, then e_y = 0; h' = h / S;
+//   3. dh       = (e W / S + l w_y) / T for the piece's rows;
+//   4. dW      += (e^T h' + l h at the rows' labels) / T, in fp32 across the
+//               pieces, rounded once at the end.
+// The label's term l = p - 1 is most of a row's gradient.  In bf16 it stays in fp32
+// and meets w_y and h as they were given, where a product's result is written out;
+// only the other words' terms have rounded operands.  With the label's value
+// rounded among e, or h' carrying its term, dW was 0.0020 and 0.0024 of its norm
+// off at 5,734 rows of 151,936, of which its own rounding is 0.0017.  (fp32: e has
+// three parts, at the label of (e_y - S), and no rounding is left to take out.)
 // c is 0 for all columns of nearly every row, so that e already is the softmax's
 // numerator and is used as it lies: the division by S goes to dh's rows and to
 // h, and of e only the label's value is touched.  Rewriting e as the logits'
@@ -32,12 +39,6 @@ namespace {
 // ms beside 12 ms of products for a piece of 8448 rows.
 constexpr int64_t kPieceBytes = int64_t(2500) << 20;
 constexpr int kRowThreads = 128;
-// bf16 calls of up to kFewRows rows hold h' in two bf16 parts for dW: dW is off by
-// 0.0017 of its norm, its own rounding, instead of 0.0024, which one label a word
-// does not average out.  The second product hides behind dW's stores as long as
-// the contraction is short: 128 rows x 1024 x 32,000 81.0 us a call, 79.3 with one
-// part; 256 rows 95.7 and 85.7.
-constexpr int kFewRows = 128;
 
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu); }
@@ -215,10 +216,70 @@ __device__ __forceinline__ void lay8(const void *src, int64_t row, int i, int D,
     }
 }
 
+__host__ __device__ inline int ce_groups(int rows) { return (rows + kCeGroup - 1) / kCeGroup; }
+
+// bf16, with dW: which of the piece's rows [r0, r0 + kCeGroup) have one label.  The
+// terms l_r h_r of dW of more than kCeAlone go as one, since a frequent word's
+// thousands of rows would otherwise all meet in the one warp that writes its row of
+// dW: 4,830 rows of 50,257 words with frequencies as 1 / rank 1.4 ms a call, 1.06
+// like this, 0.97 with all words as frequent; one word throughout 2.0 and 1.0.
+// Thread i looks for row i's label among the block's 256.
+__device__ __forceinline__ void group_labels(const CeArgs &a, int cnt, int r0, const int32_t *shifted)
+{
+    static_assert(kCeGroup == 256, "a thread a row");
+    __shared__ __align__(16) int label[kCeGroup];
+    __shared__ int places[kCeGroup / 32];
+    const int i = threadIdx.x, r = r0 + i;
+    const int64_t src = r < cnt ? a.index[a.base + r] : 0;
+    const int y = r < cnt ? shifted[src] : -1;
+    label[i] = y;
+    // the marks of these rows, 8 of 32 a piece
+    for (int w = i; w < (a.V + 31) / 32; w += kCeGroup) {
+        uint4 *mark = reinterpret_cast<uint4 *>(a.marks + static_cast<int64_t>(w) * a.mark_pitch + r0 / 32);
+        mark[0] = mark[1] = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    int first = kCeGroup, next = kCeGroup, count = 0;
+    for (int j = 0; j < min(kCeGroup, cnt - r0); j += 4) {
+        const int4 q = *reinterpret_cast<const int4 *>(label + j);
+        const int v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (v[k] == y) {
+                ++count;
+                first = min(first, j + k);
+                if (j + k > i)
+                    next = min(next, j + k);
+            }
+        }
+    }
+    const bool several = y >= 0 && count > kCeAlone, stands = several && first == i;
+    const unsigned mask = __ballot_sync(0xffffffffu, stands);
+    if (lane_id() == 0)
+        places[warp_id()] = __popc(mask);
+    __syncthreads();  // the marks are cleared, too
+    int slot = r0 / 2 + __popc(mask & ((1u << lane_id()) - 1));
+    for (int w = 0; w < warp_id(); ++w)
+        slot += places[w];
+    if (stands) {
+        a.label_first[slot] = r;
+        a.label_left[slot] = count;
+        label[i] = slot;  // nobody compares labels any more
+    }
+    __syncthreads();
+    if (y < 0)
+        return;
+    if (stands || !several)
+        atomicOr(&a.marks[static_cast<int64_t>(y / 32) * a.mark_pitch + r / 32], 1u << (r % 32));
+    a.label_slot[r] = several ? label[first] : static_cast<int32_t>(~src);
+    a.label_next[r] = next < kCeGroup ? r0 + next : -1;
+}
+
 // The piece's hidden rows next to each other (fp32: as planes), with their
 // labels; zeros up to a multiple of 64 rows, where dW's contraction ends.  The
 // first piece also clears the gradient of the rows without a label: its row r
-// then stands for row r of the call too.  A thread takes eight values.
+// then stands for row r of the call too.  A thread takes eight values.  The first
+// blocks group the labels.
 template <bool kSplit>
 __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ CeArgs a, const void *__restrict__ hidden,
                                                      const int32_t *__restrict__ shifted, int32_t *__restrict__ label,
@@ -227,7 +288,12 @@ __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ CeA
     grid_wait();
     grid_next();
     const int cnt = ce_piece_rows(a), vecs = (a.D + 7) / 8;
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x, r = at / vecs;
+    const int groups = !kSplit && a.marks != nullptr ? ce_groups(a.rows) : 0;
+    if (static_cast<int>(blockIdx.x) < groups) {
+        group_labels(a, cnt, blockIdx.x * kCeGroup, shifted);
+        return;
+    }
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) - groups) * blockDim.x + threadIdx.x, r = at / vecs;
     const int i = static_cast<int>(at - r * vecs) * 8;
     if (a.base == 0 && a.dh != nullptr && r < rows && shifted[r] < 0) {
         uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.dh) + (r * a.D + i) * (kSplit ? 4 : 2));
@@ -242,8 +308,6 @@ __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ CeA
     if (i == 0)
         label[r] = live ? shifted[src] : -1;
     lay8<kSplit>(live ? hidden : nullptr, src, i, a.D, out, r, ldh, ldh * a.rows);
-    if (!kSplit && a.h_planes == 2 && !live)
-        *reinterpret_cast<uint4 *>(out + (a.rows + r) * ldh + i) = make_uint4(0, 0, 0, 0);
 }
 
 // fp32 weight as planes.
@@ -256,6 +320,44 @@ __global__ void __launch_bounds__(256) split_weight_kernel(const float *__restri
     const int64_t at = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x, v = at / vecs;
     if (v < V)
         lay8<true>(w, v, static_cast<int>(at - v * vecs) * 8, D, out, v, ldw, ldw * V);
+}
+
+// bf16, with dW, by the block of each row with others of its label in its group, once
+// its l is written: the last of them to come sums all their terms l h, in the order
+// of the rows, so that sums repeat bit for bit.
+__device__ __forceinline__ void sum_label_terms(const CeArgs &a, int slot)
+{
+    __shared__ int last;
+    if (threadIdx.x == 0) {
+        __threadfence();
+        last = atomicSub(&a.label_left[slot], 1) == 1;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!last)
+        return;
+    constexpr int kAhead = 4;  // rows on their way together
+    for (int col = threadIdx.x * 8; col < a.D; col += kRowThreads * 8) {
+        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int r = a.label_first[slot]; r >= 0;) {
+            uint4 q[kAhead];
+            float l[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const bool live = r >= 0;
+                const int64_t row = live ? a.index[a.base + r] : 0;
+                q[k] = live ? *reinterpret_cast<const uint4 *>(a.hidden + row * a.D + col) : make_uint4(0, 0, 0, 0);
+                l[k] = live ? __ldcg(&a.label_grad[r]) : 0.f;
+                r = live ? a.label_next[r] : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                add_scaled8(sum, l[k], q[k]);
+        }
+        float4 *to = reinterpret_cast<float4 *>(a.label_sum + static_cast<int64_t>(slot) * a.D + col);
+        to[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+        to[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+    }
 }
 
 // Softmax statistics of some columns: C and S of sum e = S 2^C, and the least c.
@@ -273,7 +375,7 @@ struct Stat {
 };
 
 // One block per row of the piece: its loss, and with a gradient the row's scale
-// 1 / S, e at the label, the row of h' (where dW is wanted), and e on one c where
+// 1 / S, the label's term, the row of h' (where dW is wanted), and e on one c where
 // it is not yet.
 template <bool kSplit>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ CeArgs a,
@@ -310,6 +412,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         st.join(red[w].C, red[w].S, red[w].least);
     const int y = label[r];
     const int64_t row = a.index[a.base + r];
+    const int slot = !kSplit && a.marks != nullptr ? a.label_slot[r] : -1;
     if (threadIdx.x == 0) {
         // ln S + C ln 2 - x_y, with the whole powers of two taken out of x_y before anything is rounded
         const uint32_t bits = __float_as_uint(st.S), exponent = bits >> 23;
@@ -320,11 +423,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     }
     if (!a.keep)
         return;
-    // The label's value (p - 1) S is most of the row's gradient.  In bf16 the
-    // scale takes up what its rounding loses, and is off by that (2^-8 at most)
-    // for the others, which are rounded as much.
-    const float g = ex2_approx(fmaf(a.target[r], kLog2e, -st.C)) - st.S, held = bf16_value(bf16_bits(g));
-    const float scale = (kSplit || held == 0.f ? 1.f : g / held) * (1.f / st.S);
+    const float g = ex2_approx(fmaf(a.target[r], kLog2e, -st.C)) - st.S, scale = 1.f / st.S;  // g: (p - 1) S
     uint16_t *erow = a.e + r * a.ldg;
     const int64_t plane = a.ldg * a.rows;
     if (st.least < st.C) {
@@ -351,7 +450,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
             for (int i = 0; i < 3; ++i)
                 erow[i * plane + y] = q.p[i];
         } else {
-            erow[y] = bf16_bits(g);
+            a.label_grad[r] = g * scale;
+            erow[y] = 0;
         }
     }
     if (a.dw == nullptr)
@@ -367,25 +467,22 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         } else {
             const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(hidden) + row * a.D + i);
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-            uint32_t hi[4], lo[4];
+            uint32_t to[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float x0 = __uint_as_float(w[j] << 16) * scale, x1 = __uint_as_float(w[j] & 0xffff0000u) * scale;
-                hi[j] = pack_bf16x2(x0, x1);
-                lo[j] = pack_bf16x2(x0 - __uint_as_float(hi[j] << 16), x1 - __uint_as_float(hi[j] & 0xffff0000u));
-            }
-            *reinterpret_cast<uint4 *>(out + r * ldh + i) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if (a.h_planes == 2)
-                *reinterpret_cast<uint4 *>(out + (a.rows + r) * ldh + i) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            for (int j = 0; j < 4; ++j)
+                to[j] = pack_bf16x2(__uint_as_float(w[j] << 16) * scale, __uint_as_float(w[j] & 0xffff0000u) * scale);
+            *reinterpret_cast<uint4 *>(out + r * ldh + i) = make_uint4(to[0], to[1], to[2], to[3]);
         }
     }
+    if (!kSplit && slot >= 0)
+        sum_label_terms(a, slot);
 }
 
 size_t up(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Layout {
-    int h_planes;
-    size_t good, n_good, shifted, row_loss, index, label, target, row_scale, stats, h, w, e, acc, partial, total;
+    size_t good, n_good, shifted, row_loss, index, label, target, row_scale, label_grad, stats, h, w, e, acc, partial;
+    size_t marks, label_slot, label_next, label_first, label_left, label_sum, total;
     int64_t ldh, ldg;
     int rows, stat_tiles;
 };
@@ -400,7 +497,6 @@ Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
     L.rows = static_cast<int>(std::min<int64_t>(std::min<int64_t>(fit, 65536), (T + 63) / 64 * 64));
     L.ldh = (D + 63) / 64 * 64;
     L.stat_tiles = (V + kCeStatCols - 1) / kCeStatCols;
-    L.h_planes = grad && !split && T <= kFewRows ? 2 : 1;
     const size_t planes = split ? 3 : 1, kept = static_cast<size_t>(L.rows) * L.ldg;
     size_t o = 0;
     auto take = [&](size_t &at, size_t bytes) { at = o, o += up(bytes); };
@@ -412,8 +508,9 @@ Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
     take(L.label, sizeof(int32_t) * L.rows);
     take(L.target, sizeof(float) * L.rows);
     take(L.row_scale, sizeof(float) * L.rows);
+    take(L.label_grad, sizeof(float) * L.rows);
     take(L.stats, sizeof(float2) * L.rows * static_cast<size_t>(L.stat_tiles));
-    take(L.h, (split ? 3 : L.h_planes) * static_cast<size_t>(L.rows) * L.ldh * 2);
+    take(L.h, planes * static_cast<size_t>(L.rows) * L.ldh * 2);
     if (split)
         take(L.w, planes * V * L.ldh * 2);
     if (grad) {
@@ -424,6 +521,15 @@ Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
         const int parts =
             std::max(ce_most_parts(kCeDh, L.rows, D, V, esize), ce_most_parts(kCeDw, L.rows, D, V, esize));
         take(L.partial, sizeof(float) * kCeTileFloats * parts);
+        if (!split) {
+            const size_t groups = ce_groups(L.rows), places = groups * (kCeGroup / 2);  // sums of two rows at least
+            take(L.marks, sizeof(uint32_t) * (kCeGroup / 32) * groups * ((V + 31) / 32));
+            take(L.label_slot, sizeof(int32_t) * L.rows);
+            take(L.label_next, sizeof(int32_t) * L.rows);
+            take(L.label_first, sizeof(int32_t) * places);
+            take(L.label_left, sizeof(int32_t) * places);
+            take(L.label_sum, sizeof(float) * places * D);
+        }
     }
     L.total = o;
     return L;
@@ -458,7 +564,16 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
     a.target = reinterpret_cast<float *>(ws + L.target);
     a.row_scale = reinterpret_cast<float *>(ws + L.row_scale);
     a.keep = grad;
-    a.h_planes = L.h_planes;
+    a.label_grad = reinterpret_cast<float *>(ws + L.label_grad);
+    a.marks = !kSplit && dweight ? reinterpret_cast<uint32_t *>(ws + L.marks) : nullptr;
+    a.mark_pitch = ce_groups(L.rows) * (kCeGroup / 32);
+    a.label_slot = reinterpret_cast<int32_t *>(ws + L.label_slot);
+    a.label_next = reinterpret_cast<int32_t *>(ws + L.label_next);
+    a.label_first = reinterpret_cast<int32_t *>(ws + L.label_first);
+    a.label_left = reinterpret_cast<int32_t *>(ws + L.label_left);
+    a.label_sum = reinterpret_cast<float *>(ws + L.label_sum);
+    a.hidden = static_cast<const uint16_t *>(hidden);
+    a.weight = static_cast<const uint16_t *>(weight);
     a.dh = dhidden;
     a.dw = dweight;
     a.acc = reinterpret_cast<float *>(ws + L.acc);
@@ -481,7 +596,8 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
     }
     for (int64_t base = 0; base < rows; base += L.rows) {
         a.base = base;
-        const int64_t blocks = ((base == 0 ? std::max<int64_t>(rows, L.rows) : L.rows) * vecs + 255) / 256;
+        const int64_t blocks = ((base == 0 ? std::max<int64_t>(rows, L.rows) : L.rows) * vecs + 255) / 256 +
+                               (a.marks != nullptr ? ce_groups(L.rows) : 0);
         if (e == cudaSuccess)
             e = launch_after(gather_kernel<kSplit>, blocks, 256, 0, s, a, hidden, shifted, label, h, L.ldh, rows);
         if (e == cudaSuccess)

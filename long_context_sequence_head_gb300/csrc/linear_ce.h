@@ -20,6 +20,9 @@ constexpr int kCeMaxPairs = 80;
 // fp32; exponentials are lost 2^-78 below the least such maximum, and of h / S
 // values of h below 2^-57 (in fp32 their last 16 bits below 2^-33).
 constexpr float kCeFree = 48.f;
+// Rows that are searched for equal labels together, and how many with one label stay
+// alone.
+constexpr int kCeGroup = 256, kCeAlone = 2;
 // floats a pair leaves for one tile
 constexpr int64_t kCeTileFloats = static_cast<int64_t>(kCeTile) * kCeTile;
 
@@ -45,14 +48,23 @@ struct CeArgs {
     int rows;               // rows a piece may have
     int D, V;
     int64_t ldg;            // row pitch of e, elements
-    uint16_t *e;            // [planes][rows][ldg] exponentials, then their difference to S at the label
+    uint16_t *e;            // [planes][rows][ldg] exponentials; at the label 0 (fp32: their difference to S)
     const int32_t *index;   // good row -> row of hidden
     const int32_t *label;   // [rows] of the piece
     float2 *stats;          // [rows][stat_tiles] (c, s)
     int stat_tiles;
     float *target;          // [rows] logits of the labels
     float *row_scale;       // [rows] 1 / S
-    int h_planes;           // bf16: parts that h' has in dW, 1 or 2
+    float *label_grad;      // bf16: [rows] of the piece, l = p - 1 at the label
+    // bf16, with dW (else null): which rows of a block of kCeGroup have one label, see group_labels
+    uint32_t *marks;        // [words / 32][mark_pitch] a bit for a row alone or the first of several, by its label
+    int mark_pitch;
+    int32_t *label_slot;    // [rows] place of the several rows' sum of l h; of a row that is alone ~(row of hidden)
+    int32_t *label_next;    // [rows] the next of the several, -1: none
+    int32_t *label_first;   // [places] the first of the several
+    int32_t *label_left;    // [places] how many are still to come
+    float *label_sum;       // [places][D]
+    const uint16_t *hidden, *weight;  // bf16: as the caller gave them
     int keep;               // with a gradient: keep e
     void *dh, *dw;
     float *acc;             // dW over the pieces, in tiles (see tile_slot)
@@ -109,6 +121,20 @@ __device__ __forceinline__ void ce_total(const CeTotals &t)
     }
     if (lane_id() == 0)
         *t.total = static_cast<float>(num / static_cast<double>(den > 1 ? den : 1));
+}
+
+// Eight bf16 values from memory times f, added to x.
+__device__ __forceinline__ void add_scaled8(float *x, float f, const uint4 &q)
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 v = ffma2(make_float2(f, f), make_float2(__uint_as_float(w[j] << 16),
+                                                              __uint_as_float(w[j] & 0xffff0000u)),
+                               make_float2(x[2 * j], x[2 * j + 1]));
+        x[2 * j] = v.x;
+        x[2 * j + 1] = v.y;
+    }
 }
 
 // Rows of the piece: device data, since the number of good rows is.

@@ -325,11 +325,124 @@ __device__ __forceinline__ float grad_scale(const CeArgs &a, int cnt, int m)
     return kWhat == kCeDh ? (m < cnt ? inv * a.row_scale[m] : 0.f) : inv;
 }
 
+// kN bf16 values of a row, from column col0 on, times f; `row` may end within them.
+template <int kN>
+__device__ __forceinline__ void add_scaled(float *x, float f, const uint16_t *row, int col0, int D)
+{
+    constexpr int kOnce = kN < 16 ? kN : 16;  // registers are short: more loads on their way spill
+#pragma unroll
+    for (int j0 = 0; j0 < kN; j0 += kOnce) {
+        uint4 q[kOnce / 8];
+#pragma unroll
+        for (int j = 0; j < kOnce; j += 8)
+            q[j / 8] = col0 + j0 + j < D ? *reinterpret_cast<const uint4 *>(row + col0 + j0 + j)
+                                         : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < kOnce; j += 8)
+            add_scaled8(x + j0 + j, f, q[j / 8]);
+    }
+}
+
+// The label's term of a row of dh, l w_y / T, for kN columns (bf16).
+struct LabelWord {
+    int64_t at;  // of w_y
+    float f;     // l / T; 0 where there is no row
+
+    __device__ __forceinline__ LabelWord(const CeArgs &a, int cnt, int m)
+    {
+        const int n = *a.n_good;
+        at = m < cnt ? static_cast<int64_t>(a.label[m]) * a.D : 0;
+        f = m < cnt ? a.label_grad[m] / static_cast<float>(n > 1 ? n : 1) : 0.f;
+    }
+    template <int kN>
+    __device__ __forceinline__ void add(const CeArgs &a, float *x, int col0) const
+    {
+        if (f != 0.f)
+            add_scaled<kN>(x, f, a.weight + at, col0, a.D);
+    }
+};
+
+// The labels' terms of dW (bf16): to word m0 + lane the rows r with that label
+// among [r0, r1) (multiples of 64, a chunk of the contraction) give l_r h_r, those of
+// a group of kCeGroup rows in one.  Which rows concern the warp's 32 words is marked
+// by a bit each, 1024 rows to a load.  Their places, as offsets to r0, are listed for
+// each word in the warp's staging memory while the products run; then each lane
+// takes its own, so that as many rows' loads are on their way as words have one.
+// dW of 5,734 rows of 151,936 takes 2 % longer with these terms, 11 % where every
+// label was read instead of the marks: 23 KB a tile and warp, into an SM whose
+// operands already fill its way to L2.
+constexpr int kListed = kCeAlone * (kChunkSteps<kCeDw, false> * kCeStep / kCeGroup + 1);
+static_assert(kListed * 64 + 128 <= kWarpStaging, "lists and their lengths");
+struct LabelRows {
+    uint16_t *list;  // [kListed][32]
+    int *count;      // [32]
+
+    __device__ __forceinline__ explicit LabelRows(uint8_t *staging)
+        : list(reinterpret_cast<uint16_t *>(staging + 128)), count(reinterpret_cast<int *>(staging))
+    {
+    }
+    __device__ __noinline__ void collect(const CeArgs &a, int m0, int r0, int r1, int lane) const
+    {
+        const uint32_t *marks = a.marks + static_cast<int64_t>(m0 / 32) * a.mark_pitch;
+        count[lane] = 0;
+        __syncwarp();
+        for (int w0 = r0 / 32; w0 < r1 / 32; w0 += 32) {
+            // each lane has the marks of 32 rows and takes them one by one
+            uint32_t mark = w0 + lane < r1 / 32 ? marks[w0 + lane] : 0;
+            while (__any_sync(0xffffffffu, mark != 0)) {
+                const bool live = mark != 0;
+                const int row = (w0 + lane) * 32 + __ffs(mark) - 1;
+                const int word = live ? a.label[row] - m0 : -1;
+                const unsigned same = __match_any_sync(0xffffffffu, word);
+                const int before = __popc(same & ((1u << lane) - 1));
+                const int place = live ? count[word] + before : 0;
+                __syncwarp();
+                if (live) {
+                    list[place * 32 + word] = static_cast<uint16_t>(row - r0);
+                    if (before == 0)
+                        count[word] += __popc(same);
+                }
+                __syncwarp();
+                mark &= mark - 1;
+            }
+        }
+    }
+    __device__ __forceinline__ void take(const CeArgs &a, float (&x)[kCols], int r0, int col0, int lane) const
+    {
+        const int n = count[lane];
+        for (int i = 0; i < n; ++i) {
+            const int r = r0 + list[i * 32 + lane], slot = a.label_slot[r];
+            const float l = a.label_grad[r];
+            if (slot < 0) {
+                add_scaled<kCols>(x, l, a.hidden + static_cast<int64_t>(~slot) * a.D, col0, a.D);
+            } else {
+                const float *sum = a.label_sum + static_cast<int64_t>(slot) * a.D + col0;
+                constexpr int kOnce = 8;
+#pragma unroll
+                for (int j0 = 0; j0 < kCols; j0 += kOnce) {
+                    float4 v[kOnce / 4];
+#pragma unroll
+                    for (int j = 0; j < kOnce; j += 4)
+                        v[j / 4] = col0 + j0 + j < a.D ? *reinterpret_cast<const float4 *>(sum + j0 + j)
+                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int j = 0; j < kOnce; j += 4) {
+                        x[j0 + j] += v[j / 4].x, x[j0 + j + 1] += v[j / 4].y;
+                        x[j0 + j + 2] += v[j / 4].z, x[j0 + j + 3] += v[j / 4].w;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    }
+};
+
 // dh and dW: scaled and rounded once.  dW over several pieces is kept
 // in fp32 until the last one.
 template <int kWhat, bool kSplit>
 __device__ __forceinline__ void finish_grad(const CeArgs &a, float (&x)[kCols], int cnt, int tile, int m, int col0,
-                                            int cta, int warp, int limit, uint8_t *staging, int lane)
+                                            int cta, int warp, int limit, const LabelWord &word, uint8_t *staging,
+                                            int lane)
 {
     if (kWhat == kCeDw && a.base > 0) {
         const float4 *acc = tile_slot(a.acc, tile, cta, warp, lane);
@@ -350,6 +463,8 @@ __device__ __forceinline__ void finish_grad(const CeArgs &a, float (&x)[kCols], 
 #pragma unroll
     for (int j = 0; j < kCols; ++j)
         x[j] *= inv;
+    if (kWhat == kCeDh && !kSplit && col0 < limit)
+        word.add<kCols>(a, x, col0);
     store_rows<kSplit>(x, kWhat == kCeDh ? a.dh : a.dw, grad_row<kWhat>(a, cnt, m), a.D, col0, min(limit, a.D), staging,
                        lane);
 }
@@ -368,8 +483,7 @@ __device__ __noinline__ void totals_by_warp(const CeTotals &t)
     ce_total(t);
 }
 
-// kParts: of B, in bf16.
-template <int kWhat, bool kSplit, int kParts>
+template <int kWhat, bool kSplit>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ce_product_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                       const __grid_constant__ CUtensorMap te, const __grid_constant__ CeArgs a, const WaitCfg w)
@@ -482,20 +596,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         s ^= 1;
                         parity ^= s == 0;
                     } else {
-#pragma unroll 1
-                        for (int part = kParts - 1; part >= 0; --part, ++it) {
-                            ok = ready(s, parity);
-                            if (!ok)
-                                break;
-                            if (cta == 0)
-                                mbar_expect_tx(&full[s], 2 * (kOperandBytes + b_bytes));
-                            uint8_t *to = smem + s * kStageBytes;
-                            load_a(to, bar0 + 8 * s, m0, kc, 0);
-                            load_b(to + kOperandBytes, bar0 + 8 * s, n0, kc, part);
-                            if (++s == kStages) {
-                                s = 0;
-                                parity ^= 1;
-                            }
+                        ok = ready(s, parity);
+                        if (!ok)
+                            break;
+                        if (cta == 0)
+                            mbar_expect_tx(&full[s], 2 * (kOperandBytes + b_bytes));
+                        uint8_t *to = smem + s * kStageBytes;
+                        load_a(to, bar0 + 8 * s, m0, kc, 0);
+                        load_b(to + kOperandBytes, bar0 + 8 * s, n0, kc, 0);
+                        ++it;
+                        if (++s == kStages) {
+                            s = 0;
+                            parity ^= 1;
                         }
                     }
                 }
@@ -543,11 +655,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t third = 0;  // parity
             bool ok = true;
             while (ok && units.next(u)) {
-                constexpr int per_step = kSplit ? 1 : kParts;
-                int left = (u.k1 - u.k0) * per_step;  // stages of this unit
+                int left = u.k1 - u.k0;  // steps of this unit
                 while (ok && left > 0) {
-                    constexpr int most = kChunkSteps<kWhat, kSplit> * per_step;
-                    const int n = left < most ? left : most;  // stages of this accumulation
+                    constexpr int most = kChunkSteps<kWhat, kSplit>;
+                    const int n = left < most ? left : most;  // steps of this accumulation
                     const uint32_t acc = chunk & 1, d = tbase + acc * 256;
                     if (*abort_flag || !mbar_wait_cluster(&acc_empty[acc], ((chunk >> 1) & 1) ^ 1, w, 0xa2)) {
                         ok = false;
@@ -619,8 +730,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < kCols; ++j)
                     x[j] = 0.f;
             }
+            [[maybe_unused]] LabelWord word(a, kWhat == kCeDh && !kSplit && !u.part ? cnt : 0, m);
+            const bool words = kWhat == kCeDw && !kSplit && m - lane < a.V && col < plan.cols && n0 + col < a.D;
             for (int c = 0; c < chunks; ++c, ++chunk) {
                 const uint32_t acc = chunk & 1;
+                const int r0 = (u.k0 + c * per) * kCeStep;  // dW: the chunk's first row
+                const LabelRows rows(stage);
+                if (words)  // while the products run
+                    rows.collect(a, m - lane, r0, min(r0 + per * kCeStep, u.k1 * kCeStep), lane);
                 if (!mbar_wait_warp(&acc_full[acc], (chunk >> 1) & 1, w, 0xa5)) {
                     ok = false;
                     break;
@@ -654,6 +771,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive_cluster_relaxed(cluster_addr(&acc_empty[acc], 0));
+                if (words)
+                    rows.take(a, x, r0, n0 + col, lane);
             }
             if (!ok)
                 break;
@@ -667,7 +786,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             } else if constexpr (kWhat == kCeLogits) {
                 finish_logits<kSplit>(a, &te, x, cnt, m, n0 + col, stage, lane);
             } else {
-                finish_grad<kWhat, kSplit>(a, x, cnt, u.tile, m, n0 + col, cta, warp, n0 + plan.cols, stage, lane);
+                finish_grad<kWhat, kSplit>(a, x, cnt, u.tile, m, n0 + col, cta, warp, n0 + plan.cols, word, stage,
+                                           lane);
             }
         }
         if (!ok)
@@ -770,6 +890,10 @@ __global__ void __launch_bounds__(kJoinThreads<kSplit, kGroups>) ce_join_kernel(
 #pragma unroll
         for (int j = 0; j < kPart; ++j)
             x[j] *= inv;
+        if constexpr (kWhat == kCeDh && !kSplit) {
+            if (col < limit)
+                LabelWord(a, cnt, m_slab + lane).template add<kPart>(a, x, col);
+        }
         if (row >= 0 && col < limit)
             *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(kWhat == kCeDh ? a.dh : a.dw) +
                                        (static_cast<int64_t>(row) * a.D + col) * (kSplit ? 4 : 2)) = unit<kSplit>(x);
@@ -805,11 +929,11 @@ bool make_exp_map(CUtensorMap *map, const CeArgs &a, int planes)
                   1, 64, 32);
 }
 
-template <int kWhat, bool kSplit, int kParts = 1>
+template <int kWhat, bool kSplit>
 cudaError_t launch(const CeArgs &a, const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &te,
                    cudaStream_t s)
 {
-    auto kernel = ce_product_kernel<kWhat, kSplit, kParts>;
+    auto kernel = ce_product_kernel<kWhat, kSplit>;
     // Pairs resident at once (the schedule gives each an equal share), asked
     // for once per device; two threads that ask at the same time find the same.
     static std::atomic<int> known[kCeMaxDevices];
@@ -881,11 +1005,8 @@ cudaError_t product(CeProduct what, const CeArgs &a, const void *h, int64_t ldh,
         return ok ? launch<kCeDh, kSplit>(a, ta, tb, te, s) : cudaErrorInvalidValue;
     default:
         ok = make_map(&ta, a.e, a.V, a.rows, a.ldg, planes, kCeStep) &&
-             make_map(&tb, h, a.D, a.rows, ldh, kSplit ? planes : a.h_planes, kCeStep);
-        if (!ok)
-            return cudaErrorInvalidValue;
-        return !kSplit && a.h_planes == 2 ? launch<kCeDw, kSplit, kSplit ? 1 : 2>(a, ta, tb, te, s)
-                                          : launch<kCeDw, kSplit>(a, ta, tb, te, s);
+             make_map(&tb, h, a.D, a.rows, ldh, planes, kCeStep);
+        return ok ? launch<kCeDw, kSplit>(a, ta, tb, te, s) : cudaErrorInvalidValue;
     }
 }
 
