@@ -390,6 +390,8 @@ def _token_stride(name, t, d) -> int:
     step = sT if Np > 1 else (sB if B > 1 else (sP if P > 1 else H * d))
     if not (ok and (B == 1 or sB == Np * step) and (P == 1 or sP == B * Np * step)):
         raise ValueError(f"{name}: heads must be contiguous and tokens evenly spaced, got strides {t.stride()}")
+    if step < H * d:  # an expanded view: the library would take its stride 0 for a contiguous tensor's
+        raise ValueError(f"{name}: every token must have memory of its own, got strides {t.stride()}")
     return step
 
 
