@@ -631,6 +631,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         mbar_wait(&full[kThird], (it - 1) & 1, w, 0xaf);
                 }
             }
+            // CTA 1 has followed the products up to here, so that this wait, too, is short
+            if (cta == 1)
+                mbar_wait(drain, 0, w, 0xa4);
         }
     } else if (warp == kEpiWarps + 1) {
         // ------------------------------------------------ products
@@ -708,8 +711,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (kWhat != kCeLogits && cta == 1 && pair == 0 && a.make_totals)
             totals_by_warp(a.totals);  // this CTA's issuer has nothing else to do
         __syncwarp();
-        if (lane == 0)
-            mbar_wait(drain, 0, w, 0xa4);  // in both CTAs: every product and release is through
+        if (lane == 0 && cta == 0)
+            mbar_wait(drain, 0, w, 0xa4);  // every product and release is through
     } else {
         // ------------------------------------------------ results
         Units units(plan, pair, pairs);
