@@ -372,6 +372,8 @@ def _rope_desc(inv_freq, positions, axis_of_freq, interleaved, shape):
         axis = np.ascontiguousarray(np.asarray(axis_of_freq, dtype=np.int32))
         if axis.shape != inv.shape:
             raise ValueError(f"axis_of_freq must name one axis per frequency, got shape {axis.shape}")
+        if positions is None and axis.size:
+            axes = max(int(axis.max()) + 1, 1)  # the token's index on every axis
     desc = _RopeDesc(None if positions is None else positions.data_ptr(), inv.__array_interface__["data"][0],
                      None if axis is None else axis.__array_interface__["data"][0], 2 * inv.shape[0], axes,
                      1 if interleaved else 0)
@@ -525,8 +527,8 @@ def ulysses_qkv_norm_rope_fwd(q_seq, k_seq, v_seq, q_out, k_out, v_out, P: int, 
     (to_head) or sequence layout, contiguous; v_seq and v_out may be None.
     inv_freq: rot_dim/2 frequencies (None: no rotation); positions: int64
     [P][B][N/P], or [axes][P][B][N/P] with axis_of_freq naming each
-    frequency's axis (None: the token's index).  q_weight and k_weight [d], or
-    None for both: no norm."""
+    frequency's axis (None: the token's index, on every axis).  q_weight and
+    k_weight [d], or None for both: no norm."""
     if (v_seq is None) != (v_out is None) or (q_weight is None) != (k_weight is None):
         raise ValueError("v_seq and v_out, and q_weight and k_weight, go together")
     _five(q_seq=q_seq, k_seq=k_seq)
