@@ -126,8 +126,9 @@ uly_status ulysses_swap_batch(const uly_swap_desc *descs_host, int32_t n_descs, 
  * and is the values (f, f + rot_dim/2) of the head (interleaved = 0) or
  * (2f, 2f + 1) (interleaved = 1); values from rot_dim on are not rotated:
  *   (a, b) -> (a cos t - b sin t, b cos t + a sin t).
- * Any int64 position is valid, negative ones too; the angle is formed modulo
- * a turn with an error below |position| * 2^-53 turns.
+ * Any int64 position and any finite frequency is valid, negative ones too; the
+ * angle is formed modulo a turn with an error below 2^-25 turns (the fp32
+ * argument of the sine) plus |position| * (2^-62 + 2^-106 |inv_freq|) turns.
  */
 typedef struct {
     const int64_t *positions;    /* device [num_axes][P][B][N/P] (8-byte aligned), or

@@ -12,10 +12,11 @@
 // Everything between the load and the store is fp32 and rounded once.
 //
 // Angles.  t / 2 pi is wanted modulo one turn.  inv_freq / 2 pi, reduced to
-// [0, 1), is held as a 64-bit fraction F; F * p modulo 2^64 (one 64-bit
-// integer product that wraps) is then the turn's fraction, exact up to
-// p * 2^-53 of a turn (the rounding of inv_freq / 2 pi itself), for negative
-// positions too.  A product in fp32 would be off by 0.06 rad at a million.
+// [0, 1), is held as a 64-bit fraction F; F * p modulo 2^64 (one 64-bit integer
+// product that wraps) is then the turn's fraction, exact up to |p| times F's own
+// error, 2^-62 and 2^-106 of inv_freq, for negative positions too.  A product in fp32
+// would be off by 0.06 rad at a million.  The upper 32 bits go to the sine in fp32,
+// which rounds them by up to 2^-26 of a turn.
 //
 // Memory-bound: every value is read and written once.  A warp takes one
 // token's rows, so that its cosines and sines are made once and shared by its
@@ -780,12 +781,22 @@ cudaError_t run_d(NormRopeParams &p, bool inter, bool bwd, cudaStream_t s)
 
 }  // namespace
 
+// The part of v behind the point as a 64-bit fraction, modulo 1.
+static uint64_t fraction(double v)
+{
+    const double f = std::ldexp(std::fabs(v - std::trunc(v)), 64);
+    return v < 0 ? 0 - static_cast<uint64_t>(f) : static_cast<uint64_t>(f);
+}
+
+// inv_freq / 2 pi in three parts: the product with the nearest double of 1 / 2 pi,
+// that product's rounding error, and the product with what is left of 1 / 2 pi
+// (0.159154943091895335768883763372514362...).  Each part is cut to 64 bits, and the
+// last one's rounding and what it leaves out are below 2^-108 of inv_freq.
 uint64_t turn_fraction(double inv_freq)
 {
-    double t = inv_freq * 0.15915494309189533577;  // turns per position
-    t -= std::floor(t);
-    const double f = std::ldexp(t, 64);
-    return f >= 18446744073709551616.0 ? 0ull : static_cast<uint64_t>(f);
+    constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+    const double p = inv_freq * kHi;
+    return fraction(p) + fraction(std::fma(inv_freq, kHi, -p)) + fraction(inv_freq * kLo);
 }
 
 cudaError_t launch_norm_rope(NormRopeParams &p, int d, bool inter, bool bwd, int esize, cudaStream_t s)
