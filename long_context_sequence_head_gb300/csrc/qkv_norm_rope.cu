@@ -34,19 +34,19 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-// Rows of a run (bytes) and resident blocks per SM; each warp has a ring of kRing
-// runs.  Where little is computed per byte (fp32, or no norm) fewer runs on their
-// way are better, or reads and writes get into each other's way.  us, bf16: 64K
-// tokens, 32 + 8 + 8 heads of 128; fp32: 32K tokens, 16 + 4 + 4.
+// Rows of a run (bytes) and resident blocks per SM; a warp has one run on its way.
+// Where little is computed per byte (fp32, or no norm) fewer runs on their way are
+// better, or reads and writes get into each other's way.  us with the caches emptied
+// before each call, bf16: 64K tokens, 32 + 8 + 8 heads of 128; fp32: 32K tokens, 16 +
+// 4 + 4.
 //   forward, normed   249 (6 KB x 5 blocks), 259 (6 KB x 6), 261 (4 KB x 5), 264 (6
-//                     KB x 4), 286 (4 KB x 4), 257 (rings of two, 4 KB x 4, which
+//                     KB x 4), 286 (4 KB x 4), 257 (two runs a warp, 4 KB x 4, which
 //                     take 42 us at 8K tokens instead of 44)
 //   not normed        249 (4 KB x 4), 256 (4 KB x 5), 268 (6 KB x 5)
 //   fp32              132 (4 KB x 4), 131 (4 KB x 5), 138 (6 KB x 5)
 //   backward, normed  359 (4 KB x 5), 364 (x 4), over 430 with 2 KB or spills
 //   not normed        246 (4 KB x 4), 258 (x 5), 274 (x 3)
 //   fp32              180 (4 KB x 4), 190 (x 5), 195 (x 3)
-constexpr int kRing = 1;
 template <typename T, bool kNorm>
 constexpr bool kLight = sizeof(T) == 4 || !kNorm;
 template <typename T, bool kNorm>
@@ -347,24 +347,23 @@ struct Cursor {
     }
 };
 
-// The ring a warp keeps: kRing slots of kParts runs.
-template <int kRing, int kParts, int kRunBytes>
-struct Ring {
+// Where a warp's run lands: kParts times kRunBytes, and the barrier of its copies.
+template <int kParts, int kRunBytes>
+struct Landing {
     uint8_t *data;
-    uint64_t *bars;
+    uint64_t *bar;
 
-    __device__ __forceinline__ Ring(uint8_t *smem, int warp, int lane)
+    __device__ __forceinline__ Landing(uint8_t *smem, int warp, int lane)
     {
-        data = smem + warp * (kRing * kParts * kRunBytes);
-        bars = reinterpret_cast<uint64_t *>(smem + kWarps * (kRing * kParts * kRunBytes)) + warp * kRing;
+        data = smem + warp * (kParts * kRunBytes);
+        bar = reinterpret_cast<uint64_t *>(smem + kWarps * (kParts * kRunBytes)) + warp;
         if (lane == 0) {
-            for (int i = 0; i < kRing; ++i)
-                mbar_init(&bars[i], 1);
+            mbar_init(bar, 1);
             fence_mbar_init();
         }
         __syncwarp();
     }
-    static constexpr int kBytes = kWarps * kRing * (kParts * kRunBytes + 8);
+    static constexpr int kBytes = kWarps * (kParts * kRunBytes + 8);
 };
 
 template <typename T, int kD, bool kInter, bool kNorm>
@@ -386,39 +385,38 @@ __global__ void __launch_bounds__(kThreads, Fwd<T, kNorm>::kBlocks)
         }
     }
     __syncthreads();
-    const Ring<kRing, 1, kRunBytes> ring(smem, warp, lane);
+    const Landing<1, kRunBytes> run(smem, warp, lane);
     int lo, hi;
     chunk_places<S, kInter>(p.half, lane % S::kLanes, lo, hi);
     Cursor<S> now(p, blockIdx.x * kWarps + warp, gridDim.x * kWarps);
     Cursor<S> ahead = now;
-    auto fetch = [&](int slot) {  // a copy per tensor
+    auto fetch = [&] {  // a copy per tensor
         if (lane == 0)
-            mbar_expect_tx(&ring.bars[slot], (ahead.row1(p) - ahead.row0()) * kD * sizeof(T));
+            mbar_expect_tx(run.bar, (ahead.row1(p) - ahead.row0()) * kD * sizeof(T));
         __syncwarp();
         int h0, h1, row;
         ahead.heads(p, lane, h0, h1, row);
         if (lane < 3 && h0 < h1) {
             const T *src = static_cast<const T *>(lane == 0 ? p.q : (lane == 1 ? p.k : p.v)) +
                            ahead.k.m * (lane == 0 ? p.qs : (lane == 1 ? p.ks : p.vs)) + h0 * kD;
-            bulk_g2s(ring.data + slot * kRunBytes + row * kD * sizeof(T), src, (h1 - h0) * kD * sizeof(T),
-                     &ring.bars[slot]);
+            bulk_g2s(run.data + row * kD * sizeof(T), src, (h1 - h0) * kD * sizeof(T), run.bar);
         }
         ahead.step(p);
     };
-    int started = 0, done = 0;  // runs fetched and worked on
-    for (; started < kRing && ahead.more(); ++started)
-        fetch(started);
+    if (ahead.more())
+        fetch();
+    uint32_t phase = 0;
     Angles<kD> at;
     int last = -1;
     Turn<S, kInter, false, kNorm> turn;
     Far far;
     while (now.more()) {
-        const int slot = done % kRing;
         if (now.row0() < p.Hq + p.Hkv && at.make(p, freqs, now.k, now.k.m + now.stride, table[warp], lane))
             last = -1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&ring.bars[slot], (done / kRing) & 1, wait, 0xb1)))
+        if (!__all_sync(0xffffffffu, mbar_wait(run.bar, phase, wait, 0xb1)))
             break;
-        const T *data = reinterpret_cast<const T *>(ring.data + slot * kRunBytes);
+        phase ^= 1;
+        const T *data = reinterpret_cast<const T *>(run.data);
 #pragma unroll 1
         for (int t = 0; t < 2; ++t) {
             int h0, h1, row;
@@ -478,17 +476,13 @@ __global__ void __launch_bounds__(kThreads, Fwd<T, kNorm>::kBlocks)
                 store_row<T>(static_cast<T *>(p.vo) + far.at(h, kD), lo, hi,
                              load_row<T>(data + (row + h - h0) * kD, lo, hi));
         }
-        __syncwarp();  // the slot is read
-        if (ahead.more()) {
-            fetch(slot);
-            ++started;
-        }
-        ++done;
+        __syncwarp();  // the run is read
+        if (ahead.more())
+            fetch();
         now.step(p);
     }
-    // after a wait that ran out: the copies still on their way (bounded)
-    for (; done < started; ++done)
-        mbar_wait(&ring.bars[done % kRing], (done / kRing) & 1, wait, 0xbf);
+    if (now.more())  // after a wait that ran out: the copies still on their way (bounded)
+        mbar_wait(run.bar, phase, wait, 0xbf);
 }
 
 template <typename T, int kD, bool kInter, bool kNorm>
@@ -511,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, Bwd<T, kNorm>::kBlocks)
     }
     __syncthreads();
     constexpr int kParts = kNorm ? 2 : 1;  // a run of dy and one of x
-    const Ring<kRing, kParts, kRunBytes> ring(smem, warp, lane);
+    const Landing<kParts, kRunBytes> run(smem, warp, lane);
     int lo, hi;
     chunk_places<S, kInter>(p.half, lane % S::kLanes, lo, hi);
     // the warp's part of dw, kept between runs: [q, k][slot][d]
@@ -524,12 +518,12 @@ __global__ void __launch_bounds__(kThreads, Bwd<T, kNorm>::kBlocks)
     __syncwarp();
     Cursor<S> now(p, blockIdx.x * kWarps + warp, gridDim.x * kWarps);
     Cursor<S> ahead = now;
-    auto fetch = [&](int slot) {
+    auto fetch = [&] {
         // Lanes 0, 1, 2 (mod 4): dy of Q, K and V, a copy per rank; lanes 3 and 7: x of Q and K
-        uint8_t *to = ring.data + slot * (kParts * kRunBytes);
+        uint8_t *to = run.data;
         const int row0 = ahead.row0(), row1 = ahead.row1(p), xrows = max(min(row1, p.Hq + p.Hkv) - row0, 0);
         if (lane == 0)
-            mbar_expect_tx(&ring.bars[slot], (row1 - row0 + (kNorm ? xrows : 0)) * kD * sizeof(T));
+            mbar_expect_tx(run.bar, (row1 - row0 + (kNorm ? xrows : 0)) * kD * sizeof(T));
         __syncwarp();
         const int kind = lane & 3, t = kind < 3 ? kind : lane >> 2;
         int h0, h1, row;
@@ -542,27 +536,27 @@ __global__ void __launch_bounds__(kThreads, Bwd<T, kNorm>::kBlocks)
                 if (a >= b)
                     break;
                 bulk_g2s(to + (row + a - h0) * kD * sizeof(T), src + far.at(a, kD), (b - a) * kD * sizeof(T),
-                         &ring.bars[slot]);
+                         run.bar);
             }
         } else if (kNorm && t < 2 && h0 < h1) {
             bulk_g2s(to + kRunBytes + row * kD * sizeof(T),
                      static_cast<const T *>(t ? p.k : p.q) + ahead.k.m * (t ? p.ks : p.qs) + h0 * kD,
-                     (h1 - h0) * kD * sizeof(T), &ring.bars[slot]);
+                     (h1 - h0) * kD * sizeof(T), run.bar);
         }
         ahead.step(p);
     };
-    int started = 0, done = 0;
-    for (; started < kRing && ahead.more(); ++started)
-        fetch(started);
+    if (ahead.more())
+        fetch();
+    uint32_t phase = 0;
     Angles<kD> at;
     Turn<S, kInter, true, false> turn;
     while (now.more()) {
-        const int slot = done % kRing;
         if (now.row0() < p.Hq + p.Hkv && at.make(p, freqs, now.k, now.k.m + now.stride, table[warp], lane))
             turn.load(table[warp], p.half, lo, hi);
-        if (!__all_sync(0xffffffffu, mbar_wait(&ring.bars[slot], (done / kRing) & 1, wait, 0xb2)))
+        if (!__all_sync(0xffffffffu, mbar_wait(run.bar, phase, wait, 0xb2)))
             break;
-        const T *data = reinterpret_cast<const T *>(ring.data + slot * (kParts * kRunBytes));
+        phase ^= 1;
+        const T *data = reinterpret_cast<const T *>(run.data);
 #pragma unroll 1
         for (int t = 0; t < 2; ++t) {
             int h0, h1, row;
@@ -644,17 +638,13 @@ __global__ void __launch_bounds__(kThreads, Bwd<T, kNorm>::kBlocks)
             for (int h = h0 + sub; h < h1; h += S::kRows)
                 store_row<T>(out + h * kD, lo, hi, load_row<T>(data + (row + h - h0) * kD, lo, hi));
         }
-        __syncwarp();  // the slot is read
-        if (ahead.more()) {
-            fetch(slot);
-            ++started;
-        }
-        ++done;
+        __syncwarp();  // the run is read
+        if (ahead.more())
+            fetch();
         now.step(p);
     }
-    // after a wait that ran out: the copies still on their way (bounded)
-    for (; done < started; ++done)
-        mbar_wait(&ring.bars[done % kRing], (done / kRing) & 1, wait, 0xbf);
+    if (now.more())  // after a wait that ran out: the copies still on their way (bounded)
+        mbar_wait(run.bar, phase, wait, 0xbf);
     if constexpr (kNorm) {
         // the block's weight-gradient partial: row slots and warps, always in the same order
         __syncthreads();
@@ -728,7 +718,7 @@ cudaError_t run(NormRopeParams &p, bool bwd, cudaStream_t s)
     // every warp has had the same number of whole ones: 2048 tokens of 32 + 8 + 8
     // heads 25.3 us (parts for as many warps as there are 31.5), 4095 fp32 ones of
     // 12 + 6 + 6 25.1 (all whole 27.4).  In the forward the parts' angles cost
-    // what their rounds save (8192 tokens 43.7 us either way).
+    // what their rounds save (8192 tokens 43.7 us either way; caches emptied).
     const int64_t warps = resident * kWarps;
     p.whole = bwd || p.tokens < warps ? p.tokens / warps * warps : p.tokens;
     const int64_t rest = p.tokens - p.whole;
@@ -750,7 +740,7 @@ cudaError_t run(NormRopeParams &p, bool bwd, cudaStream_t s)
     const int64_t grid = std::min<int64_t>((p.whole + (p.tokens - p.whole) * p.splits + kWarps - 1) / kWarps, resident);
     if (!bwd) {
         auto kernel = norm_rope_fwd_kernel<T, kD, kInter, kNorm>;
-        constexpr int smem = Ring<kRing, 1, kFwdRun>::kBytes;
+        constexpr int smem = Landing<1, kFwdRun>::kBytes;
         static_assert(smem <= 40 * 1024, "with the static part, what a launch may take without asking");
         kernel<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p, wait_cfg());
         return cudaGetLastError();
@@ -758,7 +748,7 @@ cudaError_t run(NormRopeParams &p, bool bwd, cudaStream_t s)
     if (grid > kNormRopeMaxBlocks)
         return cudaErrorInvalidConfiguration;
     auto kernel = norm_rope_bwd_kernel<T, kD, kInter, kNorm>;
-    constexpr int smem = Ring<kRing, kNorm ? 2 : 1, kBwdRun>::kBytes;
+    constexpr int smem = Landing<kNorm ? 2 : 1, kBwdRun>::kBytes;
     static_assert(smem + static_cast<int>(sizeof(float)) * 24 * kD <= 48 * 1024, "as above");
     kernel<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p, wait_cfg());
     const cudaError_t e = cudaGetLastError();
