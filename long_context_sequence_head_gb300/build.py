@@ -8,9 +8,10 @@ long_context_sequence_head_gb300.build`` or through ``__graft_entry__.build()``.
 
 ``build(debug=True)`` compiles the same sources with ``-DULY_DEBUG`` into
 ``_build/debug/libulysses_gb300_debug.so``: every raw-pointer global access of
-the swap and attention kernels is checked against its buffer and a failure is
-reported as a status (ULY_ERR_BOUNDS) instead of being made.  The binding
-loads it when ULY_DEBUG_BUILD=1.
+the swap and attention kernels, and those of the norm-rotation and LM-head loss
+kernels whose place depends on data or on the schedule, are checked against their
+buffers and a failure is reported as a status (ULY_ERR_BOUNDS) instead of being
+made.  The binding loads it when ULY_DEBUG_BUILD=1.
 """
 from __future__ import annotations
 

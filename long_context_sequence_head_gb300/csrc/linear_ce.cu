@@ -187,7 +187,9 @@ __global__ void __launch_bounds__(1024) labels_kernel(const int64_t *__restrict_
                 row_loss[first + i] = 0.f;
             }
             if (y[i] >= 0) {
-                index[at++] = static_cast<int32_t>(first + i);
+                if (ULY_IN_BOUNDS(status, at, 1, rows, 0x51))
+                    index[at] = static_cast<int32_t>(first + i);
+                ++at;
                 if (!one)
                     atomicAdd(&good[static_cast<unsigned>(first + i) / (Np * B)], 1ull);
             }
@@ -269,8 +271,10 @@ __device__ __forceinline__ void group_labels(const CeArgs &a, int cnt, int r0, c
     __syncthreads();
     if (y < 0)
         return;
-    if (stands || !several)
-        atomicOr(&a.marks[static_cast<int64_t>(y / 32) * a.mark_pitch + r / 32], 1u << (r % 32));
+    const int64_t mark = static_cast<int64_t>(y / 32) * a.mark_pitch + r / 32;
+    if ((stands || !several) &&
+        ULY_IN_BOUNDS(a.status, mark, 1, static_cast<int64_t>((a.V + 31) / 32) * a.mark_pitch, 0x52))
+        atomicOr(&a.marks[mark], 1u << (r % 32));
     a.label_slot[r] = several ? label[first] : static_cast<int32_t>(~src);
     a.label_next[r] = next < kCeGroup ? r0 + next : -1;
 }
@@ -295,7 +299,8 @@ __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ CeA
     }
     const int64_t at = (static_cast<int64_t>(blockIdx.x) - groups) * blockDim.x + threadIdx.x, r = at / vecs;
     const int i = static_cast<int>(at - r * vecs) * 8;
-    if (a.base == 0 && a.dh != nullptr && r < rows && shifted[r] < 0) {
+    if (a.base == 0 && a.dh != nullptr && r < rows && shifted[r] < 0 &&
+        ULY_IN_BOUNDS(a.status, r * a.D + i, kSplit ? 4 : 8, rows * a.D, 0x53)) {
         uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.dh) + (r * a.D + i) * (kSplit ? 4 : 2));
         to[0] = make_uint4(0, 0, 0, 0);
         if (kSplit && i + 4 < a.D)
@@ -305,6 +310,9 @@ __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ CeA
         return;
     const bool live = r < cnt;
     const int64_t src = live ? a.index[a.base + r] : 0;
+    if (!ULY_IN_BOUNDS(a.status, src * a.D + i, kSplit ? 4 : 8, rows * a.D, 0x54) ||
+        !ULY_IN_BOUNDS(a.status, r * ldh + i, 8, ldh * a.rows, 0x55))
+        return;
     if (i == 0)
         label[r] = live ? shifted[src] : -1;
     lay8<kSplit>(live ? hidden : nullptr, src, i, a.D, out, r, ldh, ldh * a.rows);
@@ -345,7 +353,9 @@ __device__ __forceinline__ void sum_label_terms(const CeArgs &a, int slot)
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const bool live = r >= 0;
-                const int64_t row = live ? a.index[a.base + r] : 0;
+                int64_t row = live ? a.index[a.base + r] : 0;
+                if (!ULY_IN_BOUNDS(a.status, row, 1, a.all_rows, 0x57))
+                    row = 0;
                 q[k] = live ? *reinterpret_cast<const uint4 *>(a.hidden + row * a.D + col) : make_uint4(0, 0, 0, 0);
                 l[k] = live ? __ldcg(&a.label_grad[r]) : 0.f;
                 r = live ? a.label_next[r] : -1;
@@ -354,6 +364,8 @@ __device__ __forceinline__ void sum_label_terms(const CeArgs &a, int slot)
             for (int k = 0; k < kAhead; ++k)
                 add_scaled8(sum, l[k], q[k]);
         }
+        if (!ULY_IN_BOUNDS(a.status, static_cast<int64_t>(slot) * a.D + col, 8, a.places * a.D, 0x56))
+            continue;
         float4 *to = reinterpret_cast<float4 *>(a.label_sum + static_cast<int64_t>(slot) * a.D + col);
         to[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
         to[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
@@ -412,6 +424,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         st.join(red[w].C, red[w].S, red[w].least);
     const int y = label[r];
     const int64_t row = a.index[a.base + r];
+    if (!ULY_IN_BOUNDS(a.status, row, 1, a.all_rows, 0x58) || !ULY_IN_BOUNDS(a.status, y, 1, a.V, 0x59))
+        return;  // the whole block agrees
     const int slot = !kSplit && a.marks != nullptr ? a.label_slot[r] : -1;
     if (threadIdx.x == 0) {
         // ln S + C ln 2 - x_y, with the whole powers of two taken out of x_y before anything is rounded
@@ -483,7 +497,7 @@ size_t up(size_t x) { return (x + 255) & ~size_t(255); }
 struct Layout {
     size_t good, n_good, shifted, row_loss, index, label, target, row_scale, label_grad, stats, h, w, e, acc, partial;
     size_t marks, label_slot, label_next, label_first, label_left, label_sum, total;
-    int64_t ldh, ldg;
+    int64_t ldh, ldg, acc_slots, partial_slots, places;
     int rows, stat_tiles;
 };
 
@@ -516,19 +530,20 @@ Layout layout(int64_t B, int64_t N, int D, int V, int P, bool grad, int esize)
     if (grad) {
         take(L.e, planes * kept * 2);
         const size_t tiles = static_cast<size_t>((V + kCeTile - 1) / kCeTile) * ((D + kCeTile - 1) / kCeTile);
-        if (T > L.rows)
-            take(L.acc, sizeof(float) * kCeTileFloats * tiles);
-        const int parts =
+        L.acc_slots = T > L.rows ? tiles : 0;
+        take(L.acc, sizeof(float) * kCeTileFloats * L.acc_slots);
+        L.partial_slots =
             std::max(ce_most_parts(kCeDh, L.rows, D, V, esize), ce_most_parts(kCeDw, L.rows, D, V, esize));
-        take(L.partial, sizeof(float) * kCeTileFloats * parts);
+        take(L.partial, sizeof(float) * kCeTileFloats * L.partial_slots);
         if (!split) {
-            const size_t groups = ce_groups(L.rows), places = groups * (kCeGroup / 2);  // sums of two rows at least
+            const size_t groups = ce_groups(L.rows);
+            L.places = groups * (kCeGroup / 2);  // sums of two rows at least
             take(L.marks, sizeof(uint32_t) * (kCeGroup / 32) * groups * ((V + 31) / 32));
             take(L.label_slot, sizeof(int32_t) * L.rows);
             take(L.label_next, sizeof(int32_t) * L.rows);
-            take(L.label_first, sizeof(int32_t) * places);
-            take(L.label_left, sizeof(int32_t) * places);
-            take(L.label_sum, sizeof(float) * places * D);
+            take(L.label_first, sizeof(int32_t) * L.places);
+            take(L.label_left, sizeof(int32_t) * L.places);
+            take(L.label_sum, sizeof(float) * L.places * D);
         }
     }
     L.total = o;
@@ -579,6 +594,11 @@ cudaError_t run(const void *hidden, const void *weight, const int64_t *labels, v
     a.acc = reinterpret_cast<float *>(ws + L.acc);
     a.partial = reinterpret_cast<float *>(ws + L.partial);
     a.totals = CeTotals{row_loss, good, rows / P, P, shard_loss, total, shard_good};
+    a.all_rows = rows;
+    a.acc_slots = L.acc_slots;
+    a.partial_slots = L.partial_slots;
+    a.places = L.places;
+    a.status = device_status_ptr();
     labels_kernel<<<1, 1024, 0, s>>>(labels, shifted, good, row_loss, index, a.n_good, static_cast<unsigned>(rows),
                                      static_cast<unsigned>(N / P), static_cast<unsigned>(B), P, V,
                                      device_status_ptr());

@@ -71,6 +71,10 @@ struct CeArgs {
     float *partial;         // tiles split over the contraction
     int make_totals;        // this product's idle warp makes the totals
     CeTotals totals;
+    // for the bounds checks of debug builds
+    int64_t all_rows;                            // of hidden
+    int64_t acc_slots, partial_slots, places;    // of acc and partial, in tiles; of label_sum
+    unsigned *status;                            // device status word
 };
 
 // A sum held as hi + lo: 48 bits without the slow 64-bit units.

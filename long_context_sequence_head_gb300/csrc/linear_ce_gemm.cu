@@ -173,8 +173,11 @@ __device__ __forceinline__ void tile_origin(const Plan &p, int tile, int &m0, in
 // A tile's fp32 values in memory, as the writers hold them: per CTA and warp
 // 16 groups of 4 columns, each 32 rows x 16 bytes, so that a warp's access is
 // 512 bytes in a row.
-__device__ __forceinline__ float4 *tile_slot(float *buf, int64_t slot, int cta, int warp, int lane)
+__device__ __forceinline__ float4 *tile_slot(float *buf, int64_t slot, int cta, int warp, int lane,
+                                             [[maybe_unused]] int64_t slots, [[maybe_unused]] unsigned *status)
 {
+    if (!ULY_IN_BOUNDS(status, slot, 1, slots, 0x64))
+        slot = 0;  // there is one where there is a slot to ask for
     return reinterpret_cast<float4 *>(buf + slot * kCeTileFloats) + (cta * kEpiWarps + warp) * (kCols / 4 * 32) + lane;
 }
 
@@ -193,11 +196,12 @@ __device__ __forceinline__ uint4 unit(const float *v)
 // The warp's 32 rows x 64 columns (row = lane) to memory, 128 bytes of a row
 // per 8 lanes: through shared memory, units of 16 bytes permuted within the
 // row so that neither side meets a bank conflict.  row: where this lane's row
-// goes, negative: nowhere.  Columns from `limit` on are not written (a
-// multiple of 16 bytes).
+// goes, negative: nowhere; the tensor has `rows`.  Columns from `limit` on are not
+// written (a multiple of 16 bytes).
 template <bool kF32>
-__device__ __forceinline__ void store_rows(const float (&x)[kCols], void *out, int row, int64_t pitch, int col0,
-                                           int limit, uint8_t *staging, int lane)
+__device__ __forceinline__ void store_rows(const float (&x)[kCols], void *out, int row, [[maybe_unused]] int64_t rows,
+                                           int64_t pitch, int col0, int limit, uint8_t *staging, int lane,
+                                           [[maybe_unused]] unsigned *status)
 {
     constexpr int kPer = kF32 ? 4 : 8;  // values per unit
 #pragma unroll
@@ -214,7 +218,7 @@ __device__ __forceinline__ void store_rows(const float (&x)[kCols], void *out, i
         for (int i = 0; i < 8; ++i) {
             const int r = 4 * i + (lane >> 3), at = __shfl_sync(0xffffffffu, row, r);
             const uint4 val = *reinterpret_cast<const uint4 *>(staging + r * 128 + ((u ^ (r & 7)) << 4));
-            if (at >= 0 && col < limit)
+            if (at >= 0 && col < limit && ULY_IN_BOUNDS(status, at * pitch + col, kPer, rows * pitch, 0x61))
                 *reinterpret_cast<uint4 *>(to + at * (pitch * (16 / kPer))) = val;
         }
         __syncwarp();
@@ -268,7 +272,7 @@ __device__ __forceinline__ void finish_logits(const CeArgs &a, const CUtensorMap
         return;
     const bool live = m < cnt;
     const int y = live ? a.label[m] : -1;
-    if (y >= col0 && y < col0 + kCols) {
+    if (y >= col0 && y < col0 + kCols && ULY_IN_BOUNDS(a.status, m, 1, a.rows, 0x62)) {
 #pragma unroll
         for (int j = 0; j < kCols; ++j)
             if (y == col0 + j)
@@ -301,8 +305,9 @@ __device__ __forceinline__ void finish_logits(const CeArgs &a, const CUtensorMap
         ps[(j >> 1) & 3] = fadd2(ps[(j >> 1) & 3], make_float2(x[j], x[j + 1]));
     }
     const float2 s = fadd2(fadd2(ps[0], ps[1]), fadd2(ps[2], ps[3]));
-    if (live)
-        a.stats[static_cast<int64_t>(m) * a.stat_tiles + col0 / kCeStatCols] = make_float2(c, s.x + s.y);
+    const int64_t stat = static_cast<int64_t>(m) * a.stat_tiles + col0 / kCeStatCols;
+    if (live && ULY_IN_BOUNDS(a.status, stat, 1, static_cast<int64_t>(a.rows) * a.stat_tiles, 0x63))
+        a.stats[stat] = make_float2(c, s.x + s.y);
     if (a.keep)
         store_exponentials<kSplit>(a, te, x, m - lane, col0, staging, lane);
 }
@@ -353,6 +358,8 @@ struct LabelWord {
         const int n = *a.n_good;
         at = m < cnt ? static_cast<int64_t>(a.label[m]) * a.D : 0;
         f = m < cnt ? a.label_grad[m] / static_cast<float>(n > 1 ? n : 1) : 0.f;
+        if (!ULY_IN_BOUNDS(a.status, at, a.D, static_cast<int64_t>(a.V) * a.D, 0x65))
+            at = 0;
     }
     template <int kN>
     __device__ __forceinline__ void add(const CeArgs &a, float *x, int col0) const
@@ -413,6 +420,8 @@ struct LabelRows {
         for (int i = 0; i < n; ++i) {
             const int r = r0 + list[i * 32 + lane], slot = a.label_slot[r];
             const float l = a.label_grad[r];
+            if (!ULY_IN_BOUNDS(a.status, slot < 0 ? ~slot : slot, 1, slot < 0 ? a.all_rows : a.places, 0x66))
+                continue;
             if (slot < 0) {
                 add_scaled<kCols>(x, l, a.hidden + static_cast<int64_t>(~slot) * a.D, col0, a.D);
             } else {
@@ -445,7 +454,7 @@ __device__ __forceinline__ void finish_grad(const CeArgs &a, float (&x)[kCols], 
                                             int lane)
 {
     if (kWhat == kCeDw && a.base > 0) {
-        const float4 *acc = tile_slot(a.acc, tile, cta, warp, lane);
+        const float4 *acc = tile_slot(a.acc, tile, cta, warp, lane, a.acc_slots, a.status);
 #pragma unroll
         for (int j = 0; j < kCols / 4; ++j) {
             const float4 v = acc[j * 32];
@@ -453,7 +462,7 @@ __device__ __forceinline__ void finish_grad(const CeArgs &a, float (&x)[kCols], 
         }
     }
     if (kWhat == kCeDw && a.base + a.rows < *a.n_good) {
-        float4 *acc = tile_slot(a.acc, tile, cta, warp, lane);
+        float4 *acc = tile_slot(a.acc, tile, cta, warp, lane, a.acc_slots, a.status);
 #pragma unroll
         for (int j = 0; j < kCols / 4; ++j)
             acc[j * 32] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
@@ -465,8 +474,8 @@ __device__ __forceinline__ void finish_grad(const CeArgs &a, float (&x)[kCols], 
         x[j] *= inv;
     if (kWhat == kCeDh && !kSplit && col0 < limit)
         word.add<kCols>(a, x, col0);
-    store_rows<kSplit>(x, kWhat == kCeDh ? a.dh : a.dw, grad_row<kWhat>(a, cnt, m), a.D, col0, min(limit, a.D), staging,
-                       lane);
+    store_rows<kSplit>(x, kWhat == kCeDh ? a.dh : a.dw, grad_row<kWhat>(a, cnt, m), kWhat == kCeDh ? a.all_rows : a.V,
+                       a.D, col0, min(limit, a.D), staging, lane, a.status);
 }
 
 // The call's totals by one warp alone.
@@ -782,7 +791,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (u.part) {
                 if (kWhat == kCeDh && m - lane >= cnt)
                     continue;  // nobody reads these rows
-                float4 *slot = tile_slot(a.partial, pair, cta, warp, lane);
+                float4 *slot = tile_slot(a.partial, pair, cta, warp, lane, a.partial_slots, a.status);
 #pragma unroll
                 for (int j = 0; j < kCols / 4; ++j)
                     slot[j * 32] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
@@ -851,7 +860,7 @@ __global__ void __launch_bounds__(kJoinThreads<kSplit, kGroups>) ce_join_kernel(
         const int each = (p.runs + kGroups - 1) / kGroups, r0 = group * each, r1 = min(p.runs, r0 + each);
 #pragma unroll 4
         for (int r = r0; r < r1; ++r) {
-            const float4 *slot = tile_slot(a.partial, r * p.rem + split, cta, slab, lane);
+            const float4 *slot = tile_slot(a.partial, r * p.rem + split, cta, slab, lane, a.partial_slots, a.status);
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
                 const float4 v = slot[(part * kVecs + j) * 32];
@@ -873,15 +882,16 @@ __global__ void __launch_bounds__(kJoinThreads<kSplit, kGroups>) ce_join_kernel(
 #pragma unroll
             for (int j = 0; j < kPart; ++j)
                 x[j] += sums[g][part][j][lane];
-        if (kWhat == kCeDw) {
-            float4 *acc = tile_slot(a.acc, tile, cta, slab, lane) + part * kVecs * 32;
+        const bool more = a.base + a.rows < *a.n_good;  // rows to come
+        if (kWhat == kCeDw && (a.base > 0 || more)) {
+            float4 *acc = tile_slot(a.acc, tile, cta, slab, lane, a.acc_slots, a.status) + part * kVecs * 32;
             if (a.base > 0)
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j) {
                     const float4 v = acc[j * 32];
                     x[4 * j] += v.x, x[4 * j + 1] += v.y, x[4 * j + 2] += v.z, x[4 * j + 3] += v.w;
                 }
-            if (a.base + a.rows < *a.n_good) {
+            if (more) {
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j)
                     acc[j * 32] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
@@ -897,7 +907,9 @@ __global__ void __launch_bounds__(kJoinThreads<kSplit, kGroups>) ce_join_kernel(
             if (col < limit)
                 LabelWord(a, cnt, m_slab + lane).template add<kPart>(a, x, col);
         }
-        if (row >= 0 && col < limit)
+        if (row >= 0 && col < limit &&
+            ULY_IN_BOUNDS(a.status, static_cast<int64_t>(row) * a.D + col, kSplit ? 4 : 8,
+                          (kWhat == kCeDh ? a.all_rows : a.V) * a.D, 0x67))
             *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(kWhat == kCeDh ? a.dh : a.dw) +
                                        (static_cast<int64_t>(row) * a.D + col) * (kSplit ? 4 : 2)) = unit<kSplit>(x);
     }

@@ -148,6 +148,13 @@ struct Freqs {
     }
 };
 
+// Extents (elements) of a near tensor of H heads whose tokens are `stride` apart,
+// for the bounds checks of debug builds.
+[[maybe_unused]] __device__ __forceinline__ int64_t near_extent(const NormRopeParams &p, int64_t stride, int H, int d)
+{
+    return (p.tokens - 1) * stride + static_cast<int64_t>(H) * d;
+}
+
 // cos and sin of a token's rot/2 angles in the warp's shared table.  A lane
 // makes at most two; the positions of the next token are read while this one
 // is worked on.
@@ -157,23 +164,28 @@ struct Angles {
     uint32_t held, made;  // the token whose positions these are, and the one the table is of
 
     __device__ __forceinline__ Angles() : held(~0u), made(~0u) {}
-    __device__ __forceinline__ void read(const NormRopeParams &p, const Freqs<kD> &fr, uint32_t m, int lane)
+    __device__ __forceinline__ void read(const NormRopeParams &p, const Freqs<kD> &fr, uint32_t m, int lane,
+                                         [[maybe_unused]] unsigned *status)
     {
         held = m;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (lane + 32 * i < p.half)
-                pos[i] = p.positions[fr.axis[lane + 32 * i] * p.tokens + m];
+        for (int i = 0; i < 2; ++i) {
+            if (lane + 32 * i >= p.half)
+                continue;
+            const int64_t off = fr.axis[lane + 32 * i] * p.tokens + m;
+            if (ULY_IN_BOUNDS(status, off, 1, p.axes * p.tokens, 0x41))
+                pos[i] = p.positions[off];
+        }
     }
     // true if the table is new; `next`: the warp's next token
     __device__ __forceinline__ bool make(const NormRopeParams &p, const Freqs<kD> &fr, const Token &k, uint32_t next,
-                                         float2 *table, int lane)
+                                         float2 *table, int lane, unsigned *status)
     {
         if (made == k.m)
             return false;
         made = k.m;
         if (p.positions && held != k.m)
-            read(p, fr, k.m, lane);
+            read(p, fr, k.m, lane, status);
         __syncwarp();  // the last token's reads are done
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -188,7 +200,7 @@ struct Angles {
         }
         __syncwarp();
         if (p.positions && next < p.tokens)
-            read(p, fr, next, lane);
+            read(p, fr, next, lane, status);
         return true;
     }
 };
@@ -397,8 +409,11 @@ __global__ void __launch_bounds__(kThreads, Fwd<T, kNorm>::kBlocks)
         int h0, h1, row;
         ahead.heads(p, lane, h0, h1, row);
         if (lane < 3 && h0 < h1) {
-            const T *src = static_cast<const T *>(lane == 0 ? p.q : (lane == 1 ? p.k : p.v)) +
-                           ahead.k.m * (lane == 0 ? p.qs : (lane == 1 ? p.ks : p.vs)) + h0 * kD;
+            const T *src = static_cast<const T *>(lane == 0 ? p.q : (lane == 1 ? p.k : p.v));
+            const int64_t stride = lane == 0 ? p.qs : (lane == 1 ? p.ks : p.vs), off = ahead.k.m * stride + h0 * kD;
+            // (a check that fails is reported and the first token's rows are copied, which the barrier counts on)
+            if (ULY_IN_BOUNDS(wait.status, off, (h1 - h0) * kD, near_extent(p, stride, lane ? p.Hkv : p.Hq, kD), 0x42))
+                src += off;
             bulk_g2s(run.data + row * kD * sizeof(T), src, (h1 - h0) * kD * sizeof(T), run.bar);
         }
         ahead.step(p);
@@ -411,7 +426,8 @@ __global__ void __launch_bounds__(kThreads, Fwd<T, kNorm>::kBlocks)
     Turn<S, kInter, false, kNorm> turn;
     Far far;
     while (now.more()) {
-        if (now.row0() < p.Hq + p.Hkv && at.make(p, freqs, now.k, now.k.m + now.stride, table[warp], lane))
+        if (now.row0() < p.Hq + p.Hkv && at.make(p, freqs, now.k, now.k.m + now.stride, table[warp], lane,
+                                                  wait.status))
             last = -1;
         if (!__all_sync(0xffffffffu, mbar_wait(run.bar, phase, wait, 0xb1)))
             break;
@@ -463,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, Fwd<T, kNorm>::kBlocks)
                         y[j] = fmul2(y[j], both(rstd));
                     }
                 }
-                if (h < h1)
+                if (h < h1 && ULY_IN_BOUNDS(wait.status, far.at(h, kD), kD, p.tokens * (t ? p.Hkv : p.Hq) * kD, 0x43))
                     store_row<T>(out + far.at(h, kD), lo, hi, Raw{pack<T>(x), pack<T>(y)});
             }
         }
@@ -473,8 +489,9 @@ __global__ void __launch_bounds__(kThreads, Fwd<T, kNorm>::kBlocks)
             far = now.far(p, 2);
 #pragma unroll 2
             for (int h = h0 + sub; h < h1; h += S::kRows)
-                store_row<T>(static_cast<T *>(p.vo) + far.at(h, kD), lo, hi,
-                             load_row<T>(data + (row + h - h0) * kD, lo, hi));
+                if (ULY_IN_BOUNDS(wait.status, far.at(h, kD), kD, p.tokens * p.Hkv * kD, 0x44))
+                    store_row<T>(static_cast<T *>(p.vo) + far.at(h, kD), lo, hi,
+                                 load_row<T>(data + (row + h - h0) * kD, lo, hi));
         }
         __syncwarp();  // the run is read
         if (ahead.more())
@@ -535,12 +552,16 @@ __global__ void __launch_bounds__(kThreads, Bwd<T, kNorm>::kBlocks)
                 const int a = max(h0, i * far.per), b = min(h1, (i + 1) * far.per);
                 if (a >= b)
                     break;
-                bulk_g2s(to + (row + a - h0) * kD * sizeof(T), src + far.at(a, kD), (b - a) * kD * sizeof(T),
+                const bool ok = ULY_IN_BOUNDS(wait.status, far.at(a, kD), (b - a) * kD,
+                                              p.tokens * (t ? p.Hkv : p.Hq) * kD, 0x45);
+                bulk_g2s(to + (row + a - h0) * kD * sizeof(T), src + (ok ? far.at(a, kD) : 0), (b - a) * kD * sizeof(T),
                          run.bar);
             }
         } else if (kNorm && t < 2 && h0 < h1) {
-            bulk_g2s(to + kRunBytes + row * kD * sizeof(T),
-                     static_cast<const T *>(t ? p.k : p.q) + ahead.k.m * (t ? p.ks : p.qs) + h0 * kD,
+            const int64_t stride = t ? p.ks : p.qs, off = ahead.k.m * stride + h0 * kD;
+            const bool ok =
+                ULY_IN_BOUNDS(wait.status, off, (h1 - h0) * kD, near_extent(p, stride, t ? p.Hkv : p.Hq, kD), 0x46);
+            bulk_g2s(to + kRunBytes + row * kD * sizeof(T), static_cast<const T *>(t ? p.k : p.q) + (ok ? off : 0),
                      (h1 - h0) * kD * sizeof(T), run.bar);
         }
         ahead.step(p);
@@ -551,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, Bwd<T, kNorm>::kBlocks)
     Angles<kD> at;
     Turn<S, kInter, true, false> turn;
     while (now.more()) {
-        if (now.row0() < p.Hq + p.Hkv && at.make(p, freqs, now.k, now.k.m + now.stride, table[warp], lane))
+        if (now.row0() < p.Hq + p.Hkv && at.make(p, freqs, now.k, now.k.m + now.stride, table[warp], lane,
+                                                  wait.status))
             turn.load(table[warp], p.half, lo, hi);
         if (!__all_sync(0xffffffffu, mbar_wait(run.bar, phase, wait, 0xb2)))
             break;
@@ -563,7 +585,8 @@ __global__ void __launch_bounds__(kThreads, Bwd<T, kNorm>::kBlocks)
             now.heads(p, t, h0, h1, row);
             if (h0 >= h1)
                 continue;
-            T *out = static_cast<T *>(t ? p.dk : p.dq) + static_cast<int64_t>(now.k.m) * (t ? p.dks : p.dqs);
+            const int64_t stride = t ? p.dks : p.dqs, near = static_cast<int64_t>(now.k.m) * stride;
+            T *out = static_cast<T *>(t ? p.dk : p.dq);
             const T *rows = data + (row - h0) * kD, *xrows = rows + kRunBytes / sizeof(T);
             float2 w[2][S::kP], sum[2][S::kP];
             if (kNorm) {
@@ -609,8 +632,9 @@ __global__ void __launch_bounds__(kThreads, Bwd<T, kNorm>::kBlocks)
                             g[c][j] = fmul2(ffma2(x[c][j], both(-m), fmul2(w[c][j], g[c][j])), both(rstd));
                         }
                 }
-                if (live)
-                    store_row<T>(out + h * kD, lo, hi, Raw{pack<T>(g[0]), pack<T>(g[1])});
+                if (live && ULY_IN_BOUNDS(wait.status, near + h * kD, kD,
+                                          near_extent(p, stride, t ? p.Hkv : p.Hq, kD), 0x47))
+                    store_row<T>(out + near + h * kD, lo, hi, Raw{pack<T>(g[0]), pack<T>(g[1])});
             }
             if (kNorm) {
                 float *to = reinterpret_cast<float *>(sums[warp]) + (t * kSlots + sub) * kD;
@@ -633,10 +657,12 @@ __global__ void __launch_bounds__(kThreads, Bwd<T, kNorm>::kBlocks)
         int h0, h1, row;
         now.heads(p, 2, h0, h1, row);
         if (h0 < h1) {
-            T *out = static_cast<T *>(p.dv) + static_cast<int64_t>(now.k.m) * p.dvs;
+            const int64_t near = static_cast<int64_t>(now.k.m) * p.dvs;
 #pragma unroll 2
             for (int h = h0 + sub; h < h1; h += S::kRows)
-                store_row<T>(out + h * kD, lo, hi, load_row<T>(data + (row + h - h0) * kD, lo, hi));
+                if (ULY_IN_BOUNDS(wait.status, near + h * kD, kD, near_extent(p, p.dvs, p.Hkv, kD), 0x48))
+                    store_row<T>(static_cast<T *>(p.dv) + near + h * kD, lo, hi,
+                                 load_row<T>(data + (row + h - h0) * kD, lo, hi));
         }
         __syncwarp();  // the run is read
         if (ahead.more())
@@ -655,7 +681,9 @@ __global__ void __launch_bounds__(kThreads, Bwd<T, kNorm>::kBlocks)
 #pragma unroll
                 for (int k = 0; k < kSlots; ++k)
                     v += reinterpret_cast<const float *>(sums[w])[(i / kD * kSlots + k) * kD + i % kD];
-            p.partial[static_cast<int64_t>(blockIdx.x) * 2 * kD + i] = v;
+            const int64_t off = static_cast<int64_t>(blockIdx.x) * 2 * kD + i;
+            if (ULY_IN_BOUNDS(wait.status, off, 1, kNormRopeMaxBlocks * 2 * kD, 0x49))
+                p.partial[off] = v;
         }
     }
 }

@@ -229,6 +229,7 @@ struct NormRopeParams {
     void *dwq, *dwk;      // their gradients, each may be null
     float *partial;       // [blocks][2][d]
     const int64_t *positions;  // [axes][P][B][N/P] or null
+    int axes;
     int64_t tokens;            // P * B * N/P
     int64_t N;
     int Np, B;  // tokens per shard, sequences

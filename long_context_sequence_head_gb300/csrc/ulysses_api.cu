@@ -215,6 +215,7 @@ uly_status check_norm_rope(uly::NormRopeParams &p, int64_t B, int64_t N, int32_t
     if (reinterpret_cast<uintptr_t>(rope->positions) % 8 != 0)
         return ULY_ERR_MISALIGNED;
     p.positions = rope->positions;
+    p.axes = rope->num_axes;
     p.tokens = B * N;
     p.N = N;
     p.Np = static_cast<int>(N / P);
