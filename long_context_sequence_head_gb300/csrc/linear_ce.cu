@@ -388,9 +388,10 @@ struct Stat {
 
 // One block per row of the piece: its loss, and with a gradient the row's scale
 // 1 / S, the label's term, the row of h' (where dW is wanted), and e on one c where
-// it is not yet.
+// it is not yet.  32 registers a thread, so that blocks are set up beside the
+// logits' product (with 40 the loss of 64 rows takes 154 us instead of 150.5).
 template <bool kSplit>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ CeArgs a,
+__global__ void __launch_bounds__(kRowThreads, 16) rows_kernel(const __grid_constant__ CeArgs a,
                                                            const void *__restrict__ hidden,
                                                            const int32_t *__restrict__ label,
                                                            float *__restrict__ row_loss, uint16_t *__restrict__ out,
