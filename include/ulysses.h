@@ -450,7 +450,9 @@ uly_status ulysses_sharded_ce_loss(const void *logits, const int64_t *labels, vo
  * softmax's numerators and, for dweight, the hidden rows divided by its
  * denominators are rounded to bf16; each gradient is rounded to bf16 once.
  * fp32: operands are taken as three bf16 parts each, off by less than 2^-26 of a
- * value (values above 3.39e38, bf16's largest, count as infinite).
+ * value or 2^-134, what is more (values above 3.39e38, bf16's largest, count as
+ * infinite).  Numerators reach 2^48, and their sums with weight and hidden are
+ * formed before the division: values above 2^58 may overflow.
  * D * element size a multiple of 16 bytes, D <= 65536, V <= 2^21
  * (ULY_ERR_UNSUPPORTED otherwise); N % P == 0.
  */

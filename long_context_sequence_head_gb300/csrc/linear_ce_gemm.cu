@@ -11,11 +11,11 @@
 // K-major, one whose rows run along the output (W in dh; e and h in dW) is
 // MN-major.
 //
-// Measured (5,734 rows with labels, D = 2560, V = 151,936, bf16): logits 2.57
-// ms, dh 2.55, dW 2.41, that is 1.74 to 1.85 PFLOP/s against 1.90 of the
+// Measured (5,734 rows with labels, D = 2560, V = 151,936, bf16): logits 2.52
+// ms, dh 2.54, dW 2.47, that is 1.75 to 1.81 PFLOP/s against 1.90 of the
 // library's product in a burst; back to back the card's power limit sets the
 // clock (the same products of a constant matrix take 2.1 ms).  At D = 776 and V =
-// 50,257 (4,830 rows) the tensor cores are busy 0.64 to 0.76 of 291, 294 and 266
+// 50,257 (4,830 rows) the tensor cores are busy 0.64 to 0.76 of 289, 287 and 277
 // us: a step of 64 brings 32 KB to every SM, which at 64 bytes a clock takes the
 // 512 clocks of its products.  With half the products issued the three take 269,
 // 311 and 252 us, with half the loads 251, 242 and 248; narrower tiles (224
