@@ -198,6 +198,69 @@ uly_status ulysses_qkv_norm_rope_bwd(const void *q_seq, const void *k_seq, const
                                      const uly_rope_desc *rope_host, float eps, int32_t to_head,
                                      uly_dtype dtype, void *workspace, size_t workspace_bytes, void *stream);
 
+/* -------------------------------------------------- norms around a block */
+
+/*
+ * What stands between two blocks of a model (attention and its output
+ * projection, or a feed-forward layer; the pages leave it to the model), in one
+ * pass over the sequence-sharded tokens: the RMS norm behind a block, its gate
+ * and residual scale, the sum with the residual stream, and the RMS norm before
+ * the next block.  For a token's rows x (residual stream) and y (the block's
+ * output):
+ *   u = post_weight * y / sqrt(mean(y^2) + eps)    (u = y without post_weight)
+ *   h = x + residual_scale * gate * u
+ *   z = weight * h / sqrt(mean(h^2) + eps)
+ * in fp32, h and z rounded once (z is formed from h before its rounding).
+ * Without a block (y NULL: the norm before a model's first block) h is x.
+ *
+ * x, y           : device [P][B][N/P][D], read only; y may be NULL, then
+ *                  post_weight, gate and h are NULL too.
+ * weight, post_weight : device [D]; post_weight may be NULL (no norm behind the block).
+ * gate           : device [gate_rows][D] or NULL: gate_rows = 1, one vector for
+ *                  every token; gate_rows = B, one for each sequence; 0 with NULL.
+ * h, z           : device, like x.  h may be NULL (the last norm of a model).
+ * rstd           : device fp32 [2][P][B][N/P], 1/sqrt(mean + eps) of h and of y
+ *                  (1 without post_weight) for the backward, or NULL.
+ * No output may overlap an input or another output.
+ * N % P == 0, B * N < 2^31 tokens, a row (D elements) a multiple of 16 bytes
+ * and at most 32768 (ULY_ERR_UNSUPPORTED otherwise); eps >= 0.  One token
+ * (N = P = 1) is an ordinary call.
+ */
+uly_status ulysses_residual_norm_fwd(const void *x, const void *y, const void *weight, const void *post_weight,
+                                     const void *gate, int32_t gate_rows, float residual_scale, float eps, void *h,
+                                     void *z, float *rstd, int64_t B, int64_t N, int32_t D, int32_t P,
+                                     uly_dtype dtype, void *stream);
+
+/* Bytes of device workspace ulysses_residual_norm_bwd needs (0 for sizes it would reject). */
+size_t ulysses_residual_norm_workspace_size(int64_t B, int64_t N, int32_t D, int32_t P);
+
+/*
+ * Its backward.  With hhat and yhat the rows times their rstd (yhat = y without
+ * post_weight):
+ *   t  = dh + rstd_h (weight*dz - hhat mean(weight*dz*hhat)) = dx
+ *   du = residual_scale * gate * t
+ *   dy = rstd_y (post_weight*du - yhat mean(post_weight*du*yhat))   (dy = du without post_weight)
+ *   dweight = sum dz*hhat,  dpost_weight = sum du*yhat,
+ *   dgate = sum residual_scale * t * u over the tokens that share the gate.
+ *
+ * x, y, weight, post_weight, gate, gate_rows, residual_scale : as in the forward
+ *                  (h is formed again from x and y); rstd : from the forward.
+ * dh             : device, gradient of h from elsewhere, or NULL (none; without
+ *                  a block it is what else the gradient of x holds).
+ * dz             : device, gradient of z.
+ * dx, dy         : device, like x, written; dy NULL if and only if y is.
+ * dweight, dpost_weight [D], dgate [gate_rows][D] : device, written; each may be
+ *                  NULL.  Summed in fp32 in an order that depends on the sizes alone.
+ * workspace      : device, >= ulysses_residual_norm_workspace_size bytes; may be
+ *                  NULL if all three are.  Calls that may run at the same time
+ *                  need workspaces of their own.
+ */
+uly_status ulysses_residual_norm_bwd(const void *x, const void *y, const void *weight, const void *post_weight,
+                                     const void *gate, int32_t gate_rows, float residual_scale, const float *rstd,
+                                     const void *dh, const void *dz, void *dx, void *dy, void *dweight,
+                                     void *dpost_weight, void *dgate, int64_t B, int64_t N, int32_t D, int32_t P,
+                                     uly_dtype dtype, void *workspace, size_t workspace_bytes, void *stream);
+
 /* ------------------------------------------------------------ attention */
 
 /*

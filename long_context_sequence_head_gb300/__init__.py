@@ -33,6 +33,7 @@ _STATUS = {0: "ULY_OK", 1: "ULY_ERR_INVALID_ARG", 2: "ULY_ERR_UNSUPPORTED", 3: "
 # every symbol include/ulysses.h declares
 EXPORTED = ("ulysses_seq_to_head", "ulysses_head_to_seq", "ulysses_swap_batch", "ulysses_attn_workspace_size",
             "ulysses_qkv_norm_rope_workspace_size", "ulysses_qkv_norm_rope_fwd", "ulysses_qkv_norm_rope_bwd",
+            "ulysses_residual_norm_workspace_size", "ulysses_residual_norm_fwd", "ulysses_residual_norm_bwd",
             "ulysses_attn_tile_order",
             "ulysses_attn_fwd", "ulysses_attn_bwd", "ulysses_attn_fwd_seq", "ulysses_attn_bwd_seq",
             "ulysses_attn_bwd_noalloc", "ulysses_sharded_ce_workspace_size", "ulysses_sharded_ce_loss",
@@ -105,6 +106,12 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.ulysses_qkv_norm_rope_bwd.argtypes = ([vp] * 12 + [i64, i64, i32, i32, i32, i32] + [i64] * 5
                                               + [vp, f32, i32, i32, vp, sz, vp])
     lib.ulysses_qkv_norm_rope_bwd.restype = i32
+    lib.ulysses_residual_norm_workspace_size.argtypes = [i64, i64, i32, i32]
+    lib.ulysses_residual_norm_workspace_size.restype = sz
+    lib.ulysses_residual_norm_fwd.argtypes = [vp] * 5 + [i32, f32, f32] + [vp] * 3 + [i64, i64, i32, i32, i32, vp]
+    lib.ulysses_residual_norm_fwd.restype = i32
+    lib.ulysses_residual_norm_bwd.argtypes = ([vp] * 5 + [i32, f32] + [vp] * 8 + [i64, i64, i32, i32, i32, vp, sz, vp])
+    lib.ulysses_residual_norm_bwd.restype = i32
     lib.ulysses_sharded_linear_ce_workspace_size.argtypes = [i64, i64, i32, i32, i32, i32, i32]
     lib.ulysses_sharded_linear_ce_workspace_size.restype = sz
     lib.ulysses_sharded_linear_ce_loss.argtypes = [vp] * 8 + [i64, i64, i32, i32, i32, i32, vp, sz, vp]
@@ -611,6 +618,104 @@ def ulysses_qkv_norm_rope_bwd(q_seq, k_seq, dq_out, dk_out, dv_out, dq_seq, dk_s
             ctypes.addressof(desc), eps, 1 if to_head else 0, _dt(dq_seq), _ptr(ws),
             0 if ws is None else ws.nbytes, at.raw()))
     return dq_seq, dk_seq, dv_seq
+
+
+# --------------------------------------------------- norms around a block
+
+def ulysses_residual_norm_workspace_size(B: int, N: int, D: int, P: int) -> int:
+    return int(load().ulysses_residual_norm_workspace_size(B, N, D, P))
+
+
+def _residual_norm_args(x, P, rows, weights, gate, rstd):
+    """Shapes, types and devices of a call; returns (B, N/P, D, rows of the gate)."""
+    if x is None or x.dim() != 4 or x.shape[0] != P:
+        raise ValueError(f"x must be [P={P}][B][N/P][D], got {None if x is None else tuple(x.shape)}")
+    _, B, Np, D = x.shape
+    dtype, device = x.dtype, x.get_device()
+    if device < 0:
+        raise ValueError("tensors must live on a CUDA device")
+
+    def check(name, t, want, kind):
+        if t.shape != want or t.dtype is not kind:
+            raise ValueError(f"{name} must be {list(want)} of {kind}, got {list(t.shape)} of {t.dtype}")
+        if t.get_device() != device:
+            raise ValueError(f"all tensors must live on {x.device}, got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+
+    for name, t in rows:
+        if t is not None:
+            check(name, t, x.shape, dtype)
+    for name, t in weights:
+        if t is not None:
+            check(name, t, (D,), dtype)
+    gate_rows = 0
+    for name, t in gate:
+        if t is not None:
+            if gate[0][1] is None:
+                raise ValueError(f"{name} without a gate")
+            check(name, t, (D,) if gate[0][1].dim() == 1 else (B, D), dtype)
+            gate_rows = 1 if t.dim() == 1 else B
+    if rstd is not None:
+        check("rstd", rstd, (2, P, B, Np), torch.float32)
+    return B, Np, D, gate_rows
+
+
+def ulysses_residual_norm_fwd(x, y, h, z, P: int, weight, post_weight: Optional[torch.Tensor] = None,
+                              gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                              rstd: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None):
+    """The norm behind a block, its gate and residual scale, the sum with the
+    residual stream and the norm before the next block (see include/ulysses.h).
+
+    x, y, h, z [P][B][N/P][D]: residual stream and block output in, their sum and
+    its norm out; y (then h, post_weight and gate too) may be None before the
+    first block, h behind the last.  weight, post_weight [D]; gate [D], or [B][D]
+    with a row for each sequence; rstd [2][P][B][N/P] fp32 is filled for the
+    backward if given.  Returns (h, z, rstd)."""
+    if z is None or weight is None:
+        raise ValueError("z and weight are required")
+    if y is None and not (h is None and post_weight is None and gate is None):
+        raise ValueError("without y there is no h, post_weight or gate")
+    B, Np, D, gate_rows = _residual_norm_args(
+        x, P, (("x", x), ("y", y), ("h", h), ("z", z)), (("weight", weight), ("post_weight", post_weight)),
+        (("gate", gate),), rstd)
+    with _Launch(x.device, stream) as at:
+        _check("ulysses_residual_norm_fwd", load().ulysses_residual_norm_fwd(
+            x.data_ptr(), _ptr(y), weight.data_ptr(), _ptr(post_weight), _ptr(gate), gate_rows, residual_scale, eps,
+            _ptr(h), z.data_ptr(), _ptr(rstd), B, Np * P, D, P, _dt(x), at.raw()))
+    return h, z, rstd
+
+
+def ulysses_residual_norm_bwd(x, y, dh, dz, dx, dy, P: int, weight, rstd, post_weight: Optional[torch.Tensor] = None,
+                              gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                              dweight: Optional[torch.Tensor] = None, dpost_weight: Optional[torch.Tensor] = None,
+                              dgate: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                              stream=None):
+    """Backward of ulysses_residual_norm_fwd: x, y and rstd are the forward's,
+    dh (may be None) and dz the gradients of its outputs; writes dx, dy (None
+    without y) and, if given, the gradients of the weights and the gate."""
+    if weight is None or rstd is None or dz is None or dx is None:
+        raise ValueError("weight, rstd, dz and dx are required")
+    if (y is None) != (dy is None):
+        raise ValueError("y and dy go together")
+    if y is None and not (post_weight is None and gate is None):
+        raise ValueError("without y there is no post_weight or gate")
+    if dpost_weight is not None and post_weight is None:
+        raise ValueError("dpost_weight without post_weight")
+    B, Np, D, gate_rows = _residual_norm_args(
+        x, P, (("x", x), ("y", y), ("dh", dh), ("dz", dz), ("dx", dx), ("dy", dy)),
+        (("weight", weight), ("post_weight", post_weight), ("dweight", dweight), ("dpost_weight", dpost_weight)),
+        (("gate", gate), ("dgate", dgate)), rstd)
+    sums = dweight is not None or dpost_weight is not None or dgate is not None
+    with _Launch(x.device, stream) as at:
+        # the library checks the size of a workspace that is given
+        need = 0 if workspace is not None or not sums else ulysses_residual_norm_workspace_size(B, Np * P, D, P)
+        ws = at.scratch(workspace, need) if sums else None
+        _check("ulysses_residual_norm_bwd", load().ulysses_residual_norm_bwd(
+            x.data_ptr(), _ptr(y), weight.data_ptr(), _ptr(post_weight), _ptr(gate), gate_rows, residual_scale,
+            rstd.data_ptr(), _ptr(dh), dz.data_ptr(), dx.data_ptr(), _ptr(dy), _ptr(dweight), _ptr(dpost_weight),
+            _ptr(dgate), B, Np * P, D, P, _dt(x), _ptr(ws), 0 if ws is None else ws.nbytes, at.raw()))
+    return dx, dy
 
 
 # -------------------------------------------------------------- attention

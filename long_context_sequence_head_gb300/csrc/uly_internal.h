@@ -249,6 +249,31 @@ struct NormRopeParams {
 uint64_t turn_fraction(double inv_freq);
 cudaError_t launch_norm_rope(NormRopeParams &p, int d, bool inter, bool bwd, int esize, cudaStream_t s);
 
+// ------------------------------------------------- norms around a block
+struct ResidualNormParams {
+    const void *x, *y;           // residual stream, block output (null: none)
+    const void *w1, *w2, *gate;  // norm weights, the gate's rows; w2 and gate may be null
+    void *h, *z;                 // forward outputs; h may be null
+    float *rstd_out;             // forward: [2][T] or null
+    const float *rstd;           // backward
+    const void *dh, *dz;         // dh may be null
+    void *dx, *dy;
+    void *dw1, *dw2, *dgate;     // each may be null
+    float scale, eps;
+    int64_t T;    // tokens
+    int64_t run;  // neighbouring tokens that share a gate: N/P with a gate for every sequence, else T
+    int gates;    // rows of gate: 0, 1 or B
+    int D;
+    // set by the launch: threads a row has and the lanes its sums are taken over
+    // first, rows and stages of the ring, the blocks' sums
+    int per_row, lanes, rows, stages;
+    float *part1, *partA;  // [blocks][rows][D], [blocks + runs][rows][D]
+    int64_t part1_elems, partA_elems;
+    WaitCfg w;
+};
+size_t residual_norm_workspace(int64_t T, int64_t Np, int D);
+cudaError_t launch_residual_norm(ResidualNormParams &p, bool bwd, int esize, void *workspace, cudaStream_t s);
+
 // ------------------------------------------------------- sharded loss
 cudaError_t launch_sharded_ce(const void *logits, const int64_t *labels, void *dlogits, float *shard_loss,
                               int64_t *shard_good, float *total, int64_t B, int64_t N, int64_t V, int P, int esize,

@@ -239,6 +239,50 @@ uly_status check_linear_ce(int64_t B, int64_t N, int32_t D, int32_t V, int32_t P
     return ULY_OK;
 }
 
+// Sizes and pointers shared by ulysses_residual_norm_fwd and _bwd; fills p.
+uly_status check_residual_norm(uly::ResidualNormParams &p, const void *x, const void *y, const void *weight,
+                               const void *post_weight, const void *gate, int32_t gate_rows, float scale, int64_t B,
+                               int64_t N, int32_t D, int32_t P, uly_dtype dt)
+{
+    if (B < 1 || N < 1 || D < 1 || P < 1 || N % P != 0 || esize_of(dt) == 0 || !std::isfinite(scale) || !x || !weight)
+        return ULY_ERR_INVALID_ARG;
+    if ((gate == nullptr) != (gate_rows == 0) || (gate_rows != 0 && gate_rows != 1 && gate_rows != B) ||
+        (y == nullptr && (post_weight || gate)))
+        return ULY_ERR_INVALID_ARG;
+    const int64_t most = (int64_t(1) << 31) - 1;
+    const int64_t row = static_cast<int64_t>(D) * esize_of(dt);
+    if (B > most || N > most || B * N > most || row > 32768 || row % 16 != 0)
+        return ULY_ERR_UNSUPPORTED;
+    p.x = x, p.y = y, p.w1 = weight, p.w2 = post_weight, p.gate = gate;
+    p.scale = scale;
+    p.T = B * N;
+    p.run = gate_rows > 1 ? N / P : p.T;
+    p.gates = gate_rows;
+    p.D = D;
+    return ULY_OK;
+}
+
+// The status of buffers that are misaligned, or of an output that shares bytes
+// with an input or another output.
+uly_status check_buffers(const Rows *in, int n_in, const Rows *out, int n_out)
+{
+    for (int i = 0; i < n_in + n_out; ++i)
+        if (!aligned16(i < n_in ? in[i].p : out[i - n_in].p))
+            return ULY_ERR_MISALIGNED;
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = 0; j < n_in; ++j)
+            if (rows_overlap(out[i], in[j]))
+                return ULY_ERR_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (rows_overlap(out[i], out[j]))
+                return ULY_ERR_OVERLAP;
+    }
+    return ULY_OK;
+}
+
+// A contiguous buffer of `bytes` bytes as one row.
+Rows whole(const void *p, int64_t bytes) { return Rows{p, 1, bytes, bytes}; }
+
 // A token stride in elements (0: contiguous); false if it is too small or not a multiple of 16 bytes.
 bool token_stride(int64_t given, int H, int d, int es, int64_t &out)
 {
@@ -471,6 +515,74 @@ uly_status ulysses_qkv_norm_rope_bwd(const void *q_seq, const void *k_seq, const
     p.partial = static_cast<float *>(workspace);
     return from_cuda(uly::launch_norm_rope(p, d, rope_host->interleaved != 0, true, es,
                                            static_cast<cudaStream_t>(stream)));
+}
+
+size_t ulysses_residual_norm_workspace_size(int64_t B, int64_t N, int32_t D, int32_t P)
+{
+    if (B < 1 || N < 1 || D < 1 || P < 1 || N % P != 0 || B > (int64_t(1) << 31) - 1 ||
+        N > (int64_t(1) << 31) - 1 || B * N > (int64_t(1) << 31) - 1 || D > 16384)
+        return 0;
+    return uly::residual_norm_workspace(B * N, N / P, D);
+}
+
+uly_status ulysses_residual_norm_fwd(const void *x, const void *y, const void *weight, const void *post_weight,
+                                     const void *gate, int32_t gate_rows, float residual_scale, float eps, void *h,
+                                     void *z, float *rstd, int64_t B, int64_t N, int32_t D, int32_t P,
+                                     uly_dtype dtype, void *stream)
+{
+    ULY_NVTX_RANGE();
+    if (!z || (h && !y) || !(eps >= 0.f) || !std::isfinite(eps))
+        return ULY_ERR_INVALID_ARG;
+    uly::ResidualNormParams p = {};
+    uly_status st = check_residual_norm(p, x, y, weight, post_weight, gate, gate_rows, residual_scale, B, N, D, P, dtype);
+    if (st != ULY_OK)
+        return st;
+    const int64_t row = static_cast<int64_t>(D) * esize_of(dtype), all = p.T * row;
+    const Rows in[5] = {whole(x, all), whole(y, all), whole(weight, row), whole(post_weight, row),
+                        whole(gate, gate_rows * row)};
+    const Rows out[3] = {whole(h, all), whole(z, all), whole(rstd, p.T * 8)};
+    st = check_buffers(in, 5, out, 3);
+    if (st != ULY_OK)
+        return st;
+    if (uly::device_status_ptr() == nullptr)
+        return ULY_ERR_CUDA;
+    p.h = h, p.z = z, p.rstd_out = rstd, p.eps = eps;
+    return from_cuda(uly::launch_residual_norm(p, false, esize_of(dtype), nullptr, static_cast<cudaStream_t>(stream)));
+}
+
+uly_status ulysses_residual_norm_bwd(const void *x, const void *y, const void *weight, const void *post_weight,
+                                     const void *gate, int32_t gate_rows, float residual_scale, const float *rstd,
+                                     const void *dh, const void *dz, void *dx, void *dy, void *dweight,
+                                     void *dpost_weight, void *dgate, int64_t B, int64_t N, int32_t D, int32_t P,
+                                     uly_dtype dtype, void *workspace, size_t workspace_bytes, void *stream)
+{
+    ULY_NVTX_RANGE();
+    const bool sums = dweight || dpost_weight || dgate;
+    if (!rstd || !dz || !dx || (y == nullptr) != (dy == nullptr) || (dpost_weight && !post_weight) ||
+        (dgate && !gate) || (sums && !workspace))
+        return ULY_ERR_INVALID_ARG;
+    uly::ResidualNormParams p = {};
+    uly_status st = check_residual_norm(p, x, y, weight, post_weight, gate, gate_rows, residual_scale, B, N, D, P, dtype);
+    if (st != ULY_OK)
+        return st;
+    const int64_t row = static_cast<int64_t>(D) * esize_of(dtype), all = p.T * row;
+    const size_t need = ulysses_residual_norm_workspace_size(B, N, D, P);
+    const Rows in[8] = {whole(x, all),           whole(y, all),      whole(weight, row), whole(post_weight, row),
+                        whole(gate, gate_rows * row), whole(rstd, p.T * 8), whole(dh, all),     whole(dz, all)};
+    const Rows out[6] = {whole(dx, all),           whole(dy, all),
+                         whole(dweight, row),      whole(dpost_weight, row),
+                         whole(dgate, gate_rows * row), whole(sums ? workspace : nullptr, static_cast<int64_t>(need))};
+    st = check_buffers(in, 8, out, 6);
+    if (st != ULY_OK)
+        return st;
+    if (sums && workspace_bytes < need)
+        return ULY_ERR_WORKSPACE;
+    if (uly::device_status_ptr() == nullptr)
+        return ULY_ERR_CUDA;
+    p.rstd = rstd, p.dh = dh, p.dz = dz, p.dx = dx, p.dy = dy;
+    p.dw1 = dweight, p.dw2 = dpost_weight, p.dgate = dgate;
+    return from_cuda(uly::launch_residual_norm(p, true, esize_of(dtype), sums ? workspace : nullptr,
+                                               static_cast<cudaStream_t>(stream)));
 }
 
 uly_status ulysses_attn_tile_order(int64_t N, int32_t causal, const int32_t *cu_seqlens_host, int32_t num_docs,
