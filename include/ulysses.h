@@ -418,6 +418,78 @@ uly_status ulysses_attn_bwd_noalloc(const void *q, const void *k, const void *v,
                                     const int32_t *cu_seqlens_host, int32_t num_docs,
                                     float softmax_scale, uly_dtype dtype, void *stream);
 
+/* ------------------------------------------------- sliding-window attention */
+
+/*
+ * Causal attention over a sliding window, with the first tokens of each
+ * document staying visible (sinks): the attention of ulysses_attn_fwd with
+ *   allowed: j <= i, doc(i) == doc(j), and
+ *            i - j < window  or  j - start(doc(i)) < sinks
+ * where start(doc) is the document's first token (0 without documents).
+ * window >= N is plain causal attention.  Every row sees itself.
+ *
+ * q, o, k, v, lse, cu_seqlens_host, num_docs, softmax_scale : as in
+ *              ulysses_attn_fwd; no output may overlap an input or another
+ *              output.  K and V of every token must be finite: a value that is
+ *              not may spoil rows of its 128 neighbours that do not see it.
+ * window >= 1, sinks >= 0, any size.
+ * workspace  : device, >= ulysses_window_attn_workspace_size(..., for_bwd) bytes
+ *              (num_docs = 0 without documents).  Calls that may run at the same
+ *              time need workspaces of their own.  cu_seqlens_host is taken in
+ *              before the call returns; a captured call replays with it.
+ * Requires Hq_local % Hkv_local == 0, d in {64, 128} (bf16: d == 128).
+ */
+size_t ulysses_window_attn_workspace_size(int64_t B, int64_t N, int32_t Hq_local, int32_t Hkv_local, int32_t d,
+                                          int32_t num_shards, int64_t window, int64_t sinks, int32_t num_docs,
+                                          int32_t for_bwd, uly_dtype dtype);
+uly_status ulysses_window_attn_fwd(const void *q, const void *k, const void *v, void *o, float *lse, int64_t B,
+                                   int64_t N, int32_t Hq_local, int32_t Hkv_local, int32_t d, int32_t num_shards,
+                                   int64_t window, int64_t sinks, const int32_t *cu_seqlens_host, int32_t num_docs,
+                                   float softmax_scale, uly_dtype dtype, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/*
+ * Its backward: ulysses_attn_bwd's formulas over the same allowed pairs.  dK and
+ * dV (and dQ in fp32) are summed in an order that depends on the arguments
+ * alone; in bf16 dQ is summed with fp32 atomics, as in ulysses_attn_bwd, so its
+ * last bits may differ between calls.
+ */
+uly_status ulysses_window_attn_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                                   const void *dout, void *dq, void *dk, void *dv, int64_t B, int64_t N,
+                                   int32_t Hq_local, int32_t Hkv_local, int32_t d, int32_t num_shards, int64_t window,
+                                   int64_t sinks, const int32_t *cu_seqlens_host, int32_t num_docs,
+                                   float softmax_scale, uly_dtype dtype, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/*
+ * The same attention for one new token of every sequence, over a cache of keys
+ * and values that already holds the token's own: sequence b has lens[b] tokens,
+ * its new one at position lens[b] - 1, which sees the cache's tokens j with
+ * lens[b] - 1 - j < window or j < sinks.
+ *
+ * q, o     : device [num_shards][B][1][Hq_local][d].  lse : device fp32 [num_shards][B][Hq_local][1].
+ * k_cache, v_cache : device [num_shards][B][C][Hkv_local][d].  Token j lies in slot
+ *            j, as long as the cache holds every token; once a sequence has more
+ *            than C tokens the cache rolls (C >= sinks + window): token j lies in
+ *            slot j for j < sinks, else in slot sinks + (j - sinks) mod (C - sinks)
+ *            (the same slot while j < C).  Only the slots of tokens that are seen
+ *            are read; the others may hold anything.
+ * lens     : device int64 [B] (8-byte aligned), read on the device.  0: an empty sequence, o = 0
+ *            and lse = -inf.  Negative, or more than C with C < sinks + window: the
+ *            same, and ULY_ERR_INVALID_ARG from ulysses_get_device_status.
+ * workspace: device, >= ulysses_window_attn_decode_workspace_size bytes.  Calls that
+ *            may run at the same time need workspaces of their own.
+ * window >= 1, sinks >= 0 (more than 2^30 counts as 2^30), C <= 2^30; other
+ * rules as above.  The result has the same bits on every call.
+ */
+size_t ulysses_window_attn_decode_workspace_size(int64_t B, int64_t C, int32_t Hq_local, int32_t Hkv_local, int32_t d,
+                                                 int32_t num_shards, int64_t window, int64_t sinks, uly_dtype dtype);
+uly_status ulysses_window_attn_decode(const void *q, const void *k_cache, const void *v_cache, const int64_t *lens,
+                                      void *o, float *lse, int64_t B, int64_t C, int32_t Hq_local, int32_t Hkv_local,
+                                      int32_t d, int32_t num_shards, int64_t window, int64_t sinks,
+                                      float softmax_scale, uly_dtype dtype, void *workspace, size_t workspace_bytes,
+                                      void *stream);
+
 /* --------------------------------------------------------- ring attention */
 
 /*

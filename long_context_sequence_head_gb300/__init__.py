@@ -36,6 +36,8 @@ EXPORTED = ("ulysses_seq_to_head", "ulysses_head_to_seq", "ulysses_swap_batch", 
             "ulysses_residual_norm_workspace_size", "ulysses_residual_norm_fwd", "ulysses_residual_norm_bwd",
             "ulysses_attn_tile_order",
             "ulysses_attn_fwd", "ulysses_attn_bwd", "ulysses_attn_fwd_seq", "ulysses_attn_bwd_seq",
+            "ulysses_window_attn_workspace_size", "ulysses_window_attn_fwd", "ulysses_window_attn_bwd",
+            "ulysses_window_attn_decode_workspace_size", "ulysses_window_attn_decode",
             "ulysses_attn_bwd_noalloc", "ulysses_sharded_ce_workspace_size", "ulysses_sharded_ce_loss",
             "ulysses_sharded_linear_ce_workspace_size", "ulysses_sharded_linear_ce_loss",
             "ulysses_ring_attn_workspace_size", "ulysses_ring_attn_fwd", "ulysses_ring_attn_bwd",
@@ -88,6 +90,18 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.ulysses_attn_fwd_seq.argtypes = lib.ulysses_attn_fwd.argtypes
     lib.ulysses_attn_bwd_seq.argtypes = lib.ulysses_attn_bwd.argtypes
     lib.ulysses_attn_bwd_noalloc.argtypes = [vp] * 9 + [i64, i64, i32, i32, i32, i32, i32, vp, i32, f32, i32, vp]
+    lib.ulysses_window_attn_workspace_size.argtypes = [i64, i64, i32, i32, i32, i32, i64, i64, i32, i32, i32]
+    lib.ulysses_window_attn_workspace_size.restype = sz
+    lib.ulysses_window_attn_fwd.argtypes = ([vp] * 5 + [i64, i64, i32, i32, i32, i32, i64, i64, vp, i32, f32, i32, vp,
+                                                        sz, vp])
+    lib.ulysses_window_attn_fwd.restype = i32
+    lib.ulysses_window_attn_bwd.argtypes = ([vp] * 9 + [i64, i64, i32, i32, i32, i32, i64, i64, vp, i32, f32, i32, vp,
+                                                        sz, vp])
+    lib.ulysses_window_attn_bwd.restype = i32
+    lib.ulysses_window_attn_decode_workspace_size.argtypes = [i64, i64, i32, i32, i32, i32, i64, i64, i32]
+    lib.ulysses_window_attn_decode_workspace_size.restype = sz
+    lib.ulysses_window_attn_decode.argtypes = [vp] * 6 + [i64, i64, i32, i32, i32, i32, i64, i64, f32, i32, vp, sz, vp]
+    lib.ulysses_window_attn_decode.restype = i32
     lib.ulysses_ring_attn_workspace_size.argtypes = [i64, i64, i32, i32, i32, i32, i32, i32]
     lib.ulysses_ring_attn_workspace_size.restype = sz
     lib.ulysses_ring_attn_fwd.argtypes = [vp] * 5 + [i64, i64, i32, i32, i32, i32, i32, f32, i32, vp, sz, vp]
@@ -850,6 +864,106 @@ def ulysses_attn_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, causal: bool = T
             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, N, Hq, Hkv, d, S, int(bool(causal)), cu_p, nd,
             float(softmax_scale), _dt(q), _stream(stream)))
     return dq, dk, dv
+
+
+# ---------------------------------------------- sliding-window attention
+
+def ulysses_window_attn_workspace_size(B: int, N: int, Hq_local: int, Hkv_local: int, d: int, num_shards: int,
+                                       window: int, sinks: int, num_docs: int, for_bwd: bool,
+                                       dtype: torch.dtype) -> int:
+    dt = ULY_BF16 if dtype == torch.bfloat16 else ULY_FP32
+    return int(load().ulysses_window_attn_workspace_size(B, N, Hq_local, Hkv_local, d, num_shards, window, sinks,
+                                                         num_docs, int(bool(for_bwd)), dt))
+
+
+def _same_device(first, *ts):
+    device = first.get_device()
+    for t in ts:
+        if t.get_device() != device or device < 0:
+            _on(first, t)
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+
+
+def ulysses_window_attn_fwd(q, k, v, o, lse, window: int, sinks: int = 0, cu_seqlens: Optional[Sequence[int]] = None,
+                            softmax_scale: float = 0.0, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention over the last `window` tokens and the first `sinks` of
+    each document; writes o and lse (see include/ulysses.h)."""
+    _attn_args(q, k, v, like_q=(o,), lse=lse, lse_shape=(q.shape[0], q.shape[1], q.shape[3], q.shape[2]))
+    _same_device(q, q, k, v, o, lse)
+    S, B, N, Hq, d = q.shape
+    Hkv = k.shape[3]
+    cu_p, nd, _keep = _cu(cu_seqlens)
+    with _Launch(q.device, stream) as at:
+        # the library checks the size of a workspace that is given
+        need = 0 if workspace is not None else ulysses_window_attn_workspace_size(B, N, Hq, Hkv, d, S, window, sinks, nd,
+                                                                                  False, q.dtype)
+        ws = at.scratch(workspace, need)
+        _check("ulysses_window_attn_fwd", load().ulysses_window_attn_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, N, Hq, Hkv, d, S, window, sinks,
+            cu_p, nd, softmax_scale, _dt(q), ws.data_ptr(), ws.nbytes, at.raw()))
+    return o, lse
+
+
+def ulysses_window_attn_bwd(q, k, v, o, lse, dout, dq, dk, dv, window: int, sinks: int = 0,
+                            cu_seqlens: Optional[Sequence[int]] = None, softmax_scale: float = 0.0,
+                            workspace: Optional[torch.Tensor] = None, stream=None):
+    """Backward of ulysses_window_attn_fwd; writes dq, dk, dv."""
+    _attn_args(q, k, v, like_q=(o, dout, dq), like_k=(dk, dv), lse=lse,
+               lse_shape=(q.shape[0], q.shape[1], q.shape[3], q.shape[2]))
+    _same_device(q, q, k, v, o, lse, dout, dq, dk, dv)
+    S, B, N, Hq, d = q.shape
+    Hkv = k.shape[3]
+    cu_p, nd, _keep = _cu(cu_seqlens)
+    with _Launch(q.device, stream) as at:
+        need = 0 if workspace is not None else ulysses_window_attn_workspace_size(B, N, Hq, Hkv, d, S, window, sinks, nd,
+                                                                                  True, q.dtype)
+        ws = at.scratch(workspace, need)
+        _check("ulysses_window_attn_bwd", load().ulysses_window_attn_bwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(), dq.data_ptr(),
+            dk.data_ptr(), dv.data_ptr(), B, N, Hq, Hkv, d, S, window, sinks, cu_p, nd, softmax_scale, _dt(q),
+            ws.data_ptr(), ws.nbytes, at.raw()))
+    return dq, dk, dv
+
+
+def ulysses_window_attn_decode_workspace_size(B: int, C: int, Hq_local: int, Hkv_local: int, d: int, num_shards: int,
+                                              window: int, sinks: int, dtype: torch.dtype) -> int:
+    dt = ULY_BF16 if dtype == torch.bfloat16 else ULY_FP32
+    return int(load().ulysses_window_attn_decode_workspace_size(B, C, Hq_local, Hkv_local, d, num_shards, window, sinks,
+                                                                dt))
+
+
+def ulysses_window_attn_decode(q, k_cache, v_cache, lens, o, lse, window: int, sinks: int = 0,
+                               softmax_scale: float = 0.0, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Sliding-window attention with sinks of one new token of every sequence
+    over a cache that holds its key and value (see include/ulysses.h).
+
+    q, o [S][B][1][Hq][d]; k_cache, v_cache [S][B][C][Hkv][d], whole or rolling;
+    lens [B] int64: tokens of each sequence, the new one included; lse
+    [S][B][Hq][1] fp32."""
+    qs, ks, dtype = q.shape, k_cache.shape, q.dtype
+    if len(qs) != 5 or qs[2] != 1:
+        raise ValueError(f"q must be [S][B][1][Hq][d], got {tuple(qs)}")
+    S, B, _, Hq, d = qs
+    if len(ks) != 5 or ks[:2] != qs[:2] or ks[4] != d or v_cache.shape != ks:
+        raise ValueError(f"k_cache and v_cache must be [{S}][{B}][C][Hkv][{d}], got {tuple(ks)} and "
+                         f"{tuple(v_cache.shape)}")
+    if o.shape != qs or lse.shape != (S, B, Hq, 1):
+        raise ValueError(f"o must be {list(qs)} and lse {[S, B, Hq, 1]}, got {list(o.shape)} and {list(lse.shape)}")
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype or o.dtype is not dtype or lse.dtype is not torch.float32:
+        raise ValueError(f"the caches and o must share q's dtype {dtype}, and lse be float32")
+    if lens.dtype is not torch.int64 or lens.shape != (B,):
+        raise ValueError(f"lens must be int64 [{B}], got {lens.dtype} {list(lens.shape)}")
+    _same_device(q, q, k_cache, v_cache, lens, o, lse)
+    C, Hkv = ks[2], ks[3]
+    with _Launch(q.device, stream) as at:
+        need = 0 if workspace is not None else ulysses_window_attn_decode_workspace_size(B, C, Hq, Hkv, d, S, window,
+                                                                                         sinks, dtype)
+        ws = at.scratch(workspace, need)
+        _check("ulysses_window_attn_decode", load().ulysses_window_attn_decode(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, C,
+            Hq, Hkv, d, S, window, sinks, softmax_scale, _dt(q), ws.data_ptr(), ws.nbytes, at.raw()))
+    return o, lse
 
 
 # -------------------------------------------------------- ring attention

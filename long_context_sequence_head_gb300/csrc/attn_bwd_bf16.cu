@@ -63,6 +63,8 @@ struct BwdParams {
     int Hq, Hkv, G, n_ktiles;
     int group;  // problems interleaved in the grid
     const int32_t *order;  // with documents: key tiles, longest walk first
+    int window, sinks;     // kDecode 3
+    WindowUnits wu;
     int causal;
     const int32_t *cu;
     int num_docs;
@@ -227,7 +229,8 @@ __global__ void __launch_bounds__(256) dq_convert_kernel(const float *__restrict
 
 // ----------------------------------------------------------------- main
 // kDecode: 0 = problem-major, key tiles in index order; 1 = groups of
-// problems interleaved; 2 = the same with the host's key-tile order.
+// problems interleaved; 2 = the same with the host's key-tile order;
+// 3 = a sliding window with sinks, in units of its own.
 template <int kDecode>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -273,7 +276,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // tile's walk follows its place in its document, and the host's order
     // puts the longest walks first ----
     int n_blk, prob;
-    if constexpr (kDecode == 0) {
+    constexpr bool kWindow = kDecode == 3;
+    [[maybe_unused]] int4 unit = make_int4(0, 0, 0, -1);
+    if constexpr (kWindow) {
+        const int64_t nprob = p.SB * p.Hkv;
+        const int64_t grp = blockIdx.x / (static_cast<int64_t>(p.group) * p.wu.n_units);
+        const int64_t rem = blockIdx.x % (static_cast<int64_t>(p.group) * p.wu.n_units);
+        const int64_t gsize = (nprob - grp * p.group < p.group) ? nprob - grp * p.group : p.group;
+        const int rank = static_cast<int>(rem / gsize);
+        prob = static_cast<int>(grp * p.group + rem % gsize);
+        unit = window_unit(p.wu, p.N, p.window, kBN, rank);
+        n_blk = unit.x;
+    } else if constexpr (kDecode == 0) {
         n_blk = static_cast<int>(blockIdx.x % p.n_ktiles);
         prob = static_cast<int>(blockIdx.x / p.n_ktiles);
     } else {
@@ -295,8 +309,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     doc_range(p, key_last, tmp, row_hi);
     if (p.causal)
         row_lo = kv0;
-    const int m_lo = static_cast<int>(row_lo / kBM);
-    const int n_m = static_cast<int>((row_hi - 1) / kBM) - m_lo + 1;
+    int m_lo = static_cast<int>(row_lo / kBM);
+    int n_m = static_cast<int>((row_hi - 1) / kBM) - m_lo + 1;
+    [[maybe_unused]] const int64_t last_doc = tmp;  // start of the last key's document
+    if constexpr (kWindow) {
+        m_lo = unit.y;
+        n_m = unit.z;
+    }
     const int n_it = p.G * n_m;
 
     if (warp == kProdWarp && lane == 0) {
@@ -464,6 +483,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int64_t lo = 0, hi = 0;                    // rows that may attend to this key: [lo, hi)
         if (key < p.N) {
             doc_range(p, key, lo, hi);
+            if constexpr (kWindow)  // past the window only sinks are seen
+                if (key >= lo + p.sinks)
+                    hi = min(hi, key + p.window);
             if (p.causal)
                 lo = key;
         }
@@ -620,7 +642,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mbar_wait_warp(dkv_done, 0, p.w, 0x78) && ok) {
             tc_fence_after();
             const int64_t rowoff = p.L.off(p.N, sb, key < p.N ? key : 0, p.Hkv, kvh, kD) + c0;
-            const bool store = key < p.N && ULY_IN_BOUNDS(p.w.status, rowoff, 32, p.kv_elems, 0x29);
+            bool store = key < p.N && ULY_IN_BOUNDS(p.w.status, rowoff, 32, p.kv_elems, 0x29);
+            // a tile whose walk is cut: the sums of its last document's sinks go to the unit's slot
+            [[maybe_unused]] float *part = nullptr;
+            if constexpr (kWindow) {
+                if (unit.w >= 0) {
+                    const int64_t first = max(last_doc, kv0), end = min(last_doc + p.sinks, p.N);
+                    if (key >= first && key < end) {
+                        const int64_t off =
+                            ((static_cast<int64_t>(prob) * p.wu.slots + (unit.w >> 1)) * 2 * p.wu.rows + key - first) *
+                                kD + c0;
+                        if (ULY_IN_BOUNDS(p.w.status, off, p.wu.rows * kD + 32,
+                                          p.SB * p.Hkv * p.wu.slots * 2 * p.wu.rows * kD, 0x2a))
+                            part = p.wu.part + off;
+                        store = false;
+                    } else if (unit.w & 1) {
+                        store = false;
+                    }
+                }
+            }
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
                 const uint32_t src = (which ? tdK : tdV) + lane_off + c0;
@@ -630,6 +670,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32p(src, x);  // warp-collective: all lanes
                 tmem_ld_wait();
                 tmem_ld_fence32p(x);
+                if constexpr (kWindow)
+                    if (part != nullptr)
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            *reinterpret_cast<float4 *>(part + (which ? 0 : p.wu.rows * kD) + c) =
+                                n_it > 0 ? make_float4(__uint_as_float(x[c]), __uint_as_float(x[c + 1]),
+                                                       __uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]))
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
                 uint32_t o16[16];
 #pragma unroll
                 for (int c = 0; c < 16; ++c)
@@ -703,7 +751,12 @@ cudaError_t launch_attn_bwd_bf16(const AttnShape &s, const void *q, const void *
     p.kv_elems = s.kv_elems;
     p.w = wait_cfg();
     p.L = s.L;
-    {
+    p.window = s.window;
+    p.sinks = s.sinks;
+    p.wu = s.units;
+    if (s.window) {
+        p.group = group_for(s.units.work * p.G, s.units.longest * p.G, s.SB * s.Hkv);
+    } else {
         int64_t work = 0, longest = 0;
         for (int n = 0; n < p.n_ktiles; ++n) {
             const int64_t kv0 = static_cast<int64_t>(n) * kBN;
@@ -721,12 +774,15 @@ cudaError_t launch_attn_bwd_bf16(const AttnShape &s, const void *q, const void *
     }
     const size_t smem = BwdSmem::kTotal;
     p.order = s.order_dev;
-    auto kernel = p.order ? attn_bwd_bf16_kernel<2> : p.group > 1 ? attn_bwd_bf16_kernel<1> : attn_bwd_bf16_kernel<0>;
+    auto kernel = s.window  ? attn_bwd_bf16_kernel<3>
+                  : p.order ? attn_bwd_bf16_kernel<2>
+                  : p.group > 1 ? attn_bwd_bf16_kernel<1>
+                                : attn_bwd_bf16_kernel<0>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem));
     if (e != cudaSuccess)
         return e;
-    const int64_t units = s.SB * s.Hkv * p.n_ktiles;
+    const int64_t units = s.SB * s.Hkv * (s.window ? s.units.n_units : p.n_ktiles);
     kernel<<<static_cast<unsigned>(units), kThreads, smem, stream>>>(tq, tk, tv, tdo, p);
     e = cudaGetLastError();
     if (e != cudaSuccess)

@@ -166,7 +166,52 @@ struct RowLayout {
     }
 };
 
+// How the backward of a windowed attention is cut into units (window_attn.cu):
+// a key tile and the query tiles that see it.  A tile with sinks is seen by
+// every later row of its document; that walk, past the window's, is cut into
+// extra units, whose sums of the sinks' dK and dV are joined afterwards.
+struct WindowUnits {
+    int sink_tiles = 0;          // without documents: tiles 0 .. sink_tiles-1 have sinks
+    int extra = 0;               // extra units of each (without documents)
+    int n_units = 0;             // of a problem
+    int n_joins = 0;             // tiles to join
+    int64_t work = 0, longest = 0;  // query tiles walked by a problem's units, and by its longest
+    int slots = 0;               // partial sums of a problem
+    int rows = 0;                // keys of a slot
+    const int4 *units = nullptr; // device, with documents: {key tile, first query tile, query tiles, slot * 2 + extra or -1}
+    const int4 *joins = nullptr; // device, with documents: {first key, keys, first slot, slots}
+    float *part = nullptr;       // [problem][slot][2][rows][d] fp32: dK, dV
+};
+
+// The last query tile that sees key tile t through the window, without documents.
+__host__ __device__ inline int window_end(int64_t N, int window, int tile, int t)
+{
+    const int64_t next = (static_cast<int64_t>(t) + 1) * tile, last = next < N ? next - 1 : N - 1;
+    return static_cast<int>((last + window < N ? last + window - 1 : N - 1) / tile);
+}
+
+// Unit `rank` of a problem: {key tile, first query tile, query tiles, slot * 2 +
+// extra or -1}.  Extra units come first (with documents: the longest units).
+__device__ __forceinline__ int4 window_unit(const WindowUnits &wu, int64_t N, int window, int tile, int rank)
+{
+    if (wu.units != nullptr)
+        return wu.units[rank];
+    const int tiles = static_cast<int>((N + tile - 1) / tile), n_extra = wu.sink_tiles * wu.extra;
+    if (rank < n_extra) {
+        const int t = rank / wu.extra, e = rank % wu.extra, m0 = window_end(N, window, tile, t) + 1;
+        const int lo = m0 + static_cast<int>(static_cast<int64_t>(tiles - m0) * e / wu.extra);
+        const int hi = m0 + static_cast<int>(static_cast<int64_t>(tiles - m0) * (e + 1) / wu.extra);
+        return make_int4(t, lo, hi - lo, (t * (1 + wu.extra) + 1 + e) * 2 + 1);
+    }
+    const int t = rank - n_extra;
+    const bool sinks = t < wu.sink_tiles;
+    const int end = sinks && wu.extra == 0 ? tiles - 1 : window_end(N, window, tile, t);
+    return make_int4(t, t, end - t + 1, sinks && wu.extra > 0 ? t * (1 + wu.extra) * 2 : -1);
+}
+
 struct AttnShape {
+    int window = 0, sinks = 0;  // sliding window (0: none) and first tokens that stay visible
+    WindowUnits units;          // backward with a window
     int64_t SB;      // num_shards * B (independent (shard, batch) problems)
     int64_t N;       // tokens
     int Hq, Hkv, d;  // per shard
@@ -207,6 +252,42 @@ struct BwdScratch {
 cudaError_t launch_attn_bwd_bf16(const AttnShape &s, const void *q, const void *k, const void *v, const void *o,
                                  const float *lse, const void *dout, void *dq, void *dk, void *dv,
                                  const BwdScratch &scr, cudaStream_t stream);
+
+// fp32 with a sliding window; part of window_attn.cu's units (key tiles of 64).
+constexpr int kWindowTileF32 = 64;
+cudaError_t launch_window_fwd_f32(const AttnShape &s, const float *q, const float *k, const float *v, float *o,
+                                  float *lse, cudaStream_t stream);
+cudaError_t launch_window_bwd_f32(const AttnShape &s, const float *q, const float *k, const float *v, const float *o,
+                                  const float *lse, const float *dout, float *dq, float *dk, float *dv, float *ws_D,
+                                  cudaStream_t stream);
+
+// Sliding-window attention (window_attn.cu): workspace of a call, and the call
+// itself on arguments that were checked.
+size_t window_attn_workspace(int64_t B, int64_t N, int Hq, int Hkv, int d, int S, int64_t window, int64_t sinks,
+                             int num_docs, bool bwd, int esize);
+cudaError_t window_attn_fwd(AttnShape s, const void *q, const void *k, const void *v, void *o, float *lse, int esize,
+                            void *workspace, cudaStream_t stream);
+cudaError_t window_attn_bwd(AttnShape s, const void *q, const void *k, const void *v, const void *o, const float *lse,
+                            const void *dout, void *dq, void *dk, void *dv, int esize, void *workspace,
+                            cudaStream_t stream);
+
+// One new token of every sequence over a cache (window_decode.cu).
+struct WindowDecodeParams {
+    const void *q, *k, *v;  // [SB][Hq][d], [SB][C][Hkv][d]
+    const int64_t *lens;    // [B]
+    void *o;
+    float *lse;             // [SB][Hq]
+    int64_t SB, C;
+    int B, Hq, Hkv;
+    int window, sinks;
+    float scale_log2;
+    // set by the launch: query heads of a KV head, groups of them, blocks a group is spread over
+    int G, parts, splits;
+    float *part, *stats;    // [SB][Hq][splits][d], [SB][Hq][splits][2]
+    unsigned *status;
+};
+size_t window_decode_workspace(int64_t SB, int64_t C, int Hq, int Hkv, int d, int64_t window, int64_t sinks, int esize);
+cudaError_t launch_window_decode(WindowDecodeParams &p, int d, int esize, void *workspace, cudaStream_t s);
 
 cudaError_t launch_selftest_timeout(uint64_t limit_ns, cudaStream_t stream);
 

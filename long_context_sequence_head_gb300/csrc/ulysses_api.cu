@@ -3,6 +3,7 @@
 // device memory; every buffer belongs to the caller.
 #include <ulysses.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -282,6 +283,47 @@ uly_status check_buffers(const Rows *in, int n_in, const Rows *out, int n_out)
 
 // A contiguous buffer of `bytes` bytes as one row.
 Rows whole(const void *p, int64_t bytes) { return Rows{p, 1, bytes, bytes}; }
+
+// Arguments of the windowed attention calls; fills s and takes window and sinks
+// to what they mean for N tokens.
+uly_status check_window_attn(uly::AttnShape &s, int64_t B, int64_t N, int32_t Hq, int32_t Hkv, int32_t d, int32_t S,
+                             int64_t window, int64_t sinks, const int32_t *cu, int32_t num_docs, float scale,
+                             uly_dtype dt)
+{
+    const uly_status st = check_attn_args(B, N, Hq, Hkv, d, S, 1, cu, num_docs, dt);
+    if (st != ULY_OK)
+        return st;
+    if (window < 1 || sinks < 0)
+        return ULY_ERR_INVALID_ARG;
+    s.window = static_cast<int>(std::min(window, N));
+    s.sinks = window >= N ? 0 : static_cast<int>(std::min(sinks, N));
+    // blocks of the largest launch: 64-row tiles of every head, and the extra units
+    if ((N / 64 + 65) * Hq > ((int64_t(1) << 31) - 1) / (static_cast<int64_t>(S) * B))
+        return ULY_ERR_UNSUPPORTED;
+    s.SB = static_cast<int64_t>(S) * B;
+    s.N = N;
+    s.Hq = Hq;
+    s.Hkv = Hkv;
+    s.d = d;
+    s.causal = 1;
+    s.cu_dev = nullptr;
+    s.cu_host = cu;
+    s.order_dev = nullptr;
+    s.num_docs = cu ? num_docs : 0;
+    s.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(d));
+    s.L = uly::RowLayout{0, static_cast<int>(B), N, S};
+    s.q_elems = s.SB * N * Hq * d;
+    s.kv_elems = s.SB * N * Hkv * d;
+    s.lse_elems = s.SB * N * Hq;
+    return ULY_OK;
+}
+
+// The driver entry point and the status word that the attention kernels need.
+bool attn_ready(uly::AttnShape &s)
+{
+    s.status = uly::device_status_ptr();
+    return s.status != nullptr && uly::tensor_map_encoder() != nullptr;
+}
 
 // A token stride in elements (0: contiguous); false if it is too small or not a multiple of 16 bytes.
 bool token_stride(int64_t given, int H, int d, int es, int64_t &out)
@@ -781,6 +823,150 @@ uly_status ulysses_attn_bwd(const void *q, const void *k, const void *v, const v
     return uly::attn_bwd_impl(q, k, v, o, lse, dout, dq, dk, dv, B, N, Hq_local, Hkv_local, d, num_shards, causal,
                          cu_seqlens_host, num_docs, softmax_scale, dtype, workspace, workspace_bytes, stream,
                          uly::head_rows(B, N, num_shards));
+}
+
+size_t ulysses_window_attn_workspace_size(int64_t B, int64_t N, int32_t Hq_local, int32_t Hkv_local, int32_t d,
+                                          int32_t num_shards, int64_t window, int64_t sinks, int32_t num_docs,
+                                          int32_t for_bwd, uly_dtype dtype)
+{
+    uly::AttnShape s;
+    if (num_docs < 0 || check_window_attn(s, B, N, Hq_local, Hkv_local, d, num_shards, window, sinks, nullptr, 0, 0.f,
+                                          dtype) != ULY_OK)
+        return 0;
+    return uly::window_attn_workspace(B, N, Hq_local, Hkv_local, d, num_shards, s.window, s.sinks, num_docs,
+                                      for_bwd != 0, esize_of(dtype));
+}
+
+uly_status ulysses_window_attn_fwd(const void *q, const void *k, const void *v, void *o, float *lse, int64_t B,
+                                   int64_t N, int32_t Hq_local, int32_t Hkv_local, int32_t d, int32_t num_shards,
+                                   int64_t window, int64_t sinks, const int32_t *cu_seqlens_host, int32_t num_docs,
+                                   float softmax_scale, uly_dtype dtype, void *workspace, size_t workspace_bytes,
+                                   void *stream)
+{
+    ULY_NVTX_RANGE();
+    if (!q || !k || !v || !o || !lse || !workspace)
+        return ULY_ERR_INVALID_ARG;
+    uly::AttnShape s;
+    uly_status st = check_window_attn(s, B, N, Hq_local, Hkv_local, d, num_shards, window, sinks, cu_seqlens_host,
+                                      num_docs, softmax_scale, dtype);
+    if (st != ULY_OK)
+        return st;
+    const int es = esize_of(dtype);
+    const size_t need = uly::window_attn_workspace(B, N, Hq_local, Hkv_local, d, num_shards, s.window, s.sinks,
+                                                   s.num_docs, false, es);
+    const Rows in[3] = {whole(q, s.q_elems * es), whole(k, s.kv_elems * es), whole(v, s.kv_elems * es)};
+    const Rows out[3] = {whole(o, s.q_elems * es), whole(lse, s.lse_elems * 4),
+                         whole(workspace, static_cast<int64_t>(need))};
+    st = check_buffers(in, 3, out, 3);
+    if (st != ULY_OK)
+        return st;
+    if (workspace_bytes < need)
+        return ULY_ERR_WORKSPACE;
+    if (!attn_ready(s))
+        return ULY_ERR_CUDA;
+    return from_cuda(uly::window_attn_fwd(s, q, k, v, o, lse, es, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+uly_status ulysses_window_attn_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                                   const void *dout, void *dq, void *dk, void *dv, int64_t B, int64_t N,
+                                   int32_t Hq_local, int32_t Hkv_local, int32_t d, int32_t num_shards, int64_t window,
+                                   int64_t sinks, const int32_t *cu_seqlens_host, int32_t num_docs,
+                                   float softmax_scale, uly_dtype dtype, void *workspace, size_t workspace_bytes,
+                                   void *stream)
+{
+    ULY_NVTX_RANGE();
+    if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv || !workspace)
+        return ULY_ERR_INVALID_ARG;
+    uly::AttnShape s;
+    uly_status st = check_window_attn(s, B, N, Hq_local, Hkv_local, d, num_shards, window, sinks, cu_seqlens_host,
+                                      num_docs, softmax_scale, dtype);
+    if (st != ULY_OK)
+        return st;
+    const int es = esize_of(dtype);
+    const size_t need = uly::window_attn_workspace(B, N, Hq_local, Hkv_local, d, num_shards, s.window, s.sinks,
+                                                   s.num_docs, true, es);
+    const int64_t qb = s.q_elems * es, kb = s.kv_elems * es;
+    const Rows in[6] = {whole(q, qb), whole(k, kb), whole(v, kb), whole(o, qb), whole(lse, s.lse_elems * 4),
+                        whole(dout, qb)};
+    const Rows out[4] = {whole(dq, qb), whole(dk, kb), whole(dv, kb), whole(workspace, static_cast<int64_t>(need))};
+    st = check_buffers(in, 6, out, 4);
+    if (st != ULY_OK)
+        return st;
+    if (workspace_bytes < need)
+        return ULY_ERR_WORKSPACE;
+    if (!attn_ready(s))
+        return ULY_ERR_CUDA;
+    return from_cuda(
+        uly::window_attn_bwd(s, q, k, v, o, lse, dout, dq, dk, dv, es, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+uly_status check_window_decode(int64_t B, int64_t C, int32_t Hq, int32_t Hkv, int32_t d, int32_t S, int64_t window,
+                               int64_t sinks, uly_dtype dt)
+{
+    if (B < 1 || C < 1 || Hq < 1 || Hkv < 1 || S < 1 || Hq % Hkv != 0 || esize_of(dt) == 0 || window < 1 || sinks < 0)
+        return ULY_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || (dt == ULY_BF16 && d != 128) || C > (int64_t(1) << 30) || B > (int64_t(1) << 20) ||
+        static_cast<int64_t>(S) * B > (int64_t(1) << 20) ||
+        Hq > ((int64_t(1) << 31) - 1) / (64 * static_cast<int64_t>(S) * B))
+        return ULY_ERR_UNSUPPORTED;
+    return ULY_OK;
+}
+// no sequence has more than 2^62 tokens, and a cache of C slots shows at most C of them
+int at_most(int64_t x) { return static_cast<int>(std::min<int64_t>(x, int64_t(1) << 30)); }
+}  // namespace
+
+size_t ulysses_window_attn_decode_workspace_size(int64_t B, int64_t C, int32_t Hq, int32_t Hkv, int32_t d,
+                                                 int32_t num_shards, int64_t window, int64_t sinks, uly_dtype dtype)
+{
+    if (check_window_decode(B, C, Hq, Hkv, d, num_shards, window, sinks, dtype) != ULY_OK)
+        return 0;
+    return uly::window_decode_workspace(num_shards * B, C, Hq, Hkv, d, at_most(window), at_most(sinks),
+                                        esize_of(dtype));
+}
+
+uly_status ulysses_window_attn_decode(const void *q, const void *k_cache, const void *v_cache, const int64_t *lens,
+                                      void *o, float *lse, int64_t B, int64_t C, int32_t Hq_local, int32_t Hkv_local,
+                                      int32_t d, int32_t num_shards, int64_t window, int64_t sinks,
+                                      float softmax_scale, uly_dtype dtype, void *workspace, size_t workspace_bytes,
+                                      void *stream)
+{
+    ULY_NVTX_RANGE();
+    if (!q || !k_cache || !v_cache || !lens || !o || !lse || !workspace)
+        return ULY_ERR_INVALID_ARG;
+    uly_status st = check_window_decode(B, C, Hq_local, Hkv_local, d, num_shards, window, sinks, dtype);
+    if (st != ULY_OK)
+        return st;
+    const int es = esize_of(dtype);
+    uly::WindowDecodeParams p = {};
+    p.SB = num_shards * B;
+    p.C = C;
+    p.B = static_cast<int>(B);
+    p.Hq = Hq_local;
+    p.Hkv = Hkv_local;
+    p.window = at_most(window);
+    p.sinks = at_most(sinks);
+    const size_t need = uly::window_decode_workspace(p.SB, C, Hq_local, Hkv_local, d, p.window, p.sinks, es);
+    const int64_t qb = p.SB * Hq_local * d * es, kb = p.SB * C * Hkv_local * d * es;
+    const Rows in[3] = {whole(q, qb), whole(k_cache, kb), whole(v_cache, kb)};
+    const Rows out[3] = {whole(o, qb), whole(lse, p.SB * Hq_local * 4), whole(workspace, static_cast<int64_t>(need))};
+    st = check_buffers(in, 3, out, 3);
+    if (st != ULY_OK)
+        return st;
+    const Rows list = whole(lens, B * 8);
+    if (reinterpret_cast<uintptr_t>(lens) % 8 != 0)
+        return ULY_ERR_MISALIGNED;
+    for (const Rows &x : out)
+        if (rows_overlap(x, list))
+            return ULY_ERR_OVERLAP;
+    if (workspace_bytes < need)
+        return ULY_ERR_WORKSPACE;
+    p.status = uly::device_status_ptr();
+    if (p.status == nullptr)
+        return ULY_ERR_CUDA;
+    p.q = q, p.k = k_cache, p.v = v_cache, p.lens = lens, p.o = o, p.lse = lse;
+    p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf(static_cast<float>(d))) * 1.4426950408889634f;
+    return from_cuda(uly::launch_window_decode(p, d, es, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 uly_status ulysses_attn_fwd_seq(const void *q_seq, const void *k_seq, const void *v_seq, void *o_seq, float *lse,

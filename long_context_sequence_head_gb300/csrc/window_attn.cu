@@ -1,0 +1,343 @@
+// Sliding-window attention with sinks over the Ulysses head shards: how a call
+// is cut into work, and the small kernels around the attention kernels
+// (attn_fwd_bf16.cu, attn_bwd_bf16.cu, window_attn_f32.cu).
+//
+// Row i of a document that starts at s sees the keys j <= i of its document
+// with i - j < window, and the document's first `sinks` keys.
+//   Forward: a tile of rows walks the tiles of its window and of its sinks; all
+// tiles cost about the same, so the grid needs no order without documents.
+//   Backward: a key tile walks the query tiles that see it.  Through the window
+// these are window/tile + 1, but a tile with sinks is seen by every later row:
+// 512 tiles at 64K tokens against 33 under a window of 4096, which would run on
+// alone at the end.  The walk past the window is therefore cut into extra units
+// of about the window's length that write fp32 sums of the sinks' dK and dV
+// (and add to dQ as any unit does); window_join_kernel adds them in order.
+#include "uly_internal.h"
+
+namespace uly {
+namespace {
+
+constexpr size_t kAlign = 256;
+size_t up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
+
+// ------------------------------------------------------------- staging
+// Host integers into device memory by kernel arguments: a captured call replays
+// with the values it was given, which a copy from pageable memory would not.
+constexpr int kStage = 4000;
+struct StageParams {
+    int32_t *dst;
+    int n;
+    int32_t v[kStage];
+};
+
+__global__ void __launch_bounds__(256) stage_kernel(const __grid_constant__ StageParams p)
+{
+    for (int i = threadIdx.x; i < p.n; i += 256)
+        p.dst[i] = p.v[i];
+}
+
+cudaError_t stage(const std::vector<int32_t> &host, int32_t *dst, cudaStream_t s)
+{
+    StageParams p;
+    for (size_t at = 0; at < host.size(); at += kStage) {
+        p.dst = dst + at;
+        p.n = static_cast<int>(std::min<size_t>(kStage, host.size() - at));
+        std::copy_n(host.begin() + at, p.n, p.v);
+        stage_kernel<<<1, 256, 0, s>>>(p);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess)
+            return e;
+    }
+    return cudaSuccess;
+}
+
+// ---------------------------------------------------------------- units
+// Tiles of a walk through the window alone.
+int64_t window_tiles(int64_t window, int tile) { return (window + tile - 2) / tile + 1; }
+
+// How the walks of tiles with sinks are cut.  At most 64 extra units a document,
+// so that their sums stay small (64 tiles of 128 keys: 8 MB a problem); many
+// sinks are many tiles, which balance each other.
+struct Cut {
+    int64_t tiles_with_sinks;  // of a document, at most
+    int64_t length, most;
+
+    Cut(int64_t window, int64_t sinks, bool docs, int tile)
+        : tiles_with_sinks(sinks > 0 ? (sinks + tile - 1) / tile + (docs ? 1 : 0) : 0),
+          length(std::max<int64_t>(8, window_tiles(window, tile))),
+          most(tiles_with_sinks > 0 ? 64 / tiles_with_sinks : 0)
+    {
+    }
+    int extra(int64_t past) const
+    {
+        return past <= length / 2 ? 0 : static_cast<int>(std::min(most, (past + length - 1) / length));
+    }
+};
+
+// Most units, slots and joins of a problem whose documents are not known.
+void unit_bounds(int64_t N, int64_t window, int64_t sinks, int num_docs, int tile, int64_t &units, int64_t &slots,
+                 int64_t &joins)
+{
+    const Cut cut(window, sinks, num_docs > 0, tile);
+    const int64_t n = (N + tile - 1) / tile;
+    // only a document longer than the window has rows past it
+    const int64_t docs = num_docs > 0 ? std::min<int64_t>(num_docs, N / (window + 1)) : 1;
+    joins = std::min(n, cut.tiles_with_sinks * docs);
+    const int64_t extra = std::min(joins * cut.most, joins + cut.tiles_with_sinks * (n + docs) / cut.length);
+    units = n + extra;
+    slots = joins + extra;
+}
+
+struct Units {
+    WindowUnits u;
+    std::vector<int32_t> list;  // with documents: units, then joins, four integers each
+};
+
+Units make_units(int64_t N, int window, int sinks, const int32_t *cu, int num_docs, int tile)
+{
+    Units r;
+    WindowUnits &u = r.u;
+    const Cut cut(window, sinks, num_docs > 0, tile);
+    const int n = static_cast<int>((N + tile - 1) / tile);
+    u.rows = std::min(sinks, tile);
+    if (num_docs == 0) {
+        u.sink_tiles = static_cast<int>((std::min<int64_t>(sinks, N) + tile - 1) / tile);
+        u.extra = u.sink_tiles > 0 ? cut.extra(n - 1 - window_end(N, window, tile, 0)) : 0;
+        u.n_units = n + u.sink_tiles * u.extra;
+        u.n_joins = u.extra > 0 ? u.sink_tiles : 0;
+        u.slots = u.n_joins * (1 + u.extra);
+        for (int t = 0; t < n; ++t) {
+            const int64_t walk = window_end(N, window, tile, t) - t + 1, whole = n - t;
+            const bool sink = t < u.sink_tiles;
+            u.work += sink ? whole : walk;
+            u.longest = std::max<int64_t>(
+                u.longest, sink && u.extra > 0 ? std::max(walk, (whole - walk + u.extra - 1) / u.extra)
+                                               : sink ? whole : walk);
+        }
+        return r;
+    }
+    std::vector<int4> units, joins;
+    for (int t = 0; t < n; ++t) {
+        const int64_t k0 = static_cast<int64_t>(t) * tile, last = std::min(k0 + tile, N) - 1;
+        int64_t lo, hi;
+        doc_range_host(cu, num_docs, N, last, lo, hi);
+        const int end = static_cast<int>((std::min(last + window, hi) - 1) / tile);
+        const bool sink = lo + sinks > k0 && sinks > 0;
+        const int past = sink ? static_cast<int>((hi - 1) / tile) - end : 0;
+        const int extra = cut.extra(past);
+        u.work += end - t + 1 + past;
+        if (extra == 0) {
+            units.push_back(make_int4(t, t, end - t + 1 + past, -1));
+            continue;
+        }
+        units.push_back(make_int4(t, t, end - t + 1, u.slots * 2));
+        for (int e = 0; e < extra; ++e) {
+            const int a = static_cast<int>(static_cast<int64_t>(past) * e / extra);
+            const int b = static_cast<int>(static_cast<int64_t>(past) * (e + 1) / extra);
+            units.push_back(make_int4(t, end + 1 + a, b - a, (u.slots + 1 + e) * 2 + 1));
+        }
+        const int64_t first = std::max(lo, k0);
+        joins.push_back(make_int4(static_cast<int>(first),
+                                  static_cast<int>(std::min(std::min(lo + sinks, k0 + tile), N) - first), u.slots,
+                                  1 + extra));
+        u.slots += 1 + extra;
+    }
+    std::stable_sort(units.begin(), units.end(), [](const int4 &a, const int4 &b) { return a.z > b.z; });
+    u.longest = units[0].z;
+    u.n_units = static_cast<int>(units.size());
+    u.n_joins = static_cast<int>(joins.size());
+    for (const std::vector<int4> *v : {&units, &joins})
+        for (const int4 &x : *v)
+            r.list.insert(r.list.end(), {x.x, x.y, x.z, x.w});
+    return r;
+}
+
+// Query tiles of 128 rows in the order of their walks, the longest first.
+void tile_order(int64_t N, int window, int sinks, const int32_t *cu, int num_docs, int32_t *out)
+{
+    const int n = static_cast<int>((N + 127) / 128);
+    std::vector<int64_t> walk(n);
+    for (int t = 0; t < n; ++t) {
+        const int64_t a = static_cast<int64_t>(t) * 128, b = std::min<int64_t>(a + 127, N - 1);
+        int64_t lo, hi;
+        doc_range_host(cu, num_docs, N, a, lo, hi);
+        const int64_t first = std::max(lo, a - window + 1), sink_end = std::min(lo + sinks, first);
+        walk[t] = b / 128 - first / 128 + 1;
+        if (sink_end > lo)
+            walk[t] += std::min((sink_end - 1) / 128 + 1, first / 128) - lo / 128;
+        out[t] = t;
+    }
+    std::stable_sort(out, out + n, [&](int32_t x, int32_t y) { return walk[x] > walk[y]; });
+}
+
+// ------------------------------------------------------------ workspace
+//   cu_seqlens and, behind it, the forward's tile order or the backward's units
+//   and joins (with documents); backward: as ulysses_attn_bwd's scratch, then the
+//   slots of fp32 sums
+struct Layout {
+    size_t cu = 0, list = 0, list_ints = 0, lse2 = 0, D = 0, acc = 0, part = 0, total = 0;
+    int64_t Npad = 0;
+    int64_t units = 0, slots = 0, joins = 0;
+};
+
+Layout layout(int64_t SB, int64_t N, int Hq, int Hkv, int d, int64_t window, int64_t sinks, int num_docs, bool bwd,
+              int esize)
+{
+    Layout L;
+    const int tile = esize == 2 ? 128 : kWindowTileF32;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += up(bytes);
+        return at;
+    };
+    if (bwd)
+        unit_bounds(N, window, sinks, num_docs, tile, L.units, L.slots, L.joins);
+    if (num_docs > 0) {
+        L.cu = take((static_cast<size_t>(num_docs) + 1) * sizeof(int32_t));
+        L.list_ints = bwd ? static_cast<size_t>(L.units + L.joins) * 4 : static_cast<size_t>((N + 127) / 128);
+        L.list = take(L.list_ints * sizeof(int32_t));
+    }
+    L.Npad = (N + 127) / 128 * 128;
+    if (bwd) {
+        const size_t rows = static_cast<size_t>(SB) * Hq * L.Npad;
+        if (esize == 2) {
+            L.lse2 = take(rows * sizeof(float));
+            L.D = take(rows * sizeof(float));
+            L.acc = take(rows * d * sizeof(float));
+        } else {
+            L.D = take(static_cast<size_t>(SB) * Hq * N * sizeof(float));
+        }
+        L.part = take(static_cast<size_t>(SB) * Hkv * L.slots * 2 * std::min<int64_t>(sinks, tile) * d * sizeof(float));
+    }
+    L.total = std::max(off, kAlign);
+    return L;
+}
+
+// ---------------------------------------------------------------- join
+// dK and dV of the sinks whose walk was cut: the sums of their tile's slots, in
+// order.  One block per (tile, problem), blockDim.x / d keys at once.
+template <typename T>
+__global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ AttnShape s, T *__restrict__ dk,
+                                                          T *__restrict__ dv, int tile)
+{
+    const WindowUnits &wu = s.units;
+    const int col = threadIdx.x % s.d, keys = 256 / s.d;
+    const int64_t nprob = s.SB * s.Hkv;
+    const int64_t prob = blockIdx.x % nprob;
+    const int t = static_cast<int>(blockIdx.x / nprob);
+    const int kvh = static_cast<int>(prob % s.Hkv);
+    const int64_t sb = prob / s.Hkv;
+    int4 join;  // {first key, keys, first slot, slots}
+    if (wu.joins != nullptr) {
+        join = wu.joins[t];
+    } else {
+        const int64_t first = static_cast<int64_t>(t) * tile, end = min(s.N, static_cast<int64_t>(s.sinks));
+        join = make_int4(static_cast<int>(first), static_cast<int>(min(end - first, static_cast<int64_t>(tile))),
+                         t * (1 + wu.extra), 1 + wu.extra);
+    }
+    [[maybe_unused]] const int64_t extent = nprob * wu.slots * 2 * wu.rows * s.d;
+    const int64_t other = static_cast<int64_t>(wu.rows) * s.d;  // from a dK to its dV
+    for (int r = threadIdx.x / s.d; r < join.y; r += keys) {
+        float a = 0.f, b = 0.f;
+        for (int i = 0; i < join.w; ++i) {
+            const int64_t off = ((prob * wu.slots + join.z + i) * 2 * wu.rows + r) * s.d + col;
+            if (!ULY_IN_BOUNDS(s.status, off, other + 1, extent, 0x61))
+                break;
+            a += wu.part[off];
+            b += wu.part[off + other];
+        }
+        const int64_t off = s.L.off(s.N, sb, join.x + r, s.Hkv, kvh, s.d) + col;
+        if (!ULY_IN_BOUNDS(s.status, off, 1, s.kv_elems, 0x62))
+            break;
+        if constexpr (sizeof(T) == 2) {
+            dk[off] = static_cast<T>(pack_bf16x2(a * s.scale, 0.f));
+            dv[off] = static_cast<T>(pack_bf16x2(b, 0.f));
+        } else {
+            dk[off] = a * s.scale;
+            dv[off] = b;
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_join(const AttnShape &s, void *dk, void *dv, int tile, cudaStream_t stream)
+{
+    if (s.units.n_joins == 0)
+        return cudaSuccess;
+    window_join_kernel<T><<<static_cast<unsigned>(s.units.n_joins * s.SB * s.Hkv), 256, 0, stream>>>(
+        s, static_cast<T *>(dk), static_cast<T *>(dv), tile);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t window_attn_workspace(int64_t B, int64_t N, int Hq, int Hkv, int d, int S, int64_t window, int64_t sinks,
+                             int num_docs, bool bwd, int esize)
+{
+    return layout(B * S, N, Hq, Hkv, d, window, sinks, num_docs, bwd, esize).total;
+}
+
+cudaError_t window_attn_fwd(AttnShape s, const void *q, const void *k, const void *v, void *o, float *lse, int esize,
+                            void *workspace, cudaStream_t stream)
+{
+    const Layout L = layout(s.SB, s.N, s.Hq, s.Hkv, s.d, s.window, s.sinks, s.num_docs, false, esize);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    if (s.cu_host) {
+        const size_t list = (L.list - L.cu) / sizeof(int32_t);
+        std::vector<int32_t> host(list + L.list_ints);
+        std::copy(s.cu_host, s.cu_host + s.num_docs + 1, host.begin());
+        tile_order(s.N, s.window, s.sinks, s.cu_host, s.num_docs, host.data() + list);
+        s.cu_dev = reinterpret_cast<int32_t *>(ws + L.cu);
+        s.order_dev = reinterpret_cast<int32_t *>(ws + L.list);
+        const cudaError_t e = stage(host, reinterpret_cast<int32_t *>(ws + L.cu), stream);
+        if (e != cudaSuccess)
+            return e;
+    }
+    if (esize == 2)
+        return launch_attn_fwd_bf16(s, q, k, v, o, lse, stream);
+    return launch_window_fwd_f32(s, static_cast<const float *>(q), static_cast<const float *>(k),
+                                 static_cast<const float *>(v), static_cast<float *>(o), lse, stream);
+}
+
+cudaError_t window_attn_bwd(AttnShape s, const void *q, const void *k, const void *v, const void *o, const float *lse,
+                            const void *dout, void *dq, void *dk, void *dv, int esize, void *workspace,
+                            cudaStream_t stream)
+{
+    const int tile = esize == 2 ? 128 : kWindowTileF32;
+    const Layout L = layout(s.SB, s.N, s.Hq, s.Hkv, s.d, s.window, s.sinks, s.num_docs, true, esize);
+    Units units = make_units(s.N, s.window, s.sinks, s.cu_host, s.num_docs, tile);
+    if (units.u.slots > L.slots || units.u.n_units > L.units || units.u.n_joins > L.joins)
+        return cudaErrorInvalidValue;  // the bounds above hold, so this is never reached
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    s.units = units.u;
+    s.units.part = reinterpret_cast<float *>(ws + L.part);
+    if (s.cu_host) {
+        const size_t list = (L.list - L.cu) / sizeof(int32_t);
+        std::vector<int32_t> host(list);
+        std::copy(s.cu_host, s.cu_host + s.num_docs + 1, host.begin());
+        host.insert(host.end(), units.list.begin(), units.list.end());
+        s.cu_dev = reinterpret_cast<int32_t *>(ws + L.cu);
+        s.units.units = reinterpret_cast<int4 *>(ws + L.list);
+        s.units.joins = s.units.units + s.units.n_units;
+        const cudaError_t e = stage(host, reinterpret_cast<int32_t *>(ws + L.cu), stream);
+        if (e != cudaSuccess)
+            return e;
+    }
+    if (esize == 2) {
+        BwdScratch scr;
+        scr.lse2 = reinterpret_cast<float *>(ws + L.lse2);
+        scr.D = reinterpret_cast<float *>(ws + L.D);
+        scr.dq_acc = reinterpret_cast<float *>(ws + L.acc);
+        scr.Npad = L.Npad;
+        const cudaError_t e = launch_attn_bwd_bf16(s, q, k, v, o, lse, dout, dq, dk, dv, scr, stream);
+        return e != cudaSuccess ? e : launch_join<uint16_t>(s, dk, dv, tile, stream);
+    }
+    const cudaError_t e = launch_window_bwd_f32(
+        s, static_cast<const float *>(q), static_cast<const float *>(k), static_cast<const float *>(v),
+        static_cast<const float *>(o), lse, static_cast<const float *>(dout), static_cast<float *>(dq),
+        static_cast<float *>(dk), static_cast<float *>(dv), reinterpret_cast<float *>(ws + L.D), stream);
+    return e != cudaSuccess ? e : launch_join<float>(s, dk, dv, tile, stream);
+}
+
+}  // namespace uly
