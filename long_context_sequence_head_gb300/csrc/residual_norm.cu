@@ -14,23 +14,27 @@
 //
 // Both directions are bound by HBM: 4 (forward) and 6 (backward) values move
 // per element, against 8 and about 20 operations.  A block takes a contiguous
-// run of rows.  One warp copies them, a few rows ahead, into a ring in shared
-// memory (contiguous rows: one bulk copy a tensor and stage), so that the bytes
-// on their way do not depend on registers; the other warps hold a row (or
-// several short ones) between them, 16 bytes a lane, each thread the same
-// columns of every row, so that the columns' sums stay in registers.  The
-// backward's three row sums (S1 = sum gz hh, S2 = sum c yh b, S3 = sum c yh hh
-// with b = dh + r1 gz, so that sum c t yh = S2 - r1 mean(gz hh) S3) cross the
-// row's warps in one exchange.
+// run of rows, in slots of one long row or several short ones (contiguous, one
+// bulk copy a tensor).  One warp copies slots into a ring in shared memory, so
+// that the bytes on their way do not depend on registers; groups of one or more
+// warps take the slots in turn, a thread 16 bytes by 16 bytes of the same columns
+// of every row, so that the columns' sums stay in registers.  Few warps a row and
+// several rows at once: ten warps on one row of 2560 spent most of their time in
+// its sums (forward 455 us for 64K rows, backward 642).  The backward's three row
+// sums (S1 = sum gz hh, S2 = sum c yh b, S3 = sum c yh hh with b = dh + r1 gz, so
+// that sum c t yh = S2 - r1 mean(gz hh) S3) cross a group's warps in one exchange;
+// what both passes over a row need is formed again from the slot, which costs less
+// than the registers to hold it.
 #include "uly_internal.h"
 
 namespace uly {
 namespace {
 
-constexpr int kMaxWarps = 16;   // of a row
+constexpr int kMaxWarps = 15;   // that work on rows; with the copying one 16, which have 128 registers a thread
 constexpr int kMaxThreads = 32 * (kMaxWarps + 1);
-constexpr int kMaxStages = 8;
-constexpr int kJoinLanes = 8;   // slots a column's sum is spread over
+constexpr int kMaxSlots = 32;
+constexpr int kMaxRows = 32;    // of a slot
+constexpr int kJoinLanes = 16;  // blocks a column's sum is spread over
 
 // Elements of a 16-byte chunk as fp32 pairs.
 template <typename T>
@@ -60,98 +64,151 @@ struct Chunk {
             return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
                               __float_as_uint(v[1].y));
     }
+    // fp32 values in shared memory
+    __device__ __forceinline__ void read(const float *p)
+    {
+#pragma unroll
+        for (int i = 0; i < kP; i += 2) {
+            const float4 f = *reinterpret_cast<const float4 *>(p + 2 * i);
+            v[i] = make_float2(f.x, f.y);
+            v[i + 1] = make_float2(f.z, f.w);
+        }
+    }
 };
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ uint4 ld_chunk(const uint8_t *p) { return *reinterpret_cast<const uint4 *>(p); }
 
-// The rows of a block in stages of at most p.rows rows that share a gate.
-struct Stages {
-    int64_t row, end, run_end;
-    int64_t run;
+// The rows of a block in slots of at most p.slot_rows rows that share a gate.
+struct Slots {
+    uint32_t row, end, run_end;  // fewer than 2^31 rows
+    uint32_t run;
 
-    __device__ __forceinline__ explicit Stages(const ResidualNormParams &p)
+    __device__ __forceinline__ explicit Slots(const ResidualNormParams &p)
     {
-        row = p.T * blockIdx.x / gridDim.x;
-        end = p.T * (blockIdx.x + 1) / gridDim.x;
-        run = row / p.run;
-        run_end = (run + 1) * p.run;
+        row = static_cast<uint32_t>(p.T * blockIdx.x / gridDim.x);
+        end = static_cast<uint32_t>(p.T * (blockIdx.x + 1) / gridDim.x);
+        run = row / static_cast<uint32_t>(p.run);
+        run_end = (run + 1) * static_cast<uint32_t>(p.run);
     }
     __device__ __forceinline__ bool more() const { return row < end; }
     __device__ __forceinline__ int count(const ResidualNormParams &p) const
     {
-        const int64_t last = run_end < end ? run_end : end;
-        return last - row < p.rows ? static_cast<int>(last - row) : p.rows;
+        return static_cast<int>(min(min(run_end, end) - row, static_cast<uint32_t>(p.slot_rows)));
     }
-    // true if the next stage has another gate
+    // true if the next slot has another gate
     __device__ __forceinline__ bool next(const ResidualNormParams &p, int n)
     {
         row += n;
         if (row < run_end)
             return false;
         ++run;
-        run_end += p.run;
+        run_end += static_cast<uint32_t>(p.run);
         return true;
     }
 };
 
+// Shared memory: barriers, the groups' sums, the slots' statistics, w1 as given,
+// f = residual_scale * gate * post_weight in fp32, the ring.
 struct Smem {
     uint64_t *full, *empty;
     volatile int *abort;
-    float4 *sums;   // [groups][2][kMaxWarps]
-    uint8_t *w1, *w2, *gate, *ring;
+    float4 *sums;   // [groups][2][warps]
+    float *stats;   // backward: [slots][2][kMaxRows]
+    uint8_t *w1;
+    float *f;
+    float *scratch; // backward: [parts][D], the sums on their way out of a block
+    uint8_t *ring;
 
-    __device__ __forceinline__ Smem(uint8_t *base, int row_bytes, int groups)
+    static constexpr int kHead = 16 * kMaxSlots + 128;
+    static __host__ __device__ size_t fixed(int D, int row_bytes, int parts, int stat_slots)
+    {
+        return kHead + static_cast<size_t>(2) * kMaxWarps * sizeof(float4) +
+               static_cast<size_t>(stat_slots) * 2 * kMaxRows * sizeof(float) + row_bytes + static_cast<size_t>(1 + parts) * D * 4;
+    }
+    __device__ __forceinline__ Smem(uint8_t *base, const ResidualNormParams &p, int row_bytes)
     {
         full = reinterpret_cast<uint64_t *>(base);
-        empty = full + kMaxStages;
-        abort = reinterpret_cast<volatile int *>(empty + kMaxStages);
-        sums = reinterpret_cast<float4 *>(base + 256);
-        w1 = base + 256 + groups * 2 * kMaxWarps * sizeof(float4);
-        w2 = w1 + row_bytes;
-        gate = w2 + row_bytes;
-        ring = gate + row_bytes;
+        empty = full + kMaxSlots;
+        abort = reinterpret_cast<volatile int *>(empty + kMaxSlots);
+        sums = reinterpret_cast<float4 *>(base + kHead);
+        stats = reinterpret_cast<float *>(sums + 2 * kMaxWarps);
+        w1 = reinterpret_cast<uint8_t *>(stats + (p.rstd ? p.slots * 2 * kMaxRows : 0));
+        f = reinterpret_cast<float *>(w1 + row_bytes);
+        scratch = f + p.D;
+        ring = reinterpret_cast<uint8_t *>(scratch + static_cast<size_t>(p.parts) * p.D);
     }
 };
 
-// The copying warp: rows of n_in tensors, stage by stage.
-template <int kIn>
+// The copying warp: slots of kIn tensors' rows (some may be null); kStats: with
+// each row's two statistics, a lane a row, by 4-byte copies that arrive on the
+// same barrier.
+template <int kIn, bool kStats>
 __device__ __forceinline__ void copy_rows(const ResidualNormParams &p, const Smem &sm, const uint8_t *const *in,
                                           int row_bytes)
 {
-    Stages st(p);
-    int k = 0;
+    Slots st(p);
+    const int lane = lane_id();
+    // Every group has slots of its own: one that others fill in turn would let a
+    // group see the parity of a copy two phases back as its own.
+    const int own = p.slots / p.groups;
+    int k = 0, group = 0, at = 0;
+    uint32_t phase = 0;
     for (; st.more() && !*sm.abort; ++k) {
-        const int slot = k % p.stages, n = st.count(p);
-        if (!mbar_wait(&sm.empty[slot], ((k / p.stages) & 1) ^ 1, p.w, 0xa1)) {
+        const int slot = group * own + at, n = st.count(p);
+        if (!mbar_wait_warp(&sm.empty[slot], phase ^ 1, p.w, 0xa1)) {
             *sm.abort = 1;
             break;
         }
-        uint8_t *dst = sm.ring + static_cast<size_t>(slot) * kIn * p.rows * row_bytes;
-        const uint32_t bytes = static_cast<uint32_t>(n) * row_bytes;
-        int tensors = 0;
-#pragma unroll
-        for (int t = 0; t < kIn; ++t)
-            tensors += in[t] != nullptr;
+        if (++group == p.groups) {
+            group = 0;
+            if (++at == own) {
+                at = 0;
+                phase ^= 1;
+            }
+        }
         const bool ok = ULY_IN_BOUNDS(p.w.status, st.row, n, p.T, 0x51);
-        mbar_expect_tx(&sm.full[slot], ok ? tensors * bytes : 0);
+        if (kStats) {
+            if (ok && lane < n) {
+                const uint32_t at = smem_u32(sm.stats + slot * 2 * kMaxRows + lane);
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(p.rstd + st.row + lane)
+                             : "memory");
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + kMaxRows * 4),
+                             "l"(p.rstd + p.T + st.row + lane)
+                             : "memory");
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&sm.full[slot])) : "memory");
+        }
+        if (lane == 0) {
+            uint8_t *dst = sm.ring + static_cast<size_t>(slot) * kIn * p.slot_rows * row_bytes;
+            const uint32_t bytes = static_cast<uint32_t>(n) * row_bytes;
+            int tensors = 0;
 #pragma unroll
-        for (int t = 0; t < kIn; ++t)
-            if (ok && in[t] != nullptr)
-                bulk_g2s(dst + static_cast<size_t>(t) * p.rows * row_bytes, in[t] + st.row * row_bytes, bytes,
-                         &sm.full[slot]);
+            for (int t = 0; t < kIn; ++t)
+                tensors += in[t] != nullptr;
+            mbar_expect_tx(&sm.full[slot], ok ? tensors * bytes : 0);
+#pragma unroll
+            for (int t = 0; t < kIn; ++t)
+                if (ok && in[t] != nullptr)
+                    bulk_g2s(dst + static_cast<size_t>(t) * p.slot_rows * row_bytes, in[t] + static_cast<int64_t>(st.row) * row_bytes, bytes,
+                             &sm.full[slot]);
+        }
+        __syncwarp();
         st.next(p, n);
     }
     if (*sm.abort)  // wait (bounded) for the copies that are on their way
-        for (int i = k > p.stages ? k - p.stages : 0; i < k; ++i)
-            mbar_wait(&sm.full[i % p.stages], (i / p.stages) & 1, p.w, 0xaf);
+        for (int i = k > p.slots ? k - p.slots : 0; i < k; ++i) {
+            const int turn = i / p.groups;
+            mbar_wait(&sm.full[i % p.groups * own + turn % own], (turn / own) & 1, p.w, 0xaf);
+        }
 }
 
-// Sums over the lanes (and warps) that hold a row.  lanes: a power of two up
-// to 32, or 32 with `warps` > 1; every thread of the row gets the same bits.
+// Sums over the lanes (and the group's warps) that hold a row.  lanes: a power of
+// two up to 32; every thread of the row gets the same bits.
 template <int kN>
 struct RowSum {
     float4 *slots;
-    int lanes, warps, group, parity = 0;
+    int lanes, warps, group, warp, parity = 0;
 
     __device__ __forceinline__ void operator()(float (&s)[kN])
     {
@@ -161,11 +218,10 @@ struct RowSum {
                 s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
         if (warps == 1)
             return;
-        float4 *at = slots + parity * kMaxWarps;
+        float4 *at = slots + parity * warps;
         parity ^= 1;
-        const int w = warp_id() - group * warps;
         if (lane_id() == 0)
-            at[w] = make_float4(s[0], kN > 1 ? s[kN > 1 ? 1 : 0] : 0.f, kN > 2 ? s[kN > 2 ? 2 : 0] : 0.f, 0.f);
+            at[warp] = make_float4(s[0], kN > 1 ? s[kN > 1 ? 1 : 0] : 0.f, kN > 2 ? s[kN > 2 ? 2 : 0] : 0.f, 0.f);
         named_bar_sync(1 + group, warps * 32);
         float4 total = at[0];
         for (int i = 1; i < warps; ++i) {
@@ -180,350 +236,399 @@ struct RowSum {
     }
 };
 
-// Copies a row of weights into shared memory (the threads that work on rows).
-__device__ __forceinline__ void load_weights(uint8_t *dst, const void *src, int64_t row, int row_bytes, int threads)
-{
-    const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(src) + row * row_bytes);
-    for (int i = threadIdx.x; i < row_bytes / 16; i += threads)
-        reinterpret_cast<uint4 *>(dst)[i] = from[i];
-}
+// The threads that work on rows: which rows, which columns, and what they share.
+template <typename T, int kIn, int kSums>
+struct Worker {
+    const ResidualNormParams &p;
+    const Smem &sm;
+    int threads, row_bytes, nvec;
+    int group, sub, col, width;  // group of warps, row of those its warp holds at once, first chunk, chunks from one to the next
+    RowSum<kSums> sum;
 
-__device__ __forceinline__ bool set_up(const Smem &sm, const ResidualNormParams &p, int threads)
+    __device__ __forceinline__ Worker(const ResidualNormParams &p_, const Smem &sm_, int threads_)
+        : p(p_), sm(sm_), threads(threads_), row_bytes(p_.D * static_cast<int>(sizeof(T))), nvec(row_bytes / 16)
+    {
+        group = warp_id() / p.warps;
+        const int warp = warp_id() - group * p.warps;
+        sub = lane_id() / p.lanes;
+        col = p.lanes < 32 ? lane_id() % p.lanes : warp * 32 + lane_id();
+        width = p.lanes < 32 ? p.lanes : p.warps * 32;
+        sum.slots = sm.sums + group * 2 * p.warps;
+        sum.lanes = p.lanes;
+        sum.warps = p.warps;
+        sum.group = group;
+        sum.warp = warp;
+    }
+    // f for the rows of a run
+    __device__ __forceinline__ void load_f(uint32_t run) const
+    {
+        const T *gate = static_cast<const T *>(p.gate), *w2 = static_cast<const T *>(p.w2);
+        if (gate && p.gates > 1)
+            gate += static_cast<int64_t>(run % p.gates) * p.D;
+        for (int i = threadIdx.x; i < nvec; i += threads) {
+            Chunk<T> f, w;
+#pragma unroll
+            for (int e = 0; e < Chunk<T>::kP; ++e)
+                f.v[e] = both(p.scale);
+            for (const T *from : {gate, w2}) {
+                if (from == nullptr)
+                    continue;
+                w.unpack(reinterpret_cast<const uint4 *>(from)[i]);
+#pragma unroll
+                for (int e = 0; e < Chunk<T>::kP; ++e)
+                    f.v[e] = fmul2(f.v[e], w.v[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < Chunk<T>::kP; ++e)
+                *reinterpret_cast<float2 *>(sm.f + i * Chunk<T>::kE + 2 * e) = f.v[e];
+        }
+    }
+    // Goes through the block's slots: body(first row, row in slot, live, slot memory,
+    // slot number) for the rows of this group's, end_of_run(run) for every thread.
+    template <bool kSub, typename Body, typename EndOfRun>
+    __device__ __forceinline__ void go(unsigned site, Body body, EndOfRun end_of_run)
+    {
+        Slots st(p);
+        const int pitch = p.slot_rows * row_bytes;
+        auto rows_of = [&](int slot, uint32_t phase, uint32_t row0, int n) {
+            // after a wait that ran out the loop goes on without waiting: its outputs
+            // are invalid and the status says so
+            if (!*sm.abort && !mbar_wait(&sm.full[slot], phase, p.w, site))
+                *sm.abort = 1;
+            const uint8_t *at = sm.ring + static_cast<size_t>(slot) * kIn * pitch;
+            if constexpr (kSub) {
+                for (int r = 0; r < n; r += 32 / p.lanes) {
+                    const bool live = r + sub < n;
+                    body(row0, r + sub, live, at + (live ? r + sub : 0) * row_bytes, slot);
+                }
+            } else {
+                for (int r = 0; r < n; ++r)
+                    body(row0, r, true, at + r * row_bytes, slot);
+            }
+            __syncwarp();
+            if (lane_id() == 0)
+                mbar_arrive(&sm.empty[slot]);
+        };
+        const int own = p.slots / p.groups, first_slot = group * own;
+        int at = 0, whose = 0;
+        uint32_t phase = 0;
+        bool turn = p.gates > 1;
+        if (!turn)
+            st.row += group * p.slot_rows;
+        // with a gate for every sequence all threads go through all slots, to
+        // change it together; without, a group's slots are evenly spaced
+        while (st.more()) {
+            const uint32_t row0 = st.row, run = st.run;
+            const int n = st.count(p);
+            if (turn) {
+                named_bar_sync(15, threads);
+                load_f(run);
+                named_bar_sync(15, threads);
+            }
+            bool ours = true;
+            if (p.gates > 1) {
+                ours = whose == group;
+                whose = whose + 1 == p.groups ? 0 : whose + 1;
+                turn = st.next(p, n);
+            } else {
+                st.row += p.groups * p.slot_rows;
+            }
+            if (ours) {
+                rows_of(first_slot + at, phase, row0, n);
+                if (++at == own) {
+                    at = 0;
+                    phase ^= 1;
+                }
+            }
+            if (p.gates > 1 && (turn || !st.more()))
+                end_of_run(run);
+        }
+        if (p.gates <= 1)
+            end_of_run(0);
+    }
+};
+
+// Barriers, w1 and the first f; true for the copying warp.
+template <typename T>
+__device__ __forceinline__ bool set_up(const ResidualNormParams &p, const Smem &sm, int threads, int copies_arrive)
 {
-    if (threadIdx.x == threads) {  // lane 0 of the copying warp
-        for (int i = 0; i < p.stages; ++i) {
-            mbar_init(&sm.full[i], 1);
-            mbar_init(&sm.empty[i], threads / 32);
+    if (threadIdx.x == threads) {
+        for (int i = 0; i < p.slots; ++i) {
+            mbar_init(&sm.full[i], copies_arrive);
+            mbar_init(&sm.empty[i], p.warps);
         }
         *sm.abort = 0;
         fence_mbar_init();
     }
+    const int nvec = p.D * static_cast<int>(sizeof(T)) / 16;
+    for (int i = threadIdx.x; i < nvec; i += blockDim.x)
+        reinterpret_cast<uint4 *>(sm.w1)[i] = static_cast<const uint4 *>(p.w1)[i];
     return threadIdx.x >= threads;
 }
 
-__device__ __forceinline__ void await(const Smem &sm, const ResidualNormParams &p, int k, unsigned site)
+// kC: chunks a thread holds of its row; all but the last two are there for every
+// thread.  kSub: short rows, several a warp (kC = 1).  kPost: a norm behind the
+// block.
+template <typename T, int kC, bool kSub, bool kPost>
+__global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_fwd_kernel(
+    const __grid_constant__ ResidualNormParams p)
 {
-    // after a wait that ran out the loop goes on without waiting: its outputs
-    // are invalid and the status says so
-    if (!*sm.abort && !mbar_wait(&sm.full[k % p.stages], (k / p.stages) & 1, p.w, site))
-        *sm.abort = 1;
-}
-
-__device__ __forceinline__ uint4 ld_chunk(const uint8_t *p) { return *reinterpret_cast<const uint4 *>(p); }
-
-// kC: chunks a thread holds of its row.  kPost: a norm behind the block.
-// kFirst: no block before this norm (y is null).
-template <typename T, int kC, bool kPost, bool kFirst>
-__global__ void __launch_bounds__(kMaxThreads) residual_norm_fwd_kernel(const __grid_constant__ ResidualNormParams p)
-{
-    constexpr int kIn = kFirst ? 1 : 2, kP = Chunk<T>::kP;
+    constexpr int kIn = 2, kP = Chunk<T>::kP, kE = Chunk<T>::kE;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     const int row_bytes = p.D * static_cast<int>(sizeof(T)), nvec = row_bytes / 16;
-    const int groups = p.lanes < 32 ? 1 : p.rows;  // rows that are summed over several warps
-    const Smem sm(smem_raw, row_bytes, groups);
+    const Smem sm(smem_raw, p, row_bytes);
     const int threads = static_cast<int>(blockDim.x) - 32;
-    const bool copies = set_up(sm, p, threads);
-    if (!copies) {
-        load_weights(sm.w1, p.w1, 0, row_bytes, threads);
-        if (kPost)
-            load_weights(sm.w2, p.w2, 0, row_bytes, threads);
-    }
+    const bool copies = set_up<T>(p, sm, threads, 1);
+    Worker<T, kIn, 1> me(p, sm, threads);
+    if (!copies)
+        me.load_f(0);
     __syncthreads();
     if (copies) {
-        if (lane_id() == 0) {
-            const uint8_t *in[kIn];
-            in[0] = static_cast<const uint8_t *>(p.x);
-            if constexpr (!kFirst)
-                in[1] = static_cast<const uint8_t *>(p.y);
-            copy_rows<kIn>(p, sm, in, row_bytes);
-        }
+        const uint8_t *in[kIn] = {static_cast<const uint8_t *>(p.x), static_cast<const uint8_t *>(p.y)};
+        copy_rows<kIn, false>(p, sm, in, row_bytes);
         return;
     }
-    const int mine = threadIdx.x / p.per_row, cl = threadIdx.x % p.per_row;
-    const int group = p.lanes < 32 ? 0 : mine;
-    RowSum<1> sum{sm.sums + group * 2 * kMaxWarps, p.lanes, p.lanes < 32 ? 1 : p.per_row / 32, group};
-    const bool gated = !kFirst && p.gate != nullptr;
+    const size_t pitch = static_cast<size_t>(p.slot_rows) * row_bytes;  // of a slot's tensors
     const float inv_d = 1.f / static_cast<float>(p.D);
-    bool turn = true;
-    Stages st(p);
-    for (int k = 0; st.more(); ++k) {
-        const int n = st.count(p), slot = k % p.stages;
-        if (turn && gated) {  // this run's gate
-            named_bar_sync(15, threads);
-            load_weights(sm.gate, p.gate, p.gates > 1 ? st.run % p.gates : 0, row_bytes, threads);
-            named_bar_sync(15, threads);
-        }
-        await(sm, p, k, 0xa2);
-        const bool live = mine < n;
-        const uint8_t *from = sm.ring + static_cast<size_t>(slot) * kIn * p.rows * row_bytes +
-                              static_cast<size_t>(mine) * row_bytes;
-        Chunk<T> x[kC], y[kFirst ? 1 : kC];
+    me.template go<kSub>(
+        0xa2,
+        [&](uint32_t row0, int r, bool live, const uint8_t *from, int) {
+            // the block's output is read from the slot as often as it is needed; only
+            // the sum with the stream stays in registers
+            Chunk<T> x[kC], y;
+            auto there = [&](int c) { return (!kSub || live) && (c < kC - 2 || me.col + c * me.width < nvec); };
+            float s[1], r2 = 1.f;
+            if constexpr (kPost) {
+                float2 q = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < kC; ++c) {
-            const int at = cl + c * p.per_row;
-            const bool in = live && at < nvec;
-            x[c].unpack(in ? ld_chunk(from + at * 16) : make_uint4(0, 0, 0, 0));
-            if constexpr (!kFirst)
-                y[c].unpack(in ? ld_chunk(from + static_cast<size_t>(p.rows) * row_bytes + at * 16)
-                               : make_uint4(0, 0, 0, 0));
-        }
-        __syncwarp();
-        if (lane_id() == 0)
-            mbar_arrive(&sm.empty[slot]);
-        float r2 = 1.f;
-        if constexpr (kPost) {
+                for (int c = 0; c < kC; ++c) {
+                    if (!there(c))
+                        continue;
+                    y.unpack(ld_chunk(from + pitch + (me.col + c * me.width) * 16));
+#pragma unroll
+                    for (int e = 0; e < kP; ++e)
+                        q = ffma2(y.v[e], y.v[e], q);
+                }
+                s[0] = q.x + q.y;
+                me.sum(s);
+                r2 = rsqrtf(fmaf(s[0], inv_d, p.eps));
+            }
             float2 q = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int c = 0; c < kC; ++c)
+            for (int c = 0; c < kC; ++c) {
+                if (!there(c))
+                    continue;
+                const int at = me.col + c * me.width;
+                x[c].unpack(ld_chunk(from + at * 16));
+                if (p.y) {
+                    Chunk<T> f;
+                    f.read(sm.f + at * kE);
+                    y.unpack(ld_chunk(from + pitch + at * 16));
+#pragma unroll
+                    for (int e = 0; e < kP; ++e) {
+                        const float2 yh = kPost ? fmul2(y.v[e], both(r2)) : y.v[e];
+                        x[c].v[e] = ffma2(yh, f.v[e], x[c].v[e]);
+                    }
+                }
 #pragma unroll
                 for (int e = 0; e < kP; ++e)
-                    q = ffma2(y[c].v[e], y[c].v[e], q);
-            float s[1] = {q.x + q.y};
-            sum(s);
-            r2 = 1.f / sqrtf(fmaf(s[0], inv_d, p.eps));
-        }
-        float2 q = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < kC; ++c) {
-            const int at = cl + c * p.per_row;
-            if constexpr (!kFirst) {
-                const float2 f = both(p.scale * r2);
-                Chunk<T> w, g;
-                const bool in = at < nvec;
-                if (kPost)
-                    w.unpack(in ? ld_chunk(sm.w2 + at * 16) : make_uint4(0, 0, 0, 0));
-                if (gated)
-                    g.unpack(in ? ld_chunk(sm.gate + at * 16) : make_uint4(0, 0, 0, 0));
-#pragma unroll
-                for (int e = 0; e < kP; ++e) {
-                    float2 u = fmul2(y[c].v[e], f);
-                    if (kPost)
-                        u = fmul2(u, w.v[e]);
-                    x[c].v[e] = gated ? ffma2(u, g.v[e], x[c].v[e]) : fadd2(u, x[c].v[e]);
-                }
+                    q = ffma2(x[c].v[e], x[c].v[e], q);
             }
-#pragma unroll
-            for (int e = 0; e < kP; ++e)
-                q = ffma2(x[c].v[e], x[c].v[e], q);
-        }
-        float s[1] = {q.x + q.y};
-        sum(s);
-        const float r1 = 1.f / sqrtf(fmaf(s[0], inv_d, p.eps));
-        if (live && ULY_IN_BOUNDS(p.w.status, st.row + mine, 1, p.T, 0x52)) {
-            const int64_t row = (st.row + mine) * row_bytes;
-            if (cl == 0 && p.rstd_out) {
-                p.rstd_out[st.row + mine] = r1;
-                p.rstd_out[p.T + st.row + mine] = r2;
+            s[0] = q.x + q.y;
+            me.sum(s);
+            const float r1 = rsqrtf(fmaf(s[0], inv_d, p.eps));
+            if (!live || !ULY_IN_BOUNDS(p.w.status, row0 + r, 1, p.T, 0x52))
+                return;
+            const int64_t out = static_cast<int64_t>(row0 + r) * row_bytes;
+            if (me.col == 0 && p.rstd_out) {
+                p.rstd_out[row0 + r] = r1;
+                p.rstd_out[p.T + row0 + r] = r2;
             }
 #pragma unroll
             for (int c = 0; c < kC; ++c) {
-                const int at = cl + c * p.per_row;
-                if (at >= nvec)
+                const int at = me.col + c * me.width;
+                if (!there(c))
                     continue;
-                if (!kFirst && p.h)
-                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.h) + row + at * 16) = x[c].pack();
+                if (p.h)
+                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.h) + out + at * 16) = x[c].pack();
                 Chunk<T> w;
                 w.unpack(ld_chunk(sm.w1 + at * 16));
 #pragma unroll
                 for (int e = 0; e < kP; ++e)
                     x[c].v[e] = fmul2(fmul2(x[c].v[e], both(r1)), w.v[e]);
-                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.z) + row + at * 16) = x[c].pack();
+                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.z) + out + at * 16) = x[c].pack();
             }
-        }
-        turn = st.next(p, n);
-    }
+        },
+        [](uint32_t) {});
 }
 
-// kC: as above.  Up to one chunk a thread what both passes over a row need (before
-// and after its sums) stays in registers; with more it is formed again from the
-// stage, which is then released after the second pass.
-template <typename T, int kC, bool kPost, bool kFirst>
-__global__ void __launch_bounds__(kMaxThreads) residual_norm_bwd_kernel(const __grid_constant__ ResidualNormParams p)
+// Up to two chunks a thread what both passes over a row need stays in registers;
+// with more it is formed again.
+template <typename T, int kC, bool kSub, bool kPost>
+__global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_bwd_kernel(
+    const __grid_constant__ ResidualNormParams p)
 {
-    constexpr int kIn = kFirst ? 3 : 4, kP = Chunk<T>::kP, kE = Chunk<T>::kE;
-    constexpr bool kHold = kC == 1;
+    constexpr int kIn = 4, kP = Chunk<T>::kP, kE = Chunk<T>::kE;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     const int row_bytes = p.D * static_cast<int>(sizeof(T)), nvec = row_bytes / 16;
-    const int groups = p.lanes < 32 ? 1 : p.rows;
-    const Smem sm(smem_raw, row_bytes, groups);
+    const Smem sm(smem_raw, p, row_bytes);
     const int threads = static_cast<int>(blockDim.x) - 32;
-    const bool copies = set_up(sm, p, threads);
-    if (!copies) {
-        load_weights(sm.w1, p.w1, 0, row_bytes, threads);
-        if (kPost)
-            load_weights(sm.w2, p.w2, 0, row_bytes, threads);
-    }
+    const bool copies = set_up<T>(p, sm, threads, 33);
+    Worker<T, kIn, kPost ? 3 : 1> me(p, sm, threads);
+    if (!copies)
+        me.load_f(0);
     __syncthreads();
     if (copies) {
-        if (lane_id() == 0) {
-            const uint8_t *in[kIn];
-            in[0] = static_cast<const uint8_t *>(p.x);
-            in[1] = static_cast<const uint8_t *>(p.dz);
-            in[2] = static_cast<const uint8_t *>(p.dh);
-            if constexpr (!kFirst)
-                in[3] = static_cast<const uint8_t *>(p.y);
-            copy_rows<kIn>(p, sm, in, row_bytes);
-        }
+        const uint8_t *in[kIn] = {static_cast<const uint8_t *>(p.x), static_cast<const uint8_t *>(p.dz),
+                                  static_cast<const uint8_t *>(p.dh), static_cast<const uint8_t *>(p.y)};
+        copy_rows<kIn, true>(p, sm, in, row_bytes);
         return;
     }
-    const int mine = threadIdx.x / p.per_row, cl = threadIdx.x % p.per_row;
-    const int group = p.lanes < 32 ? 0 : mine;
-    RowSum<kPost ? 3 : 1> sum{sm.sums + group * 2 * kMaxWarps, p.lanes, p.lanes < 32 ? 1 : p.per_row / 32, group};
-    const bool gated = !kFirst && p.gate != nullptr;
-    const bool has_dh = p.dh != nullptr;
+    const bool has_dh = p.dh != nullptr, has_y = p.y != nullptr;
+    const size_t pitch = static_cast<size_t>(p.slot_rows) * row_bytes;  // of a slot's tensors
     const float inv_d = 1.f / static_cast<float>(p.D);
-    const size_t pitch = static_cast<size_t>(p.rows) * row_bytes;  // of a stage's tensors
-    float2 a1[kC][kP], aA[kFirst ? 1 : kC][kP];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    float2 a1[kC][kP], aA[kC][kP];
 #pragma unroll
     for (int c = 0; c < kC; ++c)
 #pragma unroll
-        for (int e = 0; e < kP; ++e) {
-            a1[c][e] = make_float2(0.f, 0.f);
-            if constexpr (!kFirst)
-                aA[c][e] = make_float2(0.f, 0.f);
-        }
-    // writes a thread's sums of its columns and takes them back to zero
-    auto flush = [&](float *base, int64_t slot, [[maybe_unused]] int64_t extent, float2(*a)[kP],
+        for (int e = 0; e < kP; ++e)
+            a1[c][e] = aA[c][e] = make_float2(0.f, 0.f);
+    // writes the block's sums of its columns, of all its groups in order, as one
+    // row, and takes the threads' own back to zero
+    auto flush = [&](float *base, int64_t row, [[maybe_unused]] int64_t extent, float2(&a)[kC][kP],
                      [[maybe_unused]] unsigned site) {
-        if (mine >= p.rows)  // a row of fewer lanes than a warp, and no other row beside it
+        if (p.parts == 0) {  // one row at once: the threads' columns are the block's
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                const int at = me.col + c * me.width;
+                const int64_t off = row * p.D + static_cast<int64_t>(at) * kE;
+#pragma unroll
+                for (int e = 0; e < kP; ++e) {
+                    if (at < nvec && ULY_IN_BOUNDS(p.w.status, off + 2 * e, 2, extent, site))
+                        *reinterpret_cast<float2 *>(base + off + 2 * e) = a[c][e];
+                    a[c][e] = make_float2(0.f, 0.f);
+                }
+            }
             return;
+        }
+        float *mine = sm.scratch + static_cast<size_t>(me.group * (32 / p.lanes) + me.sub) * p.D;
+        named_bar_sync(15, threads);
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
-            const int at = cl + c * p.per_row;
-            const int64_t off = (slot * p.rows + mine) * p.D + static_cast<int64_t>(at) * kE;
-            if (at < nvec && ULY_IN_BOUNDS(p.w.status, off, kE, extent, site))
+            const int at = me.col + c * me.width;
+#pragma unroll
+            for (int e = 0; e < kP; ++e) {
+                if (at < nvec)
+                    *reinterpret_cast<float2 *>(mine + at * kE + 2 * e) = a[c][e];
+                a[c][e] = make_float2(0.f, 0.f);
+            }
+        }
+        named_bar_sync(15, threads);
+        for (int i = threadIdx.x; i < p.D; i += threads) {
+            float t = sm.scratch[i];
+            for (int j = 1; j < p.parts; ++j)
+                t += sm.scratch[static_cast<size_t>(j) * p.D + i];
+            if (ULY_IN_BOUNDS(p.w.status, row * p.D + i, 1, extent, site))
+                base[row * p.D + i] = t;
+        }
+    };
+    me.template go<kSub>(
+        0xa3,
+        [&](uint32_t row0, int r, bool live, const uint8_t *from, int slot) {
+            const float *stats = sm.stats + slot * 2 * kMaxRows + r;
+            const float m1 = live ? stats[0] : 0.f, m2 = live && kPost ? stats[kMaxRows] : 0.f;
+            constexpr bool kHold = kC <= 2;
+            auto there = [&](int c) { return (!kSub || live) && (c < kC - 2 || me.col + c * me.width < nvec); };
+            // hh, yh, b = dh + r1 w1 dz and f of one chunk
+            auto form = [&](int c, Chunk<T> &hh, Chunk<T> &yh, Chunk<T> &b, Chunk<T> &f, Chunk<T> &dz, Chunk<T> &gz) {
+                const int at = me.col + c * me.width;
+                hh.unpack(ld_chunk(from + at * 16));
+                dz.unpack(ld_chunk(from + pitch + at * 16));
+                gz.unpack(ld_chunk(sm.w1 + at * 16));
+                f.read(sm.f + at * kE);
+                if (has_dh)
+                    b.unpack(ld_chunk(from + 2 * pitch + at * 16));
+                else
+                    b.unpack(zero);
+                if (has_y)
+                    yh.unpack(ld_chunk(from + 3 * pitch + at * 16));
+                else
+                    yh.unpack(zero);
+#pragma unroll
+                for (int e = 0; e < kP; ++e) {
+                    if (kPost)
+                        yh.v[e] = fmul2(yh.v[e], both(m2));
+                    hh.v[e] = fmul2(ffma2(f.v[e], yh.v[e], hh.v[e]), both(m1));
+                    gz.v[e] = fmul2(gz.v[e], dz.v[e]);
+                    b.v[e] = ffma2(gz.v[e], both(m1), b.v[e]);
+                }
+            };
+            constexpr int kKept = kHold ? kC : 1;
+            Chunk<T> hh[kKept], yh[kKept], b[kKept], f, dz, gz;
+            float2 q1 = make_float2(0.f, 0.f), q2 = q1, q3 = q1;
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                const int i = kHold ? c : 0;
+                if (!there(c))
+                    continue;
+                form(c, hh[i], yh[i], b[i], f, dz, gz);
+#pragma unroll
+                for (int e = 0; e < kP; ++e) {
+                    q1 = ffma2(gz.v[e], hh[i].v[e], q1);
+                    a1[c][e] = ffma2(dz.v[e], hh[i].v[e], a1[c][e]);
+                    if constexpr (kPost) {
+                        const float2 fy = fmul2(f.v[e], yh[i].v[e]);
+                        q2 = ffma2(fy, b[i].v[e], q2);
+                        q3 = ffma2(fy, hh[i].v[e], q3);
+                    }
+                }
+            }
+            float s[kPost ? 3 : 1];
+            s[0] = q1.x + q1.y;
+            if constexpr (kPost) {
+                s[1] = q2.x + q2.y;
+                s[2] = q3.x + q3.y;
+            }
+            me.sum(s);
+            const float k1 = m1 * (s[0] * inv_d);
+            float k2 = 0.f;
+            if constexpr (kPost)
+                k2 = m2 * (fmaf(-k1, s[2], s[1]) * inv_d);
+            if (!live || !ULY_IN_BOUNDS(p.w.status, row0 + r, 1, p.T, 0x54))
+                return;
+            const int64_t out = static_cast<int64_t>(row0 + r) * row_bytes;
+            uint8_t *dx = static_cast<uint8_t *>(p.dx) + out, *dy = static_cast<uint8_t *>(p.dy) + out;
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                const int i = kHold ? c : 0, at = me.col + c * me.width;
+                if (!there(c))
+                    continue;
+                if constexpr (kHold)
+                    f.read(sm.f + at * kE);
+                else
+                    form(c, hh[i], yh[i], b[i], f, dz, gz);
+                Chunk<T> t;
 #pragma unroll
                 for (int e = 0; e < kP; ++e)
-                    *reinterpret_cast<float2 *>(base + off + 2 * e) = a[c][e];
+                    t.v[e] = ffma2(hh[i].v[e], both(-k1), b[i].v[e]);
+                *reinterpret_cast<uint4 *>(dx + at * 16) = t.pack();
+                if (has_y) {
 #pragma unroll
-            for (int e = 0; e < kP; ++e)
-                a[c][e] = make_float2(0.f, 0.f);
-        }
-    };
-    bool turn = true;
-    Stages st(p);
-    float r1 = 0.f, r2 = 0.f;  // of the next stage's row, read a stage ahead
-    auto statistics = [&](const Stages &s) {
-        r1 = r2 = 0.f;
-        if (s.more() && mine < s.count(p) && ULY_IN_BOUNDS(p.w.status, s.row + mine, 1, p.T, 0x53)) {
-            r1 = p.rstd[s.row + mine];
-            r2 = kPost ? p.rstd[p.T + s.row + mine] : 1.f;
-        }
-    };
-    statistics(st);
-    for (int k = 0; st.more(); ++k) {
-        const int n = st.count(p), slot = k % p.stages;
-        if (turn && gated) {
-            named_bar_sync(15, threads);
-            load_weights(sm.gate, p.gate, p.gates > 1 ? st.run % p.gates : 0, row_bytes, threads);
-            named_bar_sync(15, threads);
-        }
-        const int64_t row0 = st.row, run = st.run;
-        const float m1 = r1, m2 = r2;
-        turn = st.next(p, n);
-        statistics(st);
-        await(sm, p, k, 0xa3);
-        const bool live = mine < n;
-        const uint8_t *from = sm.ring + slot * kIn * pitch + static_cast<size_t>(mine) * row_bytes;
-        // hh, yh, b = dh + r1 w1 dz and f = a g w2 (what yh has in h) of one chunk
-        auto form = [&](int c, Chunk<T> &hh, Chunk<T> &yh, Chunk<T> &b, Chunk<T> &f, Chunk<T> &dz, Chunk<T> &w) {
-            const int at = cl + c * p.per_row;
-            const bool in = live && at < nvec;
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            hh.unpack(in ? ld_chunk(from + at * 16) : zero);
-            dz.unpack(in ? ld_chunk(from + pitch + at * 16) : zero);
-            b.unpack(in && has_dh ? ld_chunk(from + 2 * pitch + at * 16) : zero);
-            w.unpack(in ? ld_chunk(sm.w1 + at * 16) : zero);
-            if constexpr (!kFirst) {
-                yh.unpack(in ? ld_chunk(from + 3 * pitch + at * 16) : zero);
-                Chunk<T> o;
-                if (gated)
-                    f.unpack(in ? ld_chunk(sm.gate + at * 16) : zero);
-                if (kPost)
-                    o.unpack(in ? ld_chunk(sm.w2 + at * 16) : zero);
-#pragma unroll
-                for (int e = 0; e < kP; ++e) {
-                    f.v[e] = gated ? fmul2(f.v[e], both(p.scale)) : both(p.scale);
-                    if (kPost) {
-                        f.v[e] = fmul2(f.v[e], o.v[e]);
-                        yh.v[e] = fmul2(yh.v[e], both(m2));
+                    for (int e = 0; e < kP; ++e) {
+                        aA[c][e] = ffma2(t.v[e], yh[i].v[e], aA[c][e]);
+                        t.v[e] = fmul2(t.v[e], f.v[e]);
+                        if constexpr (kPost)
+                            t.v[e] = ffma2(yh[i].v[e], both(-k2), fmul2(t.v[e], both(m2)));
                     }
-                    hh.v[e] = ffma2(f.v[e], yh.v[e], hh.v[e]);
+                    *reinterpret_cast<uint4 *>(dy + at * 16) = t.pack();
                 }
             }
-#pragma unroll
-            for (int e = 0; e < kP; ++e) {
-                hh.v[e] = fmul2(hh.v[e], both(m1));
-                w.v[e] = fmul2(w.v[e], dz.v[e]);
-                b.v[e] = ffma2(w.v[e], both(m1), b.v[e]);
-            }
-        };
-        Chunk<T> hh, yh, b, f, dz, gz;
-        float2 q1 = make_float2(0.f, 0.f), q2 = q1, q3 = q1;
-#pragma unroll
-        for (int c = 0; c < kC; ++c) {
-            form(c, hh, yh, b, f, dz, gz);
-#pragma unroll
-            for (int e = 0; e < kP; ++e) {
-                q1 = ffma2(gz.v[e], hh.v[e], q1);
-                a1[c][e] = ffma2(dz.v[e], hh.v[e], a1[c][e]);
-                if constexpr (kPost) {
-                    const float2 fy = fmul2(f.v[e], yh.v[e]);
-                    q2 = ffma2(fy, b.v[e], q2);
-                    q3 = ffma2(fy, hh.v[e], q3);
-                }
-            }
-        }
-        auto release = [&]() {
-            __syncwarp();
-            if (lane_id() == 0)
-                mbar_arrive(&sm.empty[slot]);
-        };
-        if (kHold)
-            release();
-        float s[kPost ? 3 : 1];
-        s[0] = q1.x + q1.y;
-        if constexpr (kPost) {
-            s[1] = q2.x + q2.y;
-            s[2] = q3.x + q3.y;
-        }
-        sum(s);
-        const float k1 = m1 * (s[0] * inv_d);
-        float k2 = 0.f;
-        if constexpr (kPost)
-            k2 = m2 * (fmaf(-k1, s[2], s[1]) * inv_d);
-        const bool store = live && ULY_IN_BOUNDS(p.w.status, row0 + mine, 1, p.T, 0x54);
-        const int64_t out = (row0 + mine) * row_bytes;
-#pragma unroll
-        for (int c = 0; c < kC; ++c) {
-            const int at = cl + c * p.per_row;
-            const bool in = store && at < nvec;
-            if (!kHold)
-                form(c, hh, yh, b, f, dz, gz);
-            Chunk<T> t;
-#pragma unroll
-            for (int e = 0; e < kP; ++e)
-                t.v[e] = ffma2(hh.v[e], both(-k1), b.v[e]);
-            if (in)
-                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.dx) + out + at * 16) = t.pack();
-            if constexpr (!kFirst) {
-#pragma unroll
-                for (int e = 0; e < kP; ++e) {
-                    aA[c][e] = ffma2(t.v[e], yh.v[e], aA[c][e]);
-                    t.v[e] = fmul2(t.v[e], f.v[e]);
-                    if constexpr (kPost)
-                        t.v[e] = ffma2(yh.v[e], both(-k2), fmul2(t.v[e], both(m2)));
-                }
-                if (in)
-                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.dy) + out + at * 16) = t.pack();
-            }
-        }
-        if (!kHold)
-            release();
-        if constexpr (!kFirst)
-            if ((turn || !st.more()) && p.partA)
+        },
+        [&](uint32_t run) {
+            if (p.partA)
                 flush(p.partA, blockIdx.x + run, p.partA_elems, aA, 0x55);
-    }
+        });
     if (p.part1)
         flush(p.part1, blockIdx.x, p.part1_elems, a1, 0x56);
 }
@@ -543,6 +648,7 @@ __global__ void __launch_bounds__(32 * kJoinLanes) residual_norm_join_kernel(con
         (void)extent;
         float s = 0.f;
         if (in)
+#pragma unroll 4
             for (int64_t r = first + j; r < last; r += kJoinLanes)
                 if (ULY_IN_BOUNDS(p.w.status, r * p.D + col, 1, extent, 0x57))
                     s += base[r * p.D + col];
@@ -573,7 +679,7 @@ __global__ void __launch_bounds__(32 * kJoinLanes) residual_norm_join_kernel(con
         }
     };
     if (p.dw1)
-        write(p.dw1, col, across(column(p.part1, 0, static_cast<int64_t>(blocks) * p.rows, p.part1_elems)));
+        write(p.dw1, col, across(column(p.part1, 0, blocks, p.part1_elems)));
     if (!p.dw2 && !p.dgate)
         return;
     auto block_of = [&](int64_t row) { return ((row + 1) * blocks - 1) / p.T; };
@@ -584,7 +690,7 @@ __global__ void __launch_bounds__(32 * kJoinLanes) residual_norm_join_kernel(con
         float s = 0.f;
         for (int64_t run = b; run < runs; run += gates) {
             const int64_t lo = block_of(run * p.run), hi = block_of((run + 1) * p.run - 1);
-            s += column(p.partA, (lo + run) * p.rows, (hi + run + 1) * p.rows, p.partA_elems);
+            s += column(p.partA, lo + run, hi + run + 1, p.partA_elems);
         }
         const float A = p.scale * across(s);
         if (p.dgate && in)
@@ -598,67 +704,88 @@ __global__ void __launch_bounds__(32 * kJoinLanes) residual_norm_join_kernel(con
 
 // How rows are laid over a block's threads.
 struct Plan {
-    int chunks, per_row, lanes, rows, stages, blocks, threads;
+    int chunks, warps, lanes, groups, parts, slot_rows, slots, blocks, threads;
     size_t smem;
 };
 
-Plan plan_for(int64_t T, int64_t run, int row_bytes, int tensors)
+Plan plan_for(int64_t T, int64_t run, int D, int esize, bool bwd)
 {
     Plan q;
-    const int nvec = row_bytes / 16;
-    q.chunks = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
-    const int need = (nvec + q.chunks - 1) / q.chunks;
-    q.per_row = 1;
-    if (need > 32)
-        q.per_row = (need + 31) / 32 * 32;
-    else
-        while (q.per_row < need)
-            q.per_row *= 2;
-    q.lanes = q.per_row < 32 ? q.per_row : 32;
-    // several short rows at once, as many as fill 256 threads, but no more than a gate's run holds
-    q.rows = 1;
-    while (q.rows * 2 * q.per_row <= 256 && q.rows * 2 <= run && (q.per_row <= 32 || q.rows < 8))
-        q.rows *= 2;
-    q.threads = (q.rows * q.per_row + 31) / 32 * 32 + 32;
-    const int stage = tensors * q.rows * row_bytes;
-    const size_t fixed = 256 + static_cast<size_t>(q.lanes < 32 ? 1 : q.rows) * 2 * kMaxWarps * sizeof(float4) +
-                         3 * static_cast<size_t>(row_bytes);
-    // two or three blocks an SM, and in all about 100 KB (their stages) on the way
-    const int per_sm = q.threads <= 384 ? 2 : 1;
-    const size_t room = (per_sm == 2 ? 110 : 220) * 1024 - fixed;
-    int64_t stages = static_cast<int64_t>(room) / stage;
-    q.stages = static_cast<int>(stages < 1 ? 1 : stages > kMaxStages ? kMaxStages : stages);
-    while (q.stages > 2 && static_cast<int64_t>(q.stages - 1) * stage * per_sm >= 128 * 1024)
-        --q.stages;
-    q.smem = fixed + static_cast<size_t>(q.stages) * stage;
-    const int64_t most = (T + q.rows - 1) / q.rows;
-    q.blocks = static_cast<int>(std::min<int64_t>(most, static_cast<int64_t>(num_sms()) * per_sm));
+    const int row_bytes = D * esize, nvec = row_bytes / 16, tensors = bwd ? 4 : 2;
+    // Chunks a thread and warps a row: as many rows at once as possible, a thread's
+    // chunks counted against it; of equals the one with fewer warps a row.
+    constexpr int kFwd[] = {1, 2, 3, 4, 6, 8, 10}, kBwd[] = {1, 2, 3, 4, 5};
+    q.chunks = 0;
+    for (int i = 0; i < (bwd ? 5 : 7); ++i) {
+        const int c = bwd ? kBwd[i] : kFwd[i], w = (nvec + 32 * c - 1) / (32 * c);
+        if (w > kMaxWarps)
+            continue;
+        const int g = kMaxWarps / w;
+        if (q.chunks == 0 || g * q.chunks >= q.groups * c)
+            q.chunks = c, q.warps = w, q.groups = g;
+    }
+    q.lanes = 32;
+    while (q.lanes > 1 && q.lanes / 2 >= nvec)
+        q.lanes /= 2;
+    q.parts = q.groups * (32 / q.lanes) > 1 ? q.groups * (32 / q.lanes) : 0;
+    // a slot: one row, or short ones up to 4 KB of a tensor, as long as every group has one
+    const int64_t share = (T + static_cast<int64_t>(num_sms()) * q.groups - 1) / (num_sms() * q.groups);
+    q.slot_rows = static_cast<int>(std::min(std::min<int64_t>(run, kMaxRows),
+                                            std::max<int64_t>(1, std::min<int64_t>(share, 4096 / row_bytes))));
+    const size_t slot = static_cast<size_t>(tensors) * q.slot_rows * row_bytes;
+    const size_t all = static_cast<size_t>(227) * 1024;
+    auto fixed = [&](int slots) { return Smem::fixed(D, row_bytes, bwd ? q.parts : 0, bwd ? slots : 0); };
+    int slots = 1;
+    while (slots < kMaxSlots && fixed(slots + 1) + (slots + 1) * slot <= all)
+        ++slots;
+    // every group its own slots, two at least where that leaves a group
+    q.groups = std::max(1, std::min(q.groups, slots / 2));
+    q.slots = slots / q.groups * q.groups;
+    while (q.slots > 2 * q.groups && (q.slots - q.groups) * slot >= 128 * 1024)
+        q.slots -= q.groups;
+    q.parts = q.groups * (32 / q.lanes) > 1 ? q.groups * (32 / q.lanes) : 0;
+    q.threads = (q.groups * q.warps + 1) * 32;
+    q.smem = fixed(q.slots) + q.slots * slot;
+    const int64_t units = (T + q.slot_rows - 1) / q.slot_rows;
+    q.blocks = static_cast<int>(std::min<int64_t>(units, num_sms()));
     return q;
 }
 
-template <typename T, int kC>
-cudaError_t launch_main(const ResidualNormParams &p, const Plan &q, bool bwd, cudaStream_t s)
+template <typename T, int kC, bool kSub>
+auto kernel_for(bool post, bool bwd) -> void (*)(const ResidualNormParams)
 {
-    using Kernel = void (*)(const ResidualNormParams);
-    Kernel k;
-    if (bwd)
-        k = !p.y ? residual_norm_bwd_kernel<T, kC, false, true>
-                 : p.w2 ? residual_norm_bwd_kernel<T, kC, true, false> : residual_norm_bwd_kernel<T, kC, false, false>;
-    else
-        k = !p.y ? residual_norm_fwd_kernel<T, kC, false, true>
-                 : p.w2 ? residual_norm_fwd_kernel<T, kC, true, false> : residual_norm_fwd_kernel<T, kC, false, false>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(q.smem));
-    if (e != cudaSuccess)
-        return e;
-    k<<<q.blocks, q.threads, q.smem, s>>>(p);
-    return cudaGetLastError();
+    if (bwd) {
+        if constexpr (kC <= 5)
+            return post ? residual_norm_bwd_kernel<T, kC, kSub, true> : residual_norm_bwd_kernel<T, kC, kSub, false>;
+        return nullptr;
+    }
+    if constexpr (kC != 5)
+        return post ? residual_norm_fwd_kernel<T, kC, kSub, true> : residual_norm_fwd_kernel<T, kC, kSub, false>;
+    return nullptr;
 }
 
 template <typename T>
 cudaError_t launch_typed(const ResidualNormParams &p, const Plan &q, bool bwd, cudaStream_t s)
 {
-    cudaError_t e = q.chunks == 1 ? launch_main<T, 1>(p, q, bwd, s)
-                                  : q.chunks == 2 ? launch_main<T, 2>(p, q, bwd, s) : launch_main<T, 4>(p, q, bwd, s);
+    const bool post = p.w2 != nullptr;
+    void (*k)(const ResidualNormParams) = nullptr;
+    switch (q.chunks) {
+    case 1: k = q.lanes < 32 ? kernel_for<T, 1, true>(post, bwd) : kernel_for<T, 1, false>(post, bwd); break;
+    case 2: k = kernel_for<T, 2, false>(post, bwd); break;
+    case 3: k = kernel_for<T, 3, false>(post, bwd); break;
+    case 4: k = kernel_for<T, 4, false>(post, bwd); break;
+    case 5: k = kernel_for<T, 5, false>(post, bwd); break;
+    case 6: k = kernel_for<T, 6, false>(post, bwd); break;
+    case 8: k = kernel_for<T, 8, false>(post, bwd); break;
+    case 10: k = kernel_for<T, 10, false>(post, bwd); break;
+    }
+    if (k == nullptr)
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(q.smem));
+    if (e != cudaSuccess)
+        return e;
+    k<<<q.blocks, q.threads, q.smem, s>>>(p);
+    e = cudaGetLastError();
     if (e != cudaSuccess || !bwd || !(p.part1 || p.partA))
         return e;
     residual_norm_join_kernel<T><<<static_cast<unsigned>((p.D + 31) / 32), 32 * kJoinLanes, 0, s>>>(p, q.blocks);
@@ -672,35 +799,36 @@ size_t up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
 void partial_bytes(const Plan &q, int64_t T, int64_t run, int D, size_t &one, size_t &gates)
 {
     const int64_t runs = (T + run - 1) / run;
-    one = up(static_cast<size_t>(q.blocks) * q.rows * D * sizeof(float));
-    gates = up(static_cast<size_t>(q.blocks + runs) * q.rows * D * sizeof(float));
+    one = up(static_cast<size_t>(q.blocks) * D * sizeof(float));
+    gates = up(static_cast<size_t>(q.blocks + runs) * D * sizeof(float));
 }
 
 }  // namespace
 
 size_t residual_norm_workspace(int64_t T, int64_t Np, int D)
 {
-    // the largest of the element types, gates shared or a sequence's own, block or none before the norm
+    // the largest of the element types, gates shared or a sequence's own
     size_t most = 0;
     for (int es = 2; es <= 4; es += 2)
-        for (int shared = 0; shared < 2; ++shared)
-            for (int tensors = 3; tensors <= 4; ++tensors) {
-                const int64_t run = shared ? T : Np;
-                size_t one, gates;
-                partial_bytes(plan_for(T, run, D * es, tensors), T, run, D, one, gates);
-                most = std::max(most, one + gates);
-            }
+        for (const int64_t run : {T, Np}) {
+            if (D * es > 32768)
+                continue;
+            size_t one, gates;
+            partial_bytes(plan_for(T, run, D, es, true), T, run, D, one, gates);
+            most = std::max(most, one + gates);
+        }
     return most;
 }
 
 cudaError_t launch_residual_norm(ResidualNormParams &p, bool bwd, int esize, void *workspace, cudaStream_t s)
 {
-    const int tensors = (bwd ? 3 : 1) + (p.y ? 1 : 0);
-    const Plan q = plan_for(p.T, p.run, p.D * esize, tensors);
-    p.per_row = q.per_row;
+    const Plan q = plan_for(p.T, p.run, p.D, esize, bwd);
+    p.warps = q.warps;
     p.lanes = q.lanes;
-    p.rows = q.rows;
-    p.stages = q.stages;
+    p.groups = q.groups;
+    p.parts = bwd ? q.parts : 0;
+    p.slot_rows = q.slot_rows;
+    p.slots = q.slots;
     p.w = wait_cfg();
     if (bwd && workspace) {
         size_t one, gates;

@@ -345,10 +345,10 @@ struct ResidualNormParams {
     int64_t run;  // neighbouring tokens that share a gate: N/P with a gate for every sequence, else T
     int gates;    // rows of gate: 0, 1 or B
     int D;
-    // set by the launch: threads a row has and the lanes its sums are taken over
-    // first, rows and stages of the ring, the blocks' sums
-    int per_row, lanes, rows, stages;
-    float *part1, *partA;  // [blocks][rows][D], [blocks + runs][rows][D]
+    // set by the launch: warps of a group and the lanes a row has in a warp, groups of
+    // a block, rows it works on at once (backward; 0 for one), rows of a slot, slots of the ring
+    int warps, lanes, groups, parts, slot_rows, slots;
+    float *part1, *partA;  // the blocks' sums: [blocks][D], [blocks + runs][D]
     int64_t part1_elems, partA_elems;
     WaitCfg w;
 };

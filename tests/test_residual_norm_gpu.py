@@ -1,4 +1,4 @@
-"""ulysses_residual_norm_fwd / _bwd against fp64 on the CPU.
+"""ulysses_residual_norm_fwd / _bwd against fp64.
 
 Tolerances, element by element: an output is off by its own rounding, u times its
 value (u = eps/2 of its type, 2^-8 in bf16, 2^-24 in fp32), and by the fp32
@@ -40,6 +40,7 @@ def make(B, N, P, D, gate, post, first, dtype, seed=0, scale=0.75):
 
 def reference(c, scale):
     """Values and gradients in fp64 by autograd, and the magnitudes that bound the fp32 arithmetic."""
+    c = _gpu(c)
     x, y, w, post, gate = (None if c[n] is None else c[n].double().requires_grad_(True)
                            for n in ("x", "y", "weight", "post", "gate"))
     D = x.shape[-1]
@@ -78,7 +79,7 @@ def reference(c, scale):
 
 
 def close(name, got, want, unit, extra):
-    got = got.detach().cpu().double()
+    got = got.detach().double()
     assert got.shape == want.shape, name
     off = (got - want).abs() - (unit * want.abs() + extra)
     worst = off.max().item()
@@ -102,6 +103,12 @@ CASES = [
     (2, 55, 5, 128, None, False, True),
     (1, 321, 1, 2560, None, False, True),
     (40, 2, 2, 16, "sequence", True, False),
+    # many slots a block: every ring goes round several times
+    (1, 9600, 4, 2560, "shared", True, False),
+    (2, 9063, 3, 776, "sequence", True, False),
+    (1, 60000, 2, 64, "shared", True, False),
+    (1, 3100, 1, 8192, None, False, False),
+    (1, 3100, 1, 2048, None, False, True),
 ]
 
 
