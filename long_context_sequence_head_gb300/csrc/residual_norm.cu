@@ -79,27 +79,41 @@ struct Chunk {
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ uint4 ld_chunk(const uint8_t *p) { return *reinterpret_cast<const uint4 *>(p); }
 
-// The rows of a block in slots of at most p.slot_rows rows that share a gate.
+// The rows of a block in slots of at most p.slot_rows rows.  Where all rows share
+// one gate, the blocks' slots alternate, so that all of them work on neighbouring
+// memory; with a gate for every sequence a block takes a run of rows, in slots
+// that share one.
 struct Slots {
-    uint32_t row, end, run_end;  // fewer than 2^31 rows
+    uint32_t row, end, run_end, step;  // fewer than 2^31 rows
     uint32_t run;
 
     __device__ __forceinline__ explicit Slots(const ResidualNormParams &p)
     {
-        row = static_cast<uint32_t>(p.T * blockIdx.x / gridDim.x);
-        end = static_cast<uint32_t>(p.T * (blockIdx.x + 1) / gridDim.x);
-        run = row / static_cast<uint32_t>(p.run);
-        run_end = (run + 1) * static_cast<uint32_t>(p.run);
+        if (p.gates > 1) {
+            row = static_cast<uint32_t>(p.T * blockIdx.x / gridDim.x);
+            end = static_cast<uint32_t>(p.T * (blockIdx.x + 1) / gridDim.x);
+            run = row / static_cast<uint32_t>(p.run);
+            run_end = (run + 1) * static_cast<uint32_t>(p.run);
+        } else {
+            row = blockIdx.x * p.slot_rows;
+            end = run_end = static_cast<uint32_t>(p.T);
+            run = 0;
+        }
+        step = gridDim.x * p.slot_rows;
     }
     __device__ __forceinline__ bool more() const { return row < end; }
     __device__ __forceinline__ int count(const ResidualNormParams &p) const
     {
         return static_cast<int>(min(min(run_end, end) - row, static_cast<uint32_t>(p.slot_rows)));
     }
-    // true if the next slot has another gate
-    __device__ __forceinline__ bool next(const ResidualNormParams &p, int n)
+    // the next slot (with one gate: the block's n-th from here); true if it has another gate
+    __device__ __forceinline__ bool next(const ResidualNormParams &p, int rows, int n = 1)
     {
-        row += n;
+        if (p.gates <= 1) {
+            row += n * step;  // below 2^31 + 15 * 152 * 32
+            return false;
+        }
+        row += rows;
         if (row < run_end)
             return false;
         ++run;
@@ -140,7 +154,7 @@ struct Smem {
     }
 };
 
-// The copying warp: slots of kIn tensors' rows (some may be null); kStats: with
+// The copying warp, which starts before the block meets: slots of kIn tensors' rows (some may be null); kStats: with
 // each row's two statistics, a lane a row, by 4-byte copies that arrive on the
 // same barrier.
 template <int kIn, bool kStats>
@@ -154,7 +168,12 @@ __device__ __forceinline__ void copy_rows(const ResidualNormParams &p, const Sme
     const int own = p.slots / p.groups;
     int k = 0, group = 0, at = 0;
     uint32_t phase = 0;
+    bool met = false;
     for (; st.more() && !*sm.abort; ++k) {
+        if (k == p.groups && !met) {  // no more until the weights are there
+            __syncthreads();
+            met = true;
+        }
         const int slot = group * own + at, n = st.count(p);
         if (!mbar_wait_warp(&sm.empty[slot], phase ^ 1, p.w, 0xa1)) {
             *sm.abort = 1;
@@ -196,6 +215,8 @@ __device__ __forceinline__ void copy_rows(const ResidualNormParams &p, const Sme
         __syncwarp();
         st.next(p, n);
     }
+    if (!met)
+        __syncthreads();
     if (*sm.abort)  // wait (bounded) for the copies that are on their way
         for (int i = k > p.slots ? k - p.slots : 0; i < k; ++i) {
             const int turn = i / p.groups;
@@ -314,7 +335,7 @@ struct Worker {
         uint32_t phase = 0;
         bool turn = p.gates > 1;
         if (!turn)
-            st.row += group * p.slot_rows;
+            st.next(p, 0, group);
         // with a gate for every sequence all threads go through all slots, to
         // change it together; without, a group's slots are evenly spaced
         while (st.more()) {
@@ -331,7 +352,7 @@ struct Worker {
                 whose = whose + 1 == p.groups ? 0 : whose + 1;
                 turn = st.next(p, n);
             } else {
-                st.row += p.groups * p.slot_rows;
+                st.next(p, n, p.groups);
             }
             if (ours) {
                 rows_of(first_slot + at, phase, row0, n);
@@ -348,25 +369,34 @@ struct Worker {
     }
 };
 
-// Barriers, w1 and the first f; true for the copying warp.
-template <typename T>
-__device__ __forceinline__ bool set_up(const ResidualNormParams &p, const Smem &sm, int threads, int copies_arrive)
+// The copying warp sets up the barriers and leaves (true); the others load w1 and
+// the first f, and wait for it.
+template <typename T, int kIn, int kSums>
+__device__ __forceinline__ bool set_up(const ResidualNormParams &p, const Smem &sm, int threads, int copies_arrive,
+                                       const Worker<T, kIn, kSums> &me)
 {
-    if (threadIdx.x == threads) {
-        for (int i = 0; i < p.slots; ++i) {
-            mbar_init(&sm.full[i], copies_arrive);
-            mbar_init(&sm.empty[i], p.warps);
+    if (threadIdx.x >= threads) {
+        if (threadIdx.x == threads) {
+            for (int i = 0; i < p.slots; ++i) {
+                mbar_init(&sm.full[i], copies_arrive);
+                mbar_init(&sm.empty[i], p.warps);
+            }
+            *sm.abort = 0;
+            fence_mbar_init();
         }
-        *sm.abort = 0;
-        fence_mbar_init();
+        __syncwarp();
+        return true;
     }
     const int nvec = p.D * static_cast<int>(sizeof(T)) / 16;
-    for (int i = threadIdx.x; i < nvec; i += blockDim.x)
+    for (int i = threadIdx.x; i < nvec; i += threads)
         reinterpret_cast<uint4 *>(sm.w1)[i] = static_cast<const uint4 *>(p.w1)[i];
-    return threadIdx.x >= threads;
+    if (p.gates <= 1)
+        me.load_f(0);
+    __syncthreads();
+    return false;
 }
 
-// kC: chunks a thread holds of its row; all but the last two are there for every
+// kC: chunks a thread holds of its row; all but the last are there for every
 // thread.  kSub: short rows, several a warp (kC = 1).  kPost: a norm behind the
 // block.
 template <typename T, int kC, bool kSub, bool kPost>
@@ -378,12 +408,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_fwd_kernel(
     const int row_bytes = p.D * static_cast<int>(sizeof(T)), nvec = row_bytes / 16;
     const Smem sm(smem_raw, p, row_bytes);
     const int threads = static_cast<int>(blockDim.x) - 32;
-    const bool copies = set_up<T>(p, sm, threads, 1);
     Worker<T, kIn, 1> me(p, sm, threads);
-    if (!copies)
-        me.load_f(0);
-    __syncthreads();
-    if (copies) {
+    if (set_up(p, sm, threads, 1, me)) {
         const uint8_t *in[kIn] = {static_cast<const uint8_t *>(p.x), static_cast<const uint8_t *>(p.y)};
         copy_rows<kIn, false>(p, sm, in, row_bytes);
         return;
@@ -396,7 +422,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_fwd_kernel(
             // the block's output is read from the slot as often as it is needed; only
             // the sum with the stream stays in registers
             Chunk<T> x[kC], y;
-            auto there = [&](int c) { return (!kSub || live) && (c < kC - 2 || me.col + c * me.width < nvec); };
+            auto there = [&](int c) { return (!kSub || live) && (c < kC - 1 || me.col + c * me.width < nvec); };
             float s[1], r2 = 1.f;
             if constexpr (kPost) {
                 float2 q = make_float2(0.f, 0.f);
@@ -450,13 +476,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_fwd_kernel(
                 if (!there(c))
                     continue;
                 if (p.h)
-                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.h) + out + at * 16) = x[c].pack();
+                    __stcs(reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.h) + out + at * 16), x[c].pack());
                 Chunk<T> w;
                 w.unpack(ld_chunk(sm.w1 + at * 16));
 #pragma unroll
                 for (int e = 0; e < kP; ++e)
                     x[c].v[e] = fmul2(fmul2(x[c].v[e], both(r1)), w.v[e]);
-                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.z) + out + at * 16) = x[c].pack();
+                __stcs(reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.z) + out + at * 16), x[c].pack());
             }
         },
         [](uint32_t) {});
@@ -473,12 +499,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_bwd_kernel(
     const int row_bytes = p.D * static_cast<int>(sizeof(T)), nvec = row_bytes / 16;
     const Smem sm(smem_raw, p, row_bytes);
     const int threads = static_cast<int>(blockDim.x) - 32;
-    const bool copies = set_up<T>(p, sm, threads, 33);
     Worker<T, kIn, kPost ? 3 : 1> me(p, sm, threads);
-    if (!copies)
-        me.load_f(0);
-    __syncthreads();
-    if (copies) {
+    if (set_up(p, sm, threads, 33, me)) {
         const uint8_t *in[kIn] = {static_cast<const uint8_t *>(p.x), static_cast<const uint8_t *>(p.dz),
                                   static_cast<const uint8_t *>(p.dh), static_cast<const uint8_t *>(p.y)};
         copy_rows<kIn, true>(p, sm, in, row_bytes);
@@ -539,7 +561,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_bwd_kernel(
             const float *stats = sm.stats + slot * 2 * kMaxRows + r;
             const float m1 = live ? stats[0] : 0.f, m2 = live && kPost ? stats[kMaxRows] : 0.f;
             constexpr bool kHold = kC <= 2;
-            auto there = [&](int c) { return (!kSub || live) && (c < kC - 2 || me.col + c * me.width < nvec); };
+            auto there = [&](int c) { return (!kSub || live) && (c < kC - 1 || me.col + c * me.width < nvec); };
             // hh, yh, b = dh + r1 w1 dz and f of one chunk
             auto form = [&](int c, Chunk<T> &hh, Chunk<T> &yh, Chunk<T> &b, Chunk<T> &f, Chunk<T> &dz, Chunk<T> &gz) {
                 const int at = me.col + c * me.width;
@@ -612,7 +634,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_bwd_kernel(
 #pragma unroll
                 for (int e = 0; e < kP; ++e)
                     t.v[e] = ffma2(hh[i].v[e], both(-k1), b[i].v[e]);
-                *reinterpret_cast<uint4 *>(dx + at * 16) = t.pack();
+                __stcs(reinterpret_cast<uint4 *>(dx + at * 16), t.pack());
                 if (has_y) {
 #pragma unroll
                     for (int e = 0; e < kP; ++e) {
@@ -621,7 +643,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_bwd_kernel(
                         if constexpr (kPost)
                             t.v[e] = ffma2(yh[i].v[e], both(-k2), fmul2(t.v[e], both(m2)));
                     }
-                    *reinterpret_cast<uint4 *>(dy + at * 16) = t.pack();
+                    __stcs(reinterpret_cast<uint4 *>(dy + at * 16), t.pack());
                 }
             }
         },
@@ -712,40 +734,42 @@ Plan plan_for(int64_t T, int64_t run, int D, int esize, bool bwd)
 {
     Plan q;
     const int row_bytes = D * esize, nvec = row_bytes / 16, tensors = bwd ? 4 : 2;
-    // Chunks a thread and warps a row: as many rows at once as possible, a thread's
-    // chunks counted against it; of equals the one with fewer warps a row.
-    constexpr int kFwd[] = {1, 2, 3, 4, 6, 8, 10}, kBwd[] = {1, 2, 3, 4, 5};
-    q.chunks = 0;
-    for (int i = 0; i < (bwd ? 5 : 7); ++i) {
-        const int c = bwd ? kBwd[i] : kFwd[i], w = (nvec + 32 * c - 1) / (32 * c);
-        if (w > kMaxWarps)
-            continue;
-        const int g = kMaxWarps / w;
-        if (q.chunks == 0 || g * q.chunks >= q.groups * c)
-            q.chunks = c, q.warps = w, q.groups = g;
-    }
+    // The ring: about 100 KB (backward 120).  More on their way do not help and are
+    // shared out unevenly: with 200 KB the first blocks of a 203 us call ended
+    // after 170, the last after 235; with 60 KB all of them after 222.
+    const int64_t room = (bwd ? 122 : 102) * 1024;
     q.lanes = 32;
     while (q.lanes > 1 && q.lanes / 2 >= nvec)
         q.lanes /= 2;
-    q.parts = q.groups * (32 / q.lanes) > 1 ? q.groups * (32 / q.lanes) : 0;
-    // a slot: one row, or short ones up to 4 KB of a tensor, as long as every group has one
-    const int64_t share = (T + static_cast<int64_t>(num_sms()) * q.groups - 1) / (num_sms() * q.groups);
-    q.slot_rows = static_cast<int>(std::min(std::min<int64_t>(run, kMaxRows),
-                                            std::max<int64_t>(1, std::min<int64_t>(share, 4096 / row_bytes))));
-    const size_t slot = static_cast<size_t>(tensors) * q.slot_rows * row_bytes;
-    const size_t all = static_cast<size_t>(227) * 1024;
-    auto fixed = [&](int slots) { return Smem::fixed(D, row_bytes, bwd ? q.parts : 0, bwd ? slots : 0); };
-    int slots = 1;
-    while (slots < kMaxSlots && fixed(slots + 1) + (slots + 1) * slot <= all)
-        ++slots;
-    // every group its own slots, two at least where that leaves a group
-    q.groups = std::max(1, std::min(q.groups, slots / 2));
-    q.slots = slots / q.groups * q.groups;
-    while (q.slots > 2 * q.groups && (q.slots - q.groups) * slot >= 128 * 1024)
-        q.slots -= q.groups;
+    // A slot: a row, or as many short ones as leave two slots for each of 15 warps,
+    // but no more than every warp has some of.
+    const int64_t share = (T + static_cast<int64_t>(num_sms()) * kMaxWarps - 1) / (num_sms() * kMaxWarps);
+    const int64_t fit = room / (2 * kMaxWarps * tensors) / row_bytes;
+    q.slot_rows = static_cast<int>(
+        std::min(std::min<int64_t>(run, kMaxRows), std::max<int64_t>(1, std::min<int64_t>(share, fit))));
+    const int64_t slot = static_cast<int64_t>(tensors) * q.slot_rows * row_bytes;
+    // Groups of two slots each, and the warps among them; a thread has up to 4 chunks
+    // of a row (backward 2, whose sums stay in registers) unless 15 warps are too few.
+    const int64_t slots = std::max<int64_t>(1, room / slot);
+    q.groups = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxWarps, slots / 2)));
+    const int cap = bwd ? 2 : 4;
+    q.warps = std::max(kMaxWarps / q.groups, std::min(kMaxWarps, (nvec + 32 * cap - 1) / (32 * cap)));
+    q.chunks = (nvec + 32 * q.warps - 1) / (32 * q.warps);
+    q.warps = (nvec + 32 * q.chunks - 1) / (32 * q.chunks);
+    q.groups = std::min(q.groups, kMaxWarps / q.warps);
     q.parts = q.groups * (32 / q.lanes) > 1 ? q.groups * (32 / q.lanes) : 0;
     q.threads = (q.groups * q.warps + 1) * 32;
-    q.smem = fixed(q.slots) + q.slots * slot;
+    // every group its own slots
+    const size_t most = static_cast<size_t>(227) * 1024;
+    auto bytes = [&](int own) {
+        const int n = own * q.groups;
+        return Smem::fixed(D, row_bytes, bwd ? q.parts : 0, bwd ? n : 0) + static_cast<size_t>(n) * slot;
+    };
+    int own = static_cast<int>(std::max<int64_t>(2, std::min<int64_t>(slots, kMaxSlots) / q.groups));
+    while (own > 1 && (own * q.groups > kMaxSlots || bytes(own) > most))
+        --own;
+    q.slots = own * q.groups;
+    q.smem = bytes(own);
     const int64_t units = (T + q.slot_rows - 1) / q.slot_rows;
     q.blocks = static_cast<int>(std::min<int64_t>(units, num_sms()));
     return q;
@@ -754,14 +778,9 @@ Plan plan_for(int64_t T, int64_t run, int D, int esize, bool bwd)
 template <typename T, int kC, bool kSub>
 auto kernel_for(bool post, bool bwd) -> void (*)(const ResidualNormParams)
 {
-    if (bwd) {
-        if constexpr (kC <= 5)
-            return post ? residual_norm_bwd_kernel<T, kC, kSub, true> : residual_norm_bwd_kernel<T, kC, kSub, false>;
-        return nullptr;
-    }
-    if constexpr (kC != 5)
-        return post ? residual_norm_fwd_kernel<T, kC, kSub, true> : residual_norm_fwd_kernel<T, kC, kSub, false>;
-    return nullptr;
+    if (bwd)
+        return post ? residual_norm_bwd_kernel<T, kC, kSub, true> : residual_norm_bwd_kernel<T, kC, kSub, false>;
+    return post ? residual_norm_fwd_kernel<T, kC, kSub, true> : residual_norm_fwd_kernel<T, kC, kSub, false>;
 }
 
 template <typename T>
@@ -775,9 +794,6 @@ cudaError_t launch_typed(const ResidualNormParams &p, const Plan &q, bool bwd, c
     case 3: k = kernel_for<T, 3, false>(post, bwd); break;
     case 4: k = kernel_for<T, 4, false>(post, bwd); break;
     case 5: k = kernel_for<T, 5, false>(post, bwd); break;
-    case 6: k = kernel_for<T, 6, false>(post, bwd); break;
-    case 8: k = kernel_for<T, 8, false>(post, bwd); break;
-    case 10: k = kernel_for<T, 10, false>(post, bwd); break;
     }
     if (k == nullptr)
         return cudaErrorInvalidValue;
