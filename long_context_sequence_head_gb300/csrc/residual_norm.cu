@@ -36,6 +36,33 @@ constexpr int kMaxSlots = 32;
 constexpr int kMaxRows = 32;    // of a slot
 constexpr int kJoinLanes = 16;  // blocks a column's sum is spread over
 
+// Shared memory by 32-bit addresses: pointers to it would take 64 bits of the
+// registers that the columns' sums need.
+__device__ __forceinline__ uint4 ld_shared(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t at)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared(uint32_t at, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ uint64_t *barrier_at(uint32_t at)
+{
+    return static_cast<uint64_t *>(__cvta_shared_to_generic(at));
+}
+
 // Elements of a 16-byte chunk as fp32 pairs.
 template <typename T>
 struct Chunk {
@@ -65,19 +92,18 @@ struct Chunk {
                               __float_as_uint(v[1].y));
     }
     // fp32 values in shared memory
-    __device__ __forceinline__ void read(const float *p)
+    __device__ __forceinline__ void read(uint32_t at)
     {
 #pragma unroll
         for (int i = 0; i < kP; i += 2) {
-            const float4 f = *reinterpret_cast<const float4 *>(p + 2 * i);
-            v[i] = make_float2(f.x, f.y);
-            v[i + 1] = make_float2(f.z, f.w);
+            const uint4 f = ld_shared(at + 8 * i);
+            v[i] = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
+            v[i + 1] = make_float2(__uint_as_float(f.z), __uint_as_float(f.w));
         }
     }
 };
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-__device__ __forceinline__ uint4 ld_chunk(const uint8_t *p) { return *reinterpret_cast<const uint4 *>(p); }
 
 // The rows of a block in slots of at most p.slot_rows rows.  Where all rows share
 // one gate, the blocks' slots alternate, so that all of them work on neighbouring
@@ -122,35 +148,41 @@ struct Slots {
     }
 };
 
-// Shared memory: barriers, the groups' sums, the slots' statistics, w1 as given,
-// f = residual_scale * gate * post_weight in fp32, the ring.
+// Shared memory (addresses): barriers, the groups' sums, the slots' statistics, w1
+// as given, f = residual_scale * gate * post_weight in fp32, the ring.
 struct Smem {
-    uint64_t *full, *empty;
-    volatile int *abort;
-    float4 *sums;   // [groups][2][warps]
-    float *stats;   // backward: [slots][2][kMaxRows]
-    uint8_t *w1;
-    float *f;
-    float *scratch; // backward: [parts][D], the sums on their way out of a block
-    uint8_t *ring;
+    uint32_t full, empty;  // [kMaxSlots] each
+    uint32_t abort;
+    uint32_t sums;         // [groups][2][warps] of 16 bytes
+    uint32_t stats;        // backward: [slots][2][kMaxRows]
+    uint32_t w1;
+    uint32_t f;
+    uint32_t scratch;      // backward: [parts][D], the sums on their way out of a block
+    uint32_t ring;
 
     static constexpr int kHead = 16 * kMaxSlots + 128;
     static __host__ __device__ size_t fixed(int D, int row_bytes, int parts, int stat_slots)
     {
-        return kHead + static_cast<size_t>(2) * kMaxWarps * sizeof(float4) +
-               static_cast<size_t>(stat_slots) * 2 * kMaxRows * sizeof(float) + row_bytes + static_cast<size_t>(1 + parts) * D * 4;
+        return kHead + static_cast<size_t>(2) * kMaxWarps * 16 +
+               static_cast<size_t>(stat_slots) * 2 * kMaxRows * sizeof(float) + row_bytes +
+               static_cast<size_t>(1 + parts) * D * 4;
     }
-    __device__ __forceinline__ Smem(uint8_t *base, const ResidualNormParams &p, int row_bytes)
+    __device__ __forceinline__ Smem(const void *base, const ResidualNormParams &p, int row_bytes)
     {
-        full = reinterpret_cast<uint64_t *>(base);
-        empty = full + kMaxSlots;
-        abort = reinterpret_cast<volatile int *>(empty + kMaxSlots);
-        sums = reinterpret_cast<float4 *>(base + kHead);
-        stats = reinterpret_cast<float *>(sums + 2 * kMaxWarps);
-        w1 = reinterpret_cast<uint8_t *>(stats + (p.rstd ? p.slots * 2 * kMaxRows : 0));
-        f = reinterpret_cast<float *>(w1 + row_bytes);
-        scratch = f + p.D;
-        ring = reinterpret_cast<uint8_t *>(scratch + static_cast<size_t>(p.parts) * p.D);
+        full = smem_u32(base);
+        empty = full + 8 * kMaxSlots;
+        abort = empty + 8 * kMaxSlots;
+        sums = full + kHead;
+        stats = sums + 2 * kMaxWarps * 16;
+        w1 = stats + (p.rstd ? p.slots * 2 * kMaxRows * 4 : 0);
+        f = w1 + row_bytes;
+        scratch = f + p.D * 4;
+        ring = scratch + p.parts * p.D * 4;
+    }
+    __device__ __forceinline__ bool aborted() const { return ld_shared_f32(abort) != 0.f; }
+    __device__ __forceinline__ void set_aborted(bool on) const
+    {
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(abort), "f"(on ? 1.f : 0.f) : "memory");
     }
 };
 
@@ -169,14 +201,14 @@ __device__ __forceinline__ void copy_rows(const ResidualNormParams &p, const Sme
     int k = 0, group = 0, at = 0;
     uint32_t phase = 0;
     bool met = false;
-    for (; st.more() && !*sm.abort; ++k) {
+    for (; st.more() && !sm.aborted(); ++k) {
         if (k == p.groups && !met) {  // no more until the weights are there
             __syncthreads();
             met = true;
         }
         const int slot = group * own + at, n = st.count(p);
-        if (!mbar_wait_warp(&sm.empty[slot], phase ^ 1, p.w, 0xa1)) {
-            *sm.abort = 1;
+        if (!mbar_wait_warp(barrier_at(sm.empty + 8 * slot), phase ^ 1, p.w, 0xa1)) {
+            sm.set_aborted(true);
             break;
         }
         if (++group == p.groups) {
@@ -189,38 +221,38 @@ __device__ __forceinline__ void copy_rows(const ResidualNormParams &p, const Sme
         const bool ok = ULY_IN_BOUNDS(p.w.status, st.row, n, p.T, 0x51);
         if (kStats) {
             if (ok && lane < n) {
-                const uint32_t at = smem_u32(sm.stats + slot * 2 * kMaxRows + lane);
+                const uint32_t at = sm.stats + (slot * 2 * kMaxRows + lane) * 4;
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(p.rstd + st.row + lane)
                              : "memory");
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + kMaxRows * 4),
                              "l"(p.rstd + p.T + st.row + lane)
                              : "memory");
             }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&sm.full[slot])) : "memory");
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(sm.full + 8 * slot) : "memory");
         }
         if (lane == 0) {
-            uint8_t *dst = sm.ring + static_cast<size_t>(slot) * kIn * p.slot_rows * row_bytes;
+            const uint32_t dst = sm.ring + slot * kIn * p.slot_rows * row_bytes;
             const uint32_t bytes = static_cast<uint32_t>(n) * row_bytes;
             int tensors = 0;
 #pragma unroll
             for (int t = 0; t < kIn; ++t)
                 tensors += in[t] != nullptr;
-            mbar_expect_tx(&sm.full[slot], ok ? tensors * bytes : 0);
+            mbar_expect_tx(barrier_at(sm.full + 8 * slot), ok ? tensors * bytes : 0);
 #pragma unroll
             for (int t = 0; t < kIn; ++t)
                 if (ok && in[t] != nullptr)
-                    bulk_g2s(dst + static_cast<size_t>(t) * p.slot_rows * row_bytes, in[t] + static_cast<int64_t>(st.row) * row_bytes, bytes,
-                             &sm.full[slot]);
+                    bulk_g2s(__cvta_shared_to_generic(dst + t * p.slot_rows * row_bytes),
+                             in[t] + static_cast<int64_t>(st.row) * row_bytes, bytes, barrier_at(sm.full + 8 * slot));
         }
         __syncwarp();
         st.next(p, n);
     }
     if (!met)
         __syncthreads();
-    if (*sm.abort)  // wait (bounded) for the copies that are on their way
+    if (sm.aborted())  // wait (bounded) for the copies that are on their way
         for (int i = k > p.slots ? k - p.slots : 0; i < k; ++i) {
             const int turn = i / p.groups;
-            mbar_wait(&sm.full[i % p.groups * own + turn % own], (turn / own) & 1, p.w, 0xaf);
+            mbar_wait(barrier_at(sm.full + 8 * (i % p.groups * own + turn % own)), (turn / own) & 1, p.w, 0xaf);
         }
 }
 
@@ -228,7 +260,7 @@ __device__ __forceinline__ void copy_rows(const ResidualNormParams &p, const Sme
 // two up to 32; every thread of the row gets the same bits.
 template <int kN>
 struct RowSum {
-    float4 *slots;
+    uint32_t slots;  // shared memory, [2][warps]
     int lanes, warps, group, warp, parity = 0;
 
     __device__ __forceinline__ void operator()(float (&s)[kN])
@@ -239,15 +271,24 @@ struct RowSum {
                 s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
         if (warps == 1)
             return;
-        float4 *at = slots + parity * warps;
+        const uint32_t at = slots + parity * warps * 16;
         parity ^= 1;
         if (lane_id() == 0)
-            at[warp] = make_float4(s[0], kN > 1 ? s[kN > 1 ? 1 : 0] : 0.f, kN > 2 ? s[kN > 2 ? 2 : 0] : 0.f, 0.f);
+            st_shared(at + warp * 16, make_uint4(__float_as_uint(s[0]), __float_as_uint(s[kN > 1 ? 1 : 0]),
+                                                 __float_as_uint(s[kN > 2 ? 2 : 0]), 0u));
         named_bar_sync(1 + group, warps * 32);
-        float4 total = at[0];
-        for (int i = 1; i < warps; ++i) {
-            const float4 o = at[i];
-            total.x += o.x, total.y += o.y, total.z += o.z;
+        float4 total = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < warps; i += 5) {  // five loads on their way at once
+            uint4 o[5];
+#pragma unroll
+            for (int j = 0; j < 5; ++j)
+                o[j] = i + j < warps ? ld_shared(at + (i + j) * 16) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < 5; ++j) {
+                total.x += __uint_as_float(o[j].x);
+                total.y += __uint_as_float(o[j].y);
+                total.z += __uint_as_float(o[j].z);
+            }
         }
         s[0] = total.x;
         if constexpr (kN > 1)
@@ -274,7 +315,7 @@ struct Worker {
         sub = lane_id() / p.lanes;
         col = p.lanes < 32 ? lane_id() % p.lanes : warp * 32 + lane_id();
         width = p.lanes < 32 ? p.lanes : p.warps * 32;
-        sum.slots = sm.sums + group * 2 * p.warps;
+        sum.slots = sm.sums + group * 2 * p.warps * 16;
         sum.lanes = p.lanes;
         sum.warps = p.warps;
         sum.group = group;
@@ -301,7 +342,9 @@ struct Worker {
             }
 #pragma unroll
             for (int e = 0; e < Chunk<T>::kP; ++e)
-                *reinterpret_cast<float2 *>(sm.f + i * Chunk<T>::kE + 2 * e) = f.v[e];
+                asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sm.f + (i * Chunk<T>::kE + 2 * e) * 4),
+                             "f"(f.v[e].x), "f"(f.v[e].y)
+                             : "memory");
         }
     }
     // Goes through the block's slots: body(first row, row in slot, live, slot memory,
@@ -314,9 +357,9 @@ struct Worker {
         auto rows_of = [&](int slot, uint32_t phase, uint32_t row0, int n) {
             // after a wait that ran out the loop goes on without waiting: its outputs
             // are invalid and the status says so
-            if (!*sm.abort && !mbar_wait(&sm.full[slot], phase, p.w, site))
-                *sm.abort = 1;
-            const uint8_t *at = sm.ring + static_cast<size_t>(slot) * kIn * pitch;
+            if (!sm.aborted() && !mbar_wait(barrier_at(sm.full + 8 * slot), phase, p.w, site))
+                sm.set_aborted(true);
+            const uint32_t at = sm.ring + slot * kIn * pitch;
             if constexpr (kSub) {
                 for (int r = 0; r < n; r += 32 / p.lanes) {
                     const bool live = r + sub < n;
@@ -328,7 +371,7 @@ struct Worker {
             }
             __syncwarp();
             if (lane_id() == 0)
-                mbar_arrive(&sm.empty[slot]);
+                mbar_arrive(barrier_at(sm.empty + 8 * slot));
         };
         const int own = p.slots / p.groups, first_slot = group * own;
         int at = 0, whose = 0;
@@ -378,10 +421,10 @@ __device__ __forceinline__ bool set_up(const ResidualNormParams &p, const Smem &
     if (threadIdx.x >= threads) {
         if (threadIdx.x == threads) {
             for (int i = 0; i < p.slots; ++i) {
-                mbar_init(&sm.full[i], copies_arrive);
-                mbar_init(&sm.empty[i], p.warps);
+                mbar_init(barrier_at(sm.full + 8 * i), copies_arrive);
+                mbar_init(barrier_at(sm.empty + 8 * i), p.warps);
             }
-            *sm.abort = 0;
+            sm.set_aborted(false);
             fence_mbar_init();
         }
         __syncwarp();
@@ -389,7 +432,12 @@ __device__ __forceinline__ bool set_up(const ResidualNormParams &p, const Smem &
     }
     const int nvec = p.D * static_cast<int>(sizeof(T)) / 16;
     for (int i = threadIdx.x; i < nvec; i += threads)
-        reinterpret_cast<uint4 *>(sm.w1)[i] = static_cast<const uint4 *>(p.w1)[i];
+        st_shared(sm.w1 + 16 * i, static_cast<const uint4 *>(p.w1)[i]);
+    if (kIn == 4 && p.dh == nullptr)  // the copies leave its place in the slots as it is
+        for (int i = threadIdx.x; i < p.slots * p.slot_rows * nvec; i += threads) {
+            const int slot = i / (p.slot_rows * nvec);
+            st_shared(sm.ring + 16 * (i + (3 * slot + 2) * p.slot_rows * nvec), make_uint4(0, 0, 0, 0));
+        }
     if (p.gates <= 1)
         me.load_f(0);
     __syncthreads();
@@ -397,9 +445,9 @@ __device__ __forceinline__ bool set_up(const ResidualNormParams &p, const Smem &
 }
 
 // kC: chunks a thread holds of its row; all but the last are there for every
-// thread.  kSub: short rows, several a warp (kC = 1).  kPost: a norm behind the
-// block.
-template <typename T, int kC, bool kSub, bool kPost>
+// thread.  kSub: short rows, several a warp (kC = 1).  kY, kPost: a block before
+// this norm, and a norm behind the block.
+template <typename T, int kC, bool kSub, bool kPost, bool kY>
 __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_fwd_kernel(
     const __grid_constant__ ResidualNormParams p)
 {
@@ -414,11 +462,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_fwd_kernel(
         copy_rows<kIn, false>(p, sm, in, row_bytes);
         return;
     }
-    const size_t pitch = static_cast<size_t>(p.slot_rows) * row_bytes;  // of a slot's tensors
+    const int pitch = p.slot_rows * row_bytes;  // of a slot's tensors
     const float inv_d = 1.f / static_cast<float>(p.D);
     me.template go<kSub>(
         0xa2,
-        [&](uint32_t row0, int r, bool live, const uint8_t *from, int) {
+        [&](uint32_t row0, int r, bool live, uint32_t from, int) {
             // the block's output is read from the slot as often as it is needed; only
             // the sum with the stream stays in registers
             Chunk<T> x[kC], y;
@@ -430,7 +478,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_fwd_kernel(
                 for (int c = 0; c < kC; ++c) {
                     if (!there(c))
                         continue;
-                    y.unpack(ld_chunk(from + pitch + (me.col + c * me.width) * 16));
+                    y.unpack(ld_shared(from + pitch + (me.col + c * me.width) * 16));
 #pragma unroll
                     for (int e = 0; e < kP; ++e)
                         q = ffma2(y.v[e], y.v[e], q);
@@ -445,11 +493,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_fwd_kernel(
                 if (!there(c))
                     continue;
                 const int at = me.col + c * me.width;
-                x[c].unpack(ld_chunk(from + at * 16));
-                if (p.y) {
+                x[c].unpack(ld_shared(from + at * 16));
+                if constexpr (kY) {
                     Chunk<T> f;
-                    f.read(sm.f + at * kE);
-                    y.unpack(ld_chunk(from + pitch + at * 16));
+                    f.read(sm.f + at * kE * 4);
+                    y.unpack(ld_shared(from + pitch + at * 16));
 #pragma unroll
                     for (int e = 0; e < kP; ++e) {
                         const float2 yh = kPost ? fmul2(y.v[e], both(r2)) : y.v[e];
@@ -475,10 +523,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_fwd_kernel(
                 const int at = me.col + c * me.width;
                 if (!there(c))
                     continue;
-                if (p.h)
+                if (kY && p.h)
                     __stcs(reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.h) + out + at * 16), x[c].pack());
                 Chunk<T> w;
-                w.unpack(ld_chunk(sm.w1 + at * 16));
+                w.unpack(ld_shared(sm.w1 + at * 16));
 #pragma unroll
                 for (int e = 0; e < kP; ++e)
                     x[c].v[e] = fmul2(fmul2(x[c].v[e], both(r1)), w.v[e]);
@@ -488,9 +536,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_fwd_kernel(
         [](uint32_t) {});
 }
 
-// Up to two chunks a thread what both passes over a row need stays in registers;
-// with more it is formed again.
-template <typename T, int kC, bool kSub, bool kPost>
+// Up to two chunks a thread what both passes over a row need stays in registers
+// (but yh: 16 registers more would spill); with more it is formed again.
+template <typename T, int kC, bool kSub, bool kPost, bool kY>
 __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_bwd_kernel(
     const __grid_constant__ ResidualNormParams p)
 {
@@ -506,10 +554,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_bwd_kernel(
         copy_rows<kIn, true>(p, sm, in, row_bytes);
         return;
     }
-    const bool has_dh = p.dh != nullptr, has_y = p.y != nullptr;
-    const size_t pitch = static_cast<size_t>(p.slot_rows) * row_bytes;  // of a slot's tensors
+    const uint32_t w_at = sm.w1 + me.col * 16, f_at = sm.f + me.col * kE * 4;
+    const int pitch = p.slot_rows * row_bytes;  // of a slot's tensors
     const float inv_d = 1.f / static_cast<float>(p.D);
-    const uint4 zero = make_uint4(0, 0, 0, 0);
     float2 a1[kC][kP], aA[kC][kP];
 #pragma unroll
     for (int c = 0; c < kC; ++c)
@@ -534,7 +581,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_bwd_kernel(
             }
             return;
         }
-        float *mine = sm.scratch + static_cast<size_t>(me.group * (32 / p.lanes) + me.sub) * p.D;
+        const uint32_t mine = sm.scratch + (me.group * (32 / p.lanes) + me.sub) * p.D * 4;
         named_bar_sync(15, threads);
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
@@ -542,65 +589,72 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_bwd_kernel(
 #pragma unroll
             for (int e = 0; e < kP; ++e) {
                 if (at < nvec)
-                    *reinterpret_cast<float2 *>(mine + at * kE + 2 * e) = a[c][e];
+                    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(mine + (at * kE + 2 * e) * 4),
+                                 "f"(a[c][e].x), "f"(a[c][e].y)
+                                 : "memory");
                 a[c][e] = make_float2(0.f, 0.f);
             }
         }
         named_bar_sync(15, threads);
         for (int i = threadIdx.x; i < p.D; i += threads) {
-            float t = sm.scratch[i];
+            float t = ld_shared_f32(sm.scratch + i * 4);
             for (int j = 1; j < p.parts; ++j)
-                t += sm.scratch[static_cast<size_t>(j) * p.D + i];
+                t += ld_shared_f32(sm.scratch + (j * p.D + i) * 4);
             if (ULY_IN_BOUNDS(p.w.status, row * p.D + i, 1, extent, site))
                 base[row * p.D + i] = t;
         }
     };
     me.template go<kSub>(
         0xa3,
-        [&](uint32_t row0, int r, bool live, const uint8_t *from, int slot) {
-            const float *stats = sm.stats + slot * 2 * kMaxRows + r;
-            const float m1 = live ? stats[0] : 0.f, m2 = live && kPost ? stats[kMaxRows] : 0.f;
+        [&](uint32_t row0, int r, bool live, uint32_t from, int slot) {
+            const uint32_t stats = sm.stats + (slot * 2 * kMaxRows + r) * 4;
+            const float m1 = live ? ld_shared_f32(stats) : 0.f, m2 = live && kPost ? ld_shared_f32(stats + kMaxRows * 4) : 0.f;
             constexpr bool kHold = kC <= 2;
             auto there = [&](int c) { return (!kSub || live) && (c < kC - 1 || me.col + c * me.width < nvec); };
+            const uint32_t x_at = from + me.col * 16, dz_at = x_at + pitch, dh_at = dz_at + pitch, y_at = dh_at + pitch;
+            auto read_y = [&](int c, Chunk<T> &yh) {
+                yh.unpack(ld_shared(y_at + c * me.width * 16));
+                if (kPost)
+#pragma unroll
+                    for (int e = 0; e < kP; ++e)
+                        yh.v[e] = fmul2(yh.v[e], both(m2));
+            };
             // hh, yh, b = dh + r1 w1 dz and f of one chunk
             auto form = [&](int c, Chunk<T> &hh, Chunk<T> &yh, Chunk<T> &b, Chunk<T> &f, Chunk<T> &dz, Chunk<T> &gz) {
-                const int at = me.col + c * me.width;
-                hh.unpack(ld_chunk(from + at * 16));
-                dz.unpack(ld_chunk(from + pitch + at * 16));
-                gz.unpack(ld_chunk(sm.w1 + at * 16));
-                f.read(sm.f + at * kE);
-                if (has_dh)
-                    b.unpack(ld_chunk(from + 2 * pitch + at * 16));
-                else
-                    b.unpack(zero);
-                if (has_y)
-                    yh.unpack(ld_chunk(from + 3 * pitch + at * 16));
-                else
-                    yh.unpack(zero);
+                const int at = c * me.width * 16;
+                hh.unpack(ld_shared(x_at + at));
+                if constexpr (kY) {
+                    f.read(f_at + c * me.width * kE * 4);
+                    read_y(c, yh);
+#pragma unroll
+                    for (int e = 0; e < kP; ++e)
+                        hh.v[e] = ffma2(f.v[e], yh.v[e], hh.v[e]);
+                }
+                dz.unpack(ld_shared(dz_at + at));
+                gz.unpack(ld_shared(w_at + at));
+                b.unpack(ld_shared(dh_at + at));
 #pragma unroll
                 for (int e = 0; e < kP; ++e) {
-                    if (kPost)
-                        yh.v[e] = fmul2(yh.v[e], both(m2));
-                    hh.v[e] = fmul2(ffma2(f.v[e], yh.v[e], hh.v[e]), both(m1));
+                    hh.v[e] = fmul2(hh.v[e], both(m1));
                     gz.v[e] = fmul2(gz.v[e], dz.v[e]);
                     b.v[e] = ffma2(gz.v[e], both(m1), b.v[e]);
                 }
             };
             constexpr int kKept = kHold ? kC : 1;
-            Chunk<T> hh[kKept], yh[kKept], b[kKept], f, dz, gz;
+            Chunk<T> hh[kKept], b[kKept], yh, f, dz, gz;
             float2 q1 = make_float2(0.f, 0.f), q2 = q1, q3 = q1;
 #pragma unroll
             for (int c = 0; c < kC; ++c) {
                 const int i = kHold ? c : 0;
                 if (!there(c))
                     continue;
-                form(c, hh[i], yh[i], b[i], f, dz, gz);
+                form(c, hh[i], yh, b[i], f, dz, gz);
 #pragma unroll
                 for (int e = 0; e < kP; ++e) {
                     q1 = ffma2(gz.v[e], hh[i].v[e], q1);
                     a1[c][e] = ffma2(dz.v[e], hh[i].v[e], a1[c][e]);
                     if constexpr (kPost) {
-                        const float2 fy = fmul2(f.v[e], yh[i].v[e]);
+                        const float2 fy = fmul2(f.v[e], yh.v[e]);
                         q2 = ffma2(fy, b[i].v[e], q2);
                         q3 = ffma2(fy, hh[i].v[e], q3);
                     }
@@ -619,31 +673,33 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_bwd_kernel(
                 k2 = m2 * (fmaf(-k1, s[2], s[1]) * inv_d);
             if (!live || !ULY_IN_BOUNDS(p.w.status, row0 + r, 1, p.T, 0x54))
                 return;
-            const int64_t out = static_cast<int64_t>(row0 + r) * row_bytes;
+            const int64_t out = static_cast<int64_t>(row0 + r) * row_bytes + me.col * 16;
             uint8_t *dx = static_cast<uint8_t *>(p.dx) + out, *dy = static_cast<uint8_t *>(p.dy) + out;
 #pragma unroll
             for (int c = 0; c < kC; ++c) {
-                const int i = kHold ? c : 0, at = me.col + c * me.width;
+                const int i = kHold ? c : 0, at = c * me.width * 16;
                 if (!there(c))
                     continue;
-                if constexpr (kHold)
-                    f.read(sm.f + at * kE);
-                else
-                    form(c, hh[i], yh[i], b[i], f, dz, gz);
+                if constexpr (!kHold) {
+                    form(c, hh[i], yh, b[i], f, dz, gz);
+                } else if constexpr (kY) {
+                    f.read(f_at + c * me.width * kE * 4);
+                    read_y(c, yh);
+                }
                 Chunk<T> t;
 #pragma unroll
                 for (int e = 0; e < kP; ++e)
                     t.v[e] = ffma2(hh[i].v[e], both(-k1), b[i].v[e]);
-                __stcs(reinterpret_cast<uint4 *>(dx + at * 16), t.pack());
-                if (has_y) {
+                __stcs(reinterpret_cast<uint4 *>(dx + at), t.pack());
+                if constexpr (kY) {
 #pragma unroll
                     for (int e = 0; e < kP; ++e) {
-                        aA[c][e] = ffma2(t.v[e], yh[i].v[e], aA[c][e]);
+                        aA[c][e] = ffma2(t.v[e], yh.v[e], aA[c][e]);
                         t.v[e] = fmul2(t.v[e], f.v[e]);
                         if constexpr (kPost)
-                            t.v[e] = ffma2(yh[i].v[e], both(-k2), fmul2(t.v[e], both(m2)));
+                            t.v[e] = ffma2(yh.v[e], both(-k2), fmul2(t.v[e], both(m2)));
                     }
-                    __stcs(reinterpret_cast<uint4 *>(dy + at * 16), t.pack());
+                    __stcs(reinterpret_cast<uint4 *>(dy + at), t.pack());
                 }
             }
         },
@@ -776,24 +832,28 @@ Plan plan_for(int64_t T, int64_t run, int D, int esize, bool bwd)
 }
 
 template <typename T, int kC, bool kSub>
-auto kernel_for(bool post, bool bwd) -> void (*)(const ResidualNormParams)
+auto kernel_for(bool post, bool y, bool bwd) -> void (*)(const ResidualNormParams)
 {
     if (bwd)
-        return post ? residual_norm_bwd_kernel<T, kC, kSub, true> : residual_norm_bwd_kernel<T, kC, kSub, false>;
-    return post ? residual_norm_fwd_kernel<T, kC, kSub, true> : residual_norm_fwd_kernel<T, kC, kSub, false>;
+        return post ? residual_norm_bwd_kernel<T, kC, kSub, true, true>
+               : y  ? residual_norm_bwd_kernel<T, kC, kSub, false, true>
+                    : residual_norm_bwd_kernel<T, kC, kSub, false, false>;
+    return post ? residual_norm_fwd_kernel<T, kC, kSub, true, true>
+           : y  ? residual_norm_fwd_kernel<T, kC, kSub, false, true>
+                : residual_norm_fwd_kernel<T, kC, kSub, false, false>;
 }
 
 template <typename T>
 cudaError_t launch_typed(const ResidualNormParams &p, const Plan &q, bool bwd, cudaStream_t s)
 {
-    const bool post = p.w2 != nullptr;
+    const bool post = p.w2 != nullptr, y = p.y != nullptr;
     void (*k)(const ResidualNormParams) = nullptr;
     switch (q.chunks) {
-    case 1: k = q.lanes < 32 ? kernel_for<T, 1, true>(post, bwd) : kernel_for<T, 1, false>(post, bwd); break;
-    case 2: k = kernel_for<T, 2, false>(post, bwd); break;
-    case 3: k = kernel_for<T, 3, false>(post, bwd); break;
-    case 4: k = kernel_for<T, 4, false>(post, bwd); break;
-    case 5: k = kernel_for<T, 5, false>(post, bwd); break;
+    case 1: k = q.lanes < 32 ? kernel_for<T, 1, true>(post, y, bwd) : kernel_for<T, 1, false>(post, y, bwd); break;
+    case 2: k = kernel_for<T, 2, false>(post, y, bwd); break;
+    case 3: k = kernel_for<T, 3, false>(post, y, bwd); break;
+    case 4: k = kernel_for<T, 4, false>(post, y, bwd); break;
+    case 5: k = kernel_for<T, 5, false>(post, y, bwd); break;
     }
     if (k == nullptr)
         return cudaErrorInvalidValue;
