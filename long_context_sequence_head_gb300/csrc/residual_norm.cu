@@ -116,8 +116,8 @@ struct Slots {
     __device__ __forceinline__ explicit Slots(const ResidualNormParams &p)
     {
         if (p.gates > 1) {
-            row = static_cast<uint32_t>(p.T * blockIdx.x / gridDim.x);
-            end = static_cast<uint32_t>(p.T * (blockIdx.x + 1) / gridDim.x);
+            row = blockIdx.x * p.block_rows;
+            end = min(row + p.block_rows, static_cast<uint32_t>(p.T));
             run = row / static_cast<uint32_t>(p.run);
             run_end = (run + 1) * static_cast<uint32_t>(p.run);
         } else {
@@ -321,21 +321,32 @@ struct Worker {
         sum.group = group;
         sum.warp = warp;
     }
-    // f for the rows of a run
+    // f for the rows of a run, and w1 with it at the start
+    template <bool kStart>
     __device__ __forceinline__ void load_f(uint32_t run) const
     {
         const T *gate = static_cast<const T *>(p.gate), *w2 = static_cast<const T *>(p.w2);
         if (gate && p.gates > 1)
             gate += static_cast<int64_t>(run % p.gates) * p.D;
         for (int i = threadIdx.x; i < nvec; i += threads) {
+            uint4 raw[3];  // on their way together
+            if (kStart)
+                raw[0] = static_cast<const uint4 *>(p.w1)[i];
+            if (gate)
+                raw[1] = reinterpret_cast<const uint4 *>(gate)[i];
+            if (w2)
+                raw[2] = reinterpret_cast<const uint4 *>(w2)[i];
+            if (kStart)
+                st_shared(sm.w1 + 16 * i, raw[0]);
             Chunk<T> f, w;
 #pragma unroll
             for (int e = 0; e < Chunk<T>::kP; ++e)
                 f.v[e] = both(p.scale);
-            for (const T *from : {gate, w2}) {
-                if (from == nullptr)
+#pragma unroll
+            for (int k = 1; k < 3; ++k) {
+                if (k == 1 ? gate == nullptr : w2 == nullptr)
                     continue;
-                w.unpack(reinterpret_cast<const uint4 *>(from)[i]);
+                w.unpack(raw[k]);
 #pragma unroll
                 for (int e = 0; e < Chunk<T>::kP; ++e)
                     f.v[e] = fmul2(f.v[e], w.v[e]);
@@ -376,8 +387,8 @@ struct Worker {
         const int own = p.slots / p.groups, first_slot = group * own;
         int at = 0, whose = 0;
         uint32_t phase = 0;
-        bool turn = p.gates > 1;
-        if (!turn)
+        bool turn = false;  // set_up loaded the first f
+        if (p.gates <= 1)
             st.next(p, 0, group);
         // with a gate for every sequence all threads go through all slots, to
         // change it together; without, a group's slots are evenly spaced
@@ -386,7 +397,7 @@ struct Worker {
             const int n = st.count(p);
             if (turn) {
                 named_bar_sync(15, threads);
-                load_f(run);
+                load_f<false>(run);
                 named_bar_sync(15, threads);
             }
             bool ours = true;
@@ -431,15 +442,12 @@ __device__ __forceinline__ bool set_up(const ResidualNormParams &p, const Smem &
         return true;
     }
     const int nvec = p.D * static_cast<int>(sizeof(T)) / 16;
-    for (int i = threadIdx.x; i < nvec; i += threads)
-        st_shared(sm.w1 + 16 * i, static_cast<const uint4 *>(p.w1)[i]);
     if (kIn == 4 && p.dh == nullptr)  // the copies leave its place in the slots as it is
         for (int i = threadIdx.x; i < p.slots * p.slot_rows * nvec; i += threads) {
             const int slot = i / (p.slot_rows * nvec);
             st_shared(sm.ring + 16 * (i + (3 * slot + 2) * p.slot_rows * nvec), make_uint4(0, 0, 0, 0));
         }
-    if (p.gates <= 1)
-        me.load_f(0);
+    me.template load_f<true>(Slots(p).run);
     __syncthreads();
     return false;
 }
@@ -707,27 +715,29 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_bwd_kernel(
             if (p.partA)
                 flush(p.partA, blockIdx.x + run, p.partA_elems, aA, 0x55);
         });
+    grid_next();
     if (p.part1)
         flush(p.part1, blockIdx.x, p.part1_elems, a1, 0x56);
 }
 
 // The weights' gradients from the blocks' sums, in an order that depends on the
-// sizes alone: a block takes 32 columns, kJoinLanes threads a column.
+// sizes alone: a block takes 32 columns of dweight (y = 0) or of the gates and
+// dpost_weight (y = 1), kJoinLanes threads a column.
 template <typename T>
 __global__ void __launch_bounds__(32 * kJoinLanes) residual_norm_join_kernel(const __grid_constant__ ResidualNormParams p,
                                                                              int blocks)
 {
     __shared__ float part[kJoinLanes][33];
+    grid_wait();
     const int lane = threadIdx.x & 31, j = threadIdx.x >> 5;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     const bool in = col < p.D;
-    // the sum of rows [first, last) of a buffer of D columns, for the threads with j = 0
-    auto column = [&](const float *base, int64_t first, int64_t last, int64_t extent) {
-        (void)extent;
+    // rows first, first + step, .. below last of a buffer of D columns
+    auto column = [&](const float *base, int64_t first, int64_t last, int step, [[maybe_unused]] int64_t extent) {
         float s = 0.f;
         if (in)
 #pragma unroll 4
-            for (int64_t r = first + j; r < last; r += kJoinLanes)
+            for (int64_t r = first; r < last; r += step)
                 if (ULY_IN_BOUNDS(p.w.status, r * p.D + col, 1, extent, 0x57))
                     s += base[r * p.D + col];
         return s;
@@ -756,25 +766,40 @@ __global__ void __launch_bounds__(32 * kJoinLanes) residual_norm_join_kernel(con
                 static_cast<float *>(w)[at] = v;
         }
     };
-    if (p.dw1)
-        write(p.dw1, col, across(column(p.part1, 0, blocks, p.part1_elems)));
+    if (blockIdx.y == 0) {
+        if (p.dw1)
+            write(p.dw1, col, across(column(p.part1, j, blocks, kJoinLanes, p.part1_elems)));
+        return;
+    }
     if (!p.dw2 && !p.dgate)
         return;
-    auto block_of = [&](int64_t row) { return ((row + 1) * blocks - 1) / p.T; };
-    const int64_t runs = (p.T + p.run - 1) / p.run;
-    const int gates = p.gates > 1 ? p.gates : 1;
-    float dw2 = 0.f;
-    for (int b = 0; b < gates; ++b) {
-        float s = 0.f;
-        for (int64_t run = b; run < runs; run += gates) {
-            const int64_t lo = block_of(run * p.run), hi = block_of((run + 1) * p.run - 1);
-            s += column(p.partA, lo + run, hi + run + 1, p.partA_elems);
-        }
-        const float A = p.scale * across(s);
+    if (p.gates <= 1) {  // one run, every block has a row of it
+        const float A = p.scale * across(column(p.partA, j, blocks, kJoinLanes, p.partA_elems));
         if (p.dgate && in)
-            write(p.dgate, b * static_cast<int64_t>(p.D) + col, p.w2 ? A * value(p.w2, col) : A);
-        if (in)
-            dw2 = p.gate ? fmaf(value(p.gate, b * static_cast<int64_t>(p.D) + col), A, dw2) : dw2 + A;
+            write(p.dgate, col, p.w2 ? A * value(p.w2, col) : A);
+        if (p.dw2 && in)
+            write(p.dw2, col, p.gate ? A * value(p.gate, col) : A);
+        return;
+    }
+    // a gate's runs, several at once where there are fewer than threads a column
+    const int runs_of = static_cast<int>(p.T / p.run / p.gates);  // runs of a gate
+    const int at_once = runs_of < kJoinLanes ? runs_of : kJoinLanes, share = kJoinLanes / at_once;
+    float dw2 = 0.f;
+    for (int b = 0; b < p.gates; ++b) {
+        float s = 0.f;
+        if (j < at_once * share)
+            for (int i = j / share; i < runs_of; i += at_once) {
+                const uint32_t run = b + static_cast<uint32_t>(i) * p.gates, first = run * static_cast<uint32_t>(p.run);
+                const uint32_t lo = first / p.block_rows, hi = (first + static_cast<uint32_t>(p.run) - 1) / p.block_rows;
+                s += column(p.partA, static_cast<int64_t>(lo) + run + j % share, static_cast<int64_t>(hi) + run + 1, share,
+                            p.partA_elems);
+            }
+        const float A = p.scale * across(s);
+        const int64_t at = b * static_cast<int64_t>(p.D) + col;
+        if (p.dgate && in)
+            write(p.dgate, at, p.w2 ? A * value(p.w2, col) : A);
+        if (p.dw2 && in)
+            dw2 = fmaf(value(p.gate, at), A, dw2);
     }
     if (p.dw2)
         write(p.dw2, col, dw2);
@@ -782,7 +807,7 @@ __global__ void __launch_bounds__(32 * kJoinLanes) residual_norm_join_kernel(con
 
 // How rows are laid over a block's threads.
 struct Plan {
-    int chunks, warps, lanes, groups, parts, slot_rows, slots, blocks, threads;
+    int chunks, warps, lanes, groups, parts, slot_rows, slots, blocks, block_rows, threads;
     size_t smem;
 };
 
@@ -828,6 +853,9 @@ Plan plan_for(int64_t T, int64_t run, int D, int esize, bool bwd)
     q.smem = bytes(own);
     const int64_t units = (T + q.slot_rows - 1) / q.slot_rows;
     q.blocks = static_cast<int>(std::min<int64_t>(units, num_sms()));
+    q.block_rows = static_cast<int>((T + q.blocks - 1) / q.blocks);
+    if (run < T)  // runs of rows: none of the blocks is empty
+        q.blocks = static_cast<int>((T + q.block_rows - 1) / q.block_rows);
     return q;
 }
 
@@ -864,8 +892,16 @@ cudaError_t launch_typed(const ResidualNormParams &p, const Plan &q, bool bwd, c
     e = cudaGetLastError();
     if (e != cudaSuccess || !bwd || !(p.part1 || p.partA))
         return e;
-    residual_norm_join_kernel<T><<<static_cast<unsigned>((p.D + 31) / 32), 32 * kJoinLanes, 0, s>>>(p, q.blocks);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((p.D + 31) / 32), 2);
+    cfg.blockDim = dim3(32 * kJoinLanes);
+    cfg.stream = s;
+    cudaLaunchAttribute early[1];  // its blocks may be set up while the kernel above ends
+    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, residual_norm_join_kernel<T>, p, q.blocks);
 }
 
 constexpr size_t kAlign = 256;
@@ -905,6 +941,7 @@ cudaError_t launch_residual_norm(ResidualNormParams &p, bool bwd, int esize, voi
     p.parts = bwd ? q.parts : 0;
     p.slot_rows = q.slot_rows;
     p.slots = q.slots;
+    p.block_rows = q.block_rows;
     p.w = wait_cfg();
     if (bwd && workspace) {
         size_t one, gates;

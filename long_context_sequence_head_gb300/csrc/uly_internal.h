@@ -348,6 +348,7 @@ struct ResidualNormParams {
     // set by the launch: warps of a group and the lanes a row has in a warp, groups of
     // a block, rows it works on at once (backward; 0 for one), rows of a slot, slots of the ring
     int warps, lanes, groups, parts, slot_rows, slots;
+    int block_rows;        // rows of a block, with a gate for every sequence
     float *part1, *partA;  // the blocks' sums: [blocks][D], [blocks + runs][D]
     int64_t part1_elems, partA_elems;
     WaitCfg w;
