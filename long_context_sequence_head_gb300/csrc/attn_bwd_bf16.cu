@@ -72,6 +72,8 @@ struct BwdParams {
     float scale;
     const float *lse2;  // [SB][Hq][Npad]
     const float *Dv;    // [SB][Hq][Npad]
+    const uint16_t *dout;  // kDecode 3: rows that see only themselves
+    int64_t q_elems;
     float *dq_acc;      // [SB][Hq][Npad/128][32][128][4]
     uint16_t *dk, *dv;  // rows like k, v
     int64_t kv_elems;   // extent of dk, dv (bounds checks of debug builds)
@@ -79,7 +81,8 @@ struct BwdParams {
     RowLayout L;
 };
 
-__device__ __forceinline__ void doc_range(const BwdParams &p, int64_t i, int64_t &lo, int64_t &hi)
+template <typename Params>
+__device__ __forceinline__ void doc_range(const Params &p, int64_t i, int64_t &lo, int64_t &hi)
 {
     lo = 0;
     hi = p.N;
@@ -169,6 +172,108 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const uint16_t *__restrict
                 Dv[row] = acc;
                 lse2[row] = lse[(sb * Hq + h) * N + i] * 1.4426950408889634f;
             }
+        }
+    }
+}
+
+// Behind it with a sliding window, for the rows that see few keys.  D_i = <dO_i,
+// O_i> is off by O's rounding, which is little against dP - D, but dS = P (dP - D)
+// of a row's largest key is the small rest of a cancellation where the row sees few
+// keys: dQ and dK of rows of two or three came out 0.006 to 0.011 of their norm off
+// (0.003 with this).  Up to kFewKeys keys D is therefore formed as sum_j P_ij dP_ij
+// from the keys themselves.  A row that sees only itself has dS = 0 exactly: it
+// takes no part in the main kernel (lse = inf), and its key's dV gets dO in the
+// epilogue.  One warp per row, as above.
+constexpr int kFewKeys = 8;
+
+struct FewRows {
+    const uint16_t *q, *k, *v, *dout;
+    const float *lse;
+    float *lse2, *Dv;
+    int64_t SB, N, Npad, rows;  // rows of a (shard, batch): all N, or the first kFewKeys of each document
+    int Hq, Hkv, window, sinks, num_docs;
+    const int32_t *cu;
+    float scale_log2;
+    RowLayout L;
+    int64_t q_elems, kv_elems;
+    unsigned *status;
+};
+
+__device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b)
+{
+    float s = bf16lo(a.x) * bf16lo(b.x);
+    s = fmaf(bf16hi(a.x), bf16hi(b.x), s);
+    s = fmaf(bf16lo(a.y), bf16lo(b.y), s);
+    s = fmaf(bf16hi(a.y), bf16hi(b.y), s);
+    s = fmaf(bf16lo(a.z), bf16lo(b.z), s);
+    s = fmaf(bf16hi(a.z), bf16hi(b.z), s);
+    s = fmaf(bf16lo(a.w), bf16lo(b.w), s);
+    return fmaf(bf16hi(a.w), bf16hi(b.w), s);
+}
+
+// over the 16 lanes that hold a head's row
+__device__ __forceinline__ float half_warp_sum(float x)
+{
+#pragma unroll
+    for (int sft = 8; sft > 0; sft >>= 1)
+        x += __shfl_xor_sync(0xffffffffu, x, sft);
+    return x;
+}
+
+__global__ void __launch_bounds__(256) window_few_kernel(const __grid_constant__ FewRows p)
+{
+    const int64_t gw = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    const int lane = lane_id();
+    if (gw >= p.SB * p.rows)
+        return;
+    const int64_t sb = gw / p.rows;
+    int64_t i = gw % p.rows, start, end;
+    if (p.rows != p.N && p.cu != nullptr) {
+        const int64_t doc = i / kFewKeys;
+        start = p.cu[doc];
+        end = p.cu[doc + 1];
+        i = start + i % kFewKeys;
+        if (i >= end)
+            return;
+    } else {
+        doc_range(p, i, start, end);
+    }
+    const int64_t w_lo = max(start, i - p.window + 1), s_hi = min(start + p.sinks, w_lo);
+    const int before = static_cast<int>(min(s_hi - start, static_cast<int64_t>(kFewKeys)));
+    const int64_t keys = before + i - w_lo + 1;
+    if (keys > kFewKeys)
+        return;
+    const int64_t off = p.L.off(p.N, sb, i, p.Hq, 0, kD);
+    // the token's Hq rows are adjacent: one check covers every read of them below
+    if (!ULY_IN_BOUNDS(p.status, off, static_cast<int64_t>(p.Hq) * kD, p.q_elems, 0x2d))
+        return;
+    const uint4 *d4 = reinterpret_cast<const uint4 *>(p.dout + off);
+    const uint4 *q4 = reinterpret_cast<const uint4 *>(p.q + off);
+    const int n16 = p.Hq * (kD / 8), G = p.Hq / p.Hkv;
+    for (int u0 = 0; u0 < n16; u0 += 32) {
+        const int u = u0 + lane, h = min(u, n16 - 1) / (kD / 8);
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        const int64_t lrow = (sb * p.Hq + h) * p.N + i, row = (sb * p.Hq + h) * p.Npad + i;
+        const bool ok = ULY_IN_BOUNDS(p.status, lrow, 1, p.SB * p.Hq * p.N, 0x2e) &&
+                        ULY_IN_BOUNDS(p.status, row, 1, p.SB * p.Hq * p.Npad, 0x2f);
+        float acc = 0.f;
+        if (keys > 1) {
+            const float l2 = ok ? p.lse[lrow] * 1.4426950408889634f : 0.f;
+            const uint4 d = u < n16 ? d4[u] : zero, q = u < n16 ? q4[u] : zero;
+            for (int j = 0; j < static_cast<int>(keys); ++j) {
+                const int64_t key = j < before ? start + j : w_lo + j - before;
+                const int64_t at = p.L.off(p.N, sb, key, p.Hkv, h / G, kD) + lane % 16 * 8;
+                const bool in = u < n16 && ULY_IN_BOUNDS(p.status, at, 8, p.kv_elems, 0x30);
+                const uint4 kk = in ? *reinterpret_cast<const uint4 *>(p.k + at) : zero;
+                const uint4 vv = in ? *reinterpret_cast<const uint4 *>(p.v + at) : zero;
+                const float s = half_warp_sum(dot8(q, kk)), dp = half_warp_sum(dot8(d, vv));
+                acc = fmaf(exp2f(fmaf(s, p.scale_log2, -l2)), dp, acc);
+            }
+        }
+        if (u < n16 && (lane & 15) == 0 && ok) {
+            p.Dv[row] = acc;
+            if (keys == 1)
+                p.lse2[row] = INFINITY;
         }
     }
 }
@@ -483,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int64_t lo = 0, hi = 0;                    // rows that may attend to this key: [lo, hi)
         if (key < p.N) {
             doc_range(p, key, lo, hi);
-            if constexpr (kWindow)  // past the window only sinks are seen
-                if (key >= lo + p.sinks)
+            if constexpr (kWindow)
+                if (key >= lo + p.sinks)  // past the window only sinks are seen
                     hi = min(hi, key + p.window);
             if (p.causal)
                 lo = key;
@@ -645,7 +750,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool store = key < p.N && ULY_IN_BOUNDS(p.w.status, rowoff, 32, p.kv_elems, 0x29);
             // a tile whose walk is cut: the sums of its last document's sinks go to the unit's slot
             [[maybe_unused]] float *part = nullptr;
+            [[maybe_unused]] bool alone = false;  // the key's own row sees no other key
             if constexpr (kWindow) {
+                if (key < p.N) {
+                    int64_t start, end;
+                    doc_range(p, key, start, end);
+                    alone = key == start || (p.window == 1 && p.sinks == 0);
+                }
                 if (unit.w >= 0) {
                     const int64_t first = max(last_doc, kv0), end = min(last_doc + p.sinks, p.N);
                     if (key >= first && key < end) {
@@ -670,7 +781,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32p(src, x);  // warp-collective: all lanes
                 tmem_ld_wait();
                 tmem_ld_fence32p(x);
-                if constexpr (kWindow)
+                if constexpr (kWindow) {
+                    // a row that sees only itself: P = 1, dS = 0, left out above; its
+                    // tile's own unit adds it
+                    if (alone && which == 0 && !(unit.w >= 0 && (unit.w & 1))) {
+                        for (int g = 0; g < p.G; ++g) {
+                            const int64_t at = p.L.off(p.N, sb, key, p.Hq, kvh * p.G + g, kD) + c0;
+                            if (!ULY_IN_BOUNDS(p.w.status, at, 32, p.q_elems, 0x32))
+                                break;
+                            const uint32_t *row = reinterpret_cast<const uint32_t *>(p.dout + at);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) {
+                                x[2 * c] = __float_as_uint(__uint_as_float(x[2 * c]) + bf16lo(row[c]));
+                                x[2 * c + 1] = __float_as_uint(__uint_as_float(x[2 * c + 1]) + bf16hi(row[c]));
+                            }
+                        }
+                    }
                     if (part != nullptr)
 #pragma unroll
                         for (int c = 0; c < 32; c += 4)
@@ -678,6 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 n_it > 0 ? make_float4(__uint_as_float(x[c]), __uint_as_float(x[c + 1]),
                                                        __uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]))
                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
                 uint32_t o16[16];
 #pragma unroll
                 for (int c = 0; c < 16; ++c)
@@ -725,6 +852,36 @@ cudaError_t launch_attn_bwd_bf16(const AttnShape &s, const void *q, const void *
         e = cudaGetLastError();
         if (e != cudaSuccess)
             return e;
+        if (s.window) {
+            FewRows w;
+            w.q = static_cast<const uint16_t *>(q);
+            w.k = static_cast<const uint16_t *>(k);
+            w.v = static_cast<const uint16_t *>(v);
+            w.dout = static_cast<const uint16_t *>(dout);
+            w.lse = lse;
+            w.lse2 = scr.lse2;
+            w.Dv = scr.D;
+            w.SB = s.SB;
+            w.N = s.N;
+            w.Npad = Npad;
+            const int64_t docs = s.num_docs > 0 ? s.num_docs : 1;
+            w.rows = s.window + s.sinks <= kFewKeys || docs * kFewKeys >= s.N ? s.N : docs * kFewKeys;
+            w.Hq = s.Hq;
+            w.Hkv = s.Hkv;
+            w.window = s.window;
+            w.sinks = s.sinks;
+            w.num_docs = s.num_docs;
+            w.cu = s.cu_dev;
+            w.scale_log2 = s.scale * 1.4426950408889634f;
+            w.L = s.L;
+            w.q_elems = s.q_elems;
+            w.kv_elems = s.kv_elems;
+            w.status = s.status;
+            window_few_kernel<<<static_cast<unsigned>((s.SB * w.rows * 32 + 255) / 256), 256, 0, stream>>>(w);
+            e = cudaGetLastError();
+            if (e != cudaSuccess)
+                return e;
+        }
         e = cudaMemsetAsync(scr.dq_acc, 0, static_cast<size_t>(s.SB) * s.Hq * Npad * kD * sizeof(float), stream);
         if (e != cudaSuccess)
             return e;
@@ -749,6 +906,8 @@ cudaError_t launch_attn_bwd_bf16(const AttnShape &s, const void *q, const void *
     p.dk = static_cast<uint16_t *>(dk);
     p.dv = static_cast<uint16_t *>(dv);
     p.kv_elems = s.kv_elems;
+    p.dout = static_cast<const uint16_t *>(dout);
+    p.q_elems = s.q_elems;
     p.w = wait_cfg();
     p.L = s.L;
     p.window = s.window;

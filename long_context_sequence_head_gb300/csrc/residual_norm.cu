@@ -390,33 +390,50 @@ struct Worker {
         bool turn = false;  // set_up loaded the first f
         if (p.gates <= 1)
             st.next(p, 0, group);
-        // with a gate for every sequence all threads go through all slots, to
-        // change it together; without, a group's slots are evenly spaced
+        auto take = [&](uint32_t row0, int n) {
+            rows_of(first_slot + at, phase, row0, n);
+            if (++at == own) {
+                at = 0;
+                phase ^= 1;
+            }
+        };
+        // With a gate for every sequence all threads meet at the end of each run, to
+        // change it together; between, and without one, a group's slots are evenly spaced.
         while (st.more()) {
-            const uint32_t row0 = st.row, run = st.run;
-            const int n = st.count(p);
+            const uint32_t run = st.run;
             if (turn) {
                 named_bar_sync(15, threads);
                 load_f<false>(run);
                 named_bar_sync(15, threads);
+                turn = false;
             }
-            bool ours = true;
-            if (p.gates > 1) {
-                ours = whose == group;
-                whose = whose + 1 == p.groups ? 0 : whose + 1;
-                turn = st.next(p, n);
-            } else {
+            if (p.gates <= 1) {
+                const uint32_t row0 = st.row;
+                const int n = st.count(p);
                 st.next(p, n, p.groups);
+                take(row0, n);
+                continue;
             }
-            if (ours) {
-                rows_of(first_slot + at, phase, row0, n);
-                if (++at == own) {
-                    at = 0;
-                    phase ^= 1;
-                }
+            // slots left in the run, and how many of them come before this group's next
+            const uint32_t last = min(st.run_end, st.end);
+            const int left = static_cast<int>((last - st.row + p.slot_rows - 1) / p.slot_rows);
+            const int before = group >= whose ? group - whose : group - whose + p.groups;
+            if (before < left) {
+                const uint32_t row0 = st.row + before * p.slot_rows;
+                const int n = static_cast<int>(min(last - row0, static_cast<uint32_t>(p.slot_rows)));
+                take(row0, n);
+                st.row = row0 + n;
+                whose = group + 1 == p.groups ? 0 : group + 1;
+            } else {
+                st.row = last;
+                whose = (whose + left) % p.groups;
             }
-            if (p.gates > 1 && (turn || !st.more()))
+            if (st.row == last) {
                 end_of_run(run);
+                ++st.run;
+                st.run_end += static_cast<uint32_t>(p.run);
+                turn = true;
+            }
         }
         if (p.gates <= 1)
             end_of_run(0);

@@ -67,6 +67,8 @@ struct RowMask {
     {
         return j >= start && j <= row && (row - j < window || j - start < sinks);
     }
+    // it sees no key but its own: dS is 0, and not what two sums of the same terms differ by
+    __device__ __forceinline__ bool alone() const { return row == start || (window == 1 && sinks == 0); }
 };
 
 // 64 rows of a tensor of H heads from token n0 on; rows past N are zero.
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(kThreads) window_dq_f32_kernel(const __grid_co
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const float p = mask[i].sees(key0 + tx + 16 * c) ? expf(x[i][c] * s.scale - L[i]) : 0.f;
-                sP[(tx + 16 * c) * kPitchP + ty + 16 * i] = p * (y[i][c] - Di[i]);
+                sP[(tx + 16 * c) * kPitchP + ty + 16 * i] = mask[i].alone() ? 0.f : p * (y[i][c] - Di[i]);
             }
         __syncthreads();
         add_product<D>(sP, sK, tx, ty, acc);
@@ -385,13 +387,16 @@ __global__ void __launch_bounds__(kThreads) window_dkv_f32_kernel(const __grid_c
     load_tile<D>(sV, v, s, sb, k0, s.Hkv, kvh, s.kv_elems);
     // rows that see the keys tx + 16 c: [key, end)
     int64_t end[4];
+    bool alone[4];  // its own row sees no other key
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const int64_t key = k0 + tx + 16 * c;
         end[c] = 0;
+        alone[c] = false;
         if (key < s.N) {
             int64_t start;
             doc_bounds(s, key, start, end[c]);
+            alone[c] = key == start || (s.window == 1 && s.sinks == 0);
             if (key >= start + s.sinks)
                 end[c] = min(end[c], key + s.window);
         }
@@ -427,7 +432,8 @@ __global__ void __launch_bounds__(kThreads) window_dkv_f32_kernel(const __grid_c
                 const int64_t row = q0 + ty + 16 * i;
                 const float p = row >= k0 + tx + 16 * c && row < end[c] ? expf(x[i][c] * s.scale - L[i]) : 0.f;
                 sP[(ty + 16 * i) * kPitchP + tx + 16 * c] = p;
-                sS[(ty + 16 * i) * kPitchP + tx + 16 * c] = p * (y[i][c] - Di[i]);
+                sS[(ty + 16 * i) * kPitchP + tx + 16 * c] =
+                    alone[c] && row == k0 + tx + 16 * c ? 0.f : p * (y[i][c] - Di[i]);
             }
         __syncthreads();
         add_product<D>(sP, sO, tx, ty, aV);
