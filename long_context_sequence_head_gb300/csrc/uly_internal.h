@@ -353,6 +353,12 @@ struct ResidualNormParams {
     int64_t part1_elems, partA_elems;
     WaitCfg w;
 };
+// How rows are laid over a block's threads.
+struct ResidualNormPlan {
+    int chunks, warps, lanes, groups, parts, slot_rows, slots, blocks, block_rows, threads;
+    size_t smem;
+};
+cudaError_t launch_residual_norm_f32(const ResidualNormParams &p, const ResidualNormPlan &q, bool bwd, cudaStream_t s);
 size_t residual_norm_workspace(int64_t T, int64_t Np, int D);
 cudaError_t launch_residual_norm(ResidualNormParams &p, bool bwd, int esize, void *workspace, cudaStream_t s);
 

@@ -37,6 +37,7 @@ constexpr int kHeads = 8;      // query heads of a unit, bf16
 constexpr int kHeadsF32 = 4;   // fp32
 constexpr float kRaise = 8.f;  // log2 units
 constexpr int kSplitMax = 64;
+constexpr int kClusterMax = 8;  // blocks that join their sums through shared memory
 
 // A sequence's visible tokens: `sinks` first ones, then `n - sinks` of the window.
 struct List {
@@ -97,12 +98,12 @@ struct Unit {
 // ------------------------------------------------------------- results
 // A block's sums (relative to m, in log2 units) go to the output, or to its
 // split's part of the workspace: [sb][Hq][split] rows of d values, then m and l.
-template <typename T, int D>
+template <typename T, int D, bool kDone = false>
 __device__ __forceinline__ void put(const WindowDecodeParams &p, const Unit &u, int head, int col, const float *x,
                                     int count, float m, float l)
 {
     const int64_t row = static_cast<int64_t>(u.sb) * p.Hq + u.h0 + head;
-    if (p.splits == 1) {
+    if (kDone || p.splits == 1) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
         if (!ULY_IN_BOUNDS(p.status, row * D + col, count, p.SB * p.Hq * D, 0x71))
             return;
@@ -227,6 +228,17 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 // 16-byte unit `unit` of row `r` of a 16-row tile, spread over the banks.
 __device__ __forceinline__ uint32_t tile_at(int r, int unit) { return r * kRowBytes + ((unit ^ (r & 7)) << 4); }
 
+// Reads of another block's shared memory (a shared::cluster address).
+__device__ __forceinline__ float2 ld_cluster(uint32_t at)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
+// kCluster: the blocks of a unit are one cluster, which joins their sums through
+// shared memory; otherwise they go through the workspace.
+template <bool kCluster>
 __global__ void __launch_bounds__(kThreads, 2) window_decode_bf16_kernel(const __grid_constant__ WindowDecodeParams p)
 {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -334,10 +346,11 @@ __global__ void __launch_bounds__(kThreads, 2) window_decode_bf16_kernel(const _
         stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     cp_async_wait<0>();
+    if constexpr (!kCluster)
+        grid_next();
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     __syncthreads();
-    grid_next();
     // the warps' sums, brought to the block's maximum: [warp][head][d], then m and l
     float *sums = reinterpret_cast<float *>(smem);
     constexpr int kPitch = kD + 4;
@@ -351,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_decode_bf16_kernel(const _
             sums[(warp * kHeads + 2 * (lane & 3) + (e & 1)) * kPitch + 16 * j + (lane >> 2) + (e >> 1) * 8] = o[j][e];
     __syncthreads();
     const int head = threadIdx.x / 16, col = threadIdx.x % 16 * 8;
-    if (head >= u.heads)
+    if (!kCluster && head >= u.heads)
         return;
     float top = -INFINITY;
 #pragma unroll
@@ -368,7 +381,48 @@ __global__ void __launch_bounds__(kThreads, 2) window_decode_bf16_kernel(const _
         for (int e = 0; e < 8; ++e)
             x[e] = fmaf(sums[(w * kHeads + head) * kPitch + col + e], f, x[e]);
     }
-    put<uint16_t, kD>(p, u, head, col, x, 8, top, total);
+    if constexpr (kCluster) {
+        // this block's sums for the others, behind what its own threads still read;
+        // then every block writes its share of the output, from all of theirs
+        float *mine = reinterpret_cast<float *>(stats + kWarps * kHeads);
+        float2 *mine_stats = reinterpret_cast<float2 *>(mine + kHeads * kD);
+        *reinterpret_cast<float4 *>(mine + head * kD + col) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4 *>(mine + head * kD + col + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        if (col == 0)
+            mine_stats[head] = make_float2(top, total);
+        cluster_sync_all();
+        for (int i = u.split * kThreads + static_cast<int>(threadIdx.x); i < u.heads * (kD / 2);
+             i += p.splits * kThreads) {
+            const int h = i / (kD / 2), at = i % (kD / 2) * 2;
+            float2 ml[kClusterMax], v[kClusterMax];
+            float most = -INFINITY;
+#pragma unroll
+            for (int b = 0; b < kClusterMax; ++b) {
+                ml[b] = make_float2(-INFINITY, 0.f);
+                v[b] = make_float2(0.f, 0.f);
+                if (b < p.splits) {
+                    ml[b] = ld_cluster(cluster_addr(mine_stats + h, b));
+                    v[b] = ld_cluster(cluster_addr(mine + h * kD + at, b));
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < kClusterMax; ++b)
+                most = fmaxf(most, ml[b].x);
+            const float against = most == -INFINITY ? 0.f : most;
+            float sum = 0.f, y[2] = {};
+#pragma unroll
+            for (int b = 0; b < kClusterMax; ++b) {
+                const float f = exp2f(ml[b].x - against);
+                sum = fmaf(ml[b].y, f, sum);
+                y[0] = fmaf(v[b].x, f, y[0]);
+                y[1] = fmaf(v[b].y, f, y[1]);
+            }
+            put<uint16_t, kD, true>(p, u, h, at, y, 2, most, sum);
+        }
+        cluster_sync_all();  // no block's memory goes while another reads it
+    } else {
+        put<uint16_t, kD>(p, u, head, col, x, 8, top, total);
+    }
 }
 
 // ---------------------------------------------------------------- fp32
@@ -470,14 +524,32 @@ __global__ void __launch_bounds__(kThreads) window_decode_f32_kernel(const __gri
     }
 }
 
-// Blocks a (sequence, KV head, group of query heads) is spread over: enough that
-// the blocks fill the GPU about four times, but no fewer than 8 steps a block.
-int splits_for(int64_t units, int64_t C, int64_t window, int64_t sinks)
+// Blocks a (sequence, KV head, group of query heads) is spread over, and whether
+// they are a cluster, which joins their sums without a second launch.  Two blocks
+// fit an SM; a block's start and end cost about as much as 200 tokens, the second
+// launch as 250.  64 units of 1,028 tokens: 9.5 us as clusters of 4 (256 blocks, one
+// wave), 12.9 of 8, 18.3 with one block each; 256 units of 4,100: 78 us with one
+// block each, 87 to 110 as clusters of 2 to 8.
+struct Spread {
+    int splits;
+    bool cluster;
+};
+
+Spread spread_for(int64_t units, int64_t C, int64_t window, int64_t sinks, int esize)
 {
-    const int64_t keys = std::min(C, sinks + window);
-    const int64_t want = (8 * static_cast<int64_t>(num_sms()) + units - 1) / units;
-    const int64_t most = (keys + 8 * kStep - 1) / (8 * kStep);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), kSplitMax)));
+    const int64_t keys = std::min(C, sinks + window), room = 2 * num_sms();
+    const int64_t most = std::min<int64_t>(kSplitMax, (keys + kWarps * kStep - 1) / (kWarps * kStep));
+    Spread best{1, false};
+    int64_t least = 0;
+    for (int n = 1; n <= most; ++n) {
+        const bool cluster = esize == 2 && n > 1 && n <= kClusterMax;
+        const int64_t cost = (units * n + room - 1) / room * ((keys + n - 1) / n + 200) + (n > 1 && !cluster ? 250 : 0);
+        if (n == 1 || cost < least) {
+            least = cost;
+            best = Spread{n, cluster};
+        }
+    }
+    return best;
 }
 
 int parts_of(int G, int esize) { return esize == 2 ? (G + kHeads - 1) / kHeads : (G + kHeadsF32 - 1) / kHeadsF32; }
@@ -489,16 +561,17 @@ size_t up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
 
 size_t window_decode_workspace(int64_t SB, int64_t C, int Hq, int Hkv, int d, int64_t window, int64_t sinks, int esize)
 {
-    const int64_t splits = splits_for(SB * Hkv * parts_of(Hq / Hkv, esize), C, window, sinks);
-    const size_t rows = static_cast<size_t>(SB) * Hq * splits;
-    return splits == 1 ? kAlign : up(rows * d * sizeof(float)) + up(rows * 2 * sizeof(float));
+    const Spread n = spread_for(SB * Hkv * parts_of(Hq / Hkv, esize), C, window, sinks, esize);
+    const size_t rows = static_cast<size_t>(SB) * Hq * n.splits;
+    return n.splits == 1 || n.cluster ? kAlign : up(rows * d * sizeof(float)) + up(rows * 2 * sizeof(float));
 }
 
 cudaError_t launch_window_decode(WindowDecodeParams &p, int d, int esize, void *workspace, cudaStream_t s)
 {
     p.G = p.Hq / p.Hkv;
     p.parts = parts_of(p.G, esize);
-    p.splits = splits_for(p.SB * p.Hkv * p.parts, p.C, p.window, p.sinks);
+    const Spread spread = spread_for(p.SB * p.Hkv * p.parts, p.C, p.window, p.sinks, esize);
+    p.splits = spread.splits;
     const size_t rows = static_cast<size_t>(p.SB) * p.Hq * p.splits;
     p.part = static_cast<float *>(workspace);
     p.stats = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + up(rows * d * sizeof(float)));
@@ -506,12 +579,28 @@ cudaError_t launch_window_decode(WindowDecodeParams &p, int d, int esize, void *
     cudaError_t e;
     if (esize == 2) {
         constexpr size_t smem = static_cast<size_t>(kWarps) * kStages * 2 * kTileBytes;
-        static_assert(smem >= kWarps * kHeads * ((kD + 4) * sizeof(float) + sizeof(float2)), "the joined sums fit");
-        e = cudaFuncSetAttribute(window_decode_bf16_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem));
+        static_assert(smem >= kHeads * (kWarps * ((kD + 4) * sizeof(float) + sizeof(float2)) + kD * sizeof(float) +
+                                        sizeof(float2)),
+                      "the joined sums fit");
+        auto kernel = spread.cluster ? window_decode_bf16_kernel<true> : window_decode_bf16_kernel<false>;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess)
             return e;
-        window_decode_bf16_kernel<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p);
+        if (spread.cluster) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(grid));
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = smem;
+            cfg.stream = s;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = static_cast<unsigned>(p.splits);
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            return cudaLaunchKernelEx(&cfg, kernel, p);
+        }
+        kernel<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p);
     } else if (d == 64) {
         window_decode_f32_kernel<64><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p);
     } else {
