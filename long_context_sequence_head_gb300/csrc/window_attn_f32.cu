@@ -429,11 +429,11 @@ __global__ void __launch_bounds__(kThreads) window_dkv_f32_kernel(const __grid_c
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const int64_t row = q0 + ty + 16 * i;
-                const float p = row >= k0 + tx + 16 * c && row < end[c] ? expf(x[i][c] * s.scale - L[i]) : 0.f;
+                const int64_t row = q0 + ty + 16 * i, key = k0 + tx + 16 * c;
+                const bool one = alone[c] && row == key;  // P = 1 and dS = 0, whatever the roundings
+                const float p = one ? 1.f : row >= key && row < end[c] ? expf(x[i][c] * s.scale - L[i]) : 0.f;
                 sP[(ty + 16 * i) * kPitchP + tx + 16 * c] = p;
-                sS[(ty + 16 * i) * kPitchP + tx + 16 * c] =
-                    alone[c] && row == k0 + tx + 16 * c ? 0.f : p * (y[i][c] - Di[i]);
+                sS[(ty + 16 * i) * kPitchP + tx + 16 * c] = one ? 0.f : p * (y[i][c] - Di[i]);
             }
         __syncthreads();
         add_product<D>(sP, sO, tx, ty, aV);

@@ -207,3 +207,35 @@ def test_gradients_against_differences(uly):
         # a value is off by about 2^-24 of its terms' magnitudes (sum |o dO| below 2^18), over a step of 2^-6 with
         # weights 18/12: 2^-24 2^18 2^6 1.5 < 2^1 at the very worst, and errors of that many terms cancel to its root
         assert abs(slope - want) <= 0.05 * (1 + 2.0 ** -4 * abs(want)), (n, slope, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("N,window,sinks,cu", [(1, 5, 3, None), (65, 1, 0, None), (300, 1, 0, [0, 130, 300]),
+                                               (4, 9, 2, [0, 1, 2, 3, 4])])
+def test_rows_that_see_only_themselves(uly, dtype, N, window, sinks, cu):
+    """dS = P (dP - <dO, O>) is 0 exactly, and so are dQ and dK; O is V, dV the group's dO."""
+    q, k, v, dout = inputs(1, 2, N, 4, 2, 128, dtype)
+    got = run(uly, q, k, v, dout, window, sinks, cu)
+    assert (got["dq"] == 0).all() and (got["dk"] == 0).all()
+    assert torch.equal(got["o"], v.repeat_interleave(2, dim=3))
+    want = dout.double().view(1, 2, N, 2, 2, 128).sum(4)
+    assert (got["dv"].double() - want).abs().max() <= torch.finfo(dtype).eps / 2 * want.abs().max()
+
+
+def test_rows_of_few_keys(uly):
+    """Rows of two to eight keys, one of which holds most of the row: dS of that key is the small rest of a
+    cancellation, which D = <dO, O> from the rounded O would lose.  Each of dS's factors is then off by a rounding
+    (P, dS: 2^-9 on average 2^-10 each) and the gradient by its own, together below 4e-3 of its norm."""
+    for N, window, sinks, cu in ((2, 9, 0, None), (4, 50, 1, None), (900, 3, 1, None), (300, 2, 1, None),
+                                 (22, 90, 1, [0, 3, 5, 9, 11, 16, 22])):
+        q, k, v, dout = inputs(2, 2, N, 8, 2, 128, BF16, seed=7)
+        first = torch.zeros(N, dtype=torch.bool, device="cuda")
+        first[torch.tensor((cu or [0, N])[:-1], device="cuda")] = True
+        common = torch.randn(128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+        q = (q.float() + 0.5 * common).to(BF16)
+        k = torch.where(first[:, None, None], k.float() + 0.5 * common, k.float()).to(BF16)
+        val, _ = reference(q, k, v, dout, allowed(N, window, sinks, cu), 1 / math.sqrt(128), True)
+        got = run(uly, q, k, v, dout, window, sinks, cu)
+        for n in ("dq", "dk"):
+            off = float((got[n].double() - val[n]).norm() / val[n].norm())
+            assert off <= 4.5e-3, (N, n, off)
