@@ -55,7 +55,6 @@ struct FwdParams {
     float *lse;
     int64_t lse_elems;  // extent for the bounds checks of debug builds
     const int32_t *order;        // with documents: query tiles, longest walk first
-    int window, sinks;           // kWindow: keys a row sees before itself, first tokens of its document it keeps seeing
     WaitCfg w;
     RowLayout L;
 };
@@ -78,20 +77,7 @@ __device__ __forceinline__ void doc_range(const FwdParams &p, int64_t i, int64_t
     hi = p.cu[a + 1];
 }
 
-// Of 32 neighbouring keys, those in [lo, hi) (both relative to the first) as bits.
-__device__ __forceinline__ uint32_t key_bits(int lo, int hi)
-{
-    lo = min(max(lo, 0), 32);
-    hi = min(max(hi, 0), 32);
-    const uint32_t below_hi = hi == 32 ? ~0u : (1u << hi) - 1u, below_lo = lo == 32 ? ~0u : (1u << lo) - 1u;
-    return below_hi & ~below_lo;
-}
-
-// kWindow: sliding-window attention.  Row i of a document that starts at s sees
-// the keys [max(s, i - window + 1), i] and [s, s + sinks).  A tile of rows walks
-// the tiles that hold its first row's sinks, then those from its first row's
-// window on: the documents that start inside the tile have theirs there too.
-template <bool kOrdered, bool kWindow>
+template <bool kOrdered>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_bf16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -133,23 +119,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     doc_range(p, row_last, dlo, key_hi);
     if (p.causal)
         key_hi = row_last + 1;
-    [[maybe_unused]] int kt_sink = 0, n_sink = 0;
-    if constexpr (kWindow) {
-        const int64_t start = key_lo;
-        key_lo = max(start, q0 - p.window + 1);
-        const int64_t sink_hi = min(start + p.sinks, key_lo);
-        kt_sink = static_cast<int>(start / kBN);
-        if (sink_hi > start)
-            n_sink = static_cast<int>(min((sink_hi - 1) / kBN + 1, key_lo / kBN)) - kt_sink;
-    }
     const int kt_lo = static_cast<int>(key_lo / kBN);
-    const int n_kv = static_cast<int>((key_hi - 1) / kBN) - kt_lo + 1 + n_sink;
-    auto key_tile = [&](int j) {
-        if constexpr (kWindow)
-            return j < n_sink ? kt_sink + j : kt_lo + j - n_sink;
-        else
-            return kt_lo + j;
-    };
+    const int n_kv = static_cast<int>((key_hi - 1) / kBN) - kt_lo + 1;
 
     if (warp == 8 && lane == 0) {
         mbar_init(q_full, 1);
@@ -194,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             int issued = 0;
             for (int j = 0; j < n_kv && !*abort_flag; ++j) {
-                const int key0 = key_tile(j) * kBN;
+                const int key0 = (kt_lo + j) * kBN;
                 bool ok = true;
                 for (int which = 0; which < 2; ++which) {
                     const int it = 2 * j + which;
@@ -307,15 +278,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             doc_range(p, row < p.N ? row : p.N - 1, lo, hi);
             if (p.causal && row + 1 < hi)
                 hi = row + 1;
-            // kWindow: the row sees [w_lo, hi) and, apart from it, [lo, s_hi)
-            [[maybe_unused]] int64_t w_lo = lo, s_hi = lo;
-            if constexpr (kWindow) {
-                w_lo = max(lo, (row < p.N ? row : p.N - 1) - p.window + 1);
-                if (lo + p.sinks >= w_lo)
-                    w_lo = lo;
-                else
-                    s_hi = lo + p.sinks;
-            }
             const uint32_t tS = tbase + t * 128 + (static_cast<uint32_t>(wq * 32) << 16);
             const uint32_t tO = tbase + 256 + t * 128 + (static_cast<uint32_t>(wq * 32) << 16);
             float m = -INFINITY, l = 0.f;
@@ -334,31 +296,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int cb = 0; cb < kBN; cb += 32)
                     tmem_ld_fence32p(u + cb);
-                const int64_t key0 = static_cast<int64_t>(key_tile(j)) * kBN;
-                bool masked = key0 < lo || key0 + kBN > hi;
+                const int64_t key0 = static_cast<int64_t>(kt_lo + j) * kBN;
+                const bool masked = key0 < lo || key0 + kBN > hi;
                 // no key of this tile is allowed for this row (a row of a later
                 // document in a query tile that straddles a document boundary)
-                bool row_empty = key0 >= hi || key0 + kBN <= lo;
-                // the allowed keys of 32 columns from `col` on
-                auto columns = [&](int col) {
-                    const int base = static_cast<int>(key0) + col;
-                    return key_bits(static_cast<int>(w_lo) - base, static_cast<int>(hi) - base) |
-                           key_bits(static_cast<int>(lo) - base, static_cast<int>(s_hi) - base);
-                };
-                if constexpr (kWindow) {
-                    masked = !((key0 >= w_lo && key0 + kBN <= hi) || (key0 >= lo && key0 + kBN <= s_hi));
-                    row_empty = (key0 >= hi || key0 + kBN <= w_lo) && (key0 >= s_hi || key0 + kBN <= lo);
-                    if (masked) {
-#pragma unroll
-                        for (int cb = 0; cb < kBN; cb += 32) {
-                            const uint32_t keep = columns(cb);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (!(keep >> c & 1u))
-                                    u[cb + c] = __float_as_uint(-INFINITY);
-                        }
-                    }
-                } else if (masked) {
+                const bool row_empty = key0 >= hi || key0 + kBN <= lo;
+                if (masked) {
                     // allowed columns of this tile: [lo_c, hi_c)
                     const int lo_c = static_cast<int>(max(lo - key0, int64_t(0)));
                     const int hi_c = static_cast<int>(min(hi - key0, int64_t(kBN)));
@@ -402,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 float alpha = 1.f;
                 bool rescale = false;
-                if ((kOrdered || kWindow) && first) {
+                if (kOrdered && first) {
                     // a row's first tile (with documents these are frequent: rows
                     // of a later document in a tile that straddles a boundary
                     // meet their first allowed key late): S, masked above, is
@@ -463,18 +406,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld_wait();
                         tmem_ld_fence32p(v);
                         tmem_ld_fence32p(v + 32);
-                        [[maybe_unused]] uint32_t keep[2] = {~0u, ~0u};
-                        if constexpr (kWindow)
-                            if (masked)
-                                keep[0] = columns(half * 64), keep[1] = columns(half * 64 + 32);
 #pragma unroll
                         for (int c = 0; c < 64; ++c) {
                             const int cg = half * 64 + c;
-                            if constexpr (kWindow) {
-                                pm[c & 7] = fmaxf(pm[c & 7], keep[c >> 5] >> (c & 31) & 1u ? __uint_as_float(v[c])
-                                                                                           : -INFINITY);
-                                continue;
-                            }
                             const float sv = (cg < lo_c || cg >= hi_c) ? -INFINITY : __uint_as_float(v[c]);
                             pm[c & 7] = fmaxf(pm[c & 7], sv);
                         }
@@ -501,19 +435,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld_fence32p(v);
                         tmem_ld_fence32p(v + 32);
                         uint32_t pk[32];
-                        [[maybe_unused]] uint32_t keep[2] = {~0u, ~0u};
-                        if constexpr (kWindow)
-                            if (masked)
-                                keep[0] = columns(half * 64), keep[1] = columns(half * 64 + 32);
 #pragma unroll
                         for (int c = 0; c < 64; c += 2) {
                             const int cg = half * 64 + c;
-                            float s0 = (cg < lo_c || cg >= hi_c) ? -INFINITY : __uint_as_float(v[c]);
-                            float s1 = (cg + 1 < lo_c || cg + 1 >= hi_c) ? -INFINITY : __uint_as_float(v[c + 1]);
-                            if constexpr (kWindow) {
-                                s0 = keep[c >> 5] >> (c & 31) & 1u ? __uint_as_float(v[c]) : -INFINITY;
-                                s1 = keep[c >> 5] >> (c & 31) & 2u ? __uint_as_float(v[c + 1]) : -INFINITY;
-                            }
+                            const float s0 = (cg < lo_c || cg >= hi_c) ? -INFINITY : __uint_as_float(v[c]);
+                            const float s1 = (cg + 1 < lo_c || cg + 1 >= hi_c) ? -INFINITY : __uint_as_float(v[c + 1]);
                             const float2 x = ffma2(make_float2(s0, s1), sl2, nm2);
                             const float2 pv = make_float2(ex2_approx(x.x), ex2_approx(x.y));
                             rs2[(c >> 1) & 3] = fadd2(rs2[(c >> 1) & 3], pv);
@@ -617,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-CUresult make_rows_map_bf16(CUtensorMap *map, const void *base, const AttnShape &s, int H)
+CUresult make_rows_map_bf16(CUtensorMap *map, const void *base, const AttnShape &s, int H, int rows)
 {
     // head layout: [S][B][N][H][d]; seq layout: [P][B][N/P][P*H][d]
     const int64_t B = s.L.B;
@@ -628,7 +554,7 @@ CUresult make_rows_map_bf16(CUtensorMap *map, const void *base, const AttnShape 
                           static_cast<cuuint64_t>(B), static_cast<cuuint64_t>(outer)};
     cuuint64_t strides[4] = {static_cast<cuuint64_t>(kD) * 2, static_cast<cuuint64_t>(Hd) * kD * 2,
                              static_cast<cuuint64_t>(T) * Hd * kD * 2, static_cast<cuuint64_t>(B) * T * Hd * kD * 2};
-    cuuint32_t box[5] = {64, 1, kBM, 1, 1};
+    cuuint32_t box[5] = {64, 1, static_cast<cuuint32_t>(rows), 1, 1};
     cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides,
                                 box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -661,12 +587,9 @@ cudaError_t launch_attn_fwd_bf16(const AttnShape &s, const void *q, const void *
     p.w = wait_cfg();
     p.L = s.L;
     p.order = s.order_dev;
-    p.window = s.window;
-    p.sinks = s.sinks;
     const int64_t units = p.SB * p.Hkv * p.npairs * p.n_qtiles;
     const size_t smem = FwdSmem::kTotal + 1024;
-    auto kernel = s.window ? (p.order ? attn_fwd_bf16_kernel<true, true> : attn_fwd_bf16_kernel<false, true>)
-                           : (p.order ? attn_fwd_bf16_kernel<true, false> : attn_fwd_bf16_kernel<false, false>);
+    auto kernel = p.order ? attn_fwd_bf16_kernel<true> : attn_fwd_bf16_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess)
         return e;

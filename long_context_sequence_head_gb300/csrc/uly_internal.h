@@ -230,8 +230,8 @@ struct AttnShape {
 };
 
 // 5-D bf16 tensor map {d, H, T, B, outer} over a row-major
-// [outer][B][T][H][d] buffer, box {64, 1, 128, 1, 1}, 128-byte swizzle.
-CUresult make_rows_map_bf16(CUtensorMap *map, const void *base, const AttnShape &s, int H);
+// [outer][B][T][H][d] buffer, box {64, 1, rows, 1, 1}, 128-byte swizzle.
+CUresult make_rows_map_bf16(CUtensorMap *map, const void *base, const AttnShape &s, int H, int rows = 128);
 
 cudaError_t launch_attn_fwd_f32(const AttnShape &s, const float *q, const float *k, const float *v, float *o,
                                 float *lse, cudaStream_t stream);
@@ -252,6 +252,9 @@ struct BwdScratch {
 cudaError_t launch_attn_bwd_bf16(const AttnShape &s, const void *q, const void *k, const void *v, const void *o,
                                  const float *lse, const void *dout, void *dq, void *dk, void *dv,
                                  const BwdScratch &scr, cudaStream_t stream);
+
+cudaError_t launch_window_fwd_bf16(const AttnShape &s, const void *q, const void *k, const void *v, void *o,
+                                   float *lse, cudaStream_t stream);
 
 // fp32 with a sliding window; part of window_attn.cu's units (key tiles of 64).
 constexpr int kWindowTileF32 = 64;

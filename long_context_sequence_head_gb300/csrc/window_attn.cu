@@ -1,6 +1,6 @@
 // Sliding-window attention with sinks over the Ulysses head shards: how a call
 // is cut into work, and the small kernels around the attention kernels
-// (attn_fwd_bf16.cu, attn_bwd_bf16.cu, window_attn_f32.cu).
+// (window_fwd_bf16.cu, attn_bwd_bf16.cu, window_attn_f32.cu).
 //
 // Row i of a document that starts at s sees the keys j <= i of its document
 // with i - j < window, and the document's first `sinks` keys.
@@ -295,7 +295,7 @@ cudaError_t window_attn_fwd(AttnShape s, const void *q, const void *k, const voi
             return e;
     }
     if (esize == 2)
-        return launch_attn_fwd_bf16(s, q, k, v, o, lse, stream);
+        return launch_window_fwd_bf16(s, q, k, v, o, lse, stream);
     return launch_window_fwd_f32(s, static_cast<const float *>(q), static_cast<const float *>(k),
                                  static_cast<const float *>(v), static_cast<float *>(o), lse, stream);
 }
