@@ -260,14 +260,24 @@ __global__ void __launch_bounds__(256) window_few_kernel(const __grid_constant__
         if (keys > 1) {
             const float l2 = ok ? p.lse[lrow] * 1.4426950408889634f : 0.f;
             const uint4 d = u < n16 ? d4[u] : zero, q = u < n16 ? q4[u] : zero;
-            for (int j = 0; j < static_cast<int>(keys); ++j) {
-                const int64_t key = j < before ? start + j : w_lo + j - before;
-                const int64_t at = p.L.off(p.N, sb, key, p.Hkv, h / G, kD) + lane % 16 * 8;
-                const bool in = u < n16 && ULY_IN_BOUNDS(p.status, at, 8, p.kv_elems, 0x30);
-                const uint4 kk = in ? *reinterpret_cast<const uint4 *>(p.k + at) : zero;
-                const uint4 vv = in ? *reinterpret_cast<const uint4 *>(p.v + at) : zero;
-                const float s = half_warp_sum(dot8(q, kk)), dp = half_warp_sum(dot8(d, vv));
-                acc = fmaf(exp2f(fmaf(s, p.scale_log2, -l2)), dp, acc);
+            for (int j0 = 0; j0 < static_cast<int>(keys); j0 += 4) {  // four keys on their way at once
+                uint4 kk[4], vv[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = j0 + e;
+                    const int64_t key = j < before ? start + j : w_lo + j - before;
+                    const int64_t at = p.L.off(p.N, sb, key, p.Hkv, h / G, kD) + lane % 16 * 8;
+                    const bool in =
+                        u < n16 && j < keys && ULY_IN_BOUNDS(p.status, at, 8, p.kv_elems, 0x30);
+                    kk[e] = in ? *reinterpret_cast<const uint4 *>(p.k + at) : zero;
+                    vv[e] = in ? *reinterpret_cast<const uint4 *>(p.v + at) : zero;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float s = half_warp_sum(dot8(q, kk[e])), dp = half_warp_sum(dot8(d, vv[e]));
+                    // a key that is not there has dP = 0
+                    acc = fmaf(j0 + e < keys ? exp2f(fmaf(s, p.scale_log2, -l2)) : 0.f, dp, acc);
+                }
             }
         }
         if (u < n16 && (lane & 15) == 0 && ok) {

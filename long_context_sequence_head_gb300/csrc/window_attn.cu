@@ -64,7 +64,7 @@ struct Cut {
 
     Cut(int64_t window, int64_t sinks, bool docs, int tile)
         : tiles_with_sinks(sinks > 0 ? (sinks + tile - 1) / tile + (docs ? 1 : 0) : 0),
-          length(std::max<int64_t>(8, window_tiles(window, tile))),
+          length(std::max<int64_t>(4, window_tiles(window, tile))),
           most(tiles_with_sinks > 0 ? 64 / tiles_with_sinks : 0)
     {
     }
@@ -216,13 +216,15 @@ Layout layout(int64_t SB, int64_t N, int Hq, int Hkv, int d, int64_t window, int
 
 // ---------------------------------------------------------------- join
 // dK and dV of the sinks whose walk was cut: the sums of their tile's slots, in
-// order.  One block per (tile, problem), blockDim.x / d keys at once.
+// order.  Blocks take a (tile, problem) and every gridDim.y-th of its keys; of 2 d
+// threads the first d sum dK, the others dV.
 template <typename T>
 __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ AttnShape s, T *__restrict__ dk,
                                                           T *__restrict__ dv, int tile)
 {
     const WindowUnits &wu = s.units;
-    const int col = threadIdx.x % s.d, keys = 256 / s.d;
+    const int col = threadIdx.x % s.d;
+    const bool second = static_cast<int>(threadIdx.x) >= s.d;
     const int64_t nprob = s.SB * s.Hkv;
     const int64_t prob = blockIdx.x % nprob;
     const int t = static_cast<int>(blockIdx.x / nprob);
@@ -237,26 +239,24 @@ __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant_
                          t * (1 + wu.extra), 1 + wu.extra);
     }
     [[maybe_unused]] const int64_t extent = nprob * wu.slots * 2 * wu.rows * s.d;
-    const int64_t other = static_cast<int64_t>(wu.rows) * s.d;  // from a dK to its dV
-    for (int r = threadIdx.x / s.d; r < join.y; r += keys) {
-        float a = 0.f, b = 0.f;
-        for (int i = 0; i < join.w; ++i) {
-            const int64_t off = ((prob * wu.slots + join.z + i) * 2 * wu.rows + r) * s.d + col;
-            if (!ULY_IN_BOUNDS(s.status, off, other + 1, extent, 0x61))
-                break;
-            a += wu.part[off];
-            b += wu.part[off + other];
-        }
+    const int64_t step = static_cast<int64_t>(2) * wu.rows * s.d;  // from a slot to the next
+    for (int r = blockIdx.y; r < join.y; r += gridDim.y) {
+        const int64_t first = (prob * wu.slots + join.z) * step + ((second ? wu.rows : 0) + r) * s.d + col;
+        float sum = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < join.w; ++i)
+            if (ULY_IN_BOUNDS(s.status, first + i * step, 1, extent, 0x61))
+                sum += wu.part[first + i * step];
+        if (!second)
+            sum *= s.scale;
         const int64_t off = s.L.off(s.N, sb, join.x + r, s.Hkv, kvh, s.d) + col;
         if (!ULY_IN_BOUNDS(s.status, off, 1, s.kv_elems, 0x62))
             break;
-        if constexpr (sizeof(T) == 2) {
-            dk[off] = static_cast<T>(pack_bf16x2(a * s.scale, 0.f));
-            dv[off] = static_cast<T>(pack_bf16x2(b, 0.f));
-        } else {
-            dk[off] = a * s.scale;
-            dv[off] = b;
-        }
+        T *out = second ? dv : dk;
+        if constexpr (sizeof(T) == 2)
+            out[off] = static_cast<T>(pack_bf16x2(sum, 0.f));
+        else
+            out[off] = sum;
     }
 }
 
@@ -265,8 +265,8 @@ cudaError_t launch_join(const AttnShape &s, void *dk, void *dv, int tile, cudaSt
 {
     if (s.units.n_joins == 0)
         return cudaSuccess;
-    window_join_kernel<T><<<static_cast<unsigned>(s.units.n_joins * s.SB * s.Hkv), 256, 0, stream>>>(
-        s, static_cast<T *>(dk), static_cast<T *>(dv), tile);
+    const dim3 grid(static_cast<unsigned>(s.units.n_joins * s.SB * s.Hkv), std::min(s.units.rows, 16));
+    window_join_kernel<T><<<grid, 2 * s.d, 0, stream>>>(s, static_cast<T *>(dk), static_cast<T *>(dv), tile);
     return cudaGetLastError();
 }
 

@@ -71,21 +71,25 @@ struct RowMask {
     __device__ __forceinline__ bool alone() const { return row == start || (window == 1 && sinks == 0); }
 };
 
-// 64 rows of a tensor of H heads from token n0 on; rows past N are zero.
+// 64 rows of a tensor of H heads (head layout) from token n0 on; rows past N are
+// zero.  All of a thread's loads are on their way at once.
 template <int D>
 __device__ __forceinline__ void load_tile(float *dst, const float *src, const AttnShape &s, int64_t sb, int64_t n0,
                                           int H, int h, [[maybe_unused]] int64_t extent)
 {
-    for (int i = threadIdx.x; i < kT * D / 4; i += kThreads) {
-        const int r = i / (D / 4), c = i % (D / 4) * 4;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (n0 + r < s.N) {
-            const int64_t off = s.L.off(s.N, sb, n0 + r, H, h, D) + c;
-            if (ULY_IN_BOUNDS(s.status, off, 4, extent, 0x63))
-                v = *reinterpret_cast<const float4 *>(src + off);
-        }
-        *reinterpret_cast<float4 *>(dst + r * (D + kPad) + c) = v;
+    constexpr int kPer = D / 4, kRows = kThreads / kPer;  // threads of a row, rows at once
+    const int r0 = threadIdx.x / kPer, c = threadIdx.x % kPer * 4;
+    const int64_t first = ((sb * s.N + n0 + r0) * H + h) * D + c, step = static_cast<int64_t>(kRows) * H * D;
+    float4 v[kT / kRows];
+#pragma unroll
+    for (int i = 0; i < kT / kRows; ++i) {
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (n0 + r0 + i * kRows < s.N && ULY_IN_BOUNDS(s.status, first + i * step, 4, extent, 0x63))
+            v[i] = *reinterpret_cast<const float4 *>(src + first + i * step);
     }
+#pragma unroll
+    for (int i = 0; i < kT / kRows; ++i)
+        *reinterpret_cast<float4 *>(dst + (r0 + i * kRows) * (D + kPad) + c) = v[i];
 }
 
 // x[i][c] = <a row ty + 16 i, b row tx + 16 c>
