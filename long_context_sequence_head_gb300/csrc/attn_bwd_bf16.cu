@@ -767,7 +767,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     doc_range(p, key, start, end);
                     alone = key == start || (p.window == 1 && p.sinks == 0);
                 }
-                if (unit.w >= 0) {
+                if (unit.w >= 0 && (unit.w & 1) && p.wu.chunks != nullptr) {
+                    store = false;  // an extra unit for dQ
+                } else if (unit.w >= 0) {
                     const int64_t first = max(last_doc, kv0), end = min(last_doc + p.sinks, p.N);
                     if (key >= first && key < end) {
                         const int64_t off =
@@ -792,6 +794,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_wait();
                 tmem_ld_fence32p(x);
                 if constexpr (kWindow) {
+                    if (part != nullptr && p.wu.chunks != nullptr)  // window_sinks.cu has this sum
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            x[c] = 0u;
                     // a row that sees only itself: P = 1, dS = 0, left out above; its
                     // tile's own unit adds it
                     if (alone && which == 0 && !(unit.w >= 0 && (unit.w & 1))) {
@@ -892,7 +898,9 @@ cudaError_t launch_attn_bwd_bf16(const AttnShape &s, const void *q, const void *
             if (e != cudaSuccess)
                 return e;
         }
-        e = cudaMemsetAsync(scr.dq_acc, 0, static_cast<size_t>(s.SB) * s.Hq * Npad * kD * sizeof(float), stream);
+        e = s.units.chunks ? launch_window_sinks(s, q, k, v, dout, scr, stream)
+                           : cudaMemsetAsync(scr.dq_acc, 0,
+                                             static_cast<size_t>(s.SB) * s.Hq * Npad * kD * sizeof(float), stream);
         if (e != cudaSuccess)
             return e;
     }

@@ -181,7 +181,19 @@ struct WindowUnits {
     const int4 *units = nullptr; // device, with documents: {key tile, first query tile, query tiles, slot * 2 + extra or -1}
     const int4 *joins = nullptr; // device, with documents: {first key, keys, first slot, slots}
     float *part = nullptr;       // [problem][slot][2][rows][d] fp32: dK, dV
+    // bf16 with up to kWindowSinksApart sinks: window_sinks.cu takes their dK and dV in
+    // documents with rows past their window, in chunks of row tiles; up to kWindowSinks
+    // also what they add to the dQ of those rows (it sets the accumulator), so that no
+    // unit is extra.  Device, three each: {first row tile, past the last, document's start
+    // or -1 for no sinks, sinks}, {slot of the sinks in their first key tile, from a key
+    // tile's to the next one's, last row tile that the main kernel walks for the first key
+    // tile, for the second}, {document's end, first row tile whose dQ is this document's to
+    // set, 0, 0}
+    const int4 *chunks = nullptr;
+    int n_chunks = 0;
+    int sinks = 0;  // of a document in the chunks, at most
 };
+constexpr int kWindowSinks = 64, kWindowSinksApart = 512;
 
 // The last query tile that sees key tile t through the window, without documents.
 __host__ __device__ inline int window_end(int64_t N, int window, int tile, int t)
@@ -249,6 +261,8 @@ struct BwdScratch {
     float *dq_acc;
     int64_t Npad;
 };
+cudaError_t launch_window_sinks(const AttnShape &s, const void *q, const void *k, const void *v, const void *dout,
+                                const BwdScratch &scr, cudaStream_t stream);
 cudaError_t launch_attn_bwd_bf16(const AttnShape &s, const void *q, const void *k, const void *v, const void *o,
                                  const float *lse, const void *dout, void *dq, void *dk, void *dv,
                                  const BwdScratch &scr, cudaStream_t stream);

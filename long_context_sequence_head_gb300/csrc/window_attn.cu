@@ -74,9 +74,22 @@ struct Cut {
     }
 };
 
-// Most units, slots and joins of a problem whose documents are not known.
-void unit_bounds(int64_t N, int64_t window, int64_t sinks, int num_docs, int tile, int64_t &units, int64_t &slots,
-                 int64_t &joins)
+// In bf16: in documents with rows past their window the dK and dV of the sinks are
+// window_sinks.cu's.  The more sinks there are the less each stands out: with 512 they
+// are the main kernel's.
+bool apart(int64_t sinks, int tile) { return tile == 128 && sinks > 0 && sinks <= kWindowSinksApart; }
+
+// Row tiles of a chunk of window_sinks.cu: as short as leaves a problem 64 of them, but
+// with many sinks (whose sums are large) 4 for each SM in all.
+int chunk_tiles(int64_t N, int64_t sinks, int64_t nprob)
+{
+    const int64_t most = sinks <= kWindowSinks ? 64 : std::clamp<int64_t>(608 / nprob, 4, 64);
+    return static_cast<int>(std::max<int64_t>(2, ((N + 127) / 128 + most - 1) / most));
+}
+
+// Most units, slots, joins and chunks of a problem whose documents are not known.
+void unit_bounds(int64_t N, int64_t window, int64_t sinks, int num_docs, int tile, int64_t nprob, int64_t &units,
+                 int64_t &slots, int64_t &joins, int64_t &chunks)
 {
     const Cut cut(window, sinks, num_docs > 0, tile);
     const int64_t n = (N + tile - 1) / tile;
@@ -86,15 +99,99 @@ void unit_bounds(int64_t N, int64_t window, int64_t sinks, int num_docs, int til
     const int64_t extra = std::min(joins * cut.most, joins + cut.tiles_with_sinks * (n + docs) / cut.length);
     units = n + extra;
     slots = joins + extra;
+    chunks = 0;
+    if (apart(sinks, tile)) {
+        // a document has chunks of its own beside those of the rows between; documents
+        // may share a tile
+        const int64_t own = std::min(n, docs), len = chunk_tiles(N, sinks, nprob), pieces = (n + len - 1) / len;
+        chunks = pieces + 3 * own + 1;
+        slots = joins + cut.tiles_with_sinks * (pieces + 2 * own);
+    }
 }
 
 struct Units {
     WindowUnits u;
-    std::vector<int32_t> list;  // with documents: units, then joins, four integers each
+    std::vector<int32_t> list;  // with documents or sinks apart: units, joins and chunks, four integers each
 };
 
-Units make_units(int64_t N, int window, int sinks, const int32_t *cu, int num_docs, int tile)
+// The units with the sinks' work apart, with documents or without.
+Units make_units_apart(int64_t N, int window, int sinks, const int32_t *cu, int num_docs, int64_t nprob)
 {
+    constexpr int tile = 128;
+    const Cut cut(window, sinks, num_docs > 0, tile);
+    const bool wide = sinks > kWindowSinks;
+    Units r;
+    WindowUnits &u = r.u;
+    const int n = static_cast<int>((N + tile - 1) / tile), len = chunk_tiles(N, sinks, nprob);
+    u.rows = std::min(sinks, tile);
+    std::vector<int4> units, joins, chunks;
+    auto fill = [&](int from, int to) {  // row tiles that only need zeros for their dQ
+        for (; !wide && from < to; from += len)
+            chunks.insert(chunks.end(), {make_int4(from, std::min(from + len, to), -1, 0), make_int4(0, 0, 0, 0),
+                                         make_int4(0, 0, 0, 0)});
+    };
+    int done = 0;  // row tiles whose dQ is set
+    for (int t = 0; t < n; ++t) {
+        const int64_t k0 = static_cast<int64_t>(t) * tile, last = std::min(k0 + tile, N) - 1;
+        int64_t lo, hi;
+        doc_range_host(cu, num_docs, N, last, lo, hi);
+        auto end_of = [&](int64_t key) { return static_cast<int>((std::min(key + window, hi) - 1) / tile); };
+        const int end = end_of(last), all = static_cast<int>((hi - 1) / tile);
+        const bool sink = lo + sinks > k0;
+        const int past = wide && sink ? all - end : 0, extra = cut.extra(past);
+        const int walk = end - t + 1 + (extra == 0 ? past : 0);
+        u.work += end - t + 1 + past;
+        units.push_back(make_int4(t, t, walk, -1));
+        // the document's first tile, whose walk ends first
+        const int first = static_cast<int>(lo / tile);
+        if (!sink || all <= end_of(static_cast<int64_t>(first) * tile + tile - 1))
+            continue;
+        units.back().w = u.slots * 2;
+        for (int e = 0; e < extra; ++e) {
+            const int from = static_cast<int>(static_cast<int64_t>(past) * e / extra);
+            const int to = static_cast<int>(static_cast<int64_t>(past) * (e + 1) / extra);
+            units.push_back(make_int4(t, end + 1 + from, to - from, 1));
+        }
+        const int pieces = (all - first + len) / len;
+        const int64_t from_key = std::max(lo, k0);
+        joins.push_back(make_int4(static_cast<int>(from_key),
+                                  static_cast<int>(std::min(std::min(lo + sinks, k0 + tile), hi) - from_key), u.slots,
+                                  1 + pieces));
+        if (t == first) {
+            // without the keys of a tile that another document ends: a walk of one tile,
+            // of its own unit
+            const int64_t whole = hi == N ? N : hi / tile * tile;
+            const int64_t next_last = std::min(k0 + 2 * tile, N) - 1;
+            const int count = static_cast<int>(std::min(lo + sinks, whole) - lo);
+            u.sinks = std::max(u.sinks, count);
+            fill(done, first);
+            for (int i = 0; i < pieces; ++i) {
+                const int from = first + i * len;
+                chunks.insert(chunks.end(),
+                              {make_int4(from, std::min(from + len, all + 1), static_cast<int>(lo), count),
+                               make_int4(u.slots + 1 + i, 1 + pieces, end, end_of(next_last)),
+                               make_int4(static_cast<int>(hi), std::max(done, first), 0, 0)});
+            }
+            done = all + 1;
+        }
+        u.slots += 1 + pieces;
+    }
+    fill(done, n);
+    std::stable_sort(units.begin(), units.end(), [](const int4 &a, const int4 &b) { return a.z > b.z; });
+    u.longest = units[0].z;
+    u.n_units = static_cast<int>(units.size());
+    u.n_joins = static_cast<int>(joins.size());
+    u.n_chunks = static_cast<int>(chunks.size() / 3);
+    for (const std::vector<int4> *v : {&units, &joins, &chunks})
+        for (const int4 &x : *v)
+            r.list.insert(r.list.end(), {x.x, x.y, x.z, x.w});
+    return r;
+}
+
+Units make_units(int64_t N, int window, int sinks, const int32_t *cu, int num_docs, int tile, int64_t nprob)
+{
+    if (apart(sinks, tile))
+        return make_units_apart(N, window, sinks, cu, num_docs, nprob);
     Units r;
     WindowUnits &u = r.u;
     const Cut cut(window, sinks, num_docs > 0, tile);
@@ -177,7 +274,7 @@ void tile_order(int64_t N, int window, int sinks, const int32_t *cu, int num_doc
 struct Layout {
     size_t cu = 0, list = 0, list_ints = 0, lse2 = 0, D = 0, acc = 0, part = 0, total = 0;
     int64_t Npad = 0;
-    int64_t units = 0, slots = 0, joins = 0;
+    int64_t units = 0, slots = 0, joins = 0, chunks = 0;
 };
 
 Layout layout(int64_t SB, int64_t N, int Hq, int Hkv, int d, int64_t window, int64_t sinks, int num_docs, bool bwd,
@@ -192,10 +289,11 @@ Layout layout(int64_t SB, int64_t N, int Hq, int Hkv, int d, int64_t window, int
         return at;
     };
     if (bwd)
-        unit_bounds(N, window, sinks, num_docs, tile, L.units, L.slots, L.joins);
-    if (num_docs > 0) {
+        unit_bounds(N, window, sinks, num_docs, tile, SB * Hkv, L.units, L.slots, L.joins, L.chunks);
+    if (num_docs > 0 || L.chunks > 0) {
         L.cu = take((static_cast<size_t>(num_docs) + 1) * sizeof(int32_t));
-        L.list_ints = bwd ? static_cast<size_t>(L.units + L.joins) * 4 : static_cast<size_t>((N + 127) / 128);
+        L.list_ints = bwd ? static_cast<size_t>(L.units + L.joins + 3 * L.chunks) * 4
+                          : static_cast<size_t>((N + 127) / 128);
         L.list = take(L.list_ints * sizeof(int32_t));
     }
     L.Npad = (N + 127) / 128 * 128;
@@ -306,20 +404,25 @@ cudaError_t window_attn_bwd(AttnShape s, const void *q, const void *k, const voi
 {
     const int tile = esize == 2 ? 128 : kWindowTileF32;
     const Layout L = layout(s.SB, s.N, s.Hq, s.Hkv, s.d, s.window, s.sinks, s.num_docs, true, esize);
-    Units units = make_units(s.N, s.window, s.sinks, s.cu_host, s.num_docs, tile);
-    if (units.u.slots > L.slots || units.u.n_units > L.units || units.u.n_joins > L.joins)
+    Units units = make_units(s.N, s.window, s.sinks, s.cu_host, s.num_docs, tile, s.SB * s.Hkv);
+    if (units.u.slots > L.slots || units.u.n_units > L.units || units.u.n_joins > L.joins ||
+        units.u.n_chunks > L.chunks)
         return cudaErrorInvalidValue;  // the bounds above hold, so this is never reached
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     s.units = units.u;
     s.units.part = reinterpret_cast<float *>(ws + L.part);
-    if (s.cu_host) {
+    if (!units.list.empty()) {
         const size_t list = (L.list - L.cu) / sizeof(int32_t);
         std::vector<int32_t> host(list);
-        std::copy(s.cu_host, s.cu_host + s.num_docs + 1, host.begin());
+        if (s.cu_host) {
+            std::copy(s.cu_host, s.cu_host + s.num_docs + 1, host.begin());
+            s.cu_dev = reinterpret_cast<int32_t *>(ws + L.cu);
+        }
         host.insert(host.end(), units.list.begin(), units.list.end());
-        s.cu_dev = reinterpret_cast<int32_t *>(ws + L.cu);
         s.units.units = reinterpret_cast<int4 *>(ws + L.list);
         s.units.joins = s.units.units + s.units.n_units;
+        if (s.units.n_chunks > 0)
+            s.units.chunks = s.units.joins + s.units.n_joins;
         const cudaError_t e = stage(host, reinterpret_cast<int32_t *>(ws + L.cu), stream);
         if (e != cudaSuccess)
             return e;
