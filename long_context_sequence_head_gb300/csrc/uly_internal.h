@@ -193,7 +193,7 @@ struct WindowUnits {
     int n_chunks = 0;
     int sinks = 0;  // of a document in the chunks, at most
 };
-constexpr int kWindowSinks = 64, kWindowSinksApart = 512;
+constexpr int kWindowSinks = 64, kWindowSinksApart = 320;
 
 // The last query tile that sees key tile t through the window, without documents.
 __host__ __device__ inline int window_end(int64_t N, int window, int tile, int t)

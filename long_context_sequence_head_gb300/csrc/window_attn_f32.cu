@@ -306,22 +306,18 @@ __global__ void __launch_bounds__(kThreads) window_pre_f32_kernel(const __grid_c
 
 // One block: dQ of 64 rows of one query head, over the forward's walk.
 template <int D>
-__global__ void __launch_bounds__(kThreads) window_dq_f32_kernel(const __grid_constant__ AttnShape s,
-                                                                 const float *__restrict__ q,
-                                                                 const float *__restrict__ k,
-                                                                 const float *__restrict__ v,
-                                                                 const float *__restrict__ lse,
-                                                                 const float *__restrict__ dout,
-                                                                 const float *__restrict__ Dv, float *__restrict__ dq)
+__device__ __forceinline__ void window_dq(const AttnShape &s, int64_t block, float *sm, const float *__restrict__ q,
+                                          const float *__restrict__ k, const float *__restrict__ v,
+                                          const float *__restrict__ lse, const float *__restrict__ dout,
+                                          const float *__restrict__ Dv, float *__restrict__ dq)
 {
-    extern __shared__ __align__(16) float sm[];
     constexpr int kTile = kT * (D + kPad);
     float *sQ = sm, *sO = sm + kTile, *sK = sm + 2 * kTile, *sV = sm + 3 * kTile, *sP = sm + 4 * kTile;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int64_t tiles = (s.N + kT - 1) / kT;
-    const int64_t q0 = blockIdx.x % tiles * kT;
-    const int h = static_cast<int>(blockIdx.x / tiles % s.Hq);
-    const int64_t sb = blockIdx.x / tiles / s.Hq;
+    const int64_t q0 = block % tiles * kT;
+    const int h = static_cast<int>(block / tiles % s.Hq);
+    const int64_t sb = block / tiles / s.Hq;
     const int kvh = h / (s.Hq / s.Hkv);
     load_tile<D>(sQ, q, s, sb, q0, s.Hq, h, s.q_elems);
     load_tile<D>(sO, dout, s, sb, q0, s.Hq, h, s.q_elems);
@@ -369,22 +365,18 @@ __global__ void __launch_bounds__(kThreads) window_dq_f32_kernel(const __grid_co
 // One block: dK and dV of 64 keys of one KV head, or its unit's part of them,
 // over the query tiles of the unit and the heads of the group.
 template <int D>
-__global__ void __launch_bounds__(kThreads) window_dkv_f32_kernel(const __grid_constant__ AttnShape s,
-                                                                  const float *__restrict__ q,
-                                                                  const float *__restrict__ k,
-                                                                  const float *__restrict__ v,
-                                                                  const float *__restrict__ lse,
-                                                                  const float *__restrict__ dout,
-                                                                  const float *__restrict__ Dv, float *__restrict__ dk,
-                                                                  float *__restrict__ dv)
+__device__ __forceinline__ void window_dkv(const AttnShape &s, int64_t block, float *sm, const float *__restrict__ q,
+                                           const float *__restrict__ k, const float *__restrict__ v,
+                                           const float *__restrict__ lse, const float *__restrict__ dout,
+                                           const float *__restrict__ Dv, float *__restrict__ dk,
+                                           float *__restrict__ dv)
 {
-    extern __shared__ __align__(16) float sm[];
     constexpr int kTile = kT * (D + kPad);
     float *sK = sm, *sV = sm + kTile, *sQ = sm + 2 * kTile, *sO = sm + 3 * kTile, *sP = sm + 4 * kTile,
           *sS = sP + kT * kPitchP;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int64_t prob = blockIdx.x % (s.SB * s.Hkv);
-    const int4 unit = window_unit(s.units, s.N, s.window, kT, static_cast<int>(blockIdx.x / (s.SB * s.Hkv)));
+    const int64_t prob = block % (s.SB * s.Hkv);
+    const int4 unit = window_unit(s.units, s.N, s.window, kT, static_cast<int>(block / (s.SB * s.Hkv)));
     const int kvh = static_cast<int>(prob % s.Hkv), G = s.Hq / s.Hkv;
     const int64_t sb = prob / s.Hkv, k0 = static_cast<int64_t>(unit.x) * kT;
     load_tile<D>(sK, k, s, sb, k0, s.Hkv, kvh, s.kv_elems);
@@ -485,6 +477,28 @@ __global__ void __launch_bounds__(kThreads) window_dkv_f32_kernel(const __grid_c
     }
 }
 
+// The blocks of dK and dV, whose walks are the longer ones, then those of dQ: a short
+// sequence has too few of either to fill the GPU (509 tokens of 2 x 4 heads of 64: 76 us,
+// 109 in two launches).  Heads of 64 let two blocks share an SM, for which their
+// registers have to spill a little: 3.6 ms against 4.1 at 8192 tokens under a window of
+// 1024, but 86 us at 509 tokens, so that grids of one block an SM keep theirs.
+template <int D, int kPerSm>
+__global__ void __launch_bounds__(kThreads, kPerSm) window_bwd_f32_kernel(const __grid_constant__ AttnShape s,
+                                                                  int64_t dkv_blocks, const float *__restrict__ q,
+                                                                  const float *__restrict__ k,
+                                                                  const float *__restrict__ v,
+                                                                  const float *__restrict__ lse,
+                                                                  const float *__restrict__ dout,
+                                                                  const float *__restrict__ Dv, float *__restrict__ dq,
+                                                                  float *__restrict__ dk, float *__restrict__ dv)
+{
+    extern __shared__ __align__(16) float sm[];
+    if (blockIdx.x < dkv_blocks)
+        window_dkv<D>(s, blockIdx.x, sm, q, k, v, lse, dout, Dv, dk, dv);
+    else
+        window_dq<D>(s, blockIdx.x - dkv_blocks, sm, q, k, v, lse, dout, Dv, dq);
+}
+
 template <typename... Params, typename... Args>
 cudaError_t launch(void (*kernel)(Params...), int64_t grid, size_t smem, cudaStream_t st, Args... args)
 {
@@ -513,12 +527,11 @@ cudaError_t bwd(const AttnShape &s, const float *q, const float *k, const float 
 {
     const int64_t tiles = (s.N + kT - 1) / kT, rows = s.SB * s.Hq * s.N;
     cudaError_t e = launch(window_pre_f32_kernel<D>, (rows * 32 + kThreads - 1) / kThreads, 0, st, s, o, dout, Dv);
+    const int64_t dkv = s.units.n_units * s.SB * s.Hkv, blocks = dkv + tiles * s.Hq * s.SB;
     if (e == cudaSuccess)
-        e = launch(window_dkv_f32_kernel<D>, s.units.n_units * s.SB * s.Hkv, 4 * tile_bytes<D>() + 2 * kPBytes, st, s,
-                   q, k, v, lse, dout, static_cast<const float *>(Dv), dk, dv);
-    if (e == cudaSuccess)
-        e = launch(window_dq_f32_kernel<D>, tiles * s.Hq * s.SB, 4 * tile_bytes<D>() + kPBytes, st, s, q, k, v, lse,
-                   dout, static_cast<const float *>(Dv), dq);
+        e = launch(D == 128 || blocks <= num_sms() ? window_bwd_f32_kernel<D, 1> : window_bwd_f32_kernel<D, D == 64 ? 2 : 1>,
+                   blocks, 4 * tile_bytes<D>() + 2 * kPBytes, st, s, dkv, q, k, v, lse, dout,
+                   static_cast<const float *>(Dv), dq, dk, dv);
     return e;
 }
 
