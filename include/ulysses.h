@@ -630,12 +630,13 @@ uly_status ulysses_selftest_wait_timeout(uint64_t limit_ns, void *stream);
 
 /*
  * Debug build only (the library compiled with -DULY_DEBUG, which checks every
- * raw-pointer global access of the swap and attention kernels, and those of the
- * norm-rotation and LM-head loss kernels whose place depends on data or on the
- * schedule, against their buffers and reports ULY_ERR_BOUNDS instead of making
- * them): launches one tiny kernel whose check is given an offset past its
- * extent, touching no memory, so that the reporting path can be tested.  The release build returns
- * ULY_ERR_UNSUPPORTED and launches nothing.
+ * raw-pointer global access of the swap and attention kernels (the windowed ones
+ * too), and those of the norm-rotation, residual-norm and LM-head loss kernels
+ * whose place depends on data or on the schedule, against their buffers and
+ * reports ULY_ERR_BOUNDS instead of making them): launches one tiny kernel whose
+ * check is given an offset past its extent, touching no memory, so that the
+ * reporting path can be tested.  The release build returns ULY_ERR_UNSUPPORTED and
+ * launches nothing.
  */
 uly_status ulysses_selftest_bounds(void *stream);
 

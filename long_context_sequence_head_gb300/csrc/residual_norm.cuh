@@ -13,19 +13,20 @@
 // its rounding).
 //
 // Both directions are bound by HBM: 4 (forward) and 6 (backward) values move
-// per element, against 8 and about 20 operations.  A block takes a contiguous
-// run of rows, in slots of one long row or several short ones (contiguous, one
-// bulk copy a tensor).  One warp copies slots into a ring in shared memory, so
-// that the bytes on their way do not depend on registers; groups of one or more
-// warps take the slots in turn, a thread 16 bytes by 16 bytes of the same columns
-// of every row, so that the columns' sums stay in registers.  Few warps a row and
-// several rows at once: ten warps on one row of 2560 spent most of their time in
-// its sums (forward 455 us for 64K rows, backward 642; now 203 and 300, HBM's time for the
-// bytes 198 and 297).  The backward's three row
-// sums (S1 = sum gz hh, S2 = sum c yh b, S3 = sum c yh hh with b = dh + r1 gz, so
-// that sum c t yh = S2 - r1 mean(gz hh) S3) cross a group's warps in one exchange;
-// what both passes over a row need is formed again from the slot, which costs less
-// than the registers to hold it.
+// per element, against 8 and about 20 operations.  Rows come in slots of one long
+// row or several short ones (contiguous, one bulk copy a tensor); a block takes every
+// gridDim-th slot, or a contiguous run of rows where every sequence has a gate of its
+// own.  One warp copies slots into a ring in shared memory, so that the bytes on their
+// way do not depend on registers; groups of one or more warps, each with slots of its
+// own, take a row at a time, a thread 16 bytes by 16 bytes of the same columns of
+// every row, so that the columns' sums stay in registers.  Few warps a row and several
+// rows at once: ten warps on one row of 2560 spent most of their time in its sums
+// (64K rows: forward 455 us, backward 642; now 203 and 300, HBM's time for the bytes
+// 198 and 297).
+//   The backward's three row sums (S1 = sum gz hh, S2 = sum c yh b, S3 = sum c yh hh
+// with b = dh + r1 gz, so that sum c t yh = S2 - r1 mean(gz hh) S3) cross a group's
+// warps in one exchange; what both passes over a row need is formed again from the
+// slot, which costs less than the registers to hold it.
 #pragma once
 
 #include "uly_internal.h"

@@ -9,9 +9,11 @@
 //   Backward: a key tile walks the query tiles that see it.  Through the window
 // these are window/tile + 1, but a tile with sinks is seen by every later row:
 // 512 tiles at 64K tokens against 33 under a window of 4096, which would run on
-// alone at the end.  The walk past the window is therefore cut into extra units
-// of about the window's length that write fp32 sums of the sinks' dK and dV
-// (and add to dQ as any unit does); window_join_kernel adds them in order.
+// alone at the end.  Up to 64 sinks in bf16 a kernel that goes over the rows takes
+// what lies past the window (window_sinks.cu).  Otherwise that walk is cut into
+// extra units of about the window's length, which add to dQ as any unit does; their
+// dK and dV are fp32 sums, or in bf16 up to 320 sinks window_sinks.cu's.
+// window_join_kernel adds such sums in order.
 #include "uly_internal.h"
 
 namespace uly {

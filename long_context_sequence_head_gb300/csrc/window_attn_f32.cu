@@ -529,8 +529,8 @@ cudaError_t bwd(const AttnShape &s, const float *q, const float *k, const float 
     cudaError_t e = launch(window_pre_f32_kernel<D>, (rows * 32 + kThreads - 1) / kThreads, 0, st, s, o, dout, Dv);
     const int64_t dkv = s.units.n_units * s.SB * s.Hkv, blocks = dkv + tiles * s.Hq * s.SB;
     if (e == cudaSuccess)
-        e = launch(D == 128 || blocks <= num_sms() ? window_bwd_f32_kernel<D, 1> : window_bwd_f32_kernel<D, D == 64 ? 2 : 1>,
-                   blocks, 4 * tile_bytes<D>() + 2 * kPBytes, st, s, dkv, q, k, v, lse, dout,
+        e = launch(blocks <= num_sms() ? window_bwd_f32_kernel<D, 1> : window_bwd_f32_kernel<D, D == 64 ? 2 : 1>, blocks,
+                   4 * tile_bytes<D>() + 2 * kPBytes, st, s, dkv, q, k, v, lse, dout,
                    static_cast<const float *>(Dv), dq, dk, dv);
     return e;
 }

@@ -14,11 +14,11 @@
 //   Tensor-bound: 64K tokens, 32 heads, window 4096, 4 sinks 3.26 ms, 1310 TFLOP/s
 // of allowed pairs (6 % more are computed in boundary tiles); 8K, window 1024: 153
 // us, 844 TFLOP/s (160 with whole tiles of sinks), of which a block's start and end
-// take about a third.  A block that stays on its SM and takes tile after tile, the next one's Q and
-// first K loaded and its first S made meanwhile, was slower: with two Q buffers and
-// three K/V slots 3.50 ms and 155 us (the slots bind), with three Q tiles taken in
-// turn and four slots 3.79 ms and 175 us (the second head waits for the first one's
-// output to leave its Q tile).
+// take about a third.  A block that stays on its SM and takes tile after tile, the
+// next one's Q and first K loaded and its first S made meanwhile, was slower: with two
+// Q buffers and three K/V slots 3.50 ms and 155 us (the slots bind), with three Q
+// tiles taken in turn and four slots 3.79 ms and 175 us (the second head waits for the
+// first one's output to leave its Q tile).
 //
 // Warp roles (320 threads), TMEM and shared memory as in attn_fwd_bf16.cu.
 #include "uly_internal.h"

@@ -18,7 +18,7 @@ def test_window_and_norm_cases_on_the_debug_build():
     b.build(debug=True)
     env = dict(os.environ, ULY_DEBUG_BUILD="1")
     r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-p", "no:cacheprovider", "-m", "gpu",
-                        "tests/test_window_attn_gpu.py", "tests/test_window_decode_gpu.py",
+                        "tests/test_window_attn_gpu.py", "tests/test_window_sinks_gpu.py", "tests/test_window_decode_gpu.py",
                         "tests/test_residual_norm_gpu.py"],
                        cwd=ROOT, env=env, capture_output=True, text=True, timeout=900)
     assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-2000:]

@@ -166,7 +166,7 @@ def test_values_and_gradients(uly, B, N, P, D, gate, post, first, dtype):
 
 @pytest.mark.parametrize("dtype,D", [(BF16, 16384), (FP32, 8192), (BF16, 8200), (FP32, 4100)])
 def test_long_rows(uly, dtype, D):
-    """Rows of up to 32 KB: two and four chunks a thread, one stage."""
+    """Rows of up to 32 KB: two and four chunks a thread, one row in a slot."""
     test_values_and_gradients(uly, 2, 9, 3, D, "sequence", True, False, dtype)
 
 

@@ -118,7 +118,7 @@ def long_sequence(uly, S, B, C, Hq, Hkv, lens, window, sinks, dtype, d):
 
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
 def test_rolling_and_whole_caches_agree(uly, dtype):
-    """The same tokens in a whole cache and in a rolling one: the same bits."""
+    """The same tokens in a whole cache and in a rolling one."""
     lens, window, sinks = [900, 517, 1], 128, 4
     q, _, _, kc, vc, n = make(1, 3, 900, 8, 2, 128, lens, window, sinks, dtype)
     rolled = [torch.full((1, 3, 140, 2, 128), float("nan"), dtype=dtype, device="cuda") for _ in range(2)]
