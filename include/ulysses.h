@@ -449,10 +449,10 @@ uly_status ulysses_window_attn_fwd(const void *q, const void *k, const void *v, 
                                    void *stream);
 
 /*
- * Its backward: ulysses_attn_bwd's formulas over the same allowed pairs.  dK and
- * dV (and dQ in fp32) are summed in an order that depends on the arguments
- * alone; in bf16 dQ is summed with fp32 atomics, as in ulysses_attn_bwd, so its
- * last bits may differ between calls.
+ * Its backward: ulysses_attn_bwd's formulas over the same allowed pairs.  q, dout
+ * and lse have to be finite too.  dK and dV (and dQ in fp32) are summed in an order
+ * that depends on the arguments alone; in bf16 dQ is summed with fp32 atomics, as in
+ * ulysses_attn_bwd, so its last bits may differ between calls.
  */
 uly_status ulysses_window_attn_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
                                    const void *dout, void *dq, void *dk, void *dv, int64_t B, int64_t N,

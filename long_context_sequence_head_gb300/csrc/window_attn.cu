@@ -14,6 +14,8 @@
 // extra units of about the window's length, which add to dQ as any unit does; their
 // dK and dV are fp32 sums, or in bf16 up to 320 sinks window_sinks.cu's.
 // window_join_kernel adds such sums in order.
+#include <new>
+
 #include "uly_internal.h"
 
 namespace uly {
@@ -83,10 +85,13 @@ struct Cut {
 bool apart(int64_t sinks, int tile) { return tile == 128 && sinks > 0 && sinks <= kWindowSinksApart; }
 
 // Row tiles of a chunk of window_sinks.cu: as short as leaves a problem 64 of them, but
-// with many sinks (whose sums are large) 4 for each SM in all.
+// with many sinks (whose sums are large) 4 for each SM in all; and whole waves.
 int chunk_tiles(int64_t N, int64_t sinks, int64_t nprob)
 {
-    const int64_t most = sinks <= kWindowSinks ? 64 : std::clamp<int64_t>(608 / nprob, 4, 64);
+    const int64_t sms = num_sms();
+    int64_t most = sinks <= kWindowSinks ? 64 : std::clamp<int64_t>(4 * sms / nprob, 4, 64);
+    if (most * nprob > sms)
+        most = std::max<int64_t>(4, most * nprob / sms * sms / nprob);
     return static_cast<int>(std::max<int64_t>(2, ((N + 127) / 128 + most - 1) / most));
 }
 
@@ -381,7 +386,7 @@ size_t window_attn_workspace(int64_t B, int64_t N, int Hq, int Hkv, int d, int S
 
 cudaError_t window_attn_fwd(AttnShape s, const void *q, const void *k, const void *v, void *o, float *lse, int esize,
                             void *workspace, cudaStream_t stream)
-{
+try {
     const Layout L = layout(s.SB, s.N, s.Hq, s.Hkv, s.d, s.window, s.sinks, s.num_docs, false, esize);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     if (s.cu_host) {
@@ -399,12 +404,14 @@ cudaError_t window_attn_fwd(AttnShape s, const void *q, const void *k, const voi
         return launch_window_fwd_bf16(s, q, k, v, o, lse, stream);
     return launch_window_fwd_f32(s, static_cast<const float *>(q), static_cast<const float *>(k),
                                  static_cast<const float *>(v), static_cast<float *>(o), lse, stream);
+} catch (const std::bad_alloc &) {
+    return cudaErrorMemoryAllocation;
 }
 
 cudaError_t window_attn_bwd(AttnShape s, const void *q, const void *k, const void *v, const void *o, const float *lse,
                             const void *dout, void *dq, void *dk, void *dv, int esize, void *workspace,
                             cudaStream_t stream)
-{
+try {
     const int tile = esize == 2 ? 128 : kWindowTileF32;
     const Layout L = layout(s.SB, s.N, s.Hq, s.Hkv, s.d, s.window, s.sinks, s.num_docs, true, esize);
     Units units = make_units(s.N, s.window, s.sinks, s.cu_host, s.num_docs, tile, s.SB * s.Hkv);
@@ -444,6 +451,8 @@ cudaError_t window_attn_bwd(AttnShape s, const void *q, const void *k, const voi
         static_cast<const float *>(o), lse, static_cast<const float *>(dout), static_cast<float *>(dq),
         static_cast<float *>(dk), static_cast<float *>(dv), reinterpret_cast<float *>(ws + L.D), stream);
     return e != cudaSuccess ? e : launch_join<float>(s, dk, dv, tile, stream);
+} catch (const std::bad_alloc &) {
+    return cudaErrorMemoryAllocation;
 }
 
 }  // namespace uly

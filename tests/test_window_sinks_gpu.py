@@ -27,6 +27,10 @@ CASES = [
     (1, 1, 700, 2, 2, 10, 64, [0, 100, 300, 400, 700]),     # a second tile of sinks that another document ends
     (1, 1, 513, 2, 1, 1, 64, [0, 127, 256, 380, 513]),
     (1, 1, 400, 2, 1, 5, 40, [0, 30, 390, 400]),        # fewer keys than sinks
+    (1, 1, 900, 3, 1, 33, 160, None),                   # 32 behind a whole tile
+    (1, 1, 900, 2, 1, 300, 161, None),
+    (1, 2, 1300, 3, 1, 7, 140, [0, 90, 700, 1300]),     # sinks that end at key 230 and 840
+    (1, 1, 1000, 2, 1, 128, 40, [0, 100, 1000]),
 ]
 
 
