@@ -109,6 +109,11 @@ CASES = [
     (1, 60000, 2, 64, "shared", True, False),
     (1, 3100, 1, 8192, None, False, False),
     (1, 3100, 1, 2048, None, False, True),
+    (1, 20000, 1, 512, "shared", True, False),
+    # many gates
+    (16, 130, 1, 264, "sequence", True, False),
+    (130, 6, 2, 776, "sequence", True, False),
+    (300, 1, 1, 72, "sequence", False, False),
 ]
 
 
