@@ -257,13 +257,13 @@ Units make_units(int64_t N, int window, int sinks, const int32_t *cu, int num_do
     return r;
 }
 
-// Query tiles of 128 rows in the order of their walks, the longest first.
-void tile_order(int64_t N, int window, int sinks, const int32_t *cu, int num_docs, int32_t *out)
+// Query tiles of `rows` rows in the order of their walks, the longest first.
+void tile_order(int64_t N, int window, int sinks, const int32_t *cu, int num_docs, int rows, int32_t *out)
 {
-    const int n = static_cast<int>((N + 127) / 128);
+    const int n = static_cast<int>((N + rows - 1) / rows);
     std::vector<int64_t> walk(n);
     for (int t = 0; t < n; ++t) {
-        const int64_t a = static_cast<int64_t>(t) * 128, b = std::min<int64_t>(a + 127, N - 1);
+        const int64_t a = static_cast<int64_t>(t) * rows, b = std::min<int64_t>(a + rows - 1, N - 1);
         int64_t lo, hi;
         doc_range_host(cu, num_docs, N, a, lo, hi);
         const int64_t first = std::max(lo, a - window + 1), sink_end = std::min(lo + sinks, first);
@@ -276,8 +276,8 @@ void tile_order(int64_t N, int window, int sinks, const int32_t *cu, int num_doc
 }
 
 // ------------------------------------------------------------ workspace
-//   cu_seqlens and, behind it, the forward's tile order or the backward's units
-//   and joins (with documents); backward: as ulysses_attn_bwd's scratch, then the
+//   cu_seqlens and, behind it, the forward's orders of tiles and of pairs of them
+//   (with documents) or the backward's units, joins and chunks; backward: as ulysses_attn_bwd's scratch, then the
 //   slots of fp32 sums
 struct Layout {
     size_t cu = 0, list = 0, list_ints = 0, lse2 = 0, D = 0, acc = 0, part = 0, total = 0;
@@ -301,7 +301,7 @@ Layout layout(int64_t SB, int64_t N, int Hq, int Hkv, int d, int64_t window, int
     if (num_docs > 0 || L.chunks > 0) {
         L.cu = take((static_cast<size_t>(num_docs) + 1) * sizeof(int32_t));
         L.list_ints = bwd ? static_cast<size_t>(L.units + L.joins + 3 * L.chunks) * 4
-                          : static_cast<size_t>((N + 127) / 128);
+                          : static_cast<size_t>((N + 127) / 128 + (N + 255) / 256);
         L.list = take(L.list_ints * sizeof(int32_t));
     }
     L.Npad = (N + 127) / 128 * 128;
@@ -393,7 +393,8 @@ try {
         const size_t list = (L.list - L.cu) / sizeof(int32_t);
         std::vector<int32_t> host(list + L.list_ints);
         std::copy(s.cu_host, s.cu_host + s.num_docs + 1, host.begin());
-        tile_order(s.N, s.window, s.sinks, s.cu_host, s.num_docs, host.data() + list);
+        tile_order(s.N, s.window, s.sinks, s.cu_host, s.num_docs, 128, host.data() + list);
+        tile_order(s.N, s.window, s.sinks, s.cu_host, s.num_docs, 256, host.data() + list + (s.N + 127) / 128);
         s.cu_dev = reinterpret_cast<int32_t *>(ws + L.cu);
         s.order_dev = reinterpret_cast<int32_t *>(ws + L.list);
         const cudaError_t e = stage(host, reinterpret_cast<int32_t *>(ws + L.cu), stream);

@@ -7,6 +7,11 @@
 // lazy rescaling (the running maximum is kept until a row's exponentials would
 // pass 2^8), P overwrites S in TMEM and is the A operand of P V.
 //
+// A head without a partner takes two neighbouring tiles of rows instead, whose walk is
+// one key tile longer: 8 such heads of 32,768 tokens, window 4096, 667 us, 1040 with a
+// tile a block.  Not where there is an SM for every tile (16 heads of 1024 tokens,
+// window 512: 23 us, 26 in pairs).
+//
 // What differs is the walk: a tile of 128 rows takes the key tiles of its window
 // and its sinks.  Up to 32 sinks are one tile of 32 keys that starts at the
 // document's first, instead of 128 that hold a few; more are whole tiles.  Window
@@ -47,6 +52,7 @@ struct Params {
     int64_t SB, N;
     int Hq, Hkv, G, n_qtiles;
     int units, pair_units;  // of the call; those of two heads come first
+    bool tall;              // single heads take two tiles of rows
     const int32_t *cu;
     int num_docs;
     int window, sinks;
@@ -79,15 +85,14 @@ __device__ __forceinline__ void doc_range(const Params &p, int i, int &lo, int &
 // A block's rows and the key tiles it walks.
 struct Unit {
     int sb, kvh, h0;  // first head
-    bool two;
-    int q0;
+    bool two;         // heads, or tiles of rows
+    int q0, down;     // first row; rows from the first tile to the second (0: two heads)
     int start;        // of the first row's document
     int n_sink;       // tiles of its sinks: one narrow one, or whole ones from tile `sink` on
     int sink, lo;     // first whole tile of sinks, first tile of the window
     int n;            // tiles
 
-    // Pairs of heads come first, then the single heads of an odd group, so that the
-    // short blocks fill the end of the launch.
+    // Pairs of heads come first, then the single heads of an odd group.
     __device__ __forceinline__ Unit(const Params &p, int u)
     {
         const int pairs = p.G / 2;
@@ -97,12 +102,19 @@ struct Unit {
             pair = u % pairs;
             rest = u / pairs;
         }
-        const int rank = rest % p.n_qtiles, prob = rest / p.n_qtiles;
+        down = !two && p.tall ? kBM : 0;
+        const int n_ranks = down ? (p.n_qtiles + 1) / 2 : p.n_qtiles;
+        const int rank = rest % n_ranks, prob = rest / n_ranks;
         kvh = prob % p.Hkv;
         sb = prob / p.Hkv;
         h0 = kvh * p.G + 2 * pair;
-        q0 = (p.order != nullptr ? p.order[rank] : p.n_qtiles - 1 - rank) * kBM;
-        const int last = min(q0 + kBM, static_cast<int>(p.N)) - 1;
+        q0 = p.order != nullptr ? p.order[down ? p.n_qtiles + rank : rank] : n_ranks - 1 - rank;
+        if (down) {
+            q0 *= 2;
+            two = q0 + 1 < p.n_qtiles;
+        }
+        q0 *= kBM;
+        const int last = min(q0 + (two ? down : 0) + kBM, static_cast<int>(p.N)) - 1;
         int end;
         doc_range(p, q0, start, end);
         const int first = max(start, q0 - p.window + 1), sink_end = min(start + p.sinks, first);
@@ -113,6 +125,7 @@ struct Unit {
             n_sink = 1;
         n = n_sink + last / kBN - lo + 1;
     }
+    __device__ __forceinline__ int head(int t) const { return down ? h0 : h0 + t; }
     __device__ __forceinline__ bool narrow(const Params &p, int j) const { return j < n_sink && p.sinks <= kFew; }
     __device__ __forceinline__ int key0(const Params &p, int j) const
     {
@@ -234,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto load_q = [&](int t) {
                 uint8_t *dst = smem + Smem::kQ + t * kTileBytes;
                 mbar_expect_tx(&q_full[t], kTileBytes);
-                p.L.tile(x.sb, x.q0, p.Hq, x.h0 + t, c1, c2, c3, c4);
+                p.L.tile(x.sb, x.q0 + t * x.down, p.Hq, x.head(t), c1, c2, c3, c4);
                 tma_load_5d(dst, &tm_q, &q_full[t], 0, c1, c2, c3, c4);
                 tma_load_5d(dst + kChunk, &tm_q, &q_full[t], 64, c1, c2, c3, c4);
             };
@@ -359,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tO = tbase + 256 + t * 128 + (static_cast<uint32_t>(wq * 32) << 16);
         const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
         if (t == 0 || x.two) {
-            const int row = x.q0 + r;
+            const int row = x.q0 + t * x.down + r;
             Row see;
             {
                 const int at = min(row, static_cast<int>(p.N) - 1);
@@ -601,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fence_async_smem();
                 if (row < p.N) {
-                    const int64_t li = (static_cast<int64_t>(x.sb) * p.Hq + x.h0 + t) * p.N + row;
+                    const int64_t li = (static_cast<int64_t>(x.sb) * p.Hq + x.head(t)) * p.N + row;
                     if (ULY_IN_BOUNDS(p.w.status, li, 1, p.lse_elems, 0x12))
                         p.lse[li] = (sm.m + __log2f(sm.l)) * 0.69314718055994530942f;
                 }
@@ -609,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_bar_sync(1 + t, 128);  // the head's four warps have staged their rows
             if (r == 0 && have_o) {
                 int c1, c2, c3, c4;
-                p.L.tile(x.sb, x.q0, p.Hq, x.h0 + t, c1, c2, c3, c4);
+                p.L.tile(x.sb, x.q0 + t * x.down, p.Hq, x.head(t), c1, c2, c3, c4);
                 tma_store_5d(&tm_o, stage, 0, c1, c2, c3, c4);
                 tma_store_5d(&tm_o, stage + kChunk, 64, c1, c2, c3, c4);
                 bulk_commit();
@@ -647,7 +660,9 @@ cudaError_t launch_window_fwd_bf16(const AttnShape &s, const void *q, const void
     p.G = s.Hq / s.Hkv;
     p.n_qtiles = static_cast<int>((s.N + kBM - 1) / kBM);
     p.pair_units = static_cast<int>(s.SB * s.Hkv * (p.G / 2) * p.n_qtiles);
-    p.units = p.pair_units + static_cast<int>(p.G % 2 ? s.SB * s.Hkv * p.n_qtiles : 0);
+    const int64_t singles = p.G % 2 ? s.SB * s.Hkv : 0;
+    p.tall = p.pair_units + singles * p.n_qtiles > num_sms();
+    p.units = p.pair_units + static_cast<int>(singles * (p.tall ? (p.n_qtiles + 1) / 2 : p.n_qtiles));
     p.cu = s.cu_dev;
     p.num_docs = s.num_docs;
     p.window = s.window;

@@ -31,6 +31,13 @@ CASES = [
     (1, 1, 900, 2, 1, 300, 161, None),
     (1, 2, 1300, 3, 1, 7, 140, [0, 90, 700, 1300]),     # sinks that end at key 230 and 840
     (1, 1, 1000, 2, 1, 128, 40, [0, 100, 1000]),
+    # enough tiles for the forward to take single heads' rows two tiles at a time
+    (4, 1, 1300, 8, 8, 200, 3, None),
+    (4, 1, 1153, 8, 8, 1, 0, None),
+    (2, 2, 1400, 6, 2, 130, 140, None),
+    (4, 1, 1200, 6, 2, 90, 30, [0, 1, 130, 300, 310, 700, 1100, 1200]),
+    (2, 2, 1290, 5, 5, 2000, 0, [0, 128, 640, 650, 1290]),
+    (5, 1, 1030, 3, 1, 17, 300, [0, 500, 1030]),
 ]
 
 
