@@ -79,10 +79,17 @@ struct Cut {
 };
 
 // In bf16: in documents with rows past their window the dK and dV of the sinks are
-// window_sinks.cu's.  The more there are the less each stands out: past 320 (an element
-// of dK 0.3 of its rms off at 64K tokens; 130: 0.47) they are the main kernel's, which
-// takes 11 ms at 64K under a window of 4096, this one 12 with 130 and 14 with 300.
-bool apart(int64_t sinks, int tile) { return tile == 128 && sinks > 0 && sinks <= kWindowSinksApart; }
+// window_sinks.cu's.  How much a sink's sum stands out goes with the root of tokens by
+// sinks, so that many sinks of few tokens are left to the main kernel (an element of dK
+// was 0.47 of its rms off with 130 sinks of 64K tokens, 0.3 with 300 of 24K), and more
+// than 320.  64K tokens under a window of 4096 take 11 ms with 513 sinks, 12 with 130
+// and 13.8 with 300 apart; 22K tokens of 256 heads, window 44, 300 sinks 15.7 ms apart.
+constexpr int64_t kTokensPerSink = 128;
+bool apart(int64_t N, int64_t sinks, int tile)
+{
+    return tile == 128 && sinks > 0 &&
+           (sinks <= kWindowSinks || (sinks <= kWindowSinksApart && N >= kTokensPerSink * sinks));
+}
 
 // Row tiles of a chunk of window_sinks.cu: as short as leaves a problem 64 of them, but
 // with many sinks (whose sums are large) 4 for each SM in all; and whole waves.
@@ -108,7 +115,7 @@ void unit_bounds(int64_t N, int64_t window, int64_t sinks, int num_docs, int til
     units = n + extra;
     slots = joins + extra;
     chunks = 0;
-    if (apart(sinks, tile)) {
+    if (apart(N, sinks, tile)) {
         // a document has chunks of its own beside those of the rows between; documents
         // may share a tile
         const int64_t own = std::min(n, docs), len = chunk_tiles(N, sinks, nprob), pieces = (n + len - 1) / len;
@@ -198,7 +205,7 @@ Units make_units_apart(int64_t N, int window, int sinks, const int32_t *cu, int 
 
 Units make_units(int64_t N, int window, int sinks, const int32_t *cu, int num_docs, int tile, int64_t nprob)
 {
-    if (apart(sinks, tile))
+    if (apart(N, sinks, tile))
         return make_units_apart(N, window, sinks, cu, num_docs, nprob);
     Units r;
     WindowUnits &u = r.u;
@@ -322,8 +329,8 @@ Layout layout(int64_t SB, int64_t N, int Hq, int Hkv, int d, int64_t window, int
 
 // ---------------------------------------------------------------- join
 // dK and dV of the sinks whose walk was cut: the sums of their tile's slots, in
-// order.  Blocks take a (tile, problem) and every gridDim.y-th of its keys; of 2 d
-// threads the first d sum dK, the others dV.
+// order.  Blocks take a (tile, problem) and one of its keys; of 2 d threads the first d
+// sum dK, the others dV.
 template <typename T>
 __global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ AttnShape s, T *__restrict__ dk,
                                                           T *__restrict__ dv, int tile)
@@ -371,7 +378,7 @@ cudaError_t launch_join(const AttnShape &s, void *dk, void *dv, int tile, cudaSt
 {
     if (s.units.n_joins == 0)
         return cudaSuccess;
-    const dim3 grid(static_cast<unsigned>(s.units.n_joins * s.SB * s.Hkv), std::min(s.units.rows, 16));
+    const dim3 grid(static_cast<unsigned>(s.units.n_joins * s.SB * s.Hkv), s.units.rows);  // at most 128
     window_join_kernel<T><<<grid, 2 * s.d, 0, stream>>>(s, static_cast<T *>(dk), static_cast<T *>(dv), tile);
     return cudaGetLastError();
 }

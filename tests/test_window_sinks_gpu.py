@@ -17,6 +17,9 @@ CASES = [
     (1, 1, 900, 2, 1, 40, 17, None),
     (2, 1, 1025, 4, 2, 1, 64, None),
     (1, 1, 1100, 2, 1, 130, 65, None),
+    (1, 1, 8400, 2, 1, 100, 65, None),                  # many sinks apart
+    (1, 1, 9100, 1, 1, 20, 70, [0, 127, 4000, 4100, 9100]),
+    (1, 1, 25700, 1, 1, 1, 200, None),
     (1, 1, 2600, 2, 1, 100, 300, None),
     (2, 1, 1400, 4, 2, 1, 512, None),
     (1, 1, 1400, 2, 1, 1, 513, None),
@@ -95,7 +98,7 @@ def sink_sums(q, k, v, dout, window, start, end, sinks):
 
 
 @pytest.mark.parametrize("window,sinks,cu", [(256, 4, None), (30, 1, None), (2000, 40, [0, 17, 9000, 9050, 24000]),
-                                             (300, 200, None)])
+                                             (300, 130, None)])
 def test_long_walks_keep_their_precision(uly, window, sinks, cu):
     """Queries share a direction that the sinks answer to, as trained ones do."""
     N, Hq, Hkv = 24000, 4, 2
