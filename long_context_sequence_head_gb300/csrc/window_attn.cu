@@ -205,7 +205,8 @@ Units make_units_apart(int64_t N, int window, int sinks, const int32_t *cu, int 
 
 Units make_units(int64_t N, int window, int sinks, const int32_t *cu, int num_docs, int tile, int64_t nprob)
 {
-    if (apart(N, sinks, tile))
+    // (a sequence without rows past its window needs no list of units)
+    if (apart(N, sinks, tile) && (num_docs > 0 || window_end(N, window, tile, 0) < (N - 1) / tile))
         return make_units_apart(N, window, sinks, cu, num_docs, nprob);
     Units r;
     WindowUnits &u = r.u;
