@@ -231,7 +231,7 @@ uly_status ulysses_residual_norm_fwd(const void *x, const void *y, const void *w
                                      void *z, float *rstd, int64_t B, int64_t N, int32_t D, int32_t P,
                                      uly_dtype dtype, void *stream);
 
-/* Bytes of device workspace ulysses_residual_norm_bwd needs (0 for sizes it would reject). */
+/* Bytes of device workspace ulysses_residual_norm_bwd needs, for either type (0 for sizes it would reject with both). */
 size_t ulysses_residual_norm_workspace_size(int64_t B, int64_t N, int32_t D, int32_t P);
 
 /*

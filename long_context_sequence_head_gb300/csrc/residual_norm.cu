@@ -68,11 +68,12 @@ void partial_bytes(const ResidualNormPlan &q, int64_t T, int64_t run, int D, siz
 
 size_t residual_norm_workspace(int64_t T, int64_t Np, int D)
 {
-    // the largest of the element types, gates shared or a sequence's own
+    // the largest of the element types, gates shared or a sequence's own; a type whose
+    // rows are no multiple of 16 bytes, which a call refuses, has no plan
     size_t most = 0;
     for (int es = 2; es <= 4; es += 2)
         for (const int64_t run : {T, Np}) {
-            if (D * es > 32768)
+            if (D * es > 32768 || D * es % 16 != 0)
                 continue;
             size_t one, gates;
             partial_bytes(plan_for(T, run, D, es, true), T, run, D, one, gates);
