@@ -78,18 +78,14 @@ struct Cut {
     }
 };
 
-// In bf16: in documents with rows past their window the dK and dV of the sinks are
-// window_sinks.cu's.  How much a sink's sum stands out goes with the root of tokens by
-// sinks, so that many sinks of few tokens are left to the main kernel (an element of dK
-// was 0.47 of its rms off with 130 sinks of 64K tokens, 0.3 with 300 of 24K), and more
-// than 320.  64K tokens under a window of 4096 take 11 ms with 513 sinks, 12 with 130
-// and 13.8 with 300 apart; 22K tokens of 256 heads, window 44, 300 sinks 15.7 ms apart.
-constexpr int64_t kTokensPerSink = 128;
-bool apart(int64_t N, int64_t sinks, int tile)
-{
-    return tile == 128 && sinks > 0 &&
-           (sinks <= kWindowSinks || (sinks <= kWindowSinksApart && N >= kTokensPerSink * sinks));
-}
+// In bf16: in documents with rows past their window the dK and dV of up to 320 sinks
+// are window_sinks.cu's, however few tokens there are for each: with P and dS in one
+// bf16 part an element of dK was 0.47 of its rms off with 130 sinks of 64K tokens, 0.3
+// with 300 of 24K, and dV of 65 sinks in documents of 2,000 to 3,900 tokens four times
+// the bound that two parts keep.  64K tokens under a window of 4096 take 11 ms with 513
+// sinks, 12 with 130 and 13.8 with 300 apart; 8K tokens, window 128, 130 sinks 214 us
+// (121 in one part), 32K, window 512, 300 sinks 954 (472).
+bool apart(int64_t sinks, int tile) { return tile == 128 && sinks > 0 && sinks <= kWindowSinksApart; }
 
 // Row tiles of a chunk of window_sinks.cu: as short as leaves a problem 64 of them, but
 // with many sinks (whose sums are large) 4 for each SM in all; and whole waves.
@@ -115,7 +111,7 @@ void unit_bounds(int64_t N, int64_t window, int64_t sinks, int num_docs, int til
     units = n + extra;
     slots = joins + extra;
     chunks = 0;
-    if (apart(N, sinks, tile)) {
+    if (apart(sinks, tile)) {
         // a document has chunks of its own beside those of the rows between; documents
         // may share a tile
         const int64_t own = std::min(n, docs), len = chunk_tiles(N, sinks, nprob), pieces = (n + len - 1) / len;
@@ -206,7 +202,7 @@ Units make_units_apart(int64_t N, int window, int sinks, const int32_t *cu, int 
 Units make_units(int64_t N, int window, int sinks, const int32_t *cu, int num_docs, int tile, int64_t nprob)
 {
     // (a sequence without rows past its window needs no list of units)
-    if (apart(N, sinks, tile) && (num_docs > 0 || window_end(N, window, tile, 0) < (N - 1) / tile))
+    if (apart(sinks, tile) && (num_docs > 0 || window_end(N, window, tile, 0) < (N - 1) / tile))
         return make_units_apart(N, window, sinks, cu, num_docs, nprob);
     Units r;
     WindowUnits &u = r.u;
