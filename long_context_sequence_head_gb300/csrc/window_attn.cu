@@ -99,24 +99,35 @@ int chunk_tiles(int64_t N, int64_t sinks, int64_t nprob)
 }
 
 // Most units, slots, joins and chunks of a problem whose documents are not known.
+// Documents follow one another, so that the tiles that each spans beside its first are
+// n - 1 at most in all: of documents with as many as a cut (or window_sinks.cu) takes
+// there are only so many, and what goes with their length is counted once, not for
+// each (8 problems of 64K tokens, window 64, 320 sinks, 500 documents: 1.3 GB of sums, 5.0
+// with every document as long as all).
 void unit_bounds(int64_t N, int64_t window, int64_t sinks, int num_docs, int tile, int64_t nprob, int64_t &units,
                  int64_t &slots, int64_t &joins, int64_t &chunks)
 {
     const Cut cut(window, sinks, num_docs > 0, tile);
-    const int64_t n = (N + tile - 1) / tile;
-    // only a document longer than the window has rows past it
-    const int64_t docs = num_docs > 0 ? std::min<int64_t>(num_docs, N / (window + 1)) : 1;
-    joins = std::min(n, cut.tiles_with_sinks * docs);
-    const int64_t extra = std::min(joins * cut.most, joins + cut.tiles_with_sinks * (n + docs) / cut.length);
+    const int64_t n = (N + tile - 1) / tile, beside = n - 1, tws = cut.tiles_with_sinks;
+    // only a document longer than the window has rows past it, and a tile's window ends
+    // `within` tiles behind it
+    const int64_t long_docs = num_docs > 0 ? std::min<int64_t>(num_docs, N / (window + 1)) : 1;
+    const int64_t within = (window + tile - 2) / tile;
+    auto documents = [&](int64_t past) { return std::min(long_docs, beside / (within + past)); };
+    // a walk is cut from length / 2 + 1 tiles past the window on
+    const int64_t walks = cut.most > 0 ? std::min(n, tws * documents(cut.length / 2 + 1)) : 0;
+    const int64_t extra = std::min(walks * cut.most, walks + tws * beside / cut.length);
     units = n + extra;
+    joins = walks;
     slots = joins + extra;
     chunks = 0;
     if (apart(sinks, tile)) {
-        // a document has chunks of its own beside those of the rows between; documents
-        // may share a tile
-        const int64_t own = std::min(n, docs), len = chunk_tiles(N, sinks, nprob), pieces = (n + len - 1) / len;
+        // a document that walks past its first tile's window has chunks of its own beside
+        // those of the rows between; documents may share a tile
+        const int64_t own = documents(1), len = chunk_tiles(N, sinks, nprob), pieces = (n + len - 1) / len;
         chunks = pieces + 3 * own + 1;
-        slots = joins + cut.tiles_with_sinks * (pieces + 2 * own);
+        joins = std::min(n, tws * own);
+        slots = 2 * joins + tws * (beside / len);
     }
 }
 
