@@ -430,8 +430,12 @@ uly_status ulysses_attn_bwd_noalloc(const void *q, const void *k, const void *v,
  *
  * q, o, k, v, lse, cu_seqlens_host, num_docs, softmax_scale : as in
  *              ulysses_attn_fwd; no output may overlap an input or another
- *              output.  K and V of every token must be finite: a value that is
- *              not may spoil rows of its 128 neighbours that do not see it.
+ *              output.  K and V of every token must be finite, padding's too
+ *              (zeros do): one that is not, at token j, may spoil rows that do not
+ *              see it, of any document, since rows and keys are taken in tiles:
+ *              those from j - 384 to j + window + 384; and, if j lies in one tile
+ *              of 128 tokens with one of the first max(sinks, 32) of a document
+ *              (sinks > 0), those from that document's start to 384 behind its end.
  * window >= 1, sinks >= 0, any size.
  * workspace  : device, >= ulysses_window_attn_workspace_size(..., for_bwd) bytes
  *              (num_docs = 0 without documents).  Calls that may run at the same
@@ -450,7 +454,7 @@ uly_status ulysses_window_attn_fwd(const void *q, const void *k, const void *v, 
 
 /*
  * Its backward: ulysses_attn_bwd's formulas over the same allowed pairs.  q, dout
- * and lse have to be finite too.  dK and dV (and dQ in fp32) are summed in an order
+ * and lse have to be finite too, or any gradient may be spoilt.  dK and dV (and dQ in fp32) are summed in an order
  * that depends on the arguments alone; in bf16 dQ is summed with fp32 atomics, as in
  * ulysses_attn_bwd, so its last bits may differ between calls.
  */
