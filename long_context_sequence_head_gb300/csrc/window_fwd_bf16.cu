@@ -166,11 +166,12 @@ struct Softmax {
         const float2 a = fadd2(fadd2(rs[0], rs[1]), fadd2(rs[2], rs[3]));
         return a.x + a.y;
     }
-    // raises m to a tile's maximum where the lazy rule asks for it; the factor of l and O
-    __device__ __forceinline__ float raise(float mx, float scale_log2, bool &rescale)
+    // raises m to a tile's maximum where that exceeds it by more than `slack`; the factor
+    // of l and O
+    __device__ __forceinline__ float raise(float mx, float scale_log2, float slack, bool &rescale)
     {
         const float cand = mx * scale_log2;
-        if (!(cand > m + kRescaleThreshold))
+        if (!(cand > m + slack))
             return 1.f;
         const float alpha = ex2_approx(m - cand);
         rescale = m != -INFINITY;
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < kBN; ++c)
                         pm[c & 7] = fmaxf(pm[c & 7], __uint_as_float(v[c]));
-                    alpha = sm.raise(Softmax::row_max(pm), p.scale_log2, rescale);
+                    alpha = sm.raise(Softmax::row_max(pm), p.scale_log2, kRescaleThreshold, rescale);
                     const float2 shift = sm.shift();
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -525,7 +526,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             pm[c & 7] = fmaxf(pm[c & 7], keep[c >> 5] >> (c & 31) & 1u ? __uint_as_float(v[c])
                                                                                        : -INFINITY);
                     }
-                    alpha = sm.raise(Softmax::row_max(pm), p.scale_log2, rescale);
+                    // A row whose first tile held few of its keys (its sinks, a window's last
+                    // ones) may have a maximum so low that every later tile's sum passes the
+                    // bound without a score 2^8 above it: raised here whatever the slack, it
+                    // comes this way once.  16K tokens of 8 heads, window 4096, 4 sinks, keys
+                    // that no query prefers: 206 us, 307 with the lazy rule here too; 64K of 32
+                    // heads 3.40 ms for 5.14.
+                    alpha = sm.raise(Softmax::row_max(pm), p.scale_log2, 0.f, rescale);
                     const float2 shift = sm.shift();
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
