@@ -16,10 +16,12 @@
 // and its sinks.  Up to 32 sinks are one tile of 32 keys that starts at the
 // document's first, instead of 128 that hold a few; more are whole tiles.  Window
 // tiles start at multiples of 128: 9 of them under a window of 1024.
-//   Tensor-bound: 64K tokens, 32 heads, window 4096, 4 sinks 3.26 ms, 1310 TFLOP/s
-// of allowed pairs (6 % more are computed in boundary tiles); 8K, window 1024: 153
-// us, 844 TFLOP/s (160 with whole tiles of sinks), of which a block's start and end
-// take about a third.  A block that stays on its SM and takes tile after tile, the
+//   64K tokens, 32 heads, window 4096, 4 sinks 3.24 ms, 1310 TFLOP/s of allowed pairs
+// (6 % more are computed in boundary tiles); 8K, window 1024: 152 us, 850 TFLOP/s (160
+// with whole tiles of sinks), of which a block's start and end take about a third.  At
+// 16K tokens under a window of 4096 the tensor pipe is busy 57 % of the cycles and the
+// exponentials' 29 %: between them and the full forward's 1,500 TFLOP/s are start and end
+// of walks of 34 tiles, 8 to 10 us a block of 60.  A block that stays on its SM and takes tile after tile, the
 // next one's Q and first K loaded and its first S made meanwhile, was slower: with two
 // Q buffers and three K/V slots 3.50 ms and 155 us (the slots bind), with three Q
 // tiles taken in turn and four slots 3.79 ms and 175 us (the second head waits for the
